@@ -16,18 +16,21 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple, Optional
 
 import torch
 
 __all__ = [
     "MIN_TOKENS", "MAX_TOKENS", "NROWS", "EwgError", "can_accumulate_embedding_wgrad",
     "accumulate_embedding_wgrad", "workspace_bytes", "plan", "apply", "read_status",
-    "library_path", "lib", "accumulate_embedding_wgrad_shard",
+    "library_path", "lib", "accumulate_embedding_wgrad_shard", "MAX_TOP", "TokenLogprobs",
+    "token_logprobs", "token_logprobs_backward", "status_workspace",
 ]
 
 MIN_TOKENS = 3073
 MAX_TOKENS = 1 << 28
 NROWS = 10
+MAX_TOP = 32
 
 _INT32, _INT64, _BF16, _FP32 = 0, 1, 2, 3
 OK, ERR_UNSUPPORTED, ERR_INVALID, ERR_CUDA, ERR_ID_OUT_OF_RANGE, ERR_TIMEOUT, ERR_BOUNDS = \
@@ -106,6 +109,13 @@ def _load(path):
     L.ewg_accumulate_host.argtypes = [vp, i32, i64, vp, i32, vp, i32, i64, i64, i64, vp,
                                       sz, vp]
     L.ewg_accumulate_host.restype = i32
+    f32 = ctypes.c_float
+    L.ewg_token_logprobs.argtypes = [vp, i32, i64, vp, i32, i64, i64, f32, i32, vp, vp, vp, vp,
+                                     vp, vp, vp, sz, vp]
+    L.ewg_token_logprobs.restype = i32
+    L.ewg_token_logprobs_backward.argtypes = [vp, i32, i64, vp, i32, i64, i64, f32, vp, vp, vp,
+                                              vp, vp, vp, i64, vp, sz, vp]
+    L.ewg_token_logprobs_backward.restype = i32
     L.ewg_read_status.argtypes = [vp, vp, ctypes.POINTER(i32)]
     L.ewg_read_status.restype = i32
     L.ewg_status_string.argtypes = [i32]
@@ -347,3 +357,134 @@ def apply(grad: torch.Tensor, main_grad: torch.Tensor, num_tokens: int,
                                   _FLOAT_CODES[main_grad.dtype], num_tokens, V, H,
                                   main_grad.stride(0) if V > 1 else H, workspace.data_ptr(),
                                   workspace.numel(), _stream_ptr(main_grad.device)))
+
+
+class TokenLogprobs(NamedTuple):
+    """What token_logprobs returns: fp32 tensors of the targets' shape, and with `top` the
+    alternatives ([*targets.shape, top] fp32 and int64, best first)."""
+    logprobs: torch.Tensor
+    entropy: torch.Tensor
+    row_max: torch.Tensor          # largest logit of the row
+    log_sum: torch.Tensor          # log of the sum of exp(scale * (logit - row_max))
+    top_logprobs: Optional[torch.Tensor]
+    top_ids: Optional[torch.Tensor]
+
+
+def status_workspace(device=None) -> torch.Tensor:
+    """The 256 device bytes in which token_logprobs and its backward leave their status."""
+    return torch.empty(256, dtype=torch.uint8, device=device or "cuda")
+
+
+def _logits_args(name, logits, targets):
+    """(num_tokens, vocab, [num_tokens, vocab] view, row stride) of logits [*targets.shape, vocab]."""
+    def no(reason):
+        raise ValueError(f"{name} does not support these tensors: {reason}")
+    if not (logits.is_cuda and targets.is_cuda) or logits.device != targets.device:
+        no("logits and targets must be on one CUDA device")
+    if logits.dtype not in _FLOAT_CODES or targets.dtype not in _ID_CODES:
+        no("logits must be bf16/fp32, targets int32/int64")
+    if logits.dim() == 0 or logits.shape[:-1] != targets.shape:
+        no("logits must be [*targets.shape, vocab]")
+    if not targets.is_contiguous():
+        no("targets must be contiguous")
+    n, V = targets.numel(), logits.shape[-1]
+    return n, V, *_rows(name, "logits", logits, n, V)
+
+
+def _rows(name, what, x, n, V):
+    """x [..., V] as [n, V] with unit inner stride, and its row stride; no copy."""
+    if x.dim() == 2 and (x.stride(1) == 1 or V <= 1):
+        return x, x.stride(0) if n > 1 else V
+    try:
+        x2 = x.view(n, V)
+    except RuntimeError:
+        x2 = None
+    if x2 is None or (x2.stride(1) != 1 and V > 1 and n > 0):
+        raise ValueError(f"{name} does not support these tensors: {what} must have rows of unit "
+                         "inner stride that share one row stride")
+    return x2, x2.stride(0) if n > 1 else V
+
+
+def _status_ws(workspace, check, device):
+    if workspace is None and check:
+        workspace = status_workspace(device)
+    return workspace, (workspace.data_ptr(), workspace.numel()) if workspace is not None else (None, 0)
+
+
+def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, *, scale: float = 1.0,
+                   top: int = 0, workspace: torch.Tensor | None = None,
+                   check: bool = False) -> TokenLogprobs:
+    """Log probabilities of `targets` under softmax(scale * logits), with entropies and the
+    `top` most likely tokens of each row (see ewg_token_logprobs in include/ewg.h).
+
+    logits: [*targets.shape, vocab], bf16 or fp32, rows of unit inner stride; targets:
+    contiguous int32/int64.  A negative target marks a row without a token: its logprob,
+    entropy, row_max and log_sum are 0 and its alternatives missing (id -1, -inf).  Logits
+    of -inf are tokens that cannot occur.  The work is enqueued on the current stream; with
+    check=True the call waits for it and raises EwgError if a target was vocab or more
+    (whose logprob is NaN).  workspace: status_workspace(), to read the status later with
+    read_status.
+    """
+    n, V, z, stride = _logits_args("token_logprobs", logits, targets)
+    if not 0 <= top <= min(V, MAX_TOP):
+        raise ValueError(f"top must be in [0, min(vocab, {MAX_TOP})]")
+    shape = targets.shape
+    out = torch.empty((4, *shape), dtype=torch.float32, device=logits.device).unbind(0)
+    top_z = torch.empty((*shape, top), dtype=torch.float32, device=logits.device) if top else None
+    top_i = torch.empty((*shape, top), dtype=torch.int64, device=logits.device) if top else None
+    with torch.cuda.device(logits.device):
+        ws, ws_args = _status_ws(workspace, check, logits.device)
+        _raise_on(lib().ewg_token_logprobs(
+            z.data_ptr(), _FLOAT_CODES[z.dtype], stride, targets.data_ptr(),
+            _ID_CODES[targets.dtype], n, V, scale, top, *(o.data_ptr() for o in out),
+            top_z.data_ptr() if top else None, top_i.data_ptr() if top else None, *ws_args,
+            _stream_ptr(logits.device)))
+        if check and n:
+            raise_on_device_status(ws)
+    return TokenLogprobs(*out, top_z, top_i)
+
+
+def token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor, row_max: torch.Tensor,
+                            log_sum: torch.Tensor, grad_logprobs: torch.Tensor, *,
+                            entropy: torch.Tensor | None = None,
+                            grad_entropy: torch.Tensor | None = None, scale: float = 1.0,
+                            out: torch.Tensor | None = None,
+                            workspace: torch.Tensor | None = None,
+                            check: bool = False) -> torch.Tensor:
+    """The gradient of token_logprobs' logprobs (and, with grad_entropy, entropies) with
+    respect to the logits, in the logits' dtype (see ewg_token_logprobs_backward in
+    include/ewg.h).
+
+    row_max, log_sum and entropy are what token_logprobs returned for these logits, targets
+    and scale; grad_logprobs and grad_entropy are fp32 of the targets' shape (entropy is only
+    read with grad_entropy).  out: where to write; out=logits replaces the logits.  Without
+    it the gradient is allocated, with the logits' row padding where that is less than an
+    eighth of a row.  Padding rows get zeros.
+    """
+    n, V, z, stride = _logits_args("token_logprobs_backward", logits, targets)
+    if grad_entropy is not None and entropy is None:
+        raise ValueError("grad_entropy needs the forward call's entropy")
+    stats = [row_max, log_sum, grad_logprobs] + ([entropy, grad_entropy] if grad_entropy is not None else [])
+    for t in stats:
+        if t.shape != targets.shape or t.dtype != torch.float32 or t.device != logits.device \
+                or not t.is_contiguous():
+            raise ValueError("row_max, log_sum, entropy and the incoming gradients must be contiguous "
+                             "fp32 tensors of the targets' shape on the logits' device")
+    if out is None:
+        # rows placed like the logits' rows, so that both are read and written in whole vectors
+        pitch = stride if V <= stride <= V + V // 8 else V
+        out = torch.empty((*targets.shape, pitch), dtype=logits.dtype, device=logits.device)[..., :V]
+    elif out.shape != logits.shape or out.dtype != logits.dtype or out.device != logits.device:
+        raise ValueError("out must have the logits' shape, dtype and device")
+    g, g_stride = _rows("token_logprobs_backward", "out", out, n, V)
+    with torch.cuda.device(logits.device):
+        ws, ws_args = _status_ws(workspace, check, logits.device)
+        _raise_on(lib().ewg_token_logprobs_backward(
+            z.data_ptr(), _FLOAT_CODES[z.dtype], stride, targets.data_ptr(),
+            _ID_CODES[targets.dtype], n, V, scale, row_max.data_ptr(), log_sum.data_ptr(),
+            entropy.data_ptr() if grad_entropy is not None else None, grad_logprobs.data_ptr(),
+            grad_entropy.data_ptr() if grad_entropy is not None else None, g.data_ptr(), g_stride,
+            *ws_args, _stream_ptr(logits.device)))
+        if check and n:
+            raise_on_device_status(ws)
+    return out

@@ -10,20 +10,14 @@
 
 #include "ewg.h"
 #include "ewg_debug.h"
+#include "ewg_host.cuh"
 #include "ewg_internal.cuh"
 
 namespace {
 
 thread_local std::string g_last_error;
 
-int fail(int code, const std::string& msg) {
-  g_last_error = msg;
-  return code;
-}
-
-int cuda_fail(cudaError_t e, const char* what) {
-  return fail(EWG_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
-}
+using namespace ewg::host;
 
 constexpr int kMaxDevices = 64;
 
@@ -37,57 +31,6 @@ struct DeviceState {
 
 std::mutex g_mu;
 DeviceState g_devices[kMaxDevices];
-
-// SM count of the current device; configures the kernels once per device.
-int current_device(int* dev, int* num_sms) {
-  cudaError_t e = cudaGetDevice(dev);
-  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-  if (*dev < 0 || *dev >= kMaxDevices) return fail(EWG_ERR_CUDA, "device index out of range");
-  std::lock_guard<std::mutex> lock(g_mu);
-  DeviceState& d = g_devices[*dev];
-  if (!d.ready) {
-    e = cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, *dev);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
-    e = ewg::prepare_kernels();
-    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
-    d.ready = true;
-  }
-  *num_sms = d.num_sms;
-  return EWG_OK;
-}
-
-bool on_device(const void* p, int dev) {
-  cudaPointerAttributes at;
-  if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
-    cudaGetLastError();  // clear the sticky-free error of a foreign pointer
-    return false;
-  }
-  return (at.type == cudaMemoryTypeDevice || at.type == cudaMemoryTypeManaged) && at.device == dev;
-}
-
-size_t elem_size(int dtype) {
-  switch (dtype) {
-    case EWG_INT32: return 4;
-    case EWG_INT64: return 8;
-    case EWG_BF16: return 2;
-    case EWG_FP32: return 4;
-    default: return 0;
-  }
-}
-
-bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-
-struct Range {
-  uintptr_t lo, hi;
-};
-
-Range span(const void* p, int64_t rows, int64_t cols, int64_t row_stride, size_t es) {
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  const uintptr_t bytes = rows > 0 ? (static_cast<uintptr_t>(rows - 1) * row_stride + cols) * es : 0;
-  return {lo, lo + bytes};
-}
-
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
 
 int check_sizes(int64_t n, int64_t V, int64_t H) {
   if (n < EWG_MIN_TOKENS || n > EWG_MAX_TOKENS)
@@ -275,6 +218,24 @@ bool pinned_host(const void* p) {
 }  // namespace
 
 void ewg::set_last_error(const char* msg) { g_last_error = msg; }
+
+// SM count of the current device; configures the kernels once per device.
+int ewg::host::current_device(int* dev, int* num_sms) {
+  cudaError_t e = cudaGetDevice(dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  if (*dev < 0 || *dev >= kMaxDevices) return fail(EWG_ERR_CUDA, "device index out of range");
+  std::lock_guard<std::mutex> lock(g_mu);
+  DeviceState& d = g_devices[*dev];
+  if (!d.ready) {
+    e = cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, *dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
+    e = ewg::prepare_kernels();
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+    d.ready = true;
+  }
+  *num_sms = d.num_sms;
+  return EWG_OK;
+}
 
 extern "C" {
 

@@ -1,0 +1,693 @@
+// Token log probabilities, entropies and best alternatives of rows of logits, and the
+// gradient of the first two.
+//
+// Per row z[0..V) with token t and scale s > 0: m = max z, x_v = s (z_v - m),
+//
+//     1 + R = sum_v exp(x_v)          (R leaves out one occurrence of the maximum)
+//     log_sum = log1p(R)
+//     log p_v = x_v - log_sum
+//     entropy = log_sum - (sum_v exp(x_v) x_v) / (1 + R)
+//
+// and for the gradients G of log p_t and E of the entropy
+//
+//     dz_v = s (G ([v = t] - p_v) - E p_v (log p_v + entropy)).
+//
+// Keeping the maximum's own term (exactly 1) out of the sum keeps the digits of the other
+// terms where a row is all but sure of one token: log p_t and the entropy of such a row are
+// about -R, and 1 + R in 32 bits would round R away.
+//
+// Both kernels are bound by the one read of the logits (and the one write of the gradient).
+#include <cfloat>
+
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+
+#include "ewg.h"
+#include "ewg_internal.cuh"
+#include "ewg_ops.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace ewg {
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// Exponents (base 2) are clamped here: 2^-200 is 0 in 32 bits, and 0 * -200 is 0 where
+// 0 * -inf (a masked logit) would be NaN.
+constexpr float kLowestExponent = -200.0f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// max that returns NaN if either is NaN (a NaN logit must reach the sums)
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+// Two 32-bit operations in one instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mov.b64 w, {%6, %7};\n\tfma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
+// 16 bytes of a row of T: kE elements.
+template <typename T>
+struct Vec;
+
+template <>
+struct Vec<__nv_bfloat16> {
+  static constexpr int kE = 8;
+  static constexpr uint32_t kNegInf = 0xff80ff80u;
+  static __device__ __forceinline__ float2 pair(uint4 v, int i) {
+    const uint32_t u = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  }
+  static __device__ __forceinline__ uint4 elementwise_max(uint4 a, uint4 b) {
+    return make_uint4(max2(a.x, b.x), max2(a.y, b.y), max2(a.z, b.z), max2(a.w, b.w));
+  }
+  static __device__ __forceinline__ float max_of(uint4 a) {
+    const uint32_t u = max2(max2(a.x, a.y), max2(a.z, a.w));
+    return fmaxf(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  }
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  }
+  static __device__ __forceinline__ uint4 pack(const float2* g) {
+    uint4 o;
+    uint32_t* w = &o.x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(g[i].y), "f"(g[i].x));
+    return o;
+  }
+  static __device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+  static __device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+};
+
+template <>
+struct Vec<float> {
+  static constexpr int kE = 4;
+  static constexpr uint32_t kNegInf = 0xff800000u;
+  static __device__ __forceinline__ float2 pair(uint4 v, int i) {
+    return i == 0 ? make_float2(__uint_as_float(v.x), __uint_as_float(v.y))
+                  : make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
+  }
+  static __device__ __forceinline__ uint4 elementwise_max(uint4 a, uint4 b) {
+    return make_uint4(max1(a.x, b.x), max1(a.y, b.y), max1(a.z, b.z), max1(a.w, b.w));
+  }
+  static __device__ __forceinline__ float max_of(uint4 a) {
+    return __uint_as_float(max1(max1(a.x, a.y), max1(a.z, a.w)));
+  }
+  static __device__ __forceinline__ uint32_t max1(uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }
+  static __device__ __forceinline__ uint4 pack(const float2* g) {
+    return make_uint4(__float_as_uint(g[0].x), __float_as_uint(g[0].y), __float_as_uint(g[1].x),
+                      __float_as_uint(g[1].y));
+  }
+  static __device__ __forceinline__ float load1(const float* p) { return *p; }
+  static __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
+};
+
+// Streaming 16-byte load: every logit is read once by the main loops.
+__device__ __forceinline__ uint4 load16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
+// Unsigned numbers in the order of the floats (-0 is first made +0).
+__device__ __forceinline__ uint32_t order_of(float f) {
+  const uint32_t u = __float_as_uint(f + 0.0f);
+  return u ^ (static_cast<uint32_t>(static_cast<int>(u) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float float_of(uint32_t o) {
+  return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
+  return v;
+}
+
+__device__ __forceinline__ long long target_of(const void* targets, int is64, long long row) {
+  return is64 ? static_cast<const long long*>(targets)[row] : static_cast<const int*>(targets)[row];
+}
+
+// Writes the call's device status: EWG_ERR_ID_OUT_OF_RANGE if a target is V or more.
+// Run by all `threads` threads of one block.
+__device__ void report_targets(const void* targets, int is64, int n, int V, int* status, int threads) {
+  bool bad = false;
+  constexpr int kU = 8;
+  for (long long i = threadIdx.x; i < n; i += static_cast<long long>(threads) * kU) {
+    long long t[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const long long at = i + static_cast<long long>(u) * threads;
+      t[u] = at < n ? target_of(targets, is64, at) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) bad |= t[u] >= V;
+  }
+  bad = __syncthreads_or(bad);
+  if (threadIdx.x == 0) *status = bad ? kStatusBadId : kStatusOk;
+}
+
+// A row's (or a slice's) statistics: maximum, the sum of the other terms relative to it (-1
+// where there is no finite logit: the terms then add up to 1 + R = 0), and the sum of
+// term * exponent (base 2).
+struct Stats {
+  float m, R, T;
+};
+
+// The list of a warp's best candidates: lane l holds the l-th best key.  Keys order by
+// logit, then by lower id; 0 is "none".
+__device__ __forceinline__ unsigned long long key_of(float z, uint32_t id) {
+  return (static_cast<unsigned long long>(order_of(z)) << 32) | (~id);
+}
+
+// Inserts the keys of all lanes (0: nothing) that belong among the best `top`.
+__device__ __forceinline__ void insert_keys(unsigned long long& list, unsigned long long& worst,
+                                            unsigned long long key, int top, int lane) {
+  unsigned mask = __ballot_sync(kAll, key > worst);
+  while (mask) {
+    const int src = __ffs(mask) - 1;
+    mask &= mask - 1;
+    const unsigned long long k = __shfl_sync(kAll, key, src);
+    if (k <= worst) continue;                       // the list has improved meanwhile
+    const int pos = __popc(__ballot_sync(kAll, list > k));
+    const unsigned long long above = __shfl_up_sync(kAll, list, 1);
+    list = lane < pos ? list : lane == pos ? k : above;
+    worst = __shfl_sync(kAll, list, top - 1);
+  }
+}
+
+constexpr int kBatch = 4;            // vectors a thread has in flight
+
+template <int kT>
+struct GroupSmem {
+  static constexpr int kWarps = kT / 32;
+  unsigned long long lists[kWarps][kMaxTop];
+  uint32_t maxima[kT];               // order_of the threads' maxima
+  uint32_t tau;
+  int num_tasks;
+  uint16_t tasks[kT];
+  uint32_t warp_max[kWarps];
+  float warp_s[kWarps], warp_t[kWarps], warp_own[kWarps];
+  int warp_holds[kWarps];            // whether the warp has the maximum
+  int warp_owner[kWarps];            // the thread held out, -1: an edge element or none
+  float own_again;
+  // what the other blocks of the cluster read
+  Stats stats;
+  unsigned long long best[kMaxTop];
+};
+
+// Forward kernel.  kT threads take a row (kT = 32: a warp, eight rows to a block; else one
+// block), or with a cluster of C blocks each block takes 1/C of it and block 0 joins the
+// results through distributed shared memory.
+//
+// One pass over the row: each thread keeps a running maximum, the sum of exponentials and
+// the sum of exponential * exponent over its vectors, rescaled once per batch of kBatch
+// vectors.  The alternatives cost the pass nothing: afterwards the top-th largest of the
+// threads' maxima bounds the row's top-th largest logit from below, and only threads whose
+// maximum reaches it (about `top` of them) can hold one; their vectors are read again (from
+// L2), a warp to a thread's vectors.  In the same way the vectors of the thread that holds the
+// maximum are summed again without it where its own term would drown the others (R < 8).
+template <typename T, int kT>
+__global__ void __launch_bounds__(kT == 32 ? 256 : kT) logprobs_kernel(const LogprobsArgs a) {
+  using V = Vec<T>;
+  constexpr int kE = V::kE;
+  constexpr int kGroups = kT == 32 ? 8 : 1;
+  constexpr int kWarps = kT / 32;
+  __shared__ GroupSmem<kT> smem_all[kGroups];
+  const int group = kT == 32 ? threadIdx.x / 32 : 0;
+  GroupSmem<kT>& sm = smem_all[group];
+  const int tid = kT == 32 ? threadIdx.x % 32 : threadIdx.x;
+  const int lane = tid % 32, warp = tid / 32;
+  auto sync = [] {
+    if constexpr (kT == 32) __syncwarp(); else __syncthreads();
+  };
+  int C = 1, rank = 0;
+  if constexpr (kT == 512) {
+    C = cg::this_cluster().num_blocks();
+    rank = cg::this_cluster().block_rank();
+  }
+
+  long long row = static_cast<long long>(blockIdx.x / C) * kGroups + group;
+  if (a.status && blockIdx.x == 0) report_targets(a.targets, a.targets_int64, a.n, a.V, a.status, blockDim.x);
+  if (row >= a.n) return;
+  const long long target = target_of(a.targets, a.targets_int64, row);
+  const int top = a.top;
+  if (target < 0) {                  // padding: the logits are not read
+    if (rank == 0) {
+      if (tid == 0) {
+        a.logprobs[row] = 0.0f;
+        a.entropy[row] = 0.0f;
+        a.row_max[row] = 0.0f;
+        a.log_sum[row] = 0.0f;
+      }
+      if (tid < top) {
+        a.top_logprobs[row * top + tid] = -INFINITY;
+        a.top_ids[row * top + tid] = -1;
+      }
+    }
+    return;
+  }
+  const T* z = static_cast<const T*>(a.logits) + row * a.row_stride;
+  float z_target = NAN;              // of a target outside [0, V)
+  if (rank == 0 && warp == 0 && target < a.V) z_target = V::load1(z + target);
+
+  // The row is `head` elements up to the first 16-byte boundary, nv whole vectors, and a
+  // tail; the up to 2 (kE - 1) elements outside the vectors go to the lanes of warp 0.
+  const int head = min(static_cast<int>((16 - reinterpret_cast<uintptr_t>(z) % 16) % 16 / sizeof(T)), a.V);
+  const int nv = (a.V - head) / kE;
+  const int edges = rank == 0 ? a.V - nv * kE : 0;
+  const uint4* zv = reinterpret_cast<const uint4*>(z + head);
+  const int per = (nv + C - 1) / C;
+  const int v0 = min(rank * per, nv), v1 = min(v0 + per, nv);
+  int edge_id = 0;
+  float edge = -INFINITY;
+  if (warp == 0 && lane < edges) {
+    edge_id = lane < head ? lane : nv * kE + lane;
+    edge = V::load1(z + edge_id);
+  }
+
+  const float c = a.scale_log2;
+  const float2 c2 = make_float2(c, c);
+  float m = -FLT_MAX;
+  float2 S2 = make_float2(0.f, 0.f), T2 = make_float2(0.f, 0.f);
+  for (int v = v0 + tid; v < v1; v += kT * kBatch) {
+    uint4 r[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      r[u] = v + u * kT < v1 ? load16(zv + v + u * kT)
+                             : make_uint4(V::kNegInf, V::kNegInf, V::kNegInf, V::kNegInf);
+    uint4 mx = r[0];
+#pragma unroll
+    for (int u = 1; u < kBatch; ++u) mx = V::elementwise_max(mx, r[u]);
+    const float m_new = fmaxf(m, V::max_of(mx));
+    const float d = fmaxf((m - m_new) * c, -1000.0f);
+    const float f = ex2(d);
+    m = m_new;
+    T2 = mul2(make_float2(f, f), fma2(make_float2(d, d), S2, T2));
+    S2 = mul2(make_float2(f, f), S2);
+    const float2 minus_m = make_float2(-m, -m);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+#pragma unroll
+      for (int i = 0; i < kE / 2; ++i) {
+        float2 t = mul2(add2(V::pair(r[u], i), minus_m), c2);
+        t.x = max_nan(t.x, kLowestExponent);
+        t.y = max_nan(t.y, kLowestExponent);
+        const float2 e = make_float2(ex2(t.x), ex2(t.y));
+        S2 = add2(S2, e);
+        T2 = fma2(e, t, T2);
+      }
+    }
+  }
+
+  // ---- the group's maximum
+  uint32_t om = __reduce_max_sync(kAll, order_of(warp == 0 ? fmaxf(m, edge) : m));
+  if (top) sm.maxima[tid] = order_of(m);
+  if constexpr (kWarps > 1) {
+    if (lane == 0) sm.warp_max[warp] = om;
+    if (tid == 0) sm.num_tasks = 0;
+    sync();
+    om = __reduce_max_sync(kAll, lane < kWarps ? sm.warp_max[lane] : 0u);
+  } else {
+    if (tid == 0) sm.num_tasks = 0;
+    sync();
+  }
+  const float M = fmaxf(float_of(om), -FLT_MAX);
+
+  // ---- its sums.  Each warp that has the maximum holds one occurrence out: an edge
+  // element's whole term, or 1 off the sum of its first thread that has it.
+  float s, t;
+  {
+    const float d = fmaxf((m - M) * c, -1000.0f);
+    const float f = ex2(d);
+    const float S = S2.x + S2.y;
+    s = S * f;
+    t = f * (T2.x + T2.y + d * S);
+  }
+  const unsigned edge_has = __ballot_sync(kAll, warp == 0 && edge == M);
+  const unsigned has = __ballot_sync(kAll, m == M);
+  const int owner = has && !edge_has ? __ffs(has) - 1 : -1;     // lane of the thread held out
+  float own = owner >= 0 ? __shfl_sync(kAll, s, owner) - 1.0f : 0.0f;
+  if (lane == owner) s = 0.0f;
+  if (warp == 0 && lane < edges) {
+    const float x = max_nan((edge - M) * c, kLowestExponent);
+    const float e = ex2(x);
+    s += edge_has && lane == __ffs(edge_has) - 1 ? 0.0f : e;
+    t += e * x;
+  }
+  s = warp_sum(s);
+  t = warp_sum(t);
+  int owner_tid = owner >= 0 ? warp * 32 + owner : -1;
+  if constexpr (kWarps > 1) {
+    if (lane == 0) {
+      sm.warp_s[warp] = s;
+      sm.warp_t[warp] = t;
+      sm.warp_own[warp] = own;
+      sm.warp_holds[warp] = has || edge_has;
+      sm.warp_owner[warp] = owner_tid;
+    }
+    sync();
+    // the first warp that has the maximum holds it out; the other warps' occurrences count
+    const bool in = lane < kWarps;
+    const int first = __ffs(__ballot_sync(kAll, in && sm.warp_holds[lane])) - 1;
+    s = warp_sum(in ? sm.warp_s[lane] + (sm.warp_holds[lane] && lane != first ? 1.0f + sm.warp_own[lane] : 0.0f)
+                    : 0.0f);
+    t = warp_sum(in ? sm.warp_t[lane] : 0.0f);
+    own = sm.warp_own[first];
+    owner_tid = sm.warp_owner[first];
+  }
+  if (s + own < 8.0f && owner_tid >= 0) {   // the same in every thread of the group
+    if (warp == owner_tid / 32) {
+      float r = 0.0f, equal = 0.0f;
+      for (int v = v0 + owner_tid + lane * kT; v < v1; v += 32 * kT) {
+        const uint4 raw = load16(zv + v);
+#pragma unroll
+        for (int i = 0; i < kE / 2; ++i) {
+          const float2 p = V::pair(raw, i);
+          if (p.x == M) equal += 1.0f; else r += ex2(max_nan((p.x - M) * c, kLowestExponent));
+          if (p.y == M) equal += 1.0f; else r += ex2(max_nan((p.y - M) * c, kLowestExponent));
+        }
+      }
+      own = warp_sum(r) + (warp_sum(equal) - 1.0f);
+      if (lane == 0) sm.own_again = own;
+    }
+    if constexpr (kWarps > 1) {
+      sync();
+      own = sm.own_again;
+    }
+  }
+  Stats st{M, s + own, t};
+
+  // ---- the group's best candidates
+  unsigned long long list = 0, worst = 0;
+  if (top) {
+    // tau: the top-th largest of the threads' maxima
+    sync();
+    if (warp == 0) {
+      uint32_t mine[kWarps], best = 0;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) {
+        mine[i] = sm.maxima[i * 32 + lane];
+        best = max(best, mine[i]);
+      }
+      int left = top;
+      uint32_t tau;
+      while (true) {
+        tau = __reduce_max_sync(kAll, best);
+        int equal = 0;
+        uint32_t next = 0;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+          equal += mine[i] == tau;
+          if (mine[i] < tau) next = max(next, mine[i]);
+        }
+        left -= __reduce_add_sync(kAll, equal);
+        if (left <= 0) break;
+        if (best == tau) best = next;               // the lane's next smaller distinct value
+        if (__reduce_max_sync(kAll, best) == 0) break;   // fewer threads than alternatives
+      }
+      if (lane == 0) sm.tau = tau;
+    }
+    sync();
+    const uint32_t tau = sm.tau;
+    const float tau_f = float_of(tau);
+    if (order_of(m) >= tau) sm.tasks[atomicAdd(&sm.num_tasks, 1)] = static_cast<uint16_t>(tid);
+    sync();
+    const int tasks = sm.num_tasks;
+    for (int i = warp; i < tasks; i += kWarps) {
+      for (int vb = v0 + sm.tasks[i]; vb < v1; vb += 32 * kT) {
+        const int v = vb + lane * kT;
+        const uint4 raw = v < v1 ? load16(zv + v) : make_uint4(V::kNegInf, V::kNegInf, V::kNegInf, V::kNegInf);
+        if (!__any_sync(kAll, V::max_of(raw) >= tau_f)) continue;
+        const uint32_t id = head + v * kE;
+#pragma unroll
+        for (int e = 0; e < kE; ++e) {
+          const float2 p = V::pair(raw, e / 2);
+          const float x = e % 2 ? p.y : p.x;
+          insert_keys(list, worst, x >= tau_f ? key_of(x, id + e) : 0ull, top, lane);
+        }
+      }
+    }
+    if (warp == 0) insert_keys(list, worst, edge >= -FLT_MAX ? key_of(edge, edge_id) : 0ull, top, lane);
+    if constexpr (kWarps > 1) {
+      if (lane < top) sm.lists[warp][lane] = list;
+      sync();
+      if (warp == 0) {
+        for (int w = 1; w < kWarps; ++w) insert_keys(list, worst, lane < top ? sm.lists[w][lane] : 0ull, top, lane);
+      }
+    }
+  }
+
+  // ---- the cluster's blocks joined, in the order of their slices
+  if constexpr (kT == 512) {
+    if (C > 1) {
+      cg::cluster_group cluster = cg::this_cluster();
+      if (tid == 0) sm.stats = st;
+      if (warp == 0 && lane < top) sm.best[lane] = list;
+      cluster.sync();
+      if (rank == 0 && warp == 0) {
+        Stats other{-FLT_MAX, -1.0f, 0.0f};
+        if (lane < C) other = *cluster.map_shared_rank(&sm.stats, lane);
+        const float Mg = float_of(__reduce_max_sync(kAll, order_of(other.m)));
+        const int first = __ffs(__ballot_sync(kAll, other.m == Mg)) - 1;
+        const float d = fmaxf((other.m - Mg) * c, -1000.0f);
+        const float f = ex2(d);
+        const float r = warp_sum(lane == first ? other.R : f * (1.0f + other.R));
+        const float tt = warp_sum(f * (other.T + d * (1.0f + other.R)));
+        st = Stats{Mg, r, tt};
+        for (int q = 1; q < C && top; ++q) {
+          const unsigned long long* theirs = cluster.map_shared_rank(&sm.best[0], q);
+          insert_keys(list, worst, lane < top ? theirs[lane] : 0ull, top, lane);
+        }
+      }
+      cluster.sync();                // the blocks' shared memory stays until it has been read
+      if (rank != 0) return;
+    }
+  }
+
+  // ---- outputs
+  if (warp != 0) return;
+  const bool empty = st.R == -1.0f;  // no finite logit
+  const float log_sum = empty ? 0.0f : log1pf(st.R);
+  if (lane == 0) {
+    a.logprobs[row] = target >= a.V ? NAN : empty ? -INFINITY : (z_target - st.m) * a.scale - log_sum;
+    a.entropy[row] = empty ? 0.0f : log_sum - st.T * kLn2 / (1.0f + st.R);
+    a.row_max[row] = empty ? -INFINITY : st.m;
+    a.log_sum[row] = log_sum;
+  }
+  if (lane < top) {
+    a.top_logprobs[row * top + lane] =
+        list ? (float_of(static_cast<uint32_t>(list >> 32)) - st.m) * a.scale - log_sum : -INFINITY;
+    a.top_ids[row * top + lane] = list ? static_cast<long long>(~static_cast<uint32_t>(list)) : -1;
+  }
+}
+
+// Gradient kernel: kT threads take kBatch * kT vectors of a row (kT = 32: a warp, eight
+// items to a block).  Items of one row are neighbours.  The vectors are the 16-byte ones of
+// the gradient's row; a logits row of another alignment is read as two vectors each, put
+// together in registers.
+//
+// With y = log2 p_v, dz_v = p_v (A + B y), A = -s (G + E entropy), B = -s E ln 2; the row's
+// token itself takes G (-expm1(log p)) for G (1 - p).
+template <typename T, int kT>
+__global__ void __launch_bounds__(256) logprobs_grad_kernel(const LogprobsGradArgs a, int items_per_row) {
+  using V = Vec<T>;
+  constexpr int kE = V::kE;
+  constexpr int kGroups = 256 / kT;
+  if (a.status && blockIdx.x == 0) report_targets(a.targets, a.targets_int64, a.n, a.V, a.status, blockDim.x);
+  const long long item = static_cast<long long>(blockIdx.x) * kGroups + threadIdx.x / kT;
+  const int tid = threadIdx.x % kT;
+  const long long row = item / items_per_row;
+  if (row >= a.n) return;
+  const int part = static_cast<int>(item - row * items_per_row);
+
+  const long long target = target_of(a.targets, a.targets_int64, row);
+  const float m = a.row_max[row];
+  const bool zero = target < 0 || target >= a.V || m == -INFINITY;
+  const float log_sum = a.log_sum[row];
+  const float G = a.grad_logprobs[row];
+  const float E = a.grad_entropy ? a.grad_entropy[row] : 0.0f;
+  const float H = a.grad_entropy ? a.entropy[row] : 0.0f;
+  const float c = a.scale_log2;
+  const float minus_ls2 = -log_sum * kLog2e;
+  const float A = -a.scale * (G + E * H), B = -a.scale * E * kLn2;
+
+  T* g = static_cast<T*>(a.grad) + row * a.grad_stride;
+  const T* z = static_cast<const T*>(a.logits) + row * a.row_stride;
+  const int head = min(static_cast<int>((16 - reinterpret_cast<uintptr_t>(g) % 16) % 16 / sizeof(T)), a.V);
+  const int nv = (a.V - head) / kE;
+
+  auto one = [&](float x, int id) {  // the gradient of one element
+    const float y = max_nan(fmaf(x - m, c, minus_ls2), kLowestExponent);
+    const float p = ex2(y);
+    if (id != static_cast<int>(target)) return p * fmaf(B, y, A);
+    const float lp = (x - m) * a.scale - log_sum;
+    return a.scale * (-G * expm1f(lp)) - (E != 0.0f ? a.scale * E * p * (fmaxf(lp, -1e30f) + H) : 0.0f);
+  };
+
+  if (part == 0) {                   // the elements outside the vectors
+    const int edges = a.V - nv * kE;
+    if (tid < edges) {
+      const int id = tid < head ? tid : nv * kE + tid;
+      V::store1(g + id, zero ? 0.0f : one(V::load1(z + id), id));
+    }
+  }
+  uint4* gv = reinterpret_cast<uint4*>(g + head);
+  const int v_begin = part * kT * kBatch + tid;
+  if (zero) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (v_begin + u * kT < nv) gv[v_begin + u * kT] = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  const T* zb = z + head;
+  const unsigned shift = reinterpret_cast<uintptr_t>(zb) % 16;
+  uint4 r[kBatch];
+  if (shift == 0) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (v_begin + u * kT < nv) r[u] = load16(reinterpret_cast<const uint4*>(zb) + v_begin + u * kT);
+  } else {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int v = v_begin + u * kT;
+      if (v >= nv) continue;
+      if (v == 0 || v == nv - 1) {   // the aligned vectors around these may leave the row
+        float2 x[kE / 2];
+#pragma unroll
+        for (int i = 0; i < kE / 2; ++i)
+          x[i] = make_float2(V::load1(zb + v * kE + 2 * i), V::load1(zb + v * kE + 2 * i + 1));
+        r[u] = V::pack(x);           // exact: the values are of type T
+      } else {
+        const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(zb + static_cast<long long>(v) * kE) - shift);
+        const uint4 lo = p[0], hi = p[1];
+        uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        if (shift & 8) {
+#pragma unroll
+          for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+        }
+        if (shift & 4) {
+#pragma unroll
+          for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+        }
+        const unsigned bits = (shift & 3) * 8;
+        r[u] = make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                          __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+      }
+    }
+  }
+  const float2 minus_m = make_float2(-m, -m), c2 = make_float2(c, c), ls2 = make_float2(minus_ls2, minus_ls2);
+  const float2 A2 = make_float2(A, A), B2 = make_float2(B, B);
+#pragma unroll
+  for (int u = 0; u < kBatch; ++u) {
+    const int v = v_begin + u * kT;
+    if (v >= nv) continue;
+    float2 out[kE / 2];
+#pragma unroll
+    for (int i = 0; i < kE / 2; ++i) {
+      float2 y = fma2(add2(V::pair(r[u], i), minus_m), c2, ls2);
+      y.x = max_nan(y.x, kLowestExponent);
+      y.y = max_nan(y.y, kLowestExponent);
+      out[i] = mul2(make_float2(ex2(y.x), ex2(y.y)), fma2(B2, y, A2));
+    }
+    const long long e = target - head - static_cast<long long>(v) * kE;
+    if (e >= 0 && e < kE) {          // the vector that holds the token
+      float* o = &out[0].x;
+      const float x = V::load1(zb + static_cast<long long>(v) * kE + e);
+      const float val = one(x, static_cast<int>(target));
+#pragma unroll
+      for (int i = 0; i < kE; ++i)
+        if (i == e) o[i] = val;
+    }
+    gv[v] = V::pack(out);
+  }
+}
+
+template <typename T, int kT>
+cudaError_t launch_forward(const LogprobsArgs& a, int cluster, cudaStream_t stream) {
+  constexpr int kGroups = kT == 32 ? 8 : 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<long long>(a.n) * cluster + kGroups - 1) / kGroups));
+  cfg.blockDim = dim3(kT * kGroups);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  if (cluster > 1) {
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = cluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+  }
+  return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, kT>, a);
+}
+
+template <typename T>
+cudaError_t launch_forward_of(const LogprobsArgs& a, int num_sms, cudaStream_t stream) {
+  const int nv = a.V / Vec<T>::kE;
+  if (nv <= 512) return launch_forward<T, 32>(a, 1, stream);
+  if (nv <= 2048 && a.n >= num_sms) return launch_forward<T, 128>(a, 1, stream);
+  // few rows: up to 8 blocks a row, each thread with a vector at least
+  int cluster = 1;
+  while (cluster < 8 && static_cast<long long>(a.n) * cluster < num_sms && nv / (2 * cluster) >= 512) cluster *= 2;
+  return launch_forward<T, 512>(a, cluster, stream);
+}
+
+template <typename T>
+cudaError_t launch_grad_of(const LogprobsGradArgs& a, cudaStream_t stream) {
+  const int nv = a.V / Vec<T>::kE + 1;
+  const bool narrow = nv <= 32 * kBatch * 4;
+  const int kT = narrow ? 32 : 256, groups = 256 / kT;
+  const int items = (nv + kT * kBatch - 1) / (kT * kBatch);
+  const long long blocks = (static_cast<long long>(a.n) * items + groups - 1) / groups;
+  if (narrow) logprobs_grad_kernel<T, 32><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a, items);
+  else logprobs_grad_kernel<T, 256><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a, items);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t prepare_logprobs() { return cudaSuccess; }
+
+cudaError_t launch_logprobs(const LogprobsArgs& a, bool bf16, int num_sms, cudaStream_t stream) {
+  return bf16 ? launch_forward_of<__nv_bfloat16>(a, num_sms, stream) : launch_forward_of<float>(a, num_sms, stream);
+}
+
+cudaError_t launch_logprobs_grad(const LogprobsGradArgs& a, bool bf16, cudaStream_t stream) {
+  return bf16 ? launch_grad_of<__nv_bfloat16>(a, stream) : launch_grad_of<float>(a, stream);
+}
+
+}  // namespace ewg

@@ -257,6 +257,71 @@ int ewg_accumulate_static(const void* ids, int ids_dtype, int64_t num_tokens,
                           int64_t num_embeddings, int64_t hidden,
                           int64_t main_grad_row_stride, void* stream, void** scratch_out);
 
+/* Most alternatives ewg_token_logprobs returns per row. */
+#define EWG_MAX_TOP 32
+
+/*
+ * Log probabilities of given tokens under rows of logits, with the entropy of each row's
+ * distribution and its most likely tokens.  Per row z[0..vocab) with token t,
+ * m = max z, x_v = scale (z_v - m), and R the sum of exp(x_v) without one occurrence of
+ * the maximum:
+ *
+ *     log_sum = log1p(R)         logprobs = x_t - log_sum
+ *     entropy = log_sum - sum_v exp(x_v) x_v / (1 + R)         row_max = m
+ *     top_ids, top_logprobs: the `top` largest logits, best first, equal ones by lower id
+ *
+ * in 32 bits, the row's sums held relative to its maximum; near-certain tokens keep the
+ * relative precision of their small -logprob and entropy.
+ *
+ *   logits    [num_tokens][vocab], EWG_BF16 or EWG_FP32, unit inner stride,
+ *             row_stride elements between rows (>= vocab; any alignment of the element)
+ *   targets   [num_tokens] contiguous, EWG_INT32 or EWG_INT64
+ *   logprobs, entropy, row_max, log_sum     [num_tokens] fp32
+ *   top_logprobs, top_ids     [num_tokens][top] fp32 and int64 (both unused for top = 0)
+ *
+ * A logit of -inf is a token that cannot occur.  A row of nothing else has log_sum 0,
+ * row_max -inf, entropy 0 and logprobs -inf; missing alternatives are id -1 at -inf.  A
+ * row with a NaN or +inf has NaN logprobs, entropy and log_sum.  A negative target marks a
+ * row without a token (padding): its logits are not read, its alternatives are missing
+ * and its other outputs are 0.  A target of vocab or more makes the row's logprobs NaN and
+ * the device status EWG_ERR_ID_OUT_OF_RANGE.
+ *
+ * Requires 0 <= num_tokens < 2^31 (0: nothing is enqueued, not even the status), 1 <= vocab < 2^31 - 64, finite
+ * scale > 0, 0 <= top <= min(vocab, EWG_MAX_TOP); outputs apart from the inputs and each
+ * other.  workspace: NULL, or 256 device bytes, 256-byte aligned, that receive the device
+ * status for ewg_read_status.  Enqueues one kernel; allocates nothing.
+ */
+int ewg_token_logprobs(const void* logits, int logits_dtype, int64_t row_stride,
+                       const void* targets, int targets_dtype, int64_t num_tokens,
+                       int64_t vocab, float scale, int top, float* logprobs, float* entropy,
+                       float* row_max, float* log_sum, float* top_logprobs, int64_t* top_ids,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The gradient of ewg_token_logprobs with respect to the logits.  With p and log p from
+ * row_max and log_sum, G = grad_logprobs and E = grad_entropy (E = 0 where it is NULL):
+ *
+ *     grad_v = scale (G ([v = t] - p_v) - E p_v (log p_v + entropy))
+ *
+ * computed in 32 bits and rounded once to the logits' dtype; at the token itself
+ * G (1 - p_t) is taken as -G expm1(log p_t).
+ *
+ * logits, targets, scale, row_max, log_sum, entropy: as given to and returned by the
+ * forward call (entropy may be NULL where grad_entropy is).  grad_logits:
+ * [num_tokens][vocab] of the logits' dtype, grad_row_stride elements between rows; either
+ * apart from every input, or the logits themselves (same address and stride), which it
+ * then replaces.  Padding rows, rows of -inf only and rows whose target is vocab or more
+ * (device status EWG_ERR_ID_OUT_OF_RANGE) get zeros.  Sizes, workspace and errors: as
+ * ewg_token_logprobs.
+ */
+int ewg_token_logprobs_backward(const void* logits, int logits_dtype, int64_t row_stride,
+                                const void* targets, int targets_dtype, int64_t num_tokens,
+                                int64_t vocab, float scale, const float* row_max,
+                                const float* log_sum, const float* entropy,
+                                const float* grad_logprobs, const float* grad_entropy,
+                                void* grad_logits, int64_t grad_row_stride, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
 /*
  * Waits for `stream`, then copies the device status of the last ewg_plan /
  * ewg_apply / ewg_accumulate that used this workspace into *status (EWG_OK,

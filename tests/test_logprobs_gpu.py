@@ -1,0 +1,377 @@
+"""token_logprobs and token_logprobs_backward against their definitions in 64 bits.
+
+Tolerances, from the operations' roundings (u = 2^-24): an exponent t = (z - m) s log2(e)
+carries at most 3 u |t|, exp2 another 2^-22, and the sum of the terms that matter has
+|t| < 40, so every term of R is within 40 * 3 u + 2^-22 < 8e-6 of its value, relatively; the
+accumulation of positive terms adds less than 2e-6 (at most 32 additions a thread, then
+trees).  So R, and with it log_sum = log1p(R) and the entropy (a sum of positive terms, each
+a multiple of such a term), are within REL = 1e-5 relatively; log p adds the roundings of x
+and of one subtraction.  A gradient's factor p has log2 p with the same error again, so its
+terms are within 2 REL of their sizes, plus the one rounding to the output's type.
+"""
+import math
+
+import pytest
+import torch
+
+import embedding_weight_grad_gb300 as ewg
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+REL = 1e-5
+U = 2.0 ** -24
+BF16, FP32 = torch.bfloat16, torch.float32
+
+
+def make(n, V, dtype, seed=0, pad=0, std=3.0, lift=12.0):
+    """Logits whose token is anything from unlikely to near certain."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    z = torch.randn(n, V, generator=g, device=DEV) * std
+    t = torch.randint(V, (n,), generator=g, device=DEV)
+    z[torch.arange(n, device=DEV), t] += torch.rand(n, generator=g, device=DEV) * lift
+    buf = torch.full((n, V + pad), float("nan"), dtype=dtype, device=DEV)
+    buf[:, :V] = z.to(dtype)
+    return buf[:, :V], t
+
+
+def reference(z, t, scale):
+    """logprobs, entropy, R, log_sum, row_max and all log p of rows with a finite logit, in 64 bits."""
+    z = z.double()
+    m = z.amax(1)
+    x = (z - m[:, None]) * scale
+    e = x.exp().scatter(1, z.argmax(1, keepdim=True), 0.0)
+    R = e.sum(1)
+    log_sum = R.log1p()
+    logp = x - log_sum[:, None]
+    xe = torch.where(e > 0, e * x, 0.0).sum(1)
+    return logp.gather(1, t.clamp_min(0).long()[:, None])[:, 0], log_sum - xe / (1 + R), R, log_sum, m, logp
+
+
+def check_forward(z, t, scale, top, r):
+    logp, entropy, R, log_sum, m, all_logp = reference(z, t, scale)
+    share = R / (1 + R)
+
+    def near(got, want, tol, what):
+        worst = ((got.double() - want).abs() - tol).max().item()
+        assert worst <= 0, (what, worst)
+    assert torch.equal(r.row_max.double(), m)
+    near(r.log_sum, log_sum, REL * share + 4 * U * log_sum, "log_sum")
+    near(r.entropy, entropy, 1.5 * REL * entropy + 1e-38, "entropy")
+    near(r.logprobs, logp, REL * share + 6 * U * logp.abs(), "logprobs")
+    if top:
+        best, ids = order(z, top)
+        assert torch.equal(r.top_ids, ids)
+        want = all_logp.gather(1, ids.clamp_min(0))
+        near(torch.where(ids >= 0, r.top_logprobs, 0.0), torch.where(ids >= 0, want, 0.0),
+             REL * share[:, None] + torch.where(ids >= 0, 6 * U * want.abs(), 0.0), "top")
+        assert bool((r.top_logprobs[ids < 0] == -math.inf).all())
+
+
+def order(z, top):
+    """The `top` largest by a stable sort (equal logits by lower id); id -1 past the finite ones."""
+    v, ids = torch.sort(z.double() + 0.0, dim=1, descending=True, stable=True)
+    v, ids = v[:, :top], ids[:, :top]
+    return v, torch.where(v > -math.inf, ids, -1)
+
+
+def check_backward(z, t, scale, G, E, got):
+    """Rows with a token and a finite logit."""
+    logp, entropy, R, log_sum, m, all_logp = reference(z, t, scale)
+    p = all_logp.exp()
+    q = p.scatter(1, t.long()[:, None], logp.expm1()[:, None])
+    plogp = torch.where(p > 0, p * all_logp, 0.0)
+    want = -G.double()[:, None] * q
+    size = G.double().abs()[:, None] * q.abs()
+    if E is not None:
+        want = want - E.double()[:, None] * (plogp + p * entropy[:, None])
+        size = size + E.double().abs()[:, None] * (plogp.abs() + p * entropy[:, None])
+    tol = scale * (2 * REL * size) + 1e-37
+    if got.dtype == BF16:
+        tol = tol + scale * want.abs() * 2.0 ** -8
+    worst = ((got.double() - scale * want).abs() - tol).max().item()
+    assert worst <= 0, worst
+
+
+def both(z, t, scale=1.0, top=0, entropy=True, seed=3):
+    r = ewg.token_logprobs(z, t, scale=scale, top=top, check=True)
+    check_forward(z, t, scale, top, r)
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    G = torch.randn(t.shape, generator=g, device=DEV)
+    E = torch.randn(t.shape, generator=g, device=DEV) if entropy else None
+    got = ewg.token_logprobs_backward(z, t, r.row_max, r.log_sum, G, entropy=r.entropy,
+                                      grad_entropy=E, scale=scale, check=True)
+    check_backward(z, t, scale, G, E, got)
+    return r, got
+
+
+SIZES = [(1, 1), (1, 2), (3, 7), (5, 31), (2, 33), (9, 63), (33, 257), (300, 1000), (17, 2047), (7, 4099),
+         (200, 12345), (160, 16400), (3, 50257), (1, 129280), (2, 129283), (700, 300), (1, 256000)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("n,V", SIZES)
+def test_sizes(n, V, dtype):
+    z, t = make(n, V, dtype, seed=n + V)
+    both(z, t, top=min(V, 5))
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("pad", [1, 2, 3, 5, 8, 40])
+def test_row_strides(dtype, pad):
+    """Rows of a wider buffer (NaN between them): every alignment of a row."""
+    for n, V in [(9, 1001), (5, 20011)]:
+        z, t = make(n, V, dtype, seed=pad, pad=pad)
+        r, got = both(z, t, scale=0.7, top=3)
+        # a gradient of another alignment than the logits: the same numbers
+        for gpad in (0, 1, 4):
+            out = torch.full((n, V + gpad), 7.0, dtype=dtype, device=DEV)
+            G = torch.ones(n, device=DEV)
+            a = ewg.token_logprobs_backward(z, t, r.row_max, r.log_sum, G, scale=0.7)
+            b = ewg.token_logprobs_backward(z, t, r.row_max, r.log_sum, G, scale=0.7, out=out[:, :V])
+            assert torch.equal(a, b)
+            assert bool((out[:, V:] == 7.0).all())
+
+
+@pytest.mark.parametrize("top", [1, 2, 20, 32])
+@pytest.mark.parametrize("n,V", [(40, 33), (6, 5000), (2, 70000), (170, 9000)])
+@pytest.mark.parametrize("kind", ["equal", "ties", "rising", "falling", "zeros of both signs"])
+def test_alternatives_order(top, n, V, kind):
+    g = torch.Generator(device=DEV).manual_seed(V)
+    z = {"equal": lambda: torch.full((n, V), 1.5, device=DEV),
+         "ties": lambda: torch.randint(-3, 4, (n, V), generator=g, device=DEV).float(),
+         "rising": lambda: torch.arange(V, device=DEV).float().expand(n, V) * 2.0 ** -6,
+         "falling": lambda: -torch.arange(V, device=DEV).float().expand(n, V) * 2.0 ** -6,
+         "zeros of both signs": lambda: torch.where(torch.rand(n, V, generator=g, device=DEV) < 0.5, 0.0, -0.0)}[kind]()
+    for dtype in (BF16, FP32):
+        zz = z.to(dtype).contiguous()
+        t = torch.randint(V, (n,), generator=g, device=DEV)
+        check_forward(zz, t, 1.0, top, ewg.token_logprobs(zz, t, top=top, check=True))
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("V", [50, 3001, 30000, 140000])
+def test_masks(dtype, V):
+    """Tokens that cannot occur, masked with -inf and with the type's lowest value."""
+    z, t = make(12, V, dtype, seed=V)
+    z = z.clone()
+    g = torch.Generator(device=DEV).manual_seed(1)
+    keep = torch.rand(12, V, generator=g, device=DEV) < 0.1
+    keep.scatter_(1, t[:, None], True)
+    z[:6] = torch.where(keep[:6], z[:6], -math.inf)
+    z[6:] = torch.where(keep[6:], z[6:], torch.finfo(dtype).min)
+    z[0] = -math.inf
+    z[0, t[0]] = 2.0                                     # one token is left: certain
+    z[6] = torch.finfo(dtype).min                        # all at the lowest value: uniform
+    r, got = both(z, t, top=8)
+    assert r.logprobs[0] == 0 and r.entropy[0] == 0
+    assert int((r.top_ids[0] >= 0).sum()) == 1
+    assert bool((got[0] == 0).all())
+    assert abs(r.entropy[6].item() - math.log(V)) < 1e-5 * math.log(V)
+
+
+@pytest.mark.parametrize("V", [40, 5000, 130000])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_rows_without_anything(dtype, V):
+    """A row of -inf only, and padding rows whose logits are NaN."""
+    z, t = make(5, V, dtype)
+    z = z.clone()
+    z[1] = -math.inf
+    z[3] = math.nan
+    t[3] = -100
+    r = ewg.token_logprobs(z, t, top=4, check=True)
+    assert r.logprobs[1] == -math.inf and r.row_max[1] == -math.inf
+    assert r.entropy[1] == 0 and r.log_sum[1] == 0
+    assert r.logprobs[3] == 0 and r.entropy[3] == 0 and r.row_max[3] == 0 and r.log_sum[3] == 0
+    for row in (1, 3):
+        assert bool((r.top_ids[row] == -1).all()) and bool((r.top_logprobs[row] == -math.inf).all())
+    ones = torch.ones(5, device=DEV)
+    got = ewg.token_logprobs_backward(z, t, r.row_max, r.log_sum, ones, entropy=r.entropy,
+                                      grad_entropy=ones, check=True)
+    assert bool((got[1] == 0).all()) and bool((got[3] == 0).all())
+    rest = [0, 2, 4]
+    check_forward(z[rest], t[rest], 1.0, 4, type(r)(*(x[rest] for x in r)))
+    check_backward(z[rest], t[rest], 1.0, ones[rest], ones[rest], got[rest])
+
+
+@pytest.mark.parametrize("V", [40, 5000, 130000])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_nan_and_infinity_show(V, bad):
+    for where in (0, V // 2, V - 1):
+        z, t = make(2, V, FP32)
+        z = z.clone()
+        z[0, where] = bad
+        r = ewg.token_logprobs(z, t, top=2, check=True)
+        assert math.isnan(r.logprobs[0]) and math.isnan(r.entropy[0]) and math.isnan(r.log_sum[0])
+        got = ewg.token_logprobs_backward(z, t, r.row_max, r.log_sum, torch.ones(2, device=DEV))
+        assert bool(got[0].isnan().any())
+        check_forward(z[1:], t[1:], 1.0, 2, type(r)(*(x[1:] for x in r)))
+
+
+@pytest.mark.parametrize("V", [64, 2000, 40000, 200000])
+def test_near_certain_rows_keep_their_digits(V):
+    """One logit 10 to 60 above the others: log p, entropy and gradient of about exp(-10) to exp(-60)."""
+    for where in (0, 1, V // 3, V - 1):
+        g = torch.Generator(device=DEV).manual_seed(where)
+        z = torch.randn(6, V, generator=g, device=DEV)
+        z[:, where] = torch.tensor([14.0, 20.0, 25.0, 33.0, 50.0, 70.0], device=DEV)
+        t = torch.full((6,), where, device=DEV)
+        both(z, t)
+        t[:] = (where + 1) % V
+        both(z, t)
+
+
+@pytest.mark.parametrize("scale", [0.01, 0.5, 1.0, 2.5])
+def test_scale_and_large_offsets(scale):
+    z, t = make(20, 4000, FP32, seed=5)
+    both(z, t, scale=scale, top=2)
+    # a power-of-two offset far above the spread: the same row, shifted exactly
+    zb = (z * 64).round() / 64
+    a, b = ewg.token_logprobs(zb, t, scale=scale), ewg.token_logprobs(zb + 4096.0, t, scale=scale)
+    assert torch.equal(a.logprobs, b.logprobs) and torch.equal(a.entropy, b.entropy)
+
+
+def test_shapes_and_target_types():
+    z, t = make(6, 777, BF16, seed=9)
+    r = ewg.token_logprobs(z, t, top=3)
+    r3 = ewg.token_logprobs(z.view(2, 3, 777), t.view(2, 3).int(), top=3)
+    assert r3.logprobs.shape == (2, 3) and r3.top_ids.shape == (2, 3, 3)
+    for a, b in zip(r, r3):
+        assert torch.equal(a, b.reshape(a.shape))
+    r1 = ewg.token_logprobs(z[2], t[2], top=3)           # a single row: a scalar target
+    assert r1.logprobs.shape == () and torch.equal(r1.top_ids, r.top_ids[2])
+    G = torch.ones(2, 3, device=DEV)
+    g3 = ewg.token_logprobs_backward(z.view(2, 3, 777), t.view(2, 3).int(), r3.row_max, r3.log_sum, G)
+    g = ewg.token_logprobs_backward(z, t, r.row_max, r.log_sum, G.view(6))
+    assert g3.shape == (2, 3, 777) and torch.equal(g3.view(6, 777), g)
+    g1 = ewg.token_logprobs_backward(z[2], t[2], r1.row_max, r1.log_sum, torch.ones((), device=DEV))
+    assert g1.shape == (777,) and torch.equal(g1, g[2])
+
+
+def test_no_rows():
+    z = torch.empty(0, 100, device=DEV)
+    t = torch.empty(0, dtype=torch.int64, device=DEV)
+    r = ewg.token_logprobs(z, t, top=2, check=True)
+    assert r.logprobs.shape == (0,) and r.top_ids.shape == (0, 2)
+    e = torch.empty(0, device=DEV)
+    assert ewg.token_logprobs_backward(z, t, e, e, e, check=True).shape == (0, 100)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("pad", [0, 3])
+def test_backward_in_place(dtype, pad):
+    z, t = make(50, 5003, dtype, pad=pad)
+    r = ewg.token_logprobs(z, t)
+    G = torch.randn(50, device=DEV)
+    want = ewg.token_logprobs_backward(z, t, r.row_max, r.log_sum, G)
+    got = ewg.token_logprobs_backward(z, t, r.row_max, r.log_sum, G, out=z)
+    assert got.data_ptr() == z.data_ptr() and torch.equal(z, want)
+
+
+def test_backward_against_differences():
+    """Central differences of the 64-bit definition (truncation ~h^2 = 1e-10)."""
+    z, t = make(4, 300, FP32, seed=2, lift=4.0)
+    G, E = torch.randn(4, device=DEV), torch.randn(4, device=DEV)
+    r = ewg.token_logprobs(z, t, scale=1.25)
+    got = ewg.token_logprobs_backward(z, t, r.row_max, r.log_sum, G, entropy=r.entropy, grad_entropy=E, scale=1.25)
+
+    def loss(x):
+        logp, entropy, *_ = reference(x, t, 1.25)
+        return G.double() * logp + E.double() * entropy
+    h = 1e-5
+    for v in torch.cat([t, torch.arange(0, 300, 41, device=DEV)]).tolist():
+        step = torch.zeros(4, 300, dtype=torch.float64, device=DEV)
+        step[:, v] = h
+        diff = (loss(z.double() + step) - loss(z.double() - step)) / (2 * h)
+        assert ((got[:, v].double() - diff).abs() <= 4 * REL * (G.abs() + 8 * E.abs())).all()
+
+
+@pytest.mark.parametrize("n,V", [(5, 100), (600, 100), (5000, 64), (3, 60000)])
+@pytest.mark.parametrize("tdt", [torch.int32, torch.int64])
+def test_targets_outside_the_vocabulary(n, V, tdt):
+    z, t = make(n, V, FP32)
+    t = t.to(tdt)
+    good = ewg.token_logprobs(z, t, top=1)
+    t2 = t.clone()
+    t2[n - 2] = V
+    ws = ewg.status_workspace()
+    r = ewg.token_logprobs(z, t2, top=1, workspace=ws)
+    assert ewg.read_status(ws) == ewg.ERR_ID_OUT_OF_RANGE
+    assert math.isnan(r.logprobs[n - 2])
+    rest = torch.arange(n, device=DEV) != n - 2
+    assert torch.equal(r.logprobs[rest], good.logprobs[rest]) and torch.equal(r.entropy, good.entropy)
+    G = torch.ones(n, device=DEV)
+    got = ewg.token_logprobs_backward(z, t2, r.row_max, r.log_sum, G, workspace=ws)
+    assert ewg.read_status(ws) == ewg.ERR_ID_OUT_OF_RANGE
+    assert bool((got[n - 2] == 0).all())
+    with pytest.raises(ewg.EwgError) as err:
+        ewg.token_logprobs(z, t2, check=True)
+    assert err.value.code == ewg.ERR_ID_OUT_OF_RANGE
+    ewg.token_logprobs(z, t, workspace=ws)               # the next call's status is its own
+    assert ewg.read_status(ws) == ewg.OK
+
+
+def test_streams_and_graph():
+    """Calls on another stream than the current one, and a captured call replayed on new logits."""
+    z, t = make(64, 20000, BF16, seed=11)
+    want = ewg.token_logprobs(z, t, top=4)
+    G = torch.randn(64, device=DEV)
+    want_g = ewg.token_logprobs_backward(z, t, want.row_max, want.log_sum, G)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream(DEV)
+    with torch.cuda.stream(s):
+        r = ewg.token_logprobs(z, t, top=4)
+        g = ewg.token_logprobs_backward(z, t, r.row_max, r.log_sum, G)
+    s.synchronize()
+    for a, b in zip(want, r):
+        assert torch.equal(a, b)
+    assert torch.equal(g, want_g)
+    src = torch.zeros_like(z)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r = ewg.token_logprobs(src, t, top=4)
+        g = ewg.token_logprobs_backward(src, t, r.row_max, r.log_sum, G)
+    src.copy_(z)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(want, r):
+        assert torch.equal(a, b)
+    assert torch.equal(g, want_g)
+
+
+def test_refusals():
+    z, t = make(8, 100, FP32)
+    r = ewg.token_logprobs(z, t)
+    G = torch.ones(8, device=DEV)
+
+    def no(call):
+        with pytest.raises((ValueError, ewg.EwgError)):
+            call()
+    no(lambda: ewg.token_logprobs(z.half(), t))
+    no(lambda: ewg.token_logprobs(z, t.short()))
+    no(lambda: ewg.token_logprobs(z, t.float()))
+    no(lambda: ewg.token_logprobs(z.cpu(), t.cpu()))
+    no(lambda: ewg.token_logprobs(z, t[:4]))
+    no(lambda: ewg.token_logprobs(z.t(), torch.zeros(100, dtype=torch.int64, device=DEV)))
+    no(lambda: ewg.token_logprobs(z[:1].expand(8, 100), t))
+    no(lambda: ewg.token_logprobs(z, torch.zeros(16, dtype=torch.int64, device=DEV)[::2]))
+    no(lambda: ewg.token_logprobs(torch.empty(8, 0, device=DEV), t))
+    for scale in (0.0, -1.0, math.inf, math.nan):
+        no(lambda: ewg.token_logprobs(z, t, scale=scale))
+    no(lambda: ewg.token_logprobs(z, t, top=33))
+    no(lambda: ewg.token_logprobs(z, t, top=-1))
+    no(lambda: ewg.token_logprobs(z[:, :3], t.clamp(max=2), top=4))
+    no(lambda: ewg.token_logprobs(z, t, workspace=torch.empty(16, dtype=torch.uint8, device=DEV)))
+    back = lambda *a, **k: ewg.token_logprobs_backward(z, t, *a, **k)
+    no(lambda: back(r.row_max, r.log_sum, G.double()))
+    no(lambda: back(r.row_max[:4], r.log_sum, G))
+    no(lambda: back(r.row_max, r.log_sum, G, grad_entropy=G))
+    no(lambda: back(r.row_max, r.log_sum, G, out=torch.empty(8, 100, dtype=BF16, device=DEV)))
+    no(lambda: back(r.row_max, r.log_sum, G, out=torch.empty(8, 99, device=DEV)))
+    buf = torch.zeros(9 * 100, device=DEV)
+    no(lambda: ewg.token_logprobs_backward(buf[:800].view(8, 100), t, r.row_max, r.log_sum, G,
+                                           out=buf[100:].view(8, 100)))      # partly the logits
+    flat = torch.zeros(8 * 100 + 8, device=DEV)
+    no(lambda: ewg.token_logprobs_backward(flat[:800].view(8, 100), t, r.row_max, r.log_sum, flat[796:804],
+                                           out=flat[:800].view(8, 100)))     # over a gradient
