@@ -25,6 +25,7 @@ __all__ = [
     "accumulate_embedding_wgrad", "workspace_bytes", "plan", "apply", "read_status",
     "library_path", "lib", "accumulate_embedding_wgrad_shard", "MAX_TOP", "TokenLogprobs",
     "token_logprobs", "token_logprobs_backward", "status_workspace",
+    "orthogonalize_update", "orthogonalize_workspace",
 ]
 
 MIN_TOKENS = 3073
@@ -116,6 +117,11 @@ def _load(path):
     L.ewg_token_logprobs_backward.argtypes = [vp, i32, i64, vp, i32, i64, i64, f32, vp, vp, vp,
                                               vp, vp, vp, i64, vp, sz, vp]
     L.ewg_token_logprobs_backward.restype = i32
+    L.ewg_orthogonalize_workspace_bytes.argtypes = [i64, i64, i64]
+    L.ewg_orthogonalize_workspace_bytes.restype = sz
+    L.ewg_orthogonalize.argtypes = [vp, i32, i64, i64, i64, i64, i64, vp, i64, i64, i32, f32,
+                                    f32, f32, vp, sz, vp]
+    L.ewg_orthogonalize.restype = i32
     L.ewg_read_status.argtypes = [vp, vp, ctypes.POINTER(i32)]
     L.ewg_read_status.restype = i32
     L.ewg_status_string.argtypes = [i32]
@@ -486,5 +492,70 @@ def token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor, row_max
             grad_entropy.data_ptr() if grad_entropy is not None else None, g.data_ptr(), g_stride,
             *ws_args, _stream_ptr(logits.device)))
         if check and n:
+            raise_on_device_status(ws)
+    return out
+
+
+def orthogonalize_workspace(shape, device=None) -> torch.Tensor:
+    """A device buffer for orthogonalize_update of a tensor of this shape (no init needed)."""
+    *lead, rows, cols = shape
+    batch = 1
+    for d in lead:
+        batch *= d
+    nbytes = int(lib().ewg_orthogonalize_workspace_bytes(max(batch, 1), rows, cols))
+    if nbytes == 0:
+        raise EwgError(ERR_UNSUPPORTED, "unsupported sizes")
+    return torch.empty(nbytes, dtype=torch.uint8, device=device or "cuda")
+
+
+def _matrices(what, x):
+    """x [..., rows, cols] as [batch, rows, cols] with unit inner stride; no copy."""
+    try:
+        x3 = x.view(-1, *x.shape[-2:]) if x.dim() != 2 else x[None]
+    except RuntimeError:
+        x3 = None
+    if x3 is None or (x3.stride(2) != 1 and x3.shape[2] > 1):
+        raise ValueError(f"orthogonalize_update does not support these tensors: {what} must have "
+                         "unit inner stride and leading dimensions that share one stride")
+    return x3
+
+
+def orthogonalize_update(grad: torch.Tensor, *, steps: int = 5,
+                         coefficients: tuple = (3.4445, -4.7750, 2.0315),
+                         out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                         check: bool = False) -> torch.Tensor:
+    """Newton-Schulz orthogonalisation of each [rows, cols] matrix of grad, in bf16 (see
+    ewg_orthogonalize in include/ewg.h): `steps` times X <- a X + (b A + c A^2) X with
+    A = X X^T, from X = grad / |grad|.
+
+    grad: [..., rows, cols] bf16 or fp32 (leading dimensions are a batch of matrices; a
+    transposed matrix is taken as such); out: bf16 of the same shape.  The work is enqueued
+    on the current stream.  workspace: orthogonalize_workspace(grad.shape), allocated when
+    not given.  check=True waits and raises EwgError if a wait on the device gave up.
+    """
+    if not grad.is_cuda or grad.dtype not in _FLOAT_CODES or grad.dim() < 2:
+        raise ValueError("orthogonalize_update does not support these tensors: grad must be "
+                         "[..., rows, cols], bf16/fp32, on a CUDA device")
+    if out is not None and (out.shape != grad.shape or out.dtype != torch.bfloat16
+                            or out.device != grad.device):
+        raise ValueError("out must be bf16 of grad's shape on grad's device")
+    if grad.stride(-1) != 1 and grad.stride(-2) == 1 and grad.shape[-1] > 1:
+        # a transposed matrix: the steps of the transpose give the transpose
+        return orthogonalize_update(grad.mT, steps=steps, coefficients=coefficients,
+                                    out=None if out is None else out.mT, workspace=workspace,
+                                    check=check).mT
+    if out is None:
+        out = torch.empty(grad.shape, dtype=torch.bfloat16, device=grad.device)
+    if grad.numel() == 0 and 0 not in grad.shape[-2:]:
+        return out
+    g3, o3 = _matrices("grad", grad), _matrices("out", out)
+    batch, rows, cols = g3.shape
+    with torch.cuda.device(grad.device):
+        ws = workspace if workspace is not None else orthogonalize_workspace(grad.shape, grad.device)
+        _raise_on(lib().ewg_orthogonalize(
+            g3.data_ptr(), _FLOAT_CODES[grad.dtype], batch, rows, cols, g3.stride(0),
+            g3.stride(1), o3.data_ptr(), o3.stride(0), o3.stride(1), steps, *coefficients,
+            ws.data_ptr(), ws.numel(), _stream_ptr(grad.device)))
+        if check:
             raise_on_device_status(ws)
     return out

@@ -12,6 +12,7 @@
 #include "ewg_debug.h"
 #include "ewg_host.cuh"
 #include "ewg_internal.cuh"
+#include "ewg_ops.cuh"
 
 namespace {
 
@@ -231,6 +232,8 @@ int ewg::host::current_device(int* dev, int* num_sms) {
     if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
     e = ewg::prepare_kernels();
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+    e = ewg::prepare_orthogonalize();
+    if (e != cudaSuccess) return cuda_fail(e, "orthogonalisation set-up");
     d.ready = true;
   }
   *num_sms = d.num_sms;

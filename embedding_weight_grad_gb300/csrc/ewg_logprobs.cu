@@ -680,8 +680,6 @@ cudaError_t launch_grad_of(const LogprobsGradArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t prepare_logprobs() { return cudaSuccess; }
-
 cudaError_t launch_logprobs(const LogprobsArgs& a, bool bf16, int num_sms, cudaStream_t stream) {
   return bf16 ? launch_forward_of<__nv_bfloat16>(a, num_sms, stream) : launch_forward_of<float>(a, num_sms, stream);
 }

@@ -68,6 +68,26 @@ int check_logits(const void* logits, int dtype, int64_t row_stride, const void* 
   return check_array({"targets", targets, {}}, elem_size(targets_dtype), dev);
 }
 
+bool ortho_sizes_ok(int64_t batch, int64_t rows, int64_t cols) {
+  if (batch < 1 || batch > 65535 || rows < 1 || cols < 1) return false;
+  const int64_t lo = rows < cols ? rows : cols, hi = rows < cols ? cols : rows;
+  if (lo > ewg::kOrthoMaxSide || hi > ewg::kOrthoMaxLong) return false;
+  return batch * ((lo + 255) / 256) * ((hi + 255) / 256) < (int64_t(1) << 30);   // blocks of a phase
+}
+
+// A [batch][rows][cols] array of matrices: its checks and its bytes.
+int ortho_array(const char* name, const void* p, size_t es, int64_t batch, int64_t rows, int64_t cols,
+                int64_t batch_stride, int64_t row_stride, int dev, Array* out) {
+  const int64_t most = int64_t(1) << 40;
+  if ((rows > 1 && row_stride < cols) || row_stride < 0 || row_stride > most || batch_stride < 0 || batch_stride > most)
+    return fail(EWG_ERR_UNSUPPORTED, std::string(name) + " row stride must be >= cols, strides below 2^40");
+  const int64_t one = (rows - 1) * row_stride + cols;
+  if (batch > 1 && batch_stride < one)
+    return fail(EWG_ERR_UNSUPPORTED, std::string(name) + " matrices overlap");
+  *out = {name, p, span(p, batch, one, batch_stride, es)};
+  return check_array(*out, es, dev);
+}
+
 float log2_scale(float scale) { return static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074); }
 
 }  // namespace
@@ -179,6 +199,58 @@ int ewg_token_logprobs_backward(const void* logits, int logits_dtype, int64_t ro
   a.status = status_word(workspace);
   cudaError_t e = ewg::launch_logprobs_grad(a, logits_dtype == EWG_BF16, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? EWG_OK : cuda_fail(e, "token log probability gradient launch");
+}
+
+size_t ewg_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t cols) {
+  if (!ortho_sizes_ok(batch, rows, cols)) return 0;
+  return ewg::make_ortho_layout(ewg::make_ortho_shape(batch, rows, cols)).total;
+}
+
+int ewg_orthogonalize(const void* grad, int grad_dtype, int64_t batch, int64_t rows, int64_t cols,
+                      int64_t grad_batch_stride, int64_t grad_row_stride, void* out, int64_t out_batch_stride,
+                      int64_t out_row_stride, int steps, float a, float b, float c, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  ewg::set_last_error("");
+  int dev = 0, sms = 0;
+  int rc = current_device(&dev, &sms);
+  if (rc) return rc;
+  if (grad_dtype != EWG_BF16 && grad_dtype != EWG_FP32) return fail(EWG_ERR_UNSUPPORTED, "grad must be bf16 or fp32");
+  if (steps < 1 || steps > EWG_MAX_ORTHO_STEPS)
+    return fail(EWG_ERR_UNSUPPORTED, "steps outside [1, EWG_MAX_ORTHO_STEPS]");
+  if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c))
+    return fail(EWG_ERR_UNSUPPORTED, "the coefficients must be finite");
+  if (batch == 0 && rows > 0 && cols > 0) return EWG_OK;
+  if (!ortho_sizes_ok(batch, rows, cols))
+    return fail(EWG_ERR_UNSUPPORTED, "sizes: 0 <= batch <= 65535, 1 <= smaller side <= 16384, larger side <= 2^20, "
+                                     "batch * ceil(rows / 256) * ceil(cols / 256) < 2^30");
+  const size_t es = elem_size(grad_dtype);
+  Array in, res;
+  if ((rc = ortho_array("grad", grad, es, batch, rows, cols, grad_batch_stride, grad_row_stride, dev, &in)) ||
+      (rc = ortho_array("out", out, 2, batch, rows, cols, out_batch_stride, out_row_stride, dev, &res)))
+    return rc;
+  const ewg::OrthoShape shape = ewg::make_ortho_shape(batch, rows, cols);
+  const size_t need = ewg::make_ortho_layout(shape).total;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < need || !on_device(workspace, dev))
+    return fail(EWG_ERR_INVALID, "workspace null, misaligned, not on the device or smaller than "
+                                 "ewg_orthogonalize_workspace_bytes(batch, rows, cols)");
+  const Array ws = flat("workspace", workspace, static_cast<int64_t>(need), 1);
+  if ((rc = check_apart(res, in)) || (rc = check_apart(ws, in)) || (rc = check_apart(ws, res))) return rc;
+  ewg::OrthoCall q{};
+  q.shape = shape;
+  q.grad = grad;
+  q.grad_bf16 = grad_dtype == EWG_BF16;
+  q.grad_batch_stride = grad_batch_stride;
+  q.grad_row_stride = grad_row_stride;
+  q.out = out;
+  q.out_batch_stride = out_batch_stride;
+  q.out_row_stride = out_row_stride;
+  q.steps = steps;
+  q.a = a;
+  q.b = b;
+  q.c = c;
+  q.workspace = workspace;
+  cudaError_t e = ewg::launch_orthogonalize(q, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? EWG_OK : cuda_fail(e, "orthogonalisation launch");
 }
 
 }  // extern "C"

@@ -1,0 +1,666 @@
+// Newton-Schulz orthogonalisation of an update.
+//
+// With X0 = G / |G|_F (its transpose where G has more rows than columns, so that X is r x c
+// with r <= c) a step is
+//
+//     A = X X^T,    B = b A + c A^2,    X <- a X + B X,
+//
+// an odd polynomial of the singular values of X that drives them towards 1.  A and A^2 are
+// symmetric: only the blocks on and below the diagonal are computed and mirrored, so a step
+// is 3 r^2 c + r^3 floating-point operations instead of 4 r^2 c + 2 r^3.
+//
+// Precision.  The products run on the tensor cores with fp16 operands (11 significant bits) and
+// fp32 accumulators.  What keeps the result near its bf16 rounding:
+//   * X itself is kept in fp32 beside the fp16 copy that feeds the products; a X is
+//     taken from it.  Directions with small singular values, which the steps enlarge by up
+//     to a^5 = 485, then carry no noise from the rounding of the large ones: B is small on
+//     them.  Without it a matrix of low effective rank loses ten times the precision.
+//   * The diagonals of A and B, their largest entries, are kept apart in fp32 and the fp16
+//     matrices have zeros there: with A = D + O, A^2 = O O + D O + O D + D^2, and
+//     B X = offdiag(B) X + diag(B) X with the fp32 X.
+//   * Everything stored in fp16 is scaled by powers of two or by the norm: X by
+//     s ~ sqrt(r c), so its entries are about 1 at first and at most 1.2 s, and A, B by
+//     rho ~ r / 16.
+//
+// Layout.  Every buffer is [., ld] with the r index inside: X^T in fp16 (two, alternating)
+// and fp32, A and B.  The accumulator of a product has its row index across the lanes of a
+// warp, so all stores of X^T and of the mirrored blocks are contiguous.  As an operand of X
+// X^T, X^T has the product's rows inside (MN-major); for B X it has the inner index inside
+// (K-major), as A and B have by symmetry.
+#include <cfloat>
+#include <cmath>
+#include <mutex>
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "ewg.h"
+#include "ewg_internal.cuh"
+#include "ewg_ops.cuh"
+#include "ewg_ptx.cuh"
+
+namespace ewg {
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+
+// ---------------------------------------------------------------- norm and first X
+
+struct OrthoIn {
+  const void* grad;
+  int bf16, tall;
+  long long batch_stride, row_stride;
+  int rows, cols;
+  int ld;
+  long long xt_batch, xm_batch;      // elements between matrices
+  float s;                           // X is stored times s
+  double* norm;                      // [batch][norm_blocks] sums of squares
+  int norm_blocks;
+  __half* xt;
+  float* xm;
+  Header* header;
+  int* barrier;
+};
+
+__device__ __forceinline__ float grad_at(const OrthoIn& a, long long i) {
+  return a.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.grad)[i])
+                : static_cast<const float*>(a.grad)[i];
+}
+
+// Sums of squares in 64 bits: neither large nor small gradients leave the range.
+__global__ void __launch_bounds__(256) ortho_norm_kernel(const OrthoIn a) {
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
+    a.header->status = kStatusOk;
+    *a.barrier = 0;
+  }
+  const long long total = static_cast<long long>(a.rows) * a.cols;
+  const long long per = (total + a.norm_blocks - 1) / a.norm_blocks;
+  const long long lo = blockIdx.x * per, hi = min(lo + per, total);
+  const long long base = blockIdx.y * a.batch_stride;
+  double sum = 0.0;
+  for (long long i = lo + threadIdx.x; i < hi; i += 256) {
+    const long long row = i / a.cols;
+    const double g = grad_at(a, base + row * a.row_stride + (i - row * a.cols));
+    sum += g * g;
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
+  __shared__ double part[8];
+  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < 8; ++w) sum += part[w];
+    a.norm[blockIdx.y * a.norm_blocks + blockIdx.x] = sum;
+  }
+}
+
+// X^T times s / |G| in fp16 and fp32, by 64 x 64 tiles of G.
+__global__ void __launch_bounds__(256) ortho_scale_kernel(const OrthoIn a) {
+  __shared__ float tile[64][65];
+  __shared__ double factor;
+  if (threadIdx.x < 32) {
+    double sum = 0.0;
+    for (int i = threadIdx.x; i < a.norm_blocks; i += 32) sum += a.norm[blockIdx.z * a.norm_blocks + i];
+#pragma unroll
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
+    if (threadIdx.x == 0) factor = sum == 0.0 ? 0.0 : a.s / sqrt(sum);   // a zero matrix stays zero
+  }
+  __syncthreads();
+  // factor = f1 f2 with f1 a power of two, so that neither product leaves fp32's range
+  int e;
+  const float f2 = static_cast<float>(frexp(factor, &e));
+  const int e1 = min(max(e, -120), 120);
+  const float f1 = ldexpf(1.0f, e1);
+  const float f3 = ldexpf(f2, min(max(e - e1, -126), 126));
+  const int row0 = blockIdx.y * 64, col0 = blockIdx.x * 64;
+  const int tx = threadIdx.x % 64, ty = threadIdx.x / 64;
+  const long long base = blockIdx.z * a.batch_stride;
+#pragma unroll 4
+  for (int k = ty; k < 64; k += 4) {
+    const int i = row0 + k, j = col0 + tx;
+    if (i < a.rows && j < a.cols) tile[k][tx] = grad_at(a, base + i * a.row_stride + j) * f1 * f3;
+  }
+  __syncthreads();
+  __half* xt = a.xt + blockIdx.z * a.xt_batch;
+  float* xm = a.xm + blockIdx.z * a.xm_batch;
+#pragma unroll 4
+  for (int k = ty; k < 64; k += 4) {
+    // the r index is G's column where G is tall, else its row
+    const int outer = (a.tall ? row0 : col0) + k, inner = (a.tall ? col0 : row0) + tx;
+    if (outer < (a.tall ? a.rows : a.cols) && inner < (a.tall ? a.cols : a.rows)) {
+      const float x = a.tall ? tile[k][tx] : tile[tx][k];
+      const long long at = static_cast<long long>(outer) * a.ld + inner;
+      xt[at] = __float2half_rn(x);
+      xm[at] = x;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- the products
+
+constexpr int kBlock = 256;          // a pair of CTAs computes 256 x 256; each CTA 128 rows
+constexpr int kStepK = 64;           // inner elements of a stage: one 128-byte swizzled row
+constexpr int kStages = 6;
+constexpr int kOperandBytes = 128 * kStepK * 2;       // one CTA's half of an operand's stage
+constexpr int kStageBytes = 2 * kOperandBytes;
+constexpr int kBoxBytes = 64 * kStepK * 2;            // one tensor copy: 64 rows of 128 bytes
+constexpr int kEpilogueWarps = 8;
+constexpr int kGemmThreads = 128 + 32 * kEpilogueWarps;
+constexpr size_t kGemmSmem = static_cast<size_t>(kStages) * kStageBytes + 1024;
+constexpr uint32_t kWaitLimit = 1u << 22;
+constexpr uint32_t kGridWaitLimit = 1u << 22;
+
+enum Phase { kGram = 0, kPoly = 1, kUpdate = 2 };
+
+struct OrthoMaps {
+  CUtensorMap xt[2], a, b;
+};
+
+struct OrthoArgs {
+  int batch, r, c, ld;
+  int steps;
+  float ca, cb, cc;                  // the polynomial's coefficients
+  float s, rho;                      // stored X = s X, stored A, B = rho A, rho B
+  __half* xt[2];
+  float* xm;
+  __half* a;
+  __half* b;
+  float* diag_a;                     // [batch][ld], unscaled
+  float* diag_b;
+  __nv_bfloat16* out;
+  long long out_batch, out_row;
+  int tall;
+  Header* header;
+  int* barrier;
+};
+
+struct GemmSmem {
+  uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
+  uint32_t tmem;
+  int abort;
+};
+
+// Shared-memory operand descriptor: 128-byte swizzle; `lead` and `stride` in bytes.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t lead, uint32_t stride) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3fff) | static_cast<uint64_t>(lead >> 4) << 16 |
+         static_cast<uint64_t>(stride >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+
+__device__ __forceinline__ int blocks_of(int n) { return (n + kBlock - 1) / kBlock; }
+
+// Block `t` of a phase: matrix, block row I, block column J.  A and B: on and below the diagonal.
+struct Tile {
+  int z, I, J;
+};
+
+__device__ __forceinline__ int tiles_of(const OrthoArgs& a, int phase) {
+  const int nr = blocks_of(a.r);
+  return a.batch * (phase == kUpdate ? nr * blocks_of(a.c) : nr * (nr + 1) / 2);
+}
+
+__device__ __forceinline__ Tile tile_at(const OrthoArgs& a, int phase, int t) {
+  const int nr = blocks_of(a.r);
+  Tile x;
+  if (phase == kUpdate) {
+    const int per = nr * blocks_of(a.c);
+    x.z = t / per;
+    t -= x.z * per;
+    x.J = t / nr;
+    x.I = t - x.J * nr;
+  } else {
+    const int per = nr * (nr + 1) / 2;
+    x.z = t / per;
+    t -= x.z * per;
+    x.I = static_cast<int>((sqrtf(8.0f * t + 1.0f) - 1.0f) * 0.5f);
+    while ((x.I + 1) * (x.I + 2) / 2 <= t) ++x.I;
+    while (x.I * (x.I + 1) / 2 > t) --x.I;
+    x.J = t - x.I * (x.I + 1) / 2;
+  }
+  return x;
+}
+
+// Waits for the phase of `bar` with the given parity; false if it gave up.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
+    if ((i & 63u) == 63u && *abort) return false;
+  }
+  return false;
+}
+
+__device__ void gave_up(const OrthoArgs& a, volatile int* abort) {
+  *abort = 1;
+  atomicExch(&a.header->status, kStatusTimeout);
+}
+
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// Stores 32 consecutive 16-bit values (16 packed words) of a row at p, `n` of them in range.
+__device__ __forceinline__ void store_row32(uint16_t* p, const uint32_t (&w)[16], int n, bool vec) {
+  if (n >= 32 && vec) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      reinterpret_cast<uint4*>(p)[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 32; ++q)
+      if (q < n) p[q] = static_cast<uint16_t>(q % 2 ? w[q / 2] >> 16 : w[q / 2]);
+  }
+}
+
+// One thread's 32 columns [j0, j0 + 32) of row i of a product, acc in fp32.
+__device__ __forceinline__ void epilogue32(const OrthoArgs& a, int phase, bool last, const Tile& x, int i, int j0,
+                                           const uint32_t (&acc)[32], __half* xt_new) {
+  const int cols = phase == kUpdate ? a.c : a.r;
+  const int n = min(32, cols - j0);
+  if (i >= a.r || n <= 0) return;
+  const long long ld = a.ld;
+  if (phase == kUpdate) {
+    const float di = a.ca + a.diag_b[x.z * ld + i];
+    const float inv = 1.0f / a.rho;
+    float* xm = a.xm + (static_cast<long long>(x.z) * a.c + j0) * ld + i;
+    float v[32];
+#pragma unroll
+    for (int q = 0; q < 32; ++q) v[q] = q < n ? xm[q * ld] : 0.0f;
+#pragma unroll
+    for (int q = 0; q < 32; ++q) v[q] = fmaf(di, v[q], __uint_as_float(acc[q]) * inv);
+    if (!last) {
+      __half* xt = xt_new + (static_cast<long long>(x.z) * a.c + j0) * ld + i;
+#pragma unroll
+      for (int q = 0; q < 32; ++q) {
+        if (q < n) {
+          xm[q * ld] = v[q];
+          xt[q * ld] = __float2half_rn(v[q]);
+        }
+      }
+    } else {
+      const float unscale = 1.0f / a.s;
+      __nv_bfloat16* out = a.out + x.z * a.out_batch;
+      if (a.tall) {                  // out is [c, r]
+#pragma unroll
+        for (int q = 0; q < 32; ++q)
+          if (q < n) out[(j0 + q) * a.out_row + i] = __float2bfloat16_rn(v[q] * unscale);
+      } else {
+        uint32_t w[16];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) w[q] = pack_bf16(v[2 * q] * unscale, v[2 * q + 1] * unscale);
+        __nv_bfloat16* p = out + i * a.out_row + j0;
+        store_row32(reinterpret_cast<uint16_t*>(p), w, n, reinterpret_cast<uintptr_t>(p) % 16 == 0);
+      }
+    }
+    return;
+  }
+  // A (from X X^T) or B (from O O)
+  float v[32];
+  float* diag = (phase == kGram ? a.diag_a : a.diag_b) + x.z * ld;
+  if (phase == kGram) {
+    const float f = a.rho / (a.s * a.s);
+#pragma unroll
+    for (int q = 0; q < 32; ++q) v[q] = __uint_as_float(acc[q]) * f;
+    const int d = i - j0;
+    if (d >= 0 && d < 32) {
+#pragma unroll
+      for (int q = 0; q < 32; ++q)
+        if (q == d) {
+          diag[i] = v[q] / a.rho;
+          v[q] = 0.0f;
+        }
+    }
+  } else {
+    const __half* o = a.a + (static_cast<long long>(x.z) * a.r + j0) * ld + i;
+    const float* da = a.diag_a + x.z * ld;
+    const float di = da[i];
+    const float f = a.cc / a.rho;
+#pragma unroll
+    for (int q = 0; q < 32; ++q) {
+      if (q < n) {
+        const float oij = __half2float(o[q * ld]);
+        v[q] = fmaf(f, __uint_as_float(acc[q]), oij * fmaf(a.cc, di + da[j0 + q], a.cb));
+        if (j0 + q == i) {
+          diag[i] = fmaf(a.cb, di, a.cc * fmaf(di, di, __uint_as_float(acc[q]) / (a.rho * a.rho)));
+          v[q] = 0.0f;
+        }
+      }
+    }
+  }
+  __half* m = (phase == kGram ? a.a : a.b) + static_cast<long long>(x.z) * a.r * ld;
+  __half* mt = m + static_cast<long long>(j0) * ld + i;
+#pragma unroll
+  for (int q = 0; q < 32; ++q)
+    if (q < n) mt[q * ld] = __float2half_rn(v[q]);
+  if (x.I != x.J) {                  // the mirror of a block below the diagonal
+    uint32_t w[16];
+#pragma unroll
+    for (int q = 0; q < 16; ++q) w[q] = pack_half(v[2 * q], v[2 * q + 1]);
+    store_row32(reinterpret_cast<uint16_t*>(m + i * ld + j0), w, n, true);
+  }
+}
+
+// All phases of all steps, one cooperative launch of CTA pairs: a pair takes blocks of 256 x
+// 256, and a barrier over the grid ends each phase.  Per CTA: warp 0 copies operands (TMA),
+// warp 1 of the pair's first CTA issues the products, warps 4-11 take finished
+// accumulators (two in tensor memory, so that the products of the next block run meanwhile).
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
+    ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const OrthoArgs a) {
+  extern __shared__ unsigned char raw[];
+  __shared__ GemmSmem sm;
+  const uint32_t stages = (ptx::smem_u32(raw) + 1023u) & ~1023u;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = ptx::cluster_rank();
+  const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      ptx::mbar_init(&sm.full[i], 1);
+      ptx::mbar_init(&sm.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&sm.acc_full[i], 1);
+      ptx::mbar_init(&sm.acc_empty[i], 2 * kEpilogueWarps);
+    }
+    ptx::mbar_init(&sm.drained, 1);
+    sm.abort = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tensor_map(&maps.xt[0]);
+    ptx::prefetch_tensor_map(&maps.xt[1]);
+    ptx::prefetch_tensor_map(&maps.a);
+    ptx::prefetch_tensor_map(&maps.b);
+  }
+  if (warp == 1) ptx::tmem_alloc_pair(&sm.tmem);
+  ptx::tmem_fence_before();
+  __syncthreads();
+  ptx::cluster_sync_all();
+  ptx::tmem_fence_after();
+  const uint32_t tmem = sm.tmem;
+  volatile int* abort = &sm.abort;
+
+  uint32_t stage = 0, stage_phase = 0;      // producer's or issuer's place in the ring
+  uint32_t acc = 0, acc_phase = 0;          // issuer's or epilogue's accumulator
+
+  for (int p = 0; p < 3 * a.steps; ++p) {
+    const int phase = p % 3, step = p / 3, cur = step & 1;
+    const int tiles = tiles_of(a, phase);
+    const int blocks_k = ((phase == kGram ? a.c : a.r) + kStepK - 1) / kStepK;
+    if (warp == 0) {
+      if (lane == 0) {
+        const CUtensorMap* ma = phase == kGram ? &maps.xt[cur] : phase == kPoly ? &maps.a : &maps.b;
+        const CUtensorMap* mb = phase == kPoly ? &maps.a : &maps.xt[cur];
+        for (int t = pair; t < tiles && !*abort; t += pairs) {
+          const Tile x = tile_at(a, phase, t);
+          const int ra = x.I * kBlock + rank * 128, rb = x.J * kBlock + rank * 128;
+          for (int kb = 0; kb < blocks_k; ++kb) {
+            if (!wait_bar(&sm.empty[stage], stage_phase ^ 1u, abort)) {
+              gave_up(a, abort);
+              break;
+            }
+            if (rank == 0) ptx::mbar_arrive_expect_tx(&sm.full[stage], 2 * kStageBytes);
+            const uint32_t bar = ptx::map_to_rank(ptx::smem_u32(&sm.full[stage]), 0);
+            const uint32_t dst = stages + stage * kStageBytes;
+            const int k = kb * kStepK;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int da = ra + 64 * h, db = rb + 64 * h;
+              ptx::tma_load_3d_pair(dst + h * kBoxBytes, ma, phase == kGram ? da : k, phase == kGram ? k : da, x.z, bar);
+              ptx::tma_load_3d_pair(dst + kOperandBytes + h * kBoxBytes, mb, phase == kGram ? db : k,
+                                    phase == kGram ? k : db, x.z, bar);
+            }
+            if (++stage == kStages) {
+              stage = 0;
+              stage_phase ^= 1u;
+            }
+          }
+        }
+      }
+      __syncwarp();
+    } else if (warp == 1 && rank == 0) {
+      if (lane == 0) {
+        // fp32 accumulator, fp16 operands, 256 x 256; X X^T has both operands MN-major
+        const uint32_t idesc = 1u << 4 | (kBlock >> 3) << 17 | (kBlock >> 4) << 24 | (phase == kGram ? 3u << 15 : 0u);
+        // K-major: 8-row groups 1024 bytes apart, 16 inner elements = 32 bytes.  MN-major:
+        // groups of 64 rows a box apart, groups of 8 inner elements 1024 bytes apart.
+        const uint32_t lead = phase == kGram ? kBoxBytes : 16;
+        const uint32_t k_bytes = phase == kGram ? 2048 : 32;
+        for (int t = pair; t < tiles && !*abort; t += pairs) {
+          if (!wait_bar(&sm.acc_empty[acc], acc_phase ^ 1u, abort)) {
+            gave_up(a, abort);
+            break;
+          }
+          ptx::tmem_fence_after();
+          const uint32_t d = tmem + acc * kBlock;
+          for (int kb = 0; kb < blocks_k; ++kb) {
+            if (!wait_bar(&sm.full[stage], stage_phase, abort)) {
+              gave_up(a, abort);
+              break;
+            }
+            ptx::tmem_fence_after();
+            const uint32_t at = stages + stage * kStageBytes;
+#pragma unroll
+            for (int k = 0; k < kStepK / 16; ++k)
+              ptx::mma_f16_pair(d, operand_desc(at + k * k_bytes, lead, 1024),
+                                operand_desc(at + kOperandBytes + k * k_bytes, lead, 1024), idesc, kb > 0 || k > 0);
+            ptx::mma_commit_pair(&sm.empty[stage]);
+            if (++stage == kStages) {
+              stage = 0;
+              stage_phase ^= 1u;
+            }
+          }
+          ptx::mma_commit_pair(&sm.acc_full[acc]);
+          if (++acc == 2) {
+            acc = 0;
+            acc_phase ^= 1u;
+          }
+        }
+      }
+      __syncwarp();
+    } else if (warp >= 4) {
+      const int quarter = warp % 4, half = (warp - 4) / 4;
+      const bool last = step == a.steps - 1;
+      for (int t = pair; t < tiles && !*abort; t += pairs) {
+        const Tile x = tile_at(a, phase, t);
+        bool ok = wait_bar(&sm.acc_full[acc], acc_phase, abort);
+        ok = __all_sync(kAll, ok);
+        if (!ok) {
+          gave_up(a, abort);
+          break;
+        }
+        ptx::tmem_fence_after();
+        const uint32_t from = tmem + acc * kBlock + half * 128 + (static_cast<uint32_t>(quarter) << 21);
+        const int i = x.I * kBlock + rank * 128 + quarter * 32 + lane;
+        const int j = x.J * kBlock + half * 128;
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          uint32_t v[32];
+          ptx::tmem_load32(v, from + q * 32);
+          ptx::tmem_wait_load();
+          epilogue32(a, phase, last, x, i, j + q * 32, v, a.xt[cur ^ 1]);
+        }
+        ptx::tmem_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(ptx::smem_u32(&sm.acc_empty[acc]), 0));
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
+      ptx::fence_proxy_async();      // what was stored is read by tensor copies next
+    }
+    if (p + 1 == 3 * a.steps) break;
+    // ---- barrier over the grid
+    if (__syncthreads_or(*abort)) break;
+    if (threadIdx.x == 0) {
+      __threadfence();
+      ptx::red_release_add(a.barrier, 1);
+      const int want = (p + 1) * static_cast<int>(gridDim.x);
+      bool there = false;
+      for (uint32_t n = 0; n < kGridWaitLimit && !there; ++n) {
+        int v;
+        asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(a.barrier) : "memory");
+        there = v >= want;
+        if (!there && (n & 255u) == 255u && *reinterpret_cast<volatile int*>(&a.header->status) == kStatusTimeout) break;
+      }
+      if (!there) gave_up(a, abort);
+    }
+    if (__syncthreads_or(*abort)) break;
+    ptx::fence_proxy_async();
+  }
+
+  // ---- end: nothing of the pair may be in flight when it leaves
+  if (__syncthreads_or(*abort)) {
+    if (warp == 1 && rank == 0 && lane == 0) {
+      ptx::mma_commit_pair(&sm.drained);
+      for (uint32_t n = 0; n < kWaitLimit && !ptx::mbar_try_wait_cluster(&sm.drained, 0); ++n) {}
+    }
+    // copies already issued land within microseconds; which of them a barrier of the pair
+    // still counts is not known after a give-up, so they get a millisecond
+    if (warp == 0)
+      for (int n = 0; n < 1000; ++n) __nanosleep(1000);
+  }
+  ptx::tmem_fence_before();
+  __syncthreads();
+  ptx::cluster_sync_all();
+  if (warp == 1) ptx::tmem_dealloc_pair(tmem);
+}
+
+// ---------------------------------------------------------------- host
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled g_encode = nullptr;
+int g_pairs[64] = {};                // per device: pairs resident at once
+
+// [batch][outer][ld] fp16 with `inner` columns used, in boxes of 64 x 64.
+cudaError_t encode(CUtensorMap* map, void* p, int64_t inner, int64_t outer, int64_t batch, int64_t ld) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer),
+                              static_cast<cuuint64_t>(batch)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * 2), static_cast<cuuint64_t>(ld * 2 * outer)};
+  const cuuint32_t box[3] = {64, 64, 1}, step[3] = {1, 1, 1};
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, p, dims, strides, box, step,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+float power_of_two_below(double x) { return static_cast<float>(std::exp2(std::floor(std::log2(x)))); }
+
+}  // namespace
+
+// Called once per device, under the library's lock.
+cudaError_t prepare_orthogonalize() {
+  if (!g_encode) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found);
+    if (e != cudaSuccess) return e;
+    if (found != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
+    g_encode = reinterpret_cast<EncodeTiled>(fn);
+  }
+  cudaError_t e = cudaFuncSetAttribute(ortho_steps_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(kGemmSmem));
+  if (e != cudaSuccess) return e;
+  int dev = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2);
+  cfg.blockDim = dim3(kGemmThreads);
+  cfg.dynamicSmemBytes = kGemmSmem;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaOccupancyMaxActiveClusters(&g_pairs[dev], ortho_steps_kernel, &cfg);
+}
+
+cudaError_t launch_orthogonalize(const OrthoCall& q, cudaStream_t stream) {
+  const OrthoShape& sh = q.shape;
+  const OrthoLayout L = make_ortho_layout(sh);
+  char* ws = static_cast<char*>(q.workspace);
+  const double s = std::fmin(std::sqrt(static_cast<double>(sh.r) * sh.c), 32768.0);
+
+  OrthoIn in{};
+  in.grad = q.grad;
+  in.bf16 = q.grad_bf16;
+  in.tall = sh.tall;
+  in.batch_stride = q.grad_batch_stride;
+  in.row_stride = q.grad_row_stride;
+  in.rows = static_cast<int>(sh.rows);
+  in.cols = static_cast<int>(sh.cols);
+  in.ld = static_cast<int>(sh.ld);
+  in.xt_batch = in.xm_batch = sh.c * sh.ld;
+  in.s = power_of_two_below(s);
+  in.norm = reinterpret_cast<double*>(ws + L.norm);
+  in.norm_blocks = sh.norm_blocks;
+  in.xt = reinterpret_cast<__half*>(ws + L.xt[0]);
+  in.xm = reinterpret_cast<float*>(ws + L.xm);
+  in.header = reinterpret_cast<Header*>(ws + L.header);
+  in.barrier = reinterpret_cast<int*>(ws + L.barrier);
+
+  OrthoMaps maps;
+  cudaError_t e = encode(&maps.xt[0], ws + L.xt[0], sh.r, sh.c, sh.batch, sh.ld);
+  if (e == cudaSuccess) e = encode(&maps.xt[1], ws + L.xt[1], sh.r, sh.c, sh.batch, sh.ld);
+  if (e == cudaSuccess) e = encode(&maps.a, ws + L.a, sh.r, sh.r, sh.batch, sh.ld);
+  if (e == cudaSuccess) e = encode(&maps.b, ws + L.b, sh.r, sh.r, sh.batch, sh.ld);
+  if (e != cudaSuccess) return e;
+
+  OrthoArgs a{};
+  a.batch = static_cast<int>(sh.batch);
+  a.r = static_cast<int>(sh.r);
+  a.c = static_cast<int>(sh.c);
+  a.ld = static_cast<int>(sh.ld);
+  a.steps = q.steps;
+  a.ca = q.a;
+  a.cb = q.b;
+  a.cc = q.c;
+  a.s = in.s;
+  a.rho = power_of_two_below(std::fmax(1.0, static_cast<double>(sh.r) / 16));
+  a.xt[0] = in.xt;
+  a.xt[1] = reinterpret_cast<__half*>(ws + L.xt[1]);
+  a.xm = in.xm;
+  a.a = reinterpret_cast<__half*>(ws + L.a);
+  a.b = reinterpret_cast<__half*>(ws + L.b);
+  a.diag_a = reinterpret_cast<float*>(ws + L.diag_a);
+  a.diag_b = reinterpret_cast<float*>(ws + L.diag_b);
+  a.out = static_cast<__nv_bfloat16*>(q.out);
+  a.out_batch = q.out_batch_stride;
+  a.out_row = q.out_row_stride;
+  a.tall = sh.tall;
+  a.header = in.header;
+  a.barrier = in.barrier;
+
+  const unsigned batch = static_cast<unsigned>(sh.batch);
+  ortho_norm_kernel<<<dim3(sh.norm_blocks, batch), 256, 0, stream>>>(in);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  ortho_scale_kernel<<<dim3((in.cols + 63) / 64, (in.rows + 63) / 64, batch), 256, 0, stream>>>(in);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+
+  int dev = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  const int64_t nr = (sh.r + kBlock - 1) / kBlock, nc = (sh.c + kBlock - 1) / kBlock;
+  const int64_t most = sh.batch * nr * nc;          // blocks of the largest phase
+  const int pairs = static_cast<int>(most < g_pairs[dev] ? most : g_pairs[dev]);
+  if (pairs < 1) return cudaErrorLaunchOutOfResources;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * pairs);
+  cfg.blockDim = dim3(kGemmThreads);
+  cfg.dynamicSmemBytes = kGemmSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeCooperative;
+  at[0].val.cooperative = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, ortho_steps_kernel, maps, a);
+}
+
+}  // namespace ewg

@@ -322,6 +322,47 @@ int ewg_token_logprobs_backward(const void* logits, int logits_dtype, int64_t ro
                                 void* grad_logits, int64_t grad_row_stride, void* workspace,
                                 size_t workspace_bytes, void* stream);
 
+/* Most Newton-Schulz steps of one ewg_orthogonalize. */
+#define EWG_MAX_ORTHO_STEPS 64
+
+/*
+ * Bytes of device workspace of ewg_orthogonalize for `batch` matrices of rows x cols (0 for
+ * unsupported sizes).  It needs no initialisation.
+ */
+size_t ewg_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t cols);
+
+/*
+ * Newton-Schulz orthogonalisation of updates, as the Muon optimiser applies it to a
+ * matrix's (momentum of the) gradient.  For each matrix G, with X0 = G / |G|_F (Frobenius
+ * norm; transposed where rows > cols, and back at the end), `steps` times
+ *
+ *     A = X X^T        X <- a X + (b A + c A^2) X
+ *
+ * The result is rounded to bf16.  The products take fp16 operands with fp32 accumulation;
+ * X and the diagonals of A and of b A + c A^2 stay in fp32, which keeps the result within
+ * about 1e-3 of the exact steps in norm, beside its own rounding, for low-rank updates too.
+ * The norm is summed in 64 bits, so the scale of G does not matter; a zero matrix stays
+ * zero, a NaN or an infinity makes its matrix NaN.  Results are deterministic.
+ *
+ *   grad    [batch][rows][cols], EWG_BF16 or EWG_FP32, unit inner stride; any alignment
+ *   out     [batch][rows][cols] bf16, unit inner stride, apart from grad
+ *   strides in elements: rows >= cols apart, matrices not overlapping
+ *   a, b, c the polynomial (Muon: 3.4445, -4.7750, 2.0315); singular values that it takes
+ *           above 1.5 may overflow the fp16 operands
+ *
+ * Requires 0 <= batch <= 65535 (0: nothing is enqueued), the smaller side at most 16384 and
+ * the larger at most 2^20, batch * ceil(rows / 256) * ceil(cols / 256) < 2^30,
+ * 1 <= steps <= EWG_MAX_ORTHO_STEPS, finite coefficients, and a workspace as above.
+ * Enqueues two small kernels and one cooperative kernel that takes every step; allocates
+ * nothing.  ewg_read_status reports EWG_ERR_TIMEOUT if a bounded wait in it gave up (out
+ * is then unspecified).
+ */
+int ewg_orthogonalize(const void* grad, int grad_dtype, int64_t batch, int64_t rows,
+                      int64_t cols, int64_t grad_batch_stride, int64_t grad_row_stride,
+                      void* out, int64_t out_batch_stride, int64_t out_row_stride, int steps,
+                      float a, float b, float c, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
 /*
  * Waits for `stream`, then copies the device status of the last ewg_plan /
  * ewg_apply / ewg_accumulate that used this workspace into *status (EWG_OK,

@@ -1,0 +1,229 @@
+"""orthogonalize_update against its definition in 64 bits.
+
+Tolerance (2-norm of the error over that of the result): the one rounding to bf16 is at most
+2^-9.  The fp16 operands of each step are rounded by at most 2^-11 of their off-diagonal
+entries, 2^-11 / sqrt(3) in the root mean square, and enter through B, whose norm is below 3
+with the default polynomial; the roundings are independent and the polynomial shrinks
+perturbations of singular values near 1, so the last two or three steps' remain:
+sqrt(3 steps * 3 operands) * 3 * 2^-11 / sqrt(3) * (off-diagonal share of about 1/2) < 2.5e-3.
+Together below TOL = 4.5e-3.
+"""
+import math
+
+import pytest
+import torch
+
+import embedding_weight_grad_gb300 as ewg
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+MUON = (3.4445, -4.7750, 2.0315)
+TOL = 4.5e-3
+BF16, FP32 = torch.bfloat16, torch.float32
+
+
+def reference(G, steps=5, coefficients=MUON):
+    a, b, c = coefficients
+    X = G.double()
+    tall = X.shape[-2] > X.shape[-1]
+    X = X.mT if tall else X
+    norm = X.norm(dim=(-2, -1), keepdim=True)
+    X = X / torch.where(norm > 0, norm, 1.0)
+    for _ in range(steps):
+        A = X @ X.mT
+        X = a * X + (b * A + c * A @ A) @ X
+    return X.mT if tall else X
+
+
+def randn(*shape, dtype=FP32, seed=0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return (torch.randn(*shape, generator=g, device=DEV) * 1e-3).to(dtype)
+
+
+def check(got, G, **how):
+    want = reference(G, **how)
+    assert got.shape == G.shape and got.dtype == BF16
+    err = ((got.double() - want).norm(dim=(-2, -1)) / want.norm(dim=(-2, -1))).max().item()
+    assert err < TOL, err
+
+
+SIZES = [(1, 1), (1, 7), (7, 1), (2, 2), (3, 5), (8, 8), (31, 33), (64, 64), (65, 63), (127, 129), (128, 1000),
+         (255, 257), (256, 256), (257, 256), (300, 300), (511, 513), (1, 5000), (5000, 3), (999, 1537), (1001, 640),
+         (64, 20000), (20000, 40), (2000, 1100)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("rows,cols", SIZES)
+def test_sizes(rows, cols, dtype):
+    G = randn(rows, cols, dtype=dtype, seed=rows + cols)
+    check(ewg.orthogonalize_update(G, check=True), G)
+
+
+@pytest.mark.parametrize("batch,rows,cols", [(1, 40, 60), (3, 17, 300), (24, 128, 128), (200, 9, 5), (5, 300, 270),
+                                             (7, 513, 260)])
+def test_batches(batch, rows, cols):
+    G = randn(batch, rows, cols, seed=batch)
+    G *= torch.logspace(-6, 6, batch, device=DEV)[:, None, None]     # each matrix has its own norm
+    X = ewg.orthogonalize_update(G, check=True)
+    check(X, G)
+    for z in (0, batch - 1):
+        assert torch.equal(X[z], ewg.orthogonalize_update(G[z]))
+    G4 = G.view(1, batch, rows, cols)
+    assert torch.equal(ewg.orthogonalize_update(G4)[0], X)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_strides(dtype):
+    """Rows of a wider buffer at odd offsets, matrices apart, transposed, and out the same way."""
+    buf = torch.full((4, 101, 333), math.nan, dtype=dtype, device=DEV)
+    G = buf[1:4, 1:91, 3:273]
+    G.copy_(randn(3, 90, 270, dtype=dtype))
+    want = ewg.orthogonalize_update(G.contiguous())
+    check(want, G)
+    assert torch.equal(ewg.orthogonalize_update(G), want)
+    out = torch.full((3, 95, 275), 7.0, dtype=BF16, device=DEV)
+    for at in (0, 1, 4):
+        out.fill_(7.0)
+        r = ewg.orthogonalize_update(G, out=out[:, 2:92, at:at + 270])
+        assert torch.equal(r, want) and r.data_ptr() == out[:, 2:92, at:at + 270].data_ptr()
+        assert int((out == 7.0).sum()) == out.numel() - want.numel()
+    T = G.mT                                                     # tall, inner stride not 1
+    assert torch.equal(ewg.orthogonalize_update(T), want.mT)
+    tall = T.contiguous()
+    assert torch.equal(ewg.orthogonalize_update(tall), want.mT)
+    out.fill_(7.0)
+    ewg.orthogonalize_update(T, out=out[:, 2:92, 1:271].mT)
+    assert torch.equal(out[:, 2:92, 1:271], want)
+
+
+@pytest.mark.parametrize("rows,cols", [(300, 500), (512, 512), (500, 130)])
+@pytest.mark.parametrize("kind", ["rank one", "low rank", "low rank and noise", "decaying", "one outlier", "diagonal",
+                                  "sparse", "orthogonal"])
+def test_spectra(rows, cols, kind):
+    """Updates whose singular values span many orders of magnitude."""
+    g = torch.Generator(device=DEV).manual_seed(4)
+    n = lambda *s: torch.randn(*s, generator=g, device=DEV)
+    r = min(rows, cols)
+    if kind == "rank one":
+        G = n(rows, 1) @ n(1, cols)
+    elif kind == "low rank":
+        G = n(rows, 12) @ n(12, cols)
+    elif kind == "low rank and noise":
+        G = n(rows, 12) @ n(12, cols) + 0.05 * n(rows, cols)
+    elif kind == "decaying":
+        u, v = torch.linalg.qr(n(rows, r))[0], torch.linalg.qr(n(cols, r))[0]
+        G = (u / (1 + torch.arange(r, device=DEV)) ** 1.5) @ v.mT
+    elif kind == "one outlier":
+        G = n(rows, cols)
+        G[rows // 2, cols // 3] = 1e4
+    elif kind == "diagonal":
+        G = torch.zeros(rows, cols, device=DEV)
+        G.diagonal().copy_(torch.rand(r, generator=g, device=DEV) + 0.01)
+    elif kind == "sparse":
+        G = n(rows, cols) * (torch.rand(rows, cols, generator=g, device=DEV) < 0.01)
+    else:
+        q = torch.linalg.qr(n(max(rows, cols), r))[0]
+        G = q if rows >= cols else q.mT.contiguous()
+    check(ewg.orthogonalize_update(G, check=True), G)
+
+
+@pytest.mark.parametrize("rows,cols", [(5, 9), (200, 300), (300, 200)])
+def test_the_scale_of_the_update_does_not_matter(rows, cols):
+    G = randn(rows, cols)
+    want = ewg.orthogonalize_update(G)
+    for k in (-60, -20, 30, 100):
+        assert torch.equal(ewg.orthogonalize_update(G * 2.0 ** k), want)
+
+
+def test_zero_and_not_finite_matrices_of_a_batch():
+    G = randn(5, 70, 300)
+    G[1] = 0
+    G[2, 69, 299] = math.nan
+    G[3, 0, 0] = math.inf
+    X = ewg.orthogonalize_update(G, check=True)
+    assert bool((X[1] == 0).all())
+    assert bool(X[2].isnan().all()) and bool(X[3].isnan().all())
+    check(X[[0, 4]], G[[0, 4]])
+
+
+@pytest.mark.parametrize("steps", [1, 2, 3, 8])
+def test_steps_and_coefficients(steps):
+    G = randn(200, 333)
+    check(ewg.orthogonalize_update(G, steps=steps, check=True), G, steps=steps)
+    cubic = (1.5, -0.5, 0.0)                 # the classical iteration
+    check(ewg.orthogonalize_update(G, steps=steps, coefficients=cubic), G, steps=steps, coefficients=cubic)
+
+
+def test_cubic_steps_converge_to_an_orthogonal_matrix():
+    G = randn(100, 700)
+    X = ewg.orthogonalize_update(G, steps=20, coefficients=(1.5, -0.5, 0.0)).double()
+    eye = torch.eye(100, dtype=torch.float64, device=DEV)
+    assert (X @ X.mT - eye).norm().item() / 10 < 2 * TOL     # |eye| = 10; X X^T doubles X's error
+
+
+def test_the_same_call_gives_the_same_bits():
+    G = randn(2, 700, 900)
+    ws = ewg.orthogonalize_workspace(G.shape)
+    first = ewg.orthogonalize_update(G, workspace=ws)
+    for fill in (0, 255):                    # whatever the workspace held
+        ws.fill_(fill)
+        assert torch.equal(ewg.orthogonalize_update(G, workspace=ws, check=True), first)
+
+
+def test_streams_and_graph():
+    Ga, Gb = randn(600, 1000, seed=1), randn(3, 300, 200, seed=2)
+    wa, wb = ewg.orthogonalize_update(Ga), ewg.orthogonalize_update(Gb)
+    torch.cuda.synchronize()
+    sa, sb = torch.cuda.Stream(DEV), torch.cuda.Stream(DEV)
+    got = []
+    for _ in range(3):
+        with torch.cuda.stream(sa):
+            xa = ewg.orthogonalize_update(Ga)
+        with torch.cuda.stream(sb):
+            xb = ewg.orthogonalize_update(Gb)
+        got.append((xa, xb))
+    torch.cuda.synchronize()
+    for xa, xb in got:
+        assert torch.equal(xa, wa) and torch.equal(xb, wb)
+    src, ws = torch.zeros_like(Ga), ewg.orthogonalize_workspace(Ga.shape)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        x = ewg.orthogonalize_update(src, workspace=ws)
+    src.copy_(Ga)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(x, wa) and ewg.read_status(ws) == ewg.OK
+
+
+def test_empty_batch():
+    assert ewg.orthogonalize_update(torch.empty(0, 4, 5, device=DEV)).shape == (0, 4, 5)
+
+
+def test_refusals():
+    G = randn(30, 40)
+
+    def no(call):
+        with pytest.raises((ValueError, ewg.EwgError)):
+            call()
+    no(lambda: ewg.orthogonalize_update(G.half()))
+    no(lambda: ewg.orthogonalize_update(G.cpu()))
+    no(lambda: ewg.orthogonalize_update(G[0]))
+    no(lambda: ewg.orthogonalize_update(G[:, ::2]))
+    no(lambda: ewg.orthogonalize_update(torch.empty(0, 5, device=DEV)))
+    no(lambda: ewg.orthogonalize_update(G[:1].expand(30, 40)))
+    no(lambda: ewg.orthogonalize_update(G[None].expand(3, 30, 40)))
+    no(lambda: ewg.orthogonalize_update(G, steps=0))
+    no(lambda: ewg.orthogonalize_update(G, steps=65))
+    no(lambda: ewg.orthogonalize_update(G, coefficients=(1.0, math.nan, 0.0)))
+    no(lambda: ewg.orthogonalize_update(G, out=torch.empty(30, 40, device=DEV)))
+    no(lambda: ewg.orthogonalize_update(G, out=torch.empty(40, 30, dtype=BF16, device=DEV)))
+    H = G.bfloat16()
+    no(lambda: ewg.orthogonalize_update(H, out=H))               # out apart from grad
+    ws = ewg.orthogonalize_workspace(G.shape)
+    no(lambda: ewg.orthogonalize_update(G, workspace=ws[:-256]))
+    no(lambda: ewg.orthogonalize_update(G, workspace=torch.empty(ws.numel() + 8, dtype=torch.uint8, device=DEV)[8:]))
+    with pytest.raises(ewg.EwgError):
+        ewg.orthogonalize_workspace((16385, 16385))
+    assert ewg.lib().ewg_orthogonalize_workspace_bytes(1, 0, 5) == 0
