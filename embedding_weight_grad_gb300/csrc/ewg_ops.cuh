@@ -77,7 +77,7 @@ inline OrthoShape make_ortho_shape(int64_t batch, int64_t rows, int64_t cols) {
   s.r = s.tall ? cols : rows;
   s.c = s.tall ? rows : cols;
   s.ld = (s.r + 7) / 8 * 8;
-  // a block sums 16384 elements or more
+  // a block (8 warps of 1024 elements) sums 16384 elements or more
   const int64_t want = (s.r * s.c + 16383) / 16384;
   s.norm_blocks = static_cast<int>(want < kNormBlocks ? want : kNormBlocks);
   return s;

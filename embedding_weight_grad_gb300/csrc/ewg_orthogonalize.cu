@@ -68,26 +68,94 @@ __device__ __forceinline__ float grad_at(const OrthoIn& a, long long i) {
                 : static_cast<const float*>(a.grad)[i];
 }
 
-// Sums of squares in 64 bits: neither large nor small gradients leave the range.
+// The sum of the squares of a lane's kLaneElems elements, to about 2^-45 of it: each square
+// and each addition with its rounding error (an fma, and Knuth's two-sum), the errors
+// summed beside.  The norm then rounds to the same fp32 factor whatever the order of the
+// elements (strides, alignment, a transposed matrix).  The elements are first scaled by the power
+// of two that brings the largest near 1, which is exact, so that neither large nor small
+// gradients leave fp32's range.  64-bit arithmetic would bound the kernel.
+constexpr int kLaneElems = 32;
+
+__device__ __forceinline__ double sum_of_squares(const float (&g)[kLaneElems]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kLaneElems; ++i) m = fmaxf(m, fabsf(g[i]));
+  const int e = min(static_cast<int>(__float_as_uint(m) >> 23), 253);
+  const float scale = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);          // 2^(127 - e)
+  float sum = 0.0f, err = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kLaneElems; ++i) {
+    const float x = __fmul_rn(g[i], scale);
+    const float p = __fmul_rn(x, x);
+    const float t = __fadd_rn(sum, p);
+    const float b = __fsub_rn(t, sum);
+    const float lost = __fadd_rn(__fsub_rn(sum, __fsub_rn(t, b)), __fsub_rn(p, b));
+    err = __fadd_rn(err, __fadd_rn(lost, __fmaf_rn(x, x, -p)));
+    sum = t;
+  }
+  const double back = __longlong_as_double(static_cast<long long>(1023 + 2 * (e - 127)) << 52);
+  // (an infinite or NaN sum has no error term)
+  return (static_cast<double>(sum) + (isfinite(sum) ? static_cast<double>(err) : 0.0)) * back;
+}
+
+// Sums of squares of one matrix per blockIdx.y, a warp to 1024 neighbouring elements of a row
+// (a matrix without gaps is one long row).  Bound by the read of G.
 __global__ void __launch_bounds__(256) ortho_norm_kernel(const OrthoIn a) {
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
     a.header->status = kStatusOk;
     *a.barrier = 0;
   }
-  const long long total = static_cast<long long>(a.rows) * a.cols;
-  const long long per = (total + a.norm_blocks - 1) / a.norm_blocks;
-  const long long lo = blockIdx.x * per, hi = min(lo + per, total);
-  const long long base = blockIdx.y * a.batch_stride;
+  constexpr int kChunk = 32 * kLaneElems;
+  const bool whole = a.row_stride == a.cols;
+  const long long cols = whole ? static_cast<long long>(a.rows) * a.cols : a.cols;
+  const int chunks_per_row = static_cast<int>((cols + kChunk - 1) / kChunk);
+  const long long chunks = static_cast<long long>(chunks_per_row) * (whole ? 1 : a.rows);
+  const int lane = threadIdx.x % 32;
   double sum = 0.0;
-  for (long long i = lo + threadIdx.x; i < hi; i += 256) {
-    const long long row = i / a.cols;
-    const double g = grad_at(a, base + row * a.row_stride + (i - row * a.cols));
-    sum += g * g;
+  for (long long q = blockIdx.x * 8 + threadIdx.x / 32; q < chunks; q += gridDim.x * 8) {
+    const long long row = whole ? 0 : q / chunks_per_row;
+    const long long col = (q - row * chunks_per_row) * kChunk;
+    const long long at = blockIdx.y * a.batch_stride + row * a.row_stride + col;
+    const int n = static_cast<int>(min(cols - col, static_cast<long long>(kChunk)));
+    float g[kLaneElems];
+    const char* p = static_cast<const char*>(a.grad) + at * (a.bf16 ? 2 : 4);
+    if (n == kChunk && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+      const uint4* v = reinterpret_cast<const uint4*>(p) + lane;
+      if (a.bf16) {
+        uint4 r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = v[32 * i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            g[8 * i + 2 * k] = __uint_as_float(w[k] << 16);
+            g[8 * i + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+          }
+        }
+      } else {
+        uint4 r[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] = v[32 * i];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          g[4 * i] = __uint_as_float(r[i].x);
+          g[4 * i + 1] = __uint_as_float(r[i].y);
+          g[4 * i + 2] = __uint_as_float(r[i].z);
+          g[4 * i + 3] = __uint_as_float(r[i].w);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLaneElems; ++i) g[i] = lane + 32 * i < n ? grad_at(a, at + lane + 32 * i) : 0.0f;
+    }
+    sum += sum_of_squares(g);
   }
 #pragma unroll
   for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
   __shared__ double part[8];
-  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = sum;
+  if (lane == 0) part[threadIdx.x / 32] = sum;
   __syncthreads();
   if (threadIdx.x == 0) {
     for (int w = 1; w < 8; ++w) sum += part[w];
@@ -257,24 +325,75 @@ __device__ __forceinline__ void store_row32(uint16_t* p, const uint32_t (&w)[16]
   }
 }
 
-// One thread's 32 columns [j0, j0 + 32) of row i of a product, acc in fp32.
-__device__ __forceinline__ void epilogue32(const OrthoArgs& a, int phase, bool last, const Tile& x, int i, int j0,
-                                           const uint32_t (&acc)[32], __half* xt_new) {
-  const int cols = phase == kUpdate ? a.c : a.r;
-  const int n = min(32, cols - j0);
+// What a thread's 32 columns [j0, j0 + 32) of row i need beside the product: X (fp32) for the
+// update, O = offdiag(A) for B.
+template <int kPhase>
+__device__ __forceinline__ void load_beside(const OrthoArgs& a, int z, int i, int j0, float (&beside)[32]) {
+  if constexpr (kPhase == kGram) return;
+  const int n = i < a.r ? (kPhase == kUpdate ? a.c : a.r) - j0 : 0;
+  const long long ld = a.ld;
+  const float* xm = a.xm + (static_cast<long long>(z) * a.c + j0) * ld + i;
+  const __half* o = a.a + (static_cast<long long>(z) * a.r + j0) * ld + i;
+#pragma unroll
+  for (int q = 0; q < 32; ++q) {
+    if constexpr (kPhase == kUpdate) beside[q] = q < n ? xm[q * ld] : 0.0f;
+    else beside[q] = q < n ? __half2float(o[q * ld]) : 0.0f;
+  }
+}
+
+// The same columns' results from the product `acc`, in fp32; the diagonals of A and B go to
+// their own arrays and leave zeros.  Run by whole warps (j0 is the warp's).
+template <int kPhase>
+__device__ __forceinline__ void finish32(const OrthoArgs& a, int z, int i, int j0, float own,
+                                         const uint32_t (&acc)[32], const float (&beside)[32], float (&v)[32]) {
+  const long long ld = a.ld;
+  if constexpr (kPhase == kUpdate) {
+    const float inv = 1.0f / a.rho;  // own = a + B_ii
+#pragma unroll
+    for (int q = 0; q < 32; ++q) v[q] = fmaf(own, beside[q], __uint_as_float(acc[q]) * inv);
+    return;
+  }
+  float on_diag = 0.0f;
+  const int d = i - j0;
+  if constexpr (kPhase == kGram) {
+    const float f = a.rho / (a.s * a.s);
+#pragma unroll
+    for (int q = 0; q < 32; ++q) {
+      v[q] = __uint_as_float(acc[q]) * f;
+      if (q == d) {
+        on_diag = v[q] / a.rho;
+        v[q] = 0.0f;
+      }
+    }
+  } else {                           // own = A_ii
+    const int j = j0 + static_cast<int>(threadIdx.x % 32);
+    const float dj_lane = j < a.r ? a.diag_a[z * ld + j] : 0.0f;
+    const float f = a.cc / a.rho, f2 = 1.0f / (a.rho * a.rho);
+#pragma unroll
+    for (int q = 0; q < 32; ++q) {
+      const float dj = __shfl_sync(kAll, dj_lane, q);
+      const float x = __uint_as_float(acc[q]);
+      v[q] = fmaf(f, x, beside[q] * fmaf(a.cc, own + dj, a.cb));
+      if (q == d) {
+        on_diag = fmaf(a.cb, own, a.cc * fmaf(own, own, x * f2));
+        v[q] = 0.0f;
+      }
+    }
+  }
+  if (d >= 0 && d < 32 && i < a.r) (kPhase == kGram ? a.diag_a : a.diag_b)[z * ld + i] = on_diag;
+}
+
+template <int kPhase>
+__device__ __forceinline__ void store32(const OrthoArgs& a, bool last, const Tile& x, int i, int j0,
+                                        const float (&v)[32], __half* xt_new) {
+  const int n = (kPhase == kUpdate ? a.c : a.r) - j0;
   if (i >= a.r || n <= 0) return;
   const long long ld = a.ld;
-  if (phase == kUpdate) {
-    const float di = a.ca + a.diag_b[x.z * ld + i];
-    const float inv = 1.0f / a.rho;
-    float* xm = a.xm + (static_cast<long long>(x.z) * a.c + j0) * ld + i;
-    float v[32];
-#pragma unroll
-    for (int q = 0; q < 32; ++q) v[q] = q < n ? xm[q * ld] : 0.0f;
-#pragma unroll
-    for (int q = 0; q < 32; ++q) v[q] = fmaf(di, v[q], __uint_as_float(acc[q]) * inv);
+  if constexpr (kPhase == kUpdate) {
     if (!last) {
-      __half* xt = xt_new + (static_cast<long long>(x.z) * a.c + j0) * ld + i;
+      const long long at = (static_cast<long long>(x.z) * a.c + j0) * ld + i;
+      float* xm = a.xm + at;
+      __half* xt = xt_new + at;
 #pragma unroll
       for (int q = 0; q < 32; ++q) {
         if (q < n) {
@@ -297,52 +416,47 @@ __device__ __forceinline__ void epilogue32(const OrthoArgs& a, int phase, bool l
         store_row32(reinterpret_cast<uint16_t*>(p), w, n, reinterpret_cast<uintptr_t>(p) % 16 == 0);
       }
     }
-    return;
-  }
-  // A (from X X^T) or B (from O O)
-  float v[32];
-  float* diag = (phase == kGram ? a.diag_a : a.diag_b) + x.z * ld;
-  if (phase == kGram) {
-    const float f = a.rho / (a.s * a.s);
-#pragma unroll
-    for (int q = 0; q < 32; ++q) v[q] = __uint_as_float(acc[q]) * f;
-    const int d = i - j0;
-    if (d >= 0 && d < 32) {
-#pragma unroll
-      for (int q = 0; q < 32; ++q)
-        if (q == d) {
-          diag[i] = v[q] / a.rho;
-          v[q] = 0.0f;
-        }
-    }
   } else {
-    const __half* o = a.a + (static_cast<long long>(x.z) * a.r + j0) * ld + i;
-    const float* da = a.diag_a + x.z * ld;
-    const float di = da[i];
-    const float f = a.cc / a.rho;
+    __half* m = (kPhase == kGram ? a.a : a.b) + static_cast<long long>(x.z) * a.r * ld;
+    __half* mt = m + static_cast<long long>(j0) * ld + i;
 #pragma unroll
-    for (int q = 0; q < 32; ++q) {
-      if (q < n) {
-        const float oij = __half2float(o[q * ld]);
-        v[q] = fmaf(f, __uint_as_float(acc[q]), oij * fmaf(a.cc, di + da[j0 + q], a.cb));
-        if (j0 + q == i) {
-          diag[i] = fmaf(a.cb, di, a.cc * fmaf(di, di, __uint_as_float(acc[q]) / (a.rho * a.rho)));
-          v[q] = 0.0f;
-        }
-      }
+    for (int q = 0; q < 32; ++q)
+      if (q < n) mt[q * ld] = __float2half_rn(v[q]);
+    if (x.I != x.J) {                // the mirror of a block below the diagonal
+      uint32_t w[16];
+#pragma unroll
+      for (int q = 0; q < 16; ++q) w[q] = pack_half(v[2 * q], v[2 * q + 1]);
+      store_row32(reinterpret_cast<uint16_t*>(m + i * ld + j0), w, n, true);
     }
   }
-  __half* m = (phase == kGram ? a.a : a.b) + static_cast<long long>(x.z) * a.r * ld;
-  __half* mt = m + static_cast<long long>(j0) * ld + i;
-#pragma unroll
-  for (int q = 0; q < 32; ++q)
-    if (q < n) mt[q * ld] = __float2half_rn(v[q]);
-  if (x.I != x.J) {                  // the mirror of a block below the diagonal
-    uint32_t w[16];
-#pragma unroll
-    for (int q = 0; q < 16; ++q) w[q] = pack_half(v[2 * q], v[2 * q + 1]);
-    store_row32(reinterpret_cast<uint16_t*>(m + i * ld + j0), w, n, true);
+}
+
+// One warp's part of a finished block: 32 rows, 128 columns from j on.  What it needs from
+// memory for the first columns is on its way before the wait for the products, for the next
+// columns while the results of the last are stored.
+template <int kPhase>
+__device__ __forceinline__ bool epilogue(const OrthoArgs& a, bool last, const Tile& x, int i, int j, uint32_t from,
+                                         uint64_t* acc_full, uint32_t parity, volatile int* abort, __half* xt_new) {
+  float own = 0.0f;
+  if (i < a.r) {
+    if constexpr (kPhase == kUpdate) own = a.ca + a.diag_b[x.z * static_cast<long long>(a.ld) + i];
+    if constexpr (kPhase == kPoly) own = a.diag_a[x.z * static_cast<long long>(a.ld) + i];
   }
+  float beside[32];
+  load_beside<kPhase>(a, x.z, i, j, beside);
+  if (!__all_sync(kAll, wait_bar(acc_full, parity, abort))) return false;
+  ptx::tmem_fence_after();
+#pragma unroll 1
+  for (int q = 0; q < 4; ++q) {
+    uint32_t acc[32];
+    float v[32];
+    ptx::tmem_load32(acc, from + q * 32);
+    ptx::tmem_wait_load();
+    finish32<kPhase>(a, x.z, i, j + q * 32, own, acc, beside, v);
+    if (q < 3) load_beside<kPhase>(a, x.z, i, j + (q + 1) * 32, beside);
+    store32<kPhase>(a, last, x, i, j + q * 32, v, xt_new);
+  }
+  return true;
 }
 
 // All phases of all steps, one cooperative launch of CTA pairs: a pair takes blocks of 256 x
@@ -466,22 +580,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       const bool last = step == a.steps - 1;
       for (int t = pair; t < tiles && !*abort; t += pairs) {
         const Tile x = tile_at(a, phase, t);
-        bool ok = wait_bar(&sm.acc_full[acc], acc_phase, abort);
-        ok = __all_sync(kAll, ok);
-        if (!ok) {
-          gave_up(a, abort);
-          break;
-        }
-        ptx::tmem_fence_after();
         const uint32_t from = tmem + acc * kBlock + half * 128 + (static_cast<uint32_t>(quarter) << 21);
         const int i = x.I * kBlock + rank * 128 + quarter * 32 + lane;
         const int j = x.J * kBlock + half * 128;
-#pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          uint32_t v[32];
-          ptx::tmem_load32(v, from + q * 32);
-          ptx::tmem_wait_load();
-          epilogue32(a, phase, last, x, i, j + q * 32, v, a.xt[cur ^ 1]);
+        uint64_t* full = &sm.acc_full[acc];
+        __half* xt_new = a.xt[cur ^ 1];
+        const bool ok = phase == kGram ? epilogue<kGram>(a, last, x, i, j, from, full, acc_phase, abort, xt_new)
+                        : phase == kPoly ? epilogue<kPoly>(a, last, x, i, j, from, full, acc_phase, abort, xt_new)
+                                         : epilogue<kUpdate>(a, last, x, i, j, from, full, acc_phase, abort, xt_new);
+        if (!ok) {
+          gave_up(a, abort);
+          break;
         }
         ptx::tmem_fence_before();
         __syncwarp();
