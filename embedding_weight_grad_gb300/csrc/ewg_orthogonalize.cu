@@ -209,20 +209,30 @@ __global__ void __launch_bounds__(256) ortho_scale_kernel(const OrthoIn a) {
 
 constexpr int kBlock = 256;          // a pair of CTAs computes 256 x 256; each CTA 128 rows
 constexpr int kStepK = 64;           // inner elements of a stage: one 128-byte swizzled row
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kOperandBytes = 128 * kStepK * 2;       // one CTA's half of an operand's stage
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kBoxBytes = 64 * kStepK * 2;            // one tensor copy: 64 rows of 128 bytes
 constexpr int kEpilogueWarps = 8;
 constexpr int kGemmThreads = 128 + 32 * kEpilogueWarps;
-constexpr size_t kGemmSmem = static_cast<size_t>(kStages) * kStageBytes + 1024;
+// Epilogue staging of one warp: pieces of 32 rows x kPiece columns.  Three buffers for what a
+// piece reads (X in fp32, or O) and, for X, its result in place; two for the fp16 result.
+constexpr int kPiece = 16;
+constexpr int kPieces = 128 / kPiece;                 // of a warp's 128 columns
+constexpr int kBesideBytes = 32 * kPiece * 4;
+constexpr int kHalfBytes = 32 * kPiece * 2;
+constexpr int kWarpStaging = 3 * kBesideBytes + 2 * kHalfBytes;
+constexpr size_t kGemmSmem = static_cast<size_t>(kStages) * kStageBytes + kEpilogueWarps * kWarpStaging + 1024;
+static_assert(kGemmSmem + 512 <= 227 * 1024, "stages and staging fit in shared memory");
 constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr uint32_t kGridWaitLimit = 1u << 22;
 
 enum Phase { kGram = 0, kPoly = 1, kUpdate = 2 };
 
 struct OrthoMaps {
-  CUtensorMap xt[2], a, b;
+  CUtensorMap xt[2], a, b;                            // operands: boxes of 64 x 64, swizzled
+  CUtensorMap xt_piece[2], a_piece, b_piece, xm_piece;  // pieces: 32 of the r index, kPiece of the other
+  CUtensorMap a_mirror, b_mirror;                     // mirrored pieces: kPiece, 32
 };
 
 struct OrthoArgs {
@@ -230,10 +240,6 @@ struct OrthoArgs {
   int steps;
   float ca, cb, cc;                  // the polynomial's coefficients
   float s, rho;                      // stored X = s X, stored A, B = rho A, rho B
-  __half* xt[2];
-  float* xm;
-  __half* a;
-  __half* b;
   float* diag_a;                     // [batch][ld], unscaled
   float* diag_b;
   __nv_bfloat16* out;
@@ -245,6 +251,7 @@ struct OrthoArgs {
 
 struct GemmSmem {
   uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
+  uint64_t beside[kEpilogueWarps][3];
   uint32_t tmem;
   int abort;
 };
@@ -312,149 +319,176 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return d;
 }
 
-// Stores 32 consecutive 16-bit values (16 packed words) of a row at p, `n` of them in range.
-__device__ __forceinline__ void store_row32(uint16_t* p, const uint32_t (&w)[16], int n, bool vec) {
-  if (n >= 32 && vec) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      reinterpret_cast<uint4*>(p)[q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
-  } else {
-#pragma unroll
-    for (int q = 0; q < 32; ++q)
-      if (q < n) p[q] = static_cast<uint16_t>(q % 2 ? w[q / 2] >> 16 : w[q / 2]);
-  }
+// Where a warp of the epilogue is: its staging, its copies, and which piece comes next.
+struct EpilogueState {
+  uint32_t staging;                  // shared-memory addresses
+  uint64_t* bars;                    // of the three read buffers
+  uint32_t loads, uses;              // pieces requested and taken so far (of phases that read)
+  uint32_t stores;                   // pieces stored so far
+};
+
+__device__ __forceinline__ float lds_f32(uint32_t at) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ float lds_half(uint32_t at) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
+  return __half2float(__ushort_as_half(v));
+}
+__device__ __forceinline__ void sts_f32(uint32_t at, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+}
+__device__ __forceinline__ void sts_half(uint32_t at, float v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(__half_as_ushort(__float2half_rn(v))) : "memory");
+}
+__device__ __forceinline__ void sts_v4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// What a thread's 32 columns [j0, j0 + 32) of row i need beside the product: X (fp32) for the
-// update, O = offdiag(A) for B.
+// One lane requests what the piece at row i0, column j0 reads.
 template <int kPhase>
-__device__ __forceinline__ void load_beside(const OrthoArgs& a, int z, int i, int j0, float (&beside)[32]) {
-  if constexpr (kPhase == kGram) return;
-  const int n = i < a.r ? (kPhase == kUpdate ? a.c : a.r) - j0 : 0;
-  const long long ld = a.ld;
-  const float* xm = a.xm + (static_cast<long long>(z) * a.c + j0) * ld + i;
-  const __half* o = a.a + (static_cast<long long>(z) * a.r + j0) * ld + i;
-#pragma unroll
-  for (int q = 0; q < 32; ++q) {
-    if constexpr (kPhase == kUpdate) beside[q] = q < n ? xm[q * ld] : 0.0f;
-    else beside[q] = q < n ? __half2float(o[q * ld]) : 0.0f;
-  }
+__device__ __forceinline__ void request_piece(const OrthoMaps& maps, EpilogueState& st, int z, int i0, int j0) {
+  const uint32_t b = st.loads % 3;
+  ptx::mbar_arrive_expect_tx(&st.bars[b], kPhase == kUpdate ? kBesideBytes : kHalfBytes);
+  ptx::tma_load_3d(st.staging + b * kBesideBytes, kPhase == kUpdate ? &maps.xm_piece : &maps.a_piece, i0, j0, z,
+                   &st.bars[b]);
 }
 
-// The same columns' results from the product `acc`, in fp32; the diagonals of A and B go to
-// their own arrays and leave zeros.  Run by whole warps (j0 is the warp's).
-template <int kPhase>
-__device__ __forceinline__ void finish32(const OrthoArgs& a, int z, int i, int j0, float own,
-                                         const uint32_t (&acc)[32], const float (&beside)[32], float (&v)[32]) {
-  const long long ld = a.ld;
-  if constexpr (kPhase == kUpdate) {
-    const float inv = 1.0f / a.rho;  // own = a + B_ii
+// The last update's piece, to the caller's matrix.
+__device__ __forceinline__ void store_out(const OrthoArgs& a, int z, int i, int j0, const float (&v)[kPiece]) {
+  const int n = min(a.c - j0, kPiece);
+  if (i >= a.r) return;
+  __nv_bfloat16* out = a.out + z * a.out_batch;
+  const float unscale = 1.0f / a.s;
+  if (a.tall) {                      // out is [c, r]: neighbouring lanes, neighbouring elements
+    __nv_bfloat16* p = out + j0 * a.out_row + i;
 #pragma unroll
-    for (int q = 0; q < 32; ++q) v[q] = fmaf(own, beside[q], __uint_as_float(acc[q]) * inv);
+    for (int q = 0; q < kPiece; ++q)
+      if (q < n) p[q * a.out_row] = __float2bfloat16_rn(v[q] * unscale);
     return;
   }
-  float on_diag = 0.0f;
-  const int d = i - j0;
-  if constexpr (kPhase == kGram) {
-    const float f = a.rho / (a.s * a.s);
+  __nv_bfloat16* p = out + i * a.out_row + j0;
+  if (n == kPiece && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+    uint32_t w[kPiece / 2];
 #pragma unroll
-    for (int q = 0; q < 32; ++q) {
-      v[q] = __uint_as_float(acc[q]) * f;
-      if (q == d) {
-        on_diag = v[q] / a.rho;
-        v[q] = 0.0f;
-      }
-    }
-  } else {                           // own = A_ii
-    const int j = j0 + static_cast<int>(threadIdx.x % 32);
-    const float dj_lane = j < a.r ? a.diag_a[z * ld + j] : 0.0f;
-    const float f = a.cc / a.rho, f2 = 1.0f / (a.rho * a.rho);
-#pragma unroll
-    for (int q = 0; q < 32; ++q) {
-      const float dj = __shfl_sync(kAll, dj_lane, q);
-      const float x = __uint_as_float(acc[q]);
-      v[q] = fmaf(f, x, beside[q] * fmaf(a.cc, own + dj, a.cb));
-      if (q == d) {
-        on_diag = fmaf(a.cb, own, a.cc * fmaf(own, own, x * f2));
-        v[q] = 0.0f;
-      }
-    }
-  }
-  if (d >= 0 && d < 32 && i < a.r) (kPhase == kGram ? a.diag_a : a.diag_b)[z * ld + i] = on_diag;
-}
-
-template <int kPhase>
-__device__ __forceinline__ void store32(const OrthoArgs& a, bool last, const Tile& x, int i, int j0,
-                                        const float (&v)[32], __half* xt_new) {
-  const int n = (kPhase == kUpdate ? a.c : a.r) - j0;
-  if (i >= a.r || n <= 0) return;
-  const long long ld = a.ld;
-  if constexpr (kPhase == kUpdate) {
-    if (!last) {
-      const long long at = (static_cast<long long>(x.z) * a.c + j0) * ld + i;
-      float* xm = a.xm + at;
-      __half* xt = xt_new + at;
-#pragma unroll
-      for (int q = 0; q < 32; ++q) {
-        if (q < n) {
-          xm[q * ld] = v[q];
-          xt[q * ld] = __float2half_rn(v[q]);
-        }
-      }
-    } else {
-      const float unscale = 1.0f / a.s;
-      __nv_bfloat16* out = a.out + x.z * a.out_batch;
-      if (a.tall) {                  // out is [c, r]
-#pragma unroll
-        for (int q = 0; q < 32; ++q)
-          if (q < n) out[(j0 + q) * a.out_row + i] = __float2bfloat16_rn(v[q] * unscale);
-      } else {
-        uint32_t w[16];
-#pragma unroll
-        for (int q = 0; q < 16; ++q) w[q] = pack_bf16(v[2 * q] * unscale, v[2 * q + 1] * unscale);
-        __nv_bfloat16* p = out + i * a.out_row + j0;
-        store_row32(reinterpret_cast<uint16_t*>(p), w, n, reinterpret_cast<uintptr_t>(p) % 16 == 0);
-      }
-    }
+    for (int q = 0; q < kPiece / 2; ++q) w[q] = pack_bf16(v[2 * q] * unscale, v[2 * q + 1] * unscale);
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
   } else {
-    __half* m = (kPhase == kGram ? a.a : a.b) + static_cast<long long>(x.z) * a.r * ld;
-    __half* mt = m + static_cast<long long>(j0) * ld + i;
 #pragma unroll
-    for (int q = 0; q < 32; ++q)
-      if (q < n) mt[q * ld] = __float2half_rn(v[q]);
-    if (x.I != x.J) {                // the mirror of a block below the diagonal
-      uint32_t w[16];
-#pragma unroll
-      for (int q = 0; q < 16; ++q) w[q] = pack_half(v[2 * q], v[2 * q + 1]);
-      store_row32(reinterpret_cast<uint16_t*>(m + i * ld + j0), w, n, true);
-    }
+    for (int q = 0; q < kPiece; ++q)
+      if (q < n) p[q] = __float2bfloat16_rn(v[q] * unscale);
   }
 }
 
-// One warp's part of a finished block: 32 rows, 128 columns from j on.  What it needs from
-// memory for the first columns is on its way before the wait for the products, for the next
-// columns while the results of the last are stored.
+// One warp's part of a finished block: 32 rows from i0, 128 columns from j, in pieces of kPiece
+// columns.  A piece's inputs come and its results go by tensor copies through shared memory,
+// which also clip what leaves the matrix; the next two pieces' inputs are under way while
+// one is computed, and the first two's before the products are done.
 template <int kPhase>
-__device__ __forceinline__ bool epilogue(const OrthoArgs& a, bool last, const Tile& x, int i, int j, uint32_t from,
-                                         uint64_t* acc_full, uint32_t parity, volatile int* abort, __half* xt_new) {
-  float own = 0.0f;
-  if (i < a.r) {
-    if constexpr (kPhase == kUpdate) own = a.ca + a.diag_b[x.z * static_cast<long long>(a.ld) + i];
-    if constexpr (kPhase == kPoly) own = a.diag_a[x.z * static_cast<long long>(a.ld) + i];
+__device__ __forceinline__ bool epilogue(const OrthoMaps& maps, const OrthoArgs& a, int step, const Tile& x, int i0,
+                                         int j, uint32_t from, uint64_t* acc_full, uint32_t parity,
+                                         volatile int* abort, EpilogueState& st) {
+  const int lane = threadIdx.x % 32;
+  const int i = i0 + lane;
+  const int cols = kPhase == kUpdate ? a.c : a.r;
+  const int pieces = i0 < a.r ? min(max((cols - j + kPiece - 1) / kPiece, 0), kPieces) : 0;
+  const long long ld = a.ld;
+  const bool last = kPhase == kUpdate && step == a.steps - 1;
+  if (kPhase != kGram && lane == 0) {
+    if (pieces > 0) request_piece<kPhase>(maps, st, x.z, i0, j), ++st.loads;
+    if (pieces > 1) request_piece<kPhase>(maps, st, x.z, i0, j + kPiece), ++st.loads;
   }
-  float beside[32];
-  load_beside<kPhase>(a, x.z, i, j, beside);
+  float own = 0.0f, dj4[4] = {};
+  if (kPhase == kUpdate && i < a.r) own = a.ca + a.diag_b[x.z * ld + i];
+  if (kPhase == kPoly) {
+    if (i < a.r) own = a.diag_a[x.z * ld + i];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) dj4[q] = j + 32 * q + lane < a.r ? a.diag_a[x.z * ld + j + 32 * q + lane] : 0.0f;
+  }
   if (!__all_sync(kAll, wait_bar(acc_full, parity, abort))) return false;
   ptx::tmem_fence_after();
+  const float f = kPhase == kUpdate ? 1.0f / a.rho : kPhase == kGram ? a.rho / (a.s * a.s) : a.cc / a.rho;
 #pragma unroll 1
-  for (int q = 0; q < 4; ++q) {
-    uint32_t acc[32];
-    float v[32];
-    ptx::tmem_load32(acc, from + q * 32);
+  for (int u = 0; u < pieces; ++u) {
+    const int j0 = j + u * kPiece;
+    uint32_t acc[kPiece];
+    float v[kPiece];
+    ptx::tmem_load16(acc, from + u * kPiece);
+    uint32_t in = 0;
+    if (kPhase != kGram) {
+      const uint32_t b = st.uses % 3;
+      if (!__all_sync(kAll, wait_bar(&st.bars[b], (st.uses / 3) & 1u, abort))) return false;
+      ++st.uses;
+      in = st.staging + b * kBesideBytes;
+    }
     ptx::tmem_wait_load();
-    finish32<kPhase>(a, x.z, i, j + q * 32, own, acc, beside, v);
-    if (q < 3) load_beside<kPhase>(a, x.z, i, j + (q + 1) * 32, beside);
-    store32<kPhase>(a, last, x, i, j + q * 32, v, xt_new);
+    if constexpr (kPhase == kUpdate) {
+#pragma unroll
+      for (int q = 0; q < kPiece; ++q)
+        v[q] = fmaf(own, lds_f32(in + (q * 32 + lane) * 4), __uint_as_float(acc[q]) * f);
+    } else {
+      const float dj_lane = u < 4 ? (u < 2 ? dj4[0] : dj4[1]) : (u < 6 ? dj4[2] : dj4[3]);
+      float diag = 0.0f;             // the product on the diagonal
+#pragma unroll
+      for (int q = 0; q < kPiece; ++q) {
+        const float p = __uint_as_float(acc[q]);
+        const bool on = j0 + q == i;
+        if (on) diag = p;
+        if constexpr (kPhase == kGram) {
+          v[q] = p * f;
+        } else {
+          const float dj = __shfl_sync(kAll, dj_lane, (u & 1) * kPiece + q);
+          v[q] = fmaf(f, p, lds_half(in + (q * 32 + lane) * 2) * fmaf(a.cc, own + dj, a.cb));
+        }
+        if (on) v[q] = 0.0f;
+      }
+      if (i >= j0 && i < j0 + kPiece && i < a.r) {
+        if constexpr (kPhase == kGram) a.diag_a[x.z * ld + i] = diag / (a.s * a.s);
+        else a.diag_b[x.z * ld + i] = fmaf(a.cb, own, a.cc * fmaf(own, own, diag / (a.rho * a.rho)));
+      }
+    }
+    if (last) {
+      store_out(a, x.z, i, j0, v);
+      __syncwarp();                  // the read buffer is free
+      if (lane == 0 && u + 2 < pieces) request_piece<kPhase>(maps, st, x.z, i0, j0 + 2 * kPiece), ++st.loads;
+      continue;
+    }
+    const uint32_t half = st.staging + 3 * kBesideBytes + (st.stores & 1u) * kHalfBytes;
+    // a mirrored piece goes to the second half of a read buffer, which O leaves free
+    const uint32_t mirror = st.staging + (st.stores % 3) * kBesideBytes + kHalfBytes;
+#pragma unroll
+    for (int q = 0; q < kPiece; ++q) {
+      if constexpr (kPhase == kUpdate) sts_f32(in + (q * 32 + lane) * 4, v[q]);
+      sts_half(half + (q * 32 + lane) * 2, v[q]);
+    }
+    if (kPhase != kUpdate && x.I != x.J) {
+      uint32_t w[kPiece / 2];
+#pragma unroll
+      for (int q = 0; q < kPiece / 2; ++q) w[q] = pack_half(v[2 * q], v[2 * q + 1]);
+      sts_v4(mirror + lane * kPiece * 2, w[0], w[1], w[2], w[3]);
+      sts_v4(mirror + lane * kPiece * 2 + 16, w[4], w[5], w[6], w[7]);
+    }
+    ++st.stores;
+    ptx::fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+      if constexpr (kPhase == kUpdate) {
+        ptx::tma_store_3d(&maps.xm_piece, i0, j0, x.z, in);
+        ptx::tma_store_3d(&maps.xt_piece[(step & 1) ^ 1], i0, j0, x.z, half);
+      } else {
+        ptx::tma_store_3d(kPhase == kGram ? &maps.a_piece : &maps.b_piece, i0, j0, x.z, half);
+        if (x.I != x.J) ptx::tma_store_3d(kPhase == kGram ? &maps.a_mirror : &maps.b_mirror, j0, i0, x.z, mirror);
+      }
+      ptx::bulk_commit();
+      // the piece before this one has left its buffers, which the next ones take
+      ptx::bulk_wait_read<1>();
+      if (kPhase != kGram && u + 2 < pieces)
+        request_piece<kPhase>(maps, st, x.z, i0, j0 + 2 * kPiece), ++st.loads;
+    }
+    __syncwarp();
   }
   return true;
 }
@@ -482,6 +516,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       ptx::mbar_init(&sm.acc_empty[i], 2 * kEpilogueWarps);
     }
     ptx::mbar_init(&sm.drained, 1);
+    for (int i = 0; i < 3 * kEpilogueWarps; ++i) ptx::mbar_init(&sm.beside[0][0] + i, 1);
     sm.abort = 0;
     ptx::fence_mbar_init();
     ptx::prefetch_tensor_map(&maps.xt[0]);
@@ -499,6 +534,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 
   uint32_t stage = 0, stage_phase = 0;      // producer's or issuer's place in the ring
   uint32_t acc = 0, acc_phase = 0;          // issuer's or epilogue's accumulator
+  EpilogueState st{};
+  if (warp >= 4) {
+    st.staging = stages + kStages * kStageBytes + (warp - 4) * kWarpStaging;
+    st.bars = sm.beside[warp - 4];
+  }
 
   for (int p = 0; p < 3 * a.steps; ++p) {
     const int phase = p % 3, step = p / 3, cur = step & 1;
@@ -577,17 +617,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       __syncwarp();
     } else if (warp >= 4) {
       const int quarter = warp % 4, half = (warp - 4) / 4;
-      const bool last = step == a.steps - 1;
       for (int t = pair; t < tiles && !*abort; t += pairs) {
         const Tile x = tile_at(a, phase, t);
         const uint32_t from = tmem + acc * kBlock + half * 128 + (static_cast<uint32_t>(quarter) << 21);
-        const int i = x.I * kBlock + rank * 128 + quarter * 32 + lane;
+        const int i0 = x.I * kBlock + rank * 128 + quarter * 32;
         const int j = x.J * kBlock + half * 128;
         uint64_t* full = &sm.acc_full[acc];
-        __half* xt_new = a.xt[cur ^ 1];
-        const bool ok = phase == kGram ? epilogue<kGram>(a, last, x, i, j, from, full, acc_phase, abort, xt_new)
-                        : phase == kPoly ? epilogue<kPoly>(a, last, x, i, j, from, full, acc_phase, abort, xt_new)
-                                         : epilogue<kUpdate>(a, last, x, i, j, from, full, acc_phase, abort, xt_new);
+        const bool ok = phase == kGram ? epilogue<kGram>(maps, a, step, x, i0, j, from, full, acc_phase, abort, st)
+                        : phase == kPoly ? epilogue<kPoly>(maps, a, step, x, i0, j, from, full, acc_phase, abort, st)
+                                         : epilogue<kUpdate>(maps, a, step, x, i0, j, from, full, acc_phase, abort, st);
         if (!ok) {
           gave_up(a, abort);
           break;
@@ -600,13 +638,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           acc_phase ^= 1u;
         }
       }
-      ptx::fence_proxy_async();      // what was stored is read by tensor copies next
+      if (lane == 0) {               // what was stored is there for the next phase
+        ptx::bulk_wait<0>();
+        ptx::fence_proxy_async();
+      }
     }
     if (p + 1 == 3 * a.steps) break;
     // ---- barrier over the grid
     if (__syncthreads_or(*abort)) break;
     if (threadIdx.x == 0) {
-      __threadfence();
       ptx::red_release_add(a.barrier, 1);
       const int want = (p + 1) * static_cast<int>(gridDim.x);
       bool there = false;
@@ -619,7 +659,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       if (!there) gave_up(a, abort);
     }
     if (__syncthreads_or(*abort)) break;
-    ptx::fence_proxy_async();
+    if (lane == 0) ptx::fence_proxy_async();   // the acquire before the next tensor copies
   }
 
   // ---- end: nothing of the pair may be in flight when it leaves
@@ -647,14 +687,17 @@ using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
 EncodeTiled g_encode = nullptr;
 int g_pairs[64] = {};                // per device: pairs resident at once
 
-// [batch][outer][ld] fp16 with `inner` columns used, in boxes of 64 x 64.
-cudaError_t encode(CUtensorMap* map, void* p, int64_t inner, int64_t outer, int64_t batch, int64_t ld) {
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer),
-                              static_cast<cuuint64_t>(batch)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * 2), static_cast<cuuint64_t>(ld * 2 * outer)};
-  const cuuint32_t box[3] = {64, 64, 1}, step[3] = {1, 1, 1};
-  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, p, dims, strides, box, step,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+// [batch][outer][ld] with `inner` columns used, in boxes of box_x x box_y.
+cudaError_t encode(CUtensorMap* map, void* p, bool fp32, const OrthoShape& sh, int64_t outer, int box_x, int box_y,
+                   bool swizzle) {
+  const cuuint64_t es = fp32 ? 4 : 2;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(sh.r), static_cast<cuuint64_t>(outer),
+                              static_cast<cuuint64_t>(sh.batch)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(sh.ld) * es, static_cast<cuuint64_t>(sh.ld * outer) * es};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_x), static_cast<cuuint32_t>(box_y), 1}, step[3] = {1, 1, 1};
+  const CUresult r = g_encode(map, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, p,
+                              dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
@@ -716,10 +759,21 @@ cudaError_t launch_orthogonalize(const OrthoCall& q, cudaStream_t stream) {
   in.barrier = reinterpret_cast<int*>(ws + L.barrier);
 
   OrthoMaps maps;
-  cudaError_t e = encode(&maps.xt[0], ws + L.xt[0], sh.r, sh.c, sh.batch, sh.ld);
-  if (e == cudaSuccess) e = encode(&maps.xt[1], ws + L.xt[1], sh.r, sh.c, sh.batch, sh.ld);
-  if (e == cudaSuccess) e = encode(&maps.a, ws + L.a, sh.r, sh.r, sh.batch, sh.ld);
-  if (e == cudaSuccess) e = encode(&maps.b, ws + L.b, sh.r, sh.r, sh.batch, sh.ld);
+  cudaError_t e = cudaSuccess;
+  auto add = [&](CUtensorMap* map, size_t at, bool fp32, int64_t outer, int x, int y, bool swizzle) {
+    if (e == cudaSuccess) e = encode(map, ws + at, fp32, sh, outer, x, y, swizzle);
+  };
+  for (int i = 0; i < 2; ++i) {
+    add(&maps.xt[i], L.xt[i], false, sh.c, 64, 64, true);
+    add(&maps.xt_piece[i], L.xt[i], false, sh.c, 32, kPiece, false);
+  }
+  add(&maps.xm_piece, L.xm, true, sh.c, 32, kPiece, false);
+  add(&maps.a, L.a, false, sh.r, 64, 64, true);
+  add(&maps.a_piece, L.a, false, sh.r, 32, kPiece, false);
+  add(&maps.a_mirror, L.a, false, sh.r, kPiece, 32, false);
+  add(&maps.b, L.b, false, sh.r, 64, 64, true);
+  add(&maps.b_piece, L.b, false, sh.r, 32, kPiece, false);
+  add(&maps.b_mirror, L.b, false, sh.r, kPiece, 32, false);
   if (e != cudaSuccess) return e;
 
   OrthoArgs a{};
@@ -733,11 +787,6 @@ cudaError_t launch_orthogonalize(const OrthoCall& q, cudaStream_t stream) {
   a.cc = q.c;
   a.s = in.s;
   a.rho = power_of_two_below(std::fmax(1.0, static_cast<double>(sh.r) / 16));
-  a.xt[0] = in.xt;
-  a.xt[1] = reinterpret_cast<__half*>(ws + L.xt[1]);
-  a.xm = in.xm;
-  a.a = reinterpret_cast<__half*>(ws + L.a);
-  a.b = reinterpret_cast<__half*>(ws + L.b);
   a.diag_a = reinterpret_cast<float*>(ws + L.diag_a);
   a.diag_b = reinterpret_cast<float*>(ws + L.diag_b);
   a.out = static_cast<__nv_bfloat16*>(q.out);
