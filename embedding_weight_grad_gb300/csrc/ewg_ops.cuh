@@ -65,7 +65,7 @@ struct OrthoShape {
 };
 
 struct OrthoLayout {
-  size_t header, barrier, norm, diag_a, diag_b, xt[2], xm, a, b, total;
+  size_t header, barrier, norm, diag_a, diag_b, xt[2], xl, a, b, total;
 };
 
 inline OrthoShape make_ortho_shape(int64_t batch, int64_t rows, int64_t cols) {
@@ -98,7 +98,7 @@ inline OrthoLayout make_ortho_layout(const OrthoShape& s) {
   L.diag_b = take(s.batch * s.ld * 4);
   L.xt[0] = take(s.batch * s.c * s.ld * 2);
   L.xt[1] = take(s.batch * s.c * s.ld * 2);
-  L.xm = take(s.batch * s.c * s.ld * 4);
+  L.xl = take(s.batch * s.c * s.ld * 2);
   L.a = take(s.batch * s.r * s.ld * 2);
   L.b = take(s.batch * s.r * s.ld * 2);
   L.total = off;

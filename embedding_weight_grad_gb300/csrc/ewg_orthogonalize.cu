@@ -11,19 +11,19 @@
 //
 // Precision.  The products run on the tensor cores with fp16 operands (11 significant bits) and
 // fp32 accumulators.  What keeps the result near its bf16 rounding:
-//   * X itself is kept in fp32 beside the fp16 copy that feeds the products; a X is
-//     taken from it.  Directions with small singular values, which the steps enlarge by up
+//   * X itself is kept to 22 bits: beside the fp16 numbers that feed the products, a second
+//     fp16 number each holds what their rounding left; a X is taken from the sum.  Directions with small singular values, which the steps enlarge by up
 //     to a^5 = 485, then carry no noise from the rounding of the large ones: B is small on
 //     them.  Without it a matrix of low effective rank loses ten times the precision.
 //   * The diagonals of A and B, their largest entries, are kept apart in fp32 and the fp16
 //     matrices have zeros there: with A = D + O, A^2 = O O + D O + O D + D^2, and
-//     B X = offdiag(B) X + diag(B) X with the fp32 X.
+//     B X = offdiag(B) X + diag(B) X with the 22-bit X.
 //   * Everything stored in fp16 is scaled by powers of two or by the norm: X by
 //     s ~ sqrt(r c), so its entries are about 1 at first and at most 1.2 s, and A, B by
 //     rho ~ r / 16.
 //
-// Layout.  Every buffer is [., ld] with the r index inside: X^T in fp16 (two, alternating)
-// and fp32, A and B.  The accumulator of a product has its row index across the lanes of a
+// Layout.  Every buffer is [., ld] fp16 with the r index inside: X^T (two, alternating), the
+// rest of X^T, A and B.  The accumulator of a product has its row index across the lanes of a
 // warp, so all stores of X^T and of the mirrored blocks are contiguous.  As an operand of X
 // X^T, X^T has the product's rows inside (MN-major); for B X it has the inner index inside
 // (K-major), as A and B have by symmetry.
@@ -53,15 +53,22 @@ struct OrthoIn {
   long long batch_stride, row_stride;
   int rows, cols;
   int ld;
-  long long xt_batch, xm_batch;      // elements between matrices
+  long long x_batch;                 // elements between matrices of X^T
   float s;                           // X is stored times s
   double* norm;                      // [batch][norm_blocks] sums of squares
   int norm_blocks;
   __half* xt;
-  float* xm;
+  __half* xl;
   Header* header;
   int* barrier;
 };
+
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float half_lo(uint32_t w) { return __half2float(__ushort_as_half(w & 0xffffu)); }
+__device__ __forceinline__ float half_hi(uint32_t w) { return __half2float(__ushort_as_half(w >> 16)); }
 
 __device__ __forceinline__ float grad_at(const OrthoIn& a, long long i) {
   return a.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.grad)[i])
@@ -163,16 +170,49 @@ __global__ void __launch_bounds__(256) ortho_norm_kernel(const OrthoIn a) {
   }
 }
 
-// X^T times s / |G| in fp16 and fp32, by 64 x 64 tiles of G.
+// X^T times s / |G|, split into two fp16 numbers, by 64 x 64 tiles of G.  Bound by the read of G
+// and the two writes.
 __global__ void __launch_bounds__(256) ortho_scale_kernel(const OrthoIn a) {
   __shared__ float tile[64][65];
   __shared__ double factor;
-  if (threadIdx.x < 32) {
+  const int tid = threadIdx.x;
+  const int row0 = blockIdx.y * 64, col0 = blockIdx.x * 64;
+  // 16 bytes of G a thread, all of its part of the tile before the wait for the norm
+  const int per = a.bf16 ? 8 : 4;                    // elements of a vector
+  const int line = 64 / per, rows = 256 / line;      // threads to a row, rows at once
+  const int cx = tid % line * per, ry = tid / line;
+  const int es = a.bf16 ? 2 : 4;
+  const char* base = static_cast<const char*>(a.grad) +
+                     (blockIdx.z * a.batch_stride + static_cast<long long>(row0) * a.row_stride + col0) * es;
+#pragma unroll 4
+  for (int k = ry; k < 64; k += rows) {
+    if (row0 + k >= a.rows) break;
+    const char* p = base + (k * a.row_stride + cx) * es;
+    const int n = a.cols - col0 - cx;
+    if (n >= per && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (a.bf16) {
+          tile[k][cx + 2 * q] = __uint_as_float(w[q] << 16);
+          tile[k][cx + 2 * q + 1] = __uint_as_float(w[q] & 0xffff0000u);
+        } else {
+          tile[k][cx + q] = __uint_as_float(w[q]);
+        }
+      }
+    } else {
+      for (int q = 0; q < per && q < n; ++q)
+        tile[k][cx + q] = a.bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[q])
+                                 : reinterpret_cast<const float*>(p)[q];
+    }
+  }
+  if (tid < 32) {
     double sum = 0.0;
-    for (int i = threadIdx.x; i < a.norm_blocks; i += 32) sum += a.norm[blockIdx.z * a.norm_blocks + i];
+    for (int i = tid; i < a.norm_blocks; i += 32) sum += a.norm[blockIdx.z * a.norm_blocks + i];
 #pragma unroll
     for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
-    if (threadIdx.x == 0) factor = sum == 0.0 ? 0.0 : a.s / sqrt(sum);   // a zero matrix stays zero
+    if (tid == 0) factor = sum == 0.0 ? 0.0 : a.s / sqrt(sum);   // a zero matrix stays zero
   }
   __syncthreads();
   // factor = f1 f2 with f1 a power of two, so that neither product leaves fp32's range
@@ -181,27 +221,29 @@ __global__ void __launch_bounds__(256) ortho_scale_kernel(const OrthoIn a) {
   const int e1 = min(max(e, -120), 120);
   const float f1 = ldexpf(1.0f, e1);
   const float f3 = ldexpf(f2, min(max(e - e1, -126), 126));
-  const int row0 = blockIdx.y * 64, col0 = blockIdx.x * 64;
-  const int tx = threadIdx.x % 64, ty = threadIdx.x / 64;
-  const long long base = blockIdx.z * a.batch_stride;
-#pragma unroll 4
-  for (int k = ty; k < 64; k += 4) {
-    const int i = row0 + k, j = col0 + tx;
-    if (i < a.rows && j < a.cols) tile[k][tx] = grad_at(a, base + i * a.row_stride + j) * f1 * f3;
-  }
-  __syncthreads();
-  __half* xt = a.xt + blockIdx.z * a.xt_batch;
-  float* xm = a.xm + blockIdx.z * a.xm_batch;
-#pragma unroll 4
-  for (int k = ty; k < 64; k += 4) {
-    // the r index is G's column where G is tall, else its row
-    const int outer = (a.tall ? row0 : col0) + k, inner = (a.tall ? col0 : row0) + tx;
-    if (outer < (a.tall ? a.rows : a.cols) && inner < (a.tall ? a.cols : a.rows)) {
-      const float x = a.tall ? tile[k][tx] : tile[tx][k];
-      const long long at = static_cast<long long>(outer) * a.ld + inner;
-      xt[at] = __float2half_rn(x);
-      xm[at] = x;
+  // the r index is G's column where G is tall, else its row
+  const int outer0 = a.tall ? row0 : col0, inner0 = a.tall ? col0 : row0;
+  const int outers = a.tall ? a.rows : a.cols, inners = a.tall ? a.cols : a.rows;
+  const int x = tid % 8 * 8;
+  if (inner0 + x >= a.ld) return;
+#pragma unroll
+  for (int k = tid / 8; k < 64; k += 32) {
+    if (outer0 + k >= outers) break;
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float v[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int in = x + 2 * q + h;
+        v[h] = inner0 + in < inners ? (a.tall ? tile[k][in] : tile[in][k]) * f1 * f3 : 0.0f;
+      }
+      hi[q] = pack_half(v[0], v[1]);
+      lo[q] = pack_half(v[0] - half_lo(hi[q]), v[1] - half_hi(hi[q]));
     }
+    const long long at = blockIdx.z * a.x_batch + static_cast<long long>(outer0 + k) * a.ld + inner0 + x;
+    *reinterpret_cast<uint4*>(a.xt + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(a.xl + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
 }
 
@@ -215,13 +257,14 @@ constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kBoxBytes = 64 * kStepK * 2;            // one tensor copy: 64 rows of 128 bytes
 constexpr int kEpilogueWarps = 8;
 constexpr int kGemmThreads = 128 + 32 * kEpilogueWarps;
-// Epilogue staging of one warp: pieces of 32 rows x kPiece columns.  Three buffers for what a
-// piece reads (X in fp32, or O) and, for X, its result in place; two for the fp16 result.
+// Epilogue staging of one warp: a ring of buffers for pieces of 32 rows x kPiece columns, two
+// fp16 numbers an element.  A piece's results replace its inputs.
 constexpr int kPiece = 16;
 constexpr int kPieces = 128 / kPiece;                 // of a warp's 128 columns
-constexpr int kBesideBytes = 32 * kPiece * 4;
 constexpr int kHalfBytes = 32 * kPiece * 2;
-constexpr int kWarpStaging = 3 * kBesideBytes + 2 * kHalfBytes;
+constexpr int kPieceBytes = 2 * kHalfBytes;
+constexpr int kRing = 4;
+constexpr int kWarpStaging = kRing * kPieceBytes;
 constexpr size_t kGemmSmem = static_cast<size_t>(kStages) * kStageBytes + kEpilogueWarps * kWarpStaging + 1024;
 static_assert(kGemmSmem + 512 <= 227 * 1024, "stages and staging fit in shared memory");
 constexpr uint32_t kWaitLimit = 1u << 22;
@@ -231,7 +274,7 @@ enum Phase { kGram = 0, kPoly = 1, kUpdate = 2 };
 
 struct OrthoMaps {
   CUtensorMap xt[2], a, b;                            // operands: boxes of 64 x 64, swizzled
-  CUtensorMap xt_piece[2], a_piece, b_piece, xm_piece;  // pieces: 32 of the r index, kPiece of the other
+  CUtensorMap xt_piece[2], xl_piece, a_piece, b_piece;  // pieces: 32 of the r index, kPiece of the other
   CUtensorMap a_mirror, b_mirror;                     // mirrored pieces: kPiece, 32
 };
 
@@ -251,7 +294,7 @@ struct OrthoArgs {
 
 struct GemmSmem {
   uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
-  uint64_t beside[kEpilogueWarps][3];
+  uint64_t piece[kEpilogueWarps][kRing];
   uint32_t tmem;
   int abort;
 };
@@ -309,51 +352,45 @@ __device__ void gave_up(const OrthoArgs& a, volatile int* abort) {
   atomicExch(&a.header->status, kStatusTimeout);
 }
 
-__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
 
-// Where a warp of the epilogue is: its staging, its copies, and which piece comes next.
+// Where a warp of the epilogue is: its staging ring and the pieces taken so far.
 struct EpilogueState {
-  uint32_t staging;                  // shared-memory addresses
-  uint64_t* bars;                    // of the three read buffers
-  uint32_t loads, uses;              // pieces requested and taken so far (of phases that read)
-  uint32_t stores;                   // pieces stored so far
+  uint32_t staging;                  // shared-memory address
+  uint64_t* bars;                    // one for each buffer: its inputs have come
+  uint32_t taken;                    // pieces taken; piece n uses buffer n % kRing
+  uint32_t parity;                   // bit b: parity of the next wait on buffer b
 };
 
-__device__ __forceinline__ float lds_f32(uint32_t at) {
-  float v;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
-  return v;
-}
 __device__ __forceinline__ float lds_half(uint32_t at) {
   uint16_t v;
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
   return __half2float(__ushort_as_half(v));
 }
-__device__ __forceinline__ void sts_f32(uint32_t at, float v) {
-  asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
-}
-__device__ __forceinline__ void sts_half(uint32_t at, float v) {
-  asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(__half_as_ushort(__float2half_rn(v))) : "memory");
+__device__ __forceinline__ void sts_half(uint32_t at, __half v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(__half_as_ushort(v)) : "memory");
 }
 __device__ __forceinline__ void sts_v4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// One lane requests what the piece at row i0, column j0 reads.
+// One lane requests the inputs of the warp's piece number n, at row i0 and column j0: X's two
+// parts for an update, O for B.
 template <int kPhase>
-__device__ __forceinline__ void request_piece(const OrthoMaps& maps, EpilogueState& st, int z, int i0, int j0) {
-  const uint32_t b = st.loads % 3;
-  ptx::mbar_arrive_expect_tx(&st.bars[b], kPhase == kUpdate ? kBesideBytes : kHalfBytes);
-  ptx::tma_load_3d(st.staging + b * kBesideBytes, kPhase == kUpdate ? &maps.xm_piece : &maps.a_piece, i0, j0, z,
-                   &st.bars[b]);
+__device__ __forceinline__ void request_piece(const OrthoMaps& maps, const EpilogueState& st, uint32_t n, int cur,
+                                              int z, int i0, int j0) {
+  const uint32_t b = n % kRing, to = st.staging + b * kPieceBytes;
+  ptx::mbar_arrive_expect_tx(&st.bars[b], kPhase == kUpdate ? kPieceBytes : kHalfBytes);
+  if constexpr (kPhase == kUpdate) {
+    ptx::tma_load_3d(to, &maps.xt_piece[cur], i0, j0, z, &st.bars[b]);
+    ptx::tma_load_3d(to + kHalfBytes, &maps.xl_piece, i0, j0, z, &st.bars[b]);
+  } else {
+    ptx::tma_load_3d(to, &maps.a_piece, i0, j0, z, &st.bars[b]);
+  }
 }
 
 // The last update's piece, to the caller's matrix.
@@ -396,10 +433,11 @@ __device__ __forceinline__ bool epilogue(const OrthoMaps& maps, const OrthoArgs&
   const int cols = kPhase == kUpdate ? a.c : a.r;
   const int pieces = i0 < a.r ? min(max((cols - j + kPiece - 1) / kPiece, 0), kPieces) : 0;
   const long long ld = a.ld;
+  const int cur = step & 1;
   const bool last = kPhase == kUpdate && step == a.steps - 1;
   if (kPhase != kGram && lane == 0) {
-    if (pieces > 0) request_piece<kPhase>(maps, st, x.z, i0, j), ++st.loads;
-    if (pieces > 1) request_piece<kPhase>(maps, st, x.z, i0, j + kPiece), ++st.loads;
+    for (int u = 0; u < 2 && u < pieces; ++u)
+      request_piece<kPhase>(maps, st, st.taken + u, cur, x.z, i0, j + u * kPiece);
   }
   float own = 0.0f, dj4[4] = {};
   if (kPhase == kUpdate && i < a.r) own = a.ca + a.diag_b[x.z * ld + i];
@@ -414,23 +452,28 @@ __device__ __forceinline__ bool epilogue(const OrthoMaps& maps, const OrthoArgs&
 #pragma unroll 1
   for (int u = 0; u < pieces; ++u) {
     const int j0 = j + u * kPiece;
+    const uint32_t b = st.taken % kRing;
+    const uint32_t buf = st.staging + b * kPieceBytes, at = buf + lane * 2;
     uint32_t acc[kPiece];
     float v[kPiece];
     ptx::tmem_load16(acc, from + u * kPiece);
-    uint32_t in = 0;
     if (kPhase != kGram) {
-      const uint32_t b = st.uses % 3;
-      if (!__all_sync(kAll, wait_bar(&st.bars[b], (st.uses / 3) & 1u, abort))) return false;
-      ++st.uses;
-      in = st.staging + b * kBesideBytes;
+      if (!__all_sync(kAll, wait_bar(&st.bars[b], (st.parity >> b) & 1u, abort))) return false;
+      st.parity ^= 1u << b;
     }
-    ptx::tmem_wait_load();
     if constexpr (kPhase == kUpdate) {
 #pragma unroll
-      for (int q = 0; q < kPiece; ++q)
-        v[q] = fmaf(own, lds_f32(in + (q * 32 + lane) * 4), __uint_as_float(acc[q]) * f);
+      for (int q = 0; q < kPiece; ++q) v[q] = lds_half(at + q * 64) + lds_half(at + kHalfBytes + q * 64);
+      ptx::tmem_wait_load();
+#pragma unroll
+      for (int q = 0; q < kPiece; ++q) v[q] = fmaf(own, v[q], __uint_as_float(acc[q]) * f);
     } else {
       const float dj_lane = u < 4 ? (u < 2 ? dj4[0] : dj4[1]) : (u < 6 ? dj4[2] : dj4[3]);
+      if constexpr (kPhase == kPoly) {
+#pragma unroll
+        for (int q = 0; q < kPiece; ++q) v[q] = lds_half(at + q * 64);
+      }
+      ptx::tmem_wait_load();
       float diag = 0.0f;             // the product on the diagonal
 #pragma unroll
       for (int q = 0; q < kPiece; ++q) {
@@ -441,7 +484,7 @@ __device__ __forceinline__ bool epilogue(const OrthoMaps& maps, const OrthoArgs&
           v[q] = p * f;
         } else {
           const float dj = __shfl_sync(kAll, dj_lane, (u & 1) * kPiece + q);
-          v[q] = fmaf(f, p, lds_half(in + (q * 32 + lane) * 2) * fmaf(a.cc, own + dj, a.cb));
+          v[q] = fmaf(f, p, v[q] * fmaf(a.cc, own + dj, a.cb));
         }
         if (on) v[q] = 0.0f;
       }
@@ -452,43 +495,42 @@ __device__ __forceinline__ bool epilogue(const OrthoMaps& maps, const OrthoArgs&
     }
     if (last) {
       store_out(a, x.z, i, j0, v);
-      __syncwarp();                  // the read buffer is free
-      if (lane == 0 && u + 2 < pieces) request_piece<kPhase>(maps, st, x.z, i0, j0 + 2 * kPiece), ++st.loads;
-      continue;
-    }
-    const uint32_t half = st.staging + 3 * kBesideBytes + (st.stores & 1u) * kHalfBytes;
-    // a mirrored piece goes to the second half of a read buffer, which O leaves free
-    const uint32_t mirror = st.staging + (st.stores % 3) * kBesideBytes + kHalfBytes;
+    } else {
 #pragma unroll
-    for (int q = 0; q < kPiece; ++q) {
-      if constexpr (kPhase == kUpdate) sts_f32(in + (q * 32 + lane) * 4, v[q]);
-      sts_half(half + (q * 32 + lane) * 2, v[q]);
-    }
-    if (kPhase != kUpdate && x.I != x.J) {
-      uint32_t w[kPiece / 2];
+      for (int q = 0; q < kPiece; ++q) {
+        const __half hi = __float2half_rn(v[q]);
+        sts_half(at + q * 64, hi);
+        if constexpr (kPhase == kUpdate) sts_half(at + kHalfBytes + q * 64, __float2half_rn(v[q] - __half2float(hi)));
+      }
+      if (kPhase != kUpdate && x.I != x.J) {          // mirrored, [row][column]
+        uint32_t w[kPiece / 2];
 #pragma unroll
-      for (int q = 0; q < kPiece / 2; ++q) w[q] = pack_half(v[2 * q], v[2 * q + 1]);
-      sts_v4(mirror + lane * kPiece * 2, w[0], w[1], w[2], w[3]);
-      sts_v4(mirror + lane * kPiece * 2 + 16, w[4], w[5], w[6], w[7]);
+        for (int q = 0; q < kPiece / 2; ++q) w[q] = pack_half(v[2 * q], v[2 * q + 1]);
+        const uint32_t m = buf + kHalfBytes + lane * kPiece * 2;
+        sts_v4(m, w[0], w[1], w[2], w[3]);
+        sts_v4(m + 16, w[4], w[5], w[6], w[7]);
+      }
+      ptx::fence_proxy_async_shared();
     }
-    ++st.stores;
-    ptx::fence_proxy_async_shared();
     __syncwarp();
     if (lane == 0) {
-      if constexpr (kPhase == kUpdate) {
-        ptx::tma_store_3d(&maps.xm_piece, i0, j0, x.z, in);
-        ptx::tma_store_3d(&maps.xt_piece[(step & 1) ^ 1], i0, j0, x.z, half);
-      } else {
-        ptx::tma_store_3d(kPhase == kGram ? &maps.a_piece : &maps.b_piece, i0, j0, x.z, half);
-        if (x.I != x.J) ptx::tma_store_3d(kPhase == kGram ? &maps.a_mirror : &maps.b_mirror, j0, i0, x.z, mirror);
+      if (!last) {
+        if constexpr (kPhase == kUpdate) {
+          ptx::tma_store_3d(&maps.xt_piece[cur ^ 1], i0, j0, x.z, buf);
+          ptx::tma_store_3d(&maps.xl_piece, i0, j0, x.z, buf + kHalfBytes);
+        } else {
+          ptx::tma_store_3d(kPhase == kGram ? &maps.a_piece : &maps.b_piece, i0, j0, x.z, buf);
+          if (x.I != x.J)
+            ptx::tma_store_3d(kPhase == kGram ? &maps.a_mirror : &maps.b_mirror, j0, i0, x.z, buf + kHalfBytes);
+        }
+        ptx::bulk_commit();
+        ptx::bulk_wait_read<kRing - 2>();   // the buffer of the piece after the next is free
       }
-      ptx::bulk_commit();
-      // the piece before this one has left its buffers, which the next ones take
-      ptx::bulk_wait_read<1>();
       if (kPhase != kGram && u + 2 < pieces)
-        request_piece<kPhase>(maps, st, x.z, i0, j0 + 2 * kPiece), ++st.loads;
+        request_piece<kPhase>(maps, st, st.taken + 2, cur, x.z, i0, j0 + 2 * kPiece);
     }
     __syncwarp();
+    ++st.taken;
   }
   return true;
 }
@@ -516,7 +558,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       ptx::mbar_init(&sm.acc_empty[i], 2 * kEpilogueWarps);
     }
     ptx::mbar_init(&sm.drained, 1);
-    for (int i = 0; i < 3 * kEpilogueWarps; ++i) ptx::mbar_init(&sm.beside[0][0] + i, 1);
+    for (int i = 0; i < kRing * kEpilogueWarps; ++i) ptx::mbar_init(&sm.piece[0][0] + i, 1);
     sm.abort = 0;
     ptx::fence_mbar_init();
     ptx::prefetch_tensor_map(&maps.xt[0]);
@@ -537,7 +579,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   EpilogueState st{};
   if (warp >= 4) {
     st.staging = stages + kStages * kStageBytes + (warp - 4) * kWarpStaging;
-    st.bars = sm.beside[warp - 4];
+    st.bars = sm.piece[warp - 4];
   }
 
   for (int p = 0; p < 3 * a.steps; ++p) {
@@ -687,16 +729,14 @@ using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
 EncodeTiled g_encode = nullptr;
 int g_pairs[64] = {};                // per device: pairs resident at once
 
-// [batch][outer][ld] with `inner` columns used, in boxes of box_x x box_y.
-cudaError_t encode(CUtensorMap* map, void* p, bool fp32, const OrthoShape& sh, int64_t outer, int box_x, int box_y,
+// [batch][outer][ld] fp16 with r columns used, in boxes of box_x x box_y.
+cudaError_t encode(CUtensorMap* map, void* p, const OrthoShape& sh, int64_t outer, int box_x, int box_y,
                    bool swizzle) {
-  const cuuint64_t es = fp32 ? 4 : 2;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(sh.r), static_cast<cuuint64_t>(outer),
                               static_cast<cuuint64_t>(sh.batch)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(sh.ld) * es, static_cast<cuuint64_t>(sh.ld * outer) * es};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(sh.ld * 2), static_cast<cuuint64_t>(sh.ld * outer * 2)};
   const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_x), static_cast<cuuint32_t>(box_y), 1}, step[3] = {1, 1, 1};
-  const CUresult r = g_encode(map, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, p,
-                              dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, p, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                               swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
@@ -749,31 +789,31 @@ cudaError_t launch_orthogonalize(const OrthoCall& q, cudaStream_t stream) {
   in.rows = static_cast<int>(sh.rows);
   in.cols = static_cast<int>(sh.cols);
   in.ld = static_cast<int>(sh.ld);
-  in.xt_batch = in.xm_batch = sh.c * sh.ld;
+  in.x_batch = sh.c * sh.ld;
   in.s = power_of_two_below(s);
   in.norm = reinterpret_cast<double*>(ws + L.norm);
   in.norm_blocks = sh.norm_blocks;
   in.xt = reinterpret_cast<__half*>(ws + L.xt[0]);
-  in.xm = reinterpret_cast<float*>(ws + L.xm);
+  in.xl = reinterpret_cast<__half*>(ws + L.xl);
   in.header = reinterpret_cast<Header*>(ws + L.header);
   in.barrier = reinterpret_cast<int*>(ws + L.barrier);
 
   OrthoMaps maps;
   cudaError_t e = cudaSuccess;
-  auto add = [&](CUtensorMap* map, size_t at, bool fp32, int64_t outer, int x, int y, bool swizzle) {
-    if (e == cudaSuccess) e = encode(map, ws + at, fp32, sh, outer, x, y, swizzle);
+  auto add = [&](CUtensorMap* map, size_t at, int64_t outer, int x, int y, bool swizzle) {
+    if (e == cudaSuccess) e = encode(map, ws + at, sh, outer, x, y, swizzle);
   };
   for (int i = 0; i < 2; ++i) {
-    add(&maps.xt[i], L.xt[i], false, sh.c, 64, 64, true);
-    add(&maps.xt_piece[i], L.xt[i], false, sh.c, 32, kPiece, false);
+    add(&maps.xt[i], L.xt[i], sh.c, 64, 64, true);
+    add(&maps.xt_piece[i], L.xt[i], sh.c, 32, kPiece, false);
   }
-  add(&maps.xm_piece, L.xm, true, sh.c, 32, kPiece, false);
-  add(&maps.a, L.a, false, sh.r, 64, 64, true);
-  add(&maps.a_piece, L.a, false, sh.r, 32, kPiece, false);
-  add(&maps.a_mirror, L.a, false, sh.r, kPiece, 32, false);
-  add(&maps.b, L.b, false, sh.r, 64, 64, true);
-  add(&maps.b_piece, L.b, false, sh.r, 32, kPiece, false);
-  add(&maps.b_mirror, L.b, false, sh.r, kPiece, 32, false);
+  add(&maps.xl_piece, L.xl, sh.c, 32, kPiece, false);
+  add(&maps.a, L.a, sh.r, 64, 64, true);
+  add(&maps.a_piece, L.a, sh.r, 32, kPiece, false);
+  add(&maps.a_mirror, L.a, sh.r, kPiece, 32, false);
+  add(&maps.b, L.b, sh.r, 64, 64, true);
+  add(&maps.b_piece, L.b, sh.r, 32, kPiece, false);
+  add(&maps.b_mirror, L.b, sh.r, kPiece, 32, false);
   if (e != cudaSuccess) return e;
 
   OrthoArgs a{};
