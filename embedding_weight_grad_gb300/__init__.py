@@ -381,40 +381,63 @@ def status_workspace(device=None) -> torch.Tensor:
     return torch.empty(256, dtype=torch.uint8, device=device or "cuda")
 
 
+# The current stream's handle without a Stream object around it (torch keeps this function
+# for generated code; the ordinary way is the fallback).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _enqueue(index, call, *args):
+    """call(*args, current stream) with device `index` current; raises on an error code."""
+    if index == torch.cuda.current_device():
+        code = call(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            code = call(*args, _raw_stream(index))
+    if code != OK:
+        _raise_on(code)
+
+
 def _logits_args(name, logits, targets):
-    """(num_tokens, vocab, [num_tokens, vocab] view, row stride) of logits [*targets.shape, vocab]."""
-    def no(reason):
-        raise ValueError(f"{name} does not support these tensors: {reason}")
-    if not (logits.is_cuda and targets.is_cuda) or logits.device != targets.device:
-        no("logits and targets must be on one CUDA device")
-    if logits.dtype not in _FLOAT_CODES or targets.dtype not in _ID_CODES:
-        no("logits must be bf16/fp32, targets int32/int64")
-    if logits.dim() == 0 or logits.shape[:-1] != targets.shape:
-        no("logits must be [*targets.shape, vocab]")
-    if not targets.is_contiguous():
-        no("targets must be contiguous")
-    n, V = targets.numel(), logits.shape[-1]
-    return n, V, *_rows(name, "logits", logits, n, V)
+    """(device index, num_tokens, vocab, row stride) of logits [*targets.shape, vocab]."""
+    index = logits.get_device()
+    shape = logits.shape
+    if index < 0 or targets.get_device() != index:
+        reason = "logits and targets must be on one CUDA device"
+    elif logits.dtype not in _FLOAT_CODES or targets.dtype not in _ID_CODES:
+        reason = "logits must be bf16/fp32, targets int32/int64"
+    elif len(shape) == 0 or shape[:-1] != targets.shape:
+        reason = "logits must be [*targets.shape, vocab]"
+    elif not targets.is_contiguous():
+        reason = "targets must be contiguous"
+    else:
+        n, V = targets.numel(), shape[-1]
+        return index, n, V, _row_stride(name, "logits", logits, n, V)
+    raise ValueError(f"{name} does not support these tensors: {reason}")
 
 
-def _rows(name, what, x, n, V):
-    """x [..., V] as [n, V] with unit inner stride, and its row stride; no copy."""
-    if x.dim() == 2 and (x.stride(1) == 1 or V <= 1):
-        return x, x.stride(0) if n > 1 else V
-    try:
-        x2 = x.view(n, V)
-    except RuntimeError:
-        x2 = None
-    if x2 is None or (x2.stride(1) != 1 and V > 1 and n > 0):
+def _row_stride(name, what, x, n, V):
+    """The stride between the n rows of x [..., V], whose elements are neighbours."""
+    if x.is_contiguous():
+        return V
+    if x.dim() != 2:
+        try:
+            x = x.view(n, V)
+        except RuntimeError:
+            x = None
+    if x is None or (x.stride(1) != 1 and V > 1 and n > 0):
         raise ValueError(f"{name} does not support these tensors: {what} must have rows of unit "
                          "inner stride that share one row stride")
-    return x2, x2.stride(0) if n > 1 else V
+    return x.stride(0) if n > 1 else V
 
 
 def _status_ws(workspace, check, device):
-    if workspace is None and check:
+    """(workspace, its pointer, its bytes); without one and without check there is none."""
+    if workspace is None:
+        if not check:
+            return None, None, 0
         workspace = status_workspace(device)
-    return workspace, (workspace.data_ptr(), workspace.numel()) if workspace is not None else (None, 0)
+    return workspace, workspace.data_ptr(), workspace.numel()
 
 
 def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, *, scale: float = 1.0,
@@ -431,23 +454,24 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, *, scale: float 
     (whose logprob is NaN).  workspace: status_workspace(), to read the status later with
     read_status.
     """
-    n, V, z, stride = _logits_args("token_logprobs", logits, targets)
+    index, n, V, stride = _logits_args("token_logprobs", logits, targets)
     if not 0 <= top <= min(V, MAX_TOP):
         raise ValueError(f"top must be in [0, min(vocab, {MAX_TOP})]")
-    shape = targets.shape
-    out = torch.empty((4, *shape), dtype=torch.float32, device=logits.device).unbind(0)
-    top_z = torch.empty((*shape, top), dtype=torch.float32, device=logits.device) if top else None
-    top_i = torch.empty((*shape, top), dtype=torch.int64, device=logits.device) if top else None
-    with torch.cuda.device(logits.device):
-        ws, ws_args = _status_ws(workspace, check, logits.device)
-        _raise_on(lib().ewg_token_logprobs(
-            z.data_ptr(), _FLOAT_CODES[z.dtype], stride, targets.data_ptr(),
-            _ID_CODES[targets.dtype], n, V, scale, top, *(o.data_ptr() for o in out),
-            top_z.data_ptr() if top else None, top_i.data_ptr() if top else None, *ws_args,
-            _stream_ptr(logits.device)))
-        if check and n:
-            raise_on_device_status(ws)
-    return TokenLogprobs(*out, top_z, top_i)
+    device, shape = logits.device, targets.shape
+    stats = torch.empty((4, *shape), dtype=torch.float32, device=device)
+    at, step = stats.data_ptr(), 4 * n
+    top_logprobs = top_ids = None
+    if top:
+        top_logprobs = torch.empty((*shape, top), dtype=torch.float32, device=device)
+        top_ids = torch.empty((*shape, top), dtype=torch.int64, device=device)
+    ws, ws_ptr, ws_bytes = _status_ws(workspace, check, device)
+    _enqueue(index, lib().ewg_token_logprobs, logits.data_ptr(), _FLOAT_CODES[logits.dtype], stride,
+             targets.data_ptr(), _ID_CODES[targets.dtype], n, V, scale, top, at, at + step,
+             at + 2 * step, at + 3 * step, top_logprobs.data_ptr() if top else None,
+             top_ids.data_ptr() if top else None, ws_ptr, ws_bytes)
+    if check and n:
+        raise_on_device_status(ws)
+    return TokenLogprobs(*stats.unbind(0), top_logprobs, top_ids)
 
 
 def token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor, row_max: torch.Tensor,
@@ -467,32 +491,35 @@ def token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor, row_max
     it the gradient is allocated, with the logits' row padding where that is less than an
     eighth of a row.  Padding rows get zeros.
     """
-    n, V, z, stride = _logits_args("token_logprobs_backward", logits, targets)
+    index, n, V, stride = _logits_args("token_logprobs_backward", logits, targets)
     if grad_entropy is not None and entropy is None:
         raise ValueError("grad_entropy needs the forward call's entropy")
-    stats = [row_max, log_sum, grad_logprobs] + ([entropy, grad_entropy] if grad_entropy is not None else [])
-    for t in stats:
-        if t.shape != targets.shape or t.dtype != torch.float32 or t.device != logits.device \
+    shape = targets.shape
+    for t in (row_max, log_sum, grad_logprobs) if grad_entropy is None else \
+            (row_max, log_sum, grad_logprobs, entropy, grad_entropy):
+        if t.shape != shape or t.dtype != torch.float32 or t.get_device() != index \
                 or not t.is_contiguous():
             raise ValueError("row_max, log_sum, entropy and the incoming gradients must be contiguous "
                              "fp32 tensors of the targets' shape on the logits' device")
     if out is None:
-        # rows placed like the logits' rows, so that both are read and written in whole vectors
-        pitch = stride if V <= stride <= V + V // 8 else V
-        out = torch.empty((*targets.shape, pitch), dtype=logits.dtype, device=logits.device)[..., :V]
-    elif out.shape != logits.shape or out.dtype != logits.dtype or out.device != logits.device:
-        raise ValueError("out must have the logits' shape, dtype and device")
-    g, g_stride = _rows("token_logprobs_backward", "out", out, n, V)
-    with torch.cuda.device(logits.device):
-        ws, ws_args = _status_ws(workspace, check, logits.device)
-        _raise_on(lib().ewg_token_logprobs_backward(
-            z.data_ptr(), _FLOAT_CODES[z.dtype], stride, targets.data_ptr(),
-            _ID_CODES[targets.dtype], n, V, scale, row_max.data_ptr(), log_sum.data_ptr(),
-            entropy.data_ptr() if grad_entropy is not None else None, grad_logprobs.data_ptr(),
-            grad_entropy.data_ptr() if grad_entropy is not None else None, g.data_ptr(), g_stride,
-            *ws_args, _stream_ptr(logits.device)))
-        if check and n:
-            raise_on_device_status(ws)
+        if stride == V or stride > V + V // 8:
+            out, out_stride = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device), V
+        else:
+            # rows placed like the logits' rows, so that both are read and written in whole vectors
+            out = torch.empty((*shape, stride), dtype=logits.dtype, device=logits.device)[..., :V]
+            out_stride = stride
+    else:
+        if out.shape != logits.shape or out.dtype != logits.dtype or out.get_device() != index:
+            raise ValueError("out must have the logits' shape, dtype and device")
+        out_stride = _row_stride("token_logprobs_backward", "out", out, n, V)
+    ws, ws_ptr, ws_bytes = _status_ws(workspace, check, logits.device)
+    both = grad_entropy is not None
+    _enqueue(index, lib().ewg_token_logprobs_backward, logits.data_ptr(), _FLOAT_CODES[logits.dtype],
+             stride, targets.data_ptr(), _ID_CODES[targets.dtype], n, V, scale, row_max.data_ptr(),
+             log_sum.data_ptr(), entropy.data_ptr() if both else None, grad_logprobs.data_ptr(),
+             grad_entropy.data_ptr() if both else None, out.data_ptr(), out_stride, ws_ptr, ws_bytes)
+    if check and n:
+        raise_on_device_status(ws)
     return out
 
 
@@ -550,12 +577,10 @@ def orthogonalize_update(grad: torch.Tensor, *, steps: int = 5,
         return out
     g3, o3 = _matrices("grad", grad), _matrices("out", out)
     batch, rows, cols = g3.shape
-    with torch.cuda.device(grad.device):
-        ws = workspace if workspace is not None else orthogonalize_workspace(grad.shape, grad.device)
-        _raise_on(lib().ewg_orthogonalize(
-            g3.data_ptr(), _FLOAT_CODES[grad.dtype], batch, rows, cols, g3.stride(0),
-            g3.stride(1), o3.data_ptr(), o3.stride(0), o3.stride(1), steps, *coefficients,
-            ws.data_ptr(), ws.numel(), _stream_ptr(grad.device)))
-        if check:
-            raise_on_device_status(ws)
+    ws = workspace if workspace is not None else orthogonalize_workspace(grad.shape, grad.device)
+    _enqueue(grad.get_device(), lib().ewg_orthogonalize, g3.data_ptr(), _FLOAT_CODES[grad.dtype],
+             batch, rows, cols, g3.stride(0), g3.stride(1), o3.data_ptr(), o3.stride(0),
+             o3.stride(1), steps, *coefficients, ws.data_ptr(), ws.numel())
+    if check:
+        raise_on_device_status(ws)
     return out

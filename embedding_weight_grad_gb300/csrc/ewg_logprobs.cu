@@ -188,38 +188,68 @@ struct Stats {
   float m, R, T;
 };
 
-// The list of a warp's best candidates: lane l holds the l-th best key.  Keys order by
-// logit, then by lower id; 0 is "none".
-__device__ __forceinline__ unsigned long long key_of(float z, uint32_t id) {
-  return (static_cast<unsigned long long>(order_of(z)) << 32) | (~id);
+// Keys order candidates by logit, then by lower id; 0 is "none".  A list of best candidates
+// is a warp's: lane l holds the l-th best key.
+using Key = unsigned long long;
+
+__device__ __forceinline__ Key key_of(float z, uint32_t id) {
+  return (static_cast<Key>(order_of(z)) << 32) | (~id);
 }
 
-// Inserts the keys of all lanes (0: nothing) that belong among the best `top`.
-__device__ __forceinline__ void insert_keys(unsigned long long& list, unsigned long long& worst,
-                                            unsigned long long key, int top, int lane) {
+// Compare-exchange with the lane `distance` away: the larger key stays where `larger`.
+__device__ __forceinline__ Key exchange(Key k, int distance, bool larger) {
+  const Key o = __shfl_xor_sync(kAll, k, distance);
+  return (o > k) == larger ? o : k;
+}
+
+// The lanes' keys as a list, best first (bitonic network).
+__device__ __forceinline__ Key sort_keys(Key k, int lane) {
+#pragma unroll
+  for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+    for (int d = size / 2; d; d /= 2) k = exchange(k, d, ((lane & d) == 0) == ((lane & size) == 0 || size == 32));
+  return k;
+}
+
+// The best 32 of two lists, as a list.
+__device__ __forceinline__ Key merge_lists(Key a, Key b, int lane) {
+  const Key r = __shfl_sync(kAll, b, 31 - lane);
+  Key k = a > r ? a : r;
+#pragma unroll
+  for (int d = 16; d; d /= 2) k = exchange(k, d, (lane & d) == 0);
+  return k;
+}
+
+// Inserts the lanes' keys (0: nothing) into a list, one after the other, while they belong
+// among its best `top`; `worst` is the list's top-th key.
+__device__ __forceinline__ void insert_keys(Key& list, Key& worst, Key key, int top, int lane) {
   unsigned mask = __ballot_sync(kAll, key > worst);
   while (mask) {
     const int src = __ffs(mask) - 1;
     mask &= mask - 1;
-    const unsigned long long k = __shfl_sync(kAll, key, src);
+    const Key k = __shfl_sync(kAll, key, src);
     if (k <= worst) continue;                       // the list has improved meanwhile
     const int pos = __popc(__ballot_sync(kAll, list > k));
-    const unsigned long long above = __shfl_up_sync(kAll, list, 1);
+    const Key above = __shfl_up_sync(kAll, list, 1);
     list = lane < pos ? list : lane == pos ? k : above;
     worst = __shfl_sync(kAll, list, top - 1);
   }
 }
 
 constexpr int kBatch = 4;            // vectors a thread has in flight
+constexpr int kMaxCluster = 8;       // blocks that share a row, at most
 
 template <int kT>
 struct GroupSmem {
   static constexpr int kWarps = kT / 32;
-  unsigned long long lists[kWarps][kMaxTop];
-  uint32_t maxima[kT];               // order_of the threads' maxima
+  static constexpr int kSets = kT < 64 ? kT : 64;    // sets of neighbouring threads
+  static constexpr int kCandidates = kT == 512 ? 256 : 64;
+  alignas(16) uint32_t maxima[kSets];   // order_of the sets' maxima
   uint32_t tau;
-  int num_tasks;
+  int num_tasks, num_candidates;
   uint16_t tasks[kT];
+  Key candidates[kCandidates];
+  Key lists[kWarps][32];
   uint32_t warp_max[kWarps];
   float warp_s[kWarps], warp_t[kWarps], warp_own[kWarps];
   int warp_holds[kWarps];            // whether the warp has the maximum
@@ -227,7 +257,7 @@ struct GroupSmem {
   float own_again;
   // what the other blocks of the cluster read
   Stats stats;
-  unsigned long long best[kMaxTop];
+  Key best[32];
 };
 
 // Forward kernel.  kT threads take a row (kT = 32: a warp, eight rows to a block; else one
@@ -237,10 +267,12 @@ struct GroupSmem {
 // One pass over the row: each thread keeps a running maximum, the sum of exponentials and
 // the sum of exponential * exponent over its vectors, rescaled once per batch of kBatch
 // vectors.  The alternatives cost the pass nothing: afterwards the top-th largest of the
-// threads' maxima bounds the row's top-th largest logit from below, and only threads whose
-// maximum reaches it (about `top` of them) can hold one; their vectors are read again (from
-// L2), a warp to a thread's vectors.  In the same way the vectors of the thread that holds the
-// maximum are summed again without it where its own term would drown the others (R < 8).
+// maxima of 64 sets of threads bounds the row's top-th largest logit from below (tau), and only
+// threads whose maximum reaches it (about `top` of them) can hold one; their vectors are
+// read again (from L2), the logits that reach tau collected (about 1.3 top of them) and sorted.
+// Where ties make them too many to collect, they are inserted into lists one by one.  In the
+// same way the vectors of the thread that holds the maximum are summed again without it
+// where its own term would drown the others (R < 8).
 template <typename T, int kT>
 __global__ void __launch_bounds__(kT == 32 ? 256 : kT) logprobs_kernel(const LogprobsArgs a) {
   using V = Vec<T>;
@@ -336,14 +368,19 @@ __global__ void __launch_bounds__(kT == 32 ? 256 : kT) logprobs_kernel(const Log
 
   // ---- the group's maximum
   uint32_t om = __reduce_max_sync(kAll, order_of(warp == 0 ? fmaxf(m, edge) : m));
-  if (top) sm.maxima[tid] = order_of(m);
+  if (top) {
+    constexpr int kSet = kT / GroupSmem<kT>::kSets;
+    float set = m;
+#pragma unroll
+    for (int d = kSet / 2; d; d /= 2) set = fmaxf(set, __shfl_xor_sync(kAll, set, d));
+    if (tid % kSet == 0) sm.maxima[tid / kSet] = order_of(set);
+  }
+  if (tid == 0) sm.num_tasks = sm.num_candidates = 0;
   if constexpr (kWarps > 1) {
     if (lane == 0) sm.warp_max[warp] = om;
-    if (tid == 0) sm.num_tasks = 0;
     sync();
     om = __reduce_max_sync(kAll, lane < kWarps ? sm.warp_max[lane] : 0u);
   } else {
-    if (tid == 0) sm.num_tasks = 0;
     sync();
   }
   const float M = fmaxf(float_of(om), -FLT_MAX);
@@ -413,34 +450,21 @@ __global__ void __launch_bounds__(kT == 32 ? 256 : kT) logprobs_kernel(const Log
   Stats st{M, s + own, t};
 
   // ---- the group's best candidates
-  unsigned long long list = 0, worst = 0;
+  Key list = 0;
   if (top) {
-    // tau: the top-th largest of the threads' maxima
-    sync();
-    if (warp == 0) {
-      uint32_t mine[kWarps], best = 0;
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) {
-        mine[i] = sm.maxima[i * 32 + lane];
-        best = max(best, mine[i]);
+    // tau: the top-th largest of the sets' maxima (there are `top` sets or more)
+    constexpr int kSets = GroupSmem<kT>::kSets, kCandidates = GroupSmem<kT>::kCandidates;
+    if (tid < kSets) {
+      const uint32_t mine = sm.maxima[tid];
+      int above = 0, not_below = 0;
+      const uint4* all = reinterpret_cast<const uint4*>(sm.maxima);
+#pragma unroll 4
+      for (int i = 0; i < kSets / 4; ++i) {
+        const uint4 w = all[i];
+        above += (w.x > mine) + (w.y > mine) + (w.z > mine) + (w.w > mine);
+        not_below += (w.x >= mine) + (w.y >= mine) + (w.z >= mine) + (w.w >= mine);
       }
-      int left = top;
-      uint32_t tau;
-      while (true) {
-        tau = __reduce_max_sync(kAll, best);
-        int equal = 0;
-        uint32_t next = 0;
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-          equal += mine[i] == tau;
-          if (mine[i] < tau) next = max(next, mine[i]);
-        }
-        left -= __reduce_add_sync(kAll, equal);
-        if (left <= 0) break;
-        if (best == tau) best = next;               // the lane's next smaller distinct value
-        if (__reduce_max_sync(kAll, best) == 0) break;   // fewer threads than alternatives
-      }
-      if (lane == 0) sm.tau = tau;
+      if (above < top && top <= not_below) sm.tau = mine;       // equal ones write the same
     }
     sync();
     const uint32_t tau = sm.tau;
@@ -448,26 +472,70 @@ __global__ void __launch_bounds__(kT == 32 ? 256 : kT) logprobs_kernel(const Log
     if (order_of(m) >= tau) sm.tasks[atomicAdd(&sm.num_tasks, 1)] = static_cast<uint16_t>(tid);
     sync();
     const int tasks = sm.num_tasks;
-    for (int i = warp; i < tasks; i += kWarps) {
-      for (int vb = v0 + sm.tasks[i]; vb < v1; vb += 32 * kT) {
-        const int v = vb + lane * kT;
-        const uint4 raw = v < v1 ? load16(zv + v) : make_uint4(V::kNegInf, V::kNegInf, V::kNegInf, V::kNegInf);
-        if (!__any_sync(kAll, V::max_of(raw) >= tau_f)) continue;
+    // a warp takes as many threads' vectors at once as it has lanes for
+    const int length = (v1 - v0 + kT - 1) / kT;
+    int width = 1;
+    while (width < 32 && width < length) width *= 2;
+    auto offer = [&](float x, uint32_t id) {
+      if (!(x >= tau_f)) return;
+      const int at = atomicAdd(&sm.num_candidates, 1);
+      if (at < kCandidates) sm.candidates[at] = key_of(x, id);
+    };
+    for (int i = (warp * 32 + lane) / width; i < tasks; i += kT / width) {
+      for (int v = v0 + sm.tasks[i] + lane % width * kT; v < v1; v += width * kT) {
+        const uint4 raw = load16(zv + v);
+        if (V::max_of(raw) < tau_f) continue;
         const uint32_t id = head + v * kE;
 #pragma unroll
-        for (int e = 0; e < kE; ++e) {
-          const float2 p = V::pair(raw, e / 2);
-          const float x = e % 2 ? p.y : p.x;
-          insert_keys(list, worst, x >= tau_f ? key_of(x, id + e) : 0ull, top, lane);
+        for (int e = 0; e < kE / 2; ++e) {
+          const float2 p = V::pair(raw, e);
+          offer(p.x, id + 2 * e);
+          offer(p.y, id + 2 * e + 1);
         }
       }
     }
-    if (warp == 0) insert_keys(list, worst, edge >= -FLT_MAX ? key_of(edge, edge_id) : 0ull, top, lane);
-    if constexpr (kWarps > 1) {
-      if (lane < top) sm.lists[warp][lane] = list;
-      sync();
-      if (warp == 0) {
-        for (int w = 1; w < kWarps; ++w) insert_keys(list, worst, lane < top ? sm.lists[w][lane] : 0ull, top, lane);
+    if (warp == 0 && lane < edges) offer(edge, edge_id);
+    sync();
+    const int found = sm.num_candidates;
+    if (found <= kCandidates) {
+      if (warp * 32 < found || warp == 0) {
+        const int at = warp * 32 + lane;
+        list = sort_keys(at < found ? sm.candidates[at] : 0, lane);
+      }
+      if (found > 32) {
+        if constexpr (kWarps > 1) {
+          if (warp * 32 < found) sm.lists[warp][lane] = list;
+          sync();
+          if (warp == 0)
+            for (int w = 1; w * 32 < found && w < kWarps; ++w) list = merge_lists(list, sm.lists[w][lane], lane);
+        } else {
+          for (int at = 32; at < found; at += 32)
+            list = merge_lists(list, sort_keys(at + lane < found ? sm.candidates[at + lane] : 0, lane), lane);
+        }
+      }
+    } else {
+      Key worst = 0;
+      for (int i = warp; i < tasks; i += kWarps) {
+        for (int vb = v0 + sm.tasks[i]; vb < v1; vb += 32 * kT) {
+          const int v = vb + lane * kT;
+          const uint4 raw = v < v1 ? load16(zv + v) : make_uint4(V::kNegInf, V::kNegInf, V::kNegInf, V::kNegInf);
+          const uint32_t id = head + v * kE;
+#pragma unroll
+          for (int e = 0; e < kE; ++e) {
+            const float2 p = V::pair(raw, e / 2);
+            const float x = e % 2 ? p.y : p.x;
+            insert_keys(list, worst, x >= tau_f ? key_of(x, id + e) : 0, top, lane);
+          }
+        }
+      }
+      if (warp == 0) insert_keys(list, worst, edge >= tau_f ? key_of(edge, edge_id) : 0, top, lane);
+      if constexpr (kWarps > 1) {
+        sm.lists[warp][lane] = lane < top ? list : 0;
+        sync();
+        if (warp == 0) {
+          list = lane < top ? list : 0;
+          for (int w = 1; w < kWarps; ++w) list = merge_lists(list, sm.lists[w][lane], lane);
+        }
       }
     }
   }
@@ -477,7 +545,7 @@ __global__ void __launch_bounds__(kT == 32 ? 256 : kT) logprobs_kernel(const Log
     if (C > 1) {
       cg::cluster_group cluster = cg::this_cluster();
       if (tid == 0) sm.stats = st;
-      if (warp == 0 && lane < top) sm.best[lane] = list;
+      if (warp == 0) sm.best[lane] = list;
       cluster.sync();
       if (rank == 0 && warp == 0) {
         Stats other{-FLT_MAX, -1.0f, 0.0f};
@@ -489,9 +557,13 @@ __global__ void __launch_bounds__(kT == 32 ? 256 : kT) logprobs_kernel(const Log
         const float r = warp_sum(lane == first ? other.R : f * (1.0f + other.R));
         const float tt = warp_sum(f * (other.T + d * (1.0f + other.R)));
         st = Stats{Mg, r, tt};
-        for (int q = 1; q < C && top; ++q) {
-          const unsigned long long* theirs = cluster.map_shared_rank(&sm.best[0], q);
-          insert_keys(list, worst, lane < top ? theirs[lane] : 0ull, top, lane);
+        if (top) {
+          Key theirs[kMaxCluster];
+#pragma unroll
+          for (int q = 1; q < kMaxCluster; ++q) theirs[q] = q < C ? cluster.map_shared_rank(&sm.best[0], q)[lane] : 0;
+#pragma unroll
+          for (int q = 1; q < kMaxCluster; ++q)
+            if (q < C) list = merge_lists(list, theirs[q], lane);
         }
       }
       cluster.sync();                // the blocks' shared memory stays until it has been read
@@ -662,7 +734,7 @@ cudaError_t launch_forward_of(const LogprobsArgs& a, int num_sms, cudaStream_t s
   if (nv <= 2048 && a.n >= num_sms) return launch_forward<T, 128>(a, 1, stream);
   // few rows: up to 8 blocks a row, each thread with a vector at least
   int cluster = 1;
-  while (cluster < 8 && static_cast<long long>(a.n) * cluster < num_sms && nv / (2 * cluster) >= 512) cluster *= 2;
+  while (cluster < kMaxCluster && static_cast<long long>(a.n) * cluster < num_sms && nv / (2 * cluster) >= 512) cluster *= 2;
   return launch_forward<T, 512>(a, cluster, stream);
 }
 
