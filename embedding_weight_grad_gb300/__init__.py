@@ -458,20 +458,20 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, *, scale: float 
     if not 0 <= top <= min(V, MAX_TOP):
         raise ValueError(f"top must be in [0, min(vocab, {MAX_TOP})]")
     device, shape = logits.device, targets.shape
-    stats = torch.empty((4, *shape), dtype=torch.float32, device=device)
-    at, step = stats.data_ptr(), 4 * n
+    # (separate allocations: views of one take longer to make)
+    stats = [torch.empty(shape, dtype=torch.float32, device=device) for _ in range(4)]
     top_logprobs = top_ids = None
     if top:
         top_logprobs = torch.empty((*shape, top), dtype=torch.float32, device=device)
         top_ids = torch.empty((*shape, top), dtype=torch.int64, device=device)
     ws, ws_ptr, ws_bytes = _status_ws(workspace, check, device)
     _enqueue(index, lib().ewg_token_logprobs, logits.data_ptr(), _FLOAT_CODES[logits.dtype], stride,
-             targets.data_ptr(), _ID_CODES[targets.dtype], n, V, scale, top, at, at + step,
-             at + 2 * step, at + 3 * step, top_logprobs.data_ptr() if top else None,
+             targets.data_ptr(), _ID_CODES[targets.dtype], n, V, scale, top,
+             *[s.data_ptr() for s in stats], top_logprobs.data_ptr() if top else None,
              top_ids.data_ptr() if top else None, ws_ptr, ws_bytes)
     if check and n:
         raise_on_device_status(ws)
-    return TokenLogprobs(*stats.unbind(0), top_logprobs, top_ids)
+    return TokenLogprobs(*stats, top_logprobs, top_ids)
 
 
 def token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor, row_max: torch.Tensor,

@@ -273,8 +273,12 @@ struct GroupSmem {
 // Where ties make them too many to collect, they are inserted into lists one by one.  In the
 // same way the vectors of the thread that holds the maximum are summed again without it
 // where its own term would drown the others (R < 8).
+//
+// 1536 threads on an SM (40 registers each): with 1280 or 2048 the large rows lose 4 to 8 %.
+constexpr int threads_of(int kT) { return kT == 32 ? 256 : kT; }
+
 template <typename T, int kT>
-__global__ void __launch_bounds__(kT == 32 ? 256 : kT) logprobs_kernel(const LogprobsArgs a) {
+__global__ void __launch_bounds__(threads_of(kT), 1536 / threads_of(kT)) logprobs_kernel(const LogprobsArgs a) {
   using V = Vec<T>;
   constexpr int kE = V::kE;
   constexpr int kGroups = kT == 32 ? 8 : 1;
@@ -296,9 +300,28 @@ __global__ void __launch_bounds__(kT == 32 ? 256 : kT) logprobs_kernel(const Log
   long long row = static_cast<long long>(blockIdx.x / C) * kGroups + group;
   if (a.status && blockIdx.x == 0) report_targets(a.targets, a.targets_int64, a.n, a.V, a.status, blockDim.x);
   if (row >= a.n) return;
-  const long long target = target_of(a.targets, a.targets_int64, row);
   const int top = a.top;
-  if (target < 0) {                  // padding: the logits are not read
+  const T* z = static_cast<const T*>(a.logits) + row * a.row_stride;
+  // The row is `head` elements up to the first 16-byte boundary, nv whole vectors, and a
+  // tail; the up to 2 (kE - 1) elements outside the vectors go to the lanes of warp 0.
+  const int head = min(static_cast<int>((16 - reinterpret_cast<uintptr_t>(z) % 16) % 16 / sizeof(T)), a.V);
+  const int nv = (a.V - head) / kE;
+  const uint4* zv = reinterpret_cast<const uint4*>(z + head);
+  const int per = (nv + C - 1) / C;
+  const int v0 = min(rank * per, nv), v1 = min(v0 + per, nv);
+  uint4 r[kBatch];
+  auto load_batch = [&](int v) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      r[u] = v + u * kT < v1 ? load16(zv + v + u * kT)
+                             : make_uint4(V::kNegInf, V::kNegInf, V::kNegInf, V::kNegInf);
+  };
+  // Short rows: on its way while the target comes.  (8192 x 129280 with 512 threads a row
+  // takes 329 us without, 344 with.)
+  constexpr bool kAhead = kT <= 128;
+  if constexpr (kAhead) load_batch(v0 + tid);
+  const long long target = target_of(a.targets, a.targets_int64, row);
+  if (target < 0) {                  // padding: the row does not matter
     if (rank == 0) {
       if (tid == 0) {
         a.logprobs[row] = 0.0f;
@@ -313,18 +336,10 @@ __global__ void __launch_bounds__(kT == 32 ? 256 : kT) logprobs_kernel(const Log
     }
     return;
   }
-  const T* z = static_cast<const T*>(a.logits) + row * a.row_stride;
   float z_target = NAN;              // of a target outside [0, V)
   if (rank == 0 && warp == 0 && target < a.V) z_target = V::load1(z + target);
 
-  // The row is `head` elements up to the first 16-byte boundary, nv whole vectors, and a
-  // tail; the up to 2 (kE - 1) elements outside the vectors go to the lanes of warp 0.
-  const int head = min(static_cast<int>((16 - reinterpret_cast<uintptr_t>(z) % 16) % 16 / sizeof(T)), a.V);
-  const int nv = (a.V - head) / kE;
   const int edges = rank == 0 ? a.V - nv * kE : 0;
-  const uint4* zv = reinterpret_cast<const uint4*>(z + head);
-  const int per = (nv + C - 1) / C;
-  const int v0 = min(rank * per, nv), v1 = min(v0 + per, nv);
   int edge_id = 0;
   float edge = -INFINITY;
   if (warp == 0 && lane < edges) {
@@ -337,11 +352,7 @@ __global__ void __launch_bounds__(kT == 32 ? 256 : kT) logprobs_kernel(const Log
   float m = -FLT_MAX;
   float2 S2 = make_float2(0.f, 0.f), T2 = make_float2(0.f, 0.f);
   for (int v = v0 + tid; v < v1; v += kT * kBatch) {
-    uint4 r[kBatch];
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u)
-      r[u] = v + u * kT < v1 ? load16(zv + v + u * kT)
-                             : make_uint4(V::kNegInf, V::kNegInf, V::kNegInf, V::kNegInf);
+    if (!kAhead || v != v0 + tid) load_batch(v);
     uint4 mx = r[0];
 #pragma unroll
     for (int u = 1; u < kBatch; ++u) mx = V::elementwise_max(mx, r[u]);
@@ -595,8 +606,11 @@ __global__ void __launch_bounds__(kT == 32 ? 256 : kT) logprobs_kernel(const Log
 //
 // With y = log2 p_v, dz_v = p_v (A + B y), A = -s (G + E entropy), B = -s E ln 2; the row's
 // token itself takes G (-expm1(log p)) for G (1 - p).
+//
+// Six blocks on an SM (40 registers a thread) and four vectors in flight each: 8192 x 50257 takes
+// 254 us, with four blocks 290, with two vectors 301.
 template <typename T, int kT>
-__global__ void __launch_bounds__(256) logprobs_grad_kernel(const LogprobsGradArgs a, int items_per_row) {
+__global__ void __launch_bounds__(256, 6) logprobs_grad_kernel(const LogprobsGradArgs a, int items_per_row) {
   using V = Vec<T>;
   constexpr int kE = V::kE;
   constexpr int kGroups = 256 / kT;
@@ -606,6 +620,24 @@ __global__ void __launch_bounds__(256) logprobs_grad_kernel(const LogprobsGradAr
   const long long row = item / items_per_row;
   if (row >= a.n) return;
   const int part = static_cast<int>(item - row * items_per_row);
+
+  T* g = static_cast<T*>(a.grad) + row * a.grad_stride;
+  const T* z = static_cast<const T*>(a.logits) + row * a.row_stride;
+  const int head = min(static_cast<int>((16 - reinterpret_cast<uintptr_t>(g) % 16) % 16 / sizeof(T)), a.V);
+  const int nv = (a.V - head) / kE;
+  uint4* gv = reinterpret_cast<uint4*>(g + head);
+  const int v_begin = part * kT * kBatch + tid;
+  const T* zb = z + head;
+  const unsigned shift = reinterpret_cast<uintptr_t>(zb) % 16;
+  uint4 r[kBatch];
+  auto load_aligned = [&] {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (v_begin + u * kT < nv) r[u] = load16(reinterpret_cast<const uint4*>(zb) + v_begin + u * kT);
+  };
+  // Short rows: on their way while the row's numbers come (a row of padding is read in
+  // vain, which costs long rows more than the wait).
+  if (kT == 32 && shift == 0) load_aligned();
 
   const long long target = target_of(a.targets, a.targets_int64, row);
   const float m = a.row_max[row];
@@ -617,11 +649,6 @@ __global__ void __launch_bounds__(256) logprobs_grad_kernel(const LogprobsGradAr
   const float c = a.scale_log2;
   const float minus_ls2 = -log_sum * kLog2e;
   const float A = -a.scale * (G + E * H), B = -a.scale * E * kLn2;
-
-  T* g = static_cast<T*>(a.grad) + row * a.grad_stride;
-  const T* z = static_cast<const T*>(a.logits) + row * a.row_stride;
-  const int head = min(static_cast<int>((16 - reinterpret_cast<uintptr_t>(g) % 16) % 16 / sizeof(T)), a.V);
-  const int nv = (a.V - head) / kE;
 
   auto one = [&](float x, int id) {  // the gradient of one element
     const float y = max_nan(fmaf(x - m, c, minus_ls2), kLowestExponent);
@@ -638,21 +665,14 @@ __global__ void __launch_bounds__(256) logprobs_grad_kernel(const LogprobsGradAr
       V::store1(g + id, zero ? 0.0f : one(V::load1(z + id), id));
     }
   }
-  uint4* gv = reinterpret_cast<uint4*>(g + head);
-  const int v_begin = part * kT * kBatch + tid;
   if (zero) {
 #pragma unroll
     for (int u = 0; u < kBatch; ++u)
       if (v_begin + u * kT < nv) gv[v_begin + u * kT] = make_uint4(0, 0, 0, 0);
     return;
   }
-  const T* zb = z + head;
-  const unsigned shift = reinterpret_cast<uintptr_t>(zb) % 16;
-  uint4 r[kBatch];
   if (shift == 0) {
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u)
-      if (v_begin + u * kT < nv) r[u] = load16(reinterpret_cast<const uint4*>(zb) + v_begin + u * kT);
+    if (kT != 32) load_aligned();
   } else {
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
@@ -729,9 +749,13 @@ cudaError_t launch_forward(const LogprobsArgs& a, int cluster, cudaStream_t stre
 
 template <typename T>
 cudaError_t launch_forward_of(const LogprobsArgs& a, int num_sms, cudaStream_t stream) {
+  // Threads of a row by its vectors, where there are rows enough to fill the device.  65536 x
+  // 4097 bf16 (512 vectors): 88 us with 32 threads, 129 with 128.  8192 x 50257 (6282): 129
+  // with 128, 131 with 256, 156 with 32 or 512.  8192 x 129280 (16160): 358 with 512 and 432
+  // with 128, with 8 alternatives.
   const int nv = a.V / Vec<T>::kE;
   if (nv <= 512) return launch_forward<T, 32>(a, 1, stream);
-  if (nv <= 2048 && a.n >= num_sms) return launch_forward<T, 128>(a, 1, stream);
+  if (nv <= 8192 && a.n >= num_sms) return launch_forward<T, 128>(a, 1, stream);
   // few rows: up to 8 blocks a row, each thread with a vector at least
   int cluster = 1;
   while (cluster < kMaxCluster && static_cast<long long>(a.n) * cluster < num_sms && nv / (2 * cluster) >= 512) cluster *= 2;
@@ -740,7 +764,7 @@ cudaError_t launch_forward_of(const LogprobsArgs& a, int num_sms, cudaStream_t s
 
 template <typename T>
 cudaError_t launch_grad_of(const LogprobsGradArgs& a, cudaStream_t stream) {
-  const int nv = a.V / Vec<T>::kE + 1;
+  const int nv = a.V >= Vec<T>::kE ? a.V / Vec<T>::kE : 1;   // an item takes the row's edges
   const bool narrow = nv <= 32 * kBatch * 4;
   const int kT = narrow ? 32 : 256, groups = 256 / kT;
   const int items = (nv + kT * kBatch - 1) / (kT * kBatch);

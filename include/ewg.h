@@ -282,7 +282,7 @@ int ewg_accumulate_static(const void* ids, int ids_dtype, int64_t num_tokens,
  * A logit of -inf is a token that cannot occur.  A row of nothing else has log_sum 0,
  * row_max -inf, entropy 0 and logprobs -inf; missing alternatives are id -1 at -inf.  A
  * row with a NaN or +inf has NaN logprobs, entropy and log_sum.  A negative target marks a
- * row without a token (padding): its logits are not read, its alternatives are missing
+ * row without a token (padding): its logits may be anything, its alternatives are missing
  * and its other outputs are 0.  A target of vocab or more makes the row's logprobs NaN and
  * the device status EWG_ERR_ID_OUT_OF_RANGE.
  *
