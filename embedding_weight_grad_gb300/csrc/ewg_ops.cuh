@@ -59,7 +59,7 @@ constexpr int kNormBlocks = 304;          // blocks summing the squares of one m
 // rows are more than the columns (the steps then work on the transpose).
 struct OrthoShape {
   int64_t batch, rows, cols;
-  int64_t r, c, ld;                       // ld: r rounded up to 8, the pitch of every buffer
+  int64_t r, c, ld;                       // ld: r rounded up to 16, the pitch of every buffer
   int norm_blocks;
   bool tall;
 };
@@ -76,7 +76,7 @@ inline OrthoShape make_ortho_shape(int64_t batch, int64_t rows, int64_t cols) {
   s.tall = rows > cols;
   s.r = s.tall ? cols : rows;
   s.c = s.tall ? rows : cols;
-  s.ld = (s.r + 7) / 8 * 8;
+  s.ld = (s.r + 15) / 16 * 16;
   // a block (8 warps of 1024 elements) sums 16384 elements or more
   const int64_t want = (s.r * s.c + 16383) / 16384;
   s.norm_blocks = static_cast<int>(want < kNormBlocks ? want : kNormBlocks);

@@ -15,12 +15,14 @@
 //     fp16 number each holds what their rounding left; a X is taken from the sum.  Directions with small singular values, which the steps enlarge by up
 //     to a^5 = 485, then carry no noise from the rounding of the large ones: B is small on
 //     them.  Without it a matrix of low effective rank loses ten times the precision.
-//   * The diagonals of A and B, their largest entries, are kept apart in fp32 and the fp16
-//     matrices have zeros there: with A = D + O, A^2 = O O + D O + O D + D^2, and
-//     B X = offdiag(B) X + diag(B) X with the 22-bit X.
-//   * Everything stored in fp16 is scaled by powers of two or by the norm: X by
-//     s ~ sqrt(r c), so its entries are about 1 at first and at most 1.2 s, and A, B by
-//     rho ~ r / 16.
+//   * What rounding left of the diagonals of A and B, their largest entries, is kept apart in
+//     fp32: (b A + c A^2)_ii takes it in, and B X = fp16(B) X + rest(diag(B)) X.  (Taking the
+//     whole diagonal out of the fp16 matrices would serve full-rank updates better, 1.8e-3
+//     instead of 2.1e-3 with the bf16 rounding's 1.66e-3, and others worse, up to 3.9e-3: in
+//     directions on which B vanishes its diagonal and the rest of it cancel, but not their
+//     products with differently rounded X.)
+//   * X is stored times s ~ sqrt(r c), a power of two, so that its entries are about 1 at first
+//     and at most 1.2 s; A and B need no scale.
 //
 // Layout.  Every buffer is [., ld] fp16 with the r index inside: X^T (two, alternating), the
 // rest of X^T, A and B.  The accumulator of a product has its row index across the lanes of a
@@ -67,8 +69,9 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ float half_lo(uint32_t w) { return __half2float(__ushort_as_half(w & 0xffffu)); }
-__device__ __forceinline__ float half_hi(uint32_t w) { return __half2float(__ushort_as_half(w >> 16)); }
+__device__ __forceinline__ float2 unpack_half(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
 
 __device__ __forceinline__ float grad_at(const OrthoIn& a, long long i) {
   return a.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.grad)[i])
@@ -239,7 +242,8 @@ __global__ void __launch_bounds__(256) ortho_scale_kernel(const OrthoIn a) {
         v[h] = inner0 + in < inners ? (a.tall ? tile[k][in] : tile[in][k]) * f1 * f3 : 0.0f;
       }
       hi[q] = pack_half(v[0], v[1]);
-      lo[q] = pack_half(v[0] - half_lo(hi[q]), v[1] - half_hi(hi[q]));
+      const float2 kept = unpack_half(hi[q]);
+      lo[q] = pack_half(v[0] - kept.x, v[1] - kept.y);
     }
     const long long at = blockIdx.z * a.x_batch + static_cast<long long>(outer0 + k) * a.ld + inner0 + x;
     *reinterpret_cast<uint4*>(a.xt + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -251,39 +255,42 @@ __global__ void __launch_bounds__(256) ortho_scale_kernel(const OrthoIn a) {
 
 constexpr int kBlock = 256;          // a pair of CTAs computes 256 x 256; each CTA 128 rows
 constexpr int kStepK = 64;           // inner elements of a stage: one 128-byte swizzled row
-constexpr int kStages = 5;
+constexpr int kStages = 6;
 constexpr int kOperandBytes = 128 * kStepK * 2;       // one CTA's half of an operand's stage
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kBoxBytes = 64 * kStepK * 2;            // one tensor copy: 64 rows of 128 bytes
+constexpr int kFirstEpilogueWarp = 4;
 constexpr int kEpilogueWarps = 8;
-constexpr int kGemmThreads = 128 + 32 * kEpilogueWarps;
-// Epilogue staging of one warp: a ring of buffers for pieces of 32 rows x kPiece columns, two
-// fp16 numbers an element.  A piece's results replace its inputs.
+constexpr int kWarpCols = 4 * kBlock / kEpilogueWarps;   // columns of an epilogue warp (all take 32 rows)
+constexpr int kGemmThreads = 32 * (kFirstEpilogueWarp + kEpilogueWarps);
+// The epilogue takes an accumulator in pieces of 32 rows x kPiece columns a warp, turned
+// through shared memory: kPiece rows of 32 fp32 numbers, 16 bytes between rows (which puts a
+// quarter-warp's 16-byte reads on different banks).
 constexpr int kPiece = 16;
-constexpr int kPieces = 128 / kPiece;                 // of a warp's 128 columns
-constexpr int kHalfBytes = 32 * kPiece * 2;
-constexpr int kPieceBytes = 2 * kHalfBytes;
-constexpr int kRing = 4;
-constexpr int kWarpStaging = kRing * kPieceBytes;
-constexpr size_t kGemmSmem = static_cast<size_t>(kStages) * kStageBytes + kEpilogueWarps * kWarpStaging + 1024;
-static_assert(kGemmSmem + 512 <= 227 * 1024, "stages and staging fit in shared memory");
+constexpr int kPieces = kWarpCols / kPiece;
+constexpr int kTurnPitch = 36;                        // floats
+constexpr int kTurnFloats = kPiece * kTurnPitch;
+constexpr size_t kGemmSmem = static_cast<size_t>(kStages) * kStageBytes + kEpilogueWarps * kTurnFloats * 4 + 1024;
+static_assert(kGemmSmem + 512 <= 227 * 1024, "stages and turning buffers fit in shared memory");
 constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr uint32_t kGridWaitLimit = 1u << 22;
 
 enum Phase { kGram = 0, kPoly = 1, kUpdate = 2 };
 
 struct OrthoMaps {
-  CUtensorMap xt[2], a, b;                            // operands: boxes of 64 x 64, swizzled
-  CUtensorMap xt_piece[2], xl_piece, a_piece, b_piece;  // pieces: 32 of the r index, kPiece of the other
-  CUtensorMap a_mirror, b_mirror;                     // mirrored pieces: kPiece, 32
+  CUtensorMap xt[2], a, b;           // boxes of 64 x 64, swizzled
 };
 
 struct OrthoArgs {
   int batch, r, c, ld;
   int steps;
   float ca, cb, cc;                  // the polynomial's coefficients
-  float s, rho;                      // stored X = s X, stored A, B = rho A, rho B
-  float* diag_a;                     // [batch][ld], unscaled
+  float s;                           // X is stored times s
+  __half* xt[2];
+  __half* xl;
+  __half* a;
+  __half* b;
+  float* diag_a;                     // [batch][ld]: what rounding left of the diagonals
   float* diag_b;
   __nv_bfloat16* out;
   long long out_batch, out_row;
@@ -294,7 +301,6 @@ struct OrthoArgs {
 
 struct GemmSmem {
   uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
-  uint64_t piece[kEpilogueWarps][kRing];
   uint32_t tmem;
   int abort;
 };
@@ -358,42 +364,57 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return d;
 }
 
-// Where a warp of the epilogue is: its staging ring and the pieces taken so far.
-struct EpilogueState {
-  uint32_t staging;                  // shared-memory address
-  uint64_t* bars;                    // one for each buffer: its inputs have come
-  uint32_t taken;                    // pieces taken; piece n uses buffer n % kRing
-  uint32_t parity;                   // bit b: parity of the next wait on buffer b
+// 16 neighbouring fp16 numbers, 32-byte aligned.
+struct Half16 {
+  uint32_t w[8];
 };
+__device__ __forceinline__ Half16 load_half16(const __half* p) {
+  Half16 h;
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(h.w[0]), "=r"(h.w[1]), "=r"(h.w[2]), "=r"(h.w[3]), "=r"(h.w[4]), "=r"(h.w[5]), "=r"(h.w[6]),
+                 "=r"(h.w[7])
+               : "l"(p)
+               : "memory");
+  return h;
+}
+__device__ __forceinline__ void store_half16(__half* p, const float (&v)[kPiece]) {
+  uint32_t w[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) w[q] = pack_half(v[2 * q], v[2 * q + 1]);
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
 
-__device__ __forceinline__ float lds_half(uint32_t at) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
-  return __half2float(__ushort_as_half(v));
-}
-__device__ __forceinline__ void sts_half(uint32_t at, __half v) {
-  asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(__half_as_ushort(v)) : "memory");
-}
-__device__ __forceinline__ void sts_v4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
-
-// One lane requests the inputs of the warp's piece number n, at row i0 and column j0: X's two
-// parts for an update, O for B.
-template <int kPhase>
-__device__ __forceinline__ void request_piece(const OrthoMaps& maps, const EpilogueState& st, uint32_t n, int cur,
-                                              int z, int i0, int j0) {
-  const uint32_t b = n % kRing, to = st.staging + b * kPieceBytes;
-  ptx::mbar_arrive_expect_tx(&st.bars[b], kPhase == kUpdate ? kPieceBytes : kHalfBytes);
-  if constexpr (kPhase == kUpdate) {
-    ptx::tma_load_3d(to, &maps.xt_piece[cur], i0, j0, z, &st.bars[b]);
-    ptx::tma_load_3d(to + kHalfBytes, &maps.xl_piece, i0, j0, z, &st.bars[b]);
-  } else {
-    ptx::tma_load_3d(to, &maps.a_piece, i0, j0, z, &st.bars[b]);
+// A piece of 32 rows x 16 columns turned through shared memory: in, lane l holds row l; out, lane
+// l holds rows 8 (l % 4) .. + 7 of columns l / 4 and l / 4 + 8.
+__device__ __forceinline__ void turn(float* buf, int lane, const float (&v)[kPiece], float (&t)[2][8]) {
+#pragma unroll
+  for (int q = 0; q < kPiece; ++q) buf[q * kTurnPitch + lane] = v[q];
+  __syncwarp();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float4* p = reinterpret_cast<const float4*>(buf + (lane / 4 + 8 * h) * kTurnPitch + lane % 4 * 8);
+    const float4 x = p[0], y = p[1];
+    t[h][0] = x.x, t[h][1] = x.y, t[h][2] = x.z, t[h][3] = x.w;
+    t[h][4] = y.x, t[h][5] = y.y, t[h][6] = y.z, t[h][7] = y.w;
   }
+  __syncwarp();
+}
+__device__ __forceinline__ void turn_back(float* buf, int lane, const float (&t)[2][8], float (&v)[kPiece]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float4* p = reinterpret_cast<float4*>(buf + (lane / 4 + 8 * h) * kTurnPitch + lane % 4 * 8);
+    p[0] = make_float4(t[h][0], t[h][1], t[h][2], t[h][3]);
+    p[1] = make_float4(t[h][4], t[h][5], t[h][6], t[h][7]);
+  }
+  __syncwarp();
+#pragma unroll
+  for (int q = 0; q < kPiece; ++q) v[q] = buf[q * kTurnPitch + lane];
+  __syncwarp();
 }
 
-// The last update's piece, to the caller's matrix.
+// The last update's piece, to the caller's matrix: lane = row i, columns j0 .. + 15 of X.
 __device__ __forceinline__ void store_out(const OrthoArgs& a, int z, int i, int j0, const float (&v)[kPiece]) {
   const int n = min(a.c - j0, kPiece);
   if (i >= a.r) return;
@@ -420,124 +441,185 @@ __device__ __forceinline__ void store_out(const OrthoArgs& a, int z, int i, int 
   }
 }
 
-// One warp's part of a finished block: 32 rows from i0, 128 columns from j, in pieces of kPiece
-// columns.  A piece's inputs come and its results go by tensor copies through shared memory,
-// which also clip what leaves the matrix; the next two pieces' inputs are under way while
-// one is computed, and the first two's before the products are done.
+// The warp has read its part of the accumulator.
+__device__ __forceinline__ void release_acc(uint32_t acc_empty) {
+  ptx::tmem_fence_before();
+  __syncwarp();
+  if (threadIdx.x % 32 == 0) ptx::mbar_arrive_cluster(acc_empty);
+}
+
+// What an epilogue warp keeps through the kernel.
+struct EpilogueWarp {
+  float* buf;                        // its turning buffer
+  volatile int* abort;
+};
+
+__device__ __forceinline__ uint4 load_v4(const __half* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  return v;
+}
+
+// One warp's part of a finished block of an update: 32 rows from i0, kWarpCols columns from j.  The
+// products are turned, so that X's two parts are read and written 16 bytes a lane; they are
+// read a piece ahead, the first before the products are done.
+__device__ __forceinline__ bool epilogue_update(const OrthoArgs& a, int step, const Tile& x, int i0, int j,
+                                                uint32_t from, uint64_t* acc_full, uint32_t parity,
+                                                uint32_t acc_empty, const EpilogueWarp& w) {
+  const int lane = threadIdx.x % 32;
+  const int pieces = i0 < a.r ? min(max((a.c - j + kPiece - 1) / kPiece, 0), kPieces) : 0;
+  const bool last = step == a.steps - 1;
+  const int ld = a.ld;
+  const int i = i0 + lane % 4 * 8;                    // this lane's rows i .. i + 7 (inside ld) ...
+  // ... and columns: piece u, h: jl + kPiece u + 8 h
+  const int jl = j + lane / 4, cols = i < a.r ? a.c - jl : 0;
+  const long long base = (static_cast<long long>(x.z) * a.c + jl) * ld + i;
+  const __half* hi_in = a.xt[step & 1] + base;
+  __half* hi_out = a.xt[(step & 1) ^ 1] + base;
+  __half* lo = a.xl + base;
+  uint4 hi[2] = {}, rest[2] = {};
+  auto load = [&](int u) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (u * kPiece + 8 * h < cols) {
+        hi[h] = load_v4(hi_in + (u * kPiece + 8 * h) * static_cast<long long>(ld));
+        rest[h] = load_v4(lo + (u * kPiece + 8 * h) * static_cast<long long>(ld));
+      }
+  };
+  load(0);
+  float own[8];                                       // a + what is left of B_ii
+#pragma unroll
+  for (int q = 0; q < 8; ++q) own[q] = i + q < a.r ? a.ca + a.diag_b[x.z * static_cast<long long>(ld) + i + q] : 0.0f;
+  if (!__all_sync(kAll, wait_bar(acc_full, parity, w.abort))) return false;
+  ptx::tmem_fence_after();
+  uint32_t acc[kPiece];
+  if (pieces > 0) ptx::tmem_load16(acc, from);
+  else release_acc(acc_empty);
+#pragma unroll 1
+  for (int u = 0; u < pieces; ++u) {
+    ptx::tmem_wait_load();
+    float v[kPiece], t[2][8];
+#pragma unroll
+    for (int q = 0; q < kPiece; ++q) v[q] = __uint_as_float(acc[q]);
+    turn(w.buf, lane, v, t);
+    if (u + 1 < pieces) ptx::tmem_load16(acc, from + (u + 1) * kPiece);
+    else release_acc(acc_empty);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t hw[4] = {hi[h].x, hi[h].y, hi[h].z, hi[h].w};
+      const uint32_t lw[4] = {rest[h].x, rest[h].y, rest[h].z, rest[h].w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float2 b = unpack_half(hw[q]), r = unpack_half(lw[q]);
+        t[h][2 * q] = fmaf(own[2 * q], b.x + r.x, t[h][2 * q]);
+        t[h][2 * q + 1] = fmaf(own[2 * q + 1], b.y + r.y, t[h][2 * q + 1]);
+      }
+    }
+    if (u + 1 < pieces) load(u + 1);
+    if (last) {
+      turn_back(w.buf, lane, t, v);
+      store_out(a, x.z, i0 + lane, j + u * kPiece, v);
+      continue;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t hw[4], lw[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        hw[q] = pack_half(t[h][2 * q], t[h][2 * q + 1]);
+        const float2 b = unpack_half(hw[q]);
+        lw[q] = pack_half(t[h][2 * q] - b.x, t[h][2 * q + 1] - b.y);
+      }
+      if (u * kPiece + 8 * h < cols) {
+        const long long at = (u * kPiece + 8 * h) * static_cast<long long>(ld);
+        *reinterpret_cast<uint4*>(hi_out + at) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+        *reinterpret_cast<uint4*>(lo + at) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+      }
+    }
+  }
+  return true;
+}
+
+// The same for A = X X^T or B = b A + c A^2: 32 rows from i0, kWarpCols columns from j of a block on
+// or below the diagonal, and its mirror.
 template <int kPhase>
-__device__ __forceinline__ bool epilogue(const OrthoMaps& maps, const OrthoArgs& a, int step, const Tile& x, int i0,
-                                         int j, uint32_t from, uint64_t* acc_full, uint32_t parity,
-                                         volatile int* abort, EpilogueState& st) {
+__device__ __forceinline__ bool epilogue_square(const OrthoArgs& a, const Tile& x, int i0, int j, uint32_t from,
+                                                uint64_t* acc_full, uint32_t parity, uint32_t acc_empty,
+                                                const EpilogueWarp& w) {
   const int lane = threadIdx.x % 32;
   const int i = i0 + lane;
-  const int cols = kPhase == kUpdate ? a.c : a.r;
-  const int pieces = i0 < a.r ? min(max((cols - j + kPiece - 1) / kPiece, 0), kPieces) : 0;
-  const long long ld = a.ld;
-  const int cur = step & 1;
-  const bool last = kPhase == kUpdate && step == a.steps - 1;
-  if (kPhase != kGram && lane == 0) {
-    for (int u = 0; u < 2 && u < pieces; ++u)
-      request_piece<kPhase>(maps, st, st.taken + u, cur, x.z, i0, j + u * kPiece);
+  const int pieces = i0 < a.r ? min(max((a.r - j + kPiece - 1) / kPiece, 0), kPieces) : 0;
+  const int ld = a.ld;
+  const long long matrix = static_cast<long long>(x.z) * a.r * ld;
+  const bool row = i < a.r;
+  const __half* o_row = a.a + matrix + static_cast<long long>(i) * ld + j;    // A_ij = A_ji, along the row
+  Half16 o = {};
+  float rest_a = 0.0f;               // what rounding left of A_ii
+  if (kPhase == kPoly && row && pieces > 0) {
+    o = load_half16(o_row);
+    rest_a = a.diag_a[x.z * static_cast<long long>(ld) + i];
   }
-  float own = 0.0f, dj4[4] = {};
-  if (kPhase == kUpdate && i < a.r) own = a.ca + a.diag_b[x.z * ld + i];
-  if (kPhase == kPoly) {
-    if (i < a.r) own = a.diag_a[x.z * ld + i];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) dj4[q] = j + 32 * q + lane < a.r ? a.diag_a[x.z * ld + j + 32 * q + lane] : 0.0f;
-  }
-  if (!__all_sync(kAll, wait_bar(acc_full, parity, abort))) return false;
+  if (!__all_sync(kAll, wait_bar(acc_full, parity, w.abort))) return false;
   ptx::tmem_fence_after();
-  const float f = kPhase == kUpdate ? 1.0f / a.rho : kPhase == kGram ? a.rho / (a.s * a.s) : a.cc / a.rho;
+  const float f = kPhase == kGram ? 1.0f / (a.s * a.s) : a.cc;
+  __half* m = (kPhase == kGram ? a.a : a.b) + matrix;
+  __half* m_row = m + static_cast<long long>(i) * ld + j;
+  const int ti = i0 + lane % 4 * 8;                   // after the turn: rows ti .. ti + 7 of ...
+  const int cols = ti < a.r ? a.r - j - lane / 4 : 0; // ... columns j + lane / 4 + kPiece u + 8 h
+  __half* m_col = m + static_cast<long long>(j + lane / 4) * ld + ti;
+  uint32_t acc[kPiece];
+  if (pieces > 0) ptx::tmem_load16(acc, from);
+  else release_acc(acc_empty);
 #pragma unroll 1
   for (int u = 0; u < pieces; ++u) {
     const int j0 = j + u * kPiece;
-    const uint32_t b = st.taken % kRing;
-    const uint32_t buf = st.staging + b * kPieceBytes, at = buf + lane * 2;
-    uint32_t acc[kPiece];
+    ptx::tmem_wait_load();
     float v[kPiece];
-    ptx::tmem_load16(acc, from + u * kPiece);
-    if (kPhase != kGram) {
-      if (!__all_sync(kAll, wait_bar(&st.bars[b], (st.parity >> b) & 1u, abort))) return false;
-      st.parity ^= 1u << b;
-    }
-    if constexpr (kPhase == kUpdate) {
 #pragma unroll
-      for (int q = 0; q < kPiece; ++q) v[q] = lds_half(at + q * 64) + lds_half(at + kHalfBytes + q * 64);
-      ptx::tmem_wait_load();
+    for (int q = 0; q < kPiece; ++q) v[q] = __uint_as_float(acc[q]) * f;
+    if constexpr (kPhase == kPoly) {
 #pragma unroll
-      for (int q = 0; q < kPiece; ++q) v[q] = fmaf(own, v[q], __uint_as_float(acc[q]) * f);
-    } else {
-      const float dj_lane = u < 4 ? (u < 2 ? dj4[0] : dj4[1]) : (u < 6 ? dj4[2] : dj4[3]);
-      if constexpr (kPhase == kPoly) {
-#pragma unroll
-        for (int q = 0; q < kPiece; ++q) v[q] = lds_half(at + q * 64);
+      for (int q = 0; q < kPiece / 2; ++q) {
+        const float2 p = unpack_half(o.w[q]);
+        v[2 * q] = fmaf(a.cb, p.x, v[2 * q]);
+        v[2 * q + 1] = fmaf(a.cb, p.y, v[2 * q + 1]);
       }
-      ptx::tmem_wait_load();
-      float diag = 0.0f;             // the product on the diagonal
+    }
+    if (j0 < i0 + 32 && i0 < j0 + kPiece) {           // the diagonal passes through the piece
+      float left = 0.0f;
 #pragma unroll
       for (int q = 0; q < kPiece; ++q) {
-        const float p = __uint_as_float(acc[q]);
-        const bool on = j0 + q == i;
-        if (on) diag = p;
-        if constexpr (kPhase == kGram) {
-          v[q] = p * f;
-        } else {
-          const float dj = __shfl_sync(kAll, dj_lane, (u & 1) * kPiece + q);
-          v[q] = fmaf(f, p, v[q] * fmaf(a.cc, own + dj, a.cb));
+        if (j0 + q != i) continue;
+        if constexpr (kPhase == kPoly) {              // rest_a to first order
+          const float2 p = unpack_half(o.w[q / 2]);
+          v[q] = fmaf(rest_a, fmaf(2.0f * a.cc, q % 2 ? p.y : p.x, a.cb), v[q]);
         }
-        if (on) v[q] = 0.0f;
+        left = v[q] - __half2float(__float2half_rn(v[q]));
       }
-      if (i >= j0 && i < j0 + kPiece && i < a.r) {
-        if constexpr (kPhase == kGram) a.diag_a[x.z * ld + i] = diag / (a.s * a.s);
-        else a.diag_b[x.z * ld + i] = fmaf(a.cb, own, a.cc * fmaf(own, own, diag / (a.rho * a.rho)));
-      }
+      if (i >= j0 && i < j0 + kPiece && row)
+        (kPhase == kGram ? a.diag_a : a.diag_b)[x.z * static_cast<long long>(ld) + i] = left;
     }
-    if (last) {
-      store_out(a, x.z, i, j0, v);
-    } else {
+    if (u + 1 < pieces) ptx::tmem_load16(acc, from + (u + 1) * kPiece);
+    else release_acc(acc_empty);
+    if (kPhase == kPoly && row && u + 1 < pieces) o = load_half16(o_row + (u + 1) * kPiece);
+    if (x.I != x.J && row) store_half16(m_row + u * kPiece, v);
+    float t[2][8];
+    turn(w.buf, lane, v, t);
 #pragma unroll
-      for (int q = 0; q < kPiece; ++q) {
-        const __half hi = __float2half_rn(v[q]);
-        sts_half(at + q * 64, hi);
-        if constexpr (kPhase == kUpdate) sts_half(at + kHalfBytes + q * 64, __float2half_rn(v[q] - __half2float(hi)));
-      }
-      if (kPhase != kUpdate && x.I != x.J) {          // mirrored, [row][column]
-        uint32_t w[kPiece / 2];
-#pragma unroll
-        for (int q = 0; q < kPiece / 2; ++q) w[q] = pack_half(v[2 * q], v[2 * q + 1]);
-        const uint32_t m = buf + kHalfBytes + lane * kPiece * 2;
-        sts_v4(m, w[0], w[1], w[2], w[3]);
-        sts_v4(m + 16, w[4], w[5], w[6], w[7]);
-      }
-      ptx::fence_proxy_async_shared();
+    for (int h = 0; h < 2; ++h) {
+      if (u * kPiece + 8 * h < cols)
+        *reinterpret_cast<uint4*>(m_col + (u * kPiece + 8 * h) * static_cast<long long>(ld)) =
+            make_uint4(pack_half(t[h][0], t[h][1]), pack_half(t[h][2], t[h][3]), pack_half(t[h][4], t[h][5]),
+                       pack_half(t[h][6], t[h][7]));
     }
-    __syncwarp();
-    if (lane == 0) {
-      if (!last) {
-        if constexpr (kPhase == kUpdate) {
-          ptx::tma_store_3d(&maps.xt_piece[cur ^ 1], i0, j0, x.z, buf);
-          ptx::tma_store_3d(&maps.xl_piece, i0, j0, x.z, buf + kHalfBytes);
-        } else {
-          ptx::tma_store_3d(kPhase == kGram ? &maps.a_piece : &maps.b_piece, i0, j0, x.z, buf);
-          if (x.I != x.J)
-            ptx::tma_store_3d(kPhase == kGram ? &maps.a_mirror : &maps.b_mirror, j0, i0, x.z, buf + kHalfBytes);
-        }
-        ptx::bulk_commit();
-        ptx::bulk_wait_read<kRing - 2>();   // the buffer of the piece after the next is free
-      }
-      if (kPhase != kGram && u + 2 < pieces)
-        request_piece<kPhase>(maps, st, st.taken + 2, cur, x.z, i0, j0 + 2 * kPiece);
-    }
-    __syncwarp();
-    ++st.taken;
   }
   return true;
 }
 
 // All phases of all steps, one cooperative launch of CTA pairs: a pair takes blocks of 256 x
 // 256, and a barrier over the grid ends each phase.  Per CTA: warp 0 copies operands (TMA),
-// warp 1 of the pair's first CTA issues the products, warps 4-11 take finished
+// warp 1 of the pair's first CTA issues the products, the other warps take finished
 // accumulators (two in tensor memory, so that the products of the next block run meanwhile).
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const OrthoArgs a) {
@@ -558,7 +640,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       ptx::mbar_init(&sm.acc_empty[i], 2 * kEpilogueWarps);
     }
     ptx::mbar_init(&sm.drained, 1);
-    for (int i = 0; i < kRing * kEpilogueWarps; ++i) ptx::mbar_init(&sm.piece[0][0] + i, 1);
     sm.abort = 0;
     ptx::fence_mbar_init();
     ptx::prefetch_tensor_map(&maps.xt[0]);
@@ -576,10 +657,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 
   uint32_t stage = 0, stage_phase = 0;      // producer's or issuer's place in the ring
   uint32_t acc = 0, acc_phase = 0;          // issuer's or epilogue's accumulator
-  EpilogueState st{};
-  if (warp >= 4) {
-    st.staging = stages + kStages * kStageBytes + (warp - 4) * kWarpStaging;
-    st.bars = sm.piece[warp - 4];
+  EpilogueWarp ew{};
+  if (warp >= kFirstEpilogueWarp) {
+    ew.buf = reinterpret_cast<float*>(raw + (stages - ptx::smem_u32(raw)) + kStages * kStageBytes) +
+             (warp - kFirstEpilogueWarp) * kTurnFloats;
+    ew.abort = abort;
   }
 
   for (int p = 0; p < 3 * a.steps; ++p) {
@@ -657,33 +739,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         }
       }
       __syncwarp();
-    } else if (warp >= 4) {
-      const int quarter = warp % 4, half = (warp - 4) / 4;
+    } else if (warp >= kFirstEpilogueWarp) {
+      const int quarter = warp % 4, part = (warp - kFirstEpilogueWarp) / 4;
       for (int t = pair; t < tiles && !*abort; t += pairs) {
         const Tile x = tile_at(a, phase, t);
-        const uint32_t from = tmem + acc * kBlock + half * 128 + (static_cast<uint32_t>(quarter) << 21);
+        const uint32_t from = tmem + acc * kBlock + part * kWarpCols + (static_cast<uint32_t>(quarter) << 21);
         const int i0 = x.I * kBlock + rank * 128 + quarter * 32;
-        const int j = x.J * kBlock + half * 128;
+        const int j = x.J * kBlock + part * kWarpCols;
         uint64_t* full = &sm.acc_full[acc];
-        const bool ok = phase == kGram ? epilogue<kGram>(maps, a, step, x, i0, j, from, full, acc_phase, abort, st)
-                        : phase == kPoly ? epilogue<kPoly>(maps, a, step, x, i0, j, from, full, acc_phase, abort, st)
-                                         : epilogue<kUpdate>(maps, a, step, x, i0, j, from, full, acc_phase, abort, st);
+        const uint32_t empty = ptx::map_to_rank(ptx::smem_u32(&sm.acc_empty[acc]), 0);
+        const bool ok = phase == kGram ? epilogue_square<kGram>(a, x, i0, j, from, full, acc_phase, empty, ew)
+                        : phase == kPoly ? epilogue_square<kPoly>(a, x, i0, j, from, full, acc_phase, empty, ew)
+                                         : epilogue_update(a, step, x, i0, j, from, full, acc_phase, empty, ew);
         if (!ok) {
           gave_up(a, abort);
           break;
         }
-        ptx::tmem_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(ptx::smem_u32(&sm.acc_empty[acc]), 0));
         if (++acc == 2) {
           acc = 0;
           acc_phase ^= 1u;
         }
       }
-      if (lane == 0) {               // what was stored is there for the next phase
-        ptx::bulk_wait<0>();
-        ptx::fence_proxy_async();
-      }
+      ptx::fence_proxy_async();      // what was stored is read by tensor copies next
     }
     if (p + 1 == 3 * a.steps) break;
     // ---- barrier over the grid
@@ -729,16 +806,14 @@ using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
 EncodeTiled g_encode = nullptr;
 int g_pairs[64] = {};                // per device: pairs resident at once
 
-// [batch][outer][ld] fp16 with r columns used, in boxes of box_x x box_y.
-cudaError_t encode(CUtensorMap* map, void* p, const OrthoShape& sh, int64_t outer, int box_x, int box_y,
-                   bool swizzle) {
+// [batch][outer][ld] fp16 with r columns used, in swizzled boxes of 64 x 64.
+cudaError_t encode(CUtensorMap* map, void* p, const OrthoShape& sh, int64_t outer) {
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(sh.r), static_cast<cuuint64_t>(outer),
                               static_cast<cuuint64_t>(sh.batch)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(sh.ld * 2), static_cast<cuuint64_t>(sh.ld * outer * 2)};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_x), static_cast<cuuint32_t>(box_y), 1}, step[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, 64, 1}, step[3] = {1, 1, 1};
   const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, p, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
@@ -800,20 +875,13 @@ cudaError_t launch_orthogonalize(const OrthoCall& q, cudaStream_t stream) {
 
   OrthoMaps maps;
   cudaError_t e = cudaSuccess;
-  auto add = [&](CUtensorMap* map, size_t at, int64_t outer, int x, int y, bool swizzle) {
-    if (e == cudaSuccess) e = encode(map, ws + at, sh, outer, x, y, swizzle);
+  auto add = [&](CUtensorMap* map, size_t at, int64_t outer) {
+    if (e == cudaSuccess) e = encode(map, ws + at, sh, outer);
   };
-  for (int i = 0; i < 2; ++i) {
-    add(&maps.xt[i], L.xt[i], sh.c, 64, 64, true);
-    add(&maps.xt_piece[i], L.xt[i], sh.c, 32, kPiece, false);
-  }
-  add(&maps.xl_piece, L.xl, sh.c, 32, kPiece, false);
-  add(&maps.a, L.a, sh.r, 64, 64, true);
-  add(&maps.a_piece, L.a, sh.r, 32, kPiece, false);
-  add(&maps.a_mirror, L.a, sh.r, kPiece, 32, false);
-  add(&maps.b, L.b, sh.r, 64, 64, true);
-  add(&maps.b_piece, L.b, sh.r, 32, kPiece, false);
-  add(&maps.b_mirror, L.b, sh.r, kPiece, 32, false);
+  add(&maps.xt[0], L.xt[0], sh.c);
+  add(&maps.xt[1], L.xt[1], sh.c);
+  add(&maps.a, L.a, sh.r);
+  add(&maps.b, L.b, sh.r);
   if (e != cudaSuccess) return e;
 
   OrthoArgs a{};
@@ -826,7 +894,11 @@ cudaError_t launch_orthogonalize(const OrthoCall& q, cudaStream_t stream) {
   a.cb = q.b;
   a.cc = q.c;
   a.s = in.s;
-  a.rho = power_of_two_below(std::fmax(1.0, static_cast<double>(sh.r) / 16));
+  a.xt[0] = in.xt;
+  a.xt[1] = reinterpret_cast<__half*>(ws + L.xt[1]);
+  a.xl = in.xl;
+  a.a = reinterpret_cast<__half*>(ws + L.a);
+  a.b = reinterpret_cast<__half*>(ws + L.b);
   a.diag_a = reinterpret_cast<float*>(ws + L.diag_a);
   a.diag_b = reinterpret_cast<float*>(ws + L.diag_b);
   a.out = static_cast<__nv_bfloat16*>(q.out);
