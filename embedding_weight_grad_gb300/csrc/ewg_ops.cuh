@@ -55,18 +55,46 @@ constexpr int kOrthoMaxSide = 16384;      // of the smaller side
 constexpr int kOrthoMaxLong = 1 << 20;    // of the larger side
 constexpr int kNormBlocks = 304;          // blocks summing the squares of one matrix, at most
 
+constexpr int kOrthoBlock = 256;          // side of the blocks the products are computed in
+constexpr int kOrthoWarps = 16;           // epilogue warps of a block
+
 // One call's sizes: matrices [rows, cols]; r the smaller side, c the larger; `tall` when the
 // rows are more than the columns (the steps then work on the transpose).
 struct OrthoShape {
   int64_t batch, rows, cols;
   int64_t r, c, ld;                       // ld: r rounded up to 16, the pitch of every buffer
+  int64_t blocks_r, blocks_c;
   int norm_blocks;
+  int split_gram, split_poly;             // parts of the inner dimension of X X^T and A A
   bool tall;
+
+  int64_t square_blocks() const { return blocks_r * (blocks_r + 1) / 2; }
+  // counters of the steps kernel for one matrix
+  int64_t counters() const {
+    return 3 * blocks_r + (split_gram > 1 || split_poly > 1 ? 2 * square_blocks() * kOrthoWarps : 0);
+  }
+  int64_t partial_floats() const {
+    const int most = split_gram > split_poly ? split_gram : split_poly;
+    return most > 1 ? batch * square_blocks() * most * kOrthoBlock * kOrthoBlock : 0;
+  }
 };
 
 struct OrthoLayout {
-  size_t header, barrier, norm, diag_a, diag_b, xt[2], xl, a, b, total;
+  size_t header, counters, norm, diag_a[2], diag_b, xt[2], xl, a[2], b, partial, total;
 };
+
+// Parts of an inner dimension of `inner` for `units` blocks: as many as leave no more units than
+// kOrthoPairs, each of at least kOrthoPartMin.
+constexpr int64_t kOrthoPairs = 76;
+constexpr int64_t kOrthoPartMin = 512;
+inline int ortho_split(int64_t units, int64_t inner) {
+  int64_t parts = kOrthoPairs / units;
+  if (parts > inner / kOrthoPartMin) parts = inner / kOrthoPartMin;
+  if (parts <= 1) return 1;
+  // no empty part: `per` inner blocks of 64 each
+  const int64_t blocks = (inner + 63) / 64, per = (blocks + parts - 1) / parts;
+  return static_cast<int>((blocks + per - 1) / per);
+}
 
 inline OrthoShape make_ortho_shape(int64_t batch, int64_t rows, int64_t cols) {
   OrthoShape s{};
@@ -77,9 +105,13 @@ inline OrthoShape make_ortho_shape(int64_t batch, int64_t rows, int64_t cols) {
   s.r = s.tall ? cols : rows;
   s.c = s.tall ? rows : cols;
   s.ld = (s.r + 15) / 16 * 16;
+  s.blocks_r = (s.r + kOrthoBlock - 1) / kOrthoBlock;
+  s.blocks_c = (s.c + kOrthoBlock - 1) / kOrthoBlock;
   // a block (8 warps of 1024 elements) sums 16384 elements or more
   const int64_t want = (s.r * s.c + 16383) / 16384;
   s.norm_blocks = static_cast<int>(want < kNormBlocks ? want : kNormBlocks);
+  s.split_gram = ortho_split(batch * s.square_blocks(), s.c);
+  s.split_poly = ortho_split(batch * s.square_blocks(), s.r);
   return s;
 }
 
@@ -92,15 +124,15 @@ inline OrthoLayout make_ortho_layout(const OrthoShape& s) {
     return at;
   };
   L.header = take(256);
-  L.barrier = take(256);
+  L.counters = take(s.batch * s.counters() * 4);
   L.norm = take(s.batch * s.norm_blocks * 8);
-  L.diag_a = take(s.batch * s.ld * 4);
+  for (int i = 0; i < 2; ++i) L.diag_a[i] = take(s.batch * s.ld * 4);
   L.diag_b = take(s.batch * s.ld * 4);
-  L.xt[0] = take(s.batch * s.c * s.ld * 2);
-  L.xt[1] = take(s.batch * s.c * s.ld * 2);
+  for (int i = 0; i < 2; ++i) L.xt[i] = take(s.batch * s.c * s.ld * 2);
   L.xl = take(s.batch * s.c * s.ld * 2);
-  L.a = take(s.batch * s.r * s.ld * 2);
+  for (int i = 0; i < 2; ++i) L.a[i] = take(s.batch * s.r * s.ld * 2);
   L.b = take(s.batch * s.r * s.ld * 2);
+  L.partial = take(s.partial_floats() * 4);
   L.total = off;
   return L;
 }

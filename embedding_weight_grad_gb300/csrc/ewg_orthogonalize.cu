@@ -29,7 +29,7 @@
 // warp, so all stores of X^T and of the mirrored blocks are contiguous.  As an operand of X
 // X^T, X^T has the product's rows inside (MN-major); for B X it has the inner index inside
 // (K-major), as A and B have by symmetry.
-#include <cfloat>
+#include <algorithm>
 #include <cmath>
 #include <mutex>
 
@@ -62,7 +62,8 @@ struct OrthoIn {
   __half* xt;
   __half* xl;
   Header* header;
-  int* barrier;
+  int* counters;                     // of the steps kernel, `num_counters` for each matrix
+  int num_counters;
 };
 
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
@@ -111,10 +112,10 @@ __device__ __forceinline__ double sum_of_squares(const float (&g)[kLaneElems]) {
 // Sums of squares of one matrix per blockIdx.y, a warp to 1024 neighbouring elements of a row
 // (a matrix without gaps is one long row).  Bound by the read of G.
 __global__ void __launch_bounds__(256) ortho_norm_kernel(const OrthoIn a) {
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
-    a.header->status = kStatusOk;
-    *a.barrier = 0;
-  }
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) a.header->status = kStatusOk;
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < a.num_counters; i += 256)
+      a.counters[static_cast<long long>(blockIdx.y) * a.num_counters + i] = 0;
   constexpr int kChunk = 32 * kLaneElems;
   const bool whole = a.row_stride == a.cols;
   const long long cols = whole ? static_cast<long long>(a.rows) * a.cols : a.cols;
@@ -273,12 +274,12 @@ constexpr int kTurnFloats = kPiece * kTurnPitch;
 constexpr size_t kGemmSmem = static_cast<size_t>(kStages) * kStageBytes + kEpilogueWarps * kTurnFloats * 4 + 1024;
 static_assert(kGemmSmem + 512 <= 227 * 1024, "stages and turning buffers fit in shared memory");
 constexpr uint32_t kWaitLimit = 1u << 22;
-constexpr uint32_t kGridWaitLimit = 1u << 22;
+constexpr uint32_t kReadyLimit = 1u << 22;
 
 enum Phase { kGram = 0, kPoly = 1, kUpdate = 2 };
 
 struct OrthoMaps {
-  CUtensorMap xt[2], a, b;           // boxes of 64 x 64, swizzled
+  CUtensorMap xt[2], a[2], b;        // boxes of 64 x 64, swizzled
 };
 
 struct OrthoArgs {
@@ -288,15 +289,18 @@ struct OrthoArgs {
   float s;                           // X is stored times s
   __half* xt[2];
   __half* xl;
-  __half* a;
+  __half* a[2];                      // of even and odd steps
   __half* b;
-  float* diag_a;                     // [batch][ld]: what rounding left of the diagonals
+  float* diag_a[2];                  // [batch][ld]: what rounding left of the diagonals
   float* diag_b;
+  int split[2];                      // parts of the inner dimension of X X^T and A A
+  float* partial;                    // split products: [batch][block][part][CTA][warp][column][row]
   __nv_bfloat16* out;
   long long out_batch, out_row;
   int tall;
   Header* header;
-  int* barrier;
+  int* ready;                        // [phase][batch][block row]: warps done, over all steps
+  int* arrived;                      // [phase][batch][block][CTA][warp]: parts done, over all steps
 };
 
 struct GemmSmem {
@@ -313,35 +317,102 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t lead, u
 
 __device__ __forceinline__ int blocks_of(int n) { return (n + kBlock - 1) / kBlock; }
 
-// Block `t` of a phase: matrix, block row I, block column J.  A and B: on and below the diagonal.
-struct Tile {
-  int z, I, J;
+// A unit of work of a pair: block (I, J) of matrix z, part `part` of its inner dimension.  A
+// and B: blocks on and below the diagonal only.
+struct Unit {
+  int z, I, J, part;
 };
 
-__device__ __forceinline__ int tiles_of(const OrthoArgs& a, int phase) {
+__device__ __forceinline__ int units_of(const OrthoArgs& a, int phase) {
   const int nr = blocks_of(a.r);
-  return a.batch * (phase == kUpdate ? nr * blocks_of(a.c) : nr * (nr + 1) / 2);
+  return a.batch * (phase == kUpdate ? nr * blocks_of(a.c) : nr * (nr + 1) / 2 * a.split[phase]);
 }
 
-__device__ __forceinline__ Tile tile_at(const OrthoArgs& a, int phase, int t) {
+// Unit t of a phase.  The orders let a phase start before the one before it has ended: the
+// update goes by rows, which is what A's blocks by rows need; B's blocks go by columns, whose
+// first ones complete B's first rows, which the update's first rows need.
+__device__ __forceinline__ Unit unit_at(const OrthoArgs& a, int phase, int t) {
   const int nr = blocks_of(a.r);
-  Tile x;
+  Unit x;
   if (phase == kUpdate) {
-    const int per = nr * blocks_of(a.c);
-    x.z = t / per;
-    t -= x.z * per;
-    x.J = t / nr;
-    x.I = t - x.J * nr;
-  } else {
-    const int per = nr * (nr + 1) / 2;
-    x.z = t / per;
-    t -= x.z * per;
-    x.I = static_cast<int>((sqrtf(8.0f * t + 1.0f) - 1.0f) * 0.5f);
-    while ((x.I + 1) * (x.I + 2) / 2 <= t) ++x.I;
-    while (x.I * (x.I + 1) / 2 > t) --x.I;
-    x.J = t - x.I * (x.I + 1) / 2;
+    const int nc = blocks_of(a.c);
+    x.z = t / (nr * nc);
+    t -= x.z * nr * nc;
+    x.I = t / nc;
+    x.J = t - x.I * nc;
+    x.part = 0;
+    return x;
   }
+  const int blocks = nr * (nr + 1) / 2, parts = a.split[phase];
+  x.z = t / (blocks * parts);
+  t -= x.z * blocks * parts;
+  x.part = t % parts;
+  t /= parts;
+  if (phase == kPoly) t = blocks - 1 - t;
+  int row = static_cast<int>((sqrtf(8.0f * t + 1.0f) - 1.0f) * 0.5f);
+  while ((row + 1) * (row + 2) / 2 <= t) ++row;
+  while (row * (row + 1) / 2 > t) --row;
+  const int col = t - row * (row + 1) / 2;
+  x.I = phase == kPoly ? nr - 1 - col : row;
+  x.J = phase == kPoly ? nr - 1 - row : col;
   return x;
+}
+
+// The inner blocks [first, last) of a unit.
+__device__ __forceinline__ void inner_of(const OrthoArgs& a, int phase, const Unit& x, int& first, int& last) {
+  const int blocks = ((phase == kGram ? a.c : a.r) + kStepK - 1) / kStepK;
+  const int per = phase == kUpdate ? blocks : (blocks + a.split[phase] - 1) / a.split[phase];
+  first = x.part * per;
+  last = min(first + per, blocks);
+}
+
+// ---- what a unit waits for.  ready[phase][z][I] counts the epilogue warps (16 a block) that
+// have stored their part of block row I of X, A or B, over all steps.  (Nothing else is
+// needed: a complete row of B needs all of A, which needs all of X of the step before, so
+// that no buffer is written while an earlier phase still reads it, with two A in turn.)
+constexpr int kWarpsOfBlock = 2 * kEpilogueWarps;
+
+__device__ __forceinline__ int* ready_at(const OrthoArgs& a, int phase, int z, int I) {
+  const int nr = blocks_of(a.r);
+  return a.ready + (static_cast<long long>(z) * 3 + phase) * nr + I;
+}
+
+__device__ bool wait_ready(const OrthoArgs& a, const int* p, int want, volatile int* abort) {
+  for (uint32_t n = 0; n < kReadyLimit; ++n) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    if (v >= want) return true;
+    if ((n & 255u) == 255u &&
+        (*abort || *reinterpret_cast<volatile int*>(&a.header->status) == kStatusTimeout))
+      return false;
+  }
+  return false;
+}
+
+// Waits until what unit x reads is there.
+__device__ bool wait_inputs(const OrthoArgs& a, int phase, int step, const Unit& x, volatile int* abort) {
+  const int nr = blocks_of(a.r), nc = blocks_of(a.c);
+  if (phase == kGram) {              // X's rows I and J of the step before
+    if (step == 0) return true;
+    const int want = step * nc * kWarpsOfBlock;
+    return wait_ready(a, ready_at(a, kUpdate, x.z, x.I), want, abort) &&
+           (x.I == x.J || wait_ready(a, ready_at(a, kUpdate, x.z, x.J), want, abort));
+  }
+  const int want = (step + 1) * nr * kWarpsOfBlock;
+  if (phase == kPoly)
+    return wait_ready(a, ready_at(a, kGram, x.z, x.I), want, abort) &&
+           (x.I == x.J || wait_ready(a, ready_at(a, kGram, x.z, x.J), want, abort));
+  return wait_ready(a, ready_at(a, kPoly, x.z, x.I), want, abort);
+}
+
+// The warp has stored its part of unit x.
+__device__ __forceinline__ void signal_ready(const OrthoArgs& a, int phase, const Unit& x) {
+  ptx::fence_proxy_async();          // tensor copies read it next
+  __syncwarp();
+  if (threadIdx.x % 32 == 0) {
+    ptx::red_release_add(ready_at(a, phase, x.z, x.I), 1);
+    if (phase != kUpdate && x.I != x.J) ptx::red_release_add(ready_at(a, phase, x.z, x.J), 1);
+  }
 }
 
 // Waits for the phase of `bar` with the given parity; false if it gave up.
@@ -452,6 +523,7 @@ __device__ __forceinline__ void release_acc(uint32_t acc_empty) {
 struct EpilogueWarp {
   float* buf;                        // its turning buffer
   volatile int* abort;
+  int rank, index;                   // its CTA of the pair, and which of the CTA's epilogue warps it is
 };
 
 __device__ __forceinline__ uint4 load_v4(const __half* p) {
@@ -461,10 +533,17 @@ __device__ __forceinline__ uint4 load_v4(const __half* p) {
   return v;
 }
 
+// wait_inputs for a warp that reads them itself.
+__device__ __forceinline__ bool warp_ready(const OrthoArgs& a, int phase, int step, const Unit& x,
+                                           volatile int* abort) {
+  const bool ok = threadIdx.x % 32 != 0 || wait_inputs(a, phase, step, x, abort);
+  return __all_sync(kAll, ok);
+}
+
 // One warp's part of a finished block of an update: 32 rows from i0, kWarpCols columns from j.  The
 // products are turned, so that X's two parts are read and written 16 bytes a lane; they are
 // read a piece ahead, the first before the products are done.
-__device__ __forceinline__ bool epilogue_update(const OrthoArgs& a, int step, const Tile& x, int i0, int j,
+__device__ __forceinline__ bool epilogue_update(const OrthoArgs& a, int step, const Unit& x, int i0, int j,
                                                 uint32_t from, uint64_t* acc_full, uint32_t parity,
                                                 uint32_t acc_empty, const EpilogueWarp& w) {
   const int lane = threadIdx.x % 32;
@@ -487,6 +566,7 @@ __device__ __forceinline__ bool epilogue_update(const OrthoArgs& a, int step, co
         rest[h] = load_v4(lo + (u * kPiece + 8 * h) * static_cast<long long>(ld));
       }
   };
+  if (!warp_ready(a, kUpdate, step, x, w.abort)) return false;
   load(0);
   float own[8];                                       // a + what is left of B_ii
 #pragma unroll
@@ -538,46 +618,97 @@ __device__ __forceinline__ bool epilogue_update(const OrthoArgs& a, int step, co
       }
     }
   }
+  if (!last) signal_ready(a, kUpdate, x);
   return true;
 }
 
 // The same for A = X X^T or B = b A + c A^2: 32 rows from i0, kWarpCols columns from j of a block on
 // or below the diagonal, and its mirror.
+//
+// Where the inner dimension is split, each part's warp stores its sums, and the one that comes
+// last adds the parts up in their order (so the result does not depend on which that is).
 template <int kPhase>
-__device__ __forceinline__ bool epilogue_square(const OrthoArgs& a, const Tile& x, int i0, int j, uint32_t from,
-                                                uint64_t* acc_full, uint32_t parity, uint32_t acc_empty,
-                                                const EpilogueWarp& w) {
+__device__ __forceinline__ bool epilogue_square(const OrthoArgs& a, int step, const Unit& x, int i0, int j,
+                                                uint32_t from, uint64_t* acc_full, uint32_t parity,
+                                                uint32_t acc_empty, const EpilogueWarp& w) {
   const int lane = threadIdx.x % 32;
   const int i = i0 + lane;
   const int pieces = i0 < a.r ? min(max((a.r - j + kPiece - 1) / kPiece, 0), kPieces) : 0;
   const int ld = a.ld;
   const long long matrix = static_cast<long long>(x.z) * a.r * ld;
   const bool row = i < a.r;
-  const __half* o_row = a.a + matrix + static_cast<long long>(i) * ld + j;    // A_ij = A_ji, along the row
+  const __half* o_row = a.a[step & 1] + matrix + static_cast<long long>(i) * ld + j;    // A_ij = A_ji, along the row
   Half16 o = {};
   float rest_a = 0.0f;               // what rounding left of A_ii
-  if (kPhase == kPoly && row && pieces > 0) {
-    o = load_half16(o_row);
-    rest_a = a.diag_a[x.z * static_cast<long long>(ld) + i];
+  if (kPhase == kPoly) {
+    if (!warp_ready(a, kPoly, step, x, w.abort)) return false;
+    if (row && pieces > 0) {
+      o = load_half16(o_row);
+      rest_a = a.diag_a[step & 1][x.z * static_cast<long long>(ld) + i];
+    }
   }
   if (!__all_sync(kAll, wait_bar(acc_full, parity, w.abort))) return false;
   ptx::tmem_fence_after();
+  const int parts = a.split[kPhase];
+  const float* sums = nullptr;       // the first part's
+  constexpr int kPartStride = kBlock * kBlock;
+  if (parts > 1) {
+    const int nr = blocks_of(a.r), blocks = nr * (nr + 1) / 2;
+    const long long block = static_cast<long long>(x.z) * blocks + x.I * (x.I + 1) / 2 + x.J;
+    const int place = w.rank * kEpilogueWarps + w.index;
+    float* first = a.partial + block * parts * kPartStride + place * (32 * kWarpCols) + lane;
+    float* mine = first + static_cast<long long>(x.part) * kPartStride;
+#pragma unroll 1
+    for (int u = 0; u < pieces; ++u) {
+      uint32_t acc[kPiece];
+      ptx::tmem_load16(acc, from + u * kPiece);
+      ptx::tmem_wait_load();
+#pragma unroll
+      for (int q = 0; q < kPiece; ++q) mine[(u * kPiece + q) * 32] = __uint_as_float(acc[q]);
+    }
+    release_acc(acc_empty);
+    int before = 0;
+    if (lane == 0)
+      before = ptx::add_acq_rel(a.arrived + ((static_cast<long long>(x.z) * 2 + kPhase) * blocks +
+                                             (block - static_cast<long long>(x.z) * blocks)) * kWarpsOfBlock + place, 1);
+    before = __shfl_sync(kAll, before, 0);
+    if (before % parts != parts - 1) return true;      // not the last part
+    sums = first;
+  }
   const float f = kPhase == kGram ? 1.0f / (a.s * a.s) : a.cc;
-  __half* m = (kPhase == kGram ? a.a : a.b) + matrix;
+  __half* m = (kPhase == kGram ? a.a[step & 1] : a.b) + matrix;
   __half* m_row = m + static_cast<long long>(i) * ld + j;
   const int ti = i0 + lane % 4 * 8;                   // after the turn: rows ti .. ti + 7 of ...
   const int cols = ti < a.r ? a.r - j - lane / 4 : 0; // ... columns j + lane / 4 + kPiece u + 8 h
   __half* m_col = m + static_cast<long long>(j + lane / 4) * ld + ti;
   uint32_t acc[kPiece];
-  if (pieces > 0) ptx::tmem_load16(acc, from);
-  else release_acc(acc_empty);
+  if (parts == 1) {
+    if (pieces > 0) ptx::tmem_load16(acc, from);
+    else release_acc(acc_empty);
+  }
 #pragma unroll 1
   for (int u = 0; u < pieces; ++u) {
     const int j0 = j + u * kPiece;
-    ptx::tmem_wait_load();
     float v[kPiece];
+    if (parts == 1) {
+      ptx::tmem_wait_load();
 #pragma unroll
-    for (int q = 0; q < kPiece; ++q) v[q] = __uint_as_float(acc[q]) * f;
+      for (int q = 0; q < kPiece; ++q) v[q] = __uint_as_float(acc[q]) * f;
+      if (u + 1 < pieces) ptx::tmem_load16(acc, from + (u + 1) * kPiece);
+      else release_acc(acc_empty);
+    } else {
+      const float* p = sums + u * kPiece * 32;
+#pragma unroll
+      for (int q = 0; q < kPiece; ++q) v[q] = p[q * 32];
+#pragma unroll 1
+      for (int k = 1; k < parts; ++k) {
+        p += kPartStride;
+#pragma unroll
+        for (int q = 0; q < kPiece; ++q) v[q] += p[q * 32];
+      }
+#pragma unroll
+      for (int q = 0; q < kPiece; ++q) v[q] *= f;
+    }
     if constexpr (kPhase == kPoly) {
 #pragma unroll
       for (int q = 0; q < kPiece / 2; ++q) {
@@ -598,10 +729,8 @@ __device__ __forceinline__ bool epilogue_square(const OrthoArgs& a, const Tile& 
         left = v[q] - __half2float(__float2half_rn(v[q]));
       }
       if (i >= j0 && i < j0 + kPiece && row)
-        (kPhase == kGram ? a.diag_a : a.diag_b)[x.z * static_cast<long long>(ld) + i] = left;
+        (kPhase == kGram ? a.diag_a[step & 1] : a.diag_b)[x.z * static_cast<long long>(ld) + i] = left;
     }
-    if (u + 1 < pieces) ptx::tmem_load16(acc, from + (u + 1) * kPiece);
-    else release_acc(acc_empty);
     if (kPhase == kPoly && row && u + 1 < pieces) o = load_half16(o_row + (u + 1) * kPiece);
     if (x.I != x.J && row) store_half16(m_row + u * kPiece, v);
     float t[2][8];
@@ -614,13 +743,17 @@ __device__ __forceinline__ bool epilogue_square(const OrthoArgs& a, const Tile& 
                        pack_half(t[h][6], t[h][7]));
     }
   }
+  signal_ready(a, kPhase, x);
   return true;
 }
 
-// All phases of all steps, one cooperative launch of CTA pairs: a pair takes blocks of 256 x
-// 256, and a barrier over the grid ends each phase.  Per CTA: warp 0 copies operands (TMA),
-// warp 1 of the pair's first CTA issues the products, the other warps take finished
-// accumulators (two in tensor memory, so that the products of the next block run meanwhile).
+// All phases of all steps, one cooperative launch of CTA pairs.  The units of all phases in
+// order go round the pairs; a unit waits for the block rows that it reads, which units before
+// it in the order store, so the earliest unfinished unit never waits and the phases (and
+// the matrices of a batch) overlap without a barrier over the grid.  Per CTA: warp 0 copies
+// operands (TMA), warp 1 of the pair's first CTA issues the products, the epilogue warps take
+// finished accumulators (two in tensor memory, so that the products of the next unit run
+// meanwhile).
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const OrthoArgs a) {
   extern __shared__ unsigned char raw[];
@@ -644,7 +777,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     ptx::fence_mbar_init();
     ptx::prefetch_tensor_map(&maps.xt[0]);
     ptx::prefetch_tensor_map(&maps.xt[1]);
-    ptx::prefetch_tensor_map(&maps.a);
+    ptx::prefetch_tensor_map(&maps.a[0]);
+    ptx::prefetch_tensor_map(&maps.a[1]);
     ptx::prefetch_tensor_map(&maps.b);
   }
   if (warp == 1) ptx::tmem_alloc_pair(&sm.tmem);
@@ -657,128 +791,113 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 
   uint32_t stage = 0, stage_phase = 0;      // producer's or issuer's place in the ring
   uint32_t acc = 0, acc_phase = 0;          // issuer's or epilogue's accumulator
-  EpilogueWarp ew{};
-  if (warp >= kFirstEpilogueWarp) {
-    ew.buf = reinterpret_cast<float*>(raw + (stages - ptx::smem_u32(raw)) + kStages * kStageBytes) +
-             (warp - kFirstEpilogueWarp) * kTurnFloats;
-    ew.abort = abort;
-  }
-
-  for (int p = 0; p < 3 * a.steps; ++p) {
-    const int phase = p % 3, step = p / 3, cur = step & 1;
-    const int tiles = tiles_of(a, phase);
-    const int blocks_k = ((phase == kGram ? a.c : a.r) + kStepK - 1) / kStepK;
-    if (warp == 0) {
-      if (lane == 0) {
-        const CUtensorMap* ma = phase == kGram ? &maps.xt[cur] : phase == kPoly ? &maps.a : &maps.b;
-        const CUtensorMap* mb = phase == kPoly ? &maps.a : &maps.xt[cur];
-        for (int t = pair; t < tiles && !*abort; t += pairs) {
-          const Tile x = tile_at(a, phase, t);
-          const int ra = x.I * kBlock + rank * 128, rb = x.J * kBlock + rank * 128;
-          for (int kb = 0; kb < blocks_k; ++kb) {
-            if (!wait_bar(&sm.empty[stage], stage_phase ^ 1u, abort)) {
-              gave_up(a, abort);
-              break;
-            }
-            if (rank == 0) ptx::mbar_arrive_expect_tx(&sm.full[stage], 2 * kStageBytes);
-            const uint32_t bar = ptx::map_to_rank(ptx::smem_u32(&sm.full[stage]), 0);
-            const uint32_t dst = stages + stage * kStageBytes;
-            const int k = kb * kStepK;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int da = ra + 64 * h, db = rb + 64 * h;
-              ptx::tma_load_3d_pair(dst + h * kBoxBytes, ma, phase == kGram ? da : k, phase == kGram ? k : da, x.z, bar);
-              ptx::tma_load_3d_pair(dst + kOperandBytes + h * kBoxBytes, mb, phase == kGram ? db : k,
-                                    phase == kGram ? k : db, x.z, bar);
-            }
-            if (++stage == kStages) {
-              stage = 0;
-              stage_phase ^= 1u;
-            }
-          }
+  auto next_stage = [&] {
+    if (++stage == kStages) {
+      stage = 0;
+      stage_phase ^= 1u;
+    }
+  };
+  auto next_acc = [&] {
+    if (++acc == 2) {
+      acc = 0;
+      acc_phase ^= 1u;
+    }
+  };
+  // body(phase, step, unit) for this pair's units in order, until one gives up
+  auto for_units = [&](auto&& body) {
+    int offset = 0;                  // units of the phases so far, modulo the pairs
+    for (int p = 0; p < 3 * a.steps; ++p) {
+      const int phase = p % 3, step = p / 3;
+      const int units = units_of(a, phase);
+      for (int t = pair >= offset ? pair - offset : pair - offset + pairs; t < units; t += pairs) {
+        if (*abort) return;
+        if (!body(phase, step, unit_at(a, phase, t))) {
+          gave_up(a, abort);
+          return;
         }
       }
-      __syncwarp();
-    } else if (warp == 1 && rank == 0) {
-      if (lane == 0) {
+      offset = (offset + units) % pairs;
+    }
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      for_units([&](int phase, int step, const Unit& x) {
+        const int cur = step & 1;
+        const CUtensorMap* ma = phase == kGram ? &maps.xt[cur] : phase == kPoly ? &maps.a[cur] : &maps.b;
+        const CUtensorMap* mb = phase == kPoly ? &maps.a[cur] : &maps.xt[cur];
+        const int ra = x.I * kBlock + rank * 128, rb = x.J * kBlock + rank * 128;
+        int k0, k1;
+        inner_of(a, phase, x, k0, k1);
+        if (!wait_inputs(a, phase, step, x, abort)) return false;
+        ptx::fence_proxy_async();    // the acquires above before the tensor copies
+        for (int kb = k0; kb < k1; ++kb) {
+          if (!wait_bar(&sm.empty[stage], stage_phase ^ 1u, abort)) return false;
+          if (rank == 0) ptx::mbar_arrive_expect_tx(&sm.full[stage], 2 * kStageBytes);
+          const uint32_t bar = ptx::map_to_rank(ptx::smem_u32(&sm.full[stage]), 0);
+          const uint32_t dst = stages + stage * kStageBytes;
+          const int k = kb * kStepK;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int da = ra + 64 * h, db = rb + 64 * h;
+            ptx::tma_load_3d_pair(dst + h * kBoxBytes, ma, phase == kGram ? da : k, phase == kGram ? k : da, x.z, bar);
+            ptx::tma_load_3d_pair(dst + kOperandBytes + h * kBoxBytes, mb, phase == kGram ? db : k,
+                                  phase == kGram ? k : db, x.z, bar);
+          }
+          next_stage();
+        }
+        return true;
+      });
+    }
+    __syncwarp();
+  } else if (warp == 1 && rank == 0) {
+    if (lane == 0) {
+      for_units([&](int phase, int, const Unit& x) {
         // fp32 accumulator, fp16 operands, 256 x 256; X X^T has both operands MN-major
         const uint32_t idesc = 1u << 4 | (kBlock >> 3) << 17 | (kBlock >> 4) << 24 | (phase == kGram ? 3u << 15 : 0u);
         // K-major: 8-row groups 1024 bytes apart, 16 inner elements = 32 bytes.  MN-major:
         // groups of 64 rows a box apart, groups of 8 inner elements 1024 bytes apart.
         const uint32_t lead = phase == kGram ? kBoxBytes : 16;
         const uint32_t k_bytes = phase == kGram ? 2048 : 32;
-        for (int t = pair; t < tiles && !*abort; t += pairs) {
-          if (!wait_bar(&sm.acc_empty[acc], acc_phase ^ 1u, abort)) {
-            gave_up(a, abort);
-            break;
-          }
+        int k0, k1;
+        inner_of(a, phase, x, k0, k1);
+        if (!wait_bar(&sm.acc_empty[acc], acc_phase ^ 1u, abort)) return false;
+        ptx::tmem_fence_after();
+        const uint32_t d = tmem + acc * kBlock;
+        for (int kb = k0; kb < k1; ++kb) {
+          if (!wait_bar(&sm.full[stage], stage_phase, abort)) return false;
           ptx::tmem_fence_after();
-          const uint32_t d = tmem + acc * kBlock;
-          for (int kb = 0; kb < blocks_k; ++kb) {
-            if (!wait_bar(&sm.full[stage], stage_phase, abort)) {
-              gave_up(a, abort);
-              break;
-            }
-            ptx::tmem_fence_after();
-            const uint32_t at = stages + stage * kStageBytes;
+          const uint32_t at = stages + stage * kStageBytes;
 #pragma unroll
-            for (int k = 0; k < kStepK / 16; ++k)
-              ptx::mma_f16_pair(d, operand_desc(at + k * k_bytes, lead, 1024),
-                                operand_desc(at + kOperandBytes + k * k_bytes, lead, 1024), idesc, kb > 0 || k > 0);
-            ptx::mma_commit_pair(&sm.empty[stage]);
-            if (++stage == kStages) {
-              stage = 0;
-              stage_phase ^= 1u;
-            }
-          }
-          ptx::mma_commit_pair(&sm.acc_full[acc]);
-          if (++acc == 2) {
-            acc = 0;
-            acc_phase ^= 1u;
-          }
+          for (int k = 0; k < kStepK / 16; ++k)
+            ptx::mma_f16_pair(d, operand_desc(at + k * k_bytes, lead, 1024),
+                              operand_desc(at + kOperandBytes + k * k_bytes, lead, 1024), idesc, kb > k0 || k > 0);
+          ptx::mma_commit_pair(&sm.empty[stage]);
+          next_stage();
         }
-      }
-      __syncwarp();
-    } else if (warp >= kFirstEpilogueWarp) {
-      const int quarter = warp % 4, part = (warp - kFirstEpilogueWarp) / 4;
-      for (int t = pair; t < tiles && !*abort; t += pairs) {
-        const Tile x = tile_at(a, phase, t);
-        const uint32_t from = tmem + acc * kBlock + part * kWarpCols + (static_cast<uint32_t>(quarter) << 21);
-        const int i0 = x.I * kBlock + rank * 128 + quarter * 32;
-        const int j = x.J * kBlock + part * kWarpCols;
-        uint64_t* full = &sm.acc_full[acc];
-        const uint32_t empty = ptx::map_to_rank(ptx::smem_u32(&sm.acc_empty[acc]), 0);
-        const bool ok = phase == kGram ? epilogue_square<kGram>(a, x, i0, j, from, full, acc_phase, empty, ew)
-                        : phase == kPoly ? epilogue_square<kPoly>(a, x, i0, j, from, full, acc_phase, empty, ew)
-                                         : epilogue_update(a, step, x, i0, j, from, full, acc_phase, empty, ew);
-        if (!ok) {
-          gave_up(a, abort);
-          break;
-        }
-        if (++acc == 2) {
-          acc = 0;
-          acc_phase ^= 1u;
-        }
-      }
-      ptx::fence_proxy_async();      // what was stored is read by tensor copies next
+        ptx::mma_commit_pair(&sm.acc_full[acc]);
+        next_acc();
+        return true;
+      });
     }
-    if (p + 1 == 3 * a.steps) break;
-    // ---- barrier over the grid
-    if (__syncthreads_or(*abort)) break;
-    if (threadIdx.x == 0) {
-      ptx::red_release_add(a.barrier, 1);
-      const int want = (p + 1) * static_cast<int>(gridDim.x);
-      bool there = false;
-      for (uint32_t n = 0; n < kGridWaitLimit && !there; ++n) {
-        int v;
-        asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(a.barrier) : "memory");
-        there = v >= want;
-        if (!there && (n & 255u) == 255u && *reinterpret_cast<volatile int*>(&a.header->status) == kStatusTimeout) break;
-      }
-      if (!there) gave_up(a, abort);
-    }
-    if (__syncthreads_or(*abort)) break;
-    if (lane == 0) ptx::fence_proxy_async();   // the acquire before the next tensor copies
+    __syncwarp();
+  } else if (warp >= kFirstEpilogueWarp) {
+    const int quarter = warp % 4, part = (warp - kFirstEpilogueWarp) / 4;
+    const EpilogueWarp ew{reinterpret_cast<float*>(raw + (stages - ptx::smem_u32(raw)) + kStages * kStageBytes) +
+                              (warp - kFirstEpilogueWarp) * kTurnFloats,
+                          abort, static_cast<int>(rank), warp - kFirstEpilogueWarp};
+    for_units([&](int phase, int step, const Unit& x) {
+      const uint32_t from = tmem + acc * kBlock + part * kWarpCols + (static_cast<uint32_t>(quarter) << 21);
+      const int i0 = x.I * kBlock + rank * 128 + quarter * 32;
+      const int j = x.J * kBlock + part * kWarpCols;
+      uint64_t* full = &sm.acc_full[acc];
+      const uint32_t empty = ptx::map_to_rank(ptx::smem_u32(&sm.acc_empty[acc]), 0);
+      const bool ok = phase == kGram ? epilogue_square<kGram>(a, step, x, i0, j, from, full, acc_phase, empty, ew)
+                      : phase == kPoly ? epilogue_square<kPoly>(a, step, x, i0, j, from, full, acc_phase, empty, ew)
+                                       : epilogue_update(a, step, x, i0, j, from, full, acc_phase, empty, ew);
+      next_acc();
+      return ok;
+    });
   }
 
   // ---- end: nothing of the pair may be in flight when it leaves
@@ -871,7 +990,9 @@ cudaError_t launch_orthogonalize(const OrthoCall& q, cudaStream_t stream) {
   in.xt = reinterpret_cast<__half*>(ws + L.xt[0]);
   in.xl = reinterpret_cast<__half*>(ws + L.xl);
   in.header = reinterpret_cast<Header*>(ws + L.header);
-  in.barrier = reinterpret_cast<int*>(ws + L.barrier);
+  const int64_t nr = sh.blocks_r, nc = sh.blocks_c;
+  in.counters = reinterpret_cast<int*>(ws + L.counters);
+  in.num_counters = static_cast<int>(sh.counters());
 
   OrthoMaps maps;
   cudaError_t e = cudaSuccess;
@@ -880,7 +1001,8 @@ cudaError_t launch_orthogonalize(const OrthoCall& q, cudaStream_t stream) {
   };
   add(&maps.xt[0], L.xt[0], sh.c);
   add(&maps.xt[1], L.xt[1], sh.c);
-  add(&maps.a, L.a, sh.r);
+  add(&maps.a[0], L.a[0], sh.r);
+  add(&maps.a[1], L.a[1], sh.r);
   add(&maps.b, L.b, sh.r);
   if (e != cudaSuccess) return e;
 
@@ -897,16 +1019,22 @@ cudaError_t launch_orthogonalize(const OrthoCall& q, cudaStream_t stream) {
   a.xt[0] = in.xt;
   a.xt[1] = reinterpret_cast<__half*>(ws + L.xt[1]);
   a.xl = in.xl;
-  a.a = reinterpret_cast<__half*>(ws + L.a);
   a.b = reinterpret_cast<__half*>(ws + L.b);
-  a.diag_a = reinterpret_cast<float*>(ws + L.diag_a);
+  for (int i = 0; i < 2; ++i) {
+    a.a[i] = reinterpret_cast<__half*>(ws + L.a[i]);
+    a.diag_a[i] = reinterpret_cast<float*>(ws + L.diag_a[i]);
+  }
   a.diag_b = reinterpret_cast<float*>(ws + L.diag_b);
   a.out = static_cast<__nv_bfloat16*>(q.out);
   a.out_batch = q.out_batch_stride;
   a.out_row = q.out_row_stride;
   a.tall = sh.tall;
   a.header = in.header;
-  a.barrier = in.barrier;
+  a.ready = in.counters;
+  a.arrived = in.counters + sh.batch * 3 * nr;
+  a.partial = reinterpret_cast<float*>(ws + L.partial);
+  a.split[kGram] = sh.split_gram;
+  a.split[kPoly] = sh.split_poly;
 
   const unsigned batch = static_cast<unsigned>(sh.batch);
   ortho_norm_kernel<<<dim3(sh.norm_blocks, batch), 256, 0, stream>>>(in);
@@ -916,9 +1044,8 @@ cudaError_t launch_orthogonalize(const OrthoCall& q, cudaStream_t stream) {
 
   int dev = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-  const int64_t nr = (sh.r + kBlock - 1) / kBlock, nc = (sh.c + kBlock - 1) / kBlock;
-  const int64_t most = sh.batch * nr * nc;          // blocks of the largest phase
-  const int pairs = static_cast<int>(most < g_pairs[dev] ? most : g_pairs[dev]);
+  const int64_t most = sh.batch * std::max(nr * nc, nr * (nr + 1) / 2 * std::max(sh.split_gram, sh.split_poly));
+  const int pairs = static_cast<int>(std::min<int64_t>(most, g_pairs[dev]));
   if (pairs < 1) return cudaErrorLaunchOutOfResources;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * pairs);
