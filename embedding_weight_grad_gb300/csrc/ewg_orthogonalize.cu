@@ -25,10 +25,12 @@
 //     and at most 1.2 s; A and B need no scale.
 //
 // Layout.  Every buffer is [., ld] fp16 with the r index inside: X^T (two, alternating), the
-// rest of X^T, A and B.  The accumulator of a product has its row index across the lanes of a
-// warp, so all stores of X^T and of the mirrored blocks are contiguous.  As an operand of X
-// X^T, X^T has the product's rows inside (MN-major); for B X it has the inner index inside
-// (K-major), as A and B have by symmetry.
+// rest of X^T, A (two, alternating) and B; of A and B only the blocks on and below the
+// diagonal.  A block above it is read as the transpose of its mirror: the tensor cores take
+// an operand with its inner index inside (K-major) or outside (MN-major), so an operand's
+// row of blocks changes from one to the other at the diagonal.  X^T is MN-major in X X^T.  The
+// update computes X^T's blocks, so that every accumulator lane holds neighbours of one row
+// of what it reads and writes.
 #include <algorithm>
 #include <cmath>
 #include <mutex>
@@ -256,30 +258,35 @@ __global__ void __launch_bounds__(256) ortho_scale_kernel(const OrthoIn a) {
 
 constexpr int kBlock = 256;          // a pair of CTAs computes 256 x 256; each CTA 128 rows
 constexpr int kStepK = 64;           // inner elements of a stage: one 128-byte swizzled row
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kOperandBytes = 128 * kStepK * 2;       // one CTA's half of an operand's stage
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kBoxBytes = 64 * kStepK * 2;            // one tensor copy: 64 rows of 128 bytes
 constexpr int kFirstEpilogueWarp = 4;
 constexpr int kEpilogueWarps = 8;
+constexpr int kWarpsOfBlock = 2 * kEpilogueWarps;     // of the pair
 constexpr int kWarpCols = 4 * kBlock / kEpilogueWarps;   // columns of an epilogue warp (all take 32 rows)
-constexpr int kGemmThreads = 32 * (kFirstEpilogueWarp + kEpilogueWarps);
-// The epilogue takes an accumulator in pieces of 32 rows x kPiece columns a warp, turned
-// through shared memory: kPiece rows of 32 fp32 numbers, 16 bytes between rows (which puts a
-// quarter-warp's 16-byte reads on different banks).
-constexpr int kPiece = 16;
+// The epilogue takes a warp's 32 rows in pieces of 64 columns, which come and go by tensor copies
+// of 128-byte rows through a slot of the warp: two parts of X, or two pieces of A or B.
+// (Copies by the threads themselves, of 32 or 64 bytes a row, took two to three times as long:
+// the path to L2 carries requests, not bytes.)
+constexpr int kPiece = 64;
 constexpr int kPieces = kWarpCols / kPiece;
-constexpr int kTurnPitch = 36;                        // floats
-constexpr int kTurnFloats = kPiece * kTurnPitch;
-constexpr size_t kGemmSmem = static_cast<size_t>(kStages) * kStageBytes + kEpilogueWarps * kTurnFloats * 4 + 1024;
-static_assert(kGemmSmem + 512 <= 227 * 1024, "stages and turning buffers fit in shared memory");
+constexpr int kPieceBytes = 32 * kPiece * 2;
+constexpr int kSlotBytes = 2 * kPieceBytes;
+constexpr int kGemmThreads = 32 * (kFirstEpilogueWarp + kEpilogueWarps);
+constexpr size_t kGemmSmem =
+    static_cast<size_t>(kStages) * kStageBytes + kEpilogueWarps * kSlotBytes + 1024;
+static_assert(kWarpsOfBlock == kOrthoWarps && kBlock == kOrthoBlock, "as the workspace is laid out for");
+static_assert(kGemmSmem + 512 <= 227 * 1024, "stages and slots fit in shared memory");
 constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr uint32_t kReadyLimit = 1u << 22;
 
 enum Phase { kGram = 0, kPoly = 1, kUpdate = 2 };
 
 struct OrthoMaps {
-  CUtensorMap xt[2], a[2], b;        // boxes of 64 x 64, swizzled
+  CUtensorMap xt[2], a[2], b;        // operands: boxes of 64 x 64
+  CUtensorMap xt_piece[2], xl_piece, a_piece[2], b_piece;   // pieces: 64 of the r index x 32
 };
 
 struct OrthoArgs {
@@ -287,12 +294,9 @@ struct OrthoArgs {
   int steps;
   float ca, cb, cc;                  // the polynomial's coefficients
   float s;                           // X is stored times s
-  __half* xt[2];
-  __half* xl;
-  __half* a[2];                      // of even and odd steps
-  __half* b;
-  float* diag_a[2];                  // [batch][ld]: what rounding left of the diagonals
+  float* diag_a[2];                  // [batch][ld]: what rounding left of the diagonals (A's of even and odd steps)
   float* diag_b;
+  int chunk;                         // matrices that go through the steps together
   int split[2];                      // parts of the inner dimension of X X^T and A A
   float* partial;                    // split products: [batch][block][part][CTA][warp][column][row]
   __nv_bfloat16* out;
@@ -305,6 +309,7 @@ struct OrthoArgs {
 
 struct GemmSmem {
   uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
+  uint64_t piece[kEpilogueWarps][2];
   uint32_t tmem;
   int abort;
 };
@@ -323,15 +328,16 @@ struct Unit {
   int z, I, J, part;
 };
 
-__device__ __forceinline__ int units_of(const OrthoArgs& a, int phase) {
+// Units of a phase for `matrices` matrices.
+__device__ __forceinline__ int units_of(const OrthoArgs& a, int phase, int matrices) {
   const int nr = blocks_of(a.r);
-  return a.batch * (phase == kUpdate ? nr * blocks_of(a.c) : nr * (nr + 1) / 2 * a.split[phase]);
+  return matrices * (phase == kUpdate ? nr * blocks_of(a.c) : nr * (nr + 1) / 2 * a.split[phase]);
 }
 
-// Unit t of a phase.  The orders let a phase start before the one before it has ended: the
+// Unit t of a phase for the matrices from z0 on.  The orders let a phase start before the one before it has ended: the
 // update goes by rows, which is what A's blocks by rows need; B's blocks go by columns, whose
 // first ones complete B's first rows, which the update's first rows need.
-__device__ __forceinline__ Unit unit_at(const OrthoArgs& a, int phase, int t) {
+__device__ __forceinline__ Unit unit_at(const OrthoArgs& a, int phase, int z0, int t) {
   const int nr = blocks_of(a.r);
   Unit x;
   if (phase == kUpdate) {
@@ -341,6 +347,7 @@ __device__ __forceinline__ Unit unit_at(const OrthoArgs& a, int phase, int t) {
     x.I = t / nc;
     x.J = t - x.I * nc;
     x.part = 0;
+    x.z += z0;
     return x;
   }
   const int blocks = nr * (nr + 1) / 2, parts = a.split[phase];
@@ -355,6 +362,7 @@ __device__ __forceinline__ Unit unit_at(const OrthoArgs& a, int phase, int t) {
   const int col = t - row * (row + 1) / 2;
   x.I = phase == kPoly ? nr - 1 - col : row;
   x.J = phase == kPoly ? nr - 1 - row : col;
+  x.z += z0;
   return x;
 }
 
@@ -366,11 +374,10 @@ __device__ __forceinline__ void inner_of(const OrthoArgs& a, int phase, const Un
   last = min(first + per, blocks);
 }
 
-// ---- what a unit waits for.  ready[phase][z][I] counts the epilogue warps (16 a block) that
+// ---- what a unit waits for.  ready[phase][z][I] counts the epilogue warps (8 a unit) that
 // have stored their part of block row I of X, A or B, over all steps.  (Nothing else is
 // needed: a complete row of B needs all of A, which needs all of X of the step before, so
 // that no buffer is written while an earlier phase still reads it, with two A in turn.)
-constexpr int kWarpsOfBlock = 2 * kEpilogueWarps;
 
 __device__ __forceinline__ int* ready_at(const OrthoArgs& a, int phase, int z, int I) {
   const int nr = blocks_of(a.r);
@@ -398,21 +405,23 @@ __device__ bool wait_inputs(const OrthoArgs& a, int phase, int step, const Unit&
     return wait_ready(a, ready_at(a, kUpdate, x.z, x.I), want, abort) &&
            (x.I == x.J || wait_ready(a, ready_at(a, kUpdate, x.z, x.J), want, abort));
   }
-  const int want = (step + 1) * nr * kWarpsOfBlock;
+  const int want = (step + 1) * nr * kWarpsOfBlock * a.split[phase == kPoly ? kGram : kPoly];
   if (phase == kPoly)
     return wait_ready(a, ready_at(a, kGram, x.z, x.I), want, abort) &&
            (x.I == x.J || wait_ready(a, ready_at(a, kGram, x.z, x.J), want, abort));
   return wait_ready(a, ready_at(a, kPoly, x.z, x.I), want, abort);
 }
 
-// The warp has stored its part of unit x.
+// The warp has stored its part of unit x, by tensor copies of lane 0 and (diagonals) plainly.
 __device__ __forceinline__ void signal_ready(const OrthoArgs& a, int phase, const Unit& x) {
-  ptx::fence_proxy_async();          // tensor copies read it next
   __syncwarp();
   if (threadIdx.x % 32 == 0) {
+    ptx::bulk_wait();
+    ptx::fence_proxy_async();
     ptx::red_release_add(ready_at(a, phase, x.z, x.I), 1);
     if (phase != kUpdate && x.I != x.J) ptx::red_release_add(ready_at(a, phase, x.z, x.J), 1);
   }
+  __syncwarp();
 }
 
 // Waits for the phase of `bar` with the given parity; false if it gave up.
@@ -435,102 +444,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return d;
 }
 
-// 16 neighbouring fp16 numbers, 32-byte aligned.
-struct Half16 {
-  uint32_t w[8];
-};
-__device__ __forceinline__ Half16 load_half16(const __half* p) {
-  Half16 h;
-  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(h.w[0]), "=r"(h.w[1]), "=r"(h.w[2]), "=r"(h.w[3]), "=r"(h.w[4]), "=r"(h.w[5]), "=r"(h.w[6]),
-                 "=r"(h.w[7])
-               : "l"(p)
-               : "memory");
-  return h;
-}
-__device__ __forceinline__ void store_half16(__half* p, const float (&v)[kPiece]) {
-  uint32_t w[8];
-#pragma unroll
-  for (int q = 0; q < 8; ++q) w[q] = pack_half(v[2 * q], v[2 * q + 1]);
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
-
-// A piece of 32 rows x 16 columns turned through shared memory: in, lane l holds row l; out, lane
-// l holds rows 8 (l % 4) .. + 7 of columns l / 4 and l / 4 + 8.
-__device__ __forceinline__ void turn(float* buf, int lane, const float (&v)[kPiece], float (&t)[2][8]) {
-#pragma unroll
-  for (int q = 0; q < kPiece; ++q) buf[q * kTurnPitch + lane] = v[q];
-  __syncwarp();
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const float4* p = reinterpret_cast<const float4*>(buf + (lane / 4 + 8 * h) * kTurnPitch + lane % 4 * 8);
-    const float4 x = p[0], y = p[1];
-    t[h][0] = x.x, t[h][1] = x.y, t[h][2] = x.z, t[h][3] = x.w;
-    t[h][4] = y.x, t[h][5] = y.y, t[h][6] = y.z, t[h][7] = y.w;
-  }
-  __syncwarp();
-}
-__device__ __forceinline__ void turn_back(float* buf, int lane, const float (&t)[2][8], float (&v)[kPiece]) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    float4* p = reinterpret_cast<float4*>(buf + (lane / 4 + 8 * h) * kTurnPitch + lane % 4 * 8);
-    p[0] = make_float4(t[h][0], t[h][1], t[h][2], t[h][3]);
-    p[1] = make_float4(t[h][4], t[h][5], t[h][6], t[h][7]);
-  }
-  __syncwarp();
-#pragma unroll
-  for (int q = 0; q < kPiece; ++q) v[q] = buf[q * kTurnPitch + lane];
-  __syncwarp();
-}
-
-// The last update's piece, to the caller's matrix: lane = row i, columns j0 .. + 15 of X.
-__device__ __forceinline__ void store_out(const OrthoArgs& a, int z, int i, int j0, const float (&v)[kPiece]) {
-  const int n = min(a.c - j0, kPiece);
-  if (i >= a.r) return;
-  __nv_bfloat16* out = a.out + z * a.out_batch;
-  const float unscale = 1.0f / a.s;
-  if (a.tall) {                      // out is [c, r]: neighbouring lanes, neighbouring elements
-    __nv_bfloat16* p = out + j0 * a.out_row + i;
-#pragma unroll
-    for (int q = 0; q < kPiece; ++q)
-      if (q < n) p[q * a.out_row] = __float2bfloat16_rn(v[q] * unscale);
-    return;
-  }
-  __nv_bfloat16* p = out + i * a.out_row + j0;
-  if (n == kPiece && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
-    uint32_t w[kPiece / 2];
-#pragma unroll
-    for (int q = 0; q < kPiece / 2; ++q) w[q] = pack_bf16(v[2 * q] * unscale, v[2 * q + 1] * unscale);
-    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-  } else {
-#pragma unroll
-    for (int q = 0; q < kPiece; ++q)
-      if (q < n) p[q] = __float2bfloat16_rn(v[q] * unscale);
-  }
-}
-
 // The warp has read its part of the accumulator.
 __device__ __forceinline__ void release_acc(uint32_t acc_empty) {
   ptx::tmem_fence_before();
   __syncwarp();
   if (threadIdx.x % 32 == 0) ptx::mbar_arrive_cluster(acc_empty);
-}
-
-// What an epilogue warp keeps through the kernel.
-struct EpilogueWarp {
-  float* buf;                        // its turning buffer
-  volatile int* abort;
-  int rank, index;                   // its CTA of the pair, and which of the CTA's epilogue warps it is
-};
-
-__device__ __forceinline__ uint4 load_v4(const __half* p) {
-  uint4 v;
-  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
-  return v;
 }
 
 // wait_inputs for a warp that reads them itself.
@@ -540,82 +458,146 @@ __device__ __forceinline__ bool warp_ready(const OrthoArgs& a, int phase, int st
   return __all_sync(kAll, ok);
 }
 
-// One warp's part of a finished block of an update: 32 rows from i0, kWarpCols columns from j.  The
-// products are turned, so that X's two parts are read and written 16 bytes a lane; they are
-// read a piece ahead, the first before the products are done.
-__device__ __forceinline__ bool epilogue_update(const OrthoArgs& a, int step, const Unit& x, int i0, int j,
-                                                uint32_t from, uint64_t* acc_full, uint32_t parity,
-                                                uint32_t acc_empty, const EpilogueWarp& w) {
-  const int lane = threadIdx.x % 32;
-  const int pieces = i0 < a.r ? min(max((a.c - j + kPiece - 1) / kPiece, 0), kPieces) : 0;
+// Where an epilogue warp finds a unit's accumulator, and its slot.
+struct Acc {
+  uint32_t from;                     // its columns in tensor memory
+  uint64_t* full;
+  uint32_t parity;
+  uint32_t empty;                    // shared::cluster address
+  volatile int* abort;
+  int place;                         // the warp's place in the pair
+  uint32_t slot;                     // shared-memory address
+  uint64_t* bars;                    // of the slot's halves: its copies have come
+};
+
+__device__ __forceinline__ uint4 lds_v4(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ void sts_v4(uint32_t at, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+// 16 bytes (8 columns) of this lane's row of a piece, in the copies' 128-byte swizzle.
+__device__ __forceinline__ uint32_t chunk_at(uint32_t piece, int chunk) {
+  const uint32_t lane = threadIdx.x % 32;
+  return piece + lane * 128 + ((chunk ^ (lane & 7)) << 4);
+}
+
+// Waits (a whole warp) for the copies into half h of the slot.
+__device__ __forceinline__ bool wait_piece(const Acc& in, int h, uint32_t& parity) {
+  if (!__all_sync(kAll, wait_bar(&in.bars[h], (parity >> h) & 1u, in.abort))) return false;
+  parity ^= 1u << h;
+  return true;
+}
+
+// The last update's piece, to the caller's matrix: lane = row jx of X^T, columns i0 .. + 7.
+__device__ __forceinline__ void store_out(const OrthoArgs& a, int z, int jx, int i0, const float (&v)[8]) {
+  const int n = min(a.r - i0, 8);
+  if (jx >= a.c || n <= 0) return;
+  __nv_bfloat16* out = a.out + z * a.out_batch;
+  const float unscale = 1.0f / a.s;
+  if (!a.tall) {                     // out is [r, c]: neighbouring lanes, neighbouring elements
+    __nv_bfloat16* p = out + i0 * a.out_row + jx;
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (q < n) p[q * a.out_row] = __float2bfloat16_rn(v[q] * unscale);
+    return;
+  }
+  __nv_bfloat16* p = out + jx * a.out_row + i0;
+  if (n == 8 && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+    uint32_t w[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) w[q] = pack_bf16(v[2 * q] * unscale, v[2 * q + 1] * unscale);
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (q < n) p[q] = __float2bfloat16_rn(v[q] * unscale);
+  }
+}
+
+// One warp's part of a finished block of an update: 32 rows of X^T from j0, kWarpCols columns from
+// i.  X's two parts of the first piece are on their way before the products are done.
+__device__ __forceinline__ bool epilogue_update(const OrthoMaps& maps, const OrthoArgs& a, int step, const Unit& x,
+                                                int j0, int i, const Acc& in, uint32_t& parity) {
+  const int lane = threadIdx.x % 32, jx = j0 + lane, cur = step & 1;
+  const int pieces = j0 < a.c ? min(max((a.r - i + kPiece - 1) / kPiece, 0), kPieces) : 0;
   const bool last = step == a.steps - 1;
-  const int ld = a.ld;
-  const int i = i0 + lane % 4 * 8;                    // this lane's rows i .. i + 7 (inside ld) ...
-  // ... and columns: piece u, h: jl + kPiece u + 8 h
-  const int jl = j + lane / 4, cols = i < a.r ? a.c - jl : 0;
-  const long long base = (static_cast<long long>(x.z) * a.c + jl) * ld + i;
-  const __half* hi_in = a.xt[step & 1] + base;
-  __half* hi_out = a.xt[(step & 1) ^ 1] + base;
-  __half* lo = a.xl + base;
-  uint4 hi[2] = {}, rest[2] = {};
-  auto load = [&](int u) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      if (u * kPiece + 8 * h < cols) {
-        hi[h] = load_v4(hi_in + (u * kPiece + 8 * h) * static_cast<long long>(ld));
-        rest[h] = load_v4(lo + (u * kPiece + 8 * h) * static_cast<long long>(ld));
-      }
+  const float* rest = a.diag_b + x.z * static_cast<long long>(a.ld) + i;
+  auto request = [&](int u) {        // one lane
+    ptx::mbar_arrive_expect_tx(&in.bars[0], kSlotBytes);
+    ptx::tma_load_3d(in.slot, &maps.xt_piece[cur], i + u * kPiece, j0, x.z, &in.bars[0]);
+    ptx::tma_load_3d(in.slot + kPieceBytes, &maps.xl_piece, i + u * kPiece, j0, x.z, &in.bars[0]);
   };
-  if (!warp_ready(a, kUpdate, step, x, w.abort)) return false;
-  load(0);
-  float own[8];                                       // a + what is left of B_ii
-#pragma unroll
-  for (int q = 0; q < 8; ++q) own[q] = i + q < a.r ? a.ca + a.diag_b[x.z * static_cast<long long>(ld) + i + q] : 0.0f;
-  if (!__all_sync(kAll, wait_bar(acc_full, parity, w.abort))) return false;
+  if (!warp_ready(a, kUpdate, step, x, in.abort)) return false;
+  if (lane == 0 && pieces > 0) {
+    ptx::fence_proxy_async();        // the acquire before the copies
+    request(0);
+  }
+  if (!__all_sync(kAll, wait_bar(in.full, in.parity, in.abort))) return false;
   ptx::tmem_fence_after();
-  uint32_t acc[kPiece];
-  if (pieces > 0) ptx::tmem_load16(acc, from);
-  else release_acc(acc_empty);
+  if (pieces == 0) release_acc(in.empty);
 #pragma unroll 1
   for (int u = 0; u < pieces; ++u) {
-    ptx::tmem_wait_load();
-    float v[kPiece], t[2][8];
+    if (!wait_piece(in, 0, parity)) return false;
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {    // 32 columns at a time
+      uint32_t acc[32];
+      ptx::tmem_load32(acc, in.from + u * kPiece + 32 * h);
+      uint4 top[4], low[4];
 #pragma unroll
-    for (int q = 0; q < kPiece; ++q) v[q] = __uint_as_float(acc[q]);
-    turn(w.buf, lane, v, t);
-    if (u + 1 < pieces) ptx::tmem_load16(acc, from + (u + 1) * kPiece);
-    else release_acc(acc_empty);
+      for (int k = 0; k < 4; ++k) {
+        top[k] = lds_v4(chunk_at(in.slot, 4 * h + k));
+        low[k] = lds_v4(chunk_at(in.slot + kPieceBytes, 4 * h + k));
+      }
+      ptx::tmem_wait_load();
+      if (u + 1 == pieces && h == 1) release_acc(in.empty);
+      const int ih = u * kPiece + 32 * h;             // from i on
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t hw[4] = {hi[h].x, hi[h].y, hi[h].z, hi[h].w};
-      const uint32_t lw[4] = {rest[h].x, rest[h].y, rest[h].z, rest[h].w};
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t tw[4] = {top[k].x, top[k].y, top[k].z, top[k].w};
+        const uint32_t lw[4] = {low[k].x, low[k].y, low[k].z, low[k].w};
+        float own[8] = {};           // what is left of B_ii
+        if (i + ih + 8 * k < a.r) {  // (then the eight lie inside ld)
+          const float4 d0 = *reinterpret_cast<const float4*>(rest + ih + 8 * k);
+          const float4 d1 = *reinterpret_cast<const float4*>(rest + ih + 8 * k + 4);
+          own[0] = d0.x, own[1] = d0.y, own[2] = d0.z, own[3] = d0.w;
+          own[4] = d1.x, own[5] = d1.y, own[6] = d1.z, own[7] = d1.w;
+        }
+        float v[8];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float2 b = unpack_half(hw[q]), r = unpack_half(lw[q]);
-        t[h][2 * q] = fmaf(own[2 * q], b.x + r.x, t[h][2 * q]);
-        t[h][2 * q + 1] = fmaf(own[2 * q + 1], b.y + r.y, t[h][2 * q + 1]);
+        for (int q = 0; q < 4; ++q) {
+          const float2 b = unpack_half(tw[q]), r = unpack_half(lw[q]);
+          v[2 * q] = fmaf(a.ca + own[2 * q], b.x + r.x, __uint_as_float(acc[8 * k + 2 * q]));
+          v[2 * q + 1] = fmaf(a.ca + own[2 * q + 1], b.y + r.y, __uint_as_float(acc[8 * k + 2 * q + 1]));
+        }
+        if (last) {
+          store_out(a, x.z, jx, i + ih + 8 * k, v);
+          continue;
+        }
+        uint32_t hw[4], rw[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          hw[q] = pack_half(v[2 * q], v[2 * q + 1]);
+          const float2 b = unpack_half(hw[q]);
+          rw[q] = pack_half(v[2 * q] - b.x, v[2 * q + 1] - b.y);
+        }
+        sts_v4(chunk_at(in.slot, 4 * h + k), make_uint4(hw[0], hw[1], hw[2], hw[3]));
+        sts_v4(chunk_at(in.slot + kPieceBytes, 4 * h + k), make_uint4(rw[0], rw[1], rw[2], rw[3]));
       }
     }
-    if (u + 1 < pieces) load(u + 1);
-    if (last) {
-      turn_back(w.buf, lane, t, v);
-      store_out(a, x.z, i0 + lane, j + u * kPiece, v);
-      continue;
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t hw[4], lw[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        hw[q] = pack_half(t[h][2 * q], t[h][2 * q + 1]);
-        const float2 b = unpack_half(hw[q]);
-        lw[q] = pack_half(t[h][2 * q] - b.x, t[h][2 * q + 1] - b.y);
+    ptx::fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+      if (!last) {
+        ptx::tma_store_3d(&maps.xt_piece[cur ^ 1], i + u * kPiece, j0, x.z, in.slot);
+        ptx::tma_store_3d(&maps.xl_piece, i + u * kPiece, j0, x.z, in.slot + kPieceBytes);
+        ptx::bulk_commit();
+        ptx::bulk_wait_read();
       }
-      if (u * kPiece + 8 * h < cols) {
-        const long long at = (u * kPiece + 8 * h) * static_cast<long long>(ld);
-        *reinterpret_cast<uint4*>(hi_out + at) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-        *reinterpret_cast<uint4*>(lo + at) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
-      }
+      if (u + 1 < pieces) request(u + 1);
     }
   }
   if (!last) signal_ready(a, kUpdate, x);
@@ -623,31 +605,32 @@ __device__ __forceinline__ bool epilogue_update(const OrthoArgs& a, int step, co
 }
 
 // The same for A = X X^T or B = b A + c A^2: 32 rows from i0, kWarpCols columns from j of a block on
-// or below the diagonal, and its mirror.
+// or below the diagonal.
 //
-// Where the inner dimension is split, each part's warp stores its sums, and the one that comes
-// last adds the parts up in their order (so the result does not depend on which that is).
+// Where the inner dimension is split, each part's warp stores its sums, waits for the other
+// parts' and finishes its share of the columns from all parts' sums, added in their order.  (The
+// units of such a phase are no more than the pairs, so the parts run at the same time.)
 template <int kPhase>
-__device__ __forceinline__ bool epilogue_square(const OrthoArgs& a, int step, const Unit& x, int i0, int j,
-                                                uint32_t from, uint64_t* acc_full, uint32_t parity,
-                                                uint32_t acc_empty, const EpilogueWarp& w) {
-  const int lane = threadIdx.x % 32;
+__device__ __forceinline__ bool epilogue_square(const OrthoMaps& maps, const OrthoArgs& a, int step, const Unit& x,
+                                                int i0, int j, const Acc& in, uint32_t& parity) {
+  const int lane = threadIdx.x % 32, cur = step & 1;
   const int i = i0 + lane;
   const int pieces = i0 < a.r ? min(max((a.r - j + kPiece - 1) / kPiece, 0), kPieces) : 0;
-  const int ld = a.ld;
-  const long long matrix = static_cast<long long>(x.z) * a.r * ld;
   const bool row = i < a.r;
-  const __half* o_row = a.a[step & 1] + matrix + static_cast<long long>(i) * ld + j;    // A_ij = A_ji, along the row
-  Half16 o = {};
+  const long long diag_at = x.z * static_cast<long long>(a.ld) + i;
   float rest_a = 0.0f;               // what rounding left of A_ii
   if (kPhase == kPoly) {
-    if (!warp_ready(a, kPoly, step, x, w.abort)) return false;
-    if (row && pieces > 0) {
-      o = load_half16(o_row);
-      rest_a = a.diag_a[step & 1][x.z * static_cast<long long>(ld) + i];
+    if (!warp_ready(a, kPoly, step, x, in.abort)) return false;
+    if (lane == 0) {
+      ptx::fence_proxy_async();      // the acquire before the copies
+      for (int u = 0; u < pieces; ++u) {
+        ptx::mbar_arrive_expect_tx(&in.bars[u], kPieceBytes);
+        ptx::tma_load_3d(in.slot + u * kPieceBytes, &maps.a_piece[cur], j + u * kPiece, i0, x.z, &in.bars[u]);
+      }
     }
+    if (row) rest_a = a.diag_a[cur][diag_at];
   }
-  if (!__all_sync(kAll, wait_bar(acc_full, parity, w.abort))) return false;
+  if (!__all_sync(kAll, wait_bar(in.full, in.parity, in.abort))) return false;
   ptx::tmem_fence_after();
   const int parts = a.split[kPhase];
   const float* sums = nullptr;       // the first part's
@@ -655,100 +638,118 @@ __device__ __forceinline__ bool epilogue_square(const OrthoArgs& a, int step, co
   if (parts > 1) {
     const int nr = blocks_of(a.r), blocks = nr * (nr + 1) / 2;
     const long long block = static_cast<long long>(x.z) * blocks + x.I * (x.I + 1) / 2 + x.J;
-    const int place = w.rank * kEpilogueWarps + w.index;
-    float* first = a.partial + block * parts * kPartStride + place * (32 * kWarpCols) + lane;
+    float* first = a.partial + block * parts * kPartStride + in.place * (32 * kWarpCols) + lane;
     float* mine = first + static_cast<long long>(x.part) * kPartStride;
 #pragma unroll 1
-    for (int u = 0; u < pieces; ++u) {
-      uint32_t acc[kPiece];
-      ptx::tmem_load16(acc, from + u * kPiece);
+    for (int u = 0; u < 2 * pieces; ++u) {
+      uint32_t acc[32];
+      ptx::tmem_load32(acc, in.from + u * 32);
       ptx::tmem_wait_load();
 #pragma unroll
-      for (int q = 0; q < kPiece; ++q) mine[(u * kPiece + q) * 32] = __uint_as_float(acc[q]);
+      for (int q = 0; q < 32; ++q) mine[(u * 32 + q) * 32] = __uint_as_float(acc[q]);
     }
-    release_acc(acc_empty);
-    int before = 0;
-    if (lane == 0)
-      before = ptx::add_acq_rel(a.arrived + ((static_cast<long long>(x.z) * 2 + kPhase) * blocks +
-                                             (block - static_cast<long long>(x.z) * blocks)) * kWarpsOfBlock + place, 1);
-    before = __shfl_sync(kAll, before, 0);
-    if (before % parts != parts - 1) return true;      // not the last part
+    release_acc(in.empty);
+    __syncwarp();
+    bool ok = true;
+    if (lane == 0) {
+      int* arrived = a.arrived + ((static_cast<long long>(x.z) * 2 + kPhase) * blocks + x.I * (x.I + 1) / 2 + x.J) *
+                                     kWarpsOfBlock + in.place;
+      ptx::red_release_add(arrived, 1);
+      ok = wait_ready(a, arrived, (step + 1) * parts, in.abort);
+    }
+    if (!__all_sync(kAll, ok)) return false;
     sums = first;
+  } else if (pieces == 0) {
+    release_acc(in.empty);
   }
   const float f = kPhase == kGram ? 1.0f / (a.s * a.s) : a.cc;
-  __half* m = (kPhase == kGram ? a.a[step & 1] : a.b) + matrix;
-  __half* m_row = m + static_cast<long long>(i) * ld + j;
-  const int ti = i0 + lane % 4 * 8;                   // after the turn: rows ti .. ti + 7 of ...
-  const int cols = ti < a.r ? a.r - j - lane / 4 : 0; // ... columns j + lane / 4 + kPiece u + 8 h
-  __half* m_col = m + static_cast<long long>(j + lane / 4) * ld + ti;
-  uint32_t acc[kPiece];
-  if (parts == 1) {
-    if (pieces > 0) ptx::tmem_load16(acc, from);
-    else release_acc(acc_empty);
-  }
 #pragma unroll 1
   for (int u = 0; u < pieces; ++u) {
-    const int j0 = j + u * kPiece;
-    float v[kPiece];
-    if (parts == 1) {
-      ptx::tmem_wait_load();
-#pragma unroll
-      for (int q = 0; q < kPiece; ++q) v[q] = __uint_as_float(acc[q]) * f;
-      if (u + 1 < pieces) ptx::tmem_load16(acc, from + (u + 1) * kPiece);
-      else release_acc(acc_empty);
-    } else {
-      const float* p = sums + u * kPiece * 32;
-#pragma unroll
-      for (int q = 0; q < kPiece; ++q) v[q] = p[q * 32];
+    const uint32_t slot = in.slot + u * kPieceBytes;
+    if (kPhase == kPoly && !wait_piece(in, u, parity)) return false;
+    if (parts > 1 && u % parts != x.part) continue;   // another part's share
 #pragma unroll 1
-      for (int k = 1; k < parts; ++k) {
-        p += kPartStride;
+    for (int h = 0; h < 2; ++h) {    // 32 columns at a time
+      const int jh = j + u * kPiece + 32 * h;
+      float v[32];
+      if (parts == 1) {
+        uint32_t acc[32];
+        ptx::tmem_load32(acc, in.from + u * kPiece + 32 * h);
+        ptx::tmem_wait_load();
+        if (u + 1 == pieces && h == 1) release_acc(in.empty);
 #pragma unroll
-        for (int q = 0; q < kPiece; ++q) v[q] += p[q * 32];
-      }
+        for (int q = 0; q < 32; ++q) v[q] = __uint_as_float(acc[q]) * f;
+      } else {
+        const float* p = sums + (u * kPiece + 32 * h) * 32;
 #pragma unroll
-      for (int q = 0; q < kPiece; ++q) v[q] *= f;
-    }
-    if constexpr (kPhase == kPoly) {
+        for (int q = 0; q < 32; ++q) v[q] = p[q * 32];
+#pragma unroll 1
+        for (int k = 1; k < parts; ++k) {
 #pragma unroll
-      for (int q = 0; q < kPiece / 2; ++q) {
-        const float2 p = unpack_half(o.w[q]);
-        v[2 * q] = fmaf(a.cb, p.x, v[2 * q]);
-        v[2 * q + 1] = fmaf(a.cb, p.y, v[2 * q + 1]);
-      }
-    }
-    if (j0 < i0 + 32 && i0 < j0 + kPiece) {           // the diagonal passes through the piece
-      float left = 0.0f;
-#pragma unroll
-      for (int q = 0; q < kPiece; ++q) {
-        if (j0 + q != i) continue;
-        if constexpr (kPhase == kPoly) {              // rest_a to first order
-          const float2 p = unpack_half(o.w[q / 2]);
-          v[q] = fmaf(rest_a, fmaf(2.0f * a.cc, q % 2 ? p.y : p.x, a.cb), v[q]);
+          for (int q = 0; q < 32; ++q) v[q] += p[k * kPartStride + q * 32];
         }
-        left = v[q] - __half2float(__float2half_rn(v[q]));
-      }
-      if (i >= j0 && i < j0 + kPiece && row)
-        (kPhase == kGram ? a.diag_a[step & 1] : a.diag_b)[x.z * static_cast<long long>(ld) + i] = left;
-    }
-    if (kPhase == kPoly && row && u + 1 < pieces) o = load_half16(o_row + (u + 1) * kPiece);
-    if (x.I != x.J && row) store_half16(m_row + u * kPiece, v);
-    float t[2][8];
-    turn(w.buf, lane, v, t);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (u * kPiece + 8 * h < cols)
-        *reinterpret_cast<uint4*>(m_col + (u * kPiece + 8 * h) * static_cast<long long>(ld)) =
-            make_uint4(pack_half(t[h][0], t[h][1]), pack_half(t[h][2], t[h][3]), pack_half(t[h][4], t[h][5]),
-                       pack_half(t[h][6], t[h][7]));
+        for (int q = 0; q < 32; ++q) v[q] *= f;
+      }
+      float own_o = 0.0f;            // A_ii as stored, where the diagonal passes through
+      if constexpr (kPhase == kPoly) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint4 o = lds_v4(chunk_at(slot, 4 * h + k));
+          const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float2 p = unpack_half(w[q]);
+            const int e = 8 * k + 2 * q;
+            if (jh + e == i) own_o = p.x;
+            if (jh + e + 1 == i) own_o = p.y;
+            v[e] = fmaf(a.cb, p.x, v[e]);
+            v[e + 1] = fmaf(a.cb, p.y, v[e + 1]);
+          }
+        }
+      }
+      if (jh < i0 + 32 && i0 < jh + 32) {             // the diagonal passes through
+        const float more = kPhase == kPoly ? rest_a * fmaf(2.0f * a.cc, own_o, a.cb) : 0.0f;   // to first order
+        float left = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 32; ++q) {
+          if (jh + q != i) continue;
+          v[q] += more;
+          left = v[q] - __half2float(__float2half_rn(v[q]));
+        }
+        if (i >= jh && i < jh + 32 && row) (kPhase == kGram ? a.diag_a[cur] : a.diag_b)[diag_at] = left;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        sts_v4(chunk_at(slot, 4 * h + k),
+               make_uint4(pack_half(v[8 * k], v[8 * k + 1]), pack_half(v[8 * k + 2], v[8 * k + 3]),
+                          pack_half(v[8 * k + 4], v[8 * k + 5]), pack_half(v[8 * k + 6], v[8 * k + 7])));
+    }
+    ptx::fence_proxy_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+      ptx::tma_store_3d(kPhase == kGram ? &maps.a_piece[cur] : &maps.b_piece, j + u * kPiece, i0, x.z, slot);
+      ptx::bulk_commit();
     }
   }
   signal_ready(a, kPhase, x);
   return true;
 }
 
-// All phases of all steps, one cooperative launch of CTA pairs.  The units of all phases in
-// order go round the pairs; a unit waits for the block rows that it reads, which units before
+// How the operands of inner block kb of a unit lie: MN-major where a block above the diagonal is
+// read from its mirror, and for X in X X^T.
+struct Majors {
+  bool a, b;
+};
+__device__ __forceinline__ Majors majors_of(int phase, const Unit& x, int kb) {
+  const int k = kb / (kBlock / kStepK);
+  if (phase == kGram) return {true, true};
+  if (phase == kPoly) return {k > x.I, k > x.J};
+  return {false, k > x.I};
+}
+
+// All phases of all steps, one cooperative launch of CTA pairs.  A chunk of the batch at a time
+// (see ortho_chunk), the units of all phases in order go round the pairs; a unit waits for the block rows that it reads, which units before
 // it in the order store, so the earliest unfinished unit never waits and the phases (and
 // the matrices of a batch) overlap without a barrier over the grid.  Per CTA: warp 0 copies
 // operands (TMA), warp 1 of the pair's first CTA issues the products, the epilogue warps take
@@ -773,6 +774,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       ptx::mbar_init(&sm.acc_empty[i], 2 * kEpilogueWarps);
     }
     ptx::mbar_init(&sm.drained, 1);
+    for (int i = 0; i < 2 * kEpilogueWarps; ++i) ptx::mbar_init(&sm.piece[0][0] + i, 1);
     sm.abort = 0;
     ptx::fence_mbar_init();
     ptx::prefetch_tensor_map(&maps.xt[0]);
@@ -805,18 +807,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   };
   // body(phase, step, unit) for this pair's units in order, until one gives up
   auto for_units = [&](auto&& body) {
-    int offset = 0;                  // units of the phases so far, modulo the pairs
-    for (int p = 0; p < 3 * a.steps; ++p) {
-      const int phase = p % 3, step = p / 3;
-      const int units = units_of(a, phase);
-      for (int t = pair >= offset ? pair - offset : pair - offset + pairs; t < units; t += pairs) {
-        if (*abort) return;
-        if (!body(phase, step, unit_at(a, phase, t))) {
-          gave_up(a, abort);
-          return;
+    int offset = 0;                  // units so far, modulo the pairs
+    for (int z0 = 0; z0 < a.batch; z0 += a.chunk) {
+      const int matrices = min(a.chunk, a.batch - z0);
+      for (int p = 0; p < 3 * a.steps; ++p) {
+        const int phase = p % 3, step = p / 3;
+        const int units = units_of(a, phase, matrices);
+        for (int t = pair >= offset ? pair - offset : pair - offset + pairs; t < units; t += pairs) {
+          if (*abort) return;
+          if (!body(phase, step, unit_at(a, phase, z0, t))) {
+            gave_up(a, abort);
+            return;
+          }
         }
+        offset = (offset + units) % pairs;
       }
-      offset = (offset + units) % pairs;
     }
   };
 
@@ -824,9 +829,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     if (lane == 0) {
       for_units([&](int phase, int step, const Unit& x) {
         const int cur = step & 1;
-        const CUtensorMap* ma = phase == kGram ? &maps.xt[cur] : phase == kPoly ? &maps.a[cur] : &maps.b;
-        const CUtensorMap* mb = phase == kPoly ? &maps.a[cur] : &maps.xt[cur];
-        const int ra = x.I * kBlock + rank * 128, rb = x.J * kBlock + rank * 128;
+        // X X^T: X, X.  A A: A, A.  Update: X^T (rows J), B (rows I).
+        const CUtensorMap* ma = phase == kPoly ? &maps.a[cur] : &maps.xt[cur];
+        const CUtensorMap* mb = phase == kGram ? &maps.xt[cur] : phase == kPoly ? &maps.a[cur] : &maps.b;
+        const int ra = (phase == kUpdate ? x.J : x.I) * kBlock + rank * 128;
+        const int rb = (phase == kUpdate ? x.I : x.J) * kBlock + rank * 128;
         int k0, k1;
         inner_of(a, phase, x, k0, k1);
         if (!wait_inputs(a, phase, step, x, abort)) return false;
@@ -837,12 +844,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           const uint32_t bar = ptx::map_to_rank(ptx::smem_u32(&sm.full[stage]), 0);
           const uint32_t dst = stages + stage * kStageBytes;
           const int k = kb * kStepK;
+          const Majors mn = majors_of(phase, x, kb);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int da = ra + 64 * h, db = rb + 64 * h;
-            ptx::tma_load_3d_pair(dst + h * kBoxBytes, ma, phase == kGram ? da : k, phase == kGram ? k : da, x.z, bar);
-            ptx::tma_load_3d_pair(dst + kOperandBytes + h * kBoxBytes, mb, phase == kGram ? db : k,
-                                  phase == kGram ? k : db, x.z, bar);
+            ptx::tma_load_3d_pair(dst + h * kBoxBytes, ma, mn.a ? da : k, mn.a ? k : da, x.z, bar);
+            ptx::tma_load_3d_pair(dst + kOperandBytes + h * kBoxBytes, mb, mn.b ? db : k, mn.b ? k : db, x.z, bar);
           }
           next_stage();
         }
@@ -853,12 +860,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   } else if (warp == 1 && rank == 0) {
     if (lane == 0) {
       for_units([&](int phase, int, const Unit& x) {
-        // fp32 accumulator, fp16 operands, 256 x 256; X X^T has both operands MN-major
-        const uint32_t idesc = 1u << 4 | (kBlock >> 3) << 17 | (kBlock >> 4) << 24 | (phase == kGram ? 3u << 15 : 0u);
-        // K-major: 8-row groups 1024 bytes apart, 16 inner elements = 32 bytes.  MN-major:
-        // groups of 64 rows a box apart, groups of 8 inner elements 1024 bytes apart.
-        const uint32_t lead = phase == kGram ? kBoxBytes : 16;
-        const uint32_t k_bytes = phase == kGram ? 2048 : 32;
         int k0, k1;
         inner_of(a, phase, x, k0, k1);
         if (!wait_bar(&sm.acc_empty[acc], acc_phase ^ 1u, abort)) return false;
@@ -868,10 +869,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           if (!wait_bar(&sm.full[stage], stage_phase, abort)) return false;
           ptx::tmem_fence_after();
           const uint32_t at = stages + stage * kStageBytes;
+          const Majors mn = majors_of(phase, x, kb);
+          // fp32 accumulator, fp16 operands, 256 x 256
+          const uint32_t idesc = 1u << 4 | (mn.a ? 1u << 15 : 0u) | (mn.b ? 1u << 16 : 0u) | (kBlock >> 3) << 17 |
+                                 (kBlock >> 4) << 24;
+          // K-major: 8-row groups 1024 bytes apart, 16 inner elements = 32 bytes.  MN-major:
+          // groups of 64 rows a box apart, groups of 8 inner elements 1024 bytes apart.
+          const uint32_t lead_a = mn.a ? kBoxBytes : 16, lead_b = mn.b ? kBoxBytes : 16;
+          const uint32_t k_a = mn.a ? 2048 : 32, k_b = mn.b ? 2048 : 32;
 #pragma unroll
           for (int k = 0; k < kStepK / 16; ++k)
-            ptx::mma_f16_pair(d, operand_desc(at + k * k_bytes, lead, 1024),
-                              operand_desc(at + kOperandBytes + k * k_bytes, lead, 1024), idesc, kb > k0 || k > 0);
+            ptx::mma_f16_pair(d, operand_desc(at + k * k_a, lead_a, 1024),
+                              operand_desc(at + kOperandBytes + k * k_b, lead_b, 1024), idesc, kb > k0 || k > 0);
           ptx::mma_commit_pair(&sm.empty[stage]);
           next_stage();
         }
@@ -882,22 +891,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     }
     __syncwarp();
   } else if (warp >= kFirstEpilogueWarp) {
-    const int quarter = warp % 4, part = (warp - kFirstEpilogueWarp) / 4;
-    const EpilogueWarp ew{reinterpret_cast<float*>(raw + (stages - ptx::smem_u32(raw)) + kStages * kStageBytes) +
-                              (warp - kFirstEpilogueWarp) * kTurnFloats,
-                          abort, static_cast<int>(rank), warp - kFirstEpilogueWarp};
+    const int index = warp - kFirstEpilogueWarp;
+    const int quarter = warp % 4, part = index / 4;
+    const uint32_t slot = stages + kStages * kStageBytes + index * kSlotBytes;
+    uint32_t parity = 0;             // of the slot's barriers
     for_units([&](int phase, int step, const Unit& x) {
-      const uint32_t from = tmem + acc * kBlock + part * kWarpCols + (static_cast<uint32_t>(quarter) << 21);
-      const int i0 = x.I * kBlock + rank * 128 + quarter * 32;
-      const int j = x.J * kBlock + part * kWarpCols;
-      uint64_t* full = &sm.acc_full[acc];
-      const uint32_t empty = ptx::map_to_rank(ptx::smem_u32(&sm.acc_empty[acc]), 0);
-      const bool ok = phase == kGram ? epilogue_square<kGram>(a, step, x, i0, j, from, full, acc_phase, empty, ew)
-                      : phase == kPoly ? epilogue_square<kPoly>(a, step, x, i0, j, from, full, acc_phase, empty, ew)
-                                       : epilogue_update(a, step, x, i0, j, from, full, acc_phase, empty, ew);
+      const Acc in{tmem + acc * kBlock + part * kWarpCols + (static_cast<uint32_t>(quarter) << 21),
+                   &sm.acc_full[acc], acc_phase, ptx::map_to_rank(ptx::smem_u32(&sm.acc_empty[acc]), 0), abort,
+                   static_cast<int>(rank) * kEpilogueWarps + index, slot, sm.piece[index]};
+      const int row = (phase == kUpdate ? x.J : x.I) * kBlock + rank * 128 + quarter * 32;
+      const int col = (phase == kUpdate ? x.I : x.J) * kBlock + part * kWarpCols;
       next_acc();
-      return ok;
+      return phase == kGram ? epilogue_square<kGram>(maps, a, step, x, row, col, in, parity)
+             : phase == kPoly ? epilogue_square<kPoly>(maps, a, step, x, row, col, in, parity)
+                              : epilogue_update(maps, a, step, x, row, col, in, parity);
     });
+    if (lane == 0) ptx::bulk_wait();
   }
 
   // ---- end: nothing of the pair may be in flight when it leaves
@@ -925,12 +934,12 @@ using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
 EncodeTiled g_encode = nullptr;
 int g_pairs[64] = {};                // per device: pairs resident at once
 
-// [batch][outer][ld] fp16 with r columns used, in swizzled boxes of 64 x 64.
-cudaError_t encode(CUtensorMap* map, void* p, const OrthoShape& sh, int64_t outer) {
+// [batch][outer][ld] fp16 with r columns used, in swizzled boxes of 64 x box_rows.
+cudaError_t encode(CUtensorMap* map, void* p, const OrthoShape& sh, int64_t outer, int box_rows) {
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(sh.r), static_cast<cuuint64_t>(outer),
                               static_cast<cuuint64_t>(sh.batch)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(sh.ld * 2), static_cast<cuuint64_t>(sh.ld * outer * 2)};
-  const cuuint32_t box[3] = {64, 64, 1}, step[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1}, step[3] = {1, 1, 1};
   const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, p, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
@@ -996,14 +1005,18 @@ cudaError_t launch_orthogonalize(const OrthoCall& q, cudaStream_t stream) {
 
   OrthoMaps maps;
   cudaError_t e = cudaSuccess;
-  auto add = [&](CUtensorMap* map, size_t at, int64_t outer) {
-    if (e == cudaSuccess) e = encode(map, ws + at, sh, outer);
+  auto add = [&](CUtensorMap* map, size_t at, int64_t outer, int box_rows) {
+    if (e == cudaSuccess) e = encode(map, ws + at, sh, outer, box_rows);
   };
-  add(&maps.xt[0], L.xt[0], sh.c);
-  add(&maps.xt[1], L.xt[1], sh.c);
-  add(&maps.a[0], L.a[0], sh.r);
-  add(&maps.a[1], L.a[1], sh.r);
-  add(&maps.b, L.b, sh.r);
+  for (int i = 0; i < 2; ++i) {
+    add(&maps.xt[i], L.xt[i], sh.c, 64);
+    add(&maps.xt_piece[i], L.xt[i], sh.c, 32);
+    add(&maps.a[i], L.a[i], sh.r, 64);
+    add(&maps.a_piece[i], L.a[i], sh.r, 32);
+  }
+  add(&maps.xl_piece, L.xl, sh.c, 32);
+  add(&maps.b, L.b, sh.r, 64);
+  add(&maps.b_piece, L.b, sh.r, 32);
   if (e != cudaSuccess) return e;
 
   OrthoArgs a{};
@@ -1016,12 +1029,7 @@ cudaError_t launch_orthogonalize(const OrthoCall& q, cudaStream_t stream) {
   a.cb = q.b;
   a.cc = q.c;
   a.s = in.s;
-  a.xt[0] = in.xt;
-  a.xt[1] = reinterpret_cast<__half*>(ws + L.xt[1]);
-  a.xl = in.xl;
-  a.b = reinterpret_cast<__half*>(ws + L.b);
   for (int i = 0; i < 2; ++i) {
-    a.a[i] = reinterpret_cast<__half*>(ws + L.a[i]);
     a.diag_a[i] = reinterpret_cast<float*>(ws + L.diag_a[i]);
   }
   a.diag_b = reinterpret_cast<float*>(ws + L.diag_b);
@@ -1033,6 +1041,7 @@ cudaError_t launch_orthogonalize(const OrthoCall& q, cudaStream_t stream) {
   a.ready = in.counters;
   a.arrived = in.counters + sh.batch * 3 * nr;
   a.partial = reinterpret_cast<float*>(ws + L.partial);
+  a.chunk = ortho_chunk(sh);
   a.split[kGram] = sh.split_gram;
   a.split[kPoly] = sh.split_poly;
 
