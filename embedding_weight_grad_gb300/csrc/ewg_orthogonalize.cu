@@ -277,6 +277,7 @@ constexpr int kSlotBytes = 2 * kPieceBytes;
 constexpr int kGemmThreads = 32 * (kFirstEpilogueWarp + kEpilogueWarps);
 constexpr size_t kGemmSmem =
     static_cast<size_t>(kStages) * kStageBytes + kEpilogueWarps * kSlotBytes + 1024;
+static_assert(kWarpCols == 128 && kPieces == 2, "a warp's columns, as the epilogue takes them");
 static_assert(kWarpsOfBlock == kOrthoWarps && kBlock == kOrthoBlock, "as the workspace is laid out for");
 static_assert(kGemmSmem + 512 <= 227 * 1024, "stages and slots fit in shared memory");
 constexpr uint32_t kWaitLimit = 1u << 22;
@@ -525,7 +526,6 @@ __device__ __forceinline__ bool epilogue_update(const OrthoMaps& maps, const Ort
   const int lane = threadIdx.x % 32, jx = j0 + lane, cur = step & 1;
   const int pieces = j0 < a.c ? min(max((a.r - i + kPiece - 1) / kPiece, 0), kPieces) : 0;
   const bool last = step == a.steps - 1;
-  const float* rest = a.diag_b + x.z * static_cast<long long>(a.ld) + i;
   auto request = [&](int u) {        // one lane
     ptx::mbar_arrive_expect_tx(&in.bars[0], kSlotBytes);
     ptx::tma_load_3d(in.slot, &maps.xt_piece[cur], i + u * kPiece, j0, x.z, &in.bars[0]);
@@ -535,6 +535,13 @@ __device__ __forceinline__ bool epilogue_update(const OrthoMaps& maps, const Ort
   if (lane == 0 && pieces > 0) {
     ptx::fence_proxy_async();        // the acquire before the copies
     request(0);
+  }
+  // a + what is left of B_ii, of column i + 32 q + lane
+  float own[kWarpCols / 32];
+#pragma unroll
+  for (int q = 0; q < kWarpCols / 32; ++q) {
+    const int col = i + 32 * q + lane;
+    own[q] = a.ca + (col < a.r ? a.diag_b[x.z * static_cast<long long>(a.ld) + col] : 0.0f);
   }
   if (!__all_sync(kAll, wait_bar(in.full, in.parity, in.abort))) return false;
   ptx::tmem_fence_after();
@@ -555,23 +562,18 @@ __device__ __forceinline__ bool epilogue_update(const OrthoMaps& maps, const Ort
       ptx::tmem_wait_load();
       if (u + 1 == pieces && h == 1) release_acc(in.empty);
       const int ih = u * kPiece + 32 * h;             // from i on
+      const float own_h = u == 0 ? (h == 0 ? own[0] : own[1]) : (h == 0 ? own[2] : own[3]);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const uint32_t tw[4] = {top[k].x, top[k].y, top[k].z, top[k].w};
         const uint32_t lw[4] = {low[k].x, low[k].y, low[k].z, low[k].w};
-        float own[8] = {};           // what is left of B_ii
-        if (i + ih + 8 * k < a.r) {  // (then the eight lie inside ld)
-          const float4 d0 = *reinterpret_cast<const float4*>(rest + ih + 8 * k);
-          const float4 d1 = *reinterpret_cast<const float4*>(rest + ih + 8 * k + 4);
-          own[0] = d0.x, own[1] = d0.y, own[2] = d0.z, own[3] = d0.w;
-          own[4] = d1.x, own[5] = d1.y, own[6] = d1.z, own[7] = d1.w;
-        }
         float v[8];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const float2 b = unpack_half(tw[q]), r = unpack_half(lw[q]);
-          v[2 * q] = fmaf(a.ca + own[2 * q], b.x + r.x, __uint_as_float(acc[8 * k + 2 * q]));
-          v[2 * q + 1] = fmaf(a.ca + own[2 * q + 1], b.y + r.y, __uint_as_float(acc[8 * k + 2 * q + 1]));
+          const int e = 8 * k + 2 * q;
+          v[2 * q] = fmaf(__shfl_sync(kAll, own_h, e), b.x + r.x, __uint_as_float(acc[e]));
+          v[2 * q + 1] = fmaf(__shfl_sync(kAll, own_h, e + 1), b.y + r.y, __uint_as_float(acc[e + 1]));
         }
         if (last) {
           store_out(a, x.z, jx, i + ih + 8 * k, v);
