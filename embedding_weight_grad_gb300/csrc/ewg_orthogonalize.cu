@@ -311,6 +311,7 @@ struct OrthoArgs {
 struct GemmSmem {
   uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
   uint64_t piece[kEpilogueWarps][2];
+  int units_done[kEpilogueWarps];    // units an epilogue warp is through with its slot for
   uint32_t tmem;
   int abort;
 };
@@ -413,14 +414,21 @@ __device__ bool wait_inputs(const OrthoArgs& a, int phase, int step, const Unit&
   return wait_ready(a, ready_at(a, kPoly, x.z, x.I), want, abort);
 }
 
-// The warp has stored its part of unit x, by tensor copies of lane 0 and (diagonals) plainly.
-__device__ __forceinline__ void signal_ready(const OrthoArgs& a, int phase, const Unit& x) {
+// The warp is through with unit x: with its slot, and (`signal`) with what it stored, by tensor
+// copies of lane 0 and (diagonals) plainly.
+__device__ __forceinline__ void unit_done(const OrthoArgs& a, int phase, const Unit& x, volatile int* units_done,
+                                          bool signal) {
   __syncwarp();
   if (threadIdx.x % 32 == 0) {
-    ptx::bulk_wait();
-    ptx::fence_proxy_async();
-    ptx::red_release_add(ready_at(a, phase, x.z, x.I), 1);
-    if (phase != kUpdate && x.I != x.J) ptx::red_release_add(ready_at(a, phase, x.z, x.J), 1);
+    ptx::bulk_wait_read();
+    __threadfence_block();
+    *units_done = *units_done + 1;
+    if (signal) {
+      ptx::bulk_wait();
+      ptx::fence_proxy_async();
+      ptx::red_release_add(ready_at(a, phase, x.z, x.I), 1);
+      if (phase != kUpdate && x.I != x.J) ptx::red_release_add(ready_at(a, phase, x.z, x.J), 1);
+    }
   }
   __syncwarp();
 }
@@ -430,6 +438,19 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
   for (uint32_t i = 0; i < kWaitLimit; ++i) {
     if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
     if ((i & 63u) == 63u && *abort) return false;
+  }
+  return false;
+}
+
+// Waits for a count in shared memory.
+__device__ __forceinline__ bool wait_count(volatile int* count, int want, volatile int* abort) {
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    if (*count >= want) {
+      __threadfence_block();
+      return true;
+    }
+    if ((i & 63u) == 63u && *abort) return false;
+    __nanosleep(20);
   }
   return false;
 }
@@ -452,13 +473,6 @@ __device__ __forceinline__ void release_acc(uint32_t acc_empty) {
   if (threadIdx.x % 32 == 0) ptx::mbar_arrive_cluster(acc_empty);
 }
 
-// wait_inputs for a warp that reads them itself.
-__device__ __forceinline__ bool warp_ready(const OrthoArgs& a, int phase, int step, const Unit& x,
-                                           volatile int* abort) {
-  const bool ok = threadIdx.x % 32 != 0 || wait_inputs(a, phase, step, x, abort);
-  return __all_sync(kAll, ok);
-}
-
 // Where an epilogue warp finds a unit's accumulator, and its slot.
 struct Acc {
   uint32_t from;                     // its columns in tensor memory
@@ -469,7 +483,40 @@ struct Acc {
   int place;                         // the warp's place in the pair
   uint32_t slot;                     // shared-memory address
   uint64_t* bars;                    // of the slot's halves: its copies have come
+  volatile int* units_done;          // of the warp
 };
+
+// The first row and column of epilogue warp w's part of a unit (it takes the 32 rows of its
+// quarter of tensor memory, which is its number in the block modulo 4).
+struct Place {
+  int row, col;
+};
+__device__ __forceinline__ Place place_of(int phase, const Unit& x, int rank, int w) {
+  static_assert(kFirstEpilogueWarp % 4 == 0, "warp w's quarter is w % 4");
+  return {(phase == kUpdate ? x.J : x.I) * kBlock + rank * 128 + w % 4 * 32,
+          (phase == kUpdate ? x.I : x.J) * kBlock + w / 4 * kWarpCols};
+}
+
+// How many pieces of a unit a warp has whose 32 rows start at `row` and columns at `col`.
+__device__ __forceinline__ int pieces_of(const OrthoArgs& a, int phase, int row, int col) {
+  if (row >= (phase == kUpdate ? a.c : a.r)) return 0;
+  return min(max((a.r - col + kPiece - 1) / kPiece, 0), kPieces);
+}
+
+// Requests piece u of what the warp's part of a unit reads beside the products (one lane): X's two
+// parts into the whole slot, or A into a half of it.
+__device__ __forceinline__ void request_piece(const OrthoMaps& maps, int phase, int step, int z, int row, int col,
+                                              int u, uint32_t slot, uint64_t* bars) {
+  const int cur = step & 1;
+  if (phase == kUpdate) {
+    ptx::mbar_arrive_expect_tx(&bars[0], kSlotBytes);
+    ptx::tma_load_3d(slot, &maps.xt_piece[cur], col + u * kPiece, row, z, &bars[0]);
+    ptx::tma_load_3d(slot + kPieceBytes, &maps.xl_piece, col + u * kPiece, row, z, &bars[0]);
+  } else {
+    ptx::mbar_arrive_expect_tx(&bars[u], kPieceBytes);
+    ptx::tma_load_3d(slot + u * kPieceBytes, &maps.a_piece[cur], col + u * kPiece, row, z, &bars[u]);
+  }
+}
 
 __device__ __forceinline__ uint4 lds_v4(uint32_t at) {
   uint4 v;
@@ -520,32 +567,21 @@ __device__ __forceinline__ void store_out(const OrthoArgs& a, int z, int jx, int
 }
 
 // One warp's part of a finished block of an update: 32 rows of X^T from j0, kWarpCols columns from
-// i.  X's two parts of the first piece are on their way before the products are done.
+// i.  X's two parts of the first piece were requested by the loading warp.
 __device__ __forceinline__ bool epilogue_update(const OrthoMaps& maps, const OrthoArgs& a, int step, const Unit& x,
                                                 int j0, int i, const Acc& in, uint32_t& parity) {
   const int lane = threadIdx.x % 32, jx = j0 + lane, cur = step & 1;
-  const int pieces = j0 < a.c ? min(max((a.r - i + kPiece - 1) / kPiece, 0), kPieces) : 0;
+  const int pieces = pieces_of(a, kUpdate, j0, i);
   const bool last = step == a.steps - 1;
-  auto request = [&](int u) {        // one lane
-    ptx::mbar_arrive_expect_tx(&in.bars[0], kSlotBytes);
-    ptx::tma_load_3d(in.slot, &maps.xt_piece[cur], i + u * kPiece, j0, x.z, &in.bars[0]);
-    ptx::tma_load_3d(in.slot + kPieceBytes, &maps.xl_piece, i + u * kPiece, j0, x.z, &in.bars[0]);
-  };
-  if (!warp_ready(a, kUpdate, step, x, in.abort)) return false;
-  if (lane == 0 && pieces > 0) {
-    ptx::fence_proxy_async();        // the acquire before the copies
-    request(0);
-  }
-  // a + what is left of B_ii, of column i + 32 q + lane
-  float own[kWarpCols / 32];
-#pragma unroll
-  for (int q = 0; q < kWarpCols / 32; ++q) {
-    const int col = i + 32 * q + lane;
-    own[q] = a.ca + (col < a.r ? a.diag_b[x.z * static_cast<long long>(a.ld) + col] : 0.0f);
-  }
   if (!__all_sync(kAll, wait_bar(in.full, in.parity, in.abort))) return false;
   ptx::tmem_fence_after();
   if (pieces == 0) release_acc(in.empty);
+  float rest[kWarpCols / 32];        // what is left of B_ii, of column i + 32 q + lane
+#pragma unroll
+  for (int q = 0; q < kWarpCols / 32; ++q) {
+    const int col = i + 32 * q + lane;
+    rest[q] = col < a.r ? a.diag_b[x.z * static_cast<long long>(a.ld) + col] : 0.0f;
+  }
 #pragma unroll 1
   for (int u = 0; u < pieces; ++u) {
     if (!wait_piece(in, 0, parity)) return false;
@@ -562,7 +598,7 @@ __device__ __forceinline__ bool epilogue_update(const OrthoMaps& maps, const Ort
       ptx::tmem_wait_load();
       if (u + 1 == pieces && h == 1) release_acc(in.empty);
       const int ih = u * kPiece + 32 * h;             // from i on
-      const float own_h = u == 0 ? (h == 0 ? own[0] : own[1]) : (h == 0 ? own[2] : own[3]);
+      const float own_h = a.ca + (u == 0 ? (h == 0 ? rest[0] : rest[1]) : (h == 0 ? rest[2] : rest[3]));
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const uint32_t tw[4] = {top[k].x, top[k].y, top[k].z, top[k].w};
@@ -599,10 +635,10 @@ __device__ __forceinline__ bool epilogue_update(const OrthoMaps& maps, const Ort
         ptx::bulk_commit();
         ptx::bulk_wait_read();
       }
-      if (u + 1 < pieces) request(u + 1);
+      if (u + 1 < pieces) request_piece(maps, kUpdate, step, x.z, j0, i, u + 1, in.slot, in.bars);
     }
   }
-  if (!last) signal_ready(a, kUpdate, x);
+  unit_done(a, kUpdate, x, in.units_done, !last);
   return true;
 }
 
@@ -617,23 +653,13 @@ __device__ __forceinline__ bool epilogue_square(const OrthoMaps& maps, const Ort
                                                 int i0, int j, const Acc& in, uint32_t& parity) {
   const int lane = threadIdx.x % 32, cur = step & 1;
   const int i = i0 + lane;
-  const int pieces = i0 < a.r ? min(max((a.r - j + kPiece - 1) / kPiece, 0), kPieces) : 0;
+  const int pieces = pieces_of(a, kPhase, i0, j);
   const bool row = i < a.r;
   const long long diag_at = x.z * static_cast<long long>(a.ld) + i;
-  float rest_a = 0.0f;               // what rounding left of A_ii
-  if (kPhase == kPoly) {
-    if (!warp_ready(a, kPoly, step, x, in.abort)) return false;
-    if (lane == 0) {
-      ptx::fence_proxy_async();      // the acquire before the copies
-      for (int u = 0; u < pieces; ++u) {
-        ptx::mbar_arrive_expect_tx(&in.bars[u], kPieceBytes);
-        ptx::tma_load_3d(in.slot + u * kPieceBytes, &maps.a_piece[cur], j + u * kPiece, i0, x.z, &in.bars[u]);
-      }
-    }
-    if (row) rest_a = a.diag_a[cur][diag_at];
-  }
   if (!__all_sync(kAll, wait_bar(in.full, in.parity, in.abort))) return false;
   ptx::tmem_fence_after();
+  float rest_a = 0.0f;               // what rounding left of A_ii
+  if (kPhase == kPoly && row) rest_a = a.diag_a[cur][diag_at];
   const int parts = a.split[kPhase];
   const float* sums = nullptr;       // the first part's
   constexpr int kPartStride = kBlock * kBlock;
@@ -734,7 +760,7 @@ __device__ __forceinline__ bool epilogue_square(const OrthoMaps& maps, const Ort
       ptx::bulk_commit();
     }
   }
-  signal_ready(a, kPhase, x);
+  unit_done(a, kPhase, x, in.units_done, true);
   return true;
 }
 
@@ -756,7 +782,7 @@ __device__ __forceinline__ Majors majors_of(int phase, const Unit& x, int kb) {
 // the matrices of a batch) overlap without a barrier over the grid.  Per CTA: warp 0 copies
 // operands (TMA), warp 1 of the pair's first CTA issues the products, the epilogue warps take
 // finished accumulators (two in tensor memory, so that the products of the next unit run
-// meanwhile).
+// meanwhile), warp 2 copies in what those read beside the products.
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const OrthoArgs a) {
   extern __shared__ unsigned char raw[];
@@ -777,6 +803,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     }
     ptx::mbar_init(&sm.drained, 1);
     for (int i = 0; i < 2 * kEpilogueWarps; ++i) ptx::mbar_init(&sm.piece[0][0] + i, 1);
+    for (int i = 0; i < kEpilogueWarps; ++i) sm.units_done[i] = 0;
     sm.abort = 0;
     ptx::fence_mbar_init();
     ptx::prefetch_tensor_map(&maps.xt[0]);
@@ -792,6 +819,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   ptx::tmem_fence_after();
   const uint32_t tmem = sm.tmem;
   volatile int* abort = &sm.abort;
+  const uint32_t slots = stages + kStages * kStageBytes;     // of the epilogue warps
 
   uint32_t stage = 0, stage_phase = 0;      // producer's or issuer's place in the ring
   uint32_t acc = 0, acc_phase = 0;          // issuer's or epilogue's accumulator
@@ -892,21 +920,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       });
     }
     __syncwarp();
+  } else if (warp == 2) {
+    // Lane w requests what epilogue warp w reads first in a unit, as soon as the block rows are
+    // there and the warp is through with its slot for the unit before.  (A count, not the
+    // parity of a barrier: units of X X^T need no loads, and the epilogue may run ahead there.)
+    const int w = lane < kEpilogueWarps ? lane : 0;
+    int units = 0;
+    for_units([&](int phase, int step, const Unit& x) {
+      bool ok = phase == kGram || lane != 0 || wait_inputs(a, phase, step, x, abort);
+      ok = ok && wait_count(&sm.units_done[w], units++, abort);
+      if (!__all_sync(kAll, ok)) return false;
+      if (phase != kGram && lane < kEpilogueWarps) {
+        ptx::fence_proxy_async();    // the acquires above before the tensor copies
+        const Place at = place_of(phase, x, rank, w);
+        const int pieces = pieces_of(a, phase, at.row, at.col);
+        for (int u = 0; u < pieces && (phase == kPoly || u == 0); ++u)
+          request_piece(maps, phase, step, x.z, at.row, at.col, u, slots + w * kSlotBytes, sm.piece[w]);
+      }
+      __syncwarp();
+      return true;
+    });
   } else if (warp >= kFirstEpilogueWarp) {
     const int index = warp - kFirstEpilogueWarp;
     const int quarter = warp % 4, part = index / 4;
-    const uint32_t slot = stages + kStages * kStageBytes + index * kSlotBytes;
     uint32_t parity = 0;             // of the slot's barriers
     for_units([&](int phase, int step, const Unit& x) {
       const Acc in{tmem + acc * kBlock + part * kWarpCols + (static_cast<uint32_t>(quarter) << 21),
                    &sm.acc_full[acc], acc_phase, ptx::map_to_rank(ptx::smem_u32(&sm.acc_empty[acc]), 0), abort,
-                   static_cast<int>(rank) * kEpilogueWarps + index, slot, sm.piece[index]};
-      const int row = (phase == kUpdate ? x.J : x.I) * kBlock + rank * 128 + quarter * 32;
-      const int col = (phase == kUpdate ? x.I : x.J) * kBlock + part * kWarpCols;
+                   static_cast<int>(rank) * kEpilogueWarps + index, slots + index * kSlotBytes, sm.piece[index],
+                   &sm.units_done[index]};
+      const Place at = place_of(phase, x, rank, index);
       next_acc();
-      return phase == kGram ? epilogue_square<kGram>(maps, a, step, x, row, col, in, parity)
-             : phase == kPoly ? epilogue_square<kPoly>(maps, a, step, x, row, col, in, parity)
-                              : epilogue_update(maps, a, step, x, row, col, in, parity);
+      return phase == kGram ? epilogue_square<kGram>(maps, a, step, x, at.row, at.col, in, parity)
+             : phase == kPoly ? epilogue_square<kPoly>(maps, a, step, x, at.row, at.col, in, parity)
+                              : epilogue_update(maps, a, step, x, at.row, at.col, in, parity);
     });
     if (lane == 0) ptx::bulk_wait();
   }
