@@ -137,16 +137,6 @@ inline OrthoLayout make_ortho_layout(const OrthoShape& s) {
   return L;
 }
 
-// Matrices of a batch that go through the steps together: as many as L2 holds with all their
-// buffers, and at least enough for every pair to have a block of each phase.
-constexpr int64_t kOrthoL2Bytes = 1000 << 20;
-inline int ortho_chunk(const OrthoShape& s) {
-  const int64_t bytes = 6 * (s.c + s.r) * s.ld;      // X^T twice and its rest, A twice, B: 2 bytes each
-  const int64_t fit = kOrthoL2Bytes / bytes, fill = (kOrthoPairs + s.square_blocks() - 1) / s.square_blocks();
-  const int64_t chunk = fit > fill ? fit : fill;
-  return static_cast<int>(chunk < s.batch ? chunk : s.batch);
-}
-
 struct OrthoCall {
   OrthoShape shape;
   const void* grad;

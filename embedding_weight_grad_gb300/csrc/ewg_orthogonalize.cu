@@ -183,35 +183,46 @@ __global__ void __launch_bounds__(256) ortho_scale_kernel(const OrthoIn a) {
   __shared__ double factor;
   const int tid = threadIdx.x;
   const int row0 = blockIdx.y * 64, col0 = blockIdx.x * 64;
-  // 16 bytes of G a thread, all of its part of the tile before the wait for the norm
-  const int per = a.bf16 ? 8 : 4;                    // elements of a vector
-  const int line = 64 / per, rows = 256 / line;      // threads to a row, rows at once
-  const int cx = tid % line * per, ry = tid / line;
   const int es = a.bf16 ? 2 : 4;
   const char* base = static_cast<const char*>(a.grad) +
                      (blockIdx.z * a.batch_stride + static_cast<long long>(row0) * a.row_stride + col0) * es;
-#pragma unroll 4
-  for (int k = ry; k < 64; k += rows) {
-    if (row0 + k >= a.rows) break;
-    const char* p = base + (k * a.row_stride + cx) * es;
-    const int n = a.cols - col0 - cx;
-    if (n >= per && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
-      const uint4 v = *reinterpret_cast<const uint4*>(p);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const long long row_bytes = a.row_stride * es;
+  if (row0 + 64 <= a.rows && col0 + 64 <= a.cols && reinterpret_cast<uintptr_t>(base) % 16 == 0 && row_bytes % 16 == 0) {
+    // 16 bytes a thread: 4 rows of 64 numbers at once in a warp for bf16, 2 for fp32
+    const int per = a.bf16 ? 8 : 4;                  // numbers of a vector
+    const int line = 64 / per, rows = 256 / line;    // threads to a row, rows at once
+    const int cx = tid % line * per, ry = tid / line;
+    uint4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (ry + k * rows < 64) v[k] = *reinterpret_cast<const uint4*>(base + (ry + k * rows) * row_bytes + cx * es);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (ry + k * rows >= 64) continue;
+      float* t = &tile[ry + k * rows][cx];
+      const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         if (a.bf16) {
-          tile[k][cx + 2 * q] = __uint_as_float(w[q] << 16);
-          tile[k][cx + 2 * q + 1] = __uint_as_float(w[q] & 0xffff0000u);
+          t[2 * q] = __uint_as_float(w[q] << 16);
+          t[2 * q + 1] = __uint_as_float(w[q] & 0xffff0000u);
         } else {
-          tile[k][cx + q] = __uint_as_float(w[q]);
+          t[q] = __uint_as_float(w[q]);
         }
       }
-    } else {
-      for (int q = 0; q < per && q < n; ++q)
-        tile[k][cx + q] = a.bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[q])
-                                 : reinterpret_cast<const float*>(p)[q];
     }
+  } else {
+    const int cx = tid % 64, ry = tid / 64;
+    float v[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const bool in = row0 + ry + 4 * k < a.rows && col0 + cx < a.cols;
+      const char* p = base + (ry + 4 * k) * row_bytes + cx * es;
+      v[k] = !in ? 0.0f : a.bf16 ? __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(p))
+                                 : *reinterpret_cast<const float*>(p);
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) tile[ry + 4 * k][cx] = v[k];
   }
   if (tid < 32) {
     double sum = 0.0;
@@ -295,9 +306,10 @@ struct OrthoArgs {
   int steps;
   float ca, cb, cc;                  // the polynomial's coefficients
   float s;                           // X is stored times s
-  float* diag_a[2];                  // [batch][ld]: what rounding left of the diagonals (A's of even and odd steps)
+  __half* a[2];                      // A of even and odd steps
+  __half* b;
+  float* diag_a[2];                  // [batch][ld]: what rounding left of the diagonals
   float* diag_b;
-  int chunk;                         // matrices that go through the steps together
   int split[2];                      // parts of the inner dimension of X X^T and A A
   float* partial;                    // split products: [batch][block][part][CTA][warp][column][row]
   __nv_bfloat16* out;
@@ -330,16 +342,15 @@ struct Unit {
   int z, I, J, part;
 };
 
-// Units of a phase for `matrices` matrices.
-__device__ __forceinline__ int units_of(const OrthoArgs& a, int phase, int matrices) {
+__device__ __forceinline__ int units_of(const OrthoArgs& a, int phase) {
   const int nr = blocks_of(a.r);
-  return matrices * (phase == kUpdate ? nr * blocks_of(a.c) : nr * (nr + 1) / 2 * a.split[phase]);
+  return a.batch * (phase == kUpdate ? nr * blocks_of(a.c) : nr * (nr + 1) / 2 * a.split[phase]);
 }
 
-// Unit t of a phase for the matrices from z0 on.  The orders let a phase start before the one before it has ended: the
+// Unit t of a phase.  The orders let a phase start before the one before it has ended: the
 // update goes by rows, which is what A's blocks by rows need; B's blocks go by columns, whose
 // first ones complete B's first rows, which the update's first rows need.
-__device__ __forceinline__ Unit unit_at(const OrthoArgs& a, int phase, int z0, int t) {
+__device__ __forceinline__ Unit unit_at(const OrthoArgs& a, int phase, int t) {
   const int nr = blocks_of(a.r);
   Unit x;
   if (phase == kUpdate) {
@@ -349,7 +360,6 @@ __device__ __forceinline__ Unit unit_at(const OrthoArgs& a, int phase, int z0, i
     x.I = t / nc;
     x.J = t - x.I * nc;
     x.part = 0;
-    x.z += z0;
     return x;
   }
   const int blocks = nr * (nr + 1) / 2, parts = a.split[phase];
@@ -364,7 +374,6 @@ __device__ __forceinline__ Unit unit_at(const OrthoArgs& a, int phase, int z0, i
   const int col = t - row * (row + 1) / 2;
   x.I = phase == kPoly ? nr - 1 - col : row;
   x.J = phase == kPoly ? nr - 1 - row : col;
-  x.z += z0;
   return x;
 }
 
@@ -642,12 +651,46 @@ __device__ __forceinline__ bool epilogue_update(const OrthoMaps& maps, const Ort
   return true;
 }
 
+// Eight columns of a row of A or B from the products v and, for B, A's numbers `o`; `d` is the
+// row less the first column, and what rounding leaves of the diagonal goes to diag[diag_at].
+template <int kPhase>
+__device__ __forceinline__ uint4 finish8(const OrthoArgs& a, int cur, float f, float (&v)[8], uint4 o, int d,
+                                         float rest_a, long long diag_at) {
+  float on = 0.0f;                   // A_ii as stored
+#pragma unroll
+  for (int q = 0; q < 8; ++q) v[q] *= f;
+  if constexpr (kPhase == kPoly) {
+    const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float2 p = unpack_half(w[q]);
+      v[2 * q] = fmaf(a.cb, p.x, v[2 * q]);
+      v[2 * q + 1] = fmaf(a.cb, p.y, v[2 * q + 1]);
+      if (d == 2 * q) on = p.x;
+      if (d == 2 * q + 1) on = p.y;
+    }
+  }
+  if (d >= 0 && d < 8) {             // the diagonal passes through
+    const float more = kPhase == kPoly ? rest_a * fmaf(2.0f * a.cc, on, a.cb) : 0.0f;   // to first order
+    float left = 0.0f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      if (q != d) continue;
+      v[q] += more;
+      left = v[q] - __half2float(__float2half_rn(v[q]));
+    }
+    if (diag_at >= 0) (kPhase == kGram ? a.diag_a[cur] : a.diag_b)[diag_at] = left;
+  }
+  return make_uint4(pack_half(v[0], v[1]), pack_half(v[2], v[3]), pack_half(v[4], v[5]), pack_half(v[6], v[7]));
+}
+
 // The same for A = X X^T or B = b A + c A^2: 32 rows from i0, kWarpCols columns from j of a block on
 // or below the diagonal.
 //
 // Where the inner dimension is split, each part's warp stores its sums, waits for the other
-// parts' and finishes its share of the columns from all parts' sums, added in their order.  (The
-// units of such a phase are no more than the pairs, so the parts run at the same time.)
+// parts' and finishes its share of the columns, in eights, from all parts' sums, added in
+// their order.  (The units of such a phase are no more than the pairs, so the parts run at
+// the same time.)
 template <int kPhase>
 __device__ __forceinline__ bool epilogue_square(const OrthoMaps& maps, const OrthoArgs& a, int step, const Unit& x,
                                                 int i0, int j, const Acc& in, uint32_t& parity) {
@@ -661,13 +704,13 @@ __device__ __forceinline__ bool epilogue_square(const OrthoMaps& maps, const Ort
   float rest_a = 0.0f;               // what rounding left of A_ii
   if (kPhase == kPoly && row) rest_a = a.diag_a[cur][diag_at];
   const int parts = a.split[kPhase];
-  const float* sums = nullptr;       // the first part's
-  constexpr int kPartStride = kBlock * kBlock;
+  const float f = kPhase == kGram ? 1.0f / (a.s * a.s) : a.cc;
   if (parts > 1) {
     const int nr = blocks_of(a.r), blocks = nr * (nr + 1) / 2;
     const long long block = static_cast<long long>(x.z) * blocks + x.I * (x.I + 1) / 2 + x.J;
-    float* first = a.partial + block * parts * kPartStride + in.place * (32 * kWarpCols) + lane;
-    float* mine = first + static_cast<long long>(x.part) * kPartStride;
+    constexpr int kPartStride = kBlock * kBlock;
+    const float* sums = a.partial + block * parts * kPartStride + in.place * (32 * kWarpCols) + lane;
+    float* mine = a.partial + (block * parts + x.part) * kPartStride + in.place * (32 * kWarpCols) + lane;
 #pragma unroll 1
     for (int u = 0; u < 2 * pieces; ++u) {
       uint32_t acc[32];
@@ -677,7 +720,6 @@ __device__ __forceinline__ bool epilogue_square(const OrthoMaps& maps, const Ort
       for (int q = 0; q < 32; ++q) mine[(u * 32 + q) * 32] = __uint_as_float(acc[q]);
     }
     release_acc(in.empty);
-    __syncwarp();
     bool ok = true;
     if (lane == 0) {
       int* arrived = a.arrived + ((static_cast<long long>(x.z) * 2 + kPhase) * blocks + x.I * (x.I + 1) / 2 + x.J) *
@@ -686,72 +728,53 @@ __device__ __forceinline__ bool epilogue_square(const OrthoMaps& maps, const Ort
       ok = wait_ready(a, arrived, (step + 1) * parts, in.abort);
     }
     if (!__all_sync(kAll, ok)) return false;
-    sums = first;
-  } else if (pieces == 0) {
-    release_acc(in.empty);
+    if (kPhase == kPoly)
+      for (int u = 0; u < pieces; ++u)
+        if (!wait_piece(in, u, parity)) return false;
+    __half* m = (kPhase == kGram ? a.a[cur] : a.b) + (static_cast<long long>(x.z) * a.r + i) * a.ld + j;
+    constexpr int kEights = kWarpCols / 8;
+#pragma unroll 1
+    for (int g = x.part * kEights / parts; g < (x.part + 1) * kEights / parts; ++g) {
+      const int jg = j + 8 * g;
+      if (jg >= a.r) break;
+      float v[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = sums[(8 * g + q) * 32];
+#pragma unroll 4
+      for (int k = 1; k < parts; ++k) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] += sums[k * kPartStride + (8 * g + q) * 32];
+      }
+      uint4 o = {};
+      if (kPhase == kPoly) o = lds_v4(chunk_at(in.slot + g / 8 * kPieceBytes, g % 8));
+      const uint4 w = finish8<kPhase>(a, cur, f, v, o, i - jg, rest_a, row ? diag_at : -1);
+      if (row) *reinterpret_cast<uint4*>(m + 8 * g) = w;
+    }
+    ptx::fence_proxy_async();        // these plain stores are read by tensor copies
+    unit_done(a, kPhase, x, in.units_done, true);
+    return true;
   }
-  const float f = kPhase == kGram ? 1.0f / (a.s * a.s) : a.cc;
+  if (pieces == 0) release_acc(in.empty);
 #pragma unroll 1
   for (int u = 0; u < pieces; ++u) {
     const uint32_t slot = in.slot + u * kPieceBytes;
     if (kPhase == kPoly && !wait_piece(in, u, parity)) return false;
-    if (parts > 1 && u % parts != x.part) continue;   // another part's share
 #pragma unroll 1
     for (int h = 0; h < 2; ++h) {    // 32 columns at a time
-      const int jh = j + u * kPiece + 32 * h;
-      float v[32];
-      if (parts == 1) {
-        uint32_t acc[32];
-        ptx::tmem_load32(acc, in.from + u * kPiece + 32 * h);
-        ptx::tmem_wait_load();
-        if (u + 1 == pieces && h == 1) release_acc(in.empty);
+      uint32_t acc[32];
+      ptx::tmem_load32(acc, in.from + u * kPiece + 32 * h);
+      ptx::tmem_wait_load();
+      if (u + 1 == pieces && h == 1) release_acc(in.empty);
 #pragma unroll
-        for (int q = 0; q < 32; ++q) v[q] = __uint_as_float(acc[q]) * f;
-      } else {
-        const float* p = sums + (u * kPiece + 32 * h) * 32;
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t at = chunk_at(slot, 4 * h + k);
+        float v[8];
 #pragma unroll
-        for (int q = 0; q < 32; ++q) v[q] = p[q * 32];
-#pragma unroll 1
-        for (int k = 1; k < parts; ++k) {
-#pragma unroll
-          for (int q = 0; q < 32; ++q) v[q] += p[k * kPartStride + q * 32];
-        }
-#pragma unroll
-        for (int q = 0; q < 32; ++q) v[q] *= f;
+        for (int q = 0; q < 8; ++q) v[q] = __uint_as_float(acc[8 * k + q]);
+        uint4 o = {};
+        if (kPhase == kPoly) o = lds_v4(at);
+        sts_v4(at, finish8<kPhase>(a, cur, f, v, o, i - (j + u * kPiece + 32 * h + 8 * k), rest_a, row ? diag_at : -1));
       }
-      float own_o = 0.0f;            // A_ii as stored, where the diagonal passes through
-      if constexpr (kPhase == kPoly) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint4 o = lds_v4(chunk_at(slot, 4 * h + k));
-          const uint32_t w[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float2 p = unpack_half(w[q]);
-            const int e = 8 * k + 2 * q;
-            if (jh + e == i) own_o = p.x;
-            if (jh + e + 1 == i) own_o = p.y;
-            v[e] = fmaf(a.cb, p.x, v[e]);
-            v[e + 1] = fmaf(a.cb, p.y, v[e + 1]);
-          }
-        }
-      }
-      if (jh < i0 + 32 && i0 < jh + 32) {             // the diagonal passes through
-        const float more = kPhase == kPoly ? rest_a * fmaf(2.0f * a.cc, own_o, a.cb) : 0.0f;   // to first order
-        float left = 0.0f;
-#pragma unroll
-        for (int q = 0; q < 32; ++q) {
-          if (jh + q != i) continue;
-          v[q] += more;
-          left = v[q] - __half2float(__float2half_rn(v[q]));
-        }
-        if (i >= jh && i < jh + 32 && row) (kPhase == kGram ? a.diag_a[cur] : a.diag_b)[diag_at] = left;
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        sts_v4(chunk_at(slot, 4 * h + k),
-               make_uint4(pack_half(v[8 * k], v[8 * k + 1]), pack_half(v[8 * k + 2], v[8 * k + 3]),
-                          pack_half(v[8 * k + 4], v[8 * k + 5]), pack_half(v[8 * k + 6], v[8 * k + 7])));
     }
     ptx::fence_proxy_async_shared();
     __syncwarp();
@@ -776,8 +799,8 @@ __device__ __forceinline__ Majors majors_of(int phase, const Unit& x, int kb) {
   return {false, k > x.I};
 }
 
-// All phases of all steps, one cooperative launch of CTA pairs.  A chunk of the batch at a time
-// (see ortho_chunk), the units of all phases in order go round the pairs; a unit waits for the block rows that it reads, which units before
+// All phases of all steps, one cooperative launch of CTA pairs.  The units of all phases in
+// order go round the pairs; a unit waits for the block rows that it reads, which units before
 // it in the order store, so the earliest unfinished unit never waits and the phases (and
 // the matrices of a batch) overlap without a barrier over the grid.  Per CTA: warp 0 copies
 // operands (TMA), warp 1 of the pair's first CTA issues the products, the epilogue warps take
@@ -838,20 +861,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   // body(phase, step, unit) for this pair's units in order, until one gives up
   auto for_units = [&](auto&& body) {
     int offset = 0;                  // units so far, modulo the pairs
-    for (int z0 = 0; z0 < a.batch; z0 += a.chunk) {
-      const int matrices = min(a.chunk, a.batch - z0);
-      for (int p = 0; p < 3 * a.steps; ++p) {
-        const int phase = p % 3, step = p / 3;
-        const int units = units_of(a, phase, matrices);
-        for (int t = pair >= offset ? pair - offset : pair - offset + pairs; t < units; t += pairs) {
-          if (*abort) return;
-          if (!body(phase, step, unit_at(a, phase, z0, t))) {
-            gave_up(a, abort);
-            return;
-          }
+    for (int p = 0; p < 3 * a.steps; ++p) {
+      const int phase = p % 3, step = p / 3;
+      const int units = units_of(a, phase);
+      for (int t = pair >= offset ? pair - offset : pair - offset + pairs; t < units; t += pairs) {
+        if (*abort) return;
+        if (!body(phase, step, unit_at(a, phase, t))) {
+          gave_up(a, abort);
+          return;
         }
-        offset = (offset + units) % pairs;
       }
+      offset = (offset + units) % pairs;
     }
   };
 
@@ -1079,8 +1099,10 @@ cudaError_t launch_orthogonalize(const OrthoCall& q, cudaStream_t stream) {
   a.cc = q.c;
   a.s = in.s;
   for (int i = 0; i < 2; ++i) {
+    a.a[i] = reinterpret_cast<__half*>(ws + L.a[i]);
     a.diag_a[i] = reinterpret_cast<float*>(ws + L.diag_a[i]);
   }
+  a.b = reinterpret_cast<__half*>(ws + L.b);
   a.diag_b = reinterpret_cast<float*>(ws + L.diag_b);
   a.out = static_cast<__nv_bfloat16*>(q.out);
   a.out_batch = q.out_batch_stride;
@@ -1090,7 +1112,6 @@ cudaError_t launch_orthogonalize(const OrthoCall& q, cudaStream_t stream) {
   a.ready = in.counters;
   a.arrived = in.counters + sh.batch * 3 * nr;
   a.partial = reinterpret_cast<float*>(ws + L.partial);
-  a.chunk = ortho_chunk(sh);
   a.split[kGram] = sh.split_gram;
   a.split[kPoly] = sh.split_poly;
 
