@@ -277,14 +277,19 @@ constexpr int kFirstEpilogueWarp = 4;
 constexpr int kEpilogueWarps = 8;
 constexpr int kWarpsOfBlock = 2 * kEpilogueWarps;     // of the pair
 constexpr int kWarpCols = 4 * kBlock / kEpilogueWarps;   // columns of an epilogue warp (all take 32 rows)
-// The epilogue takes a warp's 32 rows in pieces of 64 columns, which come and go by tensor copies
-// of 128-byte rows through a slot of the warp: two parts of X, or two pieces of A or B.
+// The epilogue takes a warp's 32 rows of A or B in pieces of 64 columns, of X in strips of 32
+// columns, which come and go by tensor copies through a slot of the warp: two pieces, or two
+// strips of both parts of X.
 // (Copies by the threads themselves, of 32 or 64 bytes a row, took two to three times as long:
 // the path to L2 carries requests, not bytes.)
 constexpr int kPiece = 64;
 constexpr int kPieces = kWarpCols / kPiece;
 constexpr int kPieceBytes = 32 * kPiece * 2;
+constexpr int kStrip = 32;
+constexpr int kStrips = kWarpCols / kStrip;
+constexpr int kStripBytes = 32 * kStrip * 2;          // of one part of X
 constexpr int kSlotBytes = 2 * kPieceBytes;
+static_assert(kSlotBytes == 4 * kStripBytes, "a slot holds two strips of both parts");
 constexpr int kGemmThreads = 32 * (kFirstEpilogueWarp + kEpilogueWarps);
 constexpr size_t kGemmSmem =
     static_cast<size_t>(kStages) * kStageBytes + kEpilogueWarps * kSlotBytes + 1024;
@@ -298,7 +303,8 @@ enum Phase { kGram = 0, kPoly = 1, kUpdate = 2 };
 
 struct OrthoMaps {
   CUtensorMap xt[2], a[2], b;        // operands: boxes of 64 x 64
-  CUtensorMap xt_piece[2], xl_piece, a_piece[2], b_piece;   // pieces: 64 of the r index x 32
+  CUtensorMap xt_strip[2], xl_strip;         // 32 of the r index x 32
+  CUtensorMap a_piece[2], b_piece;           // 64 x 32
 };
 
 struct OrthoArgs {
@@ -433,8 +439,7 @@ __device__ __forceinline__ void unit_done(const OrthoArgs& a, int phase, const U
     __threadfence_block();
     *units_done = *units_done + 1;
     if (signal) {
-      ptx::bulk_wait();
-      ptx::fence_proxy_async();
+      ptx::bulk_wait();              // its copies' writes are done, and visible to it
       ptx::red_release_add(ready_at(a, phase, x.z, x.I), 1);
       if (phase != kUpdate && x.I != x.J) ptx::red_release_add(ready_at(a, phase, x.z, x.J), 1);
     }
@@ -506,25 +511,25 @@ __device__ __forceinline__ Place place_of(int phase, const Unit& x, int rank, in
           (phase == kUpdate ? x.I : x.J) * kBlock + w / 4 * kWarpCols};
 }
 
-// How many pieces of a unit a warp has whose 32 rows start at `row` and columns at `col`.
-__device__ __forceinline__ int pieces_of(const OrthoArgs& a, int phase, int row, int col) {
-  if (row >= (phase == kUpdate ? a.c : a.r)) return 0;
-  return min(max((a.r - col + kPiece - 1) / kPiece, 0), kPieces);
+// How many pieces (or strips) of `width` columns a warp's part has that starts at (row, col).
+__device__ __forceinline__ int pieces_of(const OrthoArgs& a, int phase, const Place& at, int width) {
+  if (at.row >= (phase == kUpdate ? a.c : a.r)) return 0;
+  return min(max((a.r - at.col + width - 1) / width, 0), kWarpCols / width);
 }
 
-// Requests piece u of what the warp's part of a unit reads beside the products (one lane): X's two
-// parts into the whole slot, or A into a half of it.
-__device__ __forceinline__ void request_piece(const OrthoMaps& maps, int phase, int step, int z, int row, int col,
-                                              int u, uint32_t slot, uint64_t* bars) {
-  const int cur = step & 1;
-  if (phase == kUpdate) {
-    ptx::mbar_arrive_expect_tx(&bars[0], kSlotBytes);
-    ptx::tma_load_3d(slot, &maps.xt_piece[cur], col + u * kPiece, row, z, &bars[0]);
-    ptx::tma_load_3d(slot + kPieceBytes, &maps.xl_piece, col + u * kPiece, row, z, &bars[0]);
-  } else {
-    ptx::mbar_arrive_expect_tx(&bars[u], kPieceBytes);
-    ptx::tma_load_3d(slot + u * kPieceBytes, &maps.a_piece[cur], col + u * kPiece, row, z, &bars[u]);
-  }
+// Requests (one lane) what a warp's part of a unit reads beside the products: piece u of A, or
+// strip u of both parts of X, into half u % 2 of the slot.
+__device__ __forceinline__ void request_piece(const OrthoMaps& maps, int step, int z, const Place& at, int u,
+                                              uint32_t slot, uint64_t* bars) {
+  ptx::mbar_arrive_expect_tx(&bars[u], kPieceBytes);
+  ptx::tma_load_3d(slot + u * kPieceBytes, &maps.a_piece[step & 1], at.col + u * kPiece, at.row, z, &bars[u]);
+}
+__device__ __forceinline__ void request_strip(const OrthoMaps& maps, int step, int z, const Place& at, int u,
+                                              uint32_t slot, uint64_t* bars) {
+  const uint32_t to = slot + u % 2 * (2 * kStripBytes);
+  ptx::mbar_arrive_expect_tx(&bars[u % 2], 2 * kStripBytes);
+  ptx::tma_load_3d(to, &maps.xt_strip[step & 1], at.col + u * kStrip, at.row, z, &bars[u % 2]);
+  ptx::tma_load_3d(to + kStripBytes, &maps.xl_strip, at.col + u * kStrip, at.row, z, &bars[u % 2]);
 }
 
 __device__ __forceinline__ uint4 lds_v4(uint32_t at) {
@@ -542,6 +547,12 @@ __device__ __forceinline__ uint32_t chunk_at(uint32_t piece, int chunk) {
   return piece + lane * 128 + ((chunk ^ (lane & 7)) << 4);
 }
 
+// The same of a strip, in the 64-byte swizzle.
+__device__ __forceinline__ uint32_t strip_chunk_at(uint32_t strip, int chunk) {
+  const uint32_t lane = threadIdx.x % 32;
+  return strip + lane * 64 + ((chunk ^ ((lane >> 1) & 3)) << 4);
+}
+
 // Waits (a whole warp) for the copies into half h of the slot.
 __device__ __forceinline__ bool wait_piece(const Acc& in, int h, uint32_t& parity) {
   if (!__all_sync(kAll, wait_bar(&in.bars[h], (parity >> h) & 1u, in.abort))) return false;
@@ -549,102 +560,121 @@ __device__ __forceinline__ bool wait_piece(const Acc& in, int h, uint32_t& parit
   return true;
 }
 
-// The last update's piece, to the caller's matrix: lane = row jx of X^T, columns i0 .. + 7.
-__device__ __forceinline__ void store_out(const OrthoArgs& a, int z, int jx, int i0, const float (&v)[8]) {
-  const int n = min(a.r - i0, 8);
-  if (jx >= a.c || n <= 0) return;
-  __nv_bfloat16* out = a.out + z * a.out_batch;
-  const float unscale = 1.0f / a.s;
+// The last update's strip, to the caller's matrix: lane = row j0 + lane of X^T, columns i0 .. + 31,
+// packed in bf16; `buf` is free shared memory for 32 x 64 bytes.
+__device__ __forceinline__ void store_out(const OrthoArgs& a, int z, int j0, int i0, const uint32_t (&w)[16],
+                                          uint32_t buf) {
+  const int lane = threadIdx.x % 32, jx = j0 + lane;
+  const int n = min(a.r - i0, kStrip);
+  uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + z * a.out_batch;
   if (!a.tall) {                     // out is [r, c]: neighbouring lanes, neighbouring elements
-    __nv_bfloat16* p = out + i0 * a.out_row + jx;
+    uint16_t* p = out + i0 * a.out_row + jx;
+    if (jx >= a.c) return;
 #pragma unroll
-    for (int q = 0; q < 8; ++q)
-      if (q < n) p[q * a.out_row] = __float2bfloat16_rn(v[q] * unscale);
+    for (int q = 0; q < 32; ++q)
+      if (q < n) p[q * a.out_row] = static_cast<uint16_t>(q % 2 ? w[q / 2] >> 16 : w[q / 2]);
     return;
   }
-  __nv_bfloat16* p = out + jx * a.out_row + i0;
-  if (n == 8 && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
-    uint32_t w[4];
+  // out is [c, r]: 16 bytes at once, or through shared memory a row at a time where the rows of
+  // out are not aligned for that
+  const bool vec = reinterpret_cast<uintptr_t>(out + i0) % 16 == 0 && a.out_row % 8 == 0 && n == kStrip;
+  if (vec) {
+    if (jx >= a.c) return;
+    uint4* p = reinterpret_cast<uint4*>(out + jx * a.out_row + i0);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) w[q] = pack_bf16(v[2 * q] * unscale, v[2 * q + 1] * unscale);
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-  } else {
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-      if (q < n) p[q] = __float2bfloat16_rn(v[q] * unscale);
+    for (int k = 0; k < 4; ++k) p[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    return;
   }
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    sts_v4(strip_chunk_at(buf, k), make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]));
+  __syncwarp();
+  const int rows = min(a.c - j0, 32);
+#pragma unroll 8
+  for (int r = 0; r < 32; ++r) {     // lane = column
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];"
+                 : "=h"(v) : "r"(buf + r * 64 + (((lane / 8) ^ ((r >> 1) & 3)) << 4) + lane % 8 * 2));
+    if (r < rows && lane < n) out[(j0 + r) * a.out_row + i0 + lane] = v;
+  }
+  __syncwarp();
 }
 
-// One warp's part of a finished block of an update: 32 rows of X^T from j0, kWarpCols columns from
-// i.  X's two parts of the first piece were requested by the loading warp.
+// One warp's part of a finished block of an update: 32 rows of X^T, kWarpCols columns.  X's two
+// parts of the first two strips were requested by the loading warp.
 __device__ __forceinline__ bool epilogue_update(const OrthoMaps& maps, const OrthoArgs& a, int step, const Unit& x,
-                                                int j0, int i, const Acc& in, uint32_t& parity) {
-  const int lane = threadIdx.x % 32, jx = j0 + lane, cur = step & 1;
-  const int pieces = pieces_of(a, kUpdate, j0, i);
+                                                const Place& at, const Acc& in, uint32_t& parity) {
+  const int lane = threadIdx.x % 32, cur = step & 1;
+  const int strips = pieces_of(a, kUpdate, at, kStrip);
   const bool last = step == a.steps - 1;
   if (!__all_sync(kAll, wait_bar(in.full, in.parity, in.abort))) return false;
   ptx::tmem_fence_after();
-  if (pieces == 0) release_acc(in.empty);
-  float rest[kWarpCols / 32];        // what is left of B_ii, of column i + 32 q + lane
+  if (strips == 0) release_acc(in.empty);
+  float rest[kStrips];               // what is left of B_ii, of column 32 q + lane
 #pragma unroll
-  for (int q = 0; q < kWarpCols / 32; ++q) {
-    const int col = i + 32 * q + lane;
+  for (int q = 0; q < kStrips; ++q) {
+    const int col = at.col + 32 * q + lane;
     rest[q] = col < a.r ? a.diag_b[x.z * static_cast<long long>(a.ld) + col] : 0.0f;
   }
+  const float unscale = 1.0f / a.s;
 #pragma unroll 1
-  for (int u = 0; u < pieces; ++u) {
-    if (!wait_piece(in, 0, parity)) return false;
-#pragma unroll 1
-    for (int h = 0; h < 2; ++h) {    // 32 columns at a time
-      uint32_t acc[32];
-      ptx::tmem_load32(acc, in.from + u * kPiece + 32 * h);
-      uint4 top[4], low[4];
+  for (int u = 0; u < strips; ++u) {
+    const uint32_t strip = in.slot + u % 2 * (2 * kStripBytes);
+    uint32_t acc[kStrip];
+    ptx::tmem_load32(acc, in.from + u * kStrip);
+    if (!wait_piece(in, u % 2, parity)) return false;
+    uint4 top[4], low[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        top[k] = lds_v4(chunk_at(in.slot, 4 * h + k));
-        low[k] = lds_v4(chunk_at(in.slot + kPieceBytes, 4 * h + k));
-      }
-      ptx::tmem_wait_load();
-      if (u + 1 == pieces && h == 1) release_acc(in.empty);
-      const int ih = u * kPiece + 32 * h;             // from i on
-      const float own_h = a.ca + (u == 0 ? (h == 0 ? rest[0] : rest[1]) : (h == 0 ? rest[2] : rest[3]));
+    for (int k = 0; k < 4; ++k) {
+      top[k] = lds_v4(strip_chunk_at(strip, k));
+      low[k] = lds_v4(strip_chunk_at(strip + kStripBytes, k));
+    }
+    const float own = a.ca + (u < 2 ? (u == 0 ? rest[0] : rest[1]) : (u == 2 ? rest[2] : rest[3]));
+    ptx::tmem_wait_load();
+    if (u + 1 == strips) release_acc(in.empty);
+    uint32_t hw[16], lw[16];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t tw[4] = {top[k].x, top[k].y, top[k].z, top[k].w};
-        const uint32_t lw[4] = {low[k].x, low[k].y, low[k].z, low[k].w};
-        float v[8];
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t tk[4] = {top[k].x, top[k].y, top[k].z, top[k].w};
+      const uint32_t lk[4] = {low[k].x, low[k].y, low[k].z, low[k].w};
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float2 b = unpack_half(tw[q]), r = unpack_half(lw[q]);
-          const int e = 8 * k + 2 * q;
-          v[2 * q] = fmaf(__shfl_sync(kAll, own_h, e), b.x + r.x, __uint_as_float(acc[e]));
-          v[2 * q + 1] = fmaf(__shfl_sync(kAll, own_h, e + 1), b.y + r.y, __uint_as_float(acc[e + 1]));
-        }
+      for (int q = 0; q < 4; ++q) {
+        const float2 b = unpack_half(tk[q]), r = unpack_half(lk[q]);
+        const int e = 8 * k + 2 * q;
+        const float v0 = fmaf(__shfl_sync(kAll, own, e), b.x + r.x, __uint_as_float(acc[e]));
+        const float v1 = fmaf(__shfl_sync(kAll, own, e + 1), b.y + r.y, __uint_as_float(acc[e + 1]));
         if (last) {
-          store_out(a, x.z, jx, i + ih + 8 * k, v);
-          continue;
+          hw[e / 2] = pack_bf16(v0 * unscale, v1 * unscale);
+        } else {
+          hw[e / 2] = pack_half(v0, v1);
+          const float2 kept = unpack_half(hw[e / 2]);
+          lw[e / 2] = pack_half(v0 - kept.x, v1 - kept.y);
         }
-        uint32_t hw[4], rw[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          hw[q] = pack_half(v[2 * q], v[2 * q + 1]);
-          const float2 b = unpack_half(hw[q]);
-          rw[q] = pack_half(v[2 * q] - b.x, v[2 * q + 1] - b.y);
-        }
-        sts_v4(chunk_at(in.slot, 4 * h + k), make_uint4(hw[0], hw[1], hw[2], hw[3]));
-        sts_v4(chunk_at(in.slot + kPieceBytes, 4 * h + k), make_uint4(rw[0], rw[1], rw[2], rw[3]));
       }
     }
-    ptx::fence_proxy_async_shared();
+    if (last) {
+      __syncwarp();                  // the strip has been read
+      store_out(a, x.z, at.row, at.col + u * kStrip, hw, strip);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        sts_v4(strip_chunk_at(strip, k), make_uint4(hw[4 * k], hw[4 * k + 1], hw[4 * k + 2], hw[4 * k + 3]));
+        sts_v4(strip_chunk_at(strip + kStripBytes, k),
+               make_uint4(lw[4 * k], lw[4 * k + 1], lw[4 * k + 2], lw[4 * k + 3]));
+      }
+      ptx::fence_proxy_async_shared();
+    }
     __syncwarp();
     if (lane == 0) {
-      if (!last) {
-        ptx::tma_store_3d(&maps.xt_piece[cur ^ 1], i + u * kPiece, j0, x.z, in.slot);
-        ptx::tma_store_3d(&maps.xl_piece, i + u * kPiece, j0, x.z, in.slot + kPieceBytes);
-        ptx::bulk_commit();
+      if (u >= 1 && u + 1 < strips) {                 // into the half of the strip before this one
         ptx::bulk_wait_read();
+        request_strip(maps, step, x.z, at, u + 1, in.slot, in.bars);
       }
-      if (u + 1 < pieces) request_piece(maps, kUpdate, step, x.z, j0, i, u + 1, in.slot, in.bars);
+      if (!last) {
+        ptx::tma_store_3d(&maps.xt_strip[cur ^ 1], at.col + u * kStrip, at.row, x.z, strip);
+        ptx::tma_store_3d(&maps.xl_strip, at.col + u * kStrip, at.row, x.z, strip + kStripBytes);
+        ptx::bulk_commit();
+      }
     }
   }
   unit_done(a, kUpdate, x, in.units_done, !last);
@@ -688,15 +718,15 @@ __device__ __forceinline__ uint4 finish8(const OrthoArgs& a, int cur, float f, f
 // or below the diagonal.
 //
 // Where the inner dimension is split, each part's warp stores its sums, waits for the other
-// parts' and finishes its share of the columns, in eights, from all parts' sums, added in
-// their order.  (The units of such a phase are no more than the pairs, so the parts run at
+// parts' and finishes its share of the columns, in sixteens, from all parts' sums, added
+// in their order.  (The units of such a phase are no more than the pairs, so the parts run at
 // the same time.)
 template <int kPhase>
 __device__ __forceinline__ bool epilogue_square(const OrthoMaps& maps, const OrthoArgs& a, int step, const Unit& x,
-                                                int i0, int j, const Acc& in, uint32_t& parity) {
+                                                const Place& at, const Acc& in, uint32_t& parity) {
   const int lane = threadIdx.x % 32, cur = step & 1;
-  const int i = i0 + lane;
-  const int pieces = pieces_of(a, kPhase, i0, j);
+  const int i0 = at.row, j = at.col, i = i0 + lane;
+  const int pieces = pieces_of(a, kPhase, at, kPiece);
   const bool row = i < a.r;
   const long long diag_at = x.z * static_cast<long long>(a.ld) + i;
   if (!__all_sync(kAll, wait_bar(in.full, in.parity, in.abort))) return false;
@@ -732,23 +762,26 @@ __device__ __forceinline__ bool epilogue_square(const OrthoMaps& maps, const Ort
       for (int u = 0; u < pieces; ++u)
         if (!wait_piece(in, u, parity)) return false;
     __half* m = (kPhase == kGram ? a.a[cur] : a.b) + (static_cast<long long>(x.z) * a.r + i) * a.ld + j;
-    constexpr int kEights = kWarpCols / 8;
+    constexpr int kShares = kWarpCols / 16;
 #pragma unroll 1
-    for (int g = x.part * kEights / parts; g < (x.part + 1) * kEights / parts; ++g) {
-      const int jg = j + 8 * g;
-      if (jg >= a.r) break;
-      float v[8];
+    for (int g = x.part * kShares / parts; g < (x.part + 1) * kShares / parts; ++g) {
+      if (j + 16 * g >= a.r) break;
+      float v[2][8];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] = sums[(8 * g + q) * 32];
-#pragma unroll 4
+      for (int q = 0; q < 16; ++q) v[q / 8][q % 8] = sums[(16 * g + q) * 32];
+#pragma unroll 2
       for (int k = 1; k < parts; ++k) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] += sums[k * kPartStride + (8 * g + q) * 32];
+        for (int q = 0; q < 16; ++q) v[q / 8][q % 8] += sums[k * kPartStride + (16 * g + q) * 32];
       }
-      uint4 o = {};
-      if (kPhase == kPoly) o = lds_v4(chunk_at(in.slot + g / 8 * kPieceBytes, g % 8));
-      const uint4 w = finish8<kPhase>(a, cur, f, v, o, i - jg, rest_a, row ? diag_at : -1);
-      if (row) *reinterpret_cast<uint4*>(m + 8 * g) = w;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int col = 16 * g + 8 * e;
+        uint4 o = {};
+        if (kPhase == kPoly) o = lds_v4(chunk_at(in.slot + col / kPiece * kPieceBytes, col / 8 % 8));
+        const uint4 w = finish8<kPhase>(a, cur, f, v[e], o, i - (j + col), rest_a, row ? diag_at : -1);
+        if (row) *reinterpret_cast<uint4*>(m + col) = w;      // (the sixteen lie inside ld)
+      }
     }
     ptx::fence_proxy_async();        // these plain stores are read by tensor copies
     unit_done(a, kPhase, x, in.units_done, true);
@@ -767,13 +800,13 @@ __device__ __forceinline__ bool epilogue_square(const OrthoMaps& maps, const Ort
       if (u + 1 == pieces && h == 1) release_acc(in.empty);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const uint32_t at = chunk_at(slot, 4 * h + k);
+        const uint32_t chunk = chunk_at(slot, 4 * h + k);
         float v[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) v[q] = __uint_as_float(acc[8 * k + q]);
         uint4 o = {};
-        if (kPhase == kPoly) o = lds_v4(at);
-        sts_v4(at, finish8<kPhase>(a, cur, f, v, o, i - (j + u * kPiece + 32 * h + 8 * k), rest_a, row ? diag_at : -1));
+        if (kPhase == kPoly) o = lds_v4(chunk);
+        sts_v4(chunk, finish8<kPhase>(a, cur, f, v, o, i - (j + u * kPiece + 32 * h + 8 * k), rest_a, row ? diag_at : -1));
       }
     }
     ptx::fence_proxy_async_shared();
@@ -953,9 +986,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       if (phase != kGram && lane < kEpilogueWarps) {
         ptx::fence_proxy_async();    // the acquires above before the tensor copies
         const Place at = place_of(phase, x, rank, w);
-        const int pieces = pieces_of(a, phase, at.row, at.col);
-        for (int u = 0; u < pieces && (phase == kPoly || u == 0); ++u)
-          request_piece(maps, phase, step, x.z, at.row, at.col, u, slots + w * kSlotBytes, sm.piece[w]);
+        const int n = min(pieces_of(a, phase, at, phase == kPoly ? kPiece : kStrip), 2);
+        for (int u = 0; u < n; ++u) {
+          if (phase == kPoly) request_piece(maps, step, x.z, at, u, slots + w * kSlotBytes, sm.piece[w]);
+          else request_strip(maps, step, x.z, at, u, slots + w * kSlotBytes, sm.piece[w]);
+        }
       }
       __syncwarp();
       return true;
@@ -971,9 +1006,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                    &sm.units_done[index]};
       const Place at = place_of(phase, x, rank, index);
       next_acc();
-      return phase == kGram ? epilogue_square<kGram>(maps, a, step, x, at.row, at.col, in, parity)
-             : phase == kPoly ? epilogue_square<kPoly>(maps, a, step, x, at.row, at.col, in, parity)
-                              : epilogue_update(maps, a, step, x, at.row, at.col, in, parity);
+      return phase == kGram ? epilogue_square<kGram>(maps, a, step, x, at, in, parity)
+             : phase == kPoly ? epilogue_square<kPoly>(maps, a, step, x, at, in, parity)
+                              : epilogue_update(maps, a, step, x, at, in, parity);
     });
     if (lane == 0) ptx::bulk_wait();
   }
@@ -1003,14 +1038,14 @@ using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
 EncodeTiled g_encode = nullptr;
 int g_pairs[64] = {};                // per device: pairs resident at once
 
-// [batch][outer][ld] fp16 with r columns used, in swizzled boxes of 64 x box_rows.
-cudaError_t encode(CUtensorMap* map, void* p, const OrthoShape& sh, int64_t outer, int box_rows) {
+// [batch][outer][ld] fp16 with r columns used, in boxes of box_cols x box_rows, swizzled by their rows' bytes.
+cudaError_t encode(CUtensorMap* map, void* p, const OrthoShape& sh, int64_t outer, int box_cols, int box_rows) {
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(sh.r), static_cast<cuuint64_t>(outer),
                               static_cast<cuuint64_t>(sh.batch)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(sh.ld * 2), static_cast<cuuint64_t>(sh.ld * outer * 2)};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1}, step[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1}, step[3] = {1, 1, 1};
   const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, p, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                              box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
@@ -1074,18 +1109,18 @@ cudaError_t launch_orthogonalize(const OrthoCall& q, cudaStream_t stream) {
 
   OrthoMaps maps;
   cudaError_t e = cudaSuccess;
-  auto add = [&](CUtensorMap* map, size_t at, int64_t outer, int box_rows) {
-    if (e == cudaSuccess) e = encode(map, ws + at, sh, outer, box_rows);
+  auto add = [&](CUtensorMap* map, size_t at, int64_t outer, int box_cols, int box_rows) {
+    if (e == cudaSuccess) e = encode(map, ws + at, sh, outer, box_cols, box_rows);
   };
   for (int i = 0; i < 2; ++i) {
-    add(&maps.xt[i], L.xt[i], sh.c, 64);
-    add(&maps.xt_piece[i], L.xt[i], sh.c, 32);
-    add(&maps.a[i], L.a[i], sh.r, 64);
-    add(&maps.a_piece[i], L.a[i], sh.r, 32);
+    add(&maps.xt[i], L.xt[i], sh.c, 64, 64);
+    add(&maps.xt_strip[i], L.xt[i], sh.c, kStrip, 32);
+    add(&maps.a[i], L.a[i], sh.r, 64, 64);
+    add(&maps.a_piece[i], L.a[i], sh.r, kPiece, 32);
   }
-  add(&maps.xl_piece, L.xl, sh.c, 32);
-  add(&maps.b, L.b, sh.r, 64);
-  add(&maps.b_piece, L.b, sh.r, 32);
+  add(&maps.xl_strip, L.xl, sh.c, kStrip, 32);
+  add(&maps.b, L.b, sh.r, 64, 64);
+  add(&maps.b_piece, L.b, sh.r, kPiece, 32);
   if (e != cudaSuccess) return e;
 
   OrthoArgs a{};
