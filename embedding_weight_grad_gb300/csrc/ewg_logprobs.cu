@@ -25,6 +25,7 @@
 #include "ewg.h"
 #include "ewg_internal.cuh"
 #include "ewg_ops.cuh"
+#include "ewg_ptx.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -49,30 +50,6 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   float y;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
   return y;
-}
-
-// Two 32-bit operations in one instruction.
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("{.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-      "add.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;}"
-      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-      "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;}"
-      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-      "mov.b64 w, {%6, %7};\n\tfma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
 }
 
 // 16 bytes of a row of T: kE elements.
@@ -274,11 +251,13 @@ struct GroupSmem {
 // same way the vectors of the thread that holds the maximum are summed again without it
 // where its own term would drown the others (R < 8).
 //
-// 1536 threads on an SM (40 registers each): with 1280 or 2048 the large rows lose 4 to 8 %.
+// 1536 threads on an SM (40 registers each), 2048 for bf16 rows of 512 threads.
 constexpr int threads_of(int kT) { return kT == 32 ? 256 : kT; }
+template <typename T>
+constexpr int blocks_per_sm(int kT) { return (sizeof(T) == 2 && kT == 512 ? 2048 : 1536) / threads_of(kT); }
 
 template <typename T, int kT>
-__global__ void __launch_bounds__(threads_of(kT), 1536 / threads_of(kT)) logprobs_kernel(const LogprobsArgs a) {
+__global__ void __launch_bounds__(threads_of(kT), blocks_per_sm<T>(kT)) logprobs_kernel(const LogprobsArgs a) {
   using V = Vec<T>;
   constexpr int kE = V::kE;
   constexpr int kGroups = kT == 32 ? 8 : 1;
@@ -360,19 +339,19 @@ __global__ void __launch_bounds__(threads_of(kT), 1536 / threads_of(kT)) logprob
     const float d = fmaxf((m - m_new) * c, -1000.0f);
     const float f = ex2(d);
     m = m_new;
-    T2 = mul2(make_float2(f, f), fma2(make_float2(d, d), S2, T2));
-    S2 = mul2(make_float2(f, f), S2);
+    T2 = ptx::mul2(make_float2(f, f), ptx::fma2(make_float2(d, d), S2, T2));
+    S2 = ptx::mul2(make_float2(f, f), S2);
     const float2 minus_m = make_float2(-m, -m);
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
 #pragma unroll
       for (int i = 0; i < kE / 2; ++i) {
-        float2 t = mul2(add2(V::pair(r[u], i), minus_m), c2);
+        float2 t = ptx::mul2(ptx::add2(V::pair(r[u], i), minus_m), c2);
         t.x = max_nan(t.x, kLowestExponent);
         t.y = max_nan(t.y, kLowestExponent);
         const float2 e = make_float2(ex2(t.x), ex2(t.y));
-        S2 = add2(S2, e);
-        T2 = fma2(e, t, T2);
+        S2 = ptx::add2(S2, e);
+        T2 = ptx::fma2(e, t, T2);
       }
     }
   }
@@ -711,10 +690,10 @@ __global__ void __launch_bounds__(256, 6) logprobs_grad_kernel(const LogprobsGra
     float2 out[kE / 2];
 #pragma unroll
     for (int i = 0; i < kE / 2; ++i) {
-      float2 y = fma2(add2(V::pair(r[u], i), minus_m), c2, ls2);
+      float2 y = ptx::fma2(ptx::add2(V::pair(r[u], i), minus_m), c2, ls2);
       y.x = max_nan(y.x, kLowestExponent);
       y.y = max_nan(y.y, kLowestExponent);
-      out[i] = mul2(make_float2(ex2(y.x), ex2(y.y)), fma2(B2, y, A2));
+      out[i] = ptx::mul2(make_float2(ex2(y.x), ex2(y.y)), ptx::fma2(B2, y, A2));
     }
     const long long e = target - head - static_cast<long long>(v) * kE;
     if (e >= 0 && e < kE) {          // the vector that holds the token

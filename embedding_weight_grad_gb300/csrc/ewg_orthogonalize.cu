@@ -95,20 +95,22 @@ __device__ __forceinline__ double sum_of_squares(const float (&g)[kLaneElems]) {
   for (int i = 0; i < kLaneElems; ++i) m = fmaxf(m, fabsf(g[i]));
   const int e = min(static_cast<int>(__float_as_uint(m) >> 23), 253);
   const float scale = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);          // 2^(127 - e)
-  float sum = 0.0f, err = 0.0f;
+  float2 sum = make_float2(0.0f, 0.0f), err = sum;
+  const float2 by = make_float2(scale, scale);
 #pragma unroll
-  for (int i = 0; i < kLaneElems; ++i) {
-    const float x = __fmul_rn(g[i], scale);
-    const float p = __fmul_rn(x, x);
-    const float t = __fadd_rn(sum, p);
-    const float b = __fsub_rn(t, sum);
-    const float lost = __fadd_rn(__fsub_rn(sum, __fsub_rn(t, b)), __fsub_rn(p, b));
-    err = __fadd_rn(err, __fadd_rn(lost, __fmaf_rn(x, x, -p)));
+  for (int i = 0; i < kLaneElems; i += 2) {           // two at a time
+    const float2 x = ptx::mul2(make_float2(g[i], g[i + 1]), by);
+    const float2 p = ptx::mul2(x, x);
+    const float2 t = ptx::add2(sum, p);
+    const float2 b = ptx::sub2(t, sum);
+    const float2 lost = ptx::add2(ptx::sub2(sum, ptx::sub2(t, b)), ptx::sub2(p, b));
+    err = ptx::add2(err, ptx::add2(lost, ptx::fma2(x, x, make_float2(-p.x, -p.y))));
     sum = t;
   }
   const double back = __longlong_as_double(static_cast<long long>(1023 + 2 * (e - 127)) << 52);
+  const double all = static_cast<double>(sum.x) + static_cast<double>(sum.y);
   // (an infinite or NaN sum has no error term)
-  return (static_cast<double>(sum) + (isfinite(sum) ? static_cast<double>(err) : 0.0)) * back;
+  return (all + (isfinite(all) ? static_cast<double>(err.x) + static_cast<double>(err.y) : 0.0)) * back;
 }
 
 // Sums of squares of one matrix per blockIdx.y, a warp to 1024 neighbouring elements of a row
@@ -391,10 +393,11 @@ __device__ __forceinline__ void inner_of(const OrthoArgs& a, int phase, const Un
   last = min(first + per, blocks);
 }
 
-// ---- what a unit waits for.  ready[phase][z][I] counts the epilogue warps (8 a unit) that
+// ---- what a unit waits for.  ready[phase][z][I] counts the epilogue warps (16 a unit) that
 // have stored their part of block row I of X, A or B, over all steps.  (Nothing else is
 // needed: a complete row of B needs all of A, which needs all of X of the step before, so
-// that no buffer is written while an earlier phase still reads it, with two A in turn.)
+// that no buffer is written while an earlier phase still reads it, with two A in turn.)  What
+// other SMs stored plainly is read past L1.
 
 __device__ __forceinline__ int* ready_at(const OrthoArgs& a, int phase, int z, int I) {
   const int nr = blocks_of(a.r);
@@ -614,7 +617,7 @@ __device__ __forceinline__ bool epilogue_update(const OrthoMaps& maps, const Ort
 #pragma unroll
   for (int q = 0; q < kStrips; ++q) {
     const int col = at.col + 32 * q + lane;
-    rest[q] = col < a.r ? a.diag_b[x.z * static_cast<long long>(a.ld) + col] : 0.0f;
+    rest[q] = col < a.r ? __ldcg(a.diag_b + x.z * static_cast<long long>(a.ld) + col) : 0.0f;
   }
   const float unscale = 1.0f / a.s;
 #pragma unroll 1
@@ -732,7 +735,7 @@ __device__ __forceinline__ bool epilogue_square(const OrthoMaps& maps, const Ort
   if (!__all_sync(kAll, wait_bar(in.full, in.parity, in.abort))) return false;
   ptx::tmem_fence_after();
   float rest_a = 0.0f;               // what rounding left of A_ii
-  if (kPhase == kPoly && row) rest_a = a.diag_a[cur][diag_at];
+  if (kPhase == kPoly && row) rest_a = __ldcg(a.diag_a[cur] + diag_at);
   const int parts = a.split[kPhase];
   const float f = kPhase == kGram ? 1.0f / (a.s * a.s) : a.cc;
   if (parts > 1) {
@@ -768,11 +771,11 @@ __device__ __forceinline__ bool epilogue_square(const OrthoMaps& maps, const Ort
       if (j + 16 * g >= a.r) break;
       float v[2][8];
 #pragma unroll
-      for (int q = 0; q < 16; ++q) v[q / 8][q % 8] = sums[(16 * g + q) * 32];
+      for (int q = 0; q < 16; ++q) v[q / 8][q % 8] = __ldcg(sums + (16 * g + q) * 32);
 #pragma unroll 2
       for (int k = 1; k < parts; ++k) {
 #pragma unroll
-        for (int q = 0; q < 16; ++q) v[q / 8][q % 8] += sums[k * kPartStride + (16 * g + q) * 32];
+        for (int q = 0; q < 16; ++q) v[q / 8][q % 8] += __ldcg(sums + k * kPartStride + (16 * g + q) * 32);
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
