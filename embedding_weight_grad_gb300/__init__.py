@@ -6,6 +6,11 @@ that occur, with the values of PyTorch's sort-based embedding backward followed 
 ``main_grad.add_`` (Megatron Core API docs, ``core.fusions.fused_embedding_wgrad``:
 module docstring, ``accumulate_embedding_wgrad`` and ``can_accumulate_embedding_wgrad``).
 
+Beside it, the other operators of a training step that deal with the vocabulary and with
+main_grads: ``token_logprobs`` and ``token_logprobs_backward`` (log probabilities of given
+tokens, entropies and the most likely alternatives from logits, and their gradient) and
+``orthogonalize_update`` (the Newton-Schulz orthogonalisation of the Muon optimiser).
+
 This module only marshals arguments into the C ABI of ``libewg.so`` (declared in
 ``include/ewg.h``); every step of the computation runs in that library's CUDA
 kernels.  PyTorch supplies device memory and the current stream.  There is no CPU

@@ -1,5 +1,8 @@
 /*
- * ewg.h -- C ABI of the GB300 sparse embedding weight-gradient library.
+ * ewg.h -- C ABI of the GB300 sparse embedding weight-gradient library, and of two
+ * operators that a training step has beside it: token log probabilities with their
+ * gradient (ewg_token_logprobs, the vocabulary's other end) and the orthogonalised update of
+ * a matrix (ewg_orthogonalize).
  *
  * The operation (Megatron Core API docs, core.fusions.fused_embedding_wgrad,
  * entry accumulate_embedding_wgrad, and the module docstring):
@@ -339,8 +342,9 @@ size_t ewg_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t co
  *     A = X X^T        X <- a X + (b A + c A^2) X
  *
  * The result is rounded to bf16.  The products take fp16 operands with fp32 accumulation;
- * X and the diagonals of A and of b A + c A^2 stay in fp32, which keeps the result within
- * about 1e-3 of the exact steps in norm, beside its own rounding, for low-rank updates too.
+ * X is kept to 22 bits beside its fp16 numbers, and the diagonals of A and of b A + c A^2
+ * exactly to first order.  With the coefficients below the result is within 2.5e-3 of the
+ * exact steps in norm, of which its own rounding to bf16 is 1.7e-3; low-rank updates included.
  * The norm is summed in 64 bits, so the scale of G does not matter; a zero matrix stays
  * zero, a NaN or an infinity makes its matrix NaN.  Results are deterministic.
  *
