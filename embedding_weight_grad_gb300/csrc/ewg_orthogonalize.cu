@@ -293,8 +293,9 @@ constexpr int kStripBytes = 32 * kStrip * 2;          // of one part of X
 constexpr int kSlotBytes = 2 * kPieceBytes;
 static_assert(kSlotBytes == 4 * kStripBytes, "a slot holds two strips of both parts");
 constexpr int kGemmThreads = 32 * (kFirstEpilogueWarp + kEpilogueWarps);
+constexpr int kOwnBytes = kBlock * 4;                 // a + what is left of B_ii for a unit's columns
 constexpr size_t kGemmSmem =
-    static_cast<size_t>(kStages) * kStageBytes + kEpilogueWarps * kSlotBytes + 1024;
+    static_cast<size_t>(kStages) * kStageBytes + kEpilogueWarps * kSlotBytes + kOwnBytes + 1024;
 static_assert(kWarpCols == 128 && kPieces == 2, "a warp's columns, as the epilogue takes them");
 static_assert(kWarpsOfBlock == kOrthoWarps && kBlock == kOrthoBlock, "as the workspace is laid out for");
 static_assert(kGemmSmem + 512 <= 227 * 1024, "stages and slots fit in shared memory");
@@ -330,7 +331,7 @@ struct OrthoArgs {
 
 struct GemmSmem {
   uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
-  uint64_t piece[kEpilogueWarps][2];
+  uint64_t piece[kEpilogueWarps][2], own_full;
   int units_done[kEpilogueWarps];    // units an epilogue warp is through with its slot for
   uint32_t tmem;
   int abort;
@@ -501,6 +502,8 @@ struct Acc {
   uint32_t slot;                     // shared-memory address
   uint64_t* bars;                    // of the slot's halves: its copies have come
   volatile int* units_done;          // of the warp
+  uint32_t own;                      // shared-memory address: a + what is left of B_ii, of the warp's columns
+  uint64_t* own_full;
 };
 
 // The first row and column of epilogue warp w's part of a unit (it takes the 32 rows of its
@@ -538,6 +541,11 @@ __device__ __forceinline__ void request_strip(const OrthoMaps& maps, int step, i
 __device__ __forceinline__ uint4 lds_v4(uint32_t at) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ float2 lds_f2(uint32_t at) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at));
   return v;
 }
 __device__ __forceinline__ void sts_v4(uint32_t at, uint4 v) {
@@ -613,12 +621,9 @@ __device__ __forceinline__ bool epilogue_update(const OrthoMaps& maps, const Ort
   if (!__all_sync(kAll, wait_bar(in.full, in.parity, in.abort))) return false;
   ptx::tmem_fence_after();
   if (strips == 0) release_acc(in.empty);
-  float rest[kStrips];               // what is left of B_ii, of column 32 q + lane
-#pragma unroll
-  for (int q = 0; q < kStrips; ++q) {
-    const int col = at.col + 32 * q + lane;
-    rest[q] = col < a.r ? __ldcg(a.diag_b + x.z * static_cast<long long>(a.ld) + col) : 0.0f;
-  }
+  // (bit 2 of `parity`: of the next wait on own_full)
+  if (!__all_sync(kAll, wait_bar(in.own_full, (parity >> 2) & 1u, in.abort))) return false;
+  parity ^= 4u;
   const float unscale = 1.0f / a.s;
 #pragma unroll 1
   for (int u = 0; u < strips; ++u) {
@@ -632,7 +637,6 @@ __device__ __forceinline__ bool epilogue_update(const OrthoMaps& maps, const Ort
       top[k] = lds_v4(strip_chunk_at(strip, k));
       low[k] = lds_v4(strip_chunk_at(strip + kStripBytes, k));
     }
-    const float own = a.ca + (u < 2 ? (u == 0 ? rest[0] : rest[1]) : (u == 2 ? rest[2] : rest[3]));
     ptx::tmem_wait_load();
     if (u + 1 == strips) release_acc(in.empty);
     uint32_t hw[16], lw[16];
@@ -641,17 +645,16 @@ __device__ __forceinline__ bool epilogue_update(const OrthoMaps& maps, const Ort
       const uint32_t tk[4] = {top[k].x, top[k].y, top[k].z, top[k].w};
       const uint32_t lk[4] = {low[k].x, low[k].y, low[k].z, low[k].w};
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float2 b = unpack_half(tk[q]), r = unpack_half(lk[q]);
+      for (int q = 0; q < 4; ++q) {  // two columns at a time
         const int e = 8 * k + 2 * q;
-        const float v0 = fmaf(__shfl_sync(kAll, own, e), b.x + r.x, __uint_as_float(acc[e]));
-        const float v1 = fmaf(__shfl_sync(kAll, own, e + 1), b.y + r.y, __uint_as_float(acc[e + 1]));
+        const float2 v = ptx::fma2(lds_f2(in.own + (u * kStrip + e) * 4), ptx::add2(unpack_half(tk[q]), unpack_half(lk[q])),
+                                   make_float2(__uint_as_float(acc[e]), __uint_as_float(acc[e + 1])));
         if (last) {
-          hw[e / 2] = pack_bf16(v0 * unscale, v1 * unscale);
+          hw[e / 2] = pack_bf16(v.x * unscale, v.y * unscale);
         } else {
-          hw[e / 2] = pack_half(v0, v1);
-          const float2 kept = unpack_half(hw[e / 2]);
-          lw[e / 2] = pack_half(v0 - kept.x, v1 - kept.y);
+          hw[e / 2] = pack_half(v.x, v.y);
+          const float2 left = ptx::sub2(v, unpack_half(hw[e / 2]));
+          lw[e / 2] = pack_half(left.x, left.y);
         }
       }
     }
@@ -862,6 +865,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     }
     ptx::mbar_init(&sm.drained, 1);
     for (int i = 0; i < 2 * kEpilogueWarps; ++i) ptx::mbar_init(&sm.piece[0][0] + i, 1);
+    ptx::mbar_init(&sm.own_full, 1);
     for (int i = 0; i < kEpilogueWarps; ++i) sm.units_done[i] = 0;
     sm.abort = 0;
     ptx::fence_mbar_init();
@@ -879,6 +883,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   const uint32_t tmem = sm.tmem;
   volatile int* abort = &sm.abort;
   const uint32_t slots = stages + kStages * kStageBytes;     // of the epilogue warps
+  const uint32_t own = slots + kEpilogueWarps * kSlotBytes;
 
   uint32_t stage = 0, stage_phase = 0;      // producer's or issuer's place in the ring
   uint32_t acc = 0, acc_phase = 0;          // issuer's or epilogue's accumulator
@@ -986,6 +991,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       bool ok = phase == kGram || lane != 0 || wait_inputs(a, phase, step, x, abort);
       ok = ok && wait_count(&sm.units_done[w], units++, abort);
       if (!__all_sync(kAll, ok)) return false;
+      if (phase == kUpdate) {        // a + what is left of B_ii: eight columns a lane
+        const int col = x.I * kBlock + 8 * lane;
+        if (col < a.r) {             // (then the eight lie inside ld)
+          const float4* d = reinterpret_cast<const float4*>(a.diag_b + x.z * static_cast<long long>(a.ld) + col);
+          const float4 d0 = __ldcg(d), d1 = __ldcg(d + 1);
+          float4* to = reinterpret_cast<float4*>(raw + (own - ptx::smem_u32(raw))) + 2 * lane;
+          to[0] = make_float4(a.ca + d0.x, a.ca + d0.y, a.ca + d0.z, a.ca + d0.w);
+          to[1] = make_float4(a.ca + d1.x, a.ca + d1.y, a.ca + d1.z, a.ca + d1.w);
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sm.own_full);
+      }
       if (phase != kGram && lane < kEpilogueWarps) {
         ptx::fence_proxy_async();    // the acquires above before the tensor copies
         const Place at = place_of(phase, x, rank, w);
@@ -1006,7 +1023,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       const Acc in{tmem + acc * kBlock + part * kWarpCols + (static_cast<uint32_t>(quarter) << 21),
                    &sm.acc_full[acc], acc_phase, ptx::map_to_rank(ptx::smem_u32(&sm.acc_empty[acc]), 0), abort,
                    static_cast<int>(rank) * kEpilogueWarps + index, slots + index * kSlotBytes, sm.piece[index],
-                   &sm.units_done[index]};
+                   &sm.units_done[index], own + part * kWarpCols * 4, &sm.own_full};
       const Place at = place_of(phase, x, rank, index);
       next_acc();
       return phase == kGram ? epilogue_square<kGram>(maps, a, step, x, at, in, parity)
