@@ -288,10 +288,15 @@ constexpr int kPiece = 64;
 constexpr int kPieces = kWarpCols / kPiece;
 constexpr int kPieceBytes = 32 * kPiece * 2;
 constexpr int kStrip = 32;
-constexpr int kStrips = kWarpCols / kStrip;
 constexpr int kStripBytes = 32 * kStrip * 2;          // of one part of X
 constexpr int kSlotBytes = 2 * kPieceBytes;
 static_assert(kSlotBytes == 4 * kStripBytes, "a slot holds two strips of both parts");
+// The halves of the slots lie so that the epilogue's 128 x 256 numbers of A form an operand of the
+// tensor cores, 128 rows of 128 bytes for each 64 columns: half h of warp w (rows 32 (w % 4),
+// columns 128 (w / 4) + 64 h) comes 4 (2 (w / 4) + h) + w % 4 pieces in.
+constexpr int kHalfStride = 4 * kPieceBytes;          // between a warp's halves
+static_assert(kHalfStride == kOperandBytes, "64 columns of the CTA's rows");
+__host__ __device__ constexpr int slot_offset(int w) { return (8 * (w / 4) + w % 4) * kPieceBytes; }
 constexpr int kGemmThreads = 32 * (kFirstEpilogueWarp + kEpilogueWarps);
 constexpr int kOwnBytes = kBlock * 4;                 // a + what is left of B_ii for a unit's columns
 constexpr size_t kGemmSmem =
@@ -319,6 +324,7 @@ struct OrthoArgs {
   __half* b;
   float* diag_a[2];                  // [batch][ld]: what rounding left of the diagonals
   float* diag_b;
+  int fused;                         // matrices of one block: A stays with the pair that computed it
   int split[2];                      // parts of the inner dimension of X X^T and A A
   float* partial;                    // split products: [batch][block][part][CTA][warp][column][row]
   __nv_bfloat16* out;
@@ -331,7 +337,7 @@ struct OrthoArgs {
 
 struct GemmSmem {
   uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
-  uint64_t piece[kEpilogueWarps][2], own_full;
+  uint64_t piece[kEpilogueWarps][2], own_full, a_full;
   int units_done[kEpilogueWarps];    // units an epilogue warp is through with its slot for
   uint32_t tmem;
   int abort;
@@ -427,6 +433,7 @@ __device__ bool wait_inputs(const OrthoArgs& a, int phase, int step, const Unit&
            (x.I == x.J || wait_ready(a, ready_at(a, kUpdate, x.z, x.J), want, abort));
   }
   const int want = (step + 1) * nr * kWarpsOfBlock * a.split[phase == kPoly ? kGram : kPoly];
+  if (phase == kPoly && a.fused) return true;
   if (phase == kPoly)
     return wait_ready(a, ready_at(a, kGram, x.z, x.I), want, abort) &&
            (x.I == x.J || wait_ready(a, ready_at(a, kGram, x.z, x.J), want, abort));
@@ -504,6 +511,7 @@ struct Acc {
   volatile int* units_done;          // of the warp
   uint32_t own;                      // shared-memory address: a + what is left of B_ii, of the warp's columns
   uint64_t* own_full;
+  uint32_t a_full;                   // shared::cluster address
 };
 
 // The first row and column of epilogue warp w's part of a unit (it takes the 32 rows of its
@@ -528,11 +536,11 @@ __device__ __forceinline__ int pieces_of(const OrthoArgs& a, int phase, const Pl
 __device__ __forceinline__ void request_piece(const OrthoMaps& maps, int step, int z, const Place& at, int u,
                                               uint32_t slot, uint64_t* bars) {
   ptx::mbar_arrive_expect_tx(&bars[u], kPieceBytes);
-  ptx::tma_load_3d(slot + u * kPieceBytes, &maps.a_piece[step & 1], at.col + u * kPiece, at.row, z, &bars[u]);
+  ptx::tma_load_3d(slot + u * kHalfStride, &maps.a_piece[step & 1], at.col + u * kPiece, at.row, z, &bars[u]);
 }
 __device__ __forceinline__ void request_strip(const OrthoMaps& maps, int step, int z, const Place& at, int u,
                                               uint32_t slot, uint64_t* bars) {
-  const uint32_t to = slot + u % 2 * (2 * kStripBytes);
+  const uint32_t to = slot + u % 2 * kHalfStride;
   ptx::mbar_arrive_expect_tx(&bars[u % 2], 2 * kStripBytes);
   ptx::tma_load_3d(to, &maps.xt_strip[step & 1], at.col + u * kStrip, at.row, z, &bars[u % 2]);
   ptx::tma_load_3d(to + kStripBytes, &maps.xl_strip, at.col + u * kStrip, at.row, z, &bars[u % 2]);
@@ -627,7 +635,7 @@ __device__ __forceinline__ bool epilogue_update(const OrthoMaps& maps, const Ort
   const float unscale = 1.0f / a.s;
 #pragma unroll 1
   for (int u = 0; u < strips; ++u) {
-    const uint32_t strip = in.slot + u % 2 * (2 * kStripBytes);
+    const uint32_t strip = in.slot + u % 2 * kHalfStride;
     uint32_t acc[kStrip];
     ptx::tmem_load32(acc, in.from + u * kStrip);
     if (!wait_piece(in, u % 2, parity)) return false;
@@ -723,6 +731,9 @@ __device__ __forceinline__ uint4 finish8(const OrthoArgs& a, int cur, float f, f
 // The same for A = X X^T or B = b A + c A^2: 32 rows from i0, kWarpCols columns from j of a block on
 // or below the diagonal.
 //
+// Matrices of one block (a.fused): A is left in the slots, which form an operand, and the
+// same pair goes on to B.
+//
 // Where the inner dimension is split, each part's warp stores its sums, waits for the other
 // parts' and finishes its share of the columns, in sixteens, from all parts' sums, added
 // in their order.  (The units of such a phase are no more than the pairs, so the parts run at
@@ -784,7 +795,7 @@ __device__ __forceinline__ bool epilogue_square(const OrthoMaps& maps, const Ort
       for (int e = 0; e < 2; ++e) {
         const int col = 16 * g + 8 * e;
         uint4 o = {};
-        if (kPhase == kPoly) o = lds_v4(chunk_at(in.slot + col / kPiece * kPieceBytes, col / 8 % 8));
+        if (kPhase == kPoly) o = lds_v4(chunk_at(in.slot + col / kPiece * kHalfStride, col / 8 % 8));
         const uint4 w = finish8<kPhase>(a, cur, f, v[e], o, i - (j + col), rest_a, row ? diag_at : -1);
         if (row) *reinterpret_cast<uint4*>(m + col) = w;      // (the sixteen lie inside ld)
       }
@@ -796,8 +807,8 @@ __device__ __forceinline__ bool epilogue_square(const OrthoMaps& maps, const Ort
   if (pieces == 0) release_acc(in.empty);
 #pragma unroll 1
   for (int u = 0; u < pieces; ++u) {
-    const uint32_t slot = in.slot + u * kPieceBytes;
-    if (kPhase == kPoly && !wait_piece(in, u, parity)) return false;
+    const uint32_t slot = in.slot + u * kHalfStride;
+    if (kPhase == kPoly && !a.fused && !wait_piece(in, u, parity)) return false;
 #pragma unroll 1
     for (int h = 0; h < 2; ++h) {    // 32 columns at a time
       uint32_t acc[32];
@@ -816,13 +827,19 @@ __device__ __forceinline__ bool epilogue_square(const OrthoMaps& maps, const Ort
       }
     }
     ptx::fence_proxy_async_shared();
+    if (kPhase == kGram && a.fused) continue;         // A stays
     __syncwarp();
     if (lane == 0) {
       ptx::tma_store_3d(kPhase == kGram ? &maps.a_piece[cur] : &maps.b_piece, j + u * kPiece, i0, x.z, slot);
       ptx::bulk_commit();
     }
   }
-  unit_done(a, kPhase, x, in.units_done, true);
+  const bool stays = kPhase == kGram && a.fused;
+  if (stays) {
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive_release_cluster(in.a_full);
+  }
+  unit_done(a, kPhase, x, in.units_done, !stays);
   return true;
 }
 
@@ -836,6 +853,11 @@ __device__ __forceinline__ Majors majors_of(int phase, const Unit& x, int kb) {
   if (phase == kGram) return {true, true};
   if (phase == kPoly) return {k > x.I, k > x.J};
   return {false, k > x.I};
+}
+
+// The products' instruction descriptor: fp32 accumulator, fp16 operands, 256 x 256.
+__device__ __forceinline__ uint32_t idesc_of(Majors mn) {
+  return 1u << 4 | (mn.a ? 1u << 15 : 0u) | (mn.b ? 1u << 16 : 0u) | (kBlock >> 3) << 17 | (kBlock >> 4) << 24;
 }
 
 // All phases of all steps, one cooperative launch of CTA pairs.  The units of all phases in
@@ -866,6 +888,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     ptx::mbar_init(&sm.drained, 1);
     for (int i = 0; i < 2 * kEpilogueWarps; ++i) ptx::mbar_init(&sm.piece[0][0] + i, 1);
     ptx::mbar_init(&sm.own_full, 1);
+    ptx::mbar_init(&sm.a_full, kWarpsOfBlock);
     for (int i = 0; i < kEpilogueWarps; ++i) sm.units_done[i] = 0;
     sm.abort = 0;
     ptx::fence_mbar_init();
@@ -905,9 +928,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     for (int p = 0; p < 3 * a.steps; ++p) {
       const int phase = p % 3, step = p / 3;
       const int units = units_of(a, phase);
+      if (a.fused && phase == kPoly) continue;        // with the phase before
       for (int t = pair >= offset ? pair - offset : pair - offset + pairs; t < units; t += pairs) {
         if (*abort) return;
-        if (!body(phase, step, unit_at(a, phase, t))) {
+        if (!body(phase, step, unit_at(a, phase, t)) ||
+            (a.fused && phase == kGram && !body(kPoly, step, unit_at(a, kPoly, t)))) {
           gave_up(a, abort);
           return;
         }
@@ -916,9 +941,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     }
   };
 
+  uint32_t a_parity = 0;             // issuer's, of a_full
+
   if (warp == 0) {
     if (lane == 0) {
       for_units([&](int phase, int step, const Unit& x) {
+        if (a.fused && phase == kPoly) return true;   // its operands are there
         const int cur = step & 1;
         // X X^T: X, X.  A A: A, A.  Update: X^T (rows J), B (rows I).
         const CUtensorMap* ma = phase == kPoly ? &maps.a[cur] : &maps.xt[cur];
@@ -956,14 +984,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         if (!wait_bar(&sm.acc_empty[acc], acc_phase ^ 1u, abort)) return false;
         ptx::tmem_fence_after();
         const uint32_t d = tmem + acc * kBlock;
+        if (a.fused && phase == kPoly) {              // A as the epilogue left it, both operands
+          if (!wait_bar(&sm.a_full, a_parity, abort)) return false;
+          a_parity ^= 1u;
+          ptx::tmem_fence_after();
+          for (int kb = k0; kb < k1; ++kb) {
+            const uint32_t at = slots + kb * kOperandBytes;
+#pragma unroll
+            for (int k = 0; k < kStepK / 16; ++k) {
+              const uint64_t desc = operand_desc(at + k * 32, 16, 1024);
+              ptx::mma_f16_pair(d, desc, desc, idesc_of({false, false}), kb > k0 || k > 0);
+            }
+          }
+          ptx::mma_commit_pair(&sm.acc_full[acc]);
+          next_acc();
+          return true;
+        }
         for (int kb = k0; kb < k1; ++kb) {
           if (!wait_bar(&sm.full[stage], stage_phase, abort)) return false;
           ptx::tmem_fence_after();
           const uint32_t at = stages + stage * kStageBytes;
           const Majors mn = majors_of(phase, x, kb);
-          // fp32 accumulator, fp16 operands, 256 x 256
-          const uint32_t idesc = 1u << 4 | (mn.a ? 1u << 15 : 0u) | (mn.b ? 1u << 16 : 0u) | (kBlock >> 3) << 17 |
-                                 (kBlock >> 4) << 24;
+          const uint32_t idesc = idesc_of(mn);
           // K-major: 8-row groups 1024 bytes apart, 16 inner elements = 32 bytes.  MN-major:
           // groups of 64 rows a box apart, groups of 8 inner elements 1024 bytes apart.
           const uint32_t lead_a = mn.a ? kBoxBytes : 16, lead_b = mn.b ? kBoxBytes : 16;
@@ -1003,13 +1045,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&sm.own_full);
       }
-      if (phase != kGram && lane < kEpilogueWarps) {
+      if (phase != kGram && !(a.fused && phase == kPoly) && lane < kEpilogueWarps) {
         ptx::fence_proxy_async();    // the acquires above before the tensor copies
         const Place at = place_of(phase, x, rank, w);
         const int n = min(pieces_of(a, phase, at, phase == kPoly ? kPiece : kStrip), 2);
         for (int u = 0; u < n; ++u) {
-          if (phase == kPoly) request_piece(maps, step, x.z, at, u, slots + w * kSlotBytes, sm.piece[w]);
-          else request_strip(maps, step, x.z, at, u, slots + w * kSlotBytes, sm.piece[w]);
+          if (phase == kPoly) request_piece(maps, step, x.z, at, u, slots + slot_offset(w), sm.piece[w]);
+          else request_strip(maps, step, x.z, at, u, slots + slot_offset(w), sm.piece[w]);
         }
       }
       __syncwarp();
@@ -1022,8 +1064,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     for_units([&](int phase, int step, const Unit& x) {
       const Acc in{tmem + acc * kBlock + part * kWarpCols + (static_cast<uint32_t>(quarter) << 21),
                    &sm.acc_full[acc], acc_phase, ptx::map_to_rank(ptx::smem_u32(&sm.acc_empty[acc]), 0), abort,
-                   static_cast<int>(rank) * kEpilogueWarps + index, slots + index * kSlotBytes, sm.piece[index],
-                   &sm.units_done[index], own + part * kWarpCols * 4, &sm.own_full};
+                   static_cast<int>(rank) * kEpilogueWarps + index, slots + slot_offset(index), sm.piece[index],
+                   &sm.units_done[index], own + part * kWarpCols * 4, &sm.own_full,
+                   ptx::map_to_rank(ptx::smem_u32(&sm.a_full), 0)};
       const Place at = place_of(phase, x, rank, index);
       next_acc();
       return phase == kGram ? epilogue_square<kGram>(maps, a, step, x, at, in, parity)
@@ -1181,6 +1224,7 @@ cudaError_t launch_orthogonalize(const OrthoCall& q, cudaStream_t stream) {
   const int64_t most = sh.batch * std::max(nr * nc, nr * (nr + 1) / 2 * std::max(sh.split_gram, sh.split_poly));
   const int pairs = static_cast<int>(std::min<int64_t>(most, g_pairs[dev]));
   if (pairs < 1) return cudaErrorLaunchOutOfResources;
+  a.fused = nr == 1 && sh.split_gram == 1 && sh.batch <= pairs;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * pairs);
   cfg.blockDim = dim3(kGemmThreads);
