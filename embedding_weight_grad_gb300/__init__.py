@@ -464,7 +464,8 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, *, scale: float 
         raise ValueError(f"top must be in [0, min(vocab, {MAX_TOP})]")
     device, shape = logits.device, targets.shape
     # (separate allocations: views of one take longer to make)
-    stats = [torch.empty(shape, dtype=torch.float32, device=device) for _ in range(4)]
+    first = torch.empty(shape, dtype=torch.float32, device=device)
+    stats = (first, torch.empty_like(first), torch.empty_like(first), torch.empty_like(first))
     top_logprobs = top_ids = None
     if top:
         top_logprobs = torch.empty((*shape, top), dtype=torch.float32, device=device)

@@ -25,10 +25,30 @@ Array flat(const char* name, const void* p, int64_t count, size_t es) {
   return {name, p, span(p, 1, count, count, es)};
 }
 
-int check_array(const Array& a, size_t align, int dev) {
+// Whether pointers are memory of the current device, asking the runtime once for each 2 MiB
+// page: device memory is mapped in pages of that size, which nothing else shares, and a call's
+// small arrays mostly come from one.
+class DeviceMemory {
+ public:
+  explicit DeviceMemory(int dev) : dev_(dev) {}
+  bool has(const void* p) {
+    const uintptr_t page = reinterpret_cast<uintptr_t>(p) >> 21;
+    for (int i = 0; i < known_; ++i)
+      if (pages_[i] == page) return true;
+    if (!on_device(p, dev_)) return false;
+    if (known_ < 8) pages_[known_++] = page;
+    return true;
+  }
+
+ private:
+  int dev_, known_ = 0;
+  uintptr_t pages_[8];
+};
+
+int check_array(const Array& a, size_t align, DeviceMemory& mem) {
   if (!a.p || !aligned(a.p, align))
     return fail(EWG_ERR_UNSUPPORTED, std::string(a.name) + " is null or misaligned");
-  if (!on_device(a.p, dev))
+  if (!mem.has(a.p))
     return fail(EWG_ERR_UNSUPPORTED, std::string(a.name) + " is not memory of the current device");
   return EWG_OK;
 }
@@ -41,9 +61,9 @@ int check_apart(const Array& a, const Array& b) {
 
 constexpr size_t kStatusBytes = sizeof(ewg::Header);
 
-int check_status_workspace(void* ws, size_t bytes, int dev) {
+int check_status_workspace(void* ws, size_t bytes, DeviceMemory& mem) {
   if (!ws) return EWG_OK;
-  if (!aligned(ws, 256) || bytes < kStatusBytes || !on_device(ws, dev))
+  if (!aligned(ws, 256) || bytes < kStatusBytes || !mem.has(ws))
     return fail(EWG_ERR_INVALID, "workspace must be 256 bytes of the current device, 256-byte aligned");
   return EWG_OK;
 }
@@ -51,7 +71,7 @@ int check_status_workspace(void* ws, size_t bytes, int dev) {
 int* status_word(void* ws) { return ws ? &static_cast<ewg::Header*>(ws)->status : nullptr; }
 
 int check_logits(const void* logits, int dtype, int64_t row_stride, const void* targets, int targets_dtype,
-                 int64_t n, int64_t V, float scale, int dev) {
+                 int64_t n, int64_t V, float scale, DeviceMemory& mem) {
   if (dtype != EWG_BF16 && dtype != EWG_FP32) return fail(EWG_ERR_UNSUPPORTED, "logits must be bf16 or fp32");
   if (targets_dtype != EWG_INT32 && targets_dtype != EWG_INT64)
     return fail(EWG_ERR_UNSUPPORTED, "targets must be int32 or int64");
@@ -63,9 +83,9 @@ int check_logits(const void* logits, int dtype, int64_t row_stride, const void* 
   // byte offsets stay within 62 bits
   if (row_stride < 0 || row_stride > (int64_t(1) << 62) / (n * 4))
     return fail(EWG_ERR_UNSUPPORTED, "logits row stride is too large");
-  int rc = check_array({"logits", logits, {}}, elem_size(dtype), dev);
+  int rc = check_array({"logits", logits, {}}, elem_size(dtype), mem);
   if (rc) return rc;
-  return check_array({"targets", targets, {}}, elem_size(targets_dtype), dev);
+  return check_array({"targets", targets, {}}, elem_size(targets_dtype), mem);
 }
 
 bool ortho_sizes_ok(int64_t batch, int64_t rows, int64_t cols) {
@@ -77,7 +97,7 @@ bool ortho_sizes_ok(int64_t batch, int64_t rows, int64_t cols) {
 
 // A [batch][rows][cols] array of matrices: its checks and its bytes.
 int ortho_array(const char* name, const void* p, size_t es, int64_t batch, int64_t rows, int64_t cols,
-                int64_t batch_stride, int64_t row_stride, int dev, Array* out) {
+                int64_t batch_stride, int64_t row_stride, DeviceMemory& mem, Array* out) {
   const int64_t most = int64_t(1) << 40;
   if ((rows > 1 && row_stride < cols) || row_stride < 0 || row_stride > most || batch_stride < 0 || batch_stride > most)
     return fail(EWG_ERR_UNSUPPORTED, std::string(name) + " row stride must be >= cols, strides below 2^40");
@@ -85,7 +105,7 @@ int ortho_array(const char* name, const void* p, size_t es, int64_t batch, int64
   if (batch > 1 && batch_stride < one)
     return fail(EWG_ERR_UNSUPPORTED, std::string(name) + " matrices overlap");
   *out = {name, p, span(p, batch, one, batch_stride, es)};
-  return check_array(*out, es, dev);
+  return check_array(*out, es, mem);
 }
 
 float log2_scale(float scale) { return static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074); }
@@ -102,11 +122,12 @@ int ewg_token_logprobs(const void* logits, int logits_dtype, int64_t row_stride,
   int dev = 0, sms = 0;
   int rc = current_device(&dev, &sms);
   if (rc) return rc;
-  if ((rc = check_logits(logits, logits_dtype, row_stride, targets, targets_dtype, num_tokens, vocab, scale, dev)))
+  DeviceMemory mem(dev);
+  if ((rc = check_logits(logits, logits_dtype, row_stride, targets, targets_dtype, num_tokens, vocab, scale, mem)))
     return rc;
   if (top < 0 || top > EWG_MAX_TOP || top > vocab)
     return fail(EWG_ERR_UNSUPPORTED, "top outside [0, min(vocab, EWG_MAX_TOP)]");
-  if ((rc = check_status_workspace(workspace, workspace_bytes, dev))) return rc;
+  if ((rc = check_status_workspace(workspace, workspace_bytes, mem))) return rc;
   if (num_tokens == 0) return EWG_OK;
   const int64_t n = num_tokens;
   const Array in[2] = {{"logits", logits, span(logits, n, vocab, row_stride, elem_size(logits_dtype))},
@@ -117,7 +138,7 @@ int ewg_token_logprobs(const void* logits, int logits_dtype, int64_t row_stride,
                         flat("top_ids", top ? top_ids : nullptr, n * top, 8),
                         flat("workspace", workspace, kStatusBytes, 1)};
   for (int i = 0; i < 7; ++i) {
-    if ((i < 4 || (i < 6 && top)) && (rc = check_array(out[i], i == 5 ? 8 : 4, dev))) return rc;
+    if ((i < 4 || (i < 6 && top)) && (rc = check_array(out[i], i == 5 ? 8 : 4, mem))) return rc;
     for (const Array& a : in)
       if ((rc = check_apart(out[i], a))) return rc;
     for (int j = 0; j < i; ++j)
@@ -153,9 +174,10 @@ int ewg_token_logprobs_backward(const void* logits, int logits_dtype, int64_t ro
   int dev = 0, sms = 0;
   int rc = current_device(&dev, &sms);
   if (rc) return rc;
-  if ((rc = check_logits(logits, logits_dtype, row_stride, targets, targets_dtype, num_tokens, vocab, scale, dev)))
+  DeviceMemory mem(dev);
+  if ((rc = check_logits(logits, logits_dtype, row_stride, targets, targets_dtype, num_tokens, vocab, scale, mem)))
     return rc;
-  if ((rc = check_status_workspace(workspace, workspace_bytes, dev))) return rc;
+  if ((rc = check_status_workspace(workspace, workspace_bytes, mem))) return rc;
   if (num_tokens == 0) return EWG_OK;
   const int64_t n = num_tokens;
   const size_t es = elem_size(logits_dtype);
@@ -172,9 +194,9 @@ int ewg_token_logprobs_backward(const void* logits, int logits_dtype, int64_t ro
                        flat("grad_entropy", grad_entropy, n, 4)};
   const Array out{"grad_logits", grad_logits, span(grad_logits, n, vocab, grad_row_stride, es)};
   const Array ws = flat("workspace", workspace, kStatusBytes, 1);
-  if ((rc = check_array(out, es, dev))) return rc;
+  if ((rc = check_array(out, es, mem))) return rc;
   for (int i = 0; i < 7; ++i) {
-    if (i >= 2 && (i < 5 || grad_entropy) && (rc = check_array(in[i], 4, dev))) return rc;
+    if (i >= 2 && (i < 5 || grad_entropy) && (rc = check_array(in[i], 4, mem))) return rc;
     const bool in_place = i == 0 && logits == grad_logits && (n == 1 || row_stride == grad_row_stride);
     if (!in_place && (rc = check_apart(out, in[i]))) return rc;
     if ((rc = check_apart(ws, in[i]))) return rc;
@@ -214,6 +236,7 @@ int ewg_orthogonalize(const void* grad, int grad_dtype, int64_t batch, int64_t r
   int dev = 0, sms = 0;
   int rc = current_device(&dev, &sms);
   if (rc) return rc;
+  DeviceMemory mem(dev);
   if (grad_dtype != EWG_BF16 && grad_dtype != EWG_FP32) return fail(EWG_ERR_UNSUPPORTED, "grad must be bf16 or fp32");
   if (steps < 1 || steps > EWG_MAX_ORTHO_STEPS)
     return fail(EWG_ERR_UNSUPPORTED, "steps outside [1, EWG_MAX_ORTHO_STEPS]");
@@ -225,12 +248,12 @@ int ewg_orthogonalize(const void* grad, int grad_dtype, int64_t batch, int64_t r
                                      "batch * ceil(rows / 256) * ceil(cols / 256) < 2^30");
   const size_t es = elem_size(grad_dtype);
   Array in, res;
-  if ((rc = ortho_array("grad", grad, es, batch, rows, cols, grad_batch_stride, grad_row_stride, dev, &in)) ||
-      (rc = ortho_array("out", out, 2, batch, rows, cols, out_batch_stride, out_row_stride, dev, &res)))
+  if ((rc = ortho_array("grad", grad, es, batch, rows, cols, grad_batch_stride, grad_row_stride, mem, &in)) ||
+      (rc = ortho_array("out", out, 2, batch, rows, cols, out_batch_stride, out_row_stride, mem, &res)))
     return rc;
   const ewg::OrthoShape shape = ewg::make_ortho_shape(batch, rows, cols);
   const size_t need = ewg::make_ortho_layout(shape).total;
-  if (!workspace || !aligned(workspace, 256) || workspace_bytes < need || !on_device(workspace, dev))
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < need || !mem.has(workspace))
     return fail(EWG_ERR_INVALID, "workspace null, misaligned, not on the device or smaller than "
                                  "ewg_orthogonalize_workspace_bytes(batch, rows, cols)");
   const Array ws = flat("workspace", workspace, static_cast<int64_t>(need), 1);
