@@ -116,6 +116,7 @@ __device__ __forceinline__ double sum_of_squares(const float (&g)[kLaneElems]) {
 // Sums of squares of one matrix per blockIdx.y, a warp to 1024 neighbouring elements of a row
 // (a matrix without gaps is one long row).  Bound by the read of G.
 __global__ void __launch_bounds__(256) ortho_norm_kernel(const OrthoIn a) {
+  ptx::pdl_launch_dependents();      // the scaling kernel's reads of G
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) a.header->status = kStatusOk;
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < a.num_counters; i += 256)
@@ -226,6 +227,7 @@ __global__ void __launch_bounds__(256) ortho_scale_kernel(const OrthoIn a) {
 #pragma unroll
     for (int k = 0; k < 16; ++k) tile[ry + 4 * k][cx] = v[k];
   }
+  ptx::pdl_wait_prior_grid();        // the norm kernel has ended
   if (tid < 32) {
     double sum = 0.0;
     for (int i = tid; i < a.norm_blocks; i += 32) sum += a.norm[blockIdx.z * a.norm_blocks + i];
@@ -1216,8 +1218,19 @@ cudaError_t launch_orthogonalize(const OrthoCall& q, cudaStream_t stream) {
   const unsigned batch = static_cast<unsigned>(sh.batch);
   ortho_norm_kernel<<<dim3(sh.norm_blocks, batch), 256, 0, stream>>>(in);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  ortho_scale_kernel<<<dim3((in.cols + 63) / 64, (in.rows + 63) / 64, batch), 256, 0, stream>>>(in);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  {
+    // may start while the norm kernel runs; it waits for it before it needs the norm
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((in.cols + 63) / 64, (in.rows + 63) / 64, batch);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, ortho_scale_kernel, in)) != cudaSuccess) return e;
+  }
 
   int dev = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
