@@ -299,17 +299,10 @@ static_assert(kSlotBytes == 4 * kStripBytes, "a slot holds two strips of both pa
 constexpr int kHalfStride = 4 * kPieceBytes;          // between a warp's halves
 static_assert(kHalfStride == kOperandBytes, "64 columns of the CTA's rows");
 __host__ __device__ constexpr int slot_offset(int w) { return (8 * (w / 4) + w % 4) * kPieceBytes; }
-constexpr int kSlotsBytes = kEpilogueWarps * kSlotBytes;
-// Matrices of one block go through a step on one pair, A and B as operands in the slots.  Where X
-// is one block too (kAllStay), the strips of X come to slots of their own, for which two
-// stages make room.
-enum Fused { kSeparate = 0, kAStays = 1, kAllStay = 2 };
-constexpr int kStagesAllStay = 3;
-static_assert((kStages - kStagesAllStay) * kStageBytes == kSlotsBytes, "room for the second slots");
 constexpr int kGemmThreads = 32 * (kFirstEpilogueWarp + kEpilogueWarps);
 constexpr int kOwnBytes = kBlock * 4;                 // a + what is left of B_ii for a unit's columns
 constexpr size_t kGemmSmem =
-    static_cast<size_t>(kStages) * kStageBytes + kSlotsBytes + kOwnBytes + 1024;
+    static_cast<size_t>(kStages) * kStageBytes + kEpilogueWarps * kSlotBytes + kOwnBytes + 1024;
 static_assert(kWarpCols == 128 && kPieces == 2, "a warp's columns, as the epilogue takes them");
 static_assert(kWarpsOfBlock == kOrthoWarps && kBlock == kOrthoBlock, "as the workspace is laid out for");
 static_assert(kGemmSmem + 512 <= 227 * 1024, "stages and slots fit in shared memory");
@@ -333,7 +326,7 @@ struct OrthoArgs {
   __half* b;
   float* diag_a[2];                  // [batch][ld]: what rounding left of the diagonals
   float* diag_b;
-  int fused;                         // enum Fused
+  int fused;                         // matrices of one block: A stays with the pair that computed it
   int split[2];                      // parts of the inner dimension of X X^T and A A
   float* partial;                    // split products: [batch][block][part][CTA][warp][column][row]
   __nv_bfloat16* out;
@@ -346,7 +339,7 @@ struct OrthoArgs {
 
 struct GemmSmem {
   uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
-  uint64_t piece[kEpilogueWarps][4], own_full, operand_full;
+  uint64_t piece[kEpilogueWarps][2], own_full, a_full;
   int units_done[kEpilogueWarps];    // units an epilogue warp is through with its slot for
   uint32_t tmem;
   int abort;
@@ -516,12 +509,11 @@ struct Acc {
   volatile int* abort;
   int place;                         // the warp's place in the pair
   uint32_t slot;                     // shared-memory address
-  uint32_t second;                   // the second slot's, or 0
   uint64_t* bars;                    // of the slot's halves: its copies have come
   volatile int* units_done;          // of the warp
   uint32_t own;                      // shared-memory address: a + what is left of B_ii, of the warp's columns
   uint64_t* own_full;
-  uint32_t operand_full;             // shared::cluster address
+  uint32_t a_full;                   // shared::cluster address
 };
 
 // The first row and column of epilogue warp w's part of a unit (it takes the 32 rows of its
@@ -541,26 +533,19 @@ __device__ __forceinline__ int pieces_of(const OrthoArgs& a, int phase, const Pl
   return min(max((a.r - at.col + width - 1) / width, 0), kWarpCols / width);
 }
 
-// Requests (one lane) what a warp's part of a unit reads beside the products: piece u of A into
-// half u of the slot; strip u of both parts of X.
+// Requests (one lane) what a warp's part of a unit reads beside the products: piece u of A, or
+// strip u of both parts of X, into half u % 2 of the slot.
 __device__ __forceinline__ void request_piece(const OrthoMaps& maps, int step, int z, const Place& at, int u,
                                               uint32_t slot, uint64_t* bars) {
   ptx::mbar_arrive_expect_tx(&bars[u], kPieceBytes);
   ptx::tma_load_3d(slot + u * kHalfStride, &maps.a_piece[step & 1], at.col + u * kPiece, at.row, z, &bars[u]);
 }
-// Where strip u goes: the slot's halves in turn, or with a second slot its halves and then the
-// first's; and the number of its barrier.
-__device__ __forceinline__ uint32_t strip_at(uint32_t slot, uint32_t second, int u) {
-  return (second && u < 2 ? second : slot) + u % 2 * kHalfStride;
-}
-__device__ __forceinline__ int strip_bar(uint32_t second, int u) { return second ? u : u % 2; }
 __device__ __forceinline__ void request_strip(const OrthoMaps& maps, int step, int z, const Place& at, int u,
-                                              uint32_t slot, uint32_t second, uint64_t* bars) {
-  uint64_t* bar = &bars[strip_bar(second, u)];
-  const uint32_t to = strip_at(slot, second, u);
-  ptx::mbar_arrive_expect_tx(bar, 2 * kStripBytes);
-  ptx::tma_load_3d(to, &maps.xt_strip[step & 1], at.col + u * kStrip, at.row, z, bar);
-  ptx::tma_load_3d(to + kStripBytes, &maps.xl_strip, at.col + u * kStrip, at.row, z, bar);
+                                              uint32_t slot, uint64_t* bars) {
+  const uint32_t to = slot + u % 2 * kHalfStride;
+  ptx::mbar_arrive_expect_tx(&bars[u % 2], 2 * kStripBytes);
+  ptx::tma_load_3d(to, &maps.xt_strip[step & 1], at.col + u * kStrip, at.row, z, &bars[u % 2]);
+  ptx::tma_load_3d(to + kStripBytes, &maps.xl_strip, at.col + u * kStrip, at.row, z, &bars[u % 2]);
 }
 
 __device__ __forceinline__ uint4 lds_v4(uint32_t at) {
@@ -646,18 +631,16 @@ __device__ __forceinline__ bool epilogue_update(const OrthoMaps& maps, const Ort
   if (!__all_sync(kAll, wait_bar(in.full, in.parity, in.abort))) return false;
   ptx::tmem_fence_after();
   if (strips == 0) release_acc(in.empty);
-  if (in.second && lane == 0)        // the products are done with B in the slot
-    for (int u = 2; u < strips; ++u) request_strip(maps, step, x.z, at, u, in.slot, in.second, in.bars);
-  // (bit 4 of `parity`: of the next wait on own_full)
-  if (!__all_sync(kAll, wait_bar(in.own_full, (parity >> 4) & 1u, in.abort))) return false;
-  parity ^= 16u;
+  // (bit 2 of `parity`: of the next wait on own_full)
+  if (!__all_sync(kAll, wait_bar(in.own_full, (parity >> 2) & 1u, in.abort))) return false;
+  parity ^= 4u;
   const float unscale = 1.0f / a.s;
 #pragma unroll 1
   for (int u = 0; u < strips; ++u) {
-    const uint32_t strip = strip_at(in.slot, in.second, u);
+    const uint32_t strip = in.slot + u % 2 * kHalfStride;
     uint32_t acc[kStrip];
     ptx::tmem_load32(acc, in.from + u * kStrip);
-    if (!wait_piece(in, strip_bar(in.second, u), parity)) return false;
+    if (!wait_piece(in, u % 2, parity)) return false;
     uint4 top[4], low[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -699,9 +682,9 @@ __device__ __forceinline__ bool epilogue_update(const OrthoMaps& maps, const Ort
     }
     __syncwarp();
     if (lane == 0) {
-      if (!in.second && u >= 1 && u + 1 < strips) {   // into the half of the strip before this one
+      if (u >= 1 && u + 1 < strips) {                 // into the half of the strip before this one
         ptx::bulk_wait_read();
-        request_strip(maps, step, x.z, at, u + 1, in.slot, 0, in.bars);
+        request_strip(maps, step, x.z, at, u + 1, in.slot, in.bars);
       }
       if (!last) {
         ptx::tma_store_3d(&maps.xt_strip[cur ^ 1], at.col + u * kStrip, at.row, x.z, strip);
@@ -750,7 +733,8 @@ __device__ __forceinline__ uint4 finish8(const OrthoArgs& a, int cur, float f, f
 // The same for A = X X^T or B = b A + c A^2: 32 rows from i0, kWarpCols columns from j of a block on
 // or below the diagonal.
 //
-// Matrices of one block (enum Fused): A, and with kAllStay B, is left in the slots as an operand.
+// Matrices of one block (a.fused): A is left in the slots, which form an operand, and the
+// same pair goes on to B.
 //
 // Where the inner dimension is split, each part's warp stores its sums, waits for the other
 // parts' and finishes its share of the columns, in sixteens, from all parts' sums, added
@@ -823,7 +807,6 @@ __device__ __forceinline__ bool epilogue_square(const OrthoMaps& maps, const Ort
     return true;
   }
   if (pieces == 0) release_acc(in.empty);
-  const bool stays = a.fused == kAllStay || (kPhase == kGram && a.fused == kAStays);
 #pragma unroll 1
   for (int u = 0; u < pieces; ++u) {
     const uint32_t slot = in.slot + u * kHalfStride;
@@ -842,28 +825,23 @@ __device__ __forceinline__ bool epilogue_square(const OrthoMaps& maps, const Ort
         for (int q = 0; q < 8; ++q) v[q] = __uint_as_float(acc[8 * k + q]);
         uint4 o = {};
         if (kPhase == kPoly) o = lds_v4(chunk);
-        const int col = j + u * kPiece + 32 * h + 8 * k;
-        if (kPhase == kPoly && stays) {               // B as an operand: zeros beyond the matrix
-#pragma unroll
-          for (int q = 0; q < 8; ++q) v[q] = col + q < a.r ? v[q] : 0.0f;
-        }
-        sts_v4(chunk, finish8<kPhase>(a, cur, f, v, o, i - col, rest_a, row ? diag_at : -1));
+        sts_v4(chunk, finish8<kPhase>(a, cur, f, v, o, i - (j + u * kPiece + 32 * h + 8 * k), rest_a, row ? diag_at : -1));
       }
     }
     ptx::fence_proxy_async_shared();
-    if (stays) continue;
+    if (kPhase == kGram && a.fused) continue;         // A stays
     __syncwarp();
     if (lane == 0) {
       ptx::tma_store_3d(kPhase == kGram ? &maps.a_piece[cur] : &maps.b_piece, j + u * kPiece, i0, x.z, slot);
       ptx::bulk_commit();
     }
   }
+  const bool stays = kPhase == kGram && a.fused;
   if (stays) {
     __syncwarp();
-    if (lane == 0) ptx::mbar_arrive_release_cluster(in.operand_full);
+    if (lane == 0) ptx::mbar_arrive_release_cluster(in.a_full);
   }
-  // (the rests of B's diagonal are signalled even where B itself stays)
-  unit_done(a, kPhase, x, in.units_done, kPhase == kPoly || !stays);
+  unit_done(a, kPhase, x, in.units_done, !stays);
   return true;
 }
 
@@ -910,9 +888,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       ptx::mbar_init(&sm.acc_empty[i], 2 * kEpilogueWarps);
     }
     ptx::mbar_init(&sm.drained, 1);
-    for (int i = 0; i < 4 * kEpilogueWarps; ++i) ptx::mbar_init(&sm.piece[0][0] + i, 1);
+    for (int i = 0; i < 2 * kEpilogueWarps; ++i) ptx::mbar_init(&sm.piece[0][0] + i, 1);
     ptx::mbar_init(&sm.own_full, 1);
-    ptx::mbar_init(&sm.operand_full, kWarpsOfBlock);
+    ptx::mbar_init(&sm.a_full, kWarpsOfBlock);
     for (int i = 0; i < kEpilogueWarps; ++i) sm.units_done[i] = 0;
     sm.abort = 0;
     ptx::fence_mbar_init();
@@ -929,15 +907,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   ptx::tmem_fence_after();
   const uint32_t tmem = sm.tmem;
   volatile int* abort = &sm.abort;
-  const uint32_t num_stages = a.fused == kAllStay ? kStagesAllStay : kStages;
-  const uint32_t slots = stages + num_stages * kStageBytes;  // of the epilogue warps
-  const uint32_t second = a.fused == kAllStay ? slots + kSlotsBytes : 0;
-  const uint32_t own = stages + kStages * kStageBytes + kSlotsBytes;
+  const uint32_t slots = stages + kStages * kStageBytes;     // of the epilogue warps
+  const uint32_t own = slots + kEpilogueWarps * kSlotBytes;
 
   uint32_t stage = 0, stage_phase = 0;      // producer's or issuer's place in the ring
   uint32_t acc = 0, acc_phase = 0;          // issuer's or epilogue's accumulator
   auto next_stage = [&] {
-    if (++stage == num_stages) {
+    if (++stage == kStages) {
       stage = 0;
       stage_phase ^= 1u;
     }
@@ -954,12 +930,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     for (int p = 0; p < 3 * a.steps; ++p) {
       const int phase = p % 3, step = p / 3;
       const int units = units_of(a, phase);
-      if ((a.fused && phase == kPoly) || (a.fused == kAllStay && phase == kUpdate)) continue;   // with A
+      if (a.fused && phase == kPoly) continue;        // with the phase before
       for (int t = pair >= offset ? pair - offset : pair - offset + pairs; t < units; t += pairs) {
         if (*abort) return;
         if (!body(phase, step, unit_at(a, phase, t)) ||
-            (a.fused && phase == kGram && !body(kPoly, step, unit_at(a, kPoly, t))) ||
-            (a.fused == kAllStay && !body(kUpdate, step, unit_at(a, kUpdate, t)))) {
+            (a.fused && phase == kGram && !body(kPoly, step, unit_at(a, kPoly, t)))) {
           gave_up(a, abort);
           return;
         }
@@ -968,7 +943,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     }
   };
 
-  uint32_t operand_parity = 0;       // issuer's, of operand_full
+  uint32_t a_parity = 0;             // issuer's, of a_full
 
   if (warp == 0) {
     if (lane == 0) {
@@ -982,13 +957,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         const int rb = (phase == kUpdate ? x.I : x.J) * kBlock + rank * 128;
         int k0, k1;
         inner_of(a, phase, x, k0, k1);
-        // (kAllStay: the update needs X^T only, for which X X^T has waited)
-        const bool b_stays = a.fused == kAllStay && phase == kUpdate;
-        if (!b_stays && !wait_inputs(a, phase, step, x, abort)) return false;
+        if (!wait_inputs(a, phase, step, x, abort)) return false;
         ptx::fence_proxy_async();    // the acquires above before the tensor copies
         for (int kb = k0; kb < k1; ++kb) {
           if (!wait_bar(&sm.empty[stage], stage_phase ^ 1u, abort)) return false;
-          if (rank == 0) ptx::mbar_arrive_expect_tx(&sm.full[stage], b_stays ? kStageBytes : 2 * kStageBytes);
+          if (rank == 0) ptx::mbar_arrive_expect_tx(&sm.full[stage], 2 * kStageBytes);
           const uint32_t bar = ptx::map_to_rank(ptx::smem_u32(&sm.full[stage]), 0);
           const uint32_t dst = stages + stage * kStageBytes;
           const int k = kb * kStepK;
@@ -997,8 +970,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           for (int h = 0; h < 2; ++h) {
             const int da = ra + 64 * h, db = rb + 64 * h;
             ptx::tma_load_3d_pair(dst + h * kBoxBytes, ma, mn.a ? da : k, mn.a ? k : da, x.z, bar);
-            if (!b_stays)
-              ptx::tma_load_3d_pair(dst + kOperandBytes + h * kBoxBytes, mb, mn.b ? db : k, mn.b ? k : db, x.z, bar);
+            ptx::tma_load_3d_pair(dst + kOperandBytes + h * kBoxBytes, mb, mn.b ? db : k, mn.b ? k : db, x.z, bar);
           }
           next_stage();
         }
@@ -1014,13 +986,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         if (!wait_bar(&sm.acc_empty[acc], acc_phase ^ 1u, abort)) return false;
         ptx::tmem_fence_after();
         const uint32_t d = tmem + acc * kBlock;
-        const bool staying = a.fused && (phase == kPoly || (phase == kUpdate && a.fused == kAllStay));
-        if (staying) {               // A or B as the epilogue left it
-          if (!wait_bar(&sm.operand_full, operand_parity, abort)) return false;
-          operand_parity ^= 1u;
+        if (a.fused && phase == kPoly) {              // A as the epilogue left it, both operands
+          if (!wait_bar(&sm.a_full, a_parity, abort)) return false;
+          a_parity ^= 1u;
           ptx::tmem_fence_after();
-        }
-        if (staying && phase == kPoly) {              // A is both operands
           for (int kb = k0; kb < k1; ++kb) {
             const uint32_t at = slots + kb * kOperandBytes;
 #pragma unroll
@@ -1037,7 +1006,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           if (!wait_bar(&sm.full[stage], stage_phase, abort)) return false;
           ptx::tmem_fence_after();
           const uint32_t at = stages + stage * kStageBytes;
-          const uint32_t at_b = staying ? slots + kb * kOperandBytes : at + kOperandBytes;
           const Majors mn = majors_of(phase, x, kb);
           const uint32_t idesc = idesc_of(mn);
           // K-major: 8-row groups 1024 bytes apart, 16 inner elements = 32 bytes.  MN-major:
@@ -1046,8 +1014,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           const uint32_t k_a = mn.a ? 2048 : 32, k_b = mn.b ? 2048 : 32;
 #pragma unroll
           for (int k = 0; k < kStepK / 16; ++k)
-            ptx::mma_f16_pair(d, operand_desc(at + k * k_a, lead_a, 1024), operand_desc(at_b + k * k_b, lead_b, 1024),
-                              idesc, kb > k0 || k > 0);
+            ptx::mma_f16_pair(d, operand_desc(at + k * k_a, lead_a, 1024),
+                              operand_desc(at + kOperandBytes + k * k_b, lead_b, 1024), idesc, kb > k0 || k > 0);
           ptx::mma_commit_pair(&sm.empty[stage]);
           next_stage();
         }
@@ -1085,8 +1053,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         const int n = min(pieces_of(a, phase, at, phase == kPoly ? kPiece : kStrip), 2);
         for (int u = 0; u < n; ++u) {
           if (phase == kPoly) request_piece(maps, step, x.z, at, u, slots + slot_offset(w), sm.piece[w]);
-          else request_strip(maps, step, x.z, at, u, slots + slot_offset(w), second ? second + slot_offset(w) : 0,
-                             sm.piece[w]);
+          else request_strip(maps, step, x.z, at, u, slots + slot_offset(w), sm.piece[w]);
         }
       }
       __syncwarp();
@@ -1099,10 +1066,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     for_units([&](int phase, int step, const Unit& x) {
       const Acc in{tmem + acc * kBlock + part * kWarpCols + (static_cast<uint32_t>(quarter) << 21),
                    &sm.acc_full[acc], acc_phase, ptx::map_to_rank(ptx::smem_u32(&sm.acc_empty[acc]), 0), abort,
-                   static_cast<int>(rank) * kEpilogueWarps + index, slots + slot_offset(index),
-                   second ? second + slot_offset(index) : 0, sm.piece[index],
+                   static_cast<int>(rank) * kEpilogueWarps + index, slots + slot_offset(index), sm.piece[index],
                    &sm.units_done[index], own + part * kWarpCols * 4, &sm.own_full,
-                   ptx::map_to_rank(ptx::smem_u32(&sm.operand_full), 0)};
+                   ptx::map_to_rank(ptx::smem_u32(&sm.a_full), 0)};
       const Place at = place_of(phase, x, rank, index);
       next_acc();
       return phase == kGram ? epilogue_square<kGram>(maps, a, step, x, at, in, parity)
@@ -1271,7 +1237,7 @@ cudaError_t launch_orthogonalize(const OrthoCall& q, cudaStream_t stream) {
   const int64_t most = sh.batch * std::max(nr * nc, nr * (nr + 1) / 2 * std::max(sh.split_gram, sh.split_poly));
   const int pairs = static_cast<int>(std::min<int64_t>(most, g_pairs[dev]));
   if (pairs < 1) return cudaErrorLaunchOutOfResources;
-  a.fused = nr > 1 || sh.split_gram > 1 ? kSeparate : nc == 1 ? kAllStay : kAStays;
+  a.fused = nr == 1 && sh.split_gram == 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * pairs);
   cfg.blockDim = dim3(kGemmThreads);
