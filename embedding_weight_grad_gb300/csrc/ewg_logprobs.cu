@@ -251,7 +251,8 @@ struct GroupSmem {
 // same way the vectors of the thread that holds the maximum are summed again without it
 // where its own term would drown the others (R < 8).
 //
-// 1536 threads on an SM (40 registers each), 2048 for bf16 rows of 512 threads.
+// 1536 threads on an SM (40 registers each; 2048 take 135 us instead of 126 at 8192 x 50257, 1280
+// take 130), 2048 for bf16 rows of 512 threads.
 constexpr int threads_of(int kT) { return kT == 32 ? 256 : kT; }
 template <typename T>
 constexpr int blocks_per_sm(int kT) { return (sizeof(T) == 2 && kT == 512 ? 2048 : 1536) / threads_of(kT); }
@@ -295,8 +296,8 @@ __global__ void __launch_bounds__(threads_of(kT), blocks_per_sm<T>(kT)) logprobs
       r[u] = v + u * kT < v1 ? load16(zv + v + u * kT)
                              : make_uint4(V::kNegInf, V::kNegInf, V::kNegInf, V::kNegInf);
   };
-  // Short rows: on its way while the target comes.  (8192 x 129280 with 512 threads a row
-  // takes 329 us without, 344 with.)
+  // Short rows: on its way while the target comes.  (8192 x 50257 with 256 threads a row
+  // takes 126 us without, 132 with.)
   constexpr bool kAhead = kT <= 128;
   if constexpr (kAhead) load_batch(v0 + tid);
   const long long target = target_of(a.targets, a.targets_int64, row);
@@ -728,16 +729,30 @@ cudaError_t launch_forward(const LogprobsArgs& a, int cluster, cudaStream_t stre
 
 template <typename T>
 cudaError_t launch_forward_of(const LogprobsArgs& a, int num_sms, cudaStream_t stream) {
-  // Threads of a row by its vectors, where there are rows enough to fill the device.  65536 x
-  // 4097 bf16 (512 vectors): 88 us with 32 threads, 129 with 128.  8192 x 50257 (6282): 129
-  // with 128, 131 with 256, 156 with 32 or 512.  8192 x 129280 (16160): 358 with 512 and 432
-  // with 128, with 8 alternatives.
+  // Threads of a row by its vectors and by whether there are rows enough to fill the device
+  // (bf16 in us, without | with 8 alternatives, by threads a row):
+  //                  32         128        256        512
+  //   65536 x  4097  85 | 132  121 |  -
+  //   32768 x  8192  84 | 130   94 | 148  125 | 209
+  //     512 x  8192  7.1| 12.6  4.0| 6.1             7.2| 10.2
+  //    8192 x 32000 103 | 240   83 | 103   83 | 102  100 | 130
+  //     160 x 64000             14 |  18  7.9 | 10.3
+  //    8192 x 50257            129 | 165  126 | 148  144 | 174
+  //    8192 x 80000            197 | 270  187 | 214  211 | 231
+  //    8192 x129280            312 | 437  294 | 357  327 | 349
+  //    2048 x129280             99 | 131   85 | 101   82 |  92
+  // Short rows pay for what a row costs besides its read, which more threads raise; in long
+  // ones few threads leave each with more vectors to read again for the alternatives.
   const int nv = a.V / Vec<T>::kE;
-  if (nv <= 512) return launch_forward<T, 32>(a, 1, stream);
-  if (nv <= 8192 && a.n >= num_sms) return launch_forward<T, 128>(a, 1, stream);
-  // few rows: up to 8 blocks a row, each thread with a vector at least
+  const bool many = a.n >= 16 * num_sms;
+  if (nv <= 128 || (nv <= 1024 && many)) return launch_forward<T, 32>(a, 1, stream);
+  if (nv <= 1024 || (nv < 4096 && a.n >= num_sms)) return launch_forward<T, 128>(a, 1, stream);
+  if (a.n >= num_sms && (nv <= 12288 || (many && !a.top && nv <= 32768))) return launch_forward<T, 256>(a, 1, stream);
+  // Few rows: up to 8 blocks a row, one on an SM, of 1024 vectors at least.  Joining them
+  // costs 1.2 us, which a row of 4000 vectors does not win back (64 x 32000 bf16 with 8
+  // alternatives: 6.6 us, in two blocks 8.9; 1 x 129280: 8.0 in eight, 10.4 in one).
   int cluster = 1;
-  while (cluster < kMaxCluster && static_cast<long long>(a.n) * cluster < num_sms && nv / (2 * cluster) >= 512) cluster *= 2;
+  while (cluster < kMaxCluster && 2LL * cluster * a.n <= num_sms && nv > 4096 && nv / (2 * cluster) >= 1024) cluster *= 2;
   return launch_forward<T, 512>(a, cluster, stream);
 }
 

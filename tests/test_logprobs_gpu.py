@@ -117,6 +117,38 @@ def test_sizes(n, V, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("n,V,top", [(2500, 1111, 4), (2432, 4101, 3), (2432, 8200, 3), (160, 8300, 7), (160, 33001, 7),
+                                     (151, 33001, 7), (76, 66000, 2), (38, 140001, 9), (2432, 102403, 0), (2432, 30003, 1)])
+def test_many_rows(n, V, top, dtype):
+    """Rows enough to fill the device: other shares of a row for a thread."""
+    z, t = make(n, V, dtype, seed=n + V, pad=V % 2)
+    r = ewg.token_logprobs(z, t, scale=0.9, top=top)
+    for i in range(0, n, 256):                   # the 64-bit reference in pieces
+        part = ewg.TokenLogprobs(*(x if x is None else x[i:i + 256] for x in r))
+        check_forward(z[i:i + 256], t[i:i + 256], 0.9, top, part)
+
+
+@pytest.mark.parametrize("low", [-0.37, -1.7, -6.1])
+@pytest.mark.parametrize("n,V", [(2, 40), (2432, 4096), (2432, 200000), (1, 200000), (2, 1000000)])
+def test_equal_terms(n, V, low):
+    """All terms of R but the target's are equal, so that roundings of a running sum may all fall
+    to one side: a thread adds at most 4 a vector, 400 of them at most, each with u of the
+    sum.  Relative errors: 400 u = 2.4e-5 and REL of the terms."""
+    z = torch.full((n, V), low, device=DEV, dtype=BF16)
+    z[:, V // 2] = 1.0
+    t = torch.full((n,), V // 3, device=DEV)
+    r = ewg.token_logprobs(z, t)
+    x = z[0, 0].double() - 1.0
+    R = (V - 1) * x.exp()
+    log_sum = R.log1p()
+    entropy = log_sum - R * x / (1 + R)
+    tol = (400 * U + REL) * R / (1 + R)
+    assert bool(((r.log_sum - log_sum).abs() <= tol + 4 * U * log_sum).all())
+    assert bool(((r.logprobs - (x - log_sum)).abs() <= tol + 6 * U * (x - log_sum).abs()).all())
+    assert bool(((r.entropy - entropy).abs() <= tol * (1 - x) + 4 * U * (log_sum + x.abs())).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("pad", [1, 2, 3, 5, 8, 40])
 def test_row_strides(dtype, pad):
     """Rows of a wider buffer (NaN between them): every alignment of a row."""
