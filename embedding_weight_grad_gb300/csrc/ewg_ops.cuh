@@ -53,7 +53,7 @@ cudaError_t launch_logprobs_grad(const LogprobsGradArgs& a, bool bf16, cudaStrea
 
 constexpr int kOrthoMaxSide = 16384;      // of the smaller side
 constexpr int kOrthoMaxLong = 1 << 20;    // of the larger side
-constexpr int kNormBlocks = 304;          // blocks summing the squares of one matrix, at most
+constexpr int kNormBlocks = 304;          // blocks summing squares, at most, if the matrices are not more
 
 constexpr int kOrthoBlock = 256;          // side of the blocks the products are computed in
 constexpr int kOrthoWarps = 16;           // epilogue warps of a block
@@ -110,9 +110,11 @@ inline OrthoShape make_ortho_shape(int64_t batch, int64_t rows, int64_t cols) {
   s.ld = (s.r + 15) / 16 * 16;
   s.blocks_r = (s.r + kOrthoBlock - 1) / kOrthoBlock;
   s.blocks_c = (s.c + kOrthoBlock - 1) / kOrthoBlock;
-  // a block (8 warps of 1024 elements) sums 16384 elements or more
+  // a block (8 warps of 1024 elements) sums 16384 elements or more, and the blocks of all
+  // matrices run at once
   const int64_t want = (s.r * s.c + 16383) / 16384;
-  s.norm_blocks = static_cast<int>(want < kNormBlocks ? want : kNormBlocks);
+  const int64_t most = batch < kNormBlocks ? kNormBlocks / batch : 1;
+  s.norm_blocks = static_cast<int>(want < most ? want : most);
   s.split_gram = ortho_split(batch * s.square_blocks(), s.c);
   s.split_poly = ortho_split(batch * s.square_blocks(), s.r);
   return s;

@@ -48,12 +48,14 @@ namespace ewg {
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
+constexpr int kScaleBlocks = 4;      // blocks of the scaling kernel on an SM
 
 // ---------------------------------------------------------------- norm and first X
 
 struct OrthoIn {
   const void* grad;
   int bf16, tall;
+  int tiles_of_block;                // of the scaling kernel
   long long batch_stride, row_stride;
   int rows, cols;
   int ld;
@@ -81,45 +83,65 @@ __device__ __forceinline__ float grad_at(const OrthoIn& a, long long i) {
                 : static_cast<const float*>(a.grad)[i];
 }
 
-// The sum of the squares of a lane's kLaneElems elements, to about 2^-45 of it: each square
-// and each addition with its rounding error (an fma, and Knuth's two-sum), the errors
-// summed beside.  The norm then rounds to the same fp32 factor whatever the order of the
-// elements (strides, alignment, a transposed matrix).  The elements are first scaled by the power
-// of two that brings the largest near 1, which is exact, so that neither large nor small
-// gradients leave fp32's range.  64-bit arithmetic would bound the kernel.
+// A lane's sum of squares, to about 2^-45 of it: each square and each addition with its
+// rounding error (an fma, and Knuth's two-sum), the errors summed beside.  The norm then
+// rounds to the same fp32 factor whatever the order of the elements (strides, alignment, a
+// transposed matrix).  The elements are first scaled by the power of two that brings the
+// largest so far near 1, which is exact, so that neither large nor small gradients leave
+// fp32's range.  64-bit arithmetic, two elements a cycle on an SM, would bound the kernel: it
+// takes over once in kFlush times.
 constexpr int kLaneElems = 32;
+constexpr int kNormWarps = 8;
+constexpr int kFlush = 8;
 
-__device__ __forceinline__ double sum_of_squares(const float (&g)[kLaneElems]) {
-  float m = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kLaneElems; ++i) m = fmaxf(m, fabsf(g[i]));
-  const int e = min(static_cast<int>(__float_as_uint(m) >> 23), 253);
-  const float scale = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);          // 2^(127 - e)
-  float2 sum = make_float2(0.0f, 0.0f), err = sum;
-  const float2 by = make_float2(scale, scale);
-#pragma unroll
-  for (int i = 0; i < kLaneElems; i += 2) {           // two at a time
-    const float2 x = ptx::mul2(make_float2(g[i], g[i + 1]), by);
-    const float2 p = ptx::mul2(x, x);
-    const float2 t = ptx::add2(sum, p);
-    const float2 b = ptx::sub2(t, sum);
-    const float2 lost = ptx::add2(ptx::sub2(sum, ptx::sub2(t, b)), ptx::sub2(p, b));
-    err = ptx::add2(err, ptx::add2(lost, ptx::fma2(x, x, make_float2(-p.x, -p.y))));
-    sum = t;
+struct Squares {
+  float2 sum, err;
+  int e;                             // they are times 2^(2 (127 - e))
+
+  __device__ __forceinline__ void clear() {
+    sum = err = make_float2(0.0f, 0.0f);
+    e = 0;
   }
-  const double back = __longlong_as_double(static_cast<long long>(1023 + 2 * (e - 127)) << 52);
-  const double all = static_cast<double>(sum.x) + static_cast<double>(sum.y);
-  // (an infinite or NaN sum has no error term)
-  return (all + (isfinite(all) ? static_cast<double>(err.x) + static_cast<double>(err.y) : 0.0)) * back;
-}
+  __device__ __forceinline__ void add(const float (&g)[kLaneElems]) {
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kLaneElems; ++i) m = fmaxf(m, fabsf(g[i]));
+    const int em = min(static_cast<int>(__float_as_uint(m) >> 23), 253);
+    if (em > e) {
+      const float f = __uint_as_float(static_cast<uint32_t>(max(127 + e - em, 1)) << 23);   // 2^(e - em)
+      sum = make_float2(sum.x * f * f, sum.y * f * f);
+      err = make_float2(err.x * f * f, err.y * f * f);
+      e = em;
+    }
+    const float scale = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);              // 2^(127 - e)
+    const float2 by = make_float2(scale, scale);
+#pragma unroll
+    for (int i = 0; i < kLaneElems; i += 2) {         // two at a time
+      const float2 x = ptx::mul2(make_float2(g[i], g[i + 1]), by);
+      const float2 p = ptx::mul2(x, x);
+      const float2 t = ptx::add2(sum, p);
+      const float2 b = ptx::sub2(t, sum);
+      const float2 lost = ptx::add2(ptx::sub2(sum, ptx::sub2(t, b)), ptx::sub2(p, b));
+      err = ptx::add2(err, ptx::add2(lost, ptx::fma2(x, x, make_float2(-p.x, -p.y))));
+      sum = t;
+    }
+  }
+  __device__ __forceinline__ double value() const {
+    const double back = __longlong_as_double(static_cast<long long>(1023 + 2 * (e - 127)) << 52);
+    const double all = static_cast<double>(sum.x) + static_cast<double>(sum.y);
+    // (an infinite or NaN sum has no error term)
+    return (all + (isfinite(all) ? static_cast<double>(err.x) + static_cast<double>(err.y) : 0.0)) * back;
+  }
+};
 
 // Sums of squares of one matrix per blockIdx.y, a warp to 1024 neighbouring elements of a row
-// (a matrix without gaps is one long row).  Bound by the read of G.
-__global__ void __launch_bounds__(256) ortho_norm_kernel(const OrthoIn a) {
+// (a matrix without gaps is one long row), the next ones' loads under way meanwhile.  Bound by
+// the read of G.
+__global__ void __launch_bounds__(32 * kNormWarps, 2) ortho_norm_kernel(const OrthoIn a) {
   ptx::pdl_launch_dependents();      // the scaling kernel's reads of G
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) a.header->status = kStatusOk;
   if (blockIdx.x == 0)
-    for (int i = threadIdx.x; i < a.num_counters; i += 256)
+    for (int i = threadIdx.x; i < a.num_counters; i += 32 * kNormWarps)
       a.counters[static_cast<long long>(blockIdx.y) * a.num_counters + i] = 0;
   constexpr int kChunk = 32 * kLaneElems;
   const bool whole = a.row_stride == a.cols;
@@ -127,145 +149,194 @@ __global__ void __launch_bounds__(256) ortho_norm_kernel(const OrthoIn a) {
   const int chunks_per_row = static_cast<int>((cols + kChunk - 1) / kChunk);
   const long long chunks = static_cast<long long>(chunks_per_row) * (whole ? 1 : a.rows);
   const int lane = threadIdx.x % 32;
-  double sum = 0.0;
-  for (long long q = blockIdx.x * 8 + threadIdx.x / 32; q < chunks; q += gridDim.x * 8) {
+  // whole and aligned chunks come in vectors of 16 bytes: 8 of fp32, 4 of bf16; `vec` tells
+  uint32_t w[kLaneElems];
+  bool vec = false;
+  auto load = [&](long long q) {
     const long long row = whole ? 0 : q / chunks_per_row;
     const long long col = (q - row * chunks_per_row) * kChunk;
     const long long at = blockIdx.y * a.batch_stride + row * a.row_stride + col;
     const int n = static_cast<int>(min(cols - col, static_cast<long long>(kChunk)));
-    float g[kLaneElems];
     const char* p = static_cast<const char*>(a.grad) + at * (a.bf16 ? 2 : 4);
-    if (n == kChunk && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+    vec = n == kChunk && reinterpret_cast<uintptr_t>(p) % 16 == 0;
+    if (vec) {
       const uint4* v = reinterpret_cast<const uint4*>(p) + lane;
-      if (a.bf16) {
-        uint4 r[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) r[i] = v[32 * i];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            g[8 * i + 2 * k] = __uint_as_float(w[k] << 16);
-            g[8 * i + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-          }
-        }
-      } else {
-        uint4 r[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) r[i] = v[32 * i];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          g[4 * i] = __uint_as_float(r[i].x);
-          g[4 * i + 1] = __uint_as_float(r[i].y);
-          g[4 * i + 2] = __uint_as_float(r[i].z);
-          g[4 * i + 3] = __uint_as_float(r[i].w);
-        }
+      for (int i = 0; i < kLaneElems / 4; ++i) {
+        if (a.bf16 && i >= kLaneElems / 8) break;
+        const uint4 r = v[32 * i];
+        w[4 * i] = r.x;
+        w[4 * i + 1] = r.y;
+        w[4 * i + 2] = r.z;
+        w[4 * i + 3] = r.w;
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < kLaneElems; ++i) g[i] = lane + 32 * i < n ? grad_at(a, at + lane + 32 * i) : 0.0f;
+      for (int i = 0; i < kLaneElems; ++i)
+        w[i] = __float_as_uint(lane + 32 * i < n ? grad_at(a, at + lane + 32 * i) : 0.0f);
     }
-    sum += sum_of_squares(g);
+  };
+  double sum = 0.0;
+  Squares squares;
+  squares.clear();
+  const long long step = gridDim.x * kNormWarps;
+  long long q = blockIdx.x * kNormWarps + threadIdx.x / 32;
+  if (q < chunks) load(q);
+  for (int n = 1; q < chunks; ++n) {
+    float g[kLaneElems];
+    if (vec && a.bf16) {
+#pragma unroll
+      for (int i = 0; i < kLaneElems / 2; ++i) {
+        g[2 * i] = __uint_as_float(w[i] << 16);
+        g[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLaneElems; ++i) g[i] = __uint_as_float(w[i]);
+    }
+    q += step;
+    if (q < chunks) load(q);
+    squares.add(g);
+    if (n % kFlush == 0) {
+      sum += squares.value();
+      squares.clear();
+    }
   }
+  sum += squares.value();
 #pragma unroll
   for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
-  __shared__ double part[8];
+  __shared__ double part[kNormWarps];
   if (lane == 0) part[threadIdx.x / 32] = sum;
   __syncthreads();
   if (threadIdx.x == 0) {
-    for (int w = 1; w < 8; ++w) sum += part[w];
+    for (int w = 1; w < kNormWarps; ++w) sum += part[w];
     a.norm[blockIdx.y * a.norm_blocks + blockIdx.x] = sum;
   }
 }
 
-// X^T times s / |G|, split into two fp16 numbers, by 64 x 64 tiles of G.  Bound by the read of G
-// and the two writes.
-__global__ void __launch_bounds__(256) ortho_scale_kernel(const OrthoIn a) {
+// X^T times s / |G|, split into two fp16 numbers, by 64 x 64 tiles of G, a.tiles_of_block
+// neighbouring ones to a block, the next tile's loads under way while one is written.  Bound by the read of
+// G and the two writes.
+__global__ void __launch_bounds__(256, kScaleBlocks) ortho_scale_kernel(const OrthoIn a) {
   __shared__ float tile[64][65];
   __shared__ double factor;
   const int tid = threadIdx.x;
-  const int row0 = blockIdx.y * 64, col0 = blockIdx.x * 64;
   const int es = a.bf16 ? 2 : 4;
-  const char* base = static_cast<const char*>(a.grad) +
-                     (blockIdx.z * a.batch_stride + static_cast<long long>(row0) * a.row_stride + col0) * es;
+  const int z = blockIdx.y;
+  const int across = (a.cols + 63) / 64, share = a.tiles_of_block;
+  int t = blockIdx.x * share;
+  const int end = min(t + share, across * ((a.rows + 63) / 64));
+  if (t >= end) return;
+  int row0 = t / across * 64, col0 = t % across * 64;
   const long long row_bytes = a.row_stride * es;
-  if (row0 + 64 <= a.rows && col0 + 64 <= a.cols && reinterpret_cast<uintptr_t>(base) % 16 == 0 && row_bytes % 16 == 0) {
-    // 16 bytes a thread: 4 rows of 64 numbers at once in a warp for bf16, 2 for fp32
-    const int per = a.bf16 ? 8 : 4;                  // numbers of a vector
-    const int line = 64 / per, rows = 256 / line;    // threads to a row, rows at once
-    const int cx = tid % line * per, ry = tid / line;
-    uint4 v[4];
+
+  // A tile whole and aligned comes in vectors of 16 bytes: 4 rows of 64 numbers at once in a
+  // warp for bf16, 2 for fp32.  Any other: thread = column, every fourth row.
+  uint32_t w[16];
+  const int per = a.bf16 ? 8 : 4;                    // numbers of a vector
+  const int line = 64 / per, rows_at_once = 256 / line;
+  auto load = [&]() -> bool {
+    const char* base = static_cast<const char*>(a.grad) +
+                       (blockIdx.y * a.batch_stride + static_cast<long long>(row0) * a.row_stride + col0) * es;
+    const bool whole = row0 + 64 <= a.rows && col0 + 64 <= a.cols &&
+                       (reinterpret_cast<uintptr_t>(base) | static_cast<uintptr_t>(row_bytes)) % 16 == 0;
+    if (whole) {
+      const char* p = base + tid / line * row_bytes + tid % line * 16;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (ry + k * rows < 64) v[k] = *reinterpret_cast<const uint4*>(base + (ry + k * rows) * row_bytes + cx * es);
+      for (int k = 0; k < 4; ++k) {
+        if (a.bf16 && k >= 2) break;
+        const uint4 v = *reinterpret_cast<const uint4*>(p + k * rows_at_once * row_bytes);
+        w[4 * k] = v.x;
+        w[4 * k + 1] = v.y;
+        w[4 * k + 2] = v.z;
+        w[4 * k + 3] = v.w;
+      }
+    } else {
+      const int cx = tid % 64, ry = tid / 64;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (ry + k * rows >= 64) continue;
-      float* t = &tile[ry + k * rows][cx];
-      const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+      for (int k = 0; k < 16; ++k) {
+        const bool in = row0 + ry + 4 * k < a.rows && col0 + cx < a.cols;
+        const char* p = base + (ry + 4 * k) * row_bytes + cx * es;
+        w[k] = !in ? 0u : a.bf16 ? static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(p)) << 16
+                                 : *reinterpret_cast<const uint32_t*>(p);
+      }
+    }
+    return whole;
+  };
+  bool whole = load();
+  ptx::pdl_wait_prior_grid();        // the norm kernel has ended
+  float f1 = 0.0f, f3 = 0.0f;
+  for (bool first = true;; first = false) {
+    if (whole) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (a.bf16) {
-          t[2 * q] = __uint_as_float(w[q] << 16);
-          t[2 * q + 1] = __uint_as_float(w[q] & 0xffff0000u);
-        } else {
-          t[q] = __uint_as_float(w[q]);
+      for (int k = 0; k < 4; ++k) {
+        if (a.bf16 && k >= 2) break;
+        float* to = &tile[tid / line + k * rows_at_once][tid % line * per];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (a.bf16) {
+            to[2 * q] = __uint_as_float(w[4 * k + q] << 16);
+            to[2 * q + 1] = __uint_as_float(w[4 * k + q] & 0xffff0000u);
+          } else {
+            to[q] = __uint_as_float(w[4 * k + q]);
+          }
         }
       }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) tile[tid / 64 + 4 * k][tid % 64] = __uint_as_float(w[k]);
     }
-  } else {
-    const int cx = tid % 64, ry = tid / 64;
-    float v[16];
+    if (first && tid < 32) {
+      double sum = 0.0;
+      for (int i = tid; i < a.norm_blocks; i += 32) sum += a.norm[z * a.norm_blocks + i];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const bool in = row0 + ry + 4 * k < a.rows && col0 + cx < a.cols;
-      const char* p = base + (ry + 4 * k) * row_bytes + cx * es;
-      v[k] = !in ? 0.0f : a.bf16 ? __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(p))
-                                 : *reinterpret_cast<const float*>(p);
+      for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
+      if (tid == 0) factor = sum == 0.0 ? 0.0 : a.s / sqrt(sum);   // a zero matrix stays zero
     }
-#pragma unroll
-    for (int k = 0; k < 16; ++k) tile[ry + 4 * k][cx] = v[k];
-  }
-  ptx::pdl_wait_prior_grid();        // the norm kernel has ended
-  if (tid < 32) {
-    double sum = 0.0;
-    for (int i = tid; i < a.norm_blocks; i += 32) sum += a.norm[blockIdx.z * a.norm_blocks + i];
-#pragma unroll
-    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
-    if (tid == 0) factor = sum == 0.0 ? 0.0 : a.s / sqrt(sum);   // a zero matrix stays zero
-  }
-  __syncthreads();
-  // factor = f1 f2 with f1 a power of two, so that neither product leaves fp32's range
-  int e;
-  const float f2 = static_cast<float>(frexp(factor, &e));
-  const int e1 = min(max(e, -120), 120);
-  const float f1 = ldexpf(1.0f, e1);
-  const float f3 = ldexpf(f2, min(max(e - e1, -126), 126));
-  // the r index is G's column where G is tall, else its row
-  const int outer0 = a.tall ? row0 : col0, inner0 = a.tall ? col0 : row0;
-  const int outers = a.tall ? a.rows : a.cols, inners = a.tall ? a.cols : a.rows;
-  const int x = tid % 8 * 8;
-  if (inner0 + x >= a.ld) return;
-#pragma unroll
-  for (int k = tid / 8; k < 64; k += 32) {
-    if (outer0 + k >= outers) break;
-    uint32_t hi[4], lo[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float v[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int in = x + 2 * q + h;
-        v[h] = inner0 + in < inners ? (a.tall ? tile[k][in] : tile[in][k]) * f1 * f3 : 0.0f;
+    __syncthreads();
+    if (first) {
+      // factor = f1 f2 with f1 a power of two, so that neither product leaves fp32's range
+      int e;
+      const float f2 = static_cast<float>(frexp(factor, &e));
+      const int e1 = min(max(e, -120), 120);
+      f1 = ldexpf(1.0f, e1);
+      f3 = ldexpf(f2, min(max(e - e1, -126), 126));
+    }
+    // the r index is G's column where G is tall, else its row
+    const int outer0 = a.tall ? row0 : col0, inner0 = a.tall ? col0 : row0;
+    if (++t < end) {
+      if ((col0 += 64) >= a.cols) {
+        col0 = 0;
+        row0 += 64;
       }
-      hi[q] = pack_half(v[0], v[1]);
-      const float2 kept = unpack_half(hi[q]);
-      lo[q] = pack_half(v[0] - kept.x, v[1] - kept.y);
+      whole = load();
     }
-    const long long at = blockIdx.z * a.x_batch + static_cast<long long>(outer0 + k) * a.ld + inner0 + x;
-    *reinterpret_cast<uint4*>(a.xt + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4*>(a.xl + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    const int outers = a.tall ? a.rows : a.cols, inners = a.tall ? a.cols : a.rows;
+    const int x = tid % 8 * 8;
+    if (inner0 + x < a.ld) {
+#pragma unroll
+      for (int k = tid / 8; k < 64; k += 32) {
+        if (outer0 + k >= outers) break;
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float v[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int in = x + 2 * q + h;
+            v[h] = inner0 + in < inners ? (a.tall ? tile[k][in] : tile[in][k]) * f1 * f3 : 0.0f;
+          }
+          hi[q] = pack_half(v[0], v[1]);
+          const float2 kept = unpack_half(hi[q]);
+          lo[q] = pack_half(v[0] - kept.x, v[1] - kept.y);
+        }
+        const long long to = z * a.x_batch + static_cast<long long>(outer0 + k) * a.ld + inner0 + x;
+        *reinterpret_cast<uint4*>(a.xt + to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(a.xl + to) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+    }
+    if (t >= end) break;
+    __syncthreads();                 // the tile has been read
   }
 }
 
@@ -1216,12 +1287,16 @@ cudaError_t launch_orthogonalize(const OrthoCall& q, cudaStream_t stream) {
   a.split[kPoly] = sh.split_poly;
 
   const unsigned batch = static_cast<unsigned>(sh.batch);
-  ortho_norm_kernel<<<dim3(sh.norm_blocks, batch), 256, 0, stream>>>(in);
+  int dev = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  const int64_t tiles = (sh.cols + 63) / 64 * ((sh.rows + 63) / 64);
+  in.tiles_of_block = static_cast<int>((tiles * sh.batch + 2 * kScaleBlocks * g_pairs[dev] - 1) / (2 * kScaleBlocks * g_pairs[dev]));
+  ortho_norm_kernel<<<dim3(sh.norm_blocks, batch), 32 * kNormWarps, 0, stream>>>(in);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   {
     // may start while the norm kernel runs; it waits for it before it needs the norm
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((in.cols + 63) / 64, (in.rows + 63) / 64, batch);
+    cfg.gridDim = dim3((tiles + in.tiles_of_block - 1) / in.tiles_of_block, batch);
     cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
@@ -1232,8 +1307,6 @@ cudaError_t launch_orthogonalize(const OrthoCall& q, cudaStream_t stream) {
     if ((e = cudaLaunchKernelEx(&cfg, ortho_scale_kernel, in)) != cudaSuccess) return e;
   }
 
-  int dev = 0;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   const int64_t most = sh.batch * std::max(nr * nc, nr * (nr + 1) / 2 * std::max(sh.split_gram, sh.split_poly));
   const int pairs = static_cast<int>(std::min<int64_t>(most, g_pairs[dev]));
   if (pairs < 1) return cudaErrorLaunchOutOfResources;

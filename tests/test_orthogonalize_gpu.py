@@ -147,6 +147,22 @@ def test_zero_and_not_finite_matrices_of_a_batch():
     check(X[[0, 4]], G[[0, 4]])
 
 
+@pytest.mark.parametrize("kind", ["rising", "falling", "shuffled"])
+@pytest.mark.parametrize("base", [1e-30, 1.0, 1e30])
+@pytest.mark.parametrize("rows,cols", [(1, 400000), (2, 400001), (37, 20000), (300, 40)])
+def test_norm_of_wide_ranges(rows, cols, base, kind):
+    """One step with (1, 0, 0) is G / |G|.  Its magnitudes span 2^-24 to 1 across the elements, so
+    more than 1/100 of them (N) carry the norm.  The factor that the result has of G is off by the
+    mean of N independent roundings of 2^-9 / sqrt(3) at most: six times that and 2^-20."""
+    x = torch.linspace(-24, 0, rows * cols, device=DEV)
+    x = x.flip(0) if kind == "falling" else x[torch.randperm(x.numel(), device=DEV)] if kind == "shuffled" else x
+    G = (torch.exp2(x) * torch.where(torch.rand_like(x) < 0.5, -base, base)).reshape(rows, cols)
+    got = ewg.orthogonalize_update(G, steps=1, coefficients=(1.0, 0.0, 0.0), check=True).double()
+    G = G.double() / base
+    factor = ((got * G).sum() / (G * G).sum() * G.norm()).item()
+    assert abs(factor - 1) < 6 * 2 ** -9 / math.sqrt(3 * G.numel() / 100) + 2 ** -20
+
+
 @pytest.mark.parametrize("steps", [1, 2, 3, 8])
 def test_steps_and_coefficients(steps):
     G = randn(200, 333)
