@@ -377,8 +377,8 @@ constexpr size_t kGemmSmem =
 static_assert(kWarpCols == 128 && kPieces == 2, "a warp's columns, as the epilogue takes them");
 static_assert(kWarpsOfBlock == kOrthoWarps && kBlock == kOrthoBlock, "as the workspace is laid out for");
 static_assert(kGemmSmem + 512 <= 227 * 1024, "stages and slots fit in shared memory");
-constexpr uint32_t kWaitLimit = 1u << 22;
-constexpr uint32_t kReadyLimit = 1u << 22;
+constexpr unsigned long long kWaitLimit = 4000000000ull;      // of a wait, in ns
+constexpr uint32_t kPollLimit = 1u << 30;
 
 enum Phase { kGram = 0, kPoly = 1, kUpdate = 2 };
 
@@ -412,6 +412,7 @@ struct GemmSmem {
   uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
   uint64_t piece[kEpilogueWarps][2], own_full, a_full;
   int units_done[kEpilogueWarps];    // units an epilogue warp is through with its slot for
+  int units_ready;                   // units whose inputs are there
   uint32_t tmem;
   int abort;
 };
@@ -484,13 +485,29 @@ __device__ __forceinline__ int* ready_at(const OrthoArgs& a, int phase, int z, i
   return a.ready + (static_cast<long long>(z) * 3 + phase) * nr + I;
 }
 
+// Whether a wait is to end without what it waits for: `abort` is set, or it has lasted for
+// seconds.  Looked at once in 64 polls.  (The longest wait of a call that goes well is for most of
+// a phase: 0.3 s for the largest matrices that memory holds.)
+struct Patience {
+  unsigned long long since = 0;
+  __device__ __forceinline__ bool over(uint32_t poll, volatile int* abort) {
+    if ((poll & 63u) != 63u) return false;
+    unsigned long long now;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+    if (since == 0) since = now;
+    return *abort || now - since > kWaitLimit;
+  }
+};
+
 __device__ bool wait_ready(const OrthoArgs& a, const int* p, int want, volatile int* abort) {
-  for (uint32_t n = 0; n < kReadyLimit; ++n) {
+  Patience patience;
+  for (uint32_t n = 0; n < kPollLimit; ++n) {
     int v;
     asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
     if (v >= want) return true;
-    if ((n & 255u) == 255u &&
-        (*abort || *reinterpret_cast<volatile int*>(&a.header->status) == kStatusTimeout))
+    if (want - v > kWarpsOfBlock) __nanosleep(200);  // far from it: polls hold up who counts
+    if (patience.over(n, abort) ||
+        ((n & 255u) == 255u && *reinterpret_cast<volatile int*>(&a.header->status) == kStatusTimeout))
       return false;
   }
   return false;
@@ -533,22 +550,22 @@ __device__ __forceinline__ void unit_done(const OrthoArgs& a, int phase, const U
 
 // Waits for the phase of `bar` with the given parity; false if it gave up.
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+  Patience patience;
+  for (uint32_t i = 0; i < kPollLimit; ++i) {
     if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
-    if ((i & 63u) == 63u && *abort) return false;
+    if (patience.over(i, abort)) return false;
   }
   return false;
 }
 
 // Waits for a count in shared memory.
 __device__ __forceinline__ bool wait_count(volatile int* count, int want, volatile int* abort) {
-  for (uint32_t i = 0; i < kWaitLimit; ++i) {
-    if (*count >= want) {
-      __threadfence_block();
-      return true;
-    }
-    if ((i & 63u) == 63u && *abort) return false;
-    __nanosleep(20);
+  Patience patience;
+  for (uint32_t i = 0; i < kPollLimit; ++i) {
+    int v;
+    asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];" : "=r"(v) : "r"(ptx::smem_u32(const_cast<int*>(count))) : "memory");
+    if (v >= want) return true;
+    if (patience.over(i, abort)) return false;
   }
   return false;
 }
@@ -939,7 +956,8 @@ __device__ __forceinline__ uint32_t idesc_of(Majors mn) {
 // the matrices of a batch) overlap without a barrier over the grid.  Per CTA: warp 0 copies
 // operands (TMA), warp 1 of the pair's first CTA issues the products, the epilogue warps take
 // finished accumulators (two in tensor memory, so that the products of the next unit run
-// meanwhile), warp 2 copies in what those read beside the products.
+// meanwhile), warp 2 copies in what those read beside the products, warp 3 watches what units
+// wait for.
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const OrthoArgs a) {
   extern __shared__ unsigned char raw[];
@@ -963,6 +981,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     ptx::mbar_init(&sm.own_full, 1);
     ptx::mbar_init(&sm.a_full, kWarpsOfBlock);
     for (int i = 0; i < kEpilogueWarps; ++i) sm.units_done[i] = 0;
+    sm.units_ready = 0;
     sm.abort = 0;
     ptx::fence_mbar_init();
     ptx::prefetch_tensor_map(&maps.xt[0]);
@@ -1018,7 +1037,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 
   if (warp == 0) {
     if (lane == 0) {
+      int units = 0;
       for_units([&](int phase, int step, const Unit& x) {
+        ++units;
         if (a.fused && phase == kPoly) return true;   // its operands are there
         const int cur = step & 1;
         // X X^T: X, X.  A A: A, A.  Update: X^T (rows J), B (rows I).
@@ -1028,8 +1049,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         const int rb = (phase == kUpdate ? x.I : x.J) * kBlock + rank * 128;
         int k0, k1;
         inner_of(a, phase, x, k0, k1);
-        if (!wait_inputs(a, phase, step, x, abort)) return false;
-        ptx::fence_proxy_async();    // the acquires above before the tensor copies
+        if (!wait_count(&sm.units_ready, units, abort)) return false;
         for (int kb = k0; kb < k1; ++kb) {
           if (!wait_bar(&sm.empty[stage], stage_phase ^ 1u, abort)) return false;
           if (rank == 0) ptx::mbar_arrive_expect_tx(&sm.full[stage], 2 * kStageBytes);
@@ -1103,8 +1123,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     const int w = lane < kEpilogueWarps ? lane : 0;
     int units = 0;
     for_units([&](int phase, int step, const Unit& x) {
-      bool ok = phase == kGram || lane != 0 || wait_inputs(a, phase, step, x, abort);
-      ok = ok && wait_count(&sm.units_done[w], units++, abort);
+      bool ok = wait_count(&sm.units_done[w], units++, abort);
+      ok = ok && (phase == kGram || wait_count(&sm.units_ready, units, abort));
       if (!__all_sync(kAll, ok)) return false;
       if (phase == kUpdate) {        // a + what is left of B_ii: eight columns a lane
         const int col = x.I * kBlock + 8 * lane;
@@ -1119,7 +1139,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         if (lane == 0) ptx::mbar_arrive(&sm.own_full);
       }
       if (phase != kGram && !(a.fused && phase == kPoly) && lane < kEpilogueWarps) {
-        ptx::fence_proxy_async();    // the acquires above before the tensor copies
         const Place at = place_of(phase, x, rank, w);
         const int n = min(pieces_of(a, phase, at, phase == kPoly ? kPiece : kStrip), 2);
         for (int u = 0; u < n; ++u) {
@@ -1130,6 +1149,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       __syncwarp();
       return true;
     });
+  } else if (warp == 3) {
+    // Watches what units wait for, ahead of the copies: a poll of L2 and the fence take 0.7 us, in
+    // which the ring of operands would run low at the start of each unit (24 x 1024 x 1024: 516 us
+    // so, 548 where warps 0 and 2 poll; 256 x 256, which only waits: 108 and 105).
+    if (lane == 0) {
+      int units = 0;
+      for_units([&](int phase, int step, const Unit& x) {
+        if (!wait_inputs(a, phase, step, x, abort)) return false;
+        ptx::fence_proxy_async();    // the acquires above before the tensor copies
+        asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(ptx::smem_u32(&sm.units_ready)), "r"(++units) : "memory");
+        return true;
+      });
+    }
+    __syncwarp();
   } else if (warp >= kFirstEpilogueWarp) {
     const int index = warp - kFirstEpilogueWarp;
     const int quarter = warp % 4, part = index / 4;
@@ -1153,7 +1186,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   if (__syncthreads_or(*abort)) {
     if (warp == 1 && rank == 0 && lane == 0) {
       ptx::mma_commit_pair(&sm.drained);
-      for (uint32_t n = 0; n < kWaitLimit && !ptx::mbar_try_wait_cluster(&sm.drained, 0); ++n) {}
+      for (uint32_t n = 0; n < (1u << 22) && !ptx::mbar_try_wait_cluster(&sm.drained, 0); ++n) {}
     }
     // copies already issued land within microseconds; which of them a barrier of the pair
     // still counts is not known after a give-up, so they get a millisecond
