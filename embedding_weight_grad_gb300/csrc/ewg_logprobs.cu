@@ -16,7 +16,9 @@
 // terms where a row is all but sure of one token: log p_t and the entropy of such a row are
 // about -R, and 1 + R in 32 bits would round R away.
 //
-// Both kernels are bound by the one read of the logits (and the one write of the gradient).
+// Both kernels are bound by the one read of the logits (and the one write of the gradient):
+// 8192 x 129280 bf16 takes 294 us (7.2 TB/s; 349 with 8 alternatives, whose logits are mostly
+// gone from L2 when they are read again), its gradient 600 us (7.1 TB/s).
 #include <cfloat>
 
 #include <cooperative_groups.h>
