@@ -386,7 +386,7 @@ enum Phase { kGram = 0, kPoly = 1, kUpdate = 2 };
 
 struct OrthoMaps {
   CUtensorMap xt[2], a[2], b;        // operands: boxes of 64 x 64
-  CUtensorMap xt_strip[2], xl_strip;         // 32 of the r index x 32
+  CUtensorMap x_strip[2];                    // 32 of the r index x 32, of X^T and of its rest
   CUtensorMap a_piece[2], b_piece;           // 64 x 32
 };
 
@@ -543,8 +543,9 @@ __device__ __forceinline__ void unit_done(const OrthoArgs& a, int phase, const U
     *units_done = *units_done + 1;
     if (signal) {
       ptx::bulk_wait();              // its copies' writes are done, and visible to it
-      ptx::red_release_add(ready_at(a, phase, x.z, x.I), 1);
-      if (phase != kUpdate && x.I != x.J) ptx::red_release_add(ready_at(a, phase, x.z, x.J), 1);
+      ptx::fence_acq_rel_gpu();
+      ptx::red_relaxed_add(ready_at(a, phase, x.z, x.I), 1);
+      if (phase != kUpdate && x.I != x.J) ptx::red_relaxed_add(ready_at(a, phase, x.z, x.J), 1);
     }
   }
   __syncwarp();
@@ -634,8 +635,7 @@ __device__ __forceinline__ void request_strip(const OrthoMaps& maps, int step, i
                                               uint32_t slot, uint64_t* bars) {
   const uint32_t to = slot + u % 2 * kHalfStride;
   ptx::mbar_arrive_expect_tx(&bars[u % 2], 2 * kStripBytes);
-  ptx::tma_load_3d(to, &maps.xt_strip[step & 1], at.col + u * kStrip, at.row, z, &bars[u % 2]);
-  ptx::tma_load_3d(to + kStripBytes, &maps.xl_strip, at.col + u * kStrip, at.row, z, &bars[u % 2]);
+  ptx::tma_load_4d(to, &maps.x_strip[step & 1], at.col + u * kStrip, at.row, z, 0, &bars[u % 2]);
 }
 
 __device__ __forceinline__ uint4 lds_v4(uint32_t at) {
@@ -777,8 +777,7 @@ __device__ __forceinline__ bool epilogue_update(const OrthoMaps& maps, const Ort
         request_strip(maps, step, x.z, at, u + 1, in.slot, in.bars);
       }
       if (!last) {
-        ptx::tma_store_3d(&maps.xt_strip[cur ^ 1], at.col + u * kStrip, at.row, x.z, strip);
-        ptx::tma_store_3d(&maps.xl_strip, at.col + u * kStrip, at.row, x.z, strip + kStripBytes);
+        ptx::tma_store_4d(&maps.x_strip[cur ^ 1], at.col + u * kStrip, at.row, x.z, 0, strip);
         ptx::bulk_commit();
       }
     }
@@ -1218,14 +1217,18 @@ using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
 EncodeTiled g_encode = nullptr;
 int g_pairs[64] = {};                // per device: pairs resident at once
 
-// [batch][outer][ld] fp16 with r columns used, in boxes of box_cols x box_rows, swizzled by their rows' bytes.
-cudaError_t encode(CUtensorMap* map, void* p, const OrthoShape& sh, int64_t outer, int box_cols, int box_rows) {
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(sh.r), static_cast<cuuint64_t>(outer),
-                              static_cast<cuuint64_t>(sh.batch)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(sh.ld * 2), static_cast<cuuint64_t>(sh.ld * outer * 2)};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1}, step[3] = {1, 1, 1};
-  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, p, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+// [batch][outer][ld] fp16 with r columns used, in boxes of box_cols x box_rows, swizzled by their
+// rows' bytes; with `rest`, of this array and of one `rest` bytes behind it.
+cudaError_t encode(CUtensorMap* map, void* p, const OrthoShape& sh, int64_t outer, int box_cols, int box_rows, size_t rest) {
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(sh.r), static_cast<cuuint64_t>(outer),
+                              static_cast<cuuint64_t>(sh.batch), 2};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(sh.ld * 2), static_cast<cuuint64_t>(sh.ld * outer * 2), rest};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1, 2};
+  const cuuint32_t step[4] = {1, 1, 1, 1};
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rest ? 4 : 3, p, dims, strides, box, step,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
@@ -1289,16 +1292,15 @@ cudaError_t launch_orthogonalize(const OrthoCall& q, cudaStream_t stream) {
 
   OrthoMaps maps;
   cudaError_t e = cudaSuccess;
-  auto add = [&](CUtensorMap* map, size_t at, int64_t outer, int box_cols, int box_rows) {
-    if (e == cudaSuccess) e = encode(map, ws + at, sh, outer, box_cols, box_rows);
+  auto add = [&](CUtensorMap* map, size_t at, int64_t outer, int box_cols, int box_rows, size_t rest = 0) {
+    if (e == cudaSuccess) e = encode(map, ws + at, sh, outer, box_cols, box_rows, rest);
   };
   for (int i = 0; i < 2; ++i) {
     add(&maps.xt[i], L.xt[i], sh.c, 64, 64);
-    add(&maps.xt_strip[i], L.xt[i], sh.c, kStrip, 32);
+    add(&maps.x_strip[i], L.xt[i], sh.c, kStrip, 32, L.xl - L.xt[i]);
     add(&maps.a[i], L.a[i], sh.r, 64, 64);
     add(&maps.a_piece[i], L.a[i], sh.r, kPiece, 32);
   }
-  add(&maps.xl_strip, L.xl, sh.c, kStrip, 32);
   add(&maps.b, L.b, sh.r, 64, 64);
   add(&maps.b_piece, L.b, sh.r, kPiece, 32);
   if (e != cudaSuccess) return e;
