@@ -581,6 +581,125 @@ __global__ void __launch_bounds__(threads_of(kT), blocks_per_sm<T>(kT)) logprobs
   }
 }
 
+// Forward kernel of short rows without alternatives: kG lanes hold a row of up to kHeld kG
+// vectors in registers, a warp 32 / kG rows.  Such rows are bound by the instructions that each
+// costs a warp, most of them in the reductions, which here serve several rows at once; and with
+// the whole row at hand the maximum comes first and nothing is rescaled.  131072 x 1024 bf16
+// takes 45.6 us (5.9 TB/s; 52 where the rows are all but sure of a token), a warp a row 61.7
+// (76); 262144 x 512 45.3 and 120; 65536 x 2048 45.8 and 48.8.
+constexpr int kHeld = 8;
+
+template <typename T, int kG>
+__global__ void __launch_bounds__(256, 4) logprobs_short_kernel(const LogprobsArgs a) {
+  using V = Vec<T>;
+  constexpr int kE = V::kE;
+  constexpr int kEdges = (2 * (kE - 1) + kG - 1) / kG;
+  if (a.status && blockIdx.x == 0) report_targets(a.targets, a.targets_int64, a.n, a.V, a.status, blockDim.x);
+  const int lane = threadIdx.x % kG;
+  const long long mine = static_cast<long long>(blockIdx.x) * (256 / kG) + threadIdx.x / kG;
+  const long long row = min(mine, static_cast<long long>(a.n) - 1);    // all lanes stay for the reductions
+  const T* z = static_cast<const T*>(a.logits) + row * a.row_stride;
+  const int head = min(static_cast<int>((16 - reinterpret_cast<uintptr_t>(z) % 16) % 16 / sizeof(T)), a.V);
+  const int nv = (a.V - head) / kE, edges = a.V - nv * kE;
+  const int most = a.V / kE;         // of any row
+  const uint4* zv = reinterpret_cast<const uint4*>(z + head);
+  uint4 r[kHeld];
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u)
+    r[u] = lane + u * kG < nv ? load16(zv + lane + u * kG) : make_uint4(V::kNegInf, V::kNegInf, V::kNegInf, V::kNegInf);
+  float edge[kEdges];
+#pragma unroll
+  for (int u = 0; u < kEdges; ++u) {
+    const int e = lane + u * kG;
+    edge[u] = e < edges ? V::load1(z + (e < head ? e : nv * kE + e)) : -INFINITY;
+  }
+  const long long target = target_of(a.targets, a.targets_int64, row);
+  float z_target = 0.0f;
+  if (lane == 0 && target >= 0 && target < a.V) z_target = V::load1(z + target);
+
+  uint4 mx = r[0];
+#pragma unroll
+  for (int u = 1; u < kHeld; ++u) mx = V::elementwise_max(mx, r[u]);
+  const float held = fmaxf(V::max_of(mx), -FLT_MAX);          // the lane's vectors' maximum
+  float M = held;
+#pragma unroll
+  for (int u = 0; u < kEdges; ++u) M = fmaxf(M, edge[u]);
+#pragma unroll
+  for (int d = kG / 2; d; d /= 2) M = fmaxf(M, __shfl_xor_sync(kAll, M, d));
+
+  const float c = a.scale_log2;
+  const float2 c2 = make_float2(c, c), minus_m = make_float2(-M, -M);
+  float2 S2 = make_float2(0.f, 0.f), T2 = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u) {
+    if (u * kG >= most) break;
+#pragma unroll
+    for (int i = 0; i < kE / 2; ++i) {
+      float2 t = ptx::mul2(ptx::add2(V::pair(r[u], i), minus_m), c2);
+      t.x = max_nan(t.x, kLowestExponent);
+      t.y = max_nan(t.y, kLowestExponent);
+      const float2 e = make_float2(ex2(t.x), ex2(t.y));
+      S2 = ptx::add2(S2, e);
+      T2 = ptx::fma2(e, t, T2);
+    }
+  }
+  // One occurrence of the maximum is held out: an edge element's whole term, or 1 off the sum of
+  // the first lane that holds it.
+  float S = S2.x + S2.y, Tt = T2.x + T2.y, S_edge = 0.0f;
+  bool edge_has = false;
+#pragma unroll
+  for (int u = 0; u < kEdges; ++u) {
+    const float x = max_nan((edge[u] - M) * c, kLowestExponent);
+    const float e = ex2(x);
+    if (edge[u] == M && !edge_has) edge_has = true; else S_edge += e;
+    Tt = fmaf(e, x, Tt);
+  }
+  const int first_lane = threadIdx.x % 32 - lane;             // of the group, in the warp
+  const unsigned group = (kG == 32 ? kAll : (1u << kG % 32) - 1u) << first_lane;
+  const unsigned edges_have = __ballot_sync(kAll, edge_has) & group;
+  const unsigned lanes_have = __ballot_sync(kAll, held == M) & group;
+  const int owner = edges_have || !lanes_have ? -1 : __ffs(lanes_have) - 1 - first_lane;
+  if (edge_has && __ffs(edges_have) - 1 != static_cast<int>(threadIdx.x % 32)) S_edge += 1.0f;   // not the first
+  float own = S - 1.0f;
+  S = (lane == owner ? 0.0f : S) + S_edge;
+#pragma unroll
+  for (int d = kG / 2; d; d /= 2) {
+    S += __shfl_xor_sync(kAll, S, d);
+    Tt += __shfl_xor_sync(kAll, Tt, d);
+  }
+  own = __shfl_sync(kAll, own, max(owner, 0), kG);
+  own = owner < 0 ? 0.0f : own;
+  const bool again = owner >= 0 && S + own < 8.0f;
+  if (__any_sync(kAll, again)) {     // the owner's other terms, which that 1 drowned, a lane to each vector
+    float rest = 0.0f, equal = 0.0f;
+    if (again) {
+      for (int v = owner + lane * kG; v < nv; v += kG * kG) {
+        const uint4 raw = load16(zv + v);
+#pragma unroll
+        for (int i = 0; i < kE / 2; ++i) {
+          const float2 p = V::pair(raw, i);
+          if (p.x == M) equal += 1.0f; else rest += ex2(max_nan((p.x - M) * c, kLowestExponent));
+          if (p.y == M) equal += 1.0f; else rest += ex2(max_nan((p.y - M) * c, kLowestExponent));
+        }
+      }
+    }
+#pragma unroll
+    for (int d = kG / 2; d; d /= 2) {
+      rest += __shfl_xor_sync(kAll, rest, d);
+      equal += __shfl_xor_sync(kAll, equal, d);
+    }
+    if (again) own = rest + (equal - 1.0f);
+  }
+  const float R = S + own;
+  if (lane != 0 || mine >= a.n) return;
+  const bool padding = target < 0, empty = R == -1.0f;
+  const float log_sum = empty || padding ? 0.0f : log1pf(R);
+  a.logprobs[row] = padding ? 0.0f : target >= a.V ? NAN : empty ? -INFINITY : (z_target - M) * a.scale - log_sum;
+  a.entropy[row] = empty || padding ? 0.0f : log_sum - Tt * kLn2 / (1.0f + R);
+  a.row_max[row] = padding ? 0.0f : empty ? -INFINITY : M;
+  a.log_sum[row] = log_sum;
+}
+
 // Gradient kernel: kT threads take kBatch * kT vectors of a row (kT = 32: a warp, eight
 // items to a block).  Items of one row are neighbours.  The vectors are the 16-byte ones of
 // the gradient's row; a logits row of another alignment is read as two vectors each, put
@@ -729,6 +848,12 @@ cudaError_t launch_forward(const LogprobsArgs& a, int cluster, cudaStream_t stre
   return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, kT>, a);
 }
 
+template <typename T, int kG>
+cudaError_t launch_short(const LogprobsArgs& a, cudaStream_t stream) {
+  logprobs_short_kernel<T, kG><<<static_cast<unsigned>((a.n + 256LL / kG - 1) / (256 / kG)), 256, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
 template <typename T>
 cudaError_t launch_forward_of(const LogprobsArgs& a, int num_sms, cudaStream_t stream) {
   // Threads of a row by its vectors and by whether there are rows enough to fill the device
@@ -747,6 +872,12 @@ cudaError_t launch_forward_of(const LogprobsArgs& a, int num_sms, cudaStream_t s
   // ones few threads leave each with more vectors to read again for the alternatives.
   const int nv = a.V / Vec<T>::kE;
   const bool many = a.n >= 16 * num_sms;
+  // (kHeld vectors a lane are what 64 registers a thread hold)
+  if (!a.top && nv <= 32 * kHeld)
+    return nv <= 4 * kHeld    ? launch_short<T, 4>(a, stream)
+           : nv <= 8 * kHeld  ? launch_short<T, 8>(a, stream)
+           : nv <= 16 * kHeld ? launch_short<T, 16>(a, stream)
+                              : launch_short<T, 32>(a, stream);
   if (nv <= 128 || (nv <= 1024 && many)) return launch_forward<T, 32>(a, 1, stream);
   if (nv <= 1024 || (nv < 4096 && a.n >= num_sms)) return launch_forward<T, 128>(a, 1, stream);
   if (a.n >= num_sms && (nv <= 12288 || (many && !a.top && nv <= 32768))) return launch_forward<T, 256>(a, 1, stream);

@@ -128,6 +128,42 @@ def test_many_rows(n, V, top, dtype):
         check_forward(z[i:i + 256], t[i:i + 256], 0.9, top, part)
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("pad", [0, 1, 3])
+@pytest.mark.parametrize("V", [1, 2, 7, 8, 9, 15, 33, 64, 100, 255, 257, 300, 511, 512, 513, 1000, 1024, 1031, 1500,
+                               2047, 2048, 2056])
+def test_short_rows(V, pad, dtype):
+    """Rows held in registers, several to a warp."""
+    for n in (1, 3, 333):
+        for std, lift in ((3.0, 12.0), (0.1, 0.0), (3.0, 40.0)):
+            z, t = make(n, V, dtype, seed=n + V, pad=pad, std=std, lift=lift)
+            both(z, t, scale=0.8)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("V", [3, 50, 200, 400, 513, 1001, 2003])
+def test_short_rows_of_every_kind(V, dtype):
+    """Without alternatives short rows go another way than with them: results agree to the
+    tolerance of either, NaN and infinities alike."""
+    z, t = make(96, V, dtype, seed=V, pad=1)
+    n = torch.arange(96, device=DEV)
+    t[n % 8 == 1] = -1
+    t[n % 8 == 2] = V + 3
+    z[n % 8 == 3] = -math.inf
+    z[4::8, 1:] = -math.inf                          # one token left
+    z[5::8, 0] = z[5::8].amax(1)                     # the maximum twice, once at the row's edge
+    z[6::8, V - 1] = 50.0
+    z[6::8, V // 2] = 50.0
+    z[7, V // 2] = math.nan
+    z[15, 0] = math.inf
+    z[23] = torch.finfo(dtype).min                   # a mask of the lowest value everywhere
+    z[31, 1:] = torch.finfo(dtype).min
+    a, b = ewg.token_logprobs(z, t, scale=1.3), ewg.token_logprobs(z, t, scale=1.3, top=1)
+    for x, y in zip(a[:4], b[:4]):
+        torch.testing.assert_close(x, y, rtol=2 * REL, atol=1e-37, equal_nan=True)
+    assert torch.equal(a.row_max.nan_to_num(7.0), b.row_max.nan_to_num(7.0))
+
+
 @pytest.mark.parametrize("low", [-0.37, -1.7, -6.1])
 @pytest.mark.parametrize("n,V", [(2, 40), (2432, 4096), (2432, 200000), (1, 200000), (2, 1000000)])
 def test_equal_terms(n, V, low):
