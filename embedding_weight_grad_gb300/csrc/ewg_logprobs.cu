@@ -700,8 +700,8 @@ __global__ void __launch_bounds__(256, 4) logprobs_short_kernel(const LogprobsAr
   a.log_sum[row] = log_sum;
 }
 
-// Gradient kernel: kT threads take kBatch * kT vectors of a row (kT = 32: a warp, eight
-// items to a block).  Items of one row are neighbours.  The vectors are the 16-byte ones of
+// Gradient kernel: kT threads take kBatch * kT vectors of a row, 256 / kT such items to a block.
+// Items of one row are neighbours.  The vectors are the 16-byte ones of
 // the gradient's row; a logits row of another alignment is read as two vectors each, put
 // together in registers.
 //
@@ -718,7 +718,7 @@ __global__ void __launch_bounds__(256, 6) logprobs_grad_kernel(const LogprobsGra
   if (a.status && blockIdx.x == 0) report_targets(a.targets, a.targets_int64, a.n, a.V, a.status, blockDim.x);
   const long long item = static_cast<long long>(blockIdx.x) * kGroups + threadIdx.x / kT;
   const int tid = threadIdx.x % kT;
-  const long long row = item / items_per_row;
+  const long long row = items_per_row == 1 ? item : item / items_per_row;
   if (row >= a.n) return;
   const int part = static_cast<int>(item - row * items_per_row);
 
@@ -738,7 +738,7 @@ __global__ void __launch_bounds__(256, 6) logprobs_grad_kernel(const LogprobsGra
   };
   // Short rows: on their way while the row's numbers come (a row of padding is read in
   // vain, which costs long rows more than the wait).
-  if (kT == 32 && shift == 0) load_aligned();
+  if (kT <= 32 && shift == 0) load_aligned();
 
   const long long target = target_of(a.targets, a.targets_int64, row);
   const float m = a.row_max[row];
@@ -761,8 +761,11 @@ __global__ void __launch_bounds__(256, 6) logprobs_grad_kernel(const LogprobsGra
 
   if (part == 0) {                   // the elements outside the vectors
     const int edges = a.V - nv * kE;
-    if (tid < edges) {
-      const int id = tid < head ? tid : nv * kE + tid;
+#pragma unroll
+    for (int u = 0; u < (2 * (kE - 1) + kT - 1) / kT; ++u) {
+      const int e = tid + u * kT;
+      if (e >= edges) break;
+      const int id = e < head ? e : nv * kE + e;
       V::store1(g + id, zero ? 0.0f : one(V::load1(z + id), id));
     }
   }
@@ -773,7 +776,7 @@ __global__ void __launch_bounds__(256, 6) logprobs_grad_kernel(const LogprobsGra
     return;
   }
   if (shift == 0) {
-    if (kT != 32) load_aligned();
+    if (kT > 32) load_aligned();
   } else {
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
@@ -889,16 +892,25 @@ cudaError_t launch_forward_of(const LogprobsArgs& a, int num_sms, cudaStream_t s
   return launch_forward<T, 512>(a, cluster, stream);
 }
 
+template <typename T, int kT>
+cudaError_t launch_grad(const LogprobsGradArgs& a, int nv, cudaStream_t stream) {
+  constexpr int kGroups = 256 / kT;
+  const int items = (nv + kT * kBatch - 1) / (kT * kBatch);
+  const long long blocks = (static_cast<long long>(a.n) * items + kGroups - 1) / kGroups;
+  logprobs_grad_kernel<T, kT><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a, items);
+  return cudaGetLastError();
+}
+
 template <typename T>
 cudaError_t launch_grad_of(const LogprobsGradArgs& a, cudaStream_t stream) {
+  // as many threads an item as a short row fills (262144 x 256 bf16: 56 us with 8, 87 with 32;
+  // 1000000 x 100: 118 with 4, 354 with 32)
   const int nv = a.V >= Vec<T>::kE ? a.V / Vec<T>::kE : 1;   // an item takes the row's edges
-  const bool narrow = nv <= 32 * kBatch * 4;
-  const int kT = narrow ? 32 : 256, groups = 256 / kT;
-  const int items = (nv + kT * kBatch - 1) / (kT * kBatch);
-  const long long blocks = (static_cast<long long>(a.n) * items + groups - 1) / groups;
-  if (narrow) logprobs_grad_kernel<T, 32><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a, items);
-  else logprobs_grad_kernel<T, 256><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a, items);
-  return cudaGetLastError();
+  return nv <= 4 * kBatch     ? launch_grad<T, 4>(a, nv, stream)
+         : nv <= 8 * kBatch   ? launch_grad<T, 8>(a, nv, stream)
+         : nv <= 16 * kBatch  ? launch_grad<T, 16>(a, nv, stream)
+         : nv <= 128 * kBatch ? launch_grad<T, 32>(a, nv, stream)
+                              : launch_grad<T, 256>(a, nv, stream);
 }
 
 }  // namespace
