@@ -465,27 +465,46 @@ __global__ void __launch_bounds__(threads_of(kT), blocks_per_sm<T>(kT)) logprobs
     if (order_of(m) >= tau) sm.tasks[atomicAdd(&sm.num_tasks, 1)] = static_cast<uint16_t>(tid);
     sync();
     const int tasks = sm.num_tasks;
-    // a warp takes as many threads' vectors at once as it has lanes for
-    const int length = (v1 - v0 + kT - 1) / kT;
-    int width = 1;
-    while (width < 32 && width < length) width *= 2;
     auto offer = [&](float x, uint32_t id) {
       if (!(x >= tau_f)) return;
       const int at = atomicAdd(&sm.num_candidates, 1);
       if (at < kCandidates) sm.candidates[at] = key_of(x, id);
     };
-    for (int i = (warp * 32 + lane) / width; i < tasks; i += kT / width) {
-      for (int v = v0 + sm.tasks[i] + lane % width * kT; v < v1; v += width * kT) {
-        const uint4 raw = load16(zv + v);
-        if (V::max_of(raw) < tau_f) continue;
-        const uint32_t id = head + v * kE;
+    auto offer_vector = [&](uint4 raw, int v) {
+      if (V::max_of(raw) < tau_f) return;
+      const uint32_t id = head + v * kE;
 #pragma unroll
-        for (int e = 0; e < kE / 2; ++e) {
-          const float2 p = V::pair(raw, e);
-          offer(p.x, id + 2 * e);
-          offer(p.y, id + 2 * e + 1);
-        }
+      for (int e = 0; e < kE / 2; ++e) {
+        const float2 p = V::pair(raw, e);
+        offer(p.x, id + 2 * e);
+        offer(p.y, id + 2 * e + 1);
       }
+    };
+    const int length = (v1 - v0 + kT - 1) / kT;
+    if constexpr (kT == 256) {
+      // Up to 128 vectors of a thread: all over the block, thread i vector i % 2^shift of task
+      // i / 2^shift, kB in flight (4 for bf16 cost the main loop registers: 4 %).
+      constexpr int kB = kE == 8 ? 2 : 4;
+      int shift = 0;
+      while ((1 << shift) < length) ++shift;
+      for (int i = tid; i < tasks << shift; i += kT * kB) {
+        uint4 raw[kB];
+        int at[kB];
+#pragma unroll
+        for (int u = 0; u < kB; ++u) {
+          const int iu = i + u * kT;
+          at[u] = iu < tasks << shift ? v0 + sm.tasks[iu >> shift] + (iu & ((1 << shift) - 1)) * kT : v1;
+          raw[u] = at[u] < v1 ? load16(zv + at[u]) : make_uint4(V::kNegInf, V::kNegInf, V::kNegInf, V::kNegInf);
+        }
+#pragma unroll
+        for (int u = 0; u < kB; ++u) offer_vector(raw[u], at[u]);
+      }
+    } else {
+      // a warp takes as many threads' vectors at once as it has lanes for
+      int width = 1;
+      while (width < 32 && width < length) width *= 2;
+      for (int i = (warp * 32 + lane) / width; i < tasks; i += kT / width)
+        for (int v = v0 + sm.tasks[i] + lane % width * kT; v < v1; v += width * kT) offer_vector(load16(zv + v), v);
     }
     if (warp == 0 && lane < edges) offer(edge, edge_id);
     sync();
@@ -869,7 +888,7 @@ cudaError_t launch_forward_of(const LogprobsArgs& a, int num_sms, cudaStream_t s
   //     160 x 64000             14 |  18  7.9 | 10.3
   //    8192 x 50257            129 | 165  126 | 148  144 | 174
   //    8192 x 80000            197 | 270  187 | 214  211 | 231
-  //    8192 x129280            312 | 437  294 | 357  327 | 349
+  //    8192 x129280            312 | 437  294 | 345  327 | 349  (with 20: 425 and 383)
   //    2048 x129280             99 | 131   85 | 101   82 |  92
   // Short rows pay for what a row costs besides its read, which more threads raise; in long
   // ones few threads leave each with more vectors to read again for the alternatives.
@@ -883,7 +902,7 @@ cudaError_t launch_forward_of(const LogprobsArgs& a, int num_sms, cudaStream_t s
                               : launch_short<T, 32>(a, stream);
   if (nv <= 128 || (nv <= 1024 && many)) return launch_forward<T, 32>(a, 1, stream);
   if (nv <= 1024 || (nv < 4096 && a.n >= num_sms)) return launch_forward<T, 128>(a, 1, stream);
-  if (a.n >= num_sms && (nv <= 12288 || (many && !a.top && nv <= 32768))) return launch_forward<T, 256>(a, 1, stream);
+  if (a.n >= num_sms && (nv <= 12288 || (many && nv <= 32768 && a.top * nv <= 131072))) return launch_forward<T, 256>(a, 1, stream);
   // Few rows: up to 8 blocks a row, one on an SM, of 1024 vectors at least.  Joining them
   // costs 1.2 us, which a row of 4000 vectors does not win back (64 x 32000 bf16 with 8
   // alternatives: 6.6 us, in two blocks 8.9; 1 x 129280: 8.0 in eight, 10.4 in one).

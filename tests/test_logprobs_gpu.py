@@ -118,7 +118,8 @@ def test_sizes(n, V, dtype):
 
 @pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("n,V,top", [(2500, 1111, 4), (2432, 4101, 3), (2432, 8200, 3), (160, 8300, 7), (160, 33001, 7),
-                                     (151, 33001, 7), (76, 66000, 2), (38, 140001, 9), (2432, 102403, 0), (2432, 30003, 1)])
+                                     (151, 33001, 7), (76, 66000, 2), (38, 140001, 9), (2432, 102403, 0), (2432, 30003, 1),
+                                     (2432, 102403, 1)])
 def test_many_rows(n, V, top, dtype):
     """Rows enough to fill the device: other shares of a row for a thread."""
     z, t = make(n, V, dtype, seed=n + V, pad=V % 2)
