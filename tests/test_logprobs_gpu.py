@@ -165,6 +165,23 @@ def test_short_rows_of_every_kind(V, dtype):
     assert torch.equal(a.row_max.nan_to_num(7.0), b.row_max.nan_to_num(7.0))
 
 
+@pytest.mark.parametrize("n,V,top", [(36000, 65000, 2), (2400000, 1001, 0), (17, 140000000, 3)])
+def test_offsets_beyond_32_bits(n, V, top):
+    """More than 2^31 logits: the last rows of a large array, forward and in place backward."""
+    z = torch.full((n, V), -3.0, dtype=BF16, device=DEV)
+    last = 3
+    part, t_part = make(last, V, BF16, seed=V)
+    z[-last:] = part
+    t = torch.zeros(n, dtype=torch.int64, device=DEV)
+    t[-last:] = t_part
+    r = ewg.token_logprobs(z, t, top=top, check=True)
+    tail = ewg.TokenLogprobs(*(x if x is None else x[-last:] for x in r))
+    check_forward(part, t_part, 1.0, top, tail)
+    G = torch.ones(n, device=DEV)
+    got = ewg.token_logprobs_backward(z, t, r.row_max, r.log_sum, G, out=z, check=True)
+    check_backward(part, t_part, 1.0, G[-last:], None, got[-last:])
+
+
 @pytest.mark.parametrize("low", [-0.37, -1.7, -6.1])
 @pytest.mark.parametrize("n,V", [(2, 40), (2432, 4096), (2432, 200000), (1, 200000), (2, 1000000)])
 def test_equal_terms(n, V, low):

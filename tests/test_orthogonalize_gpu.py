@@ -147,6 +147,12 @@ def test_zero_and_not_finite_matrices_of_a_batch():
     check(X[[0, 4]], G[[0, 4]])
 
 
+@pytest.mark.parametrize("rows,cols", [(24, 1 << 20), (1 << 20, 48), (260, 100001)])
+def test_longest_sides(rows, cols):
+    G = randn(rows, cols, seed=rows)
+    check(ewg.orthogonalize_update(G, check=True), G)
+
+
 @pytest.mark.parametrize("kind", ["rising", "falling", "shuffled"])
 @pytest.mark.parametrize("base", [1e-30, 1.0, 1e30])
 @pytest.mark.parametrize("rows,cols", [(1, 400000), (2, 400001), (37, 20000), (300, 40)])
