@@ -345,8 +345,9 @@ size_t ewg_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t co
  * X is kept to 22 bits beside its fp16 numbers, and the diagonals of A and of b A + c A^2
  * exactly to first order.  With the coefficients below the result is within 2.5e-3 of the
  * exact steps in norm, of which its own rounding to bf16 is 1.7e-3; low-rank updates included.
- * The norm is summed in 64 bits, so the scale of G does not matter; a zero matrix stays
- * zero, a NaN or an infinity makes its matrix NaN.  Results are deterministic.
+ * The norm is summed to 2^-45 of it over fp32's whole range, so the scale of G does not
+ * matter; a zero matrix stays zero, a NaN or an infinity makes its matrix NaN.  The same
+ * call gives the same bits; in another batch a matrix's sums may be split otherwise.
  *
  *   grad    [batch][rows][cols], EWG_BF16 or EWG_FP32, unit inner stride; any alignment
  *   out     [batch][rows][cols] bf16, unit inner stride, apart from grad
