@@ -55,6 +55,9 @@ constexpr int kOrthoMaxSide = 16384;      // of the smaller side
 constexpr int kOrthoMaxLong = 1 << 20;    // of the larger side
 constexpr int kNormBlocks = 304;          // blocks summing squares, at most, if the matrices are not more
 
+// Smaller sides up to the first go without the tensor cores, and up to the second where the larger
+// side is not long (48 x 2048: 101 us, with them 111; 48 x 7168: 138 and 111).
+constexpr int kOrthoSmall = 32, kOrthoSmallShort = 48, kOrthoShort = 4096;
 constexpr int kOrthoBlock = 256;          // side of the blocks the products are computed in
 constexpr int kOrthoWarps = 16;           // epilogue warps of a block
 
@@ -66,8 +69,10 @@ struct OrthoShape {
   int64_t blocks_r, blocks_c;
   int norm_blocks;
   int split_gram, split_poly;             // parts of the inner dimension of X X^T and A A
+  int small_parts;                        // shares of the larger side, where the smaller one is small
   bool tall;
 
+  bool small() const { return r <= kOrthoSmall || (r <= kOrthoSmallShort && c <= kOrthoShort); }
   int64_t square_blocks() const { return blocks_r * (blocks_r + 1) / 2; }
   // counters of the steps kernel for one matrix
   int64_t counters() const {
@@ -81,6 +86,7 @@ struct OrthoShape {
 
 struct OrthoLayout {
   size_t header, counters, norm, diag_a[2], diag_b, xt[2], xl, a[2], b, partial, total;
+  size_t small_gram, small_exponents, small_m, small_factors, small_x;
 };
 
 // Parts of an inner dimension of `inner` for `units` blocks: as many as leave no more units than
@@ -115,6 +121,9 @@ inline OrthoShape make_ortho_shape(int64_t batch, int64_t rows, int64_t cols) {
   const int64_t want = (s.r * s.c + 16383) / 16384;
   const int64_t most = batch < kNormBlocks ? kNormBlocks / batch : 1;
   s.norm_blocks = static_cast<int>(want < most ? want : most);
+  // 32 shares of 64 (which one block adds up), and more once they are of 16 times that
+  const int64_t tiles = (s.c + 63) / 64, shares = tiles / 16 < 32 ? 32 : tiles / 16 < 152 ? tiles / 16 : 152;
+  s.small_parts = static_cast<int>(tiles < shares ? tiles : shares);
   s.split_gram = ortho_split(batch * s.square_blocks(), s.c);
   s.split_poly = ortho_split(batch * s.square_blocks(), s.r);
   return s;
@@ -129,6 +138,15 @@ inline OrthoLayout make_ortho_layout(const OrthoShape& s) {
     return at;
   };
   L.header = take(256);
+  if (s.small()) {
+    L.small_gram = take(s.batch * s.small_parts * s.r * s.r * 4);
+    L.small_exponents = take(s.batch * s.small_parts * 4);
+    L.small_m = take(s.batch * s.r * s.r * 4);
+    L.small_factors = take(s.batch * 8);
+    L.small_x = take(s.batch * s.c * s.r * 4);
+    L.total = off;
+    return L;
+  }
   L.counters = take(s.batch * s.counters() * 4);
   L.norm = take(s.batch * s.norm_blocks * 8);
   for (int i = 0; i < 2; ++i) L.diag_a[i] = take(s.batch * s.ld * 4);
@@ -156,5 +174,6 @@ struct OrthoCall {
 
 cudaError_t prepare_orthogonalize();   // once per device, before the first launch
 cudaError_t launch_orthogonalize(const OrthoCall& call, cudaStream_t stream);
+cudaError_t launch_orthogonalize_small(const OrthoCall& call, int num_sms, cudaStream_t stream);
 
 }  // namespace ewg

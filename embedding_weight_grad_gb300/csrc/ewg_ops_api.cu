@@ -272,7 +272,8 @@ int ewg_orthogonalize(const void* grad, int grad_dtype, int64_t batch, int64_t r
   q.b = b;
   q.c = c;
   q.workspace = workspace;
-  cudaError_t e = ewg::launch_orthogonalize(q, static_cast<cudaStream_t>(stream));
+  const cudaStream_t on = static_cast<cudaStream_t>(stream);
+  cudaError_t e = shape.small() ? ewg::launch_orthogonalize_small(q, sms, on) : ewg::launch_orthogonalize(q, on);
   return e == cudaSuccess ? EWG_OK : cuda_fail(e, "orthogonalisation launch");
 }
 

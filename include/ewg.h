@@ -341,12 +341,14 @@ size_t ewg_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t co
  *
  *     A = X X^T        X <- a X + (b A + c A^2) X
  *
- * The result is rounded to bf16.  The products take fp16 operands with fp32 accumulation;
- * X is kept to 22 bits beside its fp16 numbers, and the diagonals of A and of b A + c A^2
- * exactly to first order.  With the coefficients below the result is within 2.5e-3 of the
- * exact steps in norm, of which its own rounding to bf16 is 1.7e-3; low-rank updates included.
- * The norm is summed to 2^-45 of it over fp32's whole range, so the scale of G does not
- * matter; a zero matrix stays zero, a NaN or an infinity makes its matrix NaN.  The same
+ * The result is rounded to bf16.  Matrices with a smaller side up to 32 (up to 48 where the
+ * larger one is at most 4096) are computed in fp32 throughout and rounded once.  For others
+ * the products take fp16 operands with fp32 accumulation; X is kept to 22 bits beside its fp16
+ * numbers, and the diagonals of A and of b A + c A^2 exactly to first order.  With the
+ * coefficients below the result is then within 2.5e-3 of the exact steps in norm (2.8e-3 where
+ * the smaller side is below 64), of which its own rounding to bf16 is 1.7e-3; low-rank updates
+ * included.
+ * The norm is taken over fp32's whole range, so the scale of G does not matter; a zero matrix stays zero, a NaN or an infinity makes its matrix NaN.  The same
  * call gives the same bits; in another batch a matrix's sums may be split otherwise.
  *
  *   grad    [batch][rows][cols], EWG_BF16 or EWG_FP32, unit inner stride; any alignment
@@ -358,8 +360,8 @@ size_t ewg_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t co
  * Requires 0 <= batch <= 65535 (0: nothing is enqueued), the smaller side at most 16384 and
  * the larger at most 2^20, batch * ceil(rows / 256) * ceil(cols / 256) < 2^30,
  * 1 <= steps <= EWG_MAX_ORTHO_STEPS, finite coefficients, and a workspace as above.
- * Enqueues two small kernels and one cooperative kernel that takes every step; allocates
- * nothing.  ewg_read_status reports EWG_ERR_TIMEOUT if a bounded wait in it gave up (out
+ * Enqueues two small kernels and one cooperative kernel that takes every step, or small ones
+ * for every two steps; allocates nothing.  ewg_read_status reports EWG_ERR_TIMEOUT if a bounded wait in it gave up (out
  * is then unspecified).
  */
 int ewg_orthogonalize(const void* grad, int grad_dtype, int64_t batch, int64_t rows,

@@ -60,6 +60,34 @@ def test_sizes(rows, cols, dtype):
     check(ewg.orthogonalize_update(G, check=True), G)
 
 
+SMALL = [(1, 1), (1, 9), (4, 2), (3, 3), (8, 13), (16, 16), (17, 40), (15, 1000), (32, 32), (33, 32), (28, 30), (32, 64),
+         (31, 65), (32, 4097), (25, 777), (32, 70000),
+         (48, 48), (40, 1001), (33, 4096), (4000, 47)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("kind", ["full", "transposed", "strided", "low rank", "one large"])
+@pytest.mark.parametrize("rows,cols", SMALL)
+def test_small_sides_are_only_rounded(rows, cols, kind, dtype):
+    """A smaller side up to 32, or 48 beside one up to 4096, is computed in fp32 and rounded to bf16 once: 2^-8 of an element.  M
+    reaches a^5 = 485 on directions without weight and carries some 8 * 2^-24 of that, the
+    steps' own roundings come to less: 5e-4 of 1, about the largest singular value."""
+    G = randn(3, rows, cols, dtype=dtype, seed=rows + cols)
+    if kind == "transposed":
+        G = randn(3, cols, rows, dtype=dtype, seed=rows).mT
+    elif kind == "strided":
+        G = randn(3, rows, cols + 3, dtype=dtype, seed=rows)[:, :, 1:cols + 1]
+    elif kind == "low rank":
+        k = min(2, rows, cols)
+        G = ((randn(3, rows, k, seed=rows) * 1e3) @ randn(3, k, cols, seed=cols)).to(dtype)
+    elif kind == "one large":
+        G[:, rows // 2, cols // 2] = 3.0
+    for steps in (1, 5):
+        got, want = ewg.orthogonalize_update(G, steps=steps, check=True).double(), reference(G, steps=steps)
+        worst = ((got - want).abs() - 2.0 ** -8 * want.abs()).max().item()
+        assert worst <= 5e-4, worst
+
+
 @pytest.mark.parametrize("batch,rows,cols", [(1, 40, 60), (3, 17, 300), (24, 128, 128), (200, 9, 5), (5, 300, 270),
                                              (7, 513, 260)])
 def test_batches(batch, rows, cols):
