@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(threads_of(kT), blocks_per_sm<T>(kT)) logprobs
   if (warp == 0 && lane < edges) {
     const float x = max_nan((edge - M) * c, kLowestExponent);
     const float e = ex2(x);
-    s += edge_has && lane == __ffs(edge_has) - 1 ? 0.0f : e;
+    s += edge_has && lane == __ffs(edge_has) - 1 ? e - 1.0f : e;    // e is 1, or NaN for an infinite maximum
     t += e * x;
   }
   s = warp_sum(s);
@@ -683,7 +683,9 @@ __global__ void __launch_bounds__(256, 4) logprobs_short_kernel(const LogprobsAr
   for (int u = 0; u < kEdges; ++u) {
     const float x = max_nan((edge[u] - M) * c, kLowestExponent);
     const float e = ex2(x);
-    if (edge[u] == M && !edge_has) edge_has = true; else S_edge += e;
+    const bool held_out = edge[u] == M && !edge_has;
+    edge_has |= held_out;
+    S_edge += held_out ? e - 1.0f : e;                        // e is 1, or NaN for an infinite maximum
     Tt = fmaf(e, x, Tt);
   }
   const int first_lane = threadIdx.x % 32 - lane;             // of the group, in the warp

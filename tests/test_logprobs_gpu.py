@@ -461,3 +461,28 @@ def test_refusals():
     flat = torch.zeros(8 * 100 + 8, device=DEV)
     no(lambda: ewg.token_logprobs_backward(flat[:800].view(8, 100), t, r.row_max, r.log_sum, flat[796:804],
                                            out=flat[:800].view(8, 100)))     # over a gradient
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("n,V,top", [(8, 100, 0), (9, 1001, 0), (9, 1001, 3), (2432, 4101, 2), (9, 5003, 3), (160, 16401, 0),
+                                     (9, 33001, 4), (160, 102403, 1), (1, 140001, 2), (80, 1100003, 0)])
+def test_infinity_shows_at_every_alignment(n, V, top, dtype):
+    """A row with +inf has NaN results wherever it stands: in the row's whole vectors or in
+    the elements outside them, whether it is the row's token or not."""
+    for pad, where in ((0, 0), (1, 0), (1, V - 1), (2, V - 1), (3, 1), (1, V // 2)):
+        z, t = make(n, V, dtype, seed=V + where, pad=pad)
+        rows = torch.arange(min(n, 16), device=DEV)
+        bad = rows[rows % 2 == 0]
+        z[bad, where] = math.inf
+        t[bad] = torch.where(bad % 4 == 0, where, (where + 7) % V)
+        r = ewg.token_logprobs(z, t, scale=0.9, top=top)
+        for x in (r.logprobs, r.entropy, r.log_sum):
+            assert bool(x[bad].isnan().all()), (pad, where)
+        assert bool((r.row_max[bad] == math.inf).all())
+        for E in (None, torch.ones(n, device=DEV)):
+            got = ewg.token_logprobs_backward(z, t, r.row_max, r.log_sum, torch.ones(n, device=DEV), entropy=r.entropy,
+                                              grad_entropy=E, scale=0.9)
+            assert bool(got[bad].isnan().all()), (pad, where)
+        good = rows[rows % 2 == 1]
+        if len(good):
+            check_forward(z[good], t[good], 0.9, top, type(r)(*(x if x is None else x[good] for x in r)))
