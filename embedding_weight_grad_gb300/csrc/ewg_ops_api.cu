@@ -1,5 +1,6 @@
 // C ABI of the operators beside the embedding gradient: argument checks and launches.
 // The declarations and their contracts are in include/ewg.h.
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <initializer_list>
@@ -108,7 +109,11 @@ int ortho_array(const char* name, const void* p, size_t es, int64_t batch, int64
   return check_array(*out, es, mem);
 }
 
-float log2_scale(float scale) { return static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074); }
+// scale log2(e), at most the largest number: above, an exponent of 0 times it would be NaN, and
+// any other is clamped by the kernels all the same.
+float log2_scale(float scale) {
+  return static_cast<float>(std::fmin(static_cast<double>(scale) * 1.4426950408889634074, FLT_MAX));
+}
 
 }  // namespace
 

@@ -486,3 +486,27 @@ def test_infinity_shows_at_every_alignment(n, V, top, dtype):
         good = rows[rows % 2 == 1]
         if len(good):
             check_forward(z[good], t[good], 0.9, top, type(r)(*(x if x is None else x[good] for x in r)))
+
+
+@pytest.mark.parametrize("V,top", [(100, 0), (1001, 1), (50000, 2)])
+@pytest.mark.parametrize("scale", [2.3e38, 2.4e38, 3.4e38])
+def test_largest_scales(scale, V, top):
+    """A scale of nearly the largest number (times log2(e) it would not be one): all the weight is
+    on the largest logit, shared where it occurs twice."""
+    for dtype in (BF16, FP32):
+        z = (torch.arange(V, device=DEV) % 17).float().neg().expand(2, V).contiguous()
+        z[:, 17::17] = -20.0                             # 0 is left the only largest ...
+        z[1, V - 1] = 0.0                                # ... and has company
+        z, t = z.to(dtype), torch.zeros(2, dtype=torch.int64, device=DEV)
+        r = ewg.token_logprobs(z, t, scale=scale, top=top)
+        want = torch.tensor([0.0, math.log(2.0)], device=DEV)
+        for x in (-r.logprobs, r.log_sum, r.entropy):
+            assert bool(((x - want).abs() <= 4 * U).all()), x
+        if top:
+            assert torch.equal(r.top_ids[:, 0], t)
+        got = ewg.token_logprobs_backward(z, t, r.row_max, r.log_sum, torch.full((2,), 2.0 ** -100, device=DEV),
+                                          scale=scale)
+        half = scale * 2.0 ** -101
+        assert bool((got[0] == 0).all())
+        assert abs(got[1, 0].item() - half) <= 2.0 ** -8 * half and abs(got[1, V - 1].item() + half) <= 2.0 ** -8 * half
+        assert bool((got[1, 1:V - 1] == 0).all())
