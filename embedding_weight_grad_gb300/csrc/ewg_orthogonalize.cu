@@ -708,6 +708,7 @@ __device__ __forceinline__ void store_out(const OrthoArgs& a, int z, int j0, int
                  : "=h"(v) : "r"(buf + r * 64 + (((lane / 8) ^ ((r >> 1) & 3)) << 4) + lane % 8 * 2));
     if (r < rows && lane < n) out[(j0 + r) * a.out_row + i0 + lane] = v;
   }
+  ptx::fence_proxy_async_shared();   // the next copies into `buf` come after these plain writes
   __syncwarp();
 }
 

@@ -277,3 +277,18 @@ def test_refusals():
     with pytest.raises(ewg.EwgError):
         ewg.orthogonalize_workspace((16385, 16385))
     assert ewg.lib().ewg_orthogonalize_workspace_bytes(1, 0, 5) == 0
+
+
+@pytest.mark.parametrize("batch,rows,cols", [(1, 700, 512), (3, 300, 256), (30, 1100, 500), (4, 5000, 130)])
+def test_tall_results_of_any_alignment(batch, rows, cols):
+    """The rows of a tall result that are not aligned go out through the shared memory that the
+    next copies come into: the bits of an aligned one, call after call."""
+    G = randn(batch, rows, cols, seed=rows)
+    want = ewg.orthogonalize_update(G)
+    for at, wide in ((0, 1), (1, 7), (4, 12), (3, 5)):
+        out = torch.full((batch, rows, cols + wide), 7.0, dtype=BF16, device=DEV)
+        for _ in range(5):
+            out.fill_(7.0)
+            ewg.orthogonalize_update(G, out=out[:, :, at:at + cols], check=True)
+            assert torch.equal(out[:, :, at:at + cols], want)
+            assert int((out == 7.0).sum()) == out.numel() - want.numel()
