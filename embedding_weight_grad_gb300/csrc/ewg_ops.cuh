@@ -90,14 +90,16 @@ struct OrthoLayout {
 };
 
 // Parts of an inner dimension of `inner` for `units` blocks: as many as leave no more units than
-// kOrthoPairs, each of at least kOrthoPartMin.  Adding the parts up takes about 8 us, and
+// `pairs`, each of at least kOrthoPartMin; fewer pairs never give more parts.  The workspace is laid
+// out for kOrthoPairs, and a launch splits for the pairs that run at once where those are
+// fewer: parts wait for one another.  Adding the parts up takes about 8 us, and
 // 64 of the inner dimension 0.3 us, so that shorter ones than kOrthoSplitMin stay whole (2048 in
 // two parts: 20 us instead of 15; 4097 in four: 15 instead of 23).
 constexpr int64_t kOrthoPairs = 76;
 constexpr int64_t kOrthoPartMin = 1024;
 constexpr int64_t kOrthoSplitMin = 4096;
-inline int ortho_split(int64_t units, int64_t inner) {
-  int64_t parts = kOrthoPairs / units;
+inline int ortho_split(int64_t units, int64_t inner, int64_t pairs = kOrthoPairs) {
+  int64_t parts = (pairs < kOrthoPairs ? pairs : kOrthoPairs) / units;
   if (parts > inner / kOrthoPartMin) parts = inner / kOrthoPartMin;
   if (parts <= 1 || inner < kOrthoSplitMin) return 1;
   // no empty part: `per` inner blocks of 64 each

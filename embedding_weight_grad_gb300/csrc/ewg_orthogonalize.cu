@@ -828,8 +828,8 @@ __device__ __forceinline__ uint4 finish8(const OrthoArgs& a, int cur, float f, f
 //
 // Where the inner dimension is split, each part's warp stores its sums, waits for the other
 // parts' and finishes its share of the columns, in sixteens, from all parts' sums, added
-// in their order.  (The units of such a phase are no more than the pairs, so the parts run at
-// the same time.)
+// in their order.  (The units of such a phase are no more than the pairs of the launch, see
+// ortho_split, so the parts run at the same time.)
 template <int kPhase>
 __device__ __forceinline__ bool epilogue_square(const OrthoMaps& maps, const OrthoArgs& a, int step, const Unit& x,
                                                 const Place& at, const Acc& in, uint32_t& parity) {
@@ -1330,12 +1330,12 @@ cudaError_t launch_orthogonalize(const OrthoCall& q, cudaStream_t stream) {
   a.ready = in.counters;
   a.arrived = in.counters + sh.batch * 3 * nr;
   a.partial = reinterpret_cast<float*>(ws + L.partial);
-  a.split[kGram] = sh.split_gram;
-  a.split[kPoly] = sh.split_poly;
-
-  const unsigned batch = static_cast<unsigned>(sh.batch);
   int dev = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  a.split[kGram] = ortho_split(sh.batch * sh.square_blocks(), sh.c, g_pairs[dev]);
+  a.split[kPoly] = ortho_split(sh.batch * sh.square_blocks(), sh.r, g_pairs[dev]);
+
+  const unsigned batch = static_cast<unsigned>(sh.batch);
   const int64_t tiles = (sh.cols + 63) / 64 * ((sh.rows + 63) / 64);
   in.tiles_of_block = static_cast<int>((tiles * sh.batch + 2 * kScaleBlocks * g_pairs[dev] - 1) / (2 * kScaleBlocks * g_pairs[dev]));
   ortho_norm_kernel<<<dim3(sh.norm_blocks, batch), 32 * kNormWarps, 0, stream>>>(in);
@@ -1354,10 +1354,10 @@ cudaError_t launch_orthogonalize(const OrthoCall& q, cudaStream_t stream) {
     if ((e = cudaLaunchKernelEx(&cfg, ortho_scale_kernel, in)) != cudaSuccess) return e;
   }
 
-  const int64_t most = sh.batch * std::max(nr * nc, nr * (nr + 1) / 2 * std::max(sh.split_gram, sh.split_poly));
+  const int64_t most = sh.batch * std::max(nr * nc, nr * (nr + 1) / 2 * std::max(a.split[kGram], a.split[kPoly]));
   const int pairs = static_cast<int>(std::min<int64_t>(most, g_pairs[dev]));
   if (pairs < 1) return cudaErrorLaunchOutOfResources;
-  a.fused = nr == 1 && sh.split_gram == 1;
+  a.fused = nr == 1 && a.split[kGram] == 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * pairs);
   cfg.blockDim = dim3(kGemmThreads);
