@@ -1332,6 +1332,7 @@ cudaError_t launch_orthogonalize(const OrthoCall& q, cudaStream_t stream) {
   a.partial = reinterpret_cast<float*>(ws + L.partial);
   int dev = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if (g_pairs[dev] < 1) return cudaErrorLaunchOutOfResources;
   a.split[kGram] = ortho_split(sh.batch * sh.square_blocks(), sh.c, g_pairs[dev]);
   a.split[kPoly] = ortho_split(sh.batch * sh.square_blocks(), sh.r, g_pairs[dev]);
 
@@ -1356,7 +1357,6 @@ cudaError_t launch_orthogonalize(const OrthoCall& q, cudaStream_t stream) {
 
   const int64_t most = sh.batch * std::max(nr * nc, nr * (nr + 1) / 2 * std::max(a.split[kGram], a.split[kPoly]));
   const int pairs = static_cast<int>(std::min<int64_t>(most, g_pairs[dev]));
-  if (pairs < 1) return cudaErrorLaunchOutOfResources;
   a.fused = nr == 1 && a.split[kGram] == 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * pairs);

@@ -44,3 +44,10 @@ def test_split_parts_run_at_the_same_time(launches):
             assert (parts - 1) * -(-inner // parts) < inner, at
         if pairs >= 76:
             assert parts == room, at             # what the workspace is laid out for
+
+
+def test_a_device_without_room_is_an_error(launches):
+    """Where no pair of CTAs fits, the call returns an error (and does not divide by the pairs)."""
+    for shape in SHAPES:
+        ((code, blocks, *_),) = launches([(0, *shape)])
+        assert code != 0 and blocks == 0
