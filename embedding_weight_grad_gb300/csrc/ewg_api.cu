@@ -24,6 +24,7 @@ constexpr int kMaxDevices = 64;
 
 struct DeviceState {
   bool ready = false;
+  bool orthogonalize_ready = false;    // the steps kernel of the orthogonalised update
   int num_sms = 0;
   // ewg_accumulate_host: the stream the grad copy runs on, and the events that order it
   cudaStream_t copy_stream = nullptr;
@@ -232,11 +233,19 @@ int ewg::host::current_device(int* dev, int* num_sms) {
     if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
     e = ewg::prepare_kernels();
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
-    e = ewg::prepare_orthogonalize();
-    if (e != cudaSuccess) return cuda_fail(e, "orthogonalisation set-up");
     d.ready = true;
   }
   *num_sms = d.num_sms;
+  return EWG_OK;
+}
+
+int ewg::host::prepare_orthogonalize_on(int dev) {
+  std::lock_guard<std::mutex> lock(g_mu);
+  DeviceState& d = g_devices[dev];
+  if (d.orthogonalize_ready) return EWG_OK;
+  cudaError_t e = ewg::prepare_orthogonalize();
+  if (e != cudaSuccess) return cuda_fail(e, "orthogonalisation set-up");
+  d.orthogonalize_ready = true;
   return EWG_OK;
 }
 

@@ -24,6 +24,10 @@ inline int cuda_fail(cudaError_t e, const char* what) {
 // Index and SM count of the current device; configures the kernels once per device.
 int current_device(int* dev, int* num_sms);
 
+// Configures the steps kernel of the orthogonalised update on the current device, `dev`, once.
+// (Apart from the rest: what fails here stops no other call.)
+int prepare_orthogonalize_on(int dev);
+
 inline bool on_device(const void* p, int dev) {
   cudaPointerAttributes at;
   if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {

@@ -263,6 +263,7 @@ int ewg_orthogonalize(const void* grad, int grad_dtype, int64_t batch, int64_t r
                                  "ewg_orthogonalize_workspace_bytes(batch, rows, cols)");
   const Array ws = flat("workspace", workspace, static_cast<int64_t>(need), 1);
   if ((rc = check_apart(res, in)) || (rc = check_apart(ws, in)) || (rc = check_apart(ws, res))) return rc;
+  if (!shape.small() && (rc = prepare_orthogonalize_on(dev))) return rc;
   ewg::OrthoCall q{};
   q.shape = shape;
   q.grad = grad;

@@ -5,19 +5,25 @@ import subprocess
 
 import pytest
 
+import embedding_weight_grad_gb300 as ewg
 from embedding_weight_grad_gb300 import build as cuda_build
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 
 
+def compile_host(exe, *sources):
+    """A program of `sources` that runs without a GPU; device code only as far as the host code
+    around it needs it."""
+    subprocess.run([cuda_build.nvcc(), "-gencode", "arch=compute_103a,code=compute_103a", "-cudart", "none", "-std=c++17",
+                    "-I" + os.path.join(cuda_build.ROOT, "include"), "-I" + cuda_build.CSRC, "-o", exe, *sources,
+                    os.path.join(HERE, "host", "no_runtime.cpp"), "-ldl"], check=True, capture_output=True)
+    return exe
+
+
 @pytest.fixture(scope="module")
 def launches(tmp_path_factory):
-    exe = str(tmp_path_factory.mktemp("host") / "launches")
-    # device code only as far as the host code around it needs it
-    subprocess.run([cuda_build.nvcc(), "-gencode", "arch=compute_103a,code=compute_103a", "-cudart", "none", "-std=c++17",
-                    "-I" + os.path.join(cuda_build.ROOT, "include"), "-I" + cuda_build.CSRC, "-o", exe,
-                    os.path.join(HERE, "host", "orthogonalize_launches.cu"),
-                    os.path.join(HERE, "host", "no_runtime.cpp")], check=True, capture_output=True)
+    exe = compile_host(str(tmp_path_factory.mktemp("host") / "launches"),
+                       os.path.join(HERE, "host", "orthogonalize_launches.cu"))
 
     def run(cases):
         r = subprocess.run([exe], input="".join("%d %d %d %d\n" % c for c in cases), capture_output=True, text=True)
@@ -51,3 +57,14 @@ def test_a_device_without_room_is_an_error(launches):
     for shape in SHAPES:
         ((code, blocks, *_),) = launches([(0, *shape)])
         assert code != 0 and blocks == 0
+
+
+def test_its_set_up_concerns_no_other_call(tmp_path):
+    """Where the set-up of the steps kernel fails, the calls that do without it work all the same, and a
+    call that needs it reports the error and tries anew the next time."""
+    exe = compile_host(str(tmp_path / "set_up"), os.path.join(HERE, "host", "set_up.cu"),
+                       os.path.join(cuda_build.CSRC, "ewg_api.cu"), os.path.join(cuda_build.CSRC, "ewg_ops_api.cu"))
+    codes = subprocess.run([exe], check=True, capture_output=True, text=True).stdout.split()
+    can, accumulate, logprobs, small, large, again = map(int, codes)
+    assert (can, accumulate, logprobs, small) == (1, ewg.OK, ewg.OK, ewg.OK)
+    assert (large, again) == (ewg.ERR_CUDA, ewg.OK)
