@@ -124,9 +124,9 @@ def _load(path):
     L.ewg_token_logprobs_backward.restype = i32
     L.ewg_orthogonalize_workspace_bytes.argtypes = [i64, i64, i64]
     L.ewg_orthogonalize_workspace_bytes.restype = sz
-    L.ewg_orthogonalize.argtypes = [vp, i32, i64, i64, i64, i64, i64, vp, i64, i64, i32, f32,
-                                    f32, f32, vp, sz, vp]
-    L.ewg_orthogonalize.restype = i32
+    for f in (L.ewg_orthogonalize, L.ewg_orthogonalize_transposed):
+        f.argtypes = [vp, i32, i64, i64, i64, i64, i64, vp, i64, i64, i32, f32, f32, f32, vp, sz, vp]
+        f.restype = i32
     L.ewg_read_status.argtypes = [vp, vp, ctypes.POINTER(i32)]
     L.ewg_read_status.restype = i32
     L.ewg_status_string.argtypes = [i32]
@@ -562,9 +562,10 @@ def orthogonalize_update(grad: torch.Tensor, *, steps: int = 5,
     A = X X^T, from X = grad / |grad|.
 
     grad: [..., rows, cols] bf16 or fp32 (leading dimensions are a batch of matrices; a
-    transposed matrix is taken as such); out: bf16 of the same shape.  The work is enqueued
-    on the current stream.  workspace: orthogonalize_workspace(grad.shape), allocated when
-    not given.  check=True waits and raises EwgError if a wait on the device gave up.
+    transposed matrix is taken as such); out: bf16 of the same shape, whose rows or columns are
+    contiguous, apart from grad.  The work is enqueued on the current stream.  workspace:
+    orthogonalize_workspace(grad.shape), allocated when not given.  check=True waits and raises
+    EwgError if a wait on the device gave up.
     """
     if not grad.is_cuda or grad.dtype not in _FLOAT_CODES or grad.dim() < 2:
         raise ValueError("orthogonalize_update does not support these tensors: grad must be "
@@ -581,10 +582,13 @@ def orthogonalize_update(grad: torch.Tensor, *, steps: int = 5,
         out = torch.empty(grad.shape, dtype=torch.bfloat16, device=grad.device)
     if grad.numel() == 0 and 0 not in grad.shape[-2:]:
         return out
-    g3, o3 = _matrices("grad", grad), _matrices("out", out)
+    call, o = lib().ewg_orthogonalize, out
+    if out.stride(-1) != 1 and out.stride(-2) == 1 and out.shape[-1] > 1:
+        call, o = lib().ewg_orthogonalize_transposed, out.mT     # the other way round than grad
+    g3, o3 = _matrices("grad", grad), _matrices("out", o)
     batch, rows, cols = g3.shape
     ws = workspace if workspace is not None else orthogonalize_workspace(grad.shape, grad.device)
-    _enqueue(grad.get_device(), lib().ewg_orthogonalize, g3.data_ptr(), _FLOAT_CODES[grad.dtype],
+    _enqueue(grad.get_device(), call, g3.data_ptr(), _FLOAT_CODES[grad.dtype],
              batch, rows, cols, g3.stride(0), g3.stride(1), o3.data_ptr(), o3.stride(0),
              o3.stride(1), steps, *coefficients, ws.data_ptr(), ws.numel())
     if check:

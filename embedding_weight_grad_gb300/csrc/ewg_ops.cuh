@@ -168,6 +168,7 @@ struct OrthoCall {
   bool grad_bf16;
   int64_t grad_batch_stride, grad_row_stride;   // elements
   void* out;                                    // bf16
+  bool out_tall;                                // out is [larger side][smaller side]
   int64_t out_batch_stride, out_row_stride;
   int steps;
   float a, b, c;

@@ -115,6 +115,59 @@ float log2_scale(float scale) {
   return static_cast<float>(std::fmin(static_cast<double>(scale) * 1.4426950408889634074, FLT_MAX));
 }
 
+// ewg_orthogonalize, or with `transposed` ewg_orthogonalize_transposed.
+int orthogonalize(bool transposed, const void* grad, int grad_dtype, int64_t batch, int64_t rows, int64_t cols,
+                  int64_t grad_batch_stride, int64_t grad_row_stride, void* out, int64_t out_batch_stride,
+                  int64_t out_row_stride, int steps, float a, float b, float c, void* workspace, size_t workspace_bytes,
+                  void* stream) {
+  ewg::set_last_error("");
+  int dev = 0, sms = 0;
+  int rc = current_device(&dev, &sms);
+  if (rc) return rc;
+  DeviceMemory mem(dev);
+  if (grad_dtype != EWG_BF16 && grad_dtype != EWG_FP32) return fail(EWG_ERR_UNSUPPORTED, "grad must be bf16 or fp32");
+  if (steps < 1 || steps > EWG_MAX_ORTHO_STEPS)
+    return fail(EWG_ERR_UNSUPPORTED, "steps outside [1, EWG_MAX_ORTHO_STEPS]");
+  if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c))
+    return fail(EWG_ERR_UNSUPPORTED, "the coefficients must be finite");
+  if (batch == 0 && rows > 0 && cols > 0) return EWG_OK;
+  if (!ortho_sizes_ok(batch, rows, cols))
+    return fail(EWG_ERR_UNSUPPORTED, "sizes: 0 <= batch <= 65535, 1 <= smaller side <= 16384, larger side <= 2^20, "
+                                     "batch * ceil(rows / 256) * ceil(cols / 256) < 2^30");
+  const size_t es = elem_size(grad_dtype);
+  Array in, res;
+  if ((rc = ortho_array("grad", grad, es, batch, rows, cols, grad_batch_stride, grad_row_stride, mem, &in)) ||
+      (rc = ortho_array("out", out, 2, batch, transposed ? cols : rows, transposed ? rows : cols, out_batch_stride,
+                        out_row_stride, mem, &res)))
+    return rc;
+  const ewg::OrthoShape shape = ewg::make_ortho_shape(batch, rows, cols);
+  const size_t need = ewg::make_ortho_layout(shape).total;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < need || !mem.has(workspace))
+    return fail(EWG_ERR_INVALID, "workspace null, misaligned, not on the device or smaller than "
+                                 "ewg_orthogonalize_workspace_bytes(batch, rows, cols)");
+  const Array ws = flat("workspace", workspace, static_cast<int64_t>(need), 1);
+  if ((rc = check_apart(res, in)) || (rc = check_apart(ws, in)) || (rc = check_apart(ws, res))) return rc;
+  if (!shape.small() && (rc = prepare_orthogonalize_on(dev))) return rc;
+  ewg::OrthoCall q{};
+  q.shape = shape;
+  q.grad = grad;
+  q.grad_bf16 = grad_dtype == EWG_BF16;
+  q.grad_batch_stride = grad_batch_stride;
+  q.grad_row_stride = grad_row_stride;
+  q.out = out;
+  q.out_tall = shape.tall != transposed;
+  q.out_batch_stride = out_batch_stride;
+  q.out_row_stride = out_row_stride;
+  q.steps = steps;
+  q.a = a;
+  q.b = b;
+  q.c = c;
+  q.workspace = workspace;
+  const cudaStream_t on = static_cast<cudaStream_t>(stream);
+  cudaError_t e = shape.small() ? ewg::launch_orthogonalize_small(q, sms, on) : ewg::launch_orthogonalize(q, on);
+  return e == cudaSuccess ? EWG_OK : cuda_fail(e, "orthogonalisation launch");
+}
+
 }  // namespace
 
 extern "C" {
@@ -237,50 +290,16 @@ int ewg_orthogonalize(const void* grad, int grad_dtype, int64_t batch, int64_t r
                       int64_t grad_batch_stride, int64_t grad_row_stride, void* out, int64_t out_batch_stride,
                       int64_t out_row_stride, int steps, float a, float b, float c, void* workspace,
                       size_t workspace_bytes, void* stream) {
-  ewg::set_last_error("");
-  int dev = 0, sms = 0;
-  int rc = current_device(&dev, &sms);
-  if (rc) return rc;
-  DeviceMemory mem(dev);
-  if (grad_dtype != EWG_BF16 && grad_dtype != EWG_FP32) return fail(EWG_ERR_UNSUPPORTED, "grad must be bf16 or fp32");
-  if (steps < 1 || steps > EWG_MAX_ORTHO_STEPS)
-    return fail(EWG_ERR_UNSUPPORTED, "steps outside [1, EWG_MAX_ORTHO_STEPS]");
-  if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c))
-    return fail(EWG_ERR_UNSUPPORTED, "the coefficients must be finite");
-  if (batch == 0 && rows > 0 && cols > 0) return EWG_OK;
-  if (!ortho_sizes_ok(batch, rows, cols))
-    return fail(EWG_ERR_UNSUPPORTED, "sizes: 0 <= batch <= 65535, 1 <= smaller side <= 16384, larger side <= 2^20, "
-                                     "batch * ceil(rows / 256) * ceil(cols / 256) < 2^30");
-  const size_t es = elem_size(grad_dtype);
-  Array in, res;
-  if ((rc = ortho_array("grad", grad, es, batch, rows, cols, grad_batch_stride, grad_row_stride, mem, &in)) ||
-      (rc = ortho_array("out", out, 2, batch, rows, cols, out_batch_stride, out_row_stride, mem, &res)))
-    return rc;
-  const ewg::OrthoShape shape = ewg::make_ortho_shape(batch, rows, cols);
-  const size_t need = ewg::make_ortho_layout(shape).total;
-  if (!workspace || !aligned(workspace, 256) || workspace_bytes < need || !mem.has(workspace))
-    return fail(EWG_ERR_INVALID, "workspace null, misaligned, not on the device or smaller than "
-                                 "ewg_orthogonalize_workspace_bytes(batch, rows, cols)");
-  const Array ws = flat("workspace", workspace, static_cast<int64_t>(need), 1);
-  if ((rc = check_apart(res, in)) || (rc = check_apart(ws, in)) || (rc = check_apart(ws, res))) return rc;
-  if (!shape.small() && (rc = prepare_orthogonalize_on(dev))) return rc;
-  ewg::OrthoCall q{};
-  q.shape = shape;
-  q.grad = grad;
-  q.grad_bf16 = grad_dtype == EWG_BF16;
-  q.grad_batch_stride = grad_batch_stride;
-  q.grad_row_stride = grad_row_stride;
-  q.out = out;
-  q.out_batch_stride = out_batch_stride;
-  q.out_row_stride = out_row_stride;
-  q.steps = steps;
-  q.a = a;
-  q.b = b;
-  q.c = c;
-  q.workspace = workspace;
-  const cudaStream_t on = static_cast<cudaStream_t>(stream);
-  cudaError_t e = shape.small() ? ewg::launch_orthogonalize_small(q, sms, on) : ewg::launch_orthogonalize(q, on);
-  return e == cudaSuccess ? EWG_OK : cuda_fail(e, "orthogonalisation launch");
+  return orthogonalize(false, grad, grad_dtype, batch, rows, cols, grad_batch_stride, grad_row_stride, out,
+                       out_batch_stride, out_row_stride, steps, a, b, c, workspace, workspace_bytes, stream);
+}
+
+int ewg_orthogonalize_transposed(const void* grad, int grad_dtype, int64_t batch, int64_t rows, int64_t cols,
+                                 int64_t grad_batch_stride, int64_t grad_row_stride, void* out,
+                                 int64_t out_batch_stride, int64_t out_row_stride, int steps, float a, float b, float c,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  return orthogonalize(true, grad, grad_dtype, batch, rows, cols, grad_batch_stride, grad_row_stride, out,
+                       out_batch_stride, out_row_stride, steps, a, b, c, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

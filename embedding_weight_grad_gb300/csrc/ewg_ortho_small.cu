@@ -448,7 +448,7 @@ cudaError_t launch_orthogonalize_small(const OrthoCall& q, int num_sms, cudaStre
   a.cb = q.b;
   a.cc = q.c;
   a.first = 1;
-  a.out_tall = sh.tall;
+  a.out_tall = q.out_tall;
   a.x = reinterpret_cast<float*>(ws + L.small_x);
   a.out = static_cast<__nv_bfloat16*>(q.out);
   a.out_batch = q.out_batch_stride;

@@ -404,7 +404,7 @@ struct OrthoArgs {
   float* partial;                    // split products: [batch][block][part][CTA][warp][column][row]
   __nv_bfloat16* out;
   long long out_batch, out_row;
-  int tall;
+  int out_tall;                      // out is [c, r]
   Header* header;
   int* ready;                        // [phase][batch][block row]: warps done, over all steps
   int* arrived;                      // [phase][batch][block][CTA][warp]: parts done, over all steps
@@ -678,7 +678,7 @@ __device__ __forceinline__ void store_out(const OrthoArgs& a, int z, int j0, int
   const int lane = threadIdx.x % 32, jx = j0 + lane;
   const int n = min(a.r - i0, kStrip);
   uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + z * a.out_batch;
-  if (!a.tall) {                     // out is [r, c]: neighbouring lanes, neighbouring elements
+  if (!a.out_tall) {                 // out is [r, c]: neighbouring lanes, neighbouring elements
     uint16_t* p = out + i0 * a.out_row + jx;
     if (jx >= a.c) return;
 #pragma unroll
@@ -1325,7 +1325,7 @@ cudaError_t launch_orthogonalize(const OrthoCall& q, cudaStream_t stream) {
   a.out = static_cast<__nv_bfloat16*>(q.out);
   a.out_batch = q.out_batch_stride;
   a.out_row = q.out_row_stride;
-  a.tall = sh.tall;
+  a.out_tall = q.out_tall;
   a.header = in.header;
   a.ready = in.counters;
   a.arrived = in.counters + sh.batch * 3 * nr;

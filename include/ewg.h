@@ -371,6 +371,17 @@ int ewg_orthogonalize(const void* grad, int grad_dtype, int64_t batch, int64_t r
                       void* stream);
 
 /*
+ * ewg_orthogonalize with each result transposed: out is [batch][cols][rows], rows of it
+ * out_row_stride >= rows elements apart.  (For a grad that is the transpose of a row-major
+ * matrix and an out that is row-major, or the other way round.)
+ */
+int ewg_orthogonalize_transposed(const void* grad, int grad_dtype, int64_t batch, int64_t rows,
+                                 int64_t cols, int64_t grad_batch_stride,
+                                 int64_t grad_row_stride, void* out, int64_t out_batch_stride,
+                                 int64_t out_row_stride, int steps, float a, float b, float c,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Waits for `stream`, then copies the device status of the last ewg_plan /
  * ewg_apply / ewg_accumulate that used this workspace into *status (EWG_OK,
  * EWG_ERR_ID_OUT_OF_RANGE, EWG_ERR_INVALID or EWG_ERR_TIMEOUT).  Returns EWG_OK or

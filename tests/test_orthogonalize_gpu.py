@@ -292,3 +292,31 @@ def test_tall_results_of_any_alignment(batch, rows, cols):
             ewg.orthogonalize_update(G, out=out[:, :, at:at + cols], check=True)
             assert torch.equal(out[:, :, at:at + cols], want)
             assert int((out == 7.0).sum()) == out.numel() - want.numel()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("batch,rows,cols", [(1, 1, 1), (2, 1, 9), (1, 8, 13), (3, 32, 32), (2, 70, 300), (1, 256, 256),
+                                             (2, 333, 200), (1, 40, 5000), (1, 600, 1001)])
+def test_out_lies_as_it_likes(batch, rows, cols, dtype):
+    """A row-major or a transposed gradient into a row-major or a transposed out, in any
+    combination: the bits that the gradient has without one, and nothing written beside them."""
+    G = randn(batch, rows, cols, dtype=dtype, seed=rows)
+    for grad in (G, G.mT.contiguous().mT):
+        want = ewg.orthogonalize_update(grad, check=True)
+        for wide in (0, 1, 5, 8):
+            plain = torch.full((batch, rows, cols + wide), 7.0, dtype=BF16, device=DEV)
+            turned = torch.full((batch, cols, rows + wide), 7.0, dtype=BF16, device=DEV)
+            for buf, out in ((plain, plain[:, :, wide // 2:wide // 2 + cols]),
+                             (turned, turned[:, :, wide // 2:wide // 2 + rows].mT)):
+                got = ewg.orthogonalize_update(grad, out=out, check=True)
+                assert got.data_ptr() == out.data_ptr() and got.stride() == out.stride()
+                assert torch.equal(out, want)
+                assert int((buf == 7.0).sum()) == buf.numel() - want.numel()
+    one = torch.empty(cols, rows, dtype=BF16, device=DEV).mT
+    assert torch.equal(ewg.orthogonalize_update(G[0], out=one), ewg.orthogonalize_update(G[0]))
+
+
+def test_out_with_gaps_in_rows_and_columns_is_refused():
+    G = randn(2, 30, 40)
+    with pytest.raises(ValueError):
+        ewg.orthogonalize_update(G, out=torch.empty(2, 30, 80, dtype=BF16, device=DEV)[:, :, ::2])
