@@ -436,6 +436,12 @@ def _row_stride(name, what, x, n, V):
     return x.stride(0) if n > 1 else V
 
 
+def _written(out):
+    """Tells autograd that the library has written a caller's tensor, so that a graph that saved
+    what was there raises instead of using it."""
+    torch.autograd.graph.increment_version(out)
+
+
 def _status_ws(workspace, check, device):
     """(workspace, its pointer, its bytes); without one and without check there is none."""
     if workspace is None:
@@ -458,6 +464,10 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, *, scale: float 
     check=True the call waits for it and raises EwgError if a target was vocab or more
     (whose logprob is NaN).  workspace: status_workspace(), to read the status later with
     read_status.
+
+    The results carry no autograd graph, whether or not logits requires gradients: their
+    gradient is token_logprobs_backward, for the caller's own torch.autograd.Function or
+    training step.
     """
     index, n, V, stride = _logits_args("token_logprobs", logits, targets)
     if not 0 <= top <= min(V, MAX_TOP):
@@ -495,7 +505,8 @@ def token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor, row_max
     and scale; grad_logprobs and grad_entropy are fp32 of the targets' shape (entropy is only
     read with grad_entropy).  out: where to write; out=logits replaces the logits.  Without
     it the gradient is allocated, with the logits' row padding where that is less than an
-    eighth of a row.  Padding rows get zeros.
+    eighth of a row.  Padding rows get zeros.  (Autograd is told that out was written: a graph
+    that saved the logits replaced by it raises in its backward pass.)
     """
     index, n, V, stride = _logits_args("token_logprobs_backward", logits, targets)
     if grad_entropy is not None and entropy is None:
@@ -507,7 +518,8 @@ def token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor, row_max
                 or not t.is_contiguous():
             raise ValueError("row_max, log_sum, entropy and the incoming gradients must be contiguous "
                              "fp32 tensors of the targets' shape on the logits' device")
-    if out is None:
+    given = out is not None
+    if not given:
         if stride == V or stride > V + V // 8:
             out, out_stride = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device), V
         else:
@@ -524,6 +536,8 @@ def token_logprobs_backward(logits: torch.Tensor, targets: torch.Tensor, row_max
              stride, targets.data_ptr(), _ID_CODES[targets.dtype], n, V, scale, row_max.data_ptr(),
              log_sum.data_ptr(), entropy.data_ptr() if both else None, grad_logprobs.data_ptr(),
              grad_entropy.data_ptr() if both else None, out.data_ptr(), out_stride, ws_ptr, ws_bytes)
+    if given:
+        _written(out)
     if check and n:
         raise_on_device_status(ws)
     return out
@@ -578,7 +592,8 @@ def orthogonalize_update(grad: torch.Tensor, *, steps: int = 5,
         return orthogonalize_update(grad.mT, steps=steps, coefficients=coefficients,
                                     out=None if out is None else out.mT, workspace=workspace,
                                     check=check).mT
-    if out is None:
+    given = out is not None
+    if not given:
         out = torch.empty(grad.shape, dtype=torch.bfloat16, device=grad.device)
     if grad.numel() == 0 and 0 not in grad.shape[-2:]:
         return out
@@ -591,6 +606,8 @@ def orthogonalize_update(grad: torch.Tensor, *, steps: int = 5,
     _enqueue(grad.get_device(), call, g3.data_ptr(), _FLOAT_CODES[grad.dtype],
              batch, rows, cols, g3.stride(0), g3.stride(1), o3.data_ptr(), o3.stride(0),
              o3.stride(1), steps, *coefficients, ws.data_ptr(), ws.numel())
+    if given:
+        _written(out)
     if check:
         raise_on_device_status(ws)
     return out

@@ -510,3 +510,45 @@ def test_largest_scales(scale, V, top):
         assert bool((got[0] == 0).all())
         assert abs(got[1, 0].item() - half) <= 2.0 ** -8 * half and abs(got[1, V - 1].item() + half) <= 2.0 ** -8 * half
         assert bool((got[1, 1:V - 1] == 0).all())
+
+
+def test_autograd_is_told_of_logits_replaced():
+    """A graph that saved the logits raises once the gradient has been written over them."""
+    x = torch.randn(4, 50, device=DEV, requires_grad=True)
+    t = torch.zeros(4, dtype=torch.int64, device=DEV)
+    G = torch.ones(4, device=DEV)
+    z = x * 1.0
+    saved = (z * z).sum()
+    r = ewg.token_logprobs(z, t)
+    assert not any(y.requires_grad for y in r if y is not None)
+    version = z._version
+    ewg.token_logprobs_backward(z, t, r.row_max, r.log_sum, G)           # to a tensor of its own
+    assert z._version == version
+    ewg.token_logprobs_backward(z, t, r.row_max, r.log_sum, G, out=z)
+    assert z._version > version
+    with pytest.raises(RuntimeError, match="inplace"):
+        saved.backward()
+    with torch.inference_mode():                                          # tensors without a count
+        z = torch.randn(4, 50, device=DEV)
+        r = ewg.token_logprobs(z, t)
+        ewg.token_logprobs_backward(z, t, r.row_max, r.log_sum, G, out=z)
+
+
+def test_as_an_autograd_function():
+    """The two calls as the halves of a function: the gradient of log_softmax in 64 bits."""
+    class Logprobs(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, logits, targets):
+            r = ewg.token_logprobs(logits, targets)
+            ctx.save_for_backward(logits, targets, r.row_max, r.log_sum)
+            return r.logprobs
+
+        @staticmethod
+        def backward(ctx, grad):
+            logits, targets, row_max, log_sum = ctx.saved_tensors
+            return ewg.token_logprobs_backward(logits, targets, row_max, log_sum, grad.contiguous()), None
+    x, t = make(7, 333, FP32, seed=1)
+    x.requires_grad_()
+    w = torch.randn(7, device=DEV)
+    (Logprobs.apply(x * 1.0, t) * w).sum().backward()
+    check_backward(x.detach(), t, 1.0, w, None, x.grad)

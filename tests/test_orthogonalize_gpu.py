@@ -320,3 +320,12 @@ def test_out_with_gaps_in_rows_and_columns_is_refused():
     G = randn(2, 30, 40)
     with pytest.raises(ValueError):
         ewg.orthogonalize_update(G, out=torch.empty(2, 30, 80, dtype=BF16, device=DEV)[:, :, ::2])
+
+
+def test_autograd_is_told_of_out_written():
+    G = randn(40, 60)
+    for out in (torch.zeros(40, 60, dtype=BF16, device=DEV), torch.zeros(60, 40, dtype=BF16, device=DEV).mT):
+        for grad in (G, G.mT.contiguous().mT):
+            version = out._version
+            ewg.orthogonalize_update(grad, out=out)
+            assert out._version > version
