@@ -141,23 +141,31 @@ __device__ __forceinline__ long long target_of(const void* targets, int is64, lo
   return is64 ? static_cast<const long long*>(targets)[row] : static_cast<const int*>(targets)[row];
 }
 
-// Writes the call's device status: EWG_ERR_ID_OUT_OF_RANGE if a target is V or more.
-// Run by all `threads` threads of one block.
-__device__ void report_targets(const void* targets, int is64, int n, int V, int* status, int threads) {
+// Whether one of the targets i, i + step, i + 2 step, ... is V or more.
+__device__ __forceinline__ bool bad_target(const void* targets, int is64, int n, int V, long long i, long long step) {
   bool bad = false;
   constexpr int kU = 8;
-  for (long long i = threadIdx.x; i < n; i += static_cast<long long>(threads) * kU) {
+  for (; i < n; i += step * kU) {
     long long t[kU];
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const long long at = i + static_cast<long long>(u) * threads;
-      t[u] = at < n ? target_of(targets, is64, at) : -1;
-    }
+    for (int u = 0; u < kU; ++u) t[u] = i + u * step < n ? target_of(targets, is64, i + u * step) : -1;
 #pragma unroll
     for (int u = 0; u < kU; ++u) bad |= t[u] >= V;
   }
-  bad = __syncthreads_or(bad);
+  return bad;
+}
+
+// Writes the call's device status: EWG_ERR_ID_OUT_OF_RANGE if a target is V or more.
+// Run by all `threads` threads of one block.
+__device__ void report_targets(const void* targets, int is64, int n, int V, int* status, int threads) {
+  const bool bad = __syncthreads_or(bad_target(targets, is64, n, V, threadIdx.x, threads));
   if (threadIdx.x == 0) *status = bad ? kStatusBadId : kStatusOk;
+}
+
+// The same by a whole grid, to a status that is kStatusOk before.
+__global__ void __launch_bounds__(256) targets_kernel(const void* targets, int is64, int n, int V, int* status) {
+  const long long at = blockIdx.x * 256LL + threadIdx.x;
+  if (bad_target(targets, is64, n, V, at, gridDim.x * 256LL)) *status = kStatusBadId;
 }
 
 // A row's (or a slice's) statistics: maximum, the sum of the other terms relative to it (-1
@@ -948,13 +956,38 @@ cudaError_t launch_grad_of(const LogprobsGradArgs& a, cudaStream_t stream) {
                               : launch_grad<T, 256>(a, nv, stream);
 }
 
+// The status of a call that moves `row_bytes` for a row: by the first block of its kernel, which reads
+// all targets before the others are through where rows are long; else by a grid ahead of the kernel
+// (args.status is then null).  In us, forward and backward, bf16:
+//
+//                   no status      one block      a grid ahead
+//   1000000 x 100   74.3  119      229   335      79.5  126
+//    262144 x 256   27.5   58       47    91      31.4   64
+//    262144 x 512   47.0   98.4     51.0  98.8    51.9
+template <typename Args>
+cudaError_t report_apart(Args& a, long long row_bytes, cudaStream_t stream) {
+  if (!a.status || a.n <= 65536 || row_bytes > 1024) return cudaSuccess;
+  static_assert(kStatusOk == 0, "the word's bytes");
+  cudaError_t e = cudaMemsetAsync(a.status, 0, sizeof(int), stream);
+  if (e != cudaSuccess) return e;
+  targets_kernel<<<static_cast<unsigned>((a.n + 2047LL) / 2048), 256, 0, stream>>>(a.targets, a.targets_int64, a.n, a.V, a.status);
+  a.status = nullptr;
+  return cudaGetLastError();
+}
+
 }  // namespace
 
-cudaError_t launch_logprobs(const LogprobsArgs& a, bool bf16, int num_sms, cudaStream_t stream) {
+cudaError_t launch_logprobs(const LogprobsArgs& args, bool bf16, int num_sms, cudaStream_t stream) {
+  LogprobsArgs a = args;
+  const cudaError_t e = report_apart(a, a.V * (bf16 ? 2LL : 4LL), stream);
+  if (e != cudaSuccess) return e;
   return bf16 ? launch_forward_of<__nv_bfloat16>(a, num_sms, stream) : launch_forward_of<float>(a, num_sms, stream);
 }
 
-cudaError_t launch_logprobs_grad(const LogprobsGradArgs& a, bool bf16, cudaStream_t stream) {
+cudaError_t launch_logprobs_grad(const LogprobsGradArgs& args, bool bf16, cudaStream_t stream) {
+  LogprobsGradArgs a = args;
+  const cudaError_t e = report_apart(a, 2 * a.V * (bf16 ? 2LL : 4LL), stream);
+  if (e != cudaSuccess) return e;
   return bf16 ? launch_grad_of<__nv_bfloat16>(a, stream) : launch_grad_of<float>(a, stream);
 }
 

@@ -292,7 +292,8 @@ int ewg_accumulate_static(const void* ids, int ids_dtype, int64_t num_tokens,
  * Requires 0 <= num_tokens < 2^31 (0: nothing is enqueued, not even the status), 1 <= vocab < 2^31 - 64, finite
  * scale > 0, 0 <= top <= min(vocab, EWG_MAX_TOP); outputs apart from the inputs and each
  * other.  workspace: NULL, or 256 device bytes, 256-byte aligned, that receive the device
- * status for ewg_read_status.  Enqueues one kernel; allocates nothing.
+ * status for ewg_read_status.  Enqueues one kernel, and for the status of more than 65536 short
+ * rows a memset and a kernel over the targets before it; allocates nothing.
  */
 int ewg_token_logprobs(const void* logits, int logits_dtype, int64_t row_stride,
                        const void* targets, int targets_dtype, int64_t num_tokens,

@@ -552,3 +552,39 @@ def test_as_an_autograd_function():
     w = torch.randn(7, device=DEV)
     (Logprobs.apply(x * 1.0, t) * w).sum().backward()
     check_backward(x.detach(), t, 1.0, w, None, x.grad)
+
+
+def test_status_of_many_short_rows():
+    """The status of 3 000 000 rows costs a part of the call, not a multiple (one block read all
+    targets: 6 times), and tells of a single bad target, wherever it stands."""
+    n, V = 3000000, 40
+    z = torch.randn(n, V, device=DEV, dtype=BF16)
+    t = torch.randint(V, (n,), device=DEV)
+    ws = ewg.status_workspace()
+    r = ewg.token_logprobs(z, t)
+    G = torch.ones(n, device=DEV)
+    out = torch.empty_like(z)
+    for call in (lambda **how: ewg.token_logprobs(z, t, **how),
+                 lambda **how: ewg.token_logprobs_backward(z, t, r.row_max, r.log_sum, G, out=out, **how)):
+        def shortest(**how):
+            times = []
+            for _ in range(12):
+                a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+                a.record()
+                call(**how)
+                b.record()
+                b.synchronize()
+                times.append(a.elapsed_time(b))
+            return min(times)
+        assert shortest(workspace=ws) < 2 * shortest()
+        assert ewg.read_status(ws) == ewg.OK
+        for at in (0, 65537, 1234567, n - 1):
+            good = int(t[at])
+            t[at] = V
+            ws.fill_(0)
+            call(workspace=ws)
+            assert ewg.read_status(ws) == ewg.ERR_ID_OUT_OF_RANGE
+            t[at] = good
+        ws.fill_(255)
+        call(workspace=ws)
+        assert ewg.read_status(ws) == ewg.OK
