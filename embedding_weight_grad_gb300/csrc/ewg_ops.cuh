@@ -68,7 +68,7 @@ struct OrthoShape {
   int64_t r, c, ld;                       // ld: r rounded up to 16, the pitch of every buffer
   int64_t blocks_r, blocks_c;
   int norm_blocks;
-  int split_gram, split_poly;             // parts of the inner dimension of X X^T and A A
+  int split;                              // parts of the inner dimension of X X^T
   int small_parts;                        // shares of the larger side, where the smaller one is small
   bool tall;
 
@@ -76,11 +76,10 @@ struct OrthoShape {
   int64_t square_blocks() const { return blocks_r * (blocks_r + 1) / 2; }
   // counters of the steps kernel for one matrix
   int64_t counters() const {
-    return 3 * blocks_r + (split_gram > 1 || split_poly > 1 ? 2 * square_blocks() * kOrthoWarps : 0);
+    return 3 * blocks_r + (split > 1 ? square_blocks() * kOrthoWarps : 0);
   }
   int64_t partial_floats() const {
-    const int most = split_gram > split_poly ? split_gram : split_poly;
-    return most > 1 ? batch * square_blocks() * most * kOrthoBlock * kOrthoBlock : 0;
+    return split > 1 ? batch * square_blocks() * split * kOrthoBlock * kOrthoBlock : 0;
   }
 };
 
@@ -89,12 +88,13 @@ struct OrthoLayout {
   size_t small_gram, small_exponents, small_m, small_factors, small_x;
 };
 
-// Parts of an inner dimension of `inner` for `units` blocks: as many as leave no more units than
+// Parts of the inner dimension `inner` of X X^T for `units` blocks: as many as leave no more units than
 // `pairs`, each of at least kOrthoPartMin; fewer pairs never give more parts.  The workspace is laid
 // out for kOrthoPairs, and a launch splits for the pairs that run at once where those are
 // fewer: parts wait for one another.  Adding the parts up takes about 8 us, and
 // 64 of the inner dimension 0.3 us, so that shorter ones than kOrthoSplitMin stay whole (2048 in
-// two parts: 20 us instead of 15; 4097 in four: 15 instead of 23).
+// two parts: 20 us instead of 15; 4097 in four: 15 instead of 23).  (A A has too many blocks for a
+// split wherever its inner dimension is that long: 136 of them at 4096.)
 constexpr int64_t kOrthoPairs = 76;
 constexpr int64_t kOrthoPartMin = 1024;
 constexpr int64_t kOrthoSplitMin = 4096;
@@ -126,8 +126,7 @@ inline OrthoShape make_ortho_shape(int64_t batch, int64_t rows, int64_t cols) {
   // 32 shares of 64 (which one block adds up), and more once they are of 16 times that
   const int64_t tiles = (s.c + 63) / 64, shares = tiles / 16 < 32 ? 32 : tiles / 16 < 152 ? tiles / 16 : 152;
   s.small_parts = static_cast<int>(tiles < shares ? tiles : shares);
-  s.split_gram = ortho_split(batch * s.square_blocks(), s.c);
-  s.split_poly = ortho_split(batch * s.square_blocks(), s.r);
+  s.split = ortho_split(batch * s.square_blocks(), s.c);
   return s;
 }
 

@@ -400,14 +400,14 @@ struct OrthoArgs {
   float* diag_a[2];                  // [batch][ld]: what rounding left of the diagonals
   float* diag_b;
   int fused;                         // matrices of one block: A stays with the pair that computed it
-  int split[2];                      // parts of the inner dimension of X X^T and A A
-  float* partial;                    // split products: [batch][block][part][CTA][warp][column][row]
+  int split;                         // parts of the inner dimension of X X^T
+  float* partial;                    // a split product: [batch][block][part][CTA][warp][column][row]
   __nv_bfloat16* out;
   long long out_batch, out_row;
   int out_tall;                      // out is [c, r]
   Header* header;
   int* ready;                        // [phase][batch][block row]: warps done, over all steps
-  int* arrived;                      // [phase][batch][block][CTA][warp]: parts done, over all steps
+  int* arrived;                      // [batch][block][CTA][warp]: parts done, over all steps
 };
 
 struct GemmSmem {
@@ -433,9 +433,11 @@ struct Unit {
   int z, I, J, part;
 };
 
+__device__ __forceinline__ int parts_of(const OrthoArgs& a, int phase) { return phase == kGram ? a.split : 1; }
+
 __device__ __forceinline__ int units_of(const OrthoArgs& a, int phase) {
   const int nr = blocks_of(a.r);
-  return a.batch * (phase == kUpdate ? nr * blocks_of(a.c) : nr * (nr + 1) / 2 * a.split[phase]);
+  return a.batch * (phase == kUpdate ? nr * blocks_of(a.c) : nr * (nr + 1) / 2 * parts_of(a, phase));
 }
 
 // Unit t of a phase.  The orders let a phase start before the one before it has ended: the
@@ -453,7 +455,7 @@ __device__ __forceinline__ Unit unit_at(const OrthoArgs& a, int phase, int t) {
     x.part = 0;
     return x;
   }
-  const int blocks = nr * (nr + 1) / 2, parts = a.split[phase];
+  const int blocks = nr * (nr + 1) / 2, parts = parts_of(a, phase);
   x.z = t / (blocks * parts);
   t -= x.z * blocks * parts;
   x.part = t % parts;
@@ -471,7 +473,7 @@ __device__ __forceinline__ Unit unit_at(const OrthoArgs& a, int phase, int t) {
 // The inner blocks [first, last) of a unit.
 __device__ __forceinline__ void inner_of(const OrthoArgs& a, int phase, const Unit& x, int& first, int& last) {
   const int blocks = ((phase == kGram ? a.c : a.r) + kStepK - 1) / kStepK;
-  const int per = phase == kUpdate ? blocks : (blocks + a.split[phase] - 1) / a.split[phase];
+  const int parts = parts_of(a, phase), per = (blocks + parts - 1) / parts;
   first = x.part * per;
   last = min(first + per, blocks);
 }
@@ -524,7 +526,7 @@ __device__ bool wait_inputs(const OrthoArgs& a, int phase, int step, const Unit&
     return wait_ready(a, ready_at(a, kUpdate, x.z, x.I), want, abort) &&
            (x.I == x.J || wait_ready(a, ready_at(a, kUpdate, x.z, x.J), want, abort));
   }
-  const int want = (step + 1) * nr * kWarpsOfBlock * a.split[phase == kPoly ? kGram : kPoly];
+  const int want = (step + 1) * nr * kWarpsOfBlock * (phase == kPoly ? a.split : 1);
   if (phase == kPoly && a.fused) return true;
   if (phase == kPoly)
     return wait_ready(a, ready_at(a, kGram, x.z, x.I), want, abort) &&
@@ -826,7 +828,7 @@ __device__ __forceinline__ uint4 finish8(const OrthoArgs& a, int cur, float f, f
 // Matrices of one block (a.fused): A is left in the slots, which form an operand, and the
 // same pair goes on to B.
 //
-// Where the inner dimension is split, each part's warp stores its sums, waits for the other
+// Where the inner dimension of X X^T is split, each part's warp stores its sums, waits for the other
 // parts' and finishes its share of the columns, in sixteens, from all parts' sums, added
 // in their order.  (The units of such a phase are no more than the pairs of the launch, see
 // ortho_split, so the parts run at the same time.)
@@ -842,10 +844,9 @@ __device__ __forceinline__ bool epilogue_square(const OrthoMaps& maps, const Ort
   ptx::tmem_fence_after();
   float rest_a = 0.0f;               // what rounding left of A_ii
   if (kPhase == kPoly && row) rest_a = __ldcg(a.diag_a[cur] + diag_at);
-  const int parts = a.split[kPhase];
   const float f = kPhase == kGram ? 1.0f / (a.s * a.s) : a.cc;
-  if (parts > 1) {
-    const int nr = blocks_of(a.r), blocks = nr * (nr + 1) / 2;
+  if (kPhase == kGram && a.split > 1) {
+    const int parts = a.split, nr = blocks_of(a.r), blocks = nr * (nr + 1) / 2;
     const long long block = static_cast<long long>(x.z) * blocks + x.I * (x.I + 1) / 2 + x.J;
     constexpr int kPartStride = kBlock * kBlock;
     const float* sums = a.partial + block * parts * kPartStride + in.place * (32 * kWarpCols) + lane;
@@ -861,16 +862,12 @@ __device__ __forceinline__ bool epilogue_square(const OrthoMaps& maps, const Ort
     release_acc(in.empty);
     bool ok = true;
     if (lane == 0) {
-      int* arrived = a.arrived + ((static_cast<long long>(x.z) * 2 + kPhase) * blocks + x.I * (x.I + 1) / 2 + x.J) *
-                                     kWarpsOfBlock + in.place;
+      int* arrived = a.arrived + block * kWarpsOfBlock + in.place;
       ptx::red_release_add(arrived, 1);
       ok = wait_ready(a, arrived, (step + 1) * parts, in.abort);
     }
     if (!__all_sync(kAll, ok)) return false;
-    if (kPhase == kPoly)
-      for (int u = 0; u < pieces; ++u)
-        if (!wait_piece(in, u, parity)) return false;
-    __half* m = (kPhase == kGram ? a.a[cur] : a.b) + (static_cast<long long>(x.z) * a.r + i) * a.ld + j;
+    __half* m = a.a[cur] + (static_cast<long long>(x.z) * a.r + i) * a.ld + j;
     constexpr int kShares = kWarpCols / 16;
 #pragma unroll 1
     for (int g = x.part * kShares / parts; g < (x.part + 1) * kShares / parts; ++g) {
@@ -886,9 +883,7 @@ __device__ __forceinline__ bool epilogue_square(const OrthoMaps& maps, const Ort
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int col = 16 * g + 8 * e;
-        uint4 o = {};
-        if (kPhase == kPoly) o = lds_v4(chunk_at(in.slot + col / kPiece * kHalfStride, col / 8 % 8));
-        const uint4 w = finish8<kPhase>(a, cur, f, v[e], o, i - (j + col), rest_a, row ? diag_at : -1);
+        const uint4 w = finish8<kPhase>(a, cur, f, v[e], uint4{}, i - (j + col), rest_a, row ? diag_at : -1);
         if (row) *reinterpret_cast<uint4*>(m + col) = w;      // (the sixteen lie inside ld)
       }
     }
@@ -1333,8 +1328,7 @@ cudaError_t launch_orthogonalize(const OrthoCall& q, cudaStream_t stream) {
   int dev = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if (g_pairs[dev] < 1) return cudaErrorLaunchOutOfResources;
-  a.split[kGram] = ortho_split(sh.batch * sh.square_blocks(), sh.c, g_pairs[dev]);
-  a.split[kPoly] = ortho_split(sh.batch * sh.square_blocks(), sh.r, g_pairs[dev]);
+  a.split = ortho_split(sh.batch * sh.square_blocks(), sh.c, g_pairs[dev]);
 
   const unsigned batch = static_cast<unsigned>(sh.batch);
   const int64_t tiles = (sh.cols + 63) / 64 * ((sh.rows + 63) / 64);
@@ -1355,9 +1349,9 @@ cudaError_t launch_orthogonalize(const OrthoCall& q, cudaStream_t stream) {
     if ((e = cudaLaunchKernelEx(&cfg, ortho_scale_kernel, in)) != cudaSuccess) return e;
   }
 
-  const int64_t most = sh.batch * std::max(nr * nc, nr * (nr + 1) / 2 * std::max(a.split[kGram], a.split[kPoly]));
+  const int64_t most = sh.batch * std::max(nr * nc, nr * (nr + 1) / 2 * a.split);
   const int pairs = static_cast<int>(std::min<int64_t>(most, g_pairs[dev]));
-  a.fused = nr == 1 && a.split[kGram] == 1;
+  a.fused = nr == 1 && a.split == 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * pairs);
   cfg.blockDim = dim3(kGemmThreads);

@@ -69,8 +69,8 @@ int main() {
     q.steps = 5;
     const int code = ewg::launch_orthogonalize(q, nullptr);
     const int64_t blocks = q.shape.batch * q.shape.square_blocks();
-    std::printf("%d %d %d %lld %lld\n", code, g_blocks, g_args.split[0], static_cast<long long>(blocks) * g_args.split[0],
-                static_cast<long long>(q.shape.split_gram));
+    std::printf("%d %d %d %lld %lld\n", code, g_blocks, g_args.split, static_cast<long long>(blocks) * g_args.split,
+                static_cast<long long>(q.shape.split));
     std::fflush(stdout);
   }
   return 0;
