@@ -52,3 +52,13 @@ def test_refusals_that_need_no_gpu():
         ewg.token_logprobs_backward(z, t, z[:, 0], z[:, 0], z[:, 0])
     with pytest.raises(ValueError, match="CUDA device"):
         ewg.orthogonalize_update(z)
+
+
+def test_every_device_helper_has_a_caller():
+    """Instruction wrappers that no kernel uses are left over."""
+    csrc = cuda_build.CSRC
+    helpers = re.findall(r"__forceinline__ \w+ (\w+)\(", open(os.path.join(csrc, "ewg_ptx.cuh")).read())
+    assert len(helpers) > 40
+    text = "\n".join(open(os.path.join(csrc, f)).read() for f in sorted(os.listdir(csrc)))
+    unused = [h for h in helpers if len(re.findall(r"\b%s\(" % h, text)) < 2]
+    assert not unused, unused
