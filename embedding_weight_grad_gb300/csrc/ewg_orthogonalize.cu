@@ -379,7 +379,10 @@ constexpr size_t kGemmSmem =
 static_assert(kWarpCols == 128 && kPieces == 2, "a warp's columns, as the epilogue takes them");
 static_assert(kWarpsOfBlock == kOrthoWarps && kBlock == kOrthoBlock, "as the workspace is laid out for");
 static_assert(kGemmSmem + 512 <= 227 * 1024, "stages and slots fit in shared memory");
-constexpr unsigned long long kWaitLimit = 4000000000ull;      // of a wait, in ns
+#ifndef EWG_ORTHO_WAIT_LIMIT                                  // (a test of the limit has a shorter one)
+#define EWG_ORTHO_WAIT_LIMIT 4000000000ull
+#endif
+constexpr unsigned long long kWaitLimit = EWG_ORTHO_WAIT_LIMIT;       // of a wait, in ns
 constexpr uint32_t kPollLimit = 1u << 30;
 
 enum Phase { kGram = 0, kPoly = 1, kUpdate = 2 };
@@ -1020,15 +1023,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       acc_phase ^= 1u;
     }
   };
-  // body(phase, step, unit) for this pair's units in order, until one gives up
-  auto for_units = [&](auto&& body) {
+  // body(phase, step, unit) for this pair's units in order, until one gives up.  `whole`: by all lanes
+  // of a warp, which leave together (bodies return the same in all lanes, by a vote); else by one.
+  auto for_units = [&](bool whole, auto&& body) {
     int offset = 0;                  // units so far, modulo the pairs
     for (int p = 0; p < 3 * a.steps; ++p) {
       const int phase = p % 3, step = p / 3;
       const int units = units_of(a, phase);
       if (a.fused && phase == kPoly) continue;        // with the phase before
       for (int t = pair >= offset ? pair - offset : pair - offset + pairs; t < units; t += pairs) {
-        if (*abort) return;
+        if (whole ? __any_sync(kAll, *abort) : *abort) return;
         if (!body(phase, step, unit_at(a, phase, t)) ||
             (a.fused && phase == kGram && !body(kPoly, step, unit_at(a, kPoly, t)))) {
           gave_up(a, abort);
@@ -1044,7 +1048,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   if (warp == 0) {
     if (lane == 0) {
       int units = 0;
-      for_units([&](int phase, int step, const Unit& x) {
+      for_units(false, [&](int phase, int step, const Unit& x) {
         ++units;
         if (a.fused && phase == kPoly) return true;   // its operands are there
         const int cur = step & 1;
@@ -1077,7 +1081,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     __syncwarp();
   } else if (warp == 1 && rank == 0) {
     if (lane == 0) {
-      for_units([&](int phase, int, const Unit& x) {
+      for_units(false, [&](int phase, int, const Unit& x) {
         int k0, k1;
         inner_of(a, phase, x, k0, k1);
         if (!wait_bar(&sm.acc_empty[acc], acc_phase ^ 1u, abort)) return false;
@@ -1128,7 +1132,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     // parity of a barrier: units of X X^T need no loads, and the epilogue may run ahead there.)
     const int w = lane < kEpilogueWarps ? lane : 0;
     int units = 0;
-    for_units([&](int phase, int step, const Unit& x) {
+    for_units(true, [&](int phase, int step, const Unit& x) {
       bool ok = wait_count(&sm.units_done[w], units++, abort);
       ok = ok && (phase == kGram || wait_count(&sm.units_ready, units, abort));
       if (!__all_sync(kAll, ok)) return false;
@@ -1161,7 +1165,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     // so, 548 where warps 0 and 2 poll; 256 x 256, which only waits: 108 and 105).
     if (lane == 0) {
       int units = 0;
-      for_units([&](int phase, int step, const Unit& x) {
+      for_units(false, [&](int phase, int step, const Unit& x) {
         if (!wait_inputs(a, phase, step, x, abort)) return false;
         ptx::fence_proxy_async();    // the acquires above before the tensor copies
         asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(ptx::smem_u32(&sm.units_ready)), "r"(++units) : "memory");
@@ -1173,7 +1177,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     const int index = warp - kFirstEpilogueWarp;
     const int quarter = warp % 4, part = index / 4;
     uint32_t parity = 0;             // of the slot's barriers
-    for_units([&](int phase, int step, const Unit& x) {
+    for_units(true, [&](int phase, int step, const Unit& x) {
       const Acc in{tmem + acc * kBlock + part * kWarpCols + (static_cast<uint32_t>(quarter) << 21),
                    &sm.acc_full[acc], acc_phase, ptx::map_to_rank(ptx::smem_u32(&sm.acc_empty[acc]), 0), abort,
                    static_cast<int>(rank) * kEpilogueWarps + index, slots + slot_offset(index), sm.piece[index],
