@@ -22,6 +22,8 @@
 //     instead of 2.1e-3 with the bf16 rounding's 1.66e-3, and others worse, up to 3.9e-3: in
 //     directions on which B vanishes its diagonal and the rest of it cancel, but not their
 //     products with differently rounded X.)
+//     The operands' roundings average out over a product's terms where those are many and unlike.  Where
+//     all singular values are equal they do not, least of all for the identity: 7e-3.
 //   * X is stored times s ~ sqrt(r c), a power of two, so that its entries are about 1 at first
 //     and at most 1.2 s; A and B need no scale.
 //

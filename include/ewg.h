@@ -289,11 +289,12 @@ int ewg_accumulate_static(const void* ids, int ids_dtype, int64_t num_tokens,
  * and its other outputs are 0.  A target of vocab or more makes the row's logprobs NaN and
  * the device status EWG_ERR_ID_OUT_OF_RANGE.
  *
- * Requires 0 <= num_tokens < 2^31 (0: nothing is enqueued, not even the status), 1 <= vocab < 2^31 - 64, finite
- * scale > 0, 0 <= top <= min(vocab, EWG_MAX_TOP); outputs apart from the inputs and each
- * other.  workspace: NULL, or 256 device bytes, 256-byte aligned, that receive the device
- * status for ewg_read_status.  Enqueues one kernel, and for the status of more than 65536 short
- * rows a memset and a kernel over the targets before it; allocates nothing.
+ * Requires 0 <= num_tokens < 2^31 (0: nothing is enqueued, not even the status),
+ * 1 <= vocab < 2^31 - 64, finite scale > 0, 0 <= top <= min(vocab, EWG_MAX_TOP); outputs
+ * apart from the inputs and each other.  workspace: NULL, or 256 device bytes, 256-byte
+ * aligned, that receive the device status for ewg_read_status.  Enqueues one kernel, and for
+ * the status of more than 65536 short rows a memset and a kernel over the targets before it;
+ * allocates nothing.
  */
 int ewg_token_logprobs(const void* logits, int logits_dtype, int64_t row_stride,
                        const void* targets, int targets_dtype, int64_t num_tokens,
@@ -345,12 +346,19 @@ size_t ewg_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t co
  * The result is rounded to bf16.  Matrices with a smaller side up to 32 (up to 48 where the
  * larger one is at most 4096) are computed in fp32 throughout and rounded once.  For others
  * the products take fp16 operands with fp32 accumulation; X is kept to 22 bits beside its fp16
- * numbers, and the diagonals of A and of b A + c A^2 exactly to first order.  With the
- * coefficients below the result is then within 2.5e-3 of the exact steps in norm (2.8e-3 where
- * the smaller side is below 64), of which its own rounding to bf16 is 1.7e-3; low-rank updates
- * included.
- * The norm is taken over fp32's whole range, so the scale of G does not matter; a zero matrix stays zero, a NaN or an infinity makes its matrix NaN.  The same
- * call gives the same bits; in another batch a matrix's sums may be split otherwise.
+ * numbers, and the diagonals of A and of b A + c A^2 exactly to first order.  Five steps with
+ * the coefficients below are then within 3e-3 of the exact steps in norm (2.4e-3 where the
+ * smaller side is 256 or more), of which the rounding to bf16 is 1.7e-3, for dense updates of
+ * any decay of the singular values, low-rank ones included.  Where the singular values are all
+ * equal, or the singular vectors are unit vectors, the roundings of fp16 are the same all over
+ * and add up: within 4e-3 for orthogonal matrices, 5e-3 for diagonal ones and 9e-3 for the
+ * identity.  More steps enlarge this (measured after eight: dense updates 3.3e-3, the
+ * identity 2e-2), and each multiplies by `a` what rounding leaves in directions that a low-rank
+ * update does not have (after eight steps 2e-2, after twelve as much as the result).
+ *
+ * The norm is taken over fp32's whole range, so the scale of G does not matter; a zero matrix
+ * stays zero, a NaN or an infinity makes its matrix NaN.  The same call gives the same bits; in
+ * another batch, or as the transpose of a square matrix, sums may be made otherwise.
  *
  *   grad    [batch][rows][cols], EWG_BF16 or EWG_FP32, unit inner stride; any alignment
  *   out     [batch][rows][cols] bf16, unit inner stride, apart from grad
@@ -362,8 +370,8 @@ size_t ewg_orthogonalize_workspace_bytes(int64_t batch, int64_t rows, int64_t co
  * the larger at most 2^20, batch * ceil(rows / 256) * ceil(cols / 256) < 2^30,
  * 1 <= steps <= EWG_MAX_ORTHO_STEPS, finite coefficients, and a workspace as above.
  * Enqueues two small kernels and one cooperative kernel that takes every step, or small ones
- * for every two steps; allocates nothing.  ewg_read_status reports EWG_ERR_TIMEOUT if a bounded wait in it gave up (out
- * is then unspecified).
+ * for every two steps; allocates nothing.  ewg_read_status reports EWG_ERR_TIMEOUT if a bounded
+ * wait in it gave up (out is then unspecified).
  */
 int ewg_orthogonalize(const void* grad, int grad_dtype, int64_t batch, int64_t rows,
                       int64_t cols, int64_t grad_batch_stride, int64_t grad_row_stride,

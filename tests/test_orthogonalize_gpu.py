@@ -329,3 +329,70 @@ def test_autograd_is_told_of_out_written():
             version = out._version
             ewg.orthogonalize_update(grad, out=out)
             assert out._version > version
+
+
+def spectra(kind, rows, cols, g):
+    n = lambda *s: torch.randn(*s, generator=g, device=DEV)
+    k = min(rows, cols)
+    if kind == "dense":
+        return n(rows, cols)
+    if kind == "rank one":
+        return n(rows, 1) @ n(1, cols)
+    if kind == "low rank":
+        return n(rows, 5) @ n(5, cols)
+    if kind == "low rank and noise":
+        return n(rows, 12) @ n(12, cols) + 0.3 * n(rows, cols)
+    if kind == "outlier":
+        G = n(rows, cols)
+        G[rows // 2, cols // 3] = 1e3
+        return G
+    if kind == "rows of many sizes":
+        return n(rows, cols) * torch.logspace(0, -3, rows, device=DEV)[:, None]
+    if kind == "rows without tokens":
+        return n(rows, cols) * (torch.rand(rows, 1, generator=g, device=DEV) < 0.3)
+    if kind == "identity":
+        return torch.eye(max(rows, cols), device=DEV)[:rows, :cols].contiguous()
+    if kind == "diagonal":
+        return torch.eye(max(rows, cols), device=DEV)[:rows, :cols] * (torch.rand(rows, 1, generator=g, device=DEV) + 0.01)
+    u, v = torch.linalg.qr(n(rows, k))[0], torch.linalg.qr(n(cols, k))[0]
+    s = {"orthogonal": lambda i: 1.0 + 0 * i, "slow decay": lambda i: (1.0 + i) ** -0.5,
+         "fast decay": lambda i: (1.0 + i) ** -2.0, "linear": lambda i: 1.0 - i / k}[kind](torch.arange(k, device=DEV))
+    return (u * s) @ v.mT
+
+
+DENSE = ["dense", "rank one", "low rank", "low rank and noise", "outlier", "rows of many sizes", "rows without tokens",
+         "slow decay", "fast decay", "linear"]
+
+
+def errors(rows, cols, kind, seeds):
+    g = torch.Generator(device=DEV).manual_seed(100 * rows + cols)
+    G = torch.stack([spectra(kind, rows, cols, g) for _ in range(seeds)]) * 1e-2
+    got, want = ewg.orthogonalize_update(G, check=True).double(), reference(G)
+    size = want.norm(dim=(-2, -1)).clamp_min(1e-300)
+    return ((got - want).norm(dim=(-2, -1)) / size).max().item(), \
+        ((want.to(BF16).double() - want).norm(dim=(-2, -1)) / size).max().item()
+
+
+@pytest.mark.parametrize("rows,cols", [(33, 5000), (49, 49), (61, 50), (63, 200), (64, 64), (71, 72), (86, 73), (118, 117),
+                                       (128, 1000), (200, 333), (256, 256), (300, 299), (513, 700), (1024, 1030)])
+def test_the_promised_precision(rows, cols):
+    """What include/ewg.h promises of five steps, by the kind of update and the smaller side."""
+    dense = 3e-3 if min(rows, cols) < 256 else 2.4e-3
+    for kind in DENSE:
+        assert errors(rows, cols, kind, 3)[0] < dense, kind
+    for kind, most in (("orthogonal", 4e-3), ("diagonal", 5e-3), ("identity", 9e-3)):
+        assert errors(rows, cols, kind, 3)[0] < most, kind
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 1), (9, 1), (4, 2), (8, 13), (17, 40), (32, 32), (32, 70000), (48, 48),
+                                       (1001, 40)])
+def test_the_promised_precision_of_small_sides(rows, cols):
+    """In fp32 M makes of its own rounding 8 * 2^-24 of a^5 = 485, 2.4e-4 of the largest singular
+    value at most: d.  Where that moves an element to another bf16 number, the exact one was no
+    further than d from the middle between them: the error is that of the exact result's rounding and
+    2 d at most."""
+    for kind in [*DENSE, "orthogonal", "diagonal", "identity"]:
+        if kind in ("rows without tokens", "outlier") and min(rows, cols) < 4:
+            continue                                     # (nothing may be left of it)
+        error, rounding = errors(rows, cols, kind, 1)
+        assert error < rounding + 5e-4, kind
