@@ -17,8 +17,8 @@
 // about -R, and 1 + R in 32 bits would round R away.
 //
 // Both kernels are bound by the one read of the logits (and the one write of the gradient):
-// 8192 x 129280 bf16 takes 294 us (7.2 TB/s; 349 with 8 alternatives, whose logits are mostly
-// gone from L2 when they are read again), its gradient 600 us (7.1 TB/s).
+// 8192 x 129280 bf16 without padding takes 311 us (6.8 TB/s; 348 with 8 alternatives, whose logits
+// are mostly gone from L2 when they are read again), its gradient 608 us (7.0 TB/s).
 #include <cfloat>
 
 #include <cooperative_groups.h>
@@ -262,7 +262,9 @@ struct GroupSmem {
 // where its own term would drown the others (R < 8).
 //
 // 1536 threads on an SM (40 registers each; 2048 take 135 us instead of 126 at 8192 x 50257, 1280
-// take 130), 2048 for bf16 rows of 512 threads.
+// take 130), 2048 for bf16 rows of 512 threads: 32 registers and 96 bytes of spills each, 395 us at
+// 4096 x 310000 (1536: 390), 114 at 2048 x 129280 with 8 alternatives (115), 369 at 4096 x 256000 with
+// 8 (362).
 constexpr int threads_of(int kT) { return kT == 32 ? 256 : kT; }
 template <typename T>
 constexpr int blocks_per_sm(int kT) { return (sizeof(T) == 2 && kT == 512 ? 2048 : 1536) / threads_of(kT); }
@@ -625,7 +627,7 @@ __global__ void __launch_bounds__(threads_of(kT), blocks_per_sm<T>(kT)) logprobs
 // vectors in registers, a warp 32 / kG rows.  Such rows are bound by the instructions that each
 // costs a warp, most of them in the reductions, which here serve several rows at once; and with
 // the whole row at hand the maximum comes first and nothing is rescaled.  131072 x 1024 bf16
-// takes 45.6 us (5.9 TB/s; 52 where the rows are all but sure of a token), a warp a row 61.7
+// takes 46.5 us (5.8 TB/s; 52 where the rows are all but sure of a token), a warp a row 61.7
 // (76); 262144 x 512 45.3 and 120; 65536 x 2048 45.8 and 48.8.
 constexpr int kHeld = 8;
 
@@ -751,7 +753,9 @@ __global__ void __launch_bounds__(256, 4) logprobs_short_kernel(const LogprobsAr
 // token itself takes G (-expm1(log p)) for G (1 - p).
 //
 // Six blocks on an SM (40 registers a thread) and four vectors in flight each: 8192 x 50257 takes
-// 254 us, with four blocks 290, with two vectors 301.
+// 253 us, with four blocks 290, with two vectors 301.  The forms of few threads a row spill (bf16, 4
+// threads: 80 bytes stored and 268 loaded a thread; 8: 32 and 168): 1000000 x 100 takes 126 us so, with
+// four blocks and no spills 124 (fp32 176 and 192); 262144 x 256 64 and 67 (98 and 104).
 template <typename T, int kT>
 __global__ void __launch_bounds__(256, 6) logprobs_grad_kernel(const LogprobsGradArgs a, int items_per_row) {
   using V = Vec<T>;
@@ -914,7 +918,13 @@ cudaError_t launch_forward_of(const LogprobsArgs& a, int num_sms, cudaStream_t s
   //    8192 x129280            312 | 437  294 | 345  327 | 349  (with 20: 425 and 383)
   //    2048 x129280             99 | 131   85 | 101   82 |  92
   // Short rows pay for what a row costs besides its read, which more threads raise; in long
-  // ones few threads leave each with more vectors to read again for the alternatives.
+  // ones few threads leave each with more vectors to read again for the alternatives.  How many
+  // alternatives turn it round (256 | 512 threads, bf16, the same logits without padding):
+  //   8192 x 102400    8: 299 | 302   16: 339 | 316      4096 x 256000    2: 336 | 335    4: 350 | 340
+  //   8192 x 129280    5: 352 | 354    8: 372 | 360      fp32
+  //   4096 x 160000    3: 224 | 228    4: 229 | 228      4096 x  65536    5: 183 | 191    8: 193 | 193
+  //   4096 x 200000    3: 275 | 277    4: 282 | 279      4096 x 129280    4: 341 | 343    5: 347 | 344
+  // at 64000 to 200000 alternatives times vectors of a row; the rule's 131072 costs 4 % at most between.
   const int nv = a.V / Vec<T>::kE;
   const bool many = a.n >= 16 * num_sms;
   // (kHeld vectors a lane are what 64 registers a thread hold)

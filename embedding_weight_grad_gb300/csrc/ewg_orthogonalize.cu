@@ -963,12 +963,12 @@ __device__ __forceinline__ uint32_t idesc_of(Majors mn) {
 //
 // A pair's block of 256 x 256 uses each operand byte it reads for 256 products; a ring of five
 // stages of 64 of the inner dimension (with four, 24 x 1024 x 1024 takes 5 % longer) and the
-// epilogue's slots fill shared memory.  Whole calls of five steps: 7168 x 7168 5.0 ms, 1.47
-// PFLOP/s of the operations that count (3 r^2 c + r^3 a step), bound by the tensor cores at the
-// clock that the power limit leaves; 24 x 1024 x 1024 516 us, 1.0 PFLOP/s, by the update's
-// epilogues, which take as long as its products; 2048 x 7168 505 us, 0.98 PFLOP/s, and smaller
-// ones by the way from a phase's last product to the next one's first (5 to 8 us, three times
-// a step).
+// epilogue's slots fill shared memory.  Whole calls of five steps, each on other inputs: 7168 x 7168
+// 5.2 ms (5.0 to 5.5 by the GPU and its power), 1.42 PFLOP/s of the operations that count (3 r^2 c +
+// r^3 a step), bound by the tensor cores at the clock that the power limit leaves; 24 x 1024 x 1024
+// 549 us (510 on one input over and over), 0.94 PFLOP/s, by the update's epilogues, which take as long
+// as its products; 2048 x 7168 494 us, 1.0 PFLOP/s, and smaller ones by the way from a phase's last
+// product to the next one's first (5 to 8 us, three times a step).
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const OrthoArgs a) {
   extern __shared__ unsigned char raw[];
@@ -1163,7 +1163,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     });
   } else if (warp == 3) {
     // Watches what units wait for, ahead of the copies: a poll of L2 and the fence take 0.7 us, in
-    // which the ring of operands would run low at the start of each unit (24 x 1024 x 1024: 516 us
+    // which the ring of operands would run low at the start of each unit (24 x 1024 x 1024, one input: 516 us
     // so, 548 where warps 0 and 2 poll; 256 x 256, which only waits: 108 and 105).
     if (lane == 0) {
       int units = 0;
