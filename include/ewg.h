@@ -274,7 +274,7 @@ int ewg_accumulate_static(const void* ids, int ids_dtype, int64_t num_tokens,
  *     top_ids, top_logprobs: the `top` largest logits, best first, equal ones by lower id
  *
  * in 32 bits, the row's sums held relative to its maximum; near-certain tokens keep the
- * relative precision of their small -logprob and entropy.
+ * relative precision of their small -logprob and entropy (exponentials below 2^-126 are 0).
  *
  *   logits    [num_tokens][vocab], EWG_BF16 or EWG_FP32, unit inner stride,
  *             row_stride elements between rows (>= vocab; any alignment of the element)
