@@ -240,7 +240,7 @@ def _plain_round8(x, i, t, a, b, positive):
     the plastic number's inverse (for the root the other way round)."""
     biggest = x.abs().amax(1, keepdim=True)
     scale = biggest * (1 / 448)
-    held = scale >= 2.0 ** -120
+    held = ~(scale < 2.0 ** -120)
     inverse = torch.where(held, 1 / scale, 0.0)
     # times 2^-120, e4m3's exponents and its steps below the smallest one are fp32's own
     bits = (x * inverse * 2.0 ** -120).view(torch.int32)
