@@ -8,8 +8,10 @@ module docstring, ``accumulate_embedding_wgrad`` and ``can_accumulate_embedding_
 
 Beside it, the other operators of a training step that deal with the vocabulary and with
 main_grads: ``token_logprobs`` and ``token_logprobs_backward`` (log probabilities of given
-tokens, entropies and the most likely alternatives from logits, and their gradient) and
-``orthogonalize_update`` (the Newton-Schulz orthogonalisation of the Muon optimiser).
+tokens, entropies and the most likely alternatives from logits, and their gradient),
+``orthogonalize_update`` (the Newton-Schulz orthogonalisation of the Muon optimiser),
+``layer_norm`` and ``layer_norm_backward`` (whose weights' gradients go into main_grads) and
+``adamw_plan`` / ``adamw_step`` (AdamW over many tensors at once, with states in 32 bits or in 8).
 
 This module only marshals arguments into the C ABI of ``libewg.so`` (declared in
 ``include/ewg.h``); every step of the computation runs in that library's CUDA
@@ -30,13 +32,16 @@ __all__ = [
     "accumulate_embedding_wgrad", "workspace_bytes", "plan", "apply", "read_status",
     "library_path", "lib", "accumulate_embedding_wgrad_shard", "MAX_TOP", "TokenLogprobs",
     "token_logprobs", "token_logprobs_backward", "status_workspace",
-    "orthogonalize_update", "orthogonalize_workspace",
+    "orthogonalize_update", "orthogonalize_workspace", "LayerNorm", "layer_norm",
+    "layer_norm_backward", "layer_norm_workspace", "ADAMW_BLOCK", "AdamWPlan", "adamw_plan",
+    "adamw_step",
 ]
 
 MIN_TOKENS = 3073
 MAX_TOKENS = 1 << 28
 NROWS = 10
 MAX_TOP = 32
+ADAMW_BLOCK = 256
 
 _INT32, _INT64, _BF16, _FP32 = 0, 1, 2, 3
 OK, ERR_UNSUPPORTED, ERR_INVALID, ERR_CUDA, ERR_ID_OUT_OF_RANGE, ERR_TIMEOUT, ERR_BOUNDS = \
@@ -127,6 +132,20 @@ def _load(path):
     for f in (L.ewg_orthogonalize, L.ewg_orthogonalize_transposed):
         f.argtypes = [vp, i32, i64, i64, i64, i64, i64, vp, i64, i64, i32, f32, f32, f32, vp, sz, vp]
         f.restype = i32
+    f64 = ctypes.c_double
+    L.ewg_layer_norm.argtypes = [vp, i32, i64, i64, i64, vp, vp, i32, f64, vp, i64, vp, vp, vp]
+    L.ewg_layer_norm.restype = i32
+    L.ewg_layer_norm_workspace_bytes.argtypes = [i64, i64]
+    L.ewg_layer_norm_workspace_bytes.restype = sz
+    L.ewg_layer_norm_backward.argtypes = [vp, i64, vp, i64, i32, i64, i64, vp, vp, vp, i32, vp, i64,
+                                          vp, vp, i32, vp, sz, vp]
+    L.ewg_layer_norm_backward.restype = i32
+    L.ewg_adamw_plan_bytes.argtypes = [i64]
+    L.ewg_adamw_plan_bytes.restype = sz
+    L.ewg_adamw_plan.argtypes = [vp, i64, i32, vp, sz]
+    L.ewg_adamw_plan.restype = i32
+    L.ewg_adamw_step.argtypes = [vp, sz, i64, vp, f64, vp, f64, f64, f64, f64, vp, vp]
+    L.ewg_adamw_step.restype = i32
     L.ewg_read_status.argtypes = [vp, vp, ctypes.POINTER(i32)]
     L.ewg_read_status.restype = i32
     L.ewg_status_string.argtypes = [i32]
@@ -437,8 +456,8 @@ def _row_stride(name, what, x, n, V):
 
 
 def _written(out):
-    """Tells autograd that the library has written a caller's tensor, so that a graph that saved
-    what was there raises instead of using it."""
+    """Tells autograd that the library has written a caller's tensor (or several), so that a graph
+    that saved what was there raises instead of using it."""
     torch.autograd.graph.increment_version(out)
 
 
@@ -611,3 +630,260 @@ def orthogonalize_update(grad: torch.Tensor, *, steps: int = 5,
     if check:
         raise_on_device_status(ws)
     return out
+
+
+class LayerNorm(NamedTuple):
+    """What layer_norm returns: the normalised rows, and fp32 tensors of x.shape[:-1] that
+    layer_norm_backward takes."""
+    out: torch.Tensor
+    mean: torch.Tensor
+    rstd: torch.Tensor             # 1 / sqrt(variance + eps)
+
+
+def _norm_rows(name, what, x, shape, dtype, index):
+    """The row stride of x, whose shape, dtype and device have to be these."""
+    if x.shape != shape or x.dtype != dtype or x.get_device() != index:
+        raise ValueError(f"{name} does not support these tensors: {what} must have x's shape, dtype "
+                         "and device")
+    H = shape[-1]
+    return _row_stride(name, what, x, x.numel() // H, H)
+
+
+def _norm_vectors(name, what, vectors, H, index):
+    """(pointers, dtype code) of vectors [H], some of them None."""
+    given = [v for v in vectors if v is not None]
+    for v in given:
+        if v.shape != (H,) or v.dtype not in _FLOAT_CODES or v.dtype != given[0].dtype \
+                or v.get_device() != index or not v.is_contiguous():
+            raise ValueError(f"{name} does not support these tensors: {what} must be contiguous [hidden] "
+                             "vectors of one dtype, bf16/fp32, on x's device")
+    return [None if v is None else v.data_ptr() for v in vectors], \
+        _FLOAT_CODES[given[0].dtype] if given else _FP32
+
+
+def _norm_input(name, x):
+    index = x.get_device()
+    if index < 0 or x.dtype not in _FLOAT_CODES or x.dim() == 0 or x.shape[-1] == 0:
+        raise ValueError(f"{name} does not support these tensors: x must be [..., hidden], bf16/fp32, "
+                         "on a CUDA device")
+    return index, x.shape
+
+
+def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
+               bias: torch.Tensor | None = None, *, eps: float = 1e-5,
+               out: torch.Tensor | None = None) -> LayerNorm:
+    """Each row of x [..., hidden] less its mean, over its standard deviation, times weight, plus
+    bias (see ewg_layer_norm in include/ewg.h), with the rows' means and 1 / standard deviations.
+
+    x: bf16 or fp32, rows of unit inner stride; weight and bias: contiguous [hidden], both bf16 or
+    both fp32, whatever x is (without them ones and zeros); out: where to write, of x's shape and
+    dtype; out=x replaces x.  The work is enqueued on the current stream.
+
+    The results carry no autograd graph: their gradient is layer_norm_backward.
+    """
+    index, shape = _norm_input("layer_norm", x)
+    H = shape[-1]
+    n = x.numel() // H
+    stride = _row_stride("layer_norm", "x", x, n, H)
+    (w, b), code = _norm_vectors("layer_norm", "weight and bias", (weight, bias), H, index)
+    given = out is not None
+    if not given:
+        out, out_stride = torch.empty(shape, dtype=x.dtype, device=x.device), H
+    else:
+        out_stride = _norm_rows("layer_norm", "out", out, shape, x.dtype, index)
+    mean = torch.empty(shape[:-1], dtype=torch.float32, device=x.device)
+    rstd = torch.empty_like(mean)
+    _enqueue(index, lib().ewg_layer_norm, x.data_ptr(), _FLOAT_CODES[x.dtype], n, H, stride, w, b, code,
+             eps, out.data_ptr(), out_stride, mean.data_ptr(), rstd.data_ptr())
+    if given:
+        _written(out)
+    return LayerNorm(out, mean, rstd)
+
+
+def layer_norm_workspace(shape, device=None) -> torch.Tensor:
+    """A device buffer for layer_norm_backward of rows of this shape (no init needed)."""
+    rows = 1
+    for d in shape[:-1]:
+        rows *= d
+    nbytes = int(lib().ewg_layer_norm_workspace_bytes(rows, shape[-1]))
+    if nbytes == 0:
+        raise EwgError(ERR_UNSUPPORTED, "unsupported sizes")
+    return torch.empty(nbytes, dtype=torch.uint8, device=device or "cuda")
+
+
+def layer_norm_backward(grad: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                        weight: torch.Tensor | None = None, *,
+                        weight_main_grad: torch.Tensor | None = None,
+                        bias_main_grad: torch.Tensor | None = None,
+                        out: torch.Tensor | None = None,
+                        workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """The gradient of layer_norm with respect to x, in x's dtype; the weight's and the bias's are
+    added to weight_main_grad and bias_main_grad where these are given (see
+    ewg_layer_norm_backward in include/ewg.h).
+
+    grad: of x's shape and dtype; mean and rstd: what layer_norm returned for x; weight: as given to
+    it.  The main_grads are contiguous [hidden], both bf16 or both fp32, whatever the weight
+    is.  out: where to write; out=grad or out=x replaces it.  workspace:
+    layer_norm_workspace(x.shape), allocated when not given.  The work is enqueued on the current
+    stream; the same call gives the same bits.
+    """
+    name = "layer_norm_backward"
+    index, shape = _norm_input(name, x)
+    H = shape[-1]
+    n = x.numel() // H
+    x_stride = _row_stride(name, "x", x, n, H)
+    grad_stride = _norm_rows(name, "grad", grad, shape, x.dtype, index)
+    for t in (mean, rstd):
+        if t.shape != shape[:-1] or t.dtype != torch.float32 or t.get_device() != index or not t.is_contiguous():
+            raise ValueError("mean and rstd must be contiguous fp32 tensors of x.shape[:-1] on x's device")
+    (w,), w_code = _norm_vectors(name, "weight", (weight,), H, index)
+    main_grads, m_code = _norm_vectors(name, "main_grads", (weight_main_grad, bias_main_grad), H, index)
+    given = out is not None
+    if not given:
+        out, out_stride = torch.empty(shape, dtype=x.dtype, device=x.device), H
+    else:
+        out_stride = _norm_rows(name, "out", out, shape, x.dtype, index)
+    if n == 0:
+        return out
+    ws = workspace if workspace is not None else layer_norm_workspace(shape, x.device)
+    _enqueue(index, lib().ewg_layer_norm_backward, grad.data_ptr(), grad_stride, x.data_ptr(), x_stride,
+             _FLOAT_CODES[x.dtype], n, H, mean.data_ptr(), rstd.data_ptr(), w, w_code, out.data_ptr(),
+             out_stride, *main_grads, m_code, ws.data_ptr(), ws.numel())
+    for t, written in ((out, given), (weight_main_grad, True), (bias_main_grad, True)):
+        if written and t is not None:
+            _written(t)
+    return out
+
+
+class _AdamWTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("exp_avg", ctypes.c_void_p),
+                ("exp_avg_sq", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("copy", ctypes.c_void_p),
+                ("count", ctypes.c_int64), ("weight_decay", ctypes.c_double),
+                ("param_dtype", ctypes.c_int), ("grad_dtype", ctypes.c_int)]
+
+
+class AdamWPlan:
+    """What adamw_plan makes: the tensors of an AdamW step, checked, with their states.
+
+    params, grads, copies: the tensors given; exp_avg, exp_avg_sq, scales: lists of the states, of
+    each param's shape (scales: [blocks, 2] fp32, None in 32 bits).  state_bits 32: exp_avg and
+    exp_avg_sq are fp32.  state_bits 8: they are float8_e4m3fn, and element i of a flattened
+    tensor has the average exp_avg[i] * scales[i // ADAMW_BLOCK, 0] and the second average
+    (exp_avg_sq[i] * scales[i // ADAMW_BLOCK, 1]) ** 2.
+    """
+
+    def __init__(self, params, grads, copies, exp_avg, exp_avg_sq, scales, state_bits, index):
+        self.params, self.grads, self.copies = params, grads, copies
+        self.exp_avg, self.exp_avg_sq, self.scales = exp_avg, exp_avg_sq, scales
+        self.state_bits = state_bits
+        self._index = index
+        self._all = [t for group in (params, grads, exp_avg, exp_avg_sq, scales or (), copies or ())
+                     for t in group if t is not None]
+        self._addresses = [t.data_ptr() for t in self._all]
+        self._written = [t for group in (params, exp_avg, exp_avg_sq, scales or (), copies or ())
+                         for t in group if t is not None]
+        self._buffer = None
+
+
+def _state_list(name, given, params, dtype, shapes):
+    if given is None:
+        return [torch.zeros(s, dtype=dtype, device=p.device) for s, p in zip(shapes, params)]
+    given = list(given)
+    if len(given) != len(params) or any(t.shape != torch.Size(s) or t.dtype != dtype for t, s in zip(given, shapes)):
+        raise ValueError(f"{name} must hold a {dtype} tensor of the right shape for each param")
+    return given
+
+
+def adamw_plan(params, grads, *, state_bits: int = 32, copies=None, weight_decay=0.01,
+               exp_avg=None, exp_avg_sq=None, scales=None) -> AdamWPlan:
+    """Prepares AdamW steps of `params` (see ewg_adamw_plan in include/ewg.h) and makes their states.
+
+    params: bf16 or fp32 CUDA tensors of any shape, contiguous, of one device; grads: their
+    main_grads, bf16 or fp32, from which every adamw_step reads (the tensors, not only their present
+    values: a plan holds addresses); copies: a bf16 tensor (or None) for each param that is fp32,
+    which receives the new param rounded; weight_decay: a number, or one for each param.
+    state_bits: 32, or 8 (with a scale for every ADAMW_BLOCK elements).  exp_avg, exp_avg_sq and
+    scales: states to go on from, shaped as AdamWPlan says; zeros without them.
+
+    The plan holds the tensors; steps update the params, states and copies in place.
+    """
+    params, grads = list(params), list(grads)
+    if state_bits not in (8, 32):
+        raise ValueError("state_bits must be 8 or 32")
+    if len(grads) != len(params):
+        raise ValueError("grads must hold a tensor for each param")
+    copies = [None] * len(params) if copies is None else list(copies)
+    decays = [float(weight_decay)] * len(params) if isinstance(weight_decay, (int, float)) else list(weight_decay)
+    if len(copies) != len(params) or len(decays) != len(params):
+        raise ValueError("copies and weight_decay must hold an element for each param")
+    index = params[0].get_device() if params else None
+    for p, g, c in zip(params, grads, copies):
+        if p.get_device() < 0 or p.dtype not in _FLOAT_CODES or g.dtype not in _FLOAT_CODES:
+            raise ValueError("adamw_plan does not support these tensors: params and grads must be "
+                             "bf16/fp32, on a CUDA device")
+        if g.shape != p.shape or (c is not None and (c.shape != p.shape or c.dtype != torch.bfloat16
+                                                     or p.dtype != torch.float32)):
+            raise ValueError("grads must have the params' shapes; copies too, bf16 beside fp32 params")
+    shapes = [p.shape for p in params]
+    dtype = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
+    exp_avg = _state_list("exp_avg", exp_avg, params, dtype, shapes)
+    exp_avg_sq = _state_list("exp_avg_sq", exp_avg_sq, params, dtype, shapes)
+    if state_bits == 8:
+        blocks = [(-(-p.numel() // ADAMW_BLOCK), 2) for p in params]
+        scales = _state_list("scales", scales, params, torch.float32, blocks)
+    elif scales is not None:
+        raise ValueError("scales belong to states in 8 bits")
+    plan = AdamWPlan(params, grads, copies, exp_avg, exp_avg_sq, scales, state_bits, index)
+    for t in plan._all:
+        if t.get_device() != index or not t.is_contiguous():
+            raise ValueError("adamw_plan does not support these tensors: all must be contiguous, on one device")
+        if t.is_inference():
+            raise ValueError("adamw_plan does not support these tensors: inference tensors cannot be "
+                             "updated in place")
+    L = lib()
+    table = (_AdamWTensor * max(1, len(params)))()
+    for k, t in enumerate(table[:len(params)]):
+        t.param, t.grad = params[k].data_ptr(), grads[k].data_ptr()
+        t.exp_avg, t.exp_avg_sq = exp_avg[k].data_ptr(), exp_avg_sq[k].data_ptr()
+        t.scales = scales[k].data_ptr() if scales is not None else None
+        t.copy = copies[k].data_ptr() if copies[k] is not None else None
+        t.count, t.weight_decay = params[k].numel(), decays[k]
+        t.param_dtype, t.grad_dtype = _FLOAT_CODES[params[k].dtype], _FLOAT_CODES[grads[k].dtype]
+        table[k] = t
+    nbytes = int(L.ewg_adamw_plan_bytes(len(params)))
+    plan._buffer = (ctypes.c_uint64 * (nbytes // 8 + 1))()
+    if params:
+        with torch.cuda.device(index):
+            _raise_on(L.ewg_adamw_plan(table, len(params), state_bits, plan._buffer, ctypes.sizeof(plan._buffer)))
+    return plan
+
+
+def _scalar(name, value, dtype, index):
+    """(value, pointer) of a number or of a device scalar."""
+    if not isinstance(value, torch.Tensor):
+        return value, None
+    if value.numel() != 1 or value.dtype != dtype or value.get_device() != index:
+        raise ValueError(f"{name} must be a number, or one {dtype} element on the params' device")
+    return 0, value.data_ptr()
+
+
+def adamw_step(plan: AdamWPlan, step, *, lr, betas: tuple = (0.9, 0.999), eps: float = 1e-8,
+               grad_scale=1.0) -> None:
+    """One AdamW step of a plan's tensors (see ewg_adamw_step in include/ewg.h), the `step`-th from 1.
+
+    grad_scale multiplies the gradients: a clipping factor, or the inverse of a loss scale.  step
+    (int64), lr and grad_scale (fp32) may be CUDA tensors of one element, which the step reads on
+    the device: a captured step then follows their values.  The work is enqueued on the current
+    stream.  Raises ValueError if a tensor of the plan has moved to another address.
+    """
+    if not plan.params:
+        return
+    if [t.data_ptr() for t in plan._all] != plan._addresses:
+        raise ValueError("a tensor of the plan has moved to another address: make a new plan")
+    index = plan._index
+    step, step_ptr = _scalar("step", step, torch.int64, index)
+    lr, lr_ptr = _scalar("lr", lr, torch.float32, index)
+    grad_scale, scale_ptr = _scalar("grad_scale", grad_scale, torch.float32, index)
+    _enqueue(index, lib().ewg_adamw_step, plan._buffer, ctypes.sizeof(plan._buffer), step, step_ptr, lr, lr_ptr,
+             *betas, eps, grad_scale, scale_ptr)
+    _written(plan._written)

@@ -15,51 +15,6 @@ namespace {
 
 using namespace ewg::host;
 
-// An array of an entry point's arguments: its bytes, and its name for messages.
-struct Array {
-  const char* name;
-  const void* p;
-  Range r;
-};
-
-Array flat(const char* name, const void* p, int64_t count, size_t es) {
-  return {name, p, span(p, 1, count, count, es)};
-}
-
-// Whether pointers are memory of the current device, asking the runtime once for each 2 MiB
-// page: device memory is mapped in pages of that size, which nothing else shares, and a call's
-// small arrays mostly come from one.
-class DeviceMemory {
- public:
-  explicit DeviceMemory(int dev) : dev_(dev) {}
-  bool has(const void* p) {
-    const uintptr_t page = reinterpret_cast<uintptr_t>(p) >> 21;
-    for (int i = 0; i < known_; ++i)
-      if (pages_[i] == page) return true;
-    if (!on_device(p, dev_)) return false;
-    if (known_ < 8) pages_[known_++] = page;
-    return true;
-  }
-
- private:
-  int dev_, known_ = 0;
-  uintptr_t pages_[8];
-};
-
-int check_array(const Array& a, size_t align, DeviceMemory& mem) {
-  if (!a.p || !aligned(a.p, align))
-    return fail(EWG_ERR_UNSUPPORTED, std::string(a.name) + " is null or misaligned");
-  if (!mem.has(a.p))
-    return fail(EWG_ERR_UNSUPPORTED, std::string(a.name) + " is not memory of the current device");
-  return EWG_OK;
-}
-
-int check_apart(const Array& a, const Array& b) {
-  if (a.p && b.p && overlap(a.r, b.r))
-    return fail(EWG_ERR_UNSUPPORTED, std::string(a.name) + " overlaps " + b.name);
-  return EWG_OK;
-}
-
 constexpr size_t kStatusBytes = sizeof(ewg::Header);
 
 int check_status_workspace(void* ws, size_t bytes, DeviceMemory& mem) {

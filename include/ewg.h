@@ -1,8 +1,9 @@
 /*
- * ewg.h -- C ABI of the GB300 sparse embedding weight-gradient library, and of two
+ * ewg.h -- C ABI of the GB300 sparse embedding weight-gradient library, and of the
  * operators that a training step has beside it: token log probabilities with their
- * gradient (ewg_token_logprobs, the vocabulary's other end) and the orthogonalised update of
- * a matrix (ewg_orthogonalize).
+ * gradient (ewg_token_logprobs, the vocabulary's other end), the orthogonalised update of
+ * a matrix (ewg_orthogonalize), layer norm with its gradient (ewg_layer_norm) and the AdamW
+ * step of many tensors at once (ewg_adamw_step).
  *
  * The operation (Megatron Core API docs, core.fusions.fused_embedding_wgrad,
  * entry accumulate_embedding_wgrad, and the module docstring):
@@ -389,6 +390,140 @@ int ewg_orthogonalize_transposed(const void* grad, int grad_dtype, int64_t batch
                                  int64_t grad_row_stride, void* out, int64_t out_batch_stride,
                                  int64_t out_row_stride, int steps, float a, float b, float c,
                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Layer norm of rows.  Per row x[0..hidden), with mean and var of its elements:
+ *
+ *     rstd = 1 / sqrt(var + eps)        out_j = (x_j - mean) rstd weight_j + bias_j
+ *
+ * in 32 bits (the deviations are taken from the mean before they are squared, and the
+ * mean's own rounding is made up for), rounded once.
+ *
+ *   x       [rows][hidden], EWG_BF16 or EWG_FP32, unit inner stride, row_stride elements
+ *           between rows (>= hidden; any alignment of the element)
+ *   weight, bias     [hidden] contiguous, both of weight_dtype (EWG_BF16 or EWG_FP32); NULL
+ *           stands for ones and zeros (weight_dtype is then of no account if both are)
+ *   out     [rows][hidden] of x's dtype, out_row_stride between rows; apart from every input, or
+ *           x itself (same address and stride), which it then replaces
+ *   mean, rstd       [rows] fp32
+ *
+ * A row with a NaN or an infinity gives NaN.  Squared deviations are summed in fp32 and must
+ * stay in its range.  A row of equal elements has rstd 1 / sqrt(eps); with eps = 0 its results
+ * mean nothing.
+ *
+ * Requires 0 <= rows < 2^31 (0: nothing is enqueued), 1 <= hidden <= EWG_MAX_HIDDEN, finite
+ * eps >= 0.  Enqueues one kernel; allocates nothing.
+ */
+int ewg_layer_norm(const void* x, int x_dtype, int64_t rows, int64_t hidden, int64_t row_stride,
+                   const void* weight, const void* bias, int weight_dtype, double eps, void* out,
+                   int64_t out_row_stride, float* mean, float* rstd, void* stream);
+
+/*
+ * Bytes of device workspace of ewg_layer_norm_backward (0 for unsupported sizes).  It needs no
+ * initialisation.
+ */
+size_t ewg_layer_norm_workspace_bytes(int64_t rows, int64_t hidden);
+
+/*
+ * The gradient of ewg_layer_norm.  With n_j = (x_j - mean) rstd and u_j = grad_j weight_j,
+ *
+ *     grad_x_j = rstd (u_j - avg(u) - n_j avg(u n))
+ *     weight_main_grad_j += sum over rows of grad_j n_j
+ *     bias_main_grad_j   += sum over rows of grad_j
+ *
+ * avg over the row.  Everything is computed and summed in 32 bits; grad_x is rounded once, and
+ * a sum over the rows is added to its main_grad element in 32 bits and rounded to the main_grad's
+ * dtype.  The order of the sums depends on rows, hidden and the arrays' alignment alone: the
+ * same call gives the same bits.
+ *
+ *   grad, x    [rows][hidden] of `dtype` (EWG_BF16 or EWG_FP32), unit inner stride, any alignment
+ *   mean, rstd [rows] fp32, as ewg_layer_norm left them
+ *   weight     [hidden] contiguous of weight_dtype, or NULL for ones
+ *   grad_x     [rows][hidden] of `dtype`; apart from every input, or grad or x itself (same
+ *              address and stride), which it then replaces
+ *   weight_main_grad, bias_main_grad   [hidden] contiguous, both of main_grad_dtype (EWG_BF16 or
+ *              EWG_FP32), apart from everything else; NULL: not wanted
+ *   workspace  ewg_layer_norm_workspace_bytes(rows, hidden) device bytes, 256-byte aligned
+ *
+ * Requires sizes as ewg_layer_norm; rows = 0 enqueues nothing and leaves the main_grads as they
+ * are.  Enqueues one to three kernels; allocates nothing.
+ */
+int ewg_layer_norm_backward(const void* grad, int64_t grad_row_stride, const void* x,
+                            int64_t x_row_stride, int dtype, int64_t rows, int64_t hidden,
+                            const float* mean, const float* rstd, const void* weight,
+                            int weight_dtype, void* grad_x, int64_t grad_x_row_stride,
+                            void* weight_main_grad, void* bias_main_grad, int main_grad_dtype,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* Elements of a tensor that share a scale where AdamW's states are held in 8 bits. */
+#define EWG_ADAMW_BLOCK 256
+
+/* One tensor of an AdamW step; every pointer is device memory, contiguous. */
+typedef struct ewg_adamw_tensor {
+  void* param;          /* [count] of param_dtype: updated */
+  const void* grad;     /* [count] of grad_dtype */
+  void* exp_avg;        /* [count], fp32, or 8-bit codes (e4m3): updated */
+  void* exp_avg_sq;     /* [count], fp32, or 8-bit codes of its root (e4m3): updated */
+  float* scales;        /* 8 bits: [ceil(count / EWG_ADAMW_BLOCK)][2], else NULL: updated */
+  void* copy;           /* [count] bf16: receives the new param rounded, or NULL */
+  int64_t count;        /* elements, 0 included */
+  double weight_decay;
+  int param_dtype;      /* EWG_BF16 or EWG_FP32 (a copy: EWG_FP32) */
+  int grad_dtype;       /* EWG_BF16 or EWG_FP32 */
+} ewg_adamw_tensor;
+
+/* Bytes of host memory of a plan for this many tensors (0 for unsupported numbers). */
+size_t ewg_adamw_plan_bytes(int64_t num_tensors);
+
+/*
+ * Checks the tensors of an AdamW step and writes what ewg_adamw_step launches with into `plan`,
+ * host memory of the caller's (8-byte aligned, ewg_adamw_plan_bytes(num_tensors) bytes).
+ * Nothing is enqueued, and the tensors' contents are not read.  The plan holds the tensors'
+ * addresses: it may be used as long as they stay allocated, on the device that was current.
+ * It can be copied, and used by several threads.
+ *
+ * state_bits: 32, or 8.  In 8 bits the two moments of an element are e4m3 codes: its average is
+ * code * scales[element / EWG_ADAMW_BLOCK][0], and the root of its second average code *
+ * scales[element / EWG_ADAMW_BLOCK][1].  States begin as zeros (codes and scales).
+ *
+ * Requires 0 <= num_tensors <= 2^20, counts below 2^40, finite weight_decay >= 0, pointers
+ * aligned to their element (scales to 8 bytes), memory of the current device, and nothing that is
+ * written overlapping anything else (a tensor listed twice among it).
+ */
+int ewg_adamw_plan(const ewg_adamw_tensor* tensors, int64_t num_tensors, int state_bits,
+                   void* plan, size_t plan_bytes);
+
+/*
+ * One AdamW step of a plan's tensors.  Per element, in 32 bits, t the step's number (from 1):
+ *
+ *     g = grad_scale grad       m = beta1 m + (1 - beta1) g       v = beta2 v + (1 - beta2) g^2
+ *     param = (1 - lr weight_decay) param
+ *             - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ *
+ * and param is rounded once (a bf16 param without an fp32 master loses changes below half its
+ * step).  The copy is the new param in bf16.
+ *
+ * States in 8 bits: after the step, which uses m and v unrounded, m and sqrt(v) are taken
+ * relative to their block's scale, its largest magnitude times fl(1 / 448), and rounded to e4m3:
+ * a value at share f of the way from one level to the next goes to the upper one where f + h >= 1,
+ * h = frac(i A + t B) to 20 bits for element i of the tensor, A and B (for the root B and A) the
+ * inverse plastic number's first two powers, 0xC13FA9A9 and 0x91E10DA5 of 2^32.  Over steps and elements h
+ * runs evenly through [0, 1), so that changes smaller than a level's width, of which an
+ * average over a thousand steps consists, add up instead of being rounded away.  A root above 0 is
+ * not rounded to 0.  Blocks whose scale is below 2^-120 are held as zeros.  A gradient that is NaN
+ * or infinite makes its element NaN, and in 8 bits, from the next step on, its block.
+ *
+ *   step, lr, grad_scale     their values; where the pointer beside it is not NULL, it is a device
+ *           scalar (int64, fp32, fp32) that is read in the value's place (a step below 1 as 1),
+ *           so that a captured call follows a schedule
+ *
+ * Requires step >= 1, finite lr >= 0, 0 <= beta1, beta2 < 1, finite eps >= 0, finite grad_scale.
+ * Every element's result depends on its own tensor alone: the same bits in any plan.  Enqueues one
+ * kernel for every 400 tensors; allocates nothing.
+ */
+int ewg_adamw_step(const void* plan, size_t plan_bytes, int64_t step, const int64_t* step_on_device,
+                   double lr, const float* lr_on_device, double beta1, double beta2, double eps,
+                   double grad_scale, const float* grad_scale_on_device, void* stream);
 
 /*
  * Waits for `stream`, then copies the device status of the last ewg_plan /

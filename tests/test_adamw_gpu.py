@@ -1,0 +1,428 @@
+"""adamw_step against its definition: in 64 bits, and for 8-bit states bit by bit.
+
+Tolerances (u = 2^-24): m is off by 6 u of its two terms (beta, grad_scale, products and sum round
+once each), v (both terms positive) by 9 u relatively.  The step rate m / (root factor + eps): rate and factor come from expm1 of
+t log(beta), whose argument is off by 2 u relatively and so 1 - beta^t by at most 3 u and the
+function's own error, 2 u; with the products, the root, the division and grad_scale 24 u in all, and m's error.
+param: 3 u of its two terms, and its rounding.
+
+The codes of 8-bit states follow from the inputs by single operations in 32 bits, each rounded to
+nearest; the same operations in torch give the same bits.
+"""
+import math
+
+import pytest
+import torch
+
+import embedding_weight_grad_gb300 as ewg
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+U = 2.0 ** -24
+BF16, FP32, E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+A, B = 0xC13FA9A9, 0x91E10DA5
+
+
+def make(sizes, p_dtype=FP32, g_dtype=FP32, bits=32, copy=False, seed=0, shift=0):
+    """Tensors of these shapes somewhere in the middle of a training, each `shift` elements into
+    memory of its own, and their states."""
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+
+    def at(t, dtype, guard=0.0):
+        buf = torch.full((t.numel() + shift + 5,), guard, dtype=dtype, device=DEV) if dtype != E4M3 else \
+            torch.zeros(t.numel() + shift + 5, dtype=torch.uint8, device=DEV).view(E4M3)
+        view = buf[shift:shift + t.numel()].view(t.shape)
+        view.copy_(t)
+        return view
+    d = {k: [] for k in ("params", "grads", "copies", "exp_avg", "exp_avg_sq", "scales")}
+    for s in sizes:
+        size = (torch.randn(s, generator=gen, device=DEV) * 1.5).exp() * 1e-3
+        size = size * (torch.rand(s, generator=gen, device=DEV) > 0.1)      # some had no gradient so far
+        d["params"].append(at(torch.randn(s, generator=gen, device=DEV), p_dtype))
+        d["grads"].append(at(torch.randn(s, generator=gen, device=DEV) * size, g_dtype))
+        d["copies"].append(at(torch.zeros(s, device=DEV), BF16) if copy else None)
+        m = torch.randn(s, generator=gen, device=DEV) * size * 0.3
+        if bits == 32:
+            d["exp_avg"].append(at(m, FP32))
+            d["exp_avg_sq"].append(at(size.square(), FP32))
+        else:
+            blocks = -(-size.numel() // 256)
+            codes, scale = [], []
+            for x in (m, size):
+                whole = torch.zeros(blocks * 256, device=DEV)
+                whole[:x.numel()] = x.flatten()
+                s1 = whole.view(blocks, 256).abs().amax(1) / 448
+                codes.append((whole.view(blocks, 256) / s1.clamp_min(1e-30)[:, None]).clamp(-448, 448).flatten()[:x.numel()].view(s).to(E4M3))
+                scale.append(s1)
+            d["exp_avg"].append(at(codes[0], E4M3))
+            d["exp_avg_sq"].append(at(codes[1], E4M3))
+            d["scales"].append(torch.stack(scale, 1))
+    return d
+
+
+def plan_of(d, bits, decay):
+    return ewg.adamw_plan(d["params"], d["grads"], state_bits=bits, copies=d["copies"], weight_decay=decay,
+                          exp_avg=d["exp_avg"], exp_avg_sq=d["exp_avg_sq"], scales=d["scales"] if bits == 8 else None)
+
+
+def values8(codes, scales, column):
+    n = codes.numel()
+    return codes.float().flatten() * scales[:, column].repeat_interleave(256)[:n]
+
+
+def round8(x, t, a, b, positive):
+    """e4m3 codes and scales of x, by the definition's own operations in 32 bits."""
+    n, blocks = x.numel(), -(-x.numel() // 256)
+    whole = torch.zeros(blocks * 256, device=x.device)
+    whole[:n] = x
+    whole = whole.view(blocks, 256)
+    scale = whole.abs().amax(1) * (1 / 448)
+    held = ~(scale < 2.0 ** -120)
+    inverse = torch.where(held, 1 / scale, 0.0)
+    bits = (whole * inverse[:, None] * 2.0 ** -120).view(torch.int32).to(torch.int64) & 0xffffffff
+    i = torch.arange(blocks * 256, device=x.device).view(blocks, 256)
+    h = ((i * a + t * b) & 0xffffffff) >> 12
+    code = (((bits & 0x7fffffff) + h) >> 20).clamp(max=126)
+    if positive:
+        code = torch.where((code == 0) & (whole > 0) & held[:, None], 1, code)
+    code = code | (bits >> 31 << 7)
+    return code.to(torch.uint8).flatten()[:n], torch.where(held, scale, 0.0)
+
+
+class Reference:
+    """The step's outputs for one tensor: m, v, param in 64 bits with their tolerances; codes."""
+
+    def __init__(self, d, k, bits, t, lr, betas, eps, decay, scale):
+        b1, b2 = betas
+        p, g = d["params"][k].double().flatten(), d["grads"][k].double().flatten() * scale
+        if bits == 32:
+            m, v = d["exp_avg"][k].double().flatten(), d["exp_avg_sq"][k].double().flatten()
+        else:
+            m32 = values8(d["exp_avg"][k], d["scales"][k], 0)
+            v32 = values8(d["exp_avg_sq"][k], d["scales"][k], 1).square()
+            m, v = m32.double(), v32.double()
+            g32 = d["grads"][k].float().flatten() * torch.tensor(scale, device=DEV)
+            m32 = m32 * b1 + g32 * (1 - b1)
+            r32 = (v32 * b2 + g32 * g32 * (1 - b2)).sqrt()
+            self.code_m, scale_m = round8(m32, t, A, B, False)
+            self.code_r, scale_r = round8(r32, t, B, A, True)
+            self.scales = torch.stack([scale_m, scale_r], 1)
+        self.m, self.v = b1 * m + (1 - b1) * g, b2 * v + (1 - b2) * g * g
+        self.m_tol = 6 * U * ((b1 * m).abs() + ((1 - b1) * g).abs()) + 1e-44
+        self.v_tol = 9 * U * self.v + 1e-44
+        rate = lr / (1 - b1 ** t)
+        under = (self.v / (1 - b2 ** t)).sqrt() + eps
+        step = rate * self.m / under
+        self.p = p * (1 - lr * decay) - step
+        self.p_tol = 24 * U * step.abs() + rate * self.m_tol / under + 3 * U * (p.abs() + step.abs()) + 1e-44
+
+    def check(self, d, k, bits, before_copy=True):
+        p = d["params"][k].double().flatten()
+        tol = self.p_tol + (2.0 ** -8 * (self.p.abs() + self.p_tol) if d["params"][k].dtype == BF16 else 0)
+        near(p, self.p, tol, "param")
+        if d["copies"][k] is not None:
+            assert torch.equal(d["copies"][k], d["params"][k].bfloat16())
+        if bits == 32:
+            near(d["exp_avg"][k].double().flatten(), self.m, self.m_tol, "exp_avg")
+            near(d["exp_avg_sq"][k].double().flatten(), self.v, self.v_tol, "exp_avg_sq")
+        else:
+            assert torch.equal(d["exp_avg"][k].view(torch.uint8).flatten(), self.code_m)
+            assert torch.equal(d["exp_avg_sq"][k].view(torch.uint8).flatten(), self.code_r)
+            assert torch.equal(d["scales"][k], self.scales)
+
+
+def near(got, want, tol, what):
+    worst = ((got - want).abs() - tol).max().item() if got.numel() else 0.0
+    assert worst <= 0, (what, worst)
+
+
+def steps(d, bits, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, decay=0.1, scale=1.0, first=1, count=3):
+    """`count` steps, each checked from the state before it."""
+    plan = plan_of(d, bits, decay)
+    decays = decay if isinstance(decay, list) else [decay] * len(d["params"])
+    for t in range(first, first + count):
+        refs = [Reference(d, k, bits, t, lr, betas, eps, decays[k], scale) for k in range(len(d["params"]))]
+        ewg.adamw_step(plan, t, lr=lr, betas=betas, eps=eps, grad_scale=scale)
+        for k, r in enumerate(refs):
+            r.check(d, k, bits)
+    return plan
+
+
+SIZES = [[1], [2, 31, 32, 33], [255, 256, 257], [(3, 5), (7, 11, 13), 1], [2047, 2048, 2049, 1], [100000], [(1001, 1003)],
+         [5, (300, 257), 8, 1024, (64, 64), 1, 1, 9999]]
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("shift", [0, 1, 3, 4, 8])
+@pytest.mark.parametrize("sizes", SIZES)
+def test_sizes(sizes, shift, bits):
+    steps(make(sizes, bits=bits, seed=shift, shift=shift, copy=shift != 1), bits)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("p_dtype", [BF16, FP32])
+@pytest.mark.parametrize("g_dtype", [BF16, FP32])
+@pytest.mark.parametrize("shift", [0, 1, 8])
+def test_types(p_dtype, g_dtype, shift, bits):
+    steps(make([1000, (40, 512), 7], p_dtype, g_dtype, bits, copy=p_dtype == FP32, shift=shift), bits, scale=0.25)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_mixed_types_in_one_plan(bits):
+    parts = [make([300, 4096], p, g, bits, seed=k) for k, (p, g) in enumerate([(FP32, FP32), (BF16, BF16), (FP32, BF16), (BF16, FP32)])]
+    d = {key: sum((p[key] for p in parts), []) for key in parts[0]}
+    steps(d, bits, decay=[0.0, 0.1, 0.2, 0.0, 0.3, 0.0, 0.01, 1.0])
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("betas,eps,lr,scale,first", [((0.9, 0.999), 1e-8, 1e-3, 1.0, 1), ((0.9, 0.95), 1e-15, 3e-4, 0.1, 1000),
+                                                      ((0.0, 0.0), 1e-6, 0.1, 2.0, 7), ((0.99, 0.99999), 0.0, 1e-2, -1.0, 3000000),
+                                                      ((0.5, 0.9), 1e-3, 0.0, 1.0, 2)])
+def test_hyperparameters(betas, eps, lr, scale, first, bits):
+    d = make([5000, (33, 100)], bits=bits)
+    if eps == 0.0:                       # with eps 0 an element without a gradient would be 0 / 0
+        d["grads"] = [g + 1e-3 for g in d["grads"]]
+    steps(d, bits, lr=lr, betas=betas, eps=eps, scale=scale, first=first)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("num", [399, 400, 401, 1203])
+def test_many_tensors(num, bits):
+    """More than a launch takes."""
+    steps(make([(k * 37) % 700 for k in range(num)], bits=bits), bits, count=2)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_the_same_bits_in_any_plan_and_at_any_address(bits):
+    a, b = make([70000, 12, 3000], bits=bits), make([70000, 12, 3000], bits=bits, shift=3)
+    plan = plan_of(a, bits, 0.1)
+    alone = [ewg.adamw_plan(*[[b[key][k]] for key in ("params", "grads")], state_bits=bits, weight_decay=0.1,
+                            exp_avg=[b["exp_avg"][k]], exp_avg_sq=[b["exp_avg_sq"][k]],
+                            scales=[b["scales"][k]] if bits == 8 else None) for k in (2, 0, 1)]
+    for t in (1, 2, 3):
+        ewg.adamw_step(plan, t, lr=1e-3)
+        for p in alone:
+            ewg.adamw_step(p, t, lr=1e-3)
+    for key in ("params", "exp_avg", "exp_avg_sq", "scales"):
+        for x, y in zip(a[key], b[key]):
+            assert torch.equal(x.contiguous().view(torch.uint8), y.contiguous().view(torch.uint8)), key
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_states_start_as_zeros(bits):
+    d = make([3000, (20, 50)], bits=bits)
+    plan = ewg.adamw_plan(d["params"], d["grads"], state_bits=bits, weight_decay=0.0)
+    for key in ("exp_avg", "exp_avg_sq", "scales"):
+        d[key] = getattr(plan, key) or []
+    assert d["exp_avg"][1].shape == (20, 50) and all(bool((x.float() == 0).all()) for x in d["exp_avg"] + d["exp_avg_sq"])
+    for t in (1, 2):
+        refs = [Reference(d, k, bits, t, 1e-2, (0.9, 0.999), 1e-8, 0.0, 1.0) for k in range(2)]
+        ewg.adamw_step(plan, t, lr=1e-2)
+        for k, r in enumerate(refs):
+            r.check(d, k, bits)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_no_gradient_so_far(bits):
+    """Elements without a gradient stay but for the decay, whatever else their block has."""
+    d = make([2000], bits=bits)
+    for key in ("grads", "exp_avg", "exp_avg_sq"):
+        d[key][0].view(torch.uint8 if d[key][0].dtype == E4M3 else d[key][0].dtype)[100:300] = 0
+    p = d["params"][0].clone()
+    ewg.adamw_step(plan_of(d, bits, 0.0), 5, lr=1e-2)
+    assert torch.equal(d["params"][0][100:300], p[100:300])
+    assert not bool((d["params"][0] == p)[:100].all())
+    ewg.adamw_step(plan_of(d, bits, 0.1), 6, lr=1e-2)
+    torch.testing.assert_close(d["params"][0][100:300], p[100:300] * (1 - 1e-3), rtol=4 * U, atol=0)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_a_gradient_that_is_not_finite(bad, bits):
+    """Its element becomes NaN; in 8 bits its block's state too, and no other block's."""
+    d = make([1000], bits=bits)
+    d["grads"][0][300] = bad
+    plan = plan_of(d, bits, 0.0)
+    ewg.adamw_step(plan, 9, lr=1e-3)
+    p = d["params"][0]
+    assert bool(p[300].isnan()) and int(p.isnan().sum()) == 1
+    d["grads"][0][300] = 0.0
+    ewg.adamw_step(plan, 10, lr=1e-3)
+    broken = torch.arange(1000, device=DEV) == 300
+    if bits == 8:
+        broken = torch.arange(1000, device=DEV) // 256 == 1
+        assert not bool(d["scales"][0][1].isfinite().all()) and bool(d["scales"][0][[0, 2, 3]].isfinite().all())
+    assert torch.equal(p.isnan(), broken)
+
+
+@pytest.mark.parametrize("size", [1e-41, 1e-37, 1e-30, 1e-19, 1e15])
+def test_8_bits_of_small_and_large_gradients(size):
+    """Scales from below where a block is held as zeros up to squares near the largest number."""
+    d = make([1500], bits=8)
+    for key in ("grads", "scales"):
+        d[key][0].mul_(size * 1e3)
+    refs = Reference(d, 0, 8, 3, 1e-3, (0.9, 0.999), 1e-8, 0.1, 1.0)
+    ewg.adamw_step(plan_of(d, 8, 0.1), 3, lr=1e-3)
+    assert torch.equal(d["exp_avg"][0].view(torch.uint8), refs.code_m)
+    assert torch.equal(d["exp_avg_sq"][0].view(torch.uint8), refs.code_r)
+    assert torch.equal(d["scales"][0], refs.scales)
+    assert bool(d["params"][0].isfinite().all())
+
+
+def test_8_bits_add_up_over_steps():
+    """With beta 0 the averages are the gradients: over T steps the held values' mean is the
+    gradient but for the additive sequence's unevenness. Of T = 610 steps the share that rounds up
+    differs from the share asked for by less than 8 / T (the constants' powers keep T times it
+    within a few)."""
+    T = 610
+    g = torch.linspace(-1, 1, 512, device=DEV)
+    p = torch.zeros(512, device=DEV)
+    plan = ewg.adamw_plan([p], [g], state_bits=8, weight_decay=0.0)
+    total_m, total_r = torch.zeros(512, dtype=torch.float64, device=DEV), torch.zeros(512, dtype=torch.float64, device=DEV)
+    for t in range(1, T + 1):
+        ewg.adamw_step(plan, t, lr=0.0, betas=(0.0, 0.0))
+        total_m += values8(plan.exp_avg[0], plan.scales[0], 0).double()
+        total_r += values8(plan.exp_avg_sq[0], plan.scales[0], 1).double()
+    for total, want in ((total_m, g.double()), (total_r, g.double().abs())):
+        level = torch.ldexp(torch.ones_like(want), (torch.frexp(want.abs() * 448).exponent - 4).clamp(min=-9)) / 448
+        near(total / T, want, level * 8 / T + 4 * U, "mean")
+
+
+def test_small_roots_are_not_rounded_to_0():
+    g = torch.full((256,), 1e-9, device=DEV)
+    g[0] = 1.0
+    p = torch.zeros(256, device=DEV)
+    plan = ewg.adamw_plan([p], [g], state_bits=8, weight_decay=0.0)
+    for t in range(1, 40):
+        ewg.adamw_step(plan, t, lr=1e-3, eps=0.0)
+        assert bool((plan.exp_avg_sq[0].float() > 0).all()) and bool(p.isfinite().all())
+    assert p.abs().max().item() < 40 * 2e-3
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_device_scalars_and_capture(bits):
+    """step, lr and grad_scale on the device: the same bits as given by value; a captured step follows
+    their values."""
+    a, b = make([3000, 40], bits=bits), make([3000, 40], bits=bits)
+    pa, pb = plan_of(a, bits, 0.1), plan_of(b, bits, 0.1)
+    step, lr, scale = torch.zeros((), dtype=torch.int64, device=DEV), torch.zeros(1, device=DEV), torch.zeros((), device=DEV)
+    warm = make([10], bits=bits)
+    ewg.adamw_step(plan_of(warm, bits, 0.0), 1, lr=1e-3)     # the first launch belongs outside a capture
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step.add_(1)
+        ewg.adamw_step(pb, step, lr=lr, grad_scale=scale)
+    for t in (1, 2, 3):
+        lr.fill_(1e-3 * t)
+        scale.fill_(1.0 / t)
+        graph.replay()
+        ewg.adamw_step(pa, t, lr=lr.item(), grad_scale=scale.item())
+    for key in ("params", "exp_avg", "exp_avg_sq", "scales"):
+        for x, y in zip(a[key], b[key]):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8)), key
+    step.fill_(-5)                                   # below the first: taken as the first
+    c, e = make([100], bits=bits), make([100], bits=bits)
+    ewg.adamw_step(plan_of(c, bits, 0.0), step, lr=1e-3)
+    ewg.adamw_step(plan_of(e, bits, 0.0), 1, lr=1e-3)
+    assert torch.equal(c["params"][0], e["params"][0])
+
+
+def test_streams():
+    """Two plans' steps at once, on streams of their own."""
+    ds = [make([500000], seed=k) for k in range(2)]
+    refs = [Reference(d, 0, 32, 1, 1e-3, (0.9, 0.999), 1e-8, 0.1, 1.0) for d in ds]
+    plans = [plan_of(d, 32, 0.1) for d in ds]
+    torch.cuda.synchronize()
+    for p in plans:
+        with torch.cuda.stream(torch.cuda.Stream()):
+            ewg.adamw_step(p, 1, lr=1e-3)
+    torch.cuda.synchronize()
+    for d, r in zip(ds, refs):
+        r.check(d, 0, 32)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_more_than_2_31_elements(bits):
+    """The last elements of a tensor of more than 2^31: their thresholds go by the index's low 32 bits."""
+    n = 2 ** 31 + 1000
+    p, g = torch.zeros(n, dtype=BF16, device=DEV), torch.zeros(n, dtype=BF16, device=DEV)
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    g[-2000:] = torch.randn(2000, generator=gen, device=DEV)
+    plan = ewg.adamw_plan([p], [g], state_bits=bits, weight_decay=0.0)
+    ewg.adamw_step(plan, 1, lr=1e-2)
+    g64 = g[-2000:].double()
+    want = -1e-2 * g64 / (g64.abs() + 1e-8)
+    near(p[-2000:].double(), want, want.abs() * (2.0 ** -8 + 64 * U), "param")
+    assert int(p[:-2000].count_nonzero()) == 0
+    if bits == 8:
+        first = (n - 2000) // 256 * 256
+        m32 = g[first:].float() * (1 - 0.9)
+        i = torch.arange(first, n, device=DEV)
+        whole = torch.zeros(-(-m32.numel() // 256) * 256, device=DEV)
+        whole[:m32.numel()] = m32
+        scale = whole.view(-1, 256).abs().amax(1) * (1 / 448)
+        each = torch.where(scale > 0, 1 / scale, 0.0).repeat_interleave(256)[:m32.numel()]
+        b = (m32 * each * 2.0 ** -120).view(torch.int32).to(torch.int64) & 0xffffffff
+        code = (((b & 0x7fffffff) + (((i * A + B) & 0xffffffff) >> 12)) >> 20).clamp(max=126) | (b >> 31 << 7)
+        assert torch.equal(plan.exp_avg[0][first:].view(torch.uint8), code.to(torch.uint8))
+
+
+def test_autograd_is_told_and_moved_tensors_are_refused():
+    d = make([100, 200], copy=True)
+    d["params"] = [p.requires_grad_() for p in d["params"]]
+    plan = plan_of(d, 32, 0.0)
+    versions = [t._version for t in plan.params + plan.copies + plan.exp_avg]
+    ewg.adamw_step(plan, 1, lr=1e-3)
+    assert [t._version for t in plan.params + plan.copies + plan.exp_avg] == [v + 1 for v in versions]
+    assert plan.grads[0]._version == d["grads"][0]._version
+    plan.params[0].data = torch.zeros(100, device=DEV)
+    with pytest.raises(ValueError, match="moved"):
+        ewg.adamw_step(plan, 2, lr=1e-3)
+
+
+def test_empty_plans_and_tensors():
+    ewg.adamw_step(ewg.adamw_plan([], []), 1, lr=1e-3)
+    for bits in (32, 8):
+        d = make([0, 5, 0], bits=bits)
+        steps(d, bits)
+        e = [torch.empty(0, device=DEV)]
+        ewg.adamw_step(ewg.adamw_plan(e, [torch.empty(0, device=DEV)], state_bits=bits), 1, lr=1e-3)
+
+
+def test_refusals():
+    p, g = torch.zeros(100, device=DEV), torch.zeros(100, device=DEV)
+    q = torch.zeros(100, dtype=BF16, device=DEV)
+    both = torch.zeros(150, device=DEV)
+    for call in (lambda: ewg.adamw_plan([p], [g], state_bits=16), lambda: ewg.adamw_plan([p], []),
+                 lambda: ewg.adamw_plan([p.double()], [g]), lambda: ewg.adamw_plan([p], [g.half()]),
+                 lambda: ewg.adamw_plan([p], [g[:50]]), lambda: ewg.adamw_plan([p], [g], copies=[g.clone()]),
+                 lambda: ewg.adamw_plan([q], [g], copies=[q.clone()]), lambda: ewg.adamw_plan([p], [g], weight_decay=[0.1, 0.2]),
+                 lambda: ewg.adamw_plan([p.cpu()], [g.cpu()]), lambda: ewg.adamw_plan([p], [g.cpu()]),
+                 lambda: ewg.adamw_plan([torch.zeros(10, 10, device=DEV).t()], [g.view(10, 10)]),
+                 lambda: ewg.adamw_plan([p], [g], exp_avg=[p.bfloat16()]), lambda: ewg.adamw_plan([p], [g], exp_avg=[]),
+                 lambda: ewg.adamw_plan([p], [g], scales=[torch.zeros(1, 2, device=DEV)]),
+                 lambda: ewg.adamw_plan([p], [g], state_bits=8, scales=[torch.zeros(2, 2, device=DEV)])):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: ewg.adamw_plan([p, p], [g, g]), lambda: ewg.adamw_plan([p], [p]),
+                 lambda: ewg.adamw_plan([both[:100], both[50:]], [g, g]), lambda: ewg.adamw_plan([p], [g], exp_avg=[g]),
+                 lambda: ewg.adamw_plan([p], [g], exp_avg=[both[:100]], exp_avg_sq=[both[50:]]),
+                 lambda: ewg.adamw_plan([p], [g], weight_decay=-0.1), lambda: ewg.adamw_plan([p], [g], weight_decay=float("nan"))):
+        with pytest.raises(ewg.EwgError):
+            call()
+    shared = ewg.adamw_plan([p, both[:100]], [g, g])        # gradients may be shared: they are only read
+    before = p.clone()
+    for k in (dict(step=0), dict(lr=-1.0), dict(lr=float("inf")), dict(betas=(1.0, 0.9)), dict(betas=(0.9, -0.1)),
+              dict(eps=-1.0), dict(eps=float("nan")), dict(grad_scale=float("nan"))):
+        with pytest.raises(ewg.EwgError):
+            ewg.adamw_step(shared, **{"step": 1, "lr": 1e-3, **k})
+    for k in (dict(step=torch.ones((), device=DEV)), dict(lr=torch.ones(2, device=DEV)), dict(lr=torch.ones(())),
+              dict(grad_scale=torch.ones((), dtype=BF16, device=DEV))):
+        with pytest.raises(ValueError):
+            ewg.adamw_step(shared, **{"step": 1, "lr": 1e-3, **k})
+    assert torch.equal(p, before)
+    with torch.inference_mode():
+        i = torch.zeros(10, device=DEV)
+    with pytest.raises(ValueError, match="inference"):
+        ewg.adamw_plan([i], [torch.zeros(10, device=DEV)])
