@@ -7,8 +7,11 @@
 // and with n = (x - mean) rstd, u = g w:
 //
 //     dx = rstd (u - avg(u) - n avg(u n))     dw_j = sum over rows of g n     db_j = sum over rows of g
+#include <atomic>
+
 #include <cuda_bf16.h>
 
+#include "ewg_ptx.cuh"
 #include "ewg_train.cuh"
 
 namespace ewg {
@@ -16,10 +19,490 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 
+using ptx::add2;
+using ptx::fma2;
+using ptx::mul2;
+using ptx::sub2;
+
 __device__ __forceinline__ float load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 __device__ __forceinline__ float load(const float* p) { return *p; }
 __device__ __forceinline__ void store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void store(float* p, float v) { *p = v; }
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 from_bf16x2(uint32_t u) {
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t to_bf16x2(float2 f) {
+  uint32_t u;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(f.y), "f"(f.x));
+  return u;
+}
+
+// kE neighbouring elements of a row, which one access moves: 16 bytes where rows allow it, else 4,
+// or a single element.  Arithmetic goes by pairs, two 32-bit operations an instruction.
+template <typename T, int kE>
+struct Access;
+
+template <>
+struct Access<__nv_bfloat16, 8> {
+  using Raw = uint4;
+  static __device__ __forceinline__ void unpack(Raw v, float2* f) {
+    f[0] = from_bf16x2(v.x), f[1] = from_bf16x2(v.y), f[2] = from_bf16x2(v.z), f[3] = from_bf16x2(v.w);
+  }
+  static __device__ __forceinline__ Raw pack(const float2* f) {
+    return make_uint4(to_bf16x2(f[0]), to_bf16x2(f[1]), to_bf16x2(f[2]), to_bf16x2(f[3]));
+  }
+};
+template <>
+struct Access<__nv_bfloat16, 2> {
+  using Raw = uint32_t;
+  static __device__ __forceinline__ void unpack(Raw v, float2* f) { f[0] = from_bf16x2(v); }
+  static __device__ __forceinline__ Raw pack(const float2* f) { return to_bf16x2(f[0]); }
+};
+template <>
+struct Access<float, 4> {
+  using Raw = float4;
+  static __device__ __forceinline__ void unpack(Raw v, float2* f) {
+    f[0] = make_float2(v.x, v.y), f[1] = make_float2(v.z, v.w);
+  }
+  static __device__ __forceinline__ Raw pack(const float2* f) { return make_float4(f[0].x, f[0].y, f[1].x, f[1].y); }
+};
+
+// kE elements of a weight or bias vector of W, as pairs; for one element, in x.
+template <typename W, int kE>
+__device__ __forceinline__ void vector_part(const W* p, float2* f) {
+  if constexpr (kE == 1) {
+    if constexpr (sizeof(W) == 2) f->x = __uint_as_float(static_cast<uint32_t>(__ldg(reinterpret_cast<const unsigned short*>(p))) << 16);
+    else f->x = __ldg(p);
+  } else if constexpr (sizeof(W) == 2) {
+    uint32_t u[kE / 2];
+    if constexpr (kE == 8) *reinterpret_cast<uint4*>(u) = __ldg(reinterpret_cast<const uint4*>(p));
+    else if constexpr (kE == 4) *reinterpret_cast<uint2*>(u) = __ldg(reinterpret_cast<const uint2*>(p));
+    else u[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+#pragma unroll
+    for (int i = 0; i < kE / 2; ++i) f[i] = from_bf16x2(u[i]);
+  } else if constexpr (kE == 8) {
+    asm("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=f"(f[0].x), "=f"(f[0].y), "=f"(f[1].x), "=f"(f[1].y), "=f"(f[2].x), "=f"(f[2].y), "=f"(f[3].x), "=f"(f[3].y)
+        : "l"(p));
+  } else if constexpr (kE == 4) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(p));
+    f[0] = make_float2(v.x, v.y);
+    f[1] = make_float2(v.z, v.w);
+  } else {
+    f[0] = __ldg(reinterpret_cast<const float2*>(p));
+  }
+}
+
+// Of 2 kPairs elements that a thread has of a row, in accesses of kE: the pairs' values from where
+// access k lies at `at + k plane`, and back to where it goes to `to + k pitch`.
+template <typename T, int kE, int kPairs>
+__device__ __forceinline__ void read_pairs(const char* at, int plane, float2 (&f)[kPairs]) {
+#pragma unroll
+  for (int k = 0; k < 2 * kPairs / kE; ++k) {
+    if constexpr (kE == 1) {
+      const float v = load(reinterpret_cast<const T*>(at + k * plane));
+      if (k % 2) f[k / 2].y = v;
+      else f[k / 2].x = v;
+    } else {
+      using A = Access<T, kE>;
+      A::unpack(*reinterpret_cast<const typename A::Raw*>(at + k * plane), f + k * kE / 2);
+    }
+  }
+}
+
+template <typename T, int kE, int kPairs>
+__device__ __forceinline__ void write_pairs(T* to, int pitch, int count, const float2 (&f)[kPairs]) {
+#pragma unroll
+  for (int k = 0; k < 2 * kPairs / kE; ++k) {
+    if (k >= count) continue;
+    if constexpr (kE == 1) {
+      store(to + k * pitch, k % 2 ? f[k / 2].y : f[k / 2].x);
+    } else {
+      using A = Access<T, kE>;
+      *reinterpret_cast<typename A::Raw*>(to + k * pitch) = A::pack(f + k * kE / 2);
+    }
+  }
+}
+
+// The same of a vector of W from the thread's first column on.
+template <typename W, int kE, int kPairs>
+__device__ __forceinline__ void read_vector(const W* p, int pitch, int count, float2 (&f)[kPairs]) {
+#pragma unroll
+  for (int k = 0; k < 2 * kPairs / kE; ++k) {
+    if (k >= count) continue;
+    if constexpr (kE == 1) {
+      float2 v;
+      vector_part<W, 1>(p + k * pitch, &v);
+      if (k % 2) f[k / 2].y = v.x;
+      else f[k / 2].x = v.x;
+    } else {
+      vector_part<W, kE>(p + k * pitch, f + k * kE / 2);
+    }
+  }
+}
+// Where there is no vector, its elements are `none`.
+template <int kE, int kPairs>
+__device__ __forceinline__ void read_vector(const void* p, int bf16, int column, int pitch, int count, float none,
+                                            float2 (&f)[kPairs]) {
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) f[i] = both(none);
+  if (!p) return;
+  if (bf16) read_vector<__nv_bfloat16, kE, kPairs>(static_cast<const __nv_bfloat16*>(p) + column, pitch, count, f);
+  else read_vector<float, kE, kPairs>(static_cast<const float*>(p) + column, pitch, count, f);
+}
+
+// Sum of pairs, by halves.
+template <int kN>
+__device__ __forceinline__ float pairs_sum(const float2* f) {
+  float2 s[kN];
+#pragma unroll
+  for (int i = 0; i < kN; ++i) s[i] = f[i];
+#pragma unroll
+  for (int n = kN / 2; n; n /= 2)
+#pragma unroll
+    for (int i = 0; i < n; ++i) s[i] = add2(s[i], s[i + n]);
+  return s[0].x + s[0].y;
+}
+
+// Sums of kM numbers over a warp at once: the first steps leave half of the numbers to each half of the
+// lanes; in the end kM groups of neighbouring lanes have one number's sum each.
+template <int kM>
+__device__ __forceinline__ float warp_fold(float (&v)[kM]) {
+#pragma unroll
+  for (int m = kM / 2, d = 16; m; m /= 2, d /= 2) {
+    const bool upper = threadIdx.x & d;
+#pragma unroll
+    for (int i = 0; i < m; ++i) {
+      const float keep = upper ? v[m + i] : v[i], send = upper ? v[i] : v[m + i];
+      v[i] = keep + __shfl_xor_sync(kAll, send, d);
+    }
+  }
+#pragma unroll
+  for (int d = 16 / kM; d; d /= 2) v[0] += __shfl_xor_sync(kAll, v[0], d);
+  return v[0];
+}
+
+// Sums of kM numbers over a team, in each of its threads.  kTeam: its threads, or 0 where they are
+// several warps (`threads` of them), which meet in `slots` [kM][32], zeros where there is no warp.
+template <int kM, int kTeam>
+__device__ __forceinline__ void team_sum(float (&v)[kM], float* slots, int team, int threads) {
+  const int lane = threadIdx.x % 32;
+  if constexpr (kTeam && kTeam < 32) {
+#pragma unroll
+    for (int i = 0; i < kM; ++i)
+#pragma unroll
+      for (int d = kTeam / 2; d; d /= 2) v[i] += __shfl_xor_sync(kAll, v[i], d);
+  } else {
+    constexpr int kGroup = 32 / kM;
+    float s = warp_fold<kM>(v);
+    if constexpr (kTeam == 0) {
+      if (lane % kGroup == 0) slots[lane / kGroup * 32 + threadIdx.x % threads / 32] = s;
+      asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(threads) : "memory");
+      const float* mine = slots + lane / kGroup * 32 + lane % kGroup * kM;
+      s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kM; ++i) s += mine[i];
+#pragma unroll
+      for (int d = kGroup / 2; d; d /= 2) s += __shfl_xor_sync(kAll, s, d);
+    }
+#pragma unroll
+    for (int i = 0; i < kM; ++i) v[i] = __shfl_sync(kAll, s, i * kGroup);
+  }
+}
+
+// ---- rows of up to 8192 elements, copied ahead into shared memory
+
+constexpr int kStreamThreads = 512;                        // of a block, at most; it is the only one of its SM
+constexpr int kStreamHidden = 8192;
+
+// Of an array of rows: its first element, and the bytes from a row to the next one and from a team's batch
+// to its next one.
+struct Rows {
+  const char* p;
+  long long pitch, advance;
+};
+
+// What the two kernels below have in common.  A team of threads takes kR neighbouring rows at a
+// time, and of the batches after that one kStages - 1 are on their way: every thread copies what it will read
+// itself (kArrays arrays' rows), so that the copies need no barrier.  Where an element is too
+// small for an asynchronous copy (odd rows of bf16), kStages is 1 and a batch is read when its turn comes.
+template <typename T, int kE, int kColumns, int kR, int kArrays, int kStages, int kTeam>
+struct Stream {
+  static constexpr int kPairs = kColumns / 2;
+  static constexpr int kK = kColumns / kE, kBytes = kE * static_cast<int>(sizeof(T));
+  int threads, teams, team, thread;
+  int count;                         // of the thread's kK accesses to a row those that lie in it
+  uint32_t n, row, step;             // rows; the first row of the team's next batch to be copied; rows of all teams' batches
+  const char* from[kArrays];         // of `row`, the thread's first access
+  char* ring;
+  int stage = 0;
+
+  __device__ __forceinline__ Stream(int team_threads, int rows, int H, char* shared) {
+    n = rows;
+    threads = kTeam ? kTeam : team_threads;
+    teams = blockDim.x / threads;
+    team = threadIdx.x / threads;
+    thread = threadIdx.x % threads;
+    const int left = H / kE - thread;        // (H is a multiple of kE)
+    count = left > 0 ? (left + threads - 1) / threads : 0;
+    ring = shared + threadIdx.x * kBytes;
+    step = gridDim.x * teams * kR;
+    row = (blockIdx.x * teams + team) * kR;
+  }
+  __device__ __forceinline__ int column(int k) const { return (k * threads + thread) * kE; }
+  __device__ __forceinline__ int pitch() const { return threads * kE; }
+  // The first row of the first team of the thread's warp: teams that share a warp go on together.
+  __device__ __forceinline__ uint32_t first() const {
+    return row - (kTeam ? team % (32 / (kTeam ? kTeam : 32)) : 0) * kR;
+  }
+  __device__ __forceinline__ void source(int array, const Rows& rows) {
+    from[array] = rows.p + row * rows.pitch + thread * kBytes;
+  }
+  __device__ __forceinline__ char* place(int st, int r, int array) const {
+    return ring + ((st * kR + r) * kArrays + array) * kK * static_cast<int>(blockDim.x) * kBytes;
+  }
+  // Begins the copy of the next batch; what is not there becomes zeros.
+  __device__ __forceinline__ void copy(int st, const Rows (&rows)[kArrays]) {
+#pragma unroll
+    for (int array = 0; array < kArrays; ++array) {
+#pragma unroll
+      for (int r = 0; r < kR; ++r) {
+        const char* p = from[array] + r * rows[array].pitch;
+        char* to = place(st, r, array);
+#pragma unroll
+        for (int k = 0; k < kK; ++k) {
+          const bool there = k < count && row + r < n;
+          const char* src = there ? p + k * threads * kBytes : rows[array].p;     // (nothing is read of the latter)
+          char* at = to + k * static_cast<int>(blockDim.x) * kBytes;
+          const int bytes = there ? kBytes : 0;
+          if constexpr (kBytes == 16)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ptx::smem_u32(at)), "l"(src), "r"(bytes) : "memory");
+          else if constexpr (kBytes == 4)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(ptx::smem_u32(at)), "l"(src), "r"(bytes) : "memory");
+          else
+            *reinterpret_cast<T*>(at) = there ? *reinterpret_cast<const T*>(src) : T(0.0f);
+        }
+      }
+      from[array] += rows[array].advance;
+    }
+    row += step;
+    if constexpr (kBytes > 2) ptx::cp_async_commit();
+  }
+  // Begins the copies of the first batches.
+  __device__ __forceinline__ void start(const Rows (&rows)[kArrays]) {
+#pragma unroll
+    for (int st = 0; st < kStages - 1; ++st) copy(st, rows);
+  }
+  // Begins one more copy, waits for the oldest and returns its stage.
+  __device__ __forceinline__ int next(const Rows (&rows)[kArrays]) {
+    const int now = stage;
+    copy(now == 0 ? kStages - 1 : now - 1, rows);
+    if constexpr (kBytes > 2) ptx::cp_async_wait<kStages - 1>();
+    stage = now == kStages - 1 ? 0 : now + 1;
+    return now;
+  }
+  __device__ __forceinline__ void read(int st, int r, int array, float2 (&f)[kPairs]) const {
+    read_pairs<T, kE, kPairs>(place(st, r, array), blockDim.x * kBytes, f);
+  }
+};
+
+struct NormStream {
+  Rows x[1];
+  Rows out;
+  const void* weight;
+  const void* bias;
+  float* mean;
+  float* rstd;
+  int weight_bf16, n, H, team_threads;
+  float eps, inv_h;
+};
+
+template <typename T, int kE, int kColumns, int kR, int kStages, int kTeam>
+__global__ void __launch_bounds__(kStreamThreads) norm_stream_kernel(const NormStream a) {
+  extern __shared__ float4 shared[];
+  // slots of both sums for every team, then the ring
+  constexpr int kSlots = kTeam ? 0 : 3 * kR * 32, kPairs = kColumns / 2;
+  const int teams = blockDim.x / (kTeam ? kTeam : a.team_threads);
+  float* slots = reinterpret_cast<float*>(shared);
+  Stream<T, kE, kColumns, kR, 1, kStages, kTeam> s(a.team_threads, a.n, a.H, reinterpret_cast<char*>(slots + teams * kSlots));
+  uint32_t row = s.row, turn = s.first();
+  char* to = const_cast<char*>(a.out.p) + row * a.out.pitch + s.thread * s.kBytes;
+  s.source(0, a.x[0]);
+  s.start(a.x);
+  if constexpr (kSlots > 0) {
+    for (int i = threadIdx.x; i < teams * kSlots; i += blockDim.x) slots[i] = 0.0f;
+    __syncthreads();
+    slots += s.team * kSlots;
+  }
+  float2 w[kPairs], b[kPairs];
+  read_vector<kE, kPairs>(a.weight, a.weight_bf16, s.column(0), s.pitch(), s.count, 1.0f, w);
+  read_vector<kE, kPairs>(a.bias, a.weight_bf16, s.column(0), s.pitch(), s.count, 0.0f, b);
+  for (; turn < s.n; turn += s.step, row += s.step, to += a.out.advance) {
+    const int stage = s.next(a.x);
+    float2 d[kR][kPairs];
+    float sums[kR], pair_sums[2 * kR];
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      s.read(stage, r, 0, d[r]);
+      sums[r] = pairs_sum<kPairs>(d[r]);
+    }
+    team_sum<kR, kTeam>(sums, slots, s.team, s.threads);
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      sums[r] *= a.inv_h;
+      float2 squares[kPairs];
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        // what lies behind the row stays 0
+        d[r][i] = sub2(d[r][i], make_float2(2 * i / kE < s.count ? sums[r] : 0.0f, (2 * i + 1) / kE < s.count ? sums[r] : 0.0f));
+        squares[i] = mul2(d[r][i], d[r][i]);
+      }
+      pair_sums[r] = pairs_sum<kPairs>(d[r]);
+      pair_sums[kR + r] = pairs_sum<kPairs>(squares);
+    }
+    team_sum<2 * kR, kTeam>(pair_sums, slots + kR * 32, s.team, s.threads);
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      // sums[r] is the mean but for its rounding, which the deviations' own mean shows
+      const float rest = pair_sums[r] * a.inv_h, square = pair_sums[kR + r];
+      const float var = fmaxf(fmaf(-rest, rest, square * a.inv_h), 0.0f);
+      const float rstd = square != square ? square : 1.0f / sqrtf(var + a.eps);
+      if (row + r >= s.n) break;
+      if (s.thread == 0) {
+        a.mean[row + r] = sums[r] + rest;
+        a.rstd[row + r] = rstd;
+      }
+      const float shift = -rest * rstd;
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) d[r][i] = fma2(fma2(d[r][i], both(rstd), both(shift)), w[i], b[i]);
+      write_pairs<T, kE, kPairs>(reinterpret_cast<T*>(to + r * a.out.pitch), s.pitch(), s.count, d[r]);
+    }
+  }
+}
+
+struct NormGradStream {
+  Rows in[2];                // x, grad
+  Rows grad_x;
+  const void* weight;
+  const float* mean;
+  const float* rstd;
+  float* partial;            // null: no sums
+  int weight_bf16, n, H, team_threads;
+  float inv_h;
+};
+
+// A block's teams take batches in turn, a thread the same columns of every row: their weights and the sums
+// for the main_grads stay in its registers.
+template <typename T, int kE, int kColumns, int kR, int kStages, int kTeam>
+__global__ void __launch_bounds__(kStreamThreads) norm_grad_stream_kernel(const NormGradStream a) {
+  extern __shared__ float4 shared[];
+  ptx::pdl_launch_dependents();
+  // two batches' slots for every team, then the ring
+  constexpr int kSlots = kTeam ? 0 : 2 * 2 * kR * 32, kPairs = kColumns / 2;
+  using S = Stream<T, kE, kColumns, kR, 2, kStages, kTeam>;
+  const int teams = blockDim.x / (kTeam ? kTeam : a.team_threads);
+  float* slots = reinterpret_cast<float*>(shared);
+  S s(a.team_threads, a.n, a.H, reinterpret_cast<char*>(slots + teams * kSlots));
+  uint32_t row = s.row, turn = s.first();
+  char* to = const_cast<char*>(a.grad_x.p) + row * a.grad_x.pitch + s.thread * s.kBytes;
+  s.source(0, a.in[0]);
+  s.source(1, a.in[1]);
+  s.start(a.in);
+  float means[kR], rstds[kR];
+  auto moments = [&](uint32_t at) {
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      means[r] = at + r < s.n ? __ldg(a.mean + at + r) : 0.0f;
+      rstds[r] = at + r < s.n ? __ldg(a.rstd + at + r) : 0.0f;
+    }
+  };
+  moments(row);
+  if constexpr (kSlots > 0) {
+    for (int i = threadIdx.x; i < teams * kSlots; i += blockDim.x) slots[i] = 0.0f;
+    __syncthreads();
+    slots += s.team * kSlots;
+  }
+  float2 w[kPairs], dw[kPairs], db[kPairs];
+  read_vector<kE, kPairs>(a.weight, a.weight_bf16, s.column(0), s.pitch(), s.count, 1.0f, w);
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) dw[i] = db[i] = both(0.0f);
+  int flip = 0;
+  for (; turn < s.n; turn += s.step, row += s.step, to += a.grad_x.advance, flip ^= 1) {
+    const int stage = s.next(a.in);
+    float mean[kR], rstd[kR], sums[2 * kR];
+#pragma unroll
+    for (int r = 0; r < kR; ++r) mean[r] = means[r], rstd[r] = rstds[r];
+    moments(row + s.step);
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      float2 x[kPairs], g[kPairs], s1 = both(0.0f), s2 = both(0.0f);
+      s.read(stage, r, 0, x);
+      s.read(stage, r, 1, g);
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        const float2 n = mul2(sub2(x[i], both(mean[r])), both(rstd[r])), u = mul2(g[i], w[i]);
+        dw[i] = fma2(g[i], n, dw[i]);
+        db[i] = add2(db[i], g[i]);
+        s1 = add2(s1, u);
+        s2 = fma2(u, n, s2);
+      }
+      sums[r] = s1.x + s1.y;
+      sums[kR + r] = s2.x + s2.y;
+    }
+    team_sum<2 * kR, kTeam>(sums, slots + flip * 2 * kR * 32, s.team, s.threads);
+    // the rows are read again rather than kept: registers hold the columns' sums
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      if (row + r >= s.n) break;
+      float2 x[kPairs], g[kPairs];
+      s.read(stage, r, 0, x);
+      s.read(stage, r, 1, g);
+      // rstd (u - avg(u) - n avg(u n))
+      const float c1 = -sums[r] * a.inv_h * rstd[r], c2 = -sums[kR + r] * a.inv_h * rstd[r];
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        const float2 n = mul2(sub2(x[i], both(mean[r])), both(rstd[r])), u = mul2(g[i], w[i]);
+        x[i] = fma2(n, both(c2), fma2(u, both(rstd[r]), both(c1)));
+      }
+      write_pairs<T, kE, kPairs>(reinterpret_cast<T*>(to + r * a.grad_x.pitch), s.pitch(), s.count, x);
+    }
+  }
+  if (!a.partial) return;
+  // the teams' sums, in their order, to the block's share
+  float* out = a.partial + static_cast<long long>(blockIdx.x) * 2 * a.H;
+  float* meet = reinterpret_cast<float*>(shared);
+  if constexpr (S::kBytes > 2) ptx::cp_async_wait<0>();        // (the ring is about to be used for them)
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    float mine[kColumns];
+#pragma unroll
+    for (int c = 0; c < kColumns; ++c) {
+      const float2 v = half ? db[c / 2] : dw[c / 2];
+      mine[c] = c % 2 ? v.y : v.x;
+    }
+    if (teams > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int c = 0; c < kColumns; ++c) meet[(s.team * kColumns + c) * s.threads + s.thread] = mine[c];
+      __syncthreads();
+      for (int c = s.team; c < kColumns; c += teams) {
+        float v = 0.0f;
+        for (int t = 0; t < teams; ++t) v += meet[(t * kColumns + c) * s.threads + s.thread];
+        const int j = s.column(c / kE) + c % kE;
+        if (j < a.H) out[half * a.H + j] = v;
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < kColumns; ++c) {
+        const int j = s.column(c / kE) + c % kE;
+        if (j < a.H) out[half * a.H + j] = mine[c];
+      }
+    }
+  }
+}
 
 // Element j of a vector of bf16 or fp32.
 __device__ __forceinline__ float element(const void* p, int bf16, int j) {
@@ -48,6 +531,8 @@ __device__ __forceinline__ float2 block_sum(float2 v) {
 }
 
 constexpr int kRowThreads = 256;
+
+// ---- rows that no block holds: gone through from memory
 
 // A block goes through one row three times.
 template <typename T>
@@ -121,13 +606,27 @@ __global__ void __launch_bounds__(kRowThreads) norm_grad_columns_kernel(NormGrad
   p[a.H + j] = db;
 }
 
-// The shares of a column's sums, added up in order and to the main_grad.
-__global__ void __launch_bounds__(kRowThreads) norm_grad_join_kernel(NormGradArgs a) {
-  const int j = blockIdx.x * kRowThreads + threadIdx.x;
+// The blocks' shares of a column's sums, joined by eight threads a column in an order that depends on their
+// number alone, and added to the main_grad.
+__global__ void __launch_bounds__(256) norm_grad_join_kernel(const NormGradArgs a) {
+  ptx::pdl_wait_prior_grid();
+  __shared__ float sums[8][33];
+  const int lane = threadIdx.x % 32, group = threadIdx.x / 32;
+  const int j = blockIdx.x * 32 + lane;
   void* to = blockIdx.y == 0 ? a.weight_main_grad : a.bias_main_grad;
-  if (j >= a.H || !to) return;
+  if (!to) return;
   float s = 0.0f;
-  for (int part = 0; part < a.parts; ++part) s += a.partial[(static_cast<long long>(part) * 2 + blockIdx.y) * a.H + j];
+  if (j < a.H) {
+    const float* p = a.partial + static_cast<long long>(blockIdx.y) * a.H + j;
+#pragma unroll 4
+    for (int part = group; part < a.parts; part += 8) s += p[static_cast<long long>(part) * 2 * a.H];
+  }
+  sums[group][lane] = s;
+  __syncthreads();
+  if (group || j >= a.H) return;
+  s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s += sums[i][lane];
   if (a.main_grad_bf16) {
     __nv_bfloat16* p = static_cast<__nv_bfloat16*>(to) + j;
     store(p, load(p) + s);
@@ -136,21 +635,193 @@ __global__ void __launch_bounds__(kRowThreads) norm_grad_join_kernel(NormGradArg
   }
 }
 
+cudaError_t launch_join(const NormGradArgs& a, cudaStream_t stream) {
+  if (!a.weight_main_grad && !a.bias_main_grad) return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((a.H + 31) / 32, 2);
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, norm_grad_join_kernel, a);
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+// A launch of one of the two: threads of a team, teams of a block, blocks, shared memory.
+struct StreamShape {
+  int threads, teams, blocks;
+  size_t bytes;
+};
+
+// team: its threads, or 0 for as many warps as it takes; rows: of a batch; slots: floats for each of a batch's rows of a team of several warps; unit: bytes
+// of the ring for a thread.
+StreamShape make_stream_shape(int n, int H, int team, int columns, int most_blocks, int rows, int slots, int unit) {
+  StreamShape s{};
+  s.threads = team ? team : ((H + columns - 1) / columns + 31) / 32 * 32;
+  s.teams = kStreamThreads / s.threads;
+  if (!team && s.teams > 15) s.teams = 15;                 // named barriers 1 to 15
+  const long long want = (static_cast<long long>(n) + rows * s.teams - 1) / (rows * s.teams);
+  s.blocks = static_cast<int>(want < most_blocks ? want : most_blocks);
+  s.bytes = static_cast<size_t>(s.teams) * ((team ? 0 : slots * rows * sizeof(float)) + static_cast<size_t>(s.threads) * unit);
+  return s;
+}
+
+Rows make_rows(const void* p, long long stride, size_t size, const StreamShape& s, int rows) {
+  const long long pitch = stride * static_cast<long long>(size);
+  return {static_cast<const char*>(p), pitch, pitch * s.blocks * s.teams * rows};
+}
+
+constexpr int kMaxDevices = 64;
+
+// Lets a kernel have all of an SM's shared memory, once for each device.
+template <typename K>
+cudaError_t allow_shared(K kernel, std::atomic<bool> (&done)[kMaxDevices], int dev) {
+  if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
+  return e;
+}
+
+// Rows of a batch and stages, by what fits into registers and shared memory: 64 bytes of an array's
+// batch a thread.
+template <typename T, int kColumns>
+constexpr int batch_rows() { return 64 / (kColumns * static_cast<int>(sizeof(T))); }
+template <typename T, int kE>
+constexpr int stages(int arrays) { return kE * sizeof(T) == 2 ? 1 : arrays == 1 ? 4 : 3; }
+
+template <typename T, int kE, int kColumns, int kTeam>
+cudaError_t launch_stream(const NormArgs& a, cudaStream_t stream) {
+  constexpr int kR = batch_rows<T, kColumns>(), kStages = stages<T, kE>(1);
+  static std::atomic<bool> done[kMaxDevices];
+  const auto kernel = norm_stream_kernel<T, kE, kColumns, kR, kStages, kTeam>;
+  const cudaError_t e = allow_shared(kernel, done, a.dev);
+  if (e != cudaSuccess) return e;
+  const StreamShape s = make_stream_shape(a.n, a.H, kTeam, kColumns, a.num_sms, kR, 3 * 32,
+                                          kStages * kR * kColumns * static_cast<int>(sizeof(T)));
+  NormStream k{};
+  k.x[0] = make_rows(a.x, a.x_stride, sizeof(T), s, kR);
+  k.out = make_rows(a.out, a.out_stride, sizeof(T), s, kR);
+  k.weight = a.weight;
+  k.bias = a.bias;
+  k.mean = a.mean;
+  k.rstd = a.rstd;
+  k.weight_bf16 = a.weight_bf16;
+  k.n = a.n;
+  k.H = a.H;
+  k.team_threads = s.threads;
+  k.eps = a.eps;
+  k.inv_h = a.inv_h;
+  kernel<<<s.blocks, s.teams * s.threads, s.bytes, stream>>>(k);
+  return cudaGetLastError();
+}
+
+template <typename T, int kE, int kColumns, int kTeam>
+cudaError_t launch_stream(NormGradArgs a, cudaStream_t stream) {
+  constexpr int kR = batch_rows<T, kColumns>(), kStages = stages<T, kE>(2);
+  static std::atomic<bool> done[kMaxDevices];
+  const auto kernel = norm_grad_stream_kernel<T, kE, kColumns, kR, kStages, kTeam>;
+  const cudaError_t e = allow_shared(kernel, done, a.dev);
+  if (e != cudaSuccess) return e;
+  StreamShape s = make_stream_shape(a.n, a.H, kTeam, kColumns, a.parts, kR, 4 * 32,
+                                    kStages * kR * 2 * kColumns * static_cast<int>(sizeof(T)));
+  const size_t meet = static_cast<size_t>(s.teams) * s.threads * kColumns * sizeof(float);
+  if (s.bytes < meet) s.bytes = meet;
+  a.parts = s.blocks;
+  NormGradStream k{};
+  k.in[0] = make_rows(a.x, a.x_stride, sizeof(T), s, kR);
+  k.in[1] = make_rows(a.grad, a.grad_stride, sizeof(T), s, kR);
+  k.grad_x = make_rows(a.grad_x, a.grad_x_stride, sizeof(T), s, kR);
+  k.weight = a.weight;
+  k.mean = a.mean;
+  k.rstd = a.rstd;
+  k.partial = a.weight_main_grad || a.bias_main_grad ? a.partial : nullptr;
+  k.weight_bf16 = a.weight_bf16;
+  k.n = a.n;
+  k.H = a.H;
+  k.team_threads = s.threads;
+  k.inv_h = a.inv_h;
+  kernel<<<s.blocks, s.teams * s.threads, s.bytes, stream>>>(k);
+  return launch_join(a, stream);
+}
+
+template <typename T, int kE, int kColumns, typename Args>
+cudaError_t by_team(const Args& a, cudaStream_t stream) {
+  if (a.H <= 4 * kColumns) return launch_stream<T, kE, kColumns, 4>(a, stream);
+  if (a.H <= 8 * kColumns) return launch_stream<T, kE, kColumns, 8>(a, stream);
+  if (a.H <= 16 * kColumns) return launch_stream<T, kE, kColumns, 16>(a, stream);
+  if (a.H <= 32 * kColumns) return launch_stream<T, kE, kColumns, 32>(a, stream);
+  return launch_stream<T, kE, kColumns, 0>(a, stream);
+}
+
+// One of the kernels by a row's elements.  A thread has sixteen of them, which spreads a sum's shuffles
+// over the most (65536 x 1024 bf16 forward: 44 us, with eight 51), but for short rows of fp32,
+// of which a batch would be one (65536 x 1024 forward: 93 us, with eight 80), and short rows'
+// gradient, where the columns' sums take the registers (65536 x 256 bf16: 33 us, with eight 23).
+template <typename T, int kE>
+cudaError_t stream_rows(const NormArgs& a, cudaStream_t stream) {
+  if (sizeof(T) == 4 && a.H <= 1024) return by_team<T, kE, 8>(a, stream);
+  return by_team<T, kE, 16>(a, stream);
+}
+template <typename T, int kE>
+cudaError_t stream_rows(const NormGradArgs& a, cudaStream_t stream) {
+  if (a.H <= 1024) return by_team<T, kE, 8>(a, stream);
+  return launch_stream<T, kE, 16, 0>(a, stream);
+}
+
 template <typename T>
-cudaError_t grad(const NormGradArgs& a, cudaStream_t stream) {
+cudaError_t grad_loops(const NormGradArgs& a, cudaStream_t stream) {
   const unsigned columns = (a.H + kRowThreads - 1) / kRowThreads;
   norm_grad_rows_kernel<T><<<a.n, kRowThreads, 0, stream>>>(a);
   norm_grad_columns_kernel<T><<<dim3(columns, a.parts), kRowThreads, 0, stream>>>(a);
-  if (a.weight_main_grad || a.bias_main_grad) norm_grad_join_kernel<<<dim3(columns, 2), kRowThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_join(a, stream);
+}
+
+// Whether rows and vectors can be moved `elements` at a time.
+bool rows_aligned(const void* p, long long stride, int rows, int elements, size_t size) {
+  return reinterpret_cast<uintptr_t>(p) % (elements * size) == 0 && (rows == 1 || stride % elements == 0);
+}
+bool vector_aligned(const void* p, int bf16, int elements) {
+  return reinterpret_cast<uintptr_t>(p) % (elements * (bf16 ? 2 : 4)) == 0;
+}
+bool moves(const NormArgs& a, int elements, size_t size) {
+  return a.H % elements == 0 && rows_aligned(a.x, a.x_stride, a.n, elements, size) &&
+         rows_aligned(a.out, a.out_stride, a.n, elements, size) && vector_aligned(a.weight, a.weight_bf16, elements) &&
+         vector_aligned(a.bias, a.weight_bf16, elements);
+}
+bool moves(const NormGradArgs& a, int elements, size_t size) {
+  return a.H % elements == 0 && rows_aligned(a.x, a.x_stride, a.n, elements, size) &&
+         rows_aligned(a.grad, a.grad_stride, a.n, elements, size) &&
+         rows_aligned(a.grad_x, a.grad_x_stride, a.n, elements, size) && vector_aligned(a.weight, a.weight_bf16, elements);
+}
+
+template <typename T>
+cudaError_t forward(const NormArgs& a, cudaStream_t stream) {
+  constexpr int kWhole = 16 / sizeof(T), kWord = 4 / sizeof(T);
+  if (a.H > kStreamHidden) {
+    norm_kernel<T><<<a.n, kRowThreads, 0, stream>>>(a);
+    return cudaGetLastError();
+  }
+  if (moves(a, kWhole, sizeof(T))) return stream_rows<T, kWhole>(a, stream);
+  if (moves(a, kWord, sizeof(T))) return stream_rows<T, kWord>(a, stream);
+  return stream_rows<T, 1>(a, stream);
+}
+
+template <typename T>
+cudaError_t grad(const NormGradArgs& a, cudaStream_t stream) {
+  constexpr int kWhole = 16 / sizeof(T), kWord = 4 / sizeof(T);
+  if (a.H > kStreamHidden) return grad_loops<T>(a, stream);
+  if (moves(a, kWhole, sizeof(T))) return stream_rows<T, kWhole>(a, stream);
+  if (moves(a, kWord, sizeof(T))) return stream_rows<T, kWord>(a, stream);
+  return stream_rows<T, 1>(a, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_norm(const NormArgs& a, bool bf16, cudaStream_t stream) {
-  if (bf16) norm_kernel<__nv_bfloat16><<<a.n, kRowThreads, 0, stream>>>(a);
-  else norm_kernel<float><<<a.n, kRowThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return bf16 ? forward<__nv_bfloat16>(a, stream) : forward<float>(a, stream);
 }
 
 cudaError_t launch_norm_grad(const NormGradArgs& a, bool bf16, cudaStream_t stream) {

@@ -24,6 +24,7 @@ struct NormArgs {
   long long out_stride;
   float* mean;               // [n] each
   float* rstd;
+  int dev, num_sms;
 };
 
 struct NormGradArgs {
@@ -45,6 +46,7 @@ struct NormGradArgs {
   float2* row_sums;          // [n]: avg(u) and avg(u n)
   float* partial;            // [parts][2][H]: shares of the sums over the rows
   int parts;                 // shares of the rows
+  int dev;
 };
 
 struct NormGradLayout {

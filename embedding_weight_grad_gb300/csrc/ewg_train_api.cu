@@ -179,6 +179,8 @@ int ewg_layer_norm(const void* x, int x_dtype, int64_t rows, int64_t hidden, int
   a.out_stride = out_row_stride;
   a.mean = mean;
   a.rstd = rstd;
+  a.dev = dev;
+  a.num_sms = sms;
   const cudaError_t e = ewg::launch_norm(a, x_dtype == EWG_BF16, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? EWG_OK : cuda_fail(e, "layer norm launch");
 }
@@ -247,6 +249,7 @@ int ewg_layer_norm_backward(const void* grad, int64_t grad_row_stride, const voi
   a.row_sums = reinterpret_cast<float2*>(static_cast<char*>(workspace) + L.row_sums);
   a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + L.partial);
   a.parts = L.parts;
+  a.dev = dev;
   const cudaError_t e = ewg::launch_norm_grad(a, dtype == EWG_BF16, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? EWG_OK : cuda_fail(e, "layer norm gradient launch");
 }
