@@ -60,6 +60,56 @@ __device__ __forceinline__ float load(const float* p) { return *p; }
 __device__ __forceinline__ void store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void store(float* p, float v) { *p = v; }
 
+// 8 neighbouring elements, in one access.
+template <typename T>
+struct Eight;
+
+template <>
+struct Eight<float> {
+  static __device__ __forceinline__ void read(const float* p, float (&f)[8]) {
+    asm volatile("ld.global.L1::no_allocate.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
+                 : "l"(p) : "memory");
+  }
+  static __device__ __forceinline__ void write(float* p, const float (&f)[8]) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(f[0]), "f"(f[1]), "f"(f[2]),
+                 "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]) : "memory");
+  }
+};
+
+template <>
+struct Eight<__nv_bfloat16> {
+  static __device__ __forceinline__ void read(const __nv_bfloat16* p, float (&f)[8]) {
+    uint32_t u[4];
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "l"(p) : "memory");
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(u[i] << 16);
+      f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ void write(__nv_bfloat16* p, const float (&f)[8]) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
+    *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+  }
+};
+
+// e4m3 codes: the values that they stand for.
+__device__ __forceinline__ void eight_codes(const uint8_t* p, float (&f)[8]) {
+  uint32_t u[2];
+  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(u[0]), "=r"(u[1]) : "l"(p) : "memory");
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(u[i / 2] >> (i % 2 * 16)), __NV_E4M3));
+    const float2 v = __half22float2(h);
+    f[2 * i] = v.x;
+    f[2 * i + 1] = v.y;
+  }
+}
+
 __device__ __forceinline__ float from_code(uint8_t c) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
 }
@@ -72,7 +122,8 @@ __device__ __forceinline__ void moments(const AdamwHyper& h, float g, float& m, 
 }
 
 __device__ __forceinline__ float updated(const AdamwHyper& h, const Step& s, float decay, float p, float m, float root) {
-  return p * (1.0f - s.lr * decay) - s.rate * m / (root * s.root_factor + h.eps);
+  // (the quotient of two units in the last place: it is scaled by lr before it meets the param)
+  return p * (1.0f - s.lr * decay) - __fdividef(s.rate * m, root * s.root_factor + h.eps);
 }
 
 // A block's scale from its largest magnitude's bits (NaN is above every other), and what values are
@@ -157,6 +208,78 @@ __device__ __forceinline__ void update_block(const AdamwEntry& e, const AdamwHyp
   }
 }
 
+// The same of a whole block where every array can be moved eight elements at a time; lanes take eight
+// neighbouring ones each.
+template <typename P, typename G, int kBits>
+__device__ __forceinline__ void update_whole_block(const AdamwEntry& e, const AdamwHyper& h, const Step& s, long long base,
+                                                   int lane) {
+  const long long first = base + lane * 8;
+  P* param = static_cast<P*>(e.param) + first;
+  float p[8], g[8], m[8], v[8];
+  Eight<P>::read(param, p);
+  Eight<G>::read(static_cast<const G*>(e.grad) + first, g);
+  if constexpr (kBits == 32) {
+    float* mp = static_cast<float*>(e.exp_avg) + first;
+    float* vp = static_cast<float*>(e.exp_avg_sq) + first;
+    Eight<float>::read(mp, m);
+    Eight<float>::read(vp, v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      moments(h, g[k] * s.grad_scale, m[k], v[k]);
+      p[k] = updated(h, s, e.weight_decay, p[k], m[k], sqrtf(v[k]));
+    }
+    Eight<float>::write(mp, m);
+    Eight<float>::write(vp, v);
+  } else {
+    uint8_t* mp = static_cast<uint8_t*>(e.exp_avg) + first;
+    uint8_t* rp = static_cast<uint8_t*>(e.exp_avg_sq) + first;
+    eight_codes(mp, m);
+    eight_codes(rp, v);
+    float2* at = e.scales + base / kAdamwBlock;
+    const float2 scale = *at;
+    uint32_t top_m = 0, top_root = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      m[k] = __fmul_rn(m[k], scale.x);
+      const float r = __fmul_rn(v[k], scale.y);
+      v[k] = __fmul_rn(r, r);
+      moments(h, __fmul_rn(g[k], s.grad_scale), m[k], v[k]);
+      v[k] = sqrtf(v[k]);
+      p[k] = updated(h, s, e.weight_decay, p[k], m[k], v[k]);
+      top_m = max(top_m, __float_as_uint(m[k]) & 0x7fffffffu);
+      top_root = max(top_root, __float_as_uint(v[k]) & 0x7fffffffu);
+    }
+    top_m = __reduce_max_sync(kAll, top_m);
+    top_root = __reduce_max_sync(kAll, top_root);
+    float inverse_m, inverse_root;
+    float2 now;
+    now.x = block_scale(top_m, inverse_m);
+    now.y = block_scale(top_root, inverse_root);
+    if (lane == 0) *at = now;
+    const uint32_t n = static_cast<uint32_t>(first);
+    const uint32_t from_m = n * kWeylA + s.t * kWeylB, from_root = n * kWeylB + s.t * kWeylA;
+    uint32_t cm[2] = {}, cr[2] = {};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      cm[k / 4] |= to_code(m[k], inverse_m, (from_m + k * kWeylA) >> 12) << (k % 4 * 8);
+      uint32_t c = to_code(v[k], inverse_root, (from_root + k * kWeylB) >> 12);
+      if (c == 0 && v[k] > 0.0f && inverse_root > 0.0f) c = 1;
+      cr[k / 4] |= c << (k % 4 * 8);
+    }
+    *reinterpret_cast<uint2*>(mp) = make_uint2(cm[0], cm[1]);
+    *reinterpret_cast<uint2*>(rp) = make_uint2(cr[0], cr[1]);
+  }
+  Eight<P>::write(param, p);
+  if constexpr (sizeof(P) == 4)
+    if (e.copy) Eight<__nv_bfloat16>::write(static_cast<__nv_bfloat16*>(e.copy) + first, p);
+}
+
+template <typename P, typename G, int kBits>
+__device__ __forceinline__ void update(const AdamwEntry& e, const AdamwHyper& h, const Step& s, long long base, int lane) {
+  if ((e.flags & kAdamwWhole) && base + kAdamwBlock <= e.count) update_whole_block<P, G, kBits>(e, h, s, base, lane);
+  else update_block<P, G, kBits>(e, h, s, base, lane);
+}
+
 template <int kBits, int kTable>
 __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Launch<kTable> a) {
   const Step s = make_step(a.hyper);
@@ -172,10 +295,10 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     const long long base = static_cast<long long>(tile - e.first_tile) * kAdamwTile + warp * kAdamwBlock;
     if (base >= e.count) continue;
     switch (e.flags & (kAdamwParamBf16 | kAdamwGradBf16)) {
-      case 0: update_block<float, float, kBits>(e, a.hyper, s, base, lane); break;
-      case kAdamwParamBf16: update_block<__nv_bfloat16, float, kBits>(e, a.hyper, s, base, lane); break;
-      case kAdamwGradBf16: update_block<float, __nv_bfloat16, kBits>(e, a.hyper, s, base, lane); break;
-      default: update_block<__nv_bfloat16, __nv_bfloat16, kBits>(e, a.hyper, s, base, lane);
+      case 0: update<float, float, kBits>(e, a.hyper, s, base, lane); break;
+      case kAdamwParamBf16: update<__nv_bfloat16, float, kBits>(e, a.hyper, s, base, lane); break;
+      case kAdamwGradBf16: update<float, __nv_bfloat16, kBits>(e, a.hyper, s, base, lane); break;
+      default: update<__nv_bfloat16, __nv_bfloat16, kBits>(e, a.hyper, s, base, lane);
     }
   }
 }
