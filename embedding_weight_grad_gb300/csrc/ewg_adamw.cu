@@ -12,10 +12,13 @@
 // (an additive sequence), and the changes add up.  Rounding is an integer addition: times 2^-120,
 // e4m3's exponents are fp32's lowest, its steps below 2^-6 fp32's subnormals, and a code the
 // upper 7 bits of a number's 27.
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include "ewg_ptx.cuh"
 #include "ewg_train.cuh"
 
 namespace ewg {
@@ -23,8 +26,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr unsigned kAll = 0xffffffffu;
-constexpr float kTop = 448.0f;                                        // e4m3's largest number
-constexpr float kTopInverse = static_cast<float>(1.0 / 448.0);
+constexpr float kTopInverse = static_cast<float>(1.0 / 448.0);      // of e4m3's largest number
 constexpr float kLowestScale = 0x1p-120f;
 // the first two powers of the plastic number's inverse, of 2^32
 constexpr uint32_t kWeylA = 0xC13FA9A9u, kWeylB = 0x91E10DA5u;
@@ -55,75 +57,123 @@ __device__ __forceinline__ Step make_step(const AdamwHyper& h) {
   return s;
 }
 
-__device__ __forceinline__ float load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ float load(const float* p) { return *p; }
-__device__ __forceinline__ void store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-__device__ __forceinline__ void store(float* p, float v) { *p = v; }
+// How a warp's 256 elements lie with its lanes, eight each: neighbours, moved by one access, where every
+// array is aligned to eight of its elements and the block is whole; else one of every 32, of which
+// those that are there (`count` of the block) are moved by themselves.
+template <bool kWhole>
+struct Place {
+  static constexpr int kStep = kWhole ? 1 : 32;
+  long long first;           // of the tensor, the lane's first element
+  int left;                  // elements of the block from that one on
 
-// 8 neighbouring elements, in one access.
-template <typename T>
-struct Eight;
-
-template <>
-struct Eight<float> {
-  static __device__ __forceinline__ void read(const float* p, float (&f)[8]) {
-    asm volatile("ld.global.L1::no_allocate.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]), "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7])
-                 : "l"(p) : "memory");
-  }
-  static __device__ __forceinline__ void write(float* p, const float (&f)[8]) {
-    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(f[0]), "f"(f[1]), "f"(f[2]),
-                 "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]) : "memory");
-  }
-};
-
-template <>
-struct Eight<__nv_bfloat16> {
-  static __device__ __forceinline__ void read(const __nv_bfloat16* p, float (&f)[8]) {
-    uint32_t u[4];
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "l"(p) : "memory");
+  __device__ __forceinline__ void read(const float* p, float2 (&f)[4]) const {
+    p += first;
+    if constexpr (kWhole) {
+      asm volatile("ld.global.L1::no_allocate.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=f"(f[0].x), "=f"(f[0].y), "=f"(f[1].x), "=f"(f[1].y), "=f"(f[2].x), "=f"(f[2].y), "=f"(f[3].x),
+                     "=f"(f[3].y) : "l"(p) : "memory");
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(u[i] << 16);
-      f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+      for (int k = 0; k < 8; ++k) at(f, k) = k * 32 < left ? p[k * 32] : 0.0f;
     }
   }
-  static __device__ __forceinline__ void write(__nv_bfloat16* p, const float (&f)[8]) {
+  __device__ __forceinline__ void read(const __nv_bfloat16* p, float2 (&f)[4]) const {
+    p += first;
+    if constexpr (kWhole) {
+      uint32_t u[4];
+      asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "l"(p) : "memory");
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) at(f, k) = k * 32 < left ? __bfloat162float(p[k * 32]) : 0.0f;
+    }
+  }
+  // e4m3 codes: the values that they stand for
+  __device__ __forceinline__ void read(const uint8_t* p, float2 (&f)[4]) const {
+    p += first;
+    uint32_t u[4];                                          // two codes each
+    if constexpr (kWhole) {
+      uint32_t v[2];
+      asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "l"(p) : "memory");
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = v[i / 2] >> (i % 2 * 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        u[i] = (2 * i * 32 < left ? p[2 * i * 32] : 0) | (2 * i * 32 + 32 < left ? p[2 * i * 32 + 32] << 8 : 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      f[i] = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(u[i]), __NV_E4M3)));
+  }
+  __device__ __forceinline__ void write(float* p, const float2 (&f)[4]) const {
+    p += first;
+    if constexpr (kWhole) {
+      asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(f[0].x), "f"(f[0].y), "f"(f[1].x),
+                   "f"(f[1].y), "f"(f[2].x), "f"(f[2].y), "f"(f[3].x), "f"(f[3].y) : "memory");
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k * 32 < left) p[k * 32] = k % 2 ? f[k / 2].y : f[k / 2].x;
+    }
+  }
+  __device__ __forceinline__ void write(__nv_bfloat16* p, const float2 (&f)[4]) const {
+    p += first;
     uint32_t u[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
-    *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+    for (int i = 0; i < 4; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u[i]) : "f"(f[i].y), "f"(f[i].x));
+    if constexpr (kWhole) {
+      *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k * 32 < left) reinterpret_cast<unsigned short*>(p)[k * 32] = static_cast<unsigned short>(u[k / 2] >> (k % 2 * 16));
+    }
   }
+  // codes, each in the upper byte of a word
+  __device__ __forceinline__ void write(uint8_t* p, const uint32_t (&c)[8]) const {
+    p += first;
+    if constexpr (kWhole) {
+      uint32_t v[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        v[i] = __byte_perm(__byte_perm(c[4 * i], c[4 * i + 1], 0x0073), __byte_perm(c[4 * i + 2], c[4 * i + 3], 0x0073), 0x5410);
+      *reinterpret_cast<uint2*>(p) = make_uint2(v[0], v[1]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k * 32 < left) p[k * 32] = static_cast<uint8_t>(c[k] >> 24);
+    }
+  }
+  static __device__ __forceinline__ float& at(float2 (&f)[4], int k) { return k % 2 ? f[k / 2].y : f[k / 2].x; }
 };
 
-// e4m3 codes: the values that they stand for.
-__device__ __forceinline__ void eight_codes(const uint8_t* p, float (&f)[8]) {
-  uint32_t u[2];
-  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(u[0]), "=r"(u[1]) : "l"(p) : "memory");
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2 h(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(u[i / 2] >> (i % 2 * 16)), __NV_E4M3));
-    const float2 v = __half22float2(h);
-    f[2 * i] = v.x;
-    f[2 * i + 1] = v.y;
-  }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// (Not the packed addition: the compiler joins it with the products before it, which then are not
+// rounded.)
+__device__ __forceinline__ float2 rounded_sum(float2 a, float2 b) {
+  return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y));
 }
 
-__device__ __forceinline__ float from_code(uint8_t c) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
+// 1 / x to a unit in the last place; x is no subnormal (a root is 0 or above 2^-75).
+__device__ __forceinline__ float reciprocal(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// The moments after a gradient.  In 8 bits their rounding goes by every bit, so each
-// operation is rounded by itself, whatever the compiler would join.
-__device__ __forceinline__ void moments(const AdamwHyper& h, float g, float& m, float& v) {
-  m = __fadd_rn(__fmul_rn(m, h.beta1), __fmul_rn(g, h.rest1));
-  v = __fadd_rn(__fmul_rn(v, h.beta2), __fmul_rn(__fmul_rn(g, g), h.rest2));
+// The larger magnitude (of either sign), NaN if either is.
+__device__ __forceinline__ float larger(float a, float b) {
+  float y;
+  asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
 }
 
-__device__ __forceinline__ float updated(const AdamwHyper& h, const Step& s, float decay, float p, float m, float root) {
-  // (the quotient of two units in the last place: it is scaled by lr before it meets the param)
-  return p * (1.0f - s.lr * decay) - __fdividef(s.rate * m, root * s.root_factor + h.eps);
+__device__ __forceinline__ float largest(const float2 (&f)[4]) {
+  return larger(larger(larger(f[0].x, f[0].y), larger(f[1].x, f[1].y)), larger(larger(f[2].x, f[2].y), larger(f[3].x, f[3].y)));
 }
 
 // A block's scale from its largest magnitude's bits (NaN is above every other), and what values are
@@ -135,149 +185,96 @@ __device__ __forceinline__ float block_scale(uint32_t bits, float& inverse) {
   return none ? 0.0f : scale;
 }
 
-// e4m3 code of x relative to its block's scale, `threshold` of 20 bits.
-__device__ __forceinline__ uint32_t to_code(float x, float inverse, uint32_t threshold) {
-  const uint32_t bits = __float_as_uint(__fmul_rn(__fmul_rn(x, inverse), 0x1p-120f));
-  const uint32_t code = ((bits & 0x7fffffffu) + threshold) >> 20;
-  return (code < 126u ? code : 126u) | (bits >> 31 << 7);
+// e4m3 codes of x relative to its block's scale, in the upper bytes; their thresholds are the upper
+// 20 bits of `from` and what follows it by steps of `by`.  `lowest`: the least that a number above
+// 0 becomes (for numbers that are not negative), in the same place as a code before it is moved up.
+template <bool kSigned>
+__device__ __forceinline__ void to_codes(const float2 (&x)[4], float inverse, uint32_t from, uint32_t by, uint32_t lowest,
+                                         uint32_t (&c)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 y = ptx::mul2(ptx::mul2(x[i], both(inverse)), both(0x1p-120f));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = 2 * i + h;
+      const uint32_t bits = __float_as_uint(h ? y.y : y.x);
+      const uint32_t sum = bits + ((from + k * by) >> 12);
+      constexpr uint32_t kMost = (126u << 20) | 0xfffffu;
+      if constexpr (kSigned) {
+        c[k] = min(sum & 0x7fffffffu, kMost) << 4 | (sum & 0x80000000u);
+      } else {
+        const uint32_t least = min(__float_as_uint(h ? x[i].y : x[i].x), lowest);
+        c[k] = max(min(sum, kMost), least) << 4;
+      }
+    }
+  }
 }
 
-// A warp's 256 elements from `base` on.
-template <typename P, typename G, int kBits>
+// A warp's block of 256 elements.
+template <typename P, typename G, int kBits, bool kWhole>
 __device__ __forceinline__ void update_block(const AdamwEntry& e, const AdamwHyper& h, const Step& s, long long base, int lane) {
-  P* param = static_cast<P*>(e.param) + base;
-  const G* grad = static_cast<const G*>(e.grad) + base;
-  __nv_bfloat16* copy = e.copy ? static_cast<__nv_bfloat16*>(e.copy) + base : nullptr;
+  using ptx::fma2;
+  using ptx::mul2;
   const int count = e.count - base < kAdamwBlock ? static_cast<int>(e.count - base) : kAdamwBlock;
-  if constexpr (kBits == 32) {
-    float* mp = static_cast<float*>(e.exp_avg) + base;
-    float* vp = static_cast<float*>(e.exp_avg_sq) + base;
-    for (int i = lane; i < count; i += 32) {
-      float m = mp[i], v = vp[i];
-      moments(h, load(grad + i) * s.grad_scale, m, v);
-      const float p = updated(h, s, e.weight_decay, load(param + i), m, sqrtf(v));
-      mp[i] = m;
-      vp[i] = v;
-      store(param + i, p);
-      if (copy) store(copy + i, p);
-    }
-  } else {
-    uint8_t* mp = static_cast<uint8_t*>(e.exp_avg) + base;
-    uint8_t* rp = static_cast<uint8_t*>(e.exp_avg_sq) + base;
-    float2* at = e.scales + base / kAdamwBlock;
-    const float2 scale = *at;
-    float m[8], root[8];
-    uint32_t top_m = 0, top_root = 0;
+  const Place<kWhole> place{base + (kWhole ? lane * 8 : lane), count - lane};
+  using State = typename std::conditional<kBits == 32, float, uint8_t>::type;
+  P* param = static_cast<P*>(e.param);
+  State* exp_avg = static_cast<State*>(e.exp_avg);
+  State* exp_avg_sq = static_cast<State*>(e.exp_avg_sq);
+  float2 p[4], g[4], m[4], v[4], root[4];
+  place.read(param, p);
+  place.read(static_cast<const G*>(e.grad), g);
+  place.read(exp_avg, m);
+  place.read(exp_avg_sq, v);
+  if constexpr (kBits == 8) {
+    const float2 scale = e.scales[base / kAdamwBlock];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int i = k * 32 + lane;
-      m[k] = root[k] = 0.0f;
-      if (i < count) {
-        m[k] = __fmul_rn(from_code(mp[i]), scale.x);
-        const float r = __fmul_rn(from_code(rp[i]), scale.y);
-        float v = __fmul_rn(r, r);
-        moments(h, __fmul_rn(load(grad + i), s.grad_scale), m[k], v);
-        root[k] = sqrtf(v);
-        const float p = updated(h, s, e.weight_decay, load(param + i), m[k], root[k]);
-        store(param + i, p);
-        if (copy) store(copy + i, p);
-      }
-      const uint32_t am = __float_as_uint(m[k]) & 0x7fffffffu, ar = __float_as_uint(root[k]) & 0x7fffffffu;
-      top_m = am > top_m ? am : top_m;
-      top_root = ar > top_root ? ar : top_root;
-    }
-    top_m = __reduce_max_sync(kAll, top_m);
-    top_root = __reduce_max_sync(kAll, top_root);
-    float inverse_m, inverse_root;
-    float2 now;
-    now.x = block_scale(top_m, inverse_m);
-    now.y = block_scale(top_root, inverse_root);
-    if (lane == 0) *at = now;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int i = k * 32 + lane;
-      if (i < count) {
-        const uint32_t n = static_cast<uint32_t>(base) + i;
-        mp[i] = static_cast<uint8_t>(to_code(m[k], inverse_m, (n * kWeylA + s.t * kWeylB) >> 12));
-        uint32_t c = to_code(root[k], inverse_root, (n * kWeylB + s.t * kWeylA) >> 12);
-        // an element that has had gradients keeps a root to divide by
-        if (c == 0 && root[k] > 0.0f && inverse_root > 0.0f) c = 1;
-        rp[i] = static_cast<uint8_t>(c);
-      }
+    for (int i = 0; i < 4; ++i) {
+      m[i] = mul2(m[i], both(scale.x));
+      v[i] = mul2(v[i], both(scale.y));
+      v[i] = mul2(v[i], v[i]);
     }
   }
-}
-
-// The same of a whole block where every array can be moved eight elements at a time; lanes take eight
-// neighbouring ones each.
-template <typename P, typename G, int kBits>
-__device__ __forceinline__ void update_whole_block(const AdamwEntry& e, const AdamwHyper& h, const Step& s, long long base,
-                                                   int lane) {
-  const long long first = base + lane * 8;
-  P* param = static_cast<P*>(e.param) + first;
-  float p[8], g[8], m[8], v[8];
-  Eight<P>::read(param, p);
-  Eight<G>::read(static_cast<const G*>(e.grad) + first, g);
-  if constexpr (kBits == 32) {
-    float* mp = static_cast<float*>(e.exp_avg) + first;
-    float* vp = static_cast<float*>(e.exp_avg_sq) + first;
-    Eight<float>::read(mp, m);
-    Eight<float>::read(vp, v);
+  const float2 keep = both(1.0f - s.lr * e.weight_decay);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      moments(h, g[k] * s.grad_scale, m[k], v[k]);
-      p[k] = updated(h, s, e.weight_decay, p[k], m[k], sqrtf(v[k]));
-    }
-    Eight<float>::write(mp, m);
-    Eight<float>::write(vp, v);
-  } else {
-    uint8_t* mp = static_cast<uint8_t*>(e.exp_avg) + first;
-    uint8_t* rp = static_cast<uint8_t*>(e.exp_avg_sq) + first;
-    eight_codes(mp, m);
-    eight_codes(rp, v);
-    float2* at = e.scales + base / kAdamwBlock;
-    const float2 scale = *at;
-    uint32_t top_m = 0, top_root = 0;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      m[k] = __fmul_rn(m[k], scale.x);
-      const float r = __fmul_rn(v[k], scale.y);
-      v[k] = __fmul_rn(r, r);
-      moments(h, __fmul_rn(g[k], s.grad_scale), m[k], v[k]);
-      v[k] = sqrtf(v[k]);
-      p[k] = updated(h, s, e.weight_decay, p[k], m[k], v[k]);
-      top_m = max(top_m, __float_as_uint(m[k]) & 0x7fffffffu);
-      top_root = max(top_root, __float_as_uint(v[k]) & 0x7fffffffu);
-    }
-    top_m = __reduce_max_sync(kAll, top_m);
-    top_root = __reduce_max_sync(kAll, top_root);
-    float inverse_m, inverse_root;
-    float2 now;
-    now.x = block_scale(top_m, inverse_m);
-    now.y = block_scale(top_root, inverse_root);
-    if (lane == 0) *at = now;
-    const uint32_t n = static_cast<uint32_t>(first);
-    const uint32_t from_m = n * kWeylA + s.t * kWeylB, from_root = n * kWeylB + s.t * kWeylA;
-    uint32_t cm[2] = {}, cr[2] = {};
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      cm[k / 4] |= to_code(m[k], inverse_m, (from_m + k * kWeylA) >> 12) << (k % 4 * 8);
-      uint32_t c = to_code(v[k], inverse_root, (from_root + k * kWeylB) >> 12);
-      if (c == 0 && v[k] > 0.0f && inverse_root > 0.0f) c = 1;
-      cr[k / 4] |= c << (k % 4 * 8);
-    }
-    *reinterpret_cast<uint2*>(mp) = make_uint2(cm[0], cm[1]);
-    *reinterpret_cast<uint2*>(rp) = make_uint2(cr[0], cr[1]);
+  for (int i = 0; i < 4; ++i) {
+    // (each operation rounded by itself: the codes go by every bit of the moments)
+    g[i] = mul2(g[i], both(s.grad_scale));
+    m[i] = rounded_sum(mul2(m[i], both(h.beta1)), mul2(g[i], both(h.rest1)));
+    v[i] = rounded_sum(mul2(v[i], both(h.beta2)), mul2(mul2(g[i], g[i]), both(h.rest2)));
+    root[i] = make_float2(sqrtf(v[i].x), sqrtf(v[i].y));
+    const float2 under = fma2(root[i], both(s.root_factor), both(h.eps));
+    const float2 over = mul2(m[i], both(-s.rate));
+    p[i] = fma2(p[i], keep, mul2(over, make_float2(reciprocal(under.x), reciprocal(under.y))));
   }
-  Eight<P>::write(param, p);
+  place.write(param, p);
   if constexpr (sizeof(P) == 4)
-    if (e.copy) Eight<__nv_bfloat16>::write(static_cast<__nv_bfloat16*>(e.copy) + first, p);
+    if (e.copy) place.write(static_cast<__nv_bfloat16*>(e.copy), p);
+  if constexpr (kBits == 32) {
+    place.write(exp_avg, m);
+    place.write(exp_avg_sq, v);
+  } else {
+    const uint32_t top_m = __reduce_max_sync(kAll, __float_as_uint(largest(m)) & 0x7fffffffu);
+    const uint32_t top_root = __reduce_max_sync(kAll, __float_as_uint(largest(root)) & 0x7fffffffu);
+    float inverse_m, inverse_root;
+    float2 now;
+    now.x = block_scale(top_m, inverse_m);
+    now.y = block_scale(top_root, inverse_root);
+    if (lane == 0) e.scales[base / kAdamwBlock] = now;
+    const uint32_t n = static_cast<uint32_t>(place.first);
+    uint32_t c[8];
+    to_codes<true>(m, inverse_m, n * kWeylA + s.t * kWeylB, place.kStep * kWeylA, 0, c);
+    place.write(exp_avg, c);
+    // a root above 0 keeps a code above 0: its element goes on to be divided by it
+    to_codes<false>(root, inverse_root, n * kWeylB + s.t * kWeylA, place.kStep * kWeylB, inverse_root > 0.0f ? 1u << 20 : 0u, c);
+    place.write(exp_avg_sq, c);
+  }
 }
 
 template <typename P, typename G, int kBits>
 __device__ __forceinline__ void update(const AdamwEntry& e, const AdamwHyper& h, const Step& s, long long base, int lane) {
-  if ((e.flags & kAdamwWhole) && base + kAdamwBlock <= e.count) update_whole_block<P, G, kBits>(e, h, s, base, lane);
-  else update_block<P, G, kBits>(e, h, s, base, lane);
+  if ((e.flags & kAdamwWhole) && base + kAdamwBlock <= e.count) update_block<P, G, kBits, true>(e, h, s, base, lane);
+  else update_block<P, G, kBits, false>(e, h, s, base, lane);
 }
 
 template <int kBits, int kTable>
