@@ -57,29 +57,32 @@ __device__ __forceinline__ Step make_step(const AdamwHyper& h) {
   return s;
 }
 
-// How a warp's 256 elements lie with its lanes, eight each: neighbours, moved by one access, where every
-// array is aligned to eight of its elements and the block is whole; else one of every 32, of which
-// those that are there (`count` of the block) are moved by themselves.
-template <bool kWhole>
+// How a warp's 256 elements lie with its lanes, eight each.  kAligned: neighbours, moved by one access, of a whole
+// block of arrays that are aligned to eight of their elements; kWhole: one of every 32, of a whole block;
+// kPart: the same of a tensor's last block, of which those that are there are moved.
+enum Mode { kAligned, kWhole, kPart };
+
+template <int kMode>
 struct Place {
-  static constexpr int kStep = kWhole ? 1 : 32;
+  static constexpr int kStep = kMode == kAligned ? 1 : 32;
   long long first;           // of the tensor, the lane's first element
   int left;                  // elements of the block from that one on
 
+  __device__ __forceinline__ bool there(int k) const { return kMode != kPart || k * 32 < left; }
   __device__ __forceinline__ void read(const float* p, float2 (&f)[4]) const {
     p += first;
-    if constexpr (kWhole) {
+    if constexpr (kMode == kAligned) {
       asm volatile("ld.global.L1::no_allocate.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                    : "=f"(f[0].x), "=f"(f[0].y), "=f"(f[1].x), "=f"(f[1].y), "=f"(f[2].x), "=f"(f[2].y), "=f"(f[3].x),
                      "=f"(f[3].y) : "l"(p) : "memory");
     } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) at(f, k) = k * 32 < left ? p[k * 32] : 0.0f;
+      for (int k = 0; k < 8; ++k) at(f, k) = there(k) ? p[k * 32] : 0.0f;
     }
   }
   __device__ __forceinline__ void read(const __nv_bfloat16* p, float2 (&f)[4]) const {
     p += first;
-    if constexpr (kWhole) {
+    if constexpr (kMode == kAligned) {
       uint32_t u[4];
       asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                    : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]) : "l"(p) : "memory");
@@ -87,14 +90,14 @@ struct Place {
       for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
     } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) at(f, k) = k * 32 < left ? __bfloat162float(p[k * 32]) : 0.0f;
+      for (int k = 0; k < 8; ++k) at(f, k) = there(k) ? __bfloat162float(p[k * 32]) : 0.0f;
     }
   }
   // e4m3 codes: the values that they stand for
   __device__ __forceinline__ void read(const uint8_t* p, float2 (&f)[4]) const {
     p += first;
     uint32_t u[4];                                          // two codes each
-    if constexpr (kWhole) {
+    if constexpr (kMode == kAligned) {
       uint32_t v[2];
       asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "l"(p) : "memory");
 #pragma unroll
@@ -102,7 +105,7 @@ struct Place {
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        u[i] = (2 * i * 32 < left ? p[2 * i * 32] : 0) | (2 * i * 32 + 32 < left ? p[2 * i * 32 + 32] << 8 : 0);
+        u[i] = (there(2 * i) ? p[2 * i * 32] : 0) | (there(2 * i + 1) ? p[2 * i * 32 + 32] << 8 : 0);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -110,13 +113,13 @@ struct Place {
   }
   __device__ __forceinline__ void write(float* p, const float2 (&f)[4]) const {
     p += first;
-    if constexpr (kWhole) {
+    if constexpr (kMode == kAligned) {
       asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(f[0].x), "f"(f[0].y), "f"(f[1].x),
                    "f"(f[1].y), "f"(f[2].x), "f"(f[2].y), "f"(f[3].x), "f"(f[3].y) : "memory");
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (k * 32 < left) p[k * 32] = k % 2 ? f[k / 2].y : f[k / 2].x;
+        if (there(k)) p[k * 32] = k % 2 ? f[k / 2].y : f[k / 2].x;
     }
   }
   __device__ __forceinline__ void write(__nv_bfloat16* p, const float2 (&f)[4]) const {
@@ -124,18 +127,18 @@ struct Place {
     uint32_t u[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u[i]) : "f"(f[i].y), "f"(f[i].x));
-    if constexpr (kWhole) {
+    if constexpr (kMode == kAligned) {
       *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (k * 32 < left) reinterpret_cast<unsigned short*>(p)[k * 32] = static_cast<unsigned short>(u[k / 2] >> (k % 2 * 16));
+        if (there(k)) reinterpret_cast<unsigned short*>(p)[k * 32] = static_cast<unsigned short>(u[k / 2] >> (k % 2 * 16));
     }
   }
   // codes, each in the upper byte of a word
   __device__ __forceinline__ void write(uint8_t* p, const uint32_t (&c)[8]) const {
     p += first;
-    if constexpr (kWhole) {
+    if constexpr (kMode == kAligned) {
       uint32_t v[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -144,7 +147,7 @@ struct Place {
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (k * 32 < left) p[k * 32] = static_cast<uint8_t>(c[k] >> 24);
+        if (there(k)) p[k * 32] = static_cast<uint8_t>(c[k] >> 24);
     }
   }
   static __device__ __forceinline__ float& at(float2 (&f)[4], int k) { return k % 2 ? f[k / 2].y : f[k / 2].x; }
@@ -211,12 +214,12 @@ __device__ __forceinline__ void to_codes(const float2 (&x)[4], float inverse, ui
 }
 
 // A warp's block of 256 elements.
-template <typename P, typename G, int kBits, bool kWhole>
+template <typename P, typename G, int kBits, int kMode>
 __device__ __forceinline__ void update_block(const AdamwEntry& e, const AdamwHyper& h, const Step& s, long long base, int lane) {
   using ptx::fma2;
   using ptx::mul2;
   const int count = e.count - base < kAdamwBlock ? static_cast<int>(e.count - base) : kAdamwBlock;
-  const Place<kWhole> place{base + (kWhole ? lane * 8 : lane), count - lane};
+  const Place<kMode> place{base + (kMode == kAligned ? lane * 8 : lane), count - lane};
   using State = typename std::conditional<kBits == 32, float, uint8_t>::type;
   P* param = static_cast<P*>(e.param);
   State* exp_avg = static_cast<State*>(e.exp_avg);
@@ -273,13 +276,17 @@ __device__ __forceinline__ void update_block(const AdamwEntry& e, const AdamwHyp
 
 template <typename P, typename G, int kBits>
 __device__ __forceinline__ void update(const AdamwEntry& e, const AdamwHyper& h, const Step& s, long long base, int lane) {
-  if ((e.flags & kAdamwWhole) && base + kAdamwBlock <= e.count) update_block<P, G, kBits, true>(e, h, s, base, lane);
-  else update_block<P, G, kBits, false>(e, h, s, base, lane);
+  if (base + kAdamwBlock > e.count) update_block<P, G, kBits, kPart>(e, h, s, base, lane);
+  else if (e.flags & kAdamwAligned) update_block<P, G, kBits, kAligned>(e, h, s, base, lane);
+  else update_block<P, G, kBits, kWhole>(e, h, s, base, lane);
 }
 
 template <int kBits, int kTable>
 __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Launch<kTable> a) {
-  const Step s = make_step(a.hyper);
+  __shared__ Step shared_step;
+  if (threadIdx.x == 0) shared_step = make_step(a.hyper);
+  __syncthreads();
+  const Step s = shared_step;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   int at = 0;
   for (int tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
@@ -308,7 +315,10 @@ cudaError_t launch(const AdamwEntry* entries, int num, const AdamwHyper& h, int 
   for (int i = 0; i < num; ++i) a.entry[i] = entries[i];
   const AdamwEntry& last = entries[num - 1];
   a.tiles = last.first_tile + static_cast<int>((last.count + kAdamwTile - 1) / kAdamwTile);
-  const int most = num_sms * 8;
+  // In 32 bits a block of threads takes one tile, so that the tiles on the way are neighbours in memory (50257 x
+  // 1024 fp32: 210 us; 8 blocks an SM that go on in steps of the grid: 226).  In 8 bits the step's
+  // own numbers cost more than that brings: 32 blocks an SM (132 us; one tile each 146, 8 an SM 135).
+  const int most = kBits == 32 ? a.tiles : num_sms * 32;
   adamw_kernel<kBits, kTable><<<a.tiles < most ? a.tiles : most, kThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }

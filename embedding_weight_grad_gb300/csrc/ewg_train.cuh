@@ -91,7 +91,7 @@ struct AdamwEntry {
 enum {
   kAdamwParamBf16 = 1,
   kAdamwGradBf16 = 2,
-  kAdamwWhole = 4            // every array is aligned to eight of its elements
+  kAdamwAligned = 4          // every array is aligned to eight of its elements
 };
 
 // What a launch carries as its argument: the entries of up to this many tensors, of 32764 bytes that

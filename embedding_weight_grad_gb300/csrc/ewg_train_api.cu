@@ -109,7 +109,7 @@ int plan_adamw(const ewg_adamw_tensor* tensors, int64_t num, int state_bits, voi
     e.flags = (t.param_dtype == EWG_BF16 ? ewg::kAdamwParamBf16 : 0) | (t.grad_dtype == EWG_BF16 ? ewg::kAdamwGradBf16 : 0);
     if (aligned(t.param, 8 * ps) && aligned(t.grad, 8 * gs) && aligned(t.exp_avg, 8 * ss) &&
         aligned(t.exp_avg_sq, 8 * ss) && aligned(t.copy, 16))
-      e.flags |= ewg::kAdamwWhole;
+      e.flags |= ewg::kAdamwAligned;
     entries.push_back(e);
   }
   // by address: what is written may not begin before the end of anything, nor what is read
