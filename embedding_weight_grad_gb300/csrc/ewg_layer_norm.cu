@@ -153,6 +153,14 @@ __device__ __forceinline__ void read_vector(const void* p, int bf16, int column,
   else read_vector<float, kE, kPairs>(static_cast<const float*>(p) + column, pitch, count, f);
 }
 
+// A number near a row's mean from which deviations are taken.  bf16 elements less a number of more than
+// bf16's digits would all be rounded the same way, and their sum be off by as much; less one of bf16 they
+// are exact, and their squares' mean is at least twice the square of theirs.
+template <typename T>
+__device__ __forceinline__ float centre_of(float mean) {
+  return sizeof(T) == 2 ? __bfloat162float(__float2bfloat16_rn(mean)) : mean;
+}
+
 // Sum of pairs, by halves.
 template <int kN>
 __device__ __forceinline__ float pairs_sum(const float2* f) {
@@ -351,7 +359,7 @@ __global__ void __launch_bounds__(kStreamThreads) norm_stream_kernel(const NormS
     team_sum<kR, kTeam>(sums, slots, s.team, s.threads);
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
-      sums[r] *= a.inv_h;
+      sums[r] = centre_of<T>(sums[r] * a.inv_h);
       float2 squares[kPairs];
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) {
@@ -365,7 +373,7 @@ __global__ void __launch_bounds__(kStreamThreads) norm_stream_kernel(const NormS
     team_sum<2 * kR, kTeam>(pair_sums, slots + kR * 32, s.team, s.threads);
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
-      // sums[r] is the mean but for its rounding, which the deviations' own mean shows
+      // what sums[r] is off the mean, the deviations' own mean shows
       const float rest = pair_sums[r] * a.inv_h, square = pair_sums[kR + r];
       const float var = fmaxf(fmaf(-rest, rest, square * a.inv_h), 0.0f);
       const float rstd = square != square ? square : 1.0f / sqrtf(var + a.eps);
@@ -542,7 +550,7 @@ __global__ void __launch_bounds__(kRowThreads) norm_kernel(NormArgs a) {
   T* out = static_cast<T*>(a.out) + row * a.out_stride;
   float2 s = make_float2(0.0f, 0.0f);
   for (int j = threadIdx.x; j < a.H; j += kRowThreads) s.x += load(x + j);
-  const float near = block_sum<kRowThreads>(s).x * a.inv_h;
+  const float near = centre_of<T>(block_sum<kRowThreads>(s).x * a.inv_h);
   s = make_float2(0.0f, 0.0f);
   for (int j = threadIdx.x; j < a.H; j += kRowThreads) {
     const float d = load(x + j) - near;
@@ -550,7 +558,7 @@ __global__ void __launch_bounds__(kRowThreads) norm_kernel(NormArgs a) {
     s.y = fmaf(d, d, s.y);
   }
   s = block_sum<kRowThreads>(s);
-  // `near` is the mean but for its rounding, which the deviations' own mean shows
+  // what `near` is off the mean, the deviations' own mean shows
   const float rest = s.x * a.inv_h;
   const float var = fmaxf(fmaf(-rest, rest, s.y * a.inv_h), 0.0f);
   const float rstd = s.y != s.y ? s.y : 1.0f / sqrtf(var + a.eps);
