@@ -640,33 +640,38 @@ class LayerNorm(NamedTuple):
     rstd: torch.Tensor             # 1 / sqrt(variance + eps)
 
 
-def _norm_rows(name, what, x, shape, dtype, index):
-    """The row stride of x, whose shape, dtype and device have to be these."""
-    if x.shape != shape or x.dtype != dtype or x.get_device() != index:
-        raise ValueError(f"{name} does not support these tensors: {what} must have x's shape, dtype "
-                         "and device")
-    H = shape[-1]
-    return _row_stride(name, what, x, x.numel() // H, H)
-
-
-def _norm_vectors(name, what, vectors, H, index):
-    """(pointers, dtype code) of vectors [H], some of them None."""
-    given = [v for v in vectors if v is not None]
-    for v in given:
-        if v.shape != (H,) or v.dtype not in _FLOAT_CODES or v.dtype != given[0].dtype \
-                or v.get_device() != index or not v.is_contiguous():
-            raise ValueError(f"{name} does not support these tensors: {what} must be contiguous [hidden] "
-                             "vectors of one dtype, bf16/fp32, on x's device")
-    return [None if v is None else v.data_ptr() for v in vectors], \
-        _FLOAT_CODES[given[0].dtype] if given else _FP32
-
-
 def _norm_input(name, x):
-    index = x.get_device()
-    if index < 0 or x.dtype not in _FLOAT_CODES or x.dim() == 0 or x.shape[-1] == 0:
+    """(device index, shape, hidden, rows, row stride, dtype code) of x [..., hidden]."""
+    index, shape, code = x.get_device(), x.shape, _FLOAT_CODES.get(x.dtype)
+    H = shape[-1] if shape else 0
+    if index < 0 or code is None or H == 0:
         raise ValueError(f"{name} does not support these tensors: x must be [..., hidden], bf16/fp32, "
                          "on a CUDA device")
-    return index, x.shape
+    n = x.numel() // H
+    return index, shape, H, n, _row_stride(name, "x", x, n, H), code
+
+
+def _norm_rows(name, what, y, x, n, H):
+    """The row stride of y, which has x's shape, dtype and device."""
+    if y.shape != x.shape or y.dtype != x.dtype or y.get_device() != x.get_device():
+        raise ValueError(f"{name} does not support these tensors: {what} must have x's shape, dtype "
+                         "and device")
+    return _row_stride(name, what, y, n, H)
+
+
+def _norm_vectors(name, what, v, w, H, index):
+    """(pointer of v, pointer of w, dtype code) of two vectors [H], each of which may be None."""
+    pv = pw = dtype = None
+    if v is not None:
+        pv, dtype = v.data_ptr(), v.dtype
+    if w is not None:
+        pw, dtype = w.data_ptr(), dtype or w.dtype
+    for t in (v, w):
+        if t is not None and (t.dtype != dtype or dtype not in _FLOAT_CODES or t.shape != (H,)
+                              or t.get_device() != index or not t.is_contiguous()):
+            raise ValueError(f"{name} does not support these tensors: {what} must be contiguous [hidden] "
+                             "vectors of one dtype, bf16/fp32, on x's device")
+    return pv, pw, _FLOAT_CODES.get(dtype, _FP32)
 
 
 def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
@@ -681,20 +686,17 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
 
     The results carry no autograd graph: their gradient is layer_norm_backward.
     """
-    index, shape = _norm_input("layer_norm", x)
-    H = shape[-1]
-    n = x.numel() // H
-    stride = _row_stride("layer_norm", "x", x, n, H)
-    (w, b), code = _norm_vectors("layer_norm", "weight and bias", (weight, bias), H, index)
+    index, shape, H, n, stride, x_code = _norm_input("layer_norm", x)
+    w, b, code = _norm_vectors("layer_norm", "weight and bias", weight, bias, H, index)
     given = out is not None
-    if not given:
-        out, out_stride = torch.empty(shape, dtype=x.dtype, device=x.device), H
+    if given:
+        out_stride = _norm_rows("layer_norm", "out", out, x, n, H)
     else:
-        out_stride = _norm_rows("layer_norm", "out", out, shape, x.dtype, index)
+        out, out_stride = torch.empty(shape, dtype=x.dtype, device=x.device), H
     mean = torch.empty(shape[:-1], dtype=torch.float32, device=x.device)
     rstd = torch.empty_like(mean)
-    _enqueue(index, lib().ewg_layer_norm, x.data_ptr(), _FLOAT_CODES[x.dtype], n, H, stride, w, b, code,
-             eps, out.data_ptr(), out_stride, mean.data_ptr(), rstd.data_ptr())
+    _enqueue(index, lib().ewg_layer_norm, x.data_ptr(), x_code, n, H, stride, w, b, code, eps,
+             out.data_ptr(), out_stride, mean.data_ptr(), rstd.data_ptr())
     if given:
         _written(out)
     return LayerNorm(out, mean, rstd)
@@ -728,29 +730,32 @@ def layer_norm_backward(grad: torch.Tensor, x: torch.Tensor, mean: torch.Tensor,
     stream; the same call gives the same bits.
     """
     name = "layer_norm_backward"
-    index, shape = _norm_input(name, x)
-    H = shape[-1]
-    n = x.numel() // H
-    x_stride = _row_stride(name, "x", x, n, H)
-    grad_stride = _norm_rows(name, "grad", grad, shape, x.dtype, index)
+    index, shape, H, n, x_stride, x_code = _norm_input(name, x)
+    grad_stride = _norm_rows(name, "grad", grad, x, n, H)
+    lead = shape[:-1]
     for t in (mean, rstd):
-        if t.shape != shape[:-1] or t.dtype != torch.float32 or t.get_device() != index or not t.is_contiguous():
+        if t.shape != lead or t.dtype != torch.float32 or t.get_device() != index or not t.is_contiguous():
             raise ValueError("mean and rstd must be contiguous fp32 tensors of x.shape[:-1] on x's device")
-    (w,), w_code = _norm_vectors(name, "weight", (weight,), H, index)
-    main_grads, m_code = _norm_vectors(name, "main_grads", (weight_main_grad, bias_main_grad), H, index)
+    w, _, w_code = _norm_vectors(name, "weight", weight, None, H, index)
+    mg_w, mg_b, m_code = _norm_vectors(name, "main_grads", weight_main_grad, bias_main_grad, H, index)
     given = out is not None
-    if not given:
-        out, out_stride = torch.empty(shape, dtype=x.dtype, device=x.device), H
+    if given:
+        out_stride = _norm_rows(name, "out", out, x, n, H)
     else:
-        out_stride = _norm_rows(name, "out", out, shape, x.dtype, index)
+        out, out_stride = torch.empty(shape, dtype=x.dtype, device=x.device), H
     if n == 0:
         return out
-    ws = workspace if workspace is not None else layer_norm_workspace(shape, x.device)
-    _enqueue(index, lib().ewg_layer_norm_backward, grad.data_ptr(), grad_stride, x.data_ptr(), x_stride,
-             _FLOAT_CODES[x.dtype], n, H, mean.data_ptr(), rstd.data_ptr(), w, w_code, out.data_ptr(),
-             out_stride, *main_grads, m_code, ws.data_ptr(), ws.numel())
-    for t, written in ((out, given), (weight_main_grad, True), (bias_main_grad, True)):
-        if written and t is not None:
+    L = lib()
+    if workspace is None:
+        nbytes = L.ewg_layer_norm_workspace_bytes(n, H)
+        if nbytes == 0:
+            raise EwgError(ERR_UNSUPPORTED, "unsupported sizes")
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    _enqueue(index, L.ewg_layer_norm_backward, grad.data_ptr(), grad_stride, x.data_ptr(), x_stride,
+             x_code, n, H, mean.data_ptr(), rstd.data_ptr(), w, w_code, out.data_ptr(), out_stride,
+             mg_w, mg_b, m_code, workspace.data_ptr(), workspace.numel())
+    for t, written in ((out, given), (weight_main_grad, mg_w), (bias_main_grad, mg_b)):
+        if written:
             _written(t)
     return out
 
@@ -760,6 +765,9 @@ class _AdamWTensor(ctypes.Structure):
                 ("exp_avg_sq", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("copy", ctypes.c_void_p),
                 ("count", ctypes.c_int64), ("weight_decay", ctypes.c_double),
                 ("param_dtype", ctypes.c_int), ("grad_dtype", ctypes.c_int)]
+
+
+_data_ptr = torch.Tensor.data_ptr
 
 
 class AdamWPlan:
@@ -779,10 +787,11 @@ class AdamWPlan:
         self._index = index
         self._all = [t for group in (params, grads, exp_avg, exp_avg_sq, scales or (), copies or ())
                      for t in group if t is not None]
-        self._addresses = [t.data_ptr() for t in self._all]
+        self._addresses = list(map(_data_ptr, self._all))
         self._written = [t for group in (params, exp_avg, exp_avg_sq, scales or (), copies or ())
                          for t in group if t is not None]
-        self._buffer = None
+        self._buffer = None            # of ewg_adamw_plan, and its bytes
+        self._bytes = 0
 
 
 def _state_list(name, given, params, dtype, shapes):
@@ -851,10 +860,10 @@ def adamw_plan(params, grads, *, state_bits: int = 32, copies=None, weight_decay
         t.param_dtype, t.grad_dtype = _FLOAT_CODES[params[k].dtype], _FLOAT_CODES[grads[k].dtype]
         table[k] = t
     nbytes = int(L.ewg_adamw_plan_bytes(len(params)))
-    plan._buffer = (ctypes.c_uint64 * (nbytes // 8 + 1))()
+    plan._buffer, plan._bytes = (ctypes.c_uint64 * (nbytes // 8 + 1))(), nbytes
     if params:
         with torch.cuda.device(index):
-            _raise_on(L.ewg_adamw_plan(table, len(params), state_bits, plan._buffer, ctypes.sizeof(plan._buffer)))
+            _raise_on(L.ewg_adamw_plan(table, len(params), state_bits, plan._buffer, nbytes))
     return plan
 
 
@@ -878,12 +887,12 @@ def adamw_step(plan: AdamWPlan, step, *, lr, betas: tuple = (0.9, 0.999), eps: f
     """
     if not plan.params:
         return
-    if [t.data_ptr() for t in plan._all] != plan._addresses:
+    if list(map(_data_ptr, plan._all)) != plan._addresses:
         raise ValueError("a tensor of the plan has moved to another address: make a new plan")
     index = plan._index
     step, step_ptr = _scalar("step", step, torch.int64, index)
     lr, lr_ptr = _scalar("lr", lr, torch.float32, index)
     grad_scale, scale_ptr = _scalar("grad_scale", grad_scale, torch.float32, index)
-    _enqueue(index, lib().ewg_adamw_step, plan._buffer, ctypes.sizeof(plan._buffer), step, step_ptr, lr, lr_ptr,
+    _enqueue(index, lib().ewg_adamw_step, plan._buffer, plan._bytes, step, step_ptr, lr, lr_ptr,
              *betas, eps, grad_scale, scale_ptr)
     _written(plan._written)

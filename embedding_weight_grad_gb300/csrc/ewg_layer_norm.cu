@@ -8,6 +8,7 @@
 //
 //     dx = rstd (u - avg(u) - n avg(u n))     dw_j = sum over rows of g n     db_j = sum over rows of g
 #include <atomic>
+#include <cfloat>
 
 #include <cuda_bf16.h>
 
@@ -159,6 +160,13 @@ __device__ __forceinline__ void read_vector(const void* p, int bf16, int column,
 template <typename T>
 __device__ __forceinline__ float centre_of(float mean) {
   return sizeof(T) == 2 ? __bfloat162float(__float2bfloat16_rn(mean)) : mean;
+}
+
+// 1 / standard deviation from the averages of the deviations from some centre and of their squares; NaN where
+// an element is not finite.
+__device__ __forceinline__ float rstd_of(float rest, float square, float eps) {
+  const float var = fmaxf(fmaf(-rest, rest, square), 0.0f);
+  return square <= FLT_MAX ? 1.0f / sqrtf(var + eps) : square - square;
 }
 
 // Sum of pairs, by halves.
@@ -350,36 +358,34 @@ __global__ void __launch_bounds__(kStreamThreads) norm_stream_kernel(const NormS
   for (; turn < s.n; turn += s.step, row += s.step, to += a.out.advance) {
     const int stage = s.next(a.x);
     float2 d[kR][kPairs];
-    float sums[kR], pair_sums[2 * kR];
+    float centre[kR], sums[2 * kR];
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
       s.read(stage, r, 0, d[r]);
-      sums[r] = pairs_sum<kPairs>(d[r]);
+      centre[r] = pairs_sum<kPairs>(d[r]);
     }
-    team_sum<kR, kTeam>(sums, slots, s.team, s.threads);
+    team_sum<kR, kTeam>(centre, slots, s.team, s.threads);
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
-      sums[r] = centre_of<T>(sums[r] * a.inv_h);
+      centre[r] = centre_of<T>(centre[r] * a.inv_h);
       float2 squares[kPairs];
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) {
         // what lies behind the row stays 0
-        d[r][i] = sub2(d[r][i], make_float2(2 * i / kE < s.count ? sums[r] : 0.0f, (2 * i + 1) / kE < s.count ? sums[r] : 0.0f));
+        d[r][i] = sub2(d[r][i], make_float2(2 * i / kE < s.count ? centre[r] : 0.0f, (2 * i + 1) / kE < s.count ? centre[r] : 0.0f));
         squares[i] = mul2(d[r][i], d[r][i]);
       }
-      pair_sums[r] = pairs_sum<kPairs>(d[r]);
-      pair_sums[kR + r] = pairs_sum<kPairs>(squares);
+      sums[r] = pairs_sum<kPairs>(d[r]);
+      sums[kR + r] = pairs_sum<kPairs>(squares);
     }
-    team_sum<2 * kR, kTeam>(pair_sums, slots + kR * 32, s.team, s.threads);
+    team_sum<2 * kR, kTeam>(sums, slots + kR * 32, s.team, s.threads);
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
-      // what sums[r] is off the mean, the deviations' own mean shows
-      const float rest = pair_sums[r] * a.inv_h, square = pair_sums[kR + r];
-      const float var = fmaxf(fmaf(-rest, rest, square * a.inv_h), 0.0f);
-      const float rstd = square != square ? square : 1.0f / sqrtf(var + a.eps);
+      // what the centre is off the mean, the deviations' own mean shows
+      const float rest = sums[r] * a.inv_h, rstd = rstd_of(rest, sums[kR + r] * a.inv_h, a.eps);
       if (row + r >= s.n) break;
       if (s.thread == 0) {
-        a.mean[row + r] = sums[r] + rest;
+        a.mean[row + r] = centre[r] + rest;
         a.rstd[row + r] = rstd;
       }
       const float shift = -rest * rstd;
@@ -504,9 +510,12 @@ __global__ void __launch_bounds__(kStreamThreads) norm_grad_stream_kernel(const 
       }
     } else {
 #pragma unroll
-      for (int c = 0; c < kColumns; ++c) {
+      for (int c = 0; c < kColumns; c += kE < 4 ? 1 : 4) {
         const int j = s.column(c / kE) + c % kE;
-        if (j < a.H) out[half * a.H + j] = mine[c];
+        if (j >= a.H) continue;
+        // (rows whose vectors move whole have a multiple of four elements, and shares lie at 256 bytes)
+        if constexpr (kE >= 4) *reinterpret_cast<float4*>(out + half * a.H + j) = make_float4(mine[c], mine[c + 1], mine[c + 2], mine[c + 3]);
+        else out[half * a.H + j] = mine[c];
       }
     }
   }
@@ -560,8 +569,7 @@ __global__ void __launch_bounds__(kRowThreads) norm_kernel(NormArgs a) {
   s = block_sum<kRowThreads>(s);
   // what `near` is off the mean, the deviations' own mean shows
   const float rest = s.x * a.inv_h;
-  const float var = fmaxf(fmaf(-rest, rest, s.y * a.inv_h), 0.0f);
-  const float rstd = s.y != s.y ? s.y : 1.0f / sqrtf(var + a.eps);
+  const float rstd = rstd_of(rest, s.y * a.inv_h, a.eps);
   if (threadIdx.x == 0) {
     a.mean[row] = near + rest;
     a.rstd[row] = rstd;
@@ -614,30 +622,37 @@ __global__ void __launch_bounds__(kRowThreads) norm_grad_columns_kernel(NormGrad
   p[a.H + j] = db;
 }
 
-// The blocks' shares of a column's sums, joined by eight threads a column in an order that depends on their
+// The blocks' shares of a column's sums, joined by sixteen threads a column in an order that depends on their
 // number alone, and added to the main_grad.
-__global__ void __launch_bounds__(256) norm_grad_join_kernel(const NormGradArgs a) {
-  ptx::pdl_wait_prior_grid();
-  __shared__ float sums[8][33];
+constexpr int kJoinGroups = 16;
+
+__global__ void __launch_bounds__(32 * kJoinGroups) norm_grad_join_kernel(const NormGradArgs a) {
+  __shared__ float sums[kJoinGroups][33];
   const int lane = threadIdx.x % 32, group = threadIdx.x / 32;
   const int j = blockIdx.x * 32 + lane;
   void* to = blockIdx.y == 0 ? a.weight_main_grad : a.bias_main_grad;
   if (!to) return;
-  float s = 0.0f;
-  if (j < a.H) {
-    const float* p = a.partial + static_cast<long long>(blockIdx.y) * a.H + j;
-#pragma unroll 4
-    for (int part = group; part < a.parts; part += 8) s += p[static_cast<long long>(part) * 2 * a.H];
+  ptx::pdl_wait_prior_grid();
+  constexpr int kMost = (kNormParts + kJoinGroups - 1) / kJoinGroups;
+  float v[kMost];
+  const float* p = a.partial + static_cast<long long>(blockIdx.y) * a.H + j;
+#pragma unroll
+  for (int i = 0; i < kMost; ++i) {
+    const int part = group + i * kJoinGroups;
+    v[i] = j < a.H && part < a.parts ? p[static_cast<long long>(part) * 2 * a.H] : 0.0f;
   }
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kMost; ++i) s += v[i];
   sums[group][lane] = s;
   __syncthreads();
   if (group || j >= a.H) return;
   s = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s += sums[i][lane];
+  for (int i = 0; i < kJoinGroups; ++i) s += sums[i][lane];
   if (a.main_grad_bf16) {
-    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(to) + j;
-    store(p, load(p) + s);
+    __nv_bfloat16* q = static_cast<__nv_bfloat16*>(to) + j;
+    store(q, load(q) + s);
   } else {
     static_cast<float*>(to)[j] += s;
   }
@@ -647,7 +662,7 @@ cudaError_t launch_join(const NormGradArgs& a, cudaStream_t stream) {
   if (!a.weight_main_grad && !a.bias_main_grad) return cudaGetLastError();
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((a.H + 31) / 32, 2);
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(32 * kJoinGroups);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -693,12 +708,11 @@ cudaError_t allow_shared(K kernel, std::atomic<bool> (&done)[kMaxDevices], int d
   return e;
 }
 
-// Rows of a batch and stages, by what fits into registers and shared memory: 64 bytes of an array's
-// batch a thread.
+// Rows of a batch, 64 bytes of each array a thread, and stages, by what fits into registers and shared memory.
 template <typename T, int kColumns>
 constexpr int batch_rows() { return 64 / (kColumns * static_cast<int>(sizeof(T))); }
 template <typename T, int kE>
-constexpr int stages(int arrays) { return kE * sizeof(T) == 2 ? 1 : arrays == 1 ? 4 : 3; }
+constexpr int stages(int arrays) { return kE * sizeof(T) == 2 ? 1 : sizeof(T) == 4 && arrays == 1 ? 4 : 3; }
 
 template <typename T, int kE, int kColumns, int kTeam>
 cudaError_t launch_stream(const NormArgs& a, cudaStream_t stream) {

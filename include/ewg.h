@@ -407,8 +407,8 @@ int ewg_orthogonalize_transposed(const void* grad, int grad_dtype, int64_t batch
  *           x itself (same address and stride), which it then replaces
  *   mean, rstd       [rows] fp32
  *
- * A row with a NaN or an infinity gives NaN.  Squared deviations are summed in fp32 and must
- * stay in its range.  A row of equal elements has rstd 1 / sqrt(eps); with eps = 0 its results
+ * A row with a NaN or an infinity gives NaN, and so does one whose squared deviations' sum, in
+ * fp32, leaves its range.  A row of equal elements has rstd 1 / sqrt(eps); with eps = 0 its results
  * mean nothing.
  *
  * Requires 0 <= rows < 2^31 (0: nothing is enqueued), 1 <= hidden <= EWG_MAX_HIDDEN, finite
