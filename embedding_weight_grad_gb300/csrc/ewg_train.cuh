@@ -55,7 +55,7 @@ struct NormGradLayout {
 };
 
 constexpr int kNormParts = 152;       // shares of the rows, at most
-constexpr int kNormPartRows = 16;     // rows of a share, at least, where that leaves several
+constexpr int kNormPartRows = 2;     // rows of a share, at least, where that leaves several
 
 inline NormGradLayout make_norm_grad_layout(int64_t n, int64_t H) {
   NormGradLayout L{};
