@@ -228,10 +228,33 @@ __device__ __forceinline__ void team_sum(float (&v)[kM], float* slots, int team,
   }
 }
 
-// ---- rows of up to 8192 elements, copied ahead into shared memory
+// Sums of kM numbers over the blocks of a cluster, all threads of each having its own; `box` [2][kMostBlocks][kM]
+// is in every block's shared memory, its halves taken in turn, so that one barrier is enough.
+constexpr int kMostBlocks = 8;          // of a cluster, as many as any device runs
+
+template <int kM, int kBox>
+__device__ __forceinline__ void cluster_sum(float (&v)[kM], float (&box)[2][kMostBlocks][kBox], int& flip, int blocks, int rank) {
+  static_assert(kM <= kBox);
+  if (threadIdx.x < blocks) {
+    const uint32_t to = ptx::map_to_rank(ptx::smem_u32(&box[flip][rank][0]), threadIdx.x);
+#pragma unroll
+    for (int i = 0; i < kM; ++i) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 4 * i), "f"(v[i]) : "memory");
+  }
+  ptx::cluster_sync_all();
+#pragma unroll
+  for (int i = 0; i < kM; ++i) v[i] = 0.0f;
+  for (int b = 0; b < blocks; ++b)
+#pragma unroll
+    for (int i = 0; i < kM; ++i) v[i] += box[flip][b][i];
+  flip ^= 1;
+}
+
+// ---- rows that a block holds (or, for the gradient of those of more than 8192 elements, a cluster of up to
+// eight), copied ahead into shared memory
 
 constexpr int kStreamThreads = 512;                        // of a block, at most; it is the only one of its SM
 constexpr int kStreamHidden = 8192;
+static_assert(kStreamHidden * kMostBlocks == kNormHeld);
 
 // Of an array of rows: its first element, and the bytes from a row to the next one and from a team's batch
 // to its next one.
@@ -244,37 +267,43 @@ struct Rows {
 // time, and of the batches after that one kStages - 1 are on their way: every thread copies what it will read
 // itself (kArrays arrays' rows), so that the copies need no barrier.  Where an element is too
 // small for an asynchronous copy (odd rows of bf16), kStages is 1 and a batch is read when its turn comes.
+// A cluster's blocks are one team, each with the columns from `lead` on.
 template <typename T, int kE, int kColumns, int kR, int kArrays, int kStages, int kTeam>
 struct Stream {
   static constexpr int kPairs = kColumns / 2;
   static constexpr int kK = kColumns / kE, kBytes = kE * static_cast<int>(sizeof(T));
-  int threads, teams, team, thread;
+  int threads, teams, team, thread, lead, group;      // (group: which of the grid's blocks or clusters)
   int count;                         // of the thread's kK accesses to a row those that lie in it
   uint32_t n, row, step;             // rows; the first row of the team's next batch to be copied; rows of all teams' batches
   const char* from[kArrays];         // of `row`, the thread's first access
   char* ring;
   int stage = 0;
 
-  __device__ __forceinline__ Stream(int team_threads, int rows, int H, char* shared) {
+  __device__ __forceinline__ Stream(int team_threads, int rows, int H, int blocks, char* shared) {
     n = rows;
+    const int rank = blocks > 1 ? static_cast<int>(ptx::cluster_rank()) : 0;
+    const int share = (H / kE + blocks - 1) / blocks;       // accesses of a block
+    group = blockIdx.x / blocks;
+    lead = rank * share * kE;
     threads = kTeam ? kTeam : team_threads;
     teams = blockDim.x / threads;
     team = threadIdx.x / threads;
     thread = threadIdx.x % threads;
-    const int left = H / kE - thread;        // (H is a multiple of kE)
+    const int end = H / kE - rank * share;                  // (H is a multiple of kE)
+    const int left = (end < share ? end : share) - thread;
     count = left > 0 ? (left + threads - 1) / threads : 0;
     ring = shared + threadIdx.x * kBytes;
-    step = gridDim.x * teams * kR;
-    row = (blockIdx.x * teams + team) * kR;
+    step = gridDim.x / blocks * teams * kR;
+    row = (group * teams + team) * kR;
   }
-  __device__ __forceinline__ int column(int k) const { return (k * threads + thread) * kE; }
+  __device__ __forceinline__ int column(int k) const { return lead + (k * threads + thread) * kE; }
   __device__ __forceinline__ int pitch() const { return threads * kE; }
   // The first row of the first team of the thread's warp: teams that share a warp go on together.
   __device__ __forceinline__ uint32_t first() const {
     return row - (kTeam ? team % (32 / (kTeam ? kTeam : 32)) : 0) * kR;
   }
   __device__ __forceinline__ void source(int array, const Rows& rows) {
-    from[array] = rows.p + row * rows.pitch + thread * kBytes;
+    from[array] = rows.p + row * rows.pitch + lead * static_cast<int>(sizeof(T)) + thread * kBytes;
   }
   __device__ __forceinline__ char* place(int st, int r, int array) const {
     return ring + ((st * kR + r) * kArrays + array) * kK * static_cast<int>(blockDim.x) * kBytes;
@@ -342,9 +371,9 @@ __global__ void __launch_bounds__(kStreamThreads) norm_stream_kernel(const NormS
   constexpr int kSlots = kTeam ? 0 : 3 * kR * 32, kPairs = kColumns / 2;
   const int teams = blockDim.x / (kTeam ? kTeam : a.team_threads);
   float* slots = reinterpret_cast<float*>(shared);
-  Stream<T, kE, kColumns, kR, 1, kStages, kTeam> s(a.team_threads, a.n, a.H, reinterpret_cast<char*>(slots + teams * kSlots));
+  Stream<T, kE, kColumns, kR, 1, kStages, kTeam> s(a.team_threads, a.n, a.H, 1, reinterpret_cast<char*>(slots + teams * kSlots));
   uint32_t row = s.row, turn = s.first();
-  char* to = const_cast<char*>(a.out.p) + row * a.out.pitch + s.thread * s.kBytes;
+  char* to = const_cast<char*>(a.out.p) + row * a.out.pitch + s.column(0) * static_cast<int>(sizeof(T));
   s.source(0, a.x[0]);
   s.start(a.x);
   if constexpr (kSlots > 0) {
@@ -396,6 +425,68 @@ __global__ void __launch_bounds__(kStreamThreads) norm_stream_kernel(const NormS
   }
 }
 
+// A block takes one row, 32 elements a thread in registers; several blocks of an SM hide one another's sums.
+constexpr int kBlockThreads = 1024, kBlockPairs = 16;
+constexpr int kBlockHidden = kBlockThreads * 2 * kBlockPairs;
+
+template <typename T, int kE>
+__global__ void __launch_bounds__(kBlockThreads) norm_block_kernel(const NormStream a) {
+  __shared__ float slots[2][2 * 32];
+  const int threads = blockDim.x, thread = threadIdx.x;
+  const int count = thread < a.H / kE ? (a.H / kE - thread + threads - 1) / threads : 0;
+  const long long row = blockIdx.x;
+  const T* x = reinterpret_cast<const T*>(a.x[0].p + row * a.x[0].pitch) + thread * kE;
+  float2 d[kBlockPairs];
+#pragma unroll
+  for (int i = 0; i < kBlockPairs; ++i) d[i] = both(0.0f);
+#pragma unroll
+  for (int k = 0; k < 2 * kBlockPairs / kE; ++k) {
+    if (k >= count) continue;
+    if constexpr (kE == 1) (k % 2 ? d[k / 2].y : d[k / 2].x) = load(x + k * threads);
+    else Access<T, kE>::unpack(*reinterpret_cast<const typename Access<T, kE>::Raw*>(x + k * threads * kE), d + k * kE / 2);
+  }
+  if (thread < 2 * 32) slots[0][thread] = slots[1][thread] = 0.0f;
+  __syncthreads();
+  float centre[1] = {pairs_sum<kBlockPairs>(d)}, sums[2];
+  team_sum<1, 0>(centre, slots[0], 0, threads);
+  centre[0] = centre_of<T>(centre[0] * a.inv_h);
+  float2 squares = both(0.0f);
+#pragma unroll
+  for (int i = 0; i < kBlockPairs; ++i) {
+    d[i] = sub2(d[i], make_float2(2 * i / kE < count ? centre[0] : 0.0f, (2 * i + 1) / kE < count ? centre[0] : 0.0f));
+    squares = fma2(d[i], d[i], squares);
+  }
+  sums[0] = pairs_sum<kBlockPairs>(d);
+  sums[1] = squares.x + squares.y;
+  team_sum<2, 0>(sums, slots[1], 0, threads);
+  const float rest = sums[0] * a.inv_h, rstd = rstd_of(rest, sums[1] * a.inv_h, a.eps), shift = -rest * rstd;
+  if (thread == 0) {
+    a.mean[row] = centre[0] + rest;
+    a.rstd[row] = rstd;
+  }
+  T* out = reinterpret_cast<T*>(const_cast<char*>(a.out.p) + row * a.out.pitch) + thread * kE;
+#pragma unroll
+  for (int k = 0; k < 2 * kBlockPairs / kE; ++k) {
+    if (k >= count) continue;
+    constexpr int kP = kE > 1 ? kE / 2 : 1;
+    float2 w[kP], b[kP], y[kP];
+#pragma unroll
+    for (int i = 0; i < kP; ++i) w[i] = both(1.0f), b[i] = both(0.0f);
+    const int j = (k * threads + thread) * kE;
+    if (a.weight && a.weight_bf16) vector_part<__nv_bfloat16, kE>(static_cast<const __nv_bfloat16*>(a.weight) + j, w);
+    else if (a.weight) vector_part<float, kE>(static_cast<const float*>(a.weight) + j, w);
+    if (a.bias && a.weight_bf16) vector_part<__nv_bfloat16, kE>(static_cast<const __nv_bfloat16*>(a.bias) + j, b);
+    else if (a.bias) vector_part<float, kE>(static_cast<const float*>(a.bias) + j, b);
+#pragma unroll
+    for (int i = 0; i < kP; ++i) {
+      const float2 v = kE > 1 ? d[k * kP + i] : both(k % 2 ? d[k / 2].y : d[k / 2].x);
+      y[i] = fma2(fma2(v, both(rstd), both(shift)), w[i], b[i]);
+    }
+    if constexpr (kE == 1) store(out + k * threads, y[0].x);
+    else *reinterpret_cast<typename Access<T, kE>::Raw*>(out + k * threads * kE) = Access<T, kE>::pack(y);
+  }
+}
+
 struct NormGradStream {
   Rows in[2];                // x, grad
   Rows grad_x;
@@ -404,23 +495,26 @@ struct NormGradStream {
   const float* rstd;
   float* partial;            // null: no sums
   int weight_bf16, n, H, team_threads;
+  int blocks;                // of a cluster
   float inv_h;
 };
 
 // A block's teams take batches in turn, a thread the same columns of every row: their weights and the sums
 // for the main_grads stay in its registers.
-template <typename T, int kE, int kColumns, int kR, int kStages, int kTeam>
+template <typename T, int kE, int kColumns, int kR, int kStages, int kTeam, bool kCluster>
 __global__ void __launch_bounds__(kStreamThreads) norm_grad_stream_kernel(const NormGradStream a) {
   extern __shared__ float4 shared[];
+  __shared__ float box[2][kCluster ? kMostBlocks : 1][kCluster ? 2 * kR : 1];
+  const int blocks = kCluster ? a.blocks : 1;
   ptx::pdl_launch_dependents();
   // two batches' slots for every team, then the ring
   constexpr int kSlots = kTeam ? 0 : 2 * 2 * kR * 32, kPairs = kColumns / 2;
   using S = Stream<T, kE, kColumns, kR, 2, kStages, kTeam>;
   const int teams = blockDim.x / (kTeam ? kTeam : a.team_threads);
   float* slots = reinterpret_cast<float*>(shared);
-  S s(a.team_threads, a.n, a.H, reinterpret_cast<char*>(slots + teams * kSlots));
+  S s(a.team_threads, a.n, a.H, blocks, reinterpret_cast<char*>(slots + teams * kSlots));
   uint32_t row = s.row, turn = s.first();
-  char* to = const_cast<char*>(a.grad_x.p) + row * a.grad_x.pitch + s.thread * s.kBytes;
+  char* to = const_cast<char*>(a.grad_x.p) + row * a.grad_x.pitch + s.column(0) * static_cast<int>(sizeof(T));
   s.source(0, a.in[0]);
   s.source(1, a.in[1]);
   s.start(a.in);
@@ -433,6 +527,8 @@ __global__ void __launch_bounds__(kStreamThreads) norm_grad_stream_kernel(const 
     }
   };
   moments(row);
+  int box_flip = 0;
+  if constexpr (kCluster) ptx::cluster_sync_all();         // (all blocks are there before their memory is written)
   if constexpr (kSlots > 0) {
     for (int i = threadIdx.x; i < teams * kSlots; i += blockDim.x) slots[i] = 0.0f;
     __syncthreads();
@@ -466,6 +562,7 @@ __global__ void __launch_bounds__(kStreamThreads) norm_grad_stream_kernel(const 
       sums[kR + r] = s2.x + s2.y;
     }
     team_sum<2 * kR, kTeam>(sums, slots + flip * 2 * kR * 32, s.team, s.threads);
+    if constexpr (kCluster) cluster_sum(sums, box, box_flip, blocks, static_cast<int>(ptx::cluster_rank()));
     // the rows are read again rather than kept: registers hold the columns' sums
     asm volatile("" ::: "memory");
 #pragma unroll
@@ -486,7 +583,7 @@ __global__ void __launch_bounds__(kStreamThreads) norm_grad_stream_kernel(const 
   }
   if (!a.partial) return;
   // the teams' sums, in their order, to the block's share
-  float* out = a.partial + static_cast<long long>(blockIdx.x) * 2 * a.H;
+  float* out = a.partial + static_cast<long long>(s.group) * 2 * a.H;
   float* meet = reinterpret_cast<float*>(shared);
   if constexpr (S::kBytes > 2) ptx::cp_async_wait<0>();        // (the ring is about to be used for them)
 #pragma unroll
@@ -505,14 +602,13 @@ __global__ void __launch_bounds__(kStreamThreads) norm_grad_stream_kernel(const 
       for (int c = s.team; c < kColumns; c += teams) {
         float v = 0.0f;
         for (int t = 0; t < teams; ++t) v += meet[(t * kColumns + c) * s.threads + s.thread];
-        const int j = s.column(c / kE) + c % kE;
-        if (j < a.H) out[half * a.H + j] = v;
+        if (c / kE < s.count) out[half * a.H + s.column(c / kE) + c % kE] = v;
       }
     } else {
 #pragma unroll
       for (int c = 0; c < kColumns; c += kE < 4 ? 1 : 4) {
+        if (c / kE >= s.count) continue;
         const int j = s.column(c / kE) + c % kE;
-        if (j >= a.H) continue;
         // (rows whose vectors move whole have a multiple of four elements, and shares lie at 256 bytes)
         if constexpr (kE >= 4) *reinterpret_cast<float4*>(out + half * a.H + j) = make_float4(mine[c], mine[c + 1], mine[c + 2], mine[c + 3]);
         else out[half * a.H + j] = mine[c];
@@ -675,37 +771,84 @@ cudaError_t launch_join(const NormGradArgs& a, cudaStream_t stream) {
 
 // A launch of one of the two: threads of a team, teams of a block, blocks, shared memory.
 struct StreamShape {
-  int threads, teams, blocks;
+  int threads, teams, blocks, groups;     // blocks: of a cluster; groups: clusters, or blocks by themselves
   size_t bytes;
 };
 
-// team: its threads, or 0 for as many warps as it takes; rows: of a batch; slots: floats for each of a batch's rows of a team of several warps; unit: bytes
-// of the ring for a thread.
-StreamShape make_stream_shape(int n, int H, int team, int columns, int most_blocks, int rows, int slots, int unit) {
+// team: its threads, or 0 for as many warps as it takes; rows: of a batch; slots: floats for each of a batch's
+// rows of a team of several warps; unit: bytes of the ring for a thread.
+StreamShape make_stream_shape(int H, int access, int team, int columns, int rows, int slots, int unit) {
   StreamShape s{};
-  s.threads = team ? team : ((H + columns - 1) / columns + 31) / 32 * 32;
-  s.teams = kStreamThreads / s.threads;
+  s.blocks = 1;
+  while (s.blocks < kMostBlocks && H > s.blocks * kStreamHidden) s.blocks *= 2;
+  const int mine = (H / access + s.blocks - 1) / s.blocks * access;
+  s.threads = team ? team : ((mine + columns - 1) / columns + 31) / 32 * 32;
+  s.teams = s.blocks > 1 ? 1 : kStreamThreads / s.threads;
   if (!team && s.teams > 15) s.teams = 15;                 // named barriers 1 to 15
-  const long long want = (static_cast<long long>(n) + rows * s.teams - 1) / (rows * s.teams);
-  s.blocks = static_cast<int>(want < most_blocks ? want : most_blocks);
   s.bytes = static_cast<size_t>(s.teams) * ((team ? 0 : slots * rows * sizeof(float)) + static_cast<size_t>(s.threads) * unit);
   return s;
 }
 
+// No more groups than rows for all their teams.
+void set_groups(StreamShape& s, int n, int rows, int most) {
+  const long long want = (static_cast<long long>(n) + rows * s.teams - 1) / (rows * s.teams);
+  s.groups = static_cast<int>(want < most ? want : most);
+}
+
 Rows make_rows(const void* p, long long stride, size_t size, const StreamShape& s, int rows) {
   const long long pitch = stride * static_cast<long long>(size);
-  return {static_cast<const char*>(p), pitch, pitch * s.blocks * s.teams * rows};
+  return {static_cast<const char*>(p), pitch, pitch * s.groups * s.teams * rows};
 }
 
 constexpr int kMaxDevices = 64;
 
-// Lets a kernel have all of an SM's shared memory, once for each device.
+// A kernel's set-up on each device: whether it may have all of an SM's shared memory, and how many of its clusters
+// of 2, 4 and 8 blocks run at once.
+struct StreamSetUp {
+  std::atomic<bool> ready[kMaxDevices];
+  std::atomic<int> clusters[kMaxDevices][4];
+};
+
 template <typename K>
-cudaError_t allow_shared(K kernel, std::atomic<bool> (&done)[kMaxDevices], int dev) {
-  if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-  if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
+cudaError_t set_up(K kernel, StreamSetUp& state, int dev) {
+  if (state.ready[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 225 * 1024);
+  if (e == cudaSuccess) state.ready[dev].store(true, std::memory_order_release);
   return e;
+}
+
+cudaLaunchConfig_t stream_config(const StreamShape& s, cudaLaunchAttribute* attr, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(s.groups * s.blocks);
+  cfg.blockDim = dim3(s.teams * s.threads);
+  cfg.dynamicSmemBytes = s.bytes;
+  cfg.stream = stream;
+  if (s.blocks > 1) {
+    attr->id = cudaLaunchAttributeClusterDimension;
+    attr->val.clusterDim.x = s.blocks;
+    attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+  return cfg;
+}
+
+// Groups that run at once, `sms` of single blocks.
+template <typename K>
+cudaError_t groups_at_once(K kernel, StreamSetUp& state, StreamShape s, int dev, int sms, int* groups) {
+  *groups = sms;
+  if (s.blocks == 1) return cudaSuccess;
+  std::atomic<int>& known = state.clusters[dev][s.blocks / 4];
+  if ((*groups = known.load()) > 0) return cudaSuccess;
+  s.groups = 1;
+  s.bytes = 200 * 1024;                                    // (the same for all sizes: one block an SM)
+  cudaLaunchAttribute attr{};
+  const cudaLaunchConfig_t cfg = stream_config(s, &attr, nullptr);
+  const cudaError_t e = cudaOccupancyMaxActiveClusters(groups, kernel, &cfg);
+  if (e != cudaSuccess) return e;
+  if (*groups < 1) return cudaErrorInvalidConfiguration;
+  known.store(*groups);
+  return cudaSuccess;
 }
 
 // Rows of a batch, 64 bytes of each array a thread, and stages, by what fits into registers and shared memory.
@@ -714,18 +857,10 @@ constexpr int batch_rows() { return 64 / (kColumns * static_cast<int>(sizeof(T))
 template <typename T, int kE>
 constexpr int stages(int arrays) { return kE * sizeof(T) == 2 ? 1 : sizeof(T) == 4 && arrays == 1 ? 4 : 3; }
 
-template <typename T, int kE, int kColumns, int kTeam>
-cudaError_t launch_stream(const NormArgs& a, cudaStream_t stream) {
-  constexpr int kR = batch_rows<T, kColumns>(), kStages = stages<T, kE>(1);
-  static std::atomic<bool> done[kMaxDevices];
-  const auto kernel = norm_stream_kernel<T, kE, kColumns, kR, kStages, kTeam>;
-  const cudaError_t e = allow_shared(kernel, done, a.dev);
-  if (e != cudaSuccess) return e;
-  const StreamShape s = make_stream_shape(a.n, a.H, kTeam, kColumns, a.num_sms, kR, 3 * 32,
-                                          kStages * kR * kColumns * static_cast<int>(sizeof(T)));
+NormStream norm_stream(const NormArgs& a, size_t size, const StreamShape& s, int rows) {
   NormStream k{};
-  k.x[0] = make_rows(a.x, a.x_stride, sizeof(T), s, kR);
-  k.out = make_rows(a.out, a.out_stride, sizeof(T), s, kR);
+  k.x[0] = make_rows(a.x, a.x_stride, size, s, rows);
+  k.out = make_rows(a.out, a.out_stride, size, s, rows);
   k.weight = a.weight;
   k.bias = a.bias;
   k.mean = a.mean;
@@ -736,22 +871,42 @@ cudaError_t launch_stream(const NormArgs& a, cudaStream_t stream) {
   k.team_threads = s.threads;
   k.eps = a.eps;
   k.inv_h = a.inv_h;
-  kernel<<<s.blocks, s.teams * s.threads, s.bytes, stream>>>(k);
-  return cudaGetLastError();
+  return k;
 }
 
 template <typename T, int kE, int kColumns, int kTeam>
+cudaError_t launch_stream(const NormArgs& a, cudaStream_t stream) {
+  constexpr int kR = batch_rows<T, kColumns>(), kStages = stages<T, kE>(1);
+  static StreamSetUp state;
+  const auto kernel = norm_stream_kernel<T, kE, kColumns, kR, kStages, kTeam>;
+  const cudaError_t e = set_up(kernel, state, a.dev);
+  if (e != cudaSuccess) return e;
+  StreamShape s = make_stream_shape(a.H, kE, kTeam, kColumns, kR, 3 * 32, kStages * kR * kColumns * static_cast<int>(sizeof(T)));
+  set_groups(s, a.n, kR, a.num_sms);
+  kernel<<<s.groups, s.teams * s.threads, s.bytes, stream>>>(norm_stream(a, sizeof(T), s, kR));
+  return cudaGetLastError();
+}
+
+template <typename T, int kE>
+cudaError_t launch_block(const NormArgs& a, cudaStream_t stream) {
+  const StreamShape s{((a.H + 2 * kBlockPairs - 1) / (2 * kBlockPairs) + 31) / 32 * 32, 1, 1, 1, 0};
+  norm_block_kernel<T, kE><<<a.n, s.threads, 0, stream>>>(norm_stream(a, sizeof(T), s, 1));
+  return cudaGetLastError();
+}
+
+template <typename T, int kE, int kColumns, int kTeam, bool kCluster = false>
 cudaError_t launch_stream(NormGradArgs a, cudaStream_t stream) {
   constexpr int kR = batch_rows<T, kColumns>(), kStages = stages<T, kE>(2);
-  static std::atomic<bool> done[kMaxDevices];
-  const auto kernel = norm_grad_stream_kernel<T, kE, kColumns, kR, kStages, kTeam>;
-  const cudaError_t e = allow_shared(kernel, done, a.dev);
-  if (e != cudaSuccess) return e;
-  StreamShape s = make_stream_shape(a.n, a.H, kTeam, kColumns, a.parts, kR, 4 * 32,
-                                    kStages * kR * 2 * kColumns * static_cast<int>(sizeof(T)));
+  static StreamSetUp state;
+  const auto kernel = norm_grad_stream_kernel<T, kE, kColumns, kR, kStages, kTeam, kCluster>;
+  StreamShape s = make_stream_shape(a.H, kE, kTeam, kColumns, kR, 4 * 32, kStages * kR * 2 * kColumns * static_cast<int>(sizeof(T)));
   const size_t meet = static_cast<size_t>(s.teams) * s.threads * kColumns * sizeof(float);
   if (s.bytes < meet) s.bytes = meet;
-  a.parts = s.blocks;
+  int most = 0;
+  cudaError_t e = set_up(kernel, state, a.dev);
+  if (e != cudaSuccess || (e = groups_at_once(kernel, state, s, a.dev, a.parts, &most)) != cudaSuccess) return e;
+  set_groups(s, a.n, kR, most < a.parts ? most : a.parts);
+  a.parts = s.groups;
   NormGradStream k{};
   k.in[0] = make_rows(a.x, a.x_stride, sizeof(T), s, kR);
   k.in[1] = make_rows(a.grad, a.grad_stride, sizeof(T), s, kR);
@@ -764,8 +919,11 @@ cudaError_t launch_stream(NormGradArgs a, cudaStream_t stream) {
   k.n = a.n;
   k.H = a.H;
   k.team_threads = s.threads;
+  k.blocks = s.blocks;
   k.inv_h = a.inv_h;
-  kernel<<<s.blocks, s.teams * s.threads, s.bytes, stream>>>(k);
+  cudaLaunchAttribute attr{};
+  const cudaLaunchConfig_t cfg = stream_config(s, &attr, stream);
+  if ((e = cudaLaunchKernelEx(&cfg, kernel, k)) != cudaSuccess) return e;
   return launch_join(a, stream);
 }
 
@@ -784,11 +942,13 @@ cudaError_t by_team(const Args& a, cudaStream_t stream) {
 // gradient, where the columns' sums take the registers (65536 x 256 bf16: 33 us, with eight 23).
 template <typename T, int kE>
 cudaError_t stream_rows(const NormArgs& a, cudaStream_t stream) {
+  if (a.H > kStreamHidden) return launch_block<T, kE>(a, stream);
   if (sizeof(T) == 4 && a.H <= 1024) return by_team<T, kE, 8>(a, stream);
   return by_team<T, kE, 16>(a, stream);
 }
 template <typename T, int kE>
 cudaError_t stream_rows(const NormGradArgs& a, cudaStream_t stream) {
+  if (a.H > kStreamHidden) return launch_stream<T, kE, 16, 0, true>(a, stream);
   if (a.H <= 1024) return by_team<T, kE, 8>(a, stream);
   return launch_stream<T, kE, 16, 0>(a, stream);
 }
@@ -822,7 +982,7 @@ bool moves(const NormGradArgs& a, int elements, size_t size) {
 template <typename T>
 cudaError_t forward(const NormArgs& a, cudaStream_t stream) {
   constexpr int kWhole = 16 / sizeof(T), kWord = 4 / sizeof(T);
-  if (a.H > kStreamHidden) {
+  if (a.H > kBlockHidden) {
     norm_kernel<T><<<a.n, kRowThreads, 0, stream>>>(a);
     return cudaGetLastError();
   }
@@ -834,7 +994,7 @@ cudaError_t forward(const NormArgs& a, cudaStream_t stream) {
 template <typename T>
 cudaError_t grad(const NormGradArgs& a, cudaStream_t stream) {
   constexpr int kWhole = 16 / sizeof(T), kWord = 4 / sizeof(T);
-  if (a.H > kStreamHidden) return grad_loops<T>(a, stream);
+  if (a.H > kNormHeld) return grad_loops<T>(a, stream);
   if (moves(a, kWhole, sizeof(T))) return stream_rows<T, kWhole>(a, stream);
   if (moves(a, kWord, sizeof(T))) return stream_rows<T, kWord>(a, stream);
   return stream_rows<T, 1>(a, stream);

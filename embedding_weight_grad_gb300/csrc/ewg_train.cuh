@@ -43,7 +43,7 @@ struct NormGradArgs {
   void* weight_main_grad;    // [H] of bf16 or fp32, or null
   void* bias_main_grad;
   int main_grad_bf16;
-  float2* row_sums;          // [n]: avg(u) and avg(u n)
+  float2* row_sums;          // [n]: avg(u) and avg(u n), for rows of more than kNormHeld elements
   float* partial;            // [parts][2][H]: shares of the sums over the rows
   int parts;                 // shares of the rows
   int dev;
@@ -54,6 +54,7 @@ struct NormGradLayout {
   int parts;
 };
 
+constexpr int kNormHeld = 65536;      // elements of a row that the gradient goes through once, at most
 constexpr int kNormParts = 152;       // shares of the rows, at most
 constexpr int kNormPartRows = 2;     // rows of a share, at least, where that leaves several
 
@@ -62,7 +63,7 @@ inline NormGradLayout make_norm_grad_layout(int64_t n, int64_t H) {
   const int64_t want = (n + kNormPartRows - 1) / kNormPartRows;
   L.parts = static_cast<int>(want < kNormParts ? want : kNormParts);
   L.row_sums = 0;
-  L.partial = (static_cast<size_t>(n) * sizeof(float2) + 255) / 256 * 256;
+  L.partial = H > kNormHeld ? (static_cast<size_t>(n) * sizeof(float2) + 255) / 256 * 256 : 0;
   L.total = L.partial + (static_cast<size_t>(L.parts) * 2 * H * sizeof(float) + 255) / 256 * 256;
   return L;
 }

@@ -170,7 +170,7 @@ int ewg_layer_norm(const void* x, int x_dtype, int64_t rows, int64_t hidden, int
   }
   ewg::NormArgs a{};
   a.x = x;
-  a.x_stride = row_stride;
+  a.x_stride = rows > 1 ? row_stride : hidden;
   a.weight = weight;
   a.bias = bias;
   a.weight_bf16 = weight_dtype == EWG_BF16;
@@ -179,7 +179,7 @@ int ewg_layer_norm(const void* x, int x_dtype, int64_t rows, int64_t hidden, int
   a.eps = static_cast<float>(eps);
   a.inv_h = static_cast<float>(1.0 / static_cast<double>(hidden));
   a.out = out;
-  a.out_stride = out_row_stride;
+  a.out_stride = rows > 1 ? out_row_stride : hidden;
   a.mean = mean;
   a.rstd = rstd;
   a.dev = dev;
@@ -234,9 +234,9 @@ int ewg_layer_norm_backward(const void* grad, int64_t grad_row_stride, const voi
   }
   ewg::NormGradArgs a{};
   a.grad = grad;
-  a.grad_stride = grad_row_stride;
+  a.grad_stride = rows > 1 ? grad_row_stride : hidden;
   a.x = x;
-  a.x_stride = x_row_stride;
+  a.x_stride = rows > 1 ? x_row_stride : hidden;
   a.mean = mean;
   a.rstd = rstd;
   a.weight = weight;
@@ -245,7 +245,7 @@ int ewg_layer_norm_backward(const void* grad, int64_t grad_row_stride, const voi
   a.H = static_cast<int>(hidden);
   a.inv_h = static_cast<float>(1.0 / static_cast<double>(hidden));
   a.grad_x = grad_x;
-  a.grad_x_stride = grad_x_row_stride;
+  a.grad_x_stride = rows > 1 ? grad_x_row_stride : hidden;
   a.weight_main_grad = weight_main_grad;
   a.bias_main_grad = bias_main_grad;
   a.main_grad_bf16 = main_grad_dtype == EWG_BF16;

@@ -433,8 +433,8 @@ size_t ewg_layer_norm_workspace_bytes(int64_t rows, int64_t hidden);
  *
  * avg over the row.  Everything is computed and summed in 32 bits; grad_x is rounded once, and
  * a sum over the rows is added to its main_grad element in 32 bits and rounded to the main_grad's
- * dtype.  The order of the sums depends on rows, hidden and the arrays' alignment alone: the
- * same call gives the same bits.
+ * dtype.  The order of the sums depends on rows, hidden, the arrays' alignment and, for hidden above
+ * 8192, the device: the same call gives the same bits.
  *
  *   grad, x    [rows][hidden] of `dtype` (EWG_BF16 or EWG_FP32), unit inner stride, any alignment
  *   mean, rstd [rows] fp32, as ewg_layer_norm left them
@@ -501,7 +501,8 @@ int ewg_adamw_plan(const ewg_adamw_tensor* tensors, int64_t num_tensors, int sta
  *             - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
  *
  * and param is rounded once (a bf16 param without an fp32 master loses changes below half its
- * step).  The copy is the new param in bf16.
+ * step).  The copy is the new param in bf16.  With eps = 0 an element without a gradient so far is
+ * 0 / 0.
  *
  * States in 8 bits: after the step, which uses m and v unrounded, m and sqrt(v) are taken
  * relative to their block's scale, its largest magnitude times fl(1 / 448), and rounded to e4m3:
