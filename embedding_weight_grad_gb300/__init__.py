@@ -640,38 +640,41 @@ class LayerNorm(NamedTuple):
     rstd: torch.Tensor             # 1 / sqrt(variance + eps)
 
 
+# (These calls are often bound by the host, so that their checks are few and taken once.)
 def _norm_input(name, x):
-    """(device index, shape, hidden, rows, row stride, dtype code) of x [..., hidden]."""
-    index, shape, code = x.get_device(), x.shape, _FLOAT_CODES.get(x.dtype)
-    H = shape[-1] if shape else 0
+    """(device index, hidden, rows, row stride, dtype code) of x [..., hidden]."""
+    index, code = x.get_device(), _FLOAT_CODES.get(x.dtype)
+    H = x.shape[-1] if x.dim() else 0
     if index < 0 or code is None or H == 0:
         raise ValueError(f"{name} does not support these tensors: x must be [..., hidden], bf16/fp32, "
                          "on a CUDA device")
     n = x.numel() // H
-    return index, shape, H, n, _row_stride(name, "x", x, n, H), code
+    return index, H, n, H if x.is_contiguous() else _row_stride(name, "x", x, n, H), code
 
 
 def _norm_rows(name, what, y, x, n, H):
     """The row stride of y, which has x's shape, dtype and device."""
-    if y.shape != x.shape or y.dtype != x.dtype or y.get_device() != x.get_device():
+    if y.dtype != x.dtype or y.shape != x.shape or y.get_device() != x.get_device():
         raise ValueError(f"{name} does not support these tensors: {what} must have x's shape, dtype "
                          "and device")
-    return _row_stride(name, what, y, n, H)
+    return H if y.is_contiguous() else _row_stride(name, what, y, n, H)
 
 
 def _norm_vectors(name, what, v, w, H, index):
     """(pointer of v, pointer of w, dtype code) of two vectors [H], each of which may be None."""
-    pv = pw = dtype = None
-    if v is not None:
-        pv, dtype = v.data_ptr(), v.dtype
-    if w is not None:
-        pw, dtype = w.data_ptr(), dtype or w.dtype
-    for t in (v, w):
-        if t is not None and (t.dtype != dtype or dtype not in _FLOAT_CODES or t.shape != (H,)
-                              or t.get_device() != index or not t.is_contiguous()):
-            raise ValueError(f"{name} does not support these tensors: {what} must be contiguous [hidden] "
-                             "vectors of one dtype, bf16/fp32, on x's device")
-    return pv, pw, _FLOAT_CODES.get(dtype, _FP32)
+    if v is None:
+        v, w = w, None
+        if v is None:
+            return None, None, _FP32
+        return (None, *_norm_vectors(name, what, v, None, H, index)[::2])
+    dtype = v.dtype
+    code = _FLOAT_CODES.get(dtype)
+    if code is None or v.shape != (H,) or v.get_device() != index or not v.is_contiguous() or (
+            w is not None and (w.dtype != dtype or w.shape != (H,) or w.get_device() != index
+                               or not w.is_contiguous())):
+        raise ValueError(f"{name} does not support these tensors: {what} must be contiguous [hidden] "
+                         "vectors of one dtype, bf16/fp32, on x's device")
+    return v.data_ptr(), None if w is None else w.data_ptr(), code
 
 
 def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
@@ -686,14 +689,15 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
 
     The results carry no autograd graph: their gradient is layer_norm_backward.
     """
-    index, shape, H, n, stride, x_code = _norm_input("layer_norm", x)
+    index, H, n, stride, x_code = _norm_input("layer_norm", x)
     w, b, code = _norm_vectors("layer_norm", "weight and bias", weight, bias, H, index)
     given = out is not None
     if given:
         out_stride = _norm_rows("layer_norm", "out", out, x, n, H)
     else:
-        out, out_stride = torch.empty(shape, dtype=x.dtype, device=x.device), H
-    mean = torch.empty(shape[:-1], dtype=torch.float32, device=x.device)
+        out_stride = H
+        out = torch.empty_like(x) if stride == H else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
     rstd = torch.empty_like(mean)
     _enqueue(index, lib().ewg_layer_norm, x.data_ptr(), x_code, n, H, stride, w, b, code, eps,
              out.data_ptr(), out_stride, mean.data_ptr(), rstd.data_ptr())
@@ -730,9 +734,9 @@ def layer_norm_backward(grad: torch.Tensor, x: torch.Tensor, mean: torch.Tensor,
     stream; the same call gives the same bits.
     """
     name = "layer_norm_backward"
-    index, shape, H, n, x_stride, x_code = _norm_input(name, x)
+    index, H, n, x_stride, x_code = _norm_input(name, x)
     grad_stride = _norm_rows(name, "grad", grad, x, n, H)
-    lead = shape[:-1]
+    lead = x.shape[:-1]
     for t in (mean, rstd):
         if t.shape != lead or t.dtype != torch.float32 or t.get_device() != index or not t.is_contiguous():
             raise ValueError("mean and rstd must be contiguous fp32 tensors of x.shape[:-1] on x's device")
@@ -742,7 +746,8 @@ def layer_norm_backward(grad: torch.Tensor, x: torch.Tensor, mean: torch.Tensor,
     if given:
         out_stride = _norm_rows(name, "out", out, x, n, H)
     else:
-        out, out_stride = torch.empty(shape, dtype=x.dtype, device=x.device), H
+        out_stride = H
+        out = torch.empty_like(x) if x_stride == H else torch.empty(x.shape, dtype=x.dtype, device=x.device)
     if n == 0:
         return out
     L = lib()
