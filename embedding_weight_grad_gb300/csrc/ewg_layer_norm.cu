@@ -53,8 +53,8 @@ __device__ __forceinline__ uint32_t to_bf16x2(float2 f) {
   return u;
 }
 
-// kE neighbouring elements of a row, which one access moves: 16 bytes where rows allow it, else 4,
-// or a single element.  Arithmetic goes by pairs, two 32-bit operations an instruction.
+// kE neighbouring elements of a row, which one access moves: 16 bytes, or a single element where rows' alignments
+// do not allow that.  Arithmetic goes by pairs, two 32-bit operations an instruction.
 template <typename T, int kE>
 struct Access;
 
@@ -69,12 +69,6 @@ struct Access<__nv_bfloat16, 8> {
   }
 };
 template <>
-struct Access<__nv_bfloat16, 2> {
-  using Raw = uint32_t;
-  static __device__ __forceinline__ void unpack(Raw v, float2* f) { f[0] = from_bf16x2(v); }
-  static __device__ __forceinline__ Raw pack(const float2* f) { return to_bf16x2(f[0]); }
-};
-template <>
 struct Access<float, 4> {
   using Raw = float4;
   static __device__ __forceinline__ void unpack(Raw v, float2* f) {
@@ -82,6 +76,11 @@ struct Access<float, 4> {
   }
   static __device__ __forceinline__ Raw pack(const float2* f) { return make_float4(f[0].x, f[0].y, f[1].x, f[1].y); }
 };
+
+// Element j of a vector of bf16 or fp32.
+__device__ __forceinline__ float element(const void* p, int bf16, int j) {
+  return bf16 ? load(static_cast<const __nv_bfloat16*>(p) + j) : load(static_cast<const float*>(p) + j);
+}
 
 // kE elements of a weight or bias vector of W, as pairs; for one element, in x.
 template <typename W, int kE>
@@ -92,20 +91,17 @@ __device__ __forceinline__ void vector_part(const W* p, float2* f) {
   } else if constexpr (sizeof(W) == 2) {
     alignas(16) uint32_t u[kE / 2];
     if constexpr (kE == 8) *reinterpret_cast<uint4*>(u) = __ldg(reinterpret_cast<const uint4*>(p));
-    else if constexpr (kE == 4) *reinterpret_cast<uint2*>(u) = __ldg(reinterpret_cast<const uint2*>(p));
-    else u[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+    else *reinterpret_cast<uint2*>(u) = __ldg(reinterpret_cast<const uint2*>(p));
 #pragma unroll
     for (int i = 0; i < kE / 2; ++i) f[i] = from_bf16x2(u[i]);
   } else if constexpr (kE == 8) {
     asm("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
         : "=f"(f[0].x), "=f"(f[0].y), "=f"(f[1].x), "=f"(f[1].y), "=f"(f[2].x), "=f"(f[2].y), "=f"(f[3].x), "=f"(f[3].y)
         : "l"(p));
-  } else if constexpr (kE == 4) {
+  } else {
     const float4 v = __ldg(reinterpret_cast<const float4*>(p));
     f[0] = make_float2(v.x, v.y);
     f[1] = make_float2(v.z, v.w);
-  } else {
-    f[0] = __ldg(reinterpret_cast<const float2*>(p));
   }
 }
 
@@ -158,7 +154,7 @@ __device__ __forceinline__ void read_vector(const W* p, int pitch, int count, fl
 }
 // Where there is no vector, its elements are `none`.
 template <int kE, int kPairs>
-__device__ __forceinline__ void read_vector(const void* p, int bf16, int column, int pitch, int count, float none,
+__device__ __forceinline__ void vector_columns(const void* p, int bf16, int column, int pitch, int count, float none,
                                             float2 (&f)[kPairs]) {
 #pragma unroll
   for (int i = 0; i < kPairs; ++i) f[i] = both(none);
@@ -279,44 +275,71 @@ struct Rows {
 // What the two kernels below have in common.  A team of threads takes kR neighbouring rows at a
 // time, and of the batches after that one kStages - 1 are on their way: every thread copies what it will read
 // itself (kArrays arrays' rows), so that the copies need no barrier.  Where an element is too
-// small for an asynchronous copy (odd rows of bf16), kStages is 1 and a batch is read when its turn comes.
+// small for an asynchronous copy (single elements of bf16), kStages is 1 and a batch is read when its turn comes.
 // A cluster's blocks are one team, each with the columns from `lead` on.
-template <typename T, int kE, int kColumns, int kR, int kArrays, int kStages, int kTeam>
+//
+// kShift: rows that begin anywhere, all arrays' alike.  Their places in 16 bytes repeat every `period` rows; a
+// group takes rows of one place only, so that columns stay with their threads.  Accesses begin at the first 16 bytes
+// within the row; the elements before them and behind the last whole one, less than two accesses' together, are
+// the team's first threads' extra ones, one each, which are loaded by themselves a batch ahead.
+template <typename T, int kE, int kColumns, int kR, int kArrays, int kStages, int kTeam, bool kShift>
 struct Stream {
   static constexpr int kPairs = kColumns / 2;
   static constexpr int kK = kColumns / kE, kBytes = kE * static_cast<int>(sizeof(T));
+  static_assert(!kShift || kBytes == 16);
   int threads, teams, team, thread, lead, group;      // (group: which of the grid's blocks or clusters)
   int count;                         // of the thread's kK accesses to a row those that lie in it
+  int period, place_of, head;        // kShift: which of the period's rows are the group's; their elements before the accesses
+  int extra = -1;                    // the column of the thread's extra element
   uint32_t n, row, step;             // rows; the first row of the team's next batch to be copied; rows of all teams' batches
   const char* from[kArrays];         // of `row`, the thread's first access
   char* ring;
   int stage = 0;
 
-  __device__ __forceinline__ Stream(int team_threads, int rows, int H, int blocks, char* shared) {
-    n = rows;
+  __device__ __forceinline__ Stream(int team_threads, int rows, int H, int blocks, int period_, const Rows& like, char* shared) {
     const int rank = blocks > 1 ? static_cast<int>(ptx::cluster_rank()) : 0;
-    const int share = (H / kE + blocks - 1) / blocks;       // accesses of a block
     group = blockIdx.x / blocks;
+    int groups = gridDim.x / blocks, mine = group, accesses = H / kE;       // (without kShift H is a multiple of kE)
+    period = 1, place_of = head = 0, n = rows;
+    if constexpr (kShift) {
+      period = period_;
+      place_of = group % period;
+      groups /= period, mine /= period;
+      n = rows > place_of ? (rows - place_of + period - 1) / period : 0;
+      const int off = static_cast<int>(reinterpret_cast<uintptr_t>(like.p + place_of * like.pitch) % 16) / static_cast<int>(sizeof(T));
+      head = (kE - off) % kE < H ? (kE - off) % kE : H;
+      accesses = (H - head) / kE;
+    }
+    const int share = (accesses + blocks - 1) / blocks;     // accesses of a block
     lead = rank * share * kE;
     threads = kTeam ? kTeam : team_threads;
     teams = blockDim.x / threads;
     team = threadIdx.x / threads;
     thread = threadIdx.x % threads;
-    const int end = H / kE - rank * share;                  // (H is a multiple of kE)
+    const int end = accesses - rank * share;
     const int left = (end < share ? end : share) - thread;
     count = left > 0 ? (left + threads - 1) / threads : 0;
+    if constexpr (kShift) {
+      const int behind = head + accesses * kE;               // (the first column behind the accesses)
+      if (thread < head) extra = thread;
+      else if (thread < head + H - behind) extra = behind + thread - head;
+    }
     ring = shared + threadIdx.x * kBytes;
-    step = gridDim.x / blocks * teams * kR;
-    row = (group * teams + team) * kR;
+    step = groups * teams * kR;
+    row = (mine * teams + team) * kR;
   }
-  __device__ __forceinline__ int column(int k) const { return lead + (k * threads + thread) * kE; }
+  __device__ __forceinline__ int column(int k) const { return lead + head + (k * threads + thread) * kE; }
   __device__ __forceinline__ int pitch() const { return threads * kE; }
+  // Which of the arrays' rows is the group's `r`th.
+  __device__ __forceinline__ uint32_t index(uint32_t r) const { return kShift ? place_of + period * r : r; }
+  __device__ __forceinline__ long long bytes_to(const Rows& rows, int r) const { return kShift ? r * (rows.pitch * period) : r * rows.pitch; }
+  // The thread's first access to the team's first row.
+  __device__ __forceinline__ const char* begin(const Rows& rows) const {
+    return rows.p + index(row) * rows.pitch + column(0) * static_cast<int>(sizeof(T));
+  }
   // The first row of the first team of the thread's warp: teams that share a warp go on together.
   __device__ __forceinline__ uint32_t first() const {
     return row - (kTeam ? team % (32 / (kTeam ? kTeam : 32)) : 0) * kR;
-  }
-  __device__ __forceinline__ void source(int array, const Rows& rows) {
-    from[array] = rows.p + row * rows.pitch + lead * static_cast<int>(sizeof(T)) + thread * kBytes;
   }
   __device__ __forceinline__ char* place(int st, int r, int array) const {
     return ring + ((st * kR + r) * kArrays + array) * kK * static_cast<int>(blockDim.x) * kBytes;
@@ -325,14 +348,17 @@ struct Stream {
   __device__ __forceinline__ void copy(int st, const Rows (&rows)[kArrays]) {
 #pragma unroll
     for (int array = 0; array < kArrays; ++array) {
+      const char* none = rows[array].p;
+      if constexpr (kShift) none -= reinterpret_cast<uintptr_t>(none) % 16;
 #pragma unroll
       for (int r = 0; r < kR; ++r) {
-        const char* p = from[array] + r * rows[array].pitch;
+        const char* p = from[array] + bytes_to(rows[array], r);
         char* to = place(st, r, array);
 #pragma unroll
         for (int k = 0; k < kK; ++k) {
           const bool there = k < count && row + r < n;
-          const char* src = there ? p + k * threads * kBytes : rows[array].p;     // (nothing is read of the latter)
+          // (where nothing is there nothing is read: the address is an aligned one all the same)
+          const char* src = there ? p + k * threads * kBytes : none;
           char* at = to + k * static_cast<int>(blockDim.x) * kBytes;
           const int bytes = there ? kBytes : 0;
           if constexpr (kBytes == 16)
@@ -351,6 +377,8 @@ struct Stream {
   // Begins the copies of the first batches.
   __device__ __forceinline__ void start(const Rows (&rows)[kArrays]) {
 #pragma unroll
+    for (int array = 0; array < kArrays; ++array) from[array] = begin(rows[array]);
+#pragma unroll
     for (int st = 0; st < kStages - 1; ++st) copy(st, rows);
   }
   // Begins one more copy, waits for the oldest and returns its stage.
@@ -364,6 +392,32 @@ struct Stream {
   __device__ __forceinline__ void read(int st, int r, int array, float2 (&f)[kPairs]) const {
     read_pairs<T, kE, kPairs>(place(st, r, array), blockDim.x * kBytes, f);
   }
+  // The address of the thread's extra element of the group's row r; and that element, 0 where there is none.
+  __device__ __forceinline__ T* extra_of(const Rows& rows, uint32_t r) const {
+    return reinterpret_cast<T*>(const_cast<char*>(rows.p) + index(r) * rows.pitch) + extra;
+  }
+  __device__ __forceinline__ float read_extra(const Rows& rows, uint32_t r) const {
+    return extra >= 0 && r < n ? load(extra_of(rows, r)) : 0.0f;
+  }
+  // Whether the thread's element c is in the row.
+  __device__ __forceinline__ bool in_row(int c) const { return c / kE < count; }
+  __device__ __forceinline__ void write(char* to, const float2 (&f)[kPairs]) const {
+    write_pairs<T, kE, kPairs>(reinterpret_cast<T*>(to), pitch(), count, f);
+  }
+  // The thread's columns of a vector, `none` each where there is no vector.
+  __device__ __forceinline__ void read_vector(const void* p, int bf16, float none, float2 (&f)[kPairs]) const {
+    if constexpr (kShift) {
+#pragma unroll
+      for (int c = 0; c < kColumns; ++c) {
+        float v = none;
+        if (p && in_row(c)) v = element(p, bf16, column(c / kE) + c % kE);
+        if (c % 2) f[c / 2].y = v;
+        else f[c / 2].x = v;
+      }
+    } else {
+      vector_columns<kE, kPairs>(p, bf16, column(0), pitch(), count, none, f);
+    }
+  }
 };
 
 struct NormStream {
@@ -374,20 +428,21 @@ struct NormStream {
   float* mean;
   float* rstd;
   int weight_bf16, n, H, team_threads;
+  int period;                // rows whose places in 16 bytes differ
   float eps, inv_h;
 };
 
-template <typename T, int kE, int kColumns, int kR, int kStages, int kTeam>
+template <typename T, int kE, int kColumns, int kR, int kStages, int kTeam, bool kShift>
 __global__ void __launch_bounds__(kStreamThreads) norm_stream_kernel(const NormStream a) {
   extern __shared__ float4 shared[];
   // slots of both sums for every team, then the ring
   constexpr int kSlots = kTeam ? 0 : 3 * kR * 32, kPairs = kColumns / 2;
   const int teams = blockDim.x / (kTeam ? kTeam : a.team_threads);
   float* slots = reinterpret_cast<float*>(shared);
-  Stream<T, kE, kColumns, kR, 1, kStages, kTeam> s(a.team_threads, a.n, a.H, 1, reinterpret_cast<char*>(slots + teams * kSlots));
+  Stream<T, kE, kColumns, kR, 1, kStages, kTeam, kShift> s(a.team_threads, a.n, a.H, 1, a.period, a.x[0],
+                                                           reinterpret_cast<char*>(slots + teams * kSlots));
   uint32_t row = s.row, turn = s.first();
-  char* to = const_cast<char*>(a.out.p) + row * a.out.pitch + s.column(0) * static_cast<int>(sizeof(T));
-  s.source(0, a.x[0]);
+  char* to = const_cast<char*>(s.begin(a.out));
   s.start(a.x);
   if constexpr (kSlots > 0) {
     for (int i = threadIdx.x; i < teams * kSlots; i += blockDim.x) slots[i] = 0.0f;
@@ -395,8 +450,14 @@ __global__ void __launch_bounds__(kStreamThreads) norm_stream_kernel(const NormS
     slots += s.team * kSlots;
   }
   float2 w[kPairs], b[kPairs];
-  read_vector<kE, kPairs>(a.weight, a.weight_bf16, s.column(0), s.pitch(), s.count, 1.0f, w);
-  read_vector<kE, kPairs>(a.bias, a.weight_bf16, s.column(0), s.pitch(), s.count, 0.0f, b);
+  s.read_vector(a.weight, a.weight_bf16, 1.0f, w);
+  s.read_vector(a.bias, a.weight_bf16, 0.0f, b);
+  const float extra_w = kShift && s.extra >= 0 && a.weight ? element(a.weight, a.weight_bf16, s.extra) : 1.0f;
+  const float extra_b = kShift && s.extra >= 0 && a.bias ? element(a.bias, a.weight_bf16, s.extra) : 0.0f;
+  float extras[kR], extra[kR];
+  if constexpr (kShift)
+#pragma unroll
+    for (int r = 0; r < kR; ++r) extras[r] = s.read_extra(a.x[0], row + r);
   for (; turn < s.n; turn += s.step, row += s.step, to += a.out.advance) {
     const int stage = s.next(a.x);
     float2 d[kR][kPairs];
@@ -405,20 +466,30 @@ __global__ void __launch_bounds__(kStreamThreads) norm_stream_kernel(const NormS
     for (int r = 0; r < kR; ++r) {
       s.read(stage, r, 0, d[r]);
       centre[r] = pairs_sum<kPairs>(d[r]);
+      if constexpr (kShift) {
+        extra[r] = extras[r];
+        centre[r] += extra[r];
+        extras[r] = s.read_extra(a.x[0], row + s.step + r);
+      }
     }
     team_sum<kR, kTeam>(centre, slots, s.team, s.threads);
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
       centre[r] = centre_of<T>(centre[r] * a.inv_h);
       float2 squares[kPairs];
+      // (what is not in the row stays 0)
 #pragma unroll
-      for (int i = 0; i < kPairs; ++i) {
-        // what lies behind the row stays 0
+      for (int i = 0; i < kPairs; ++i)
         d[r][i] = sub2(d[r][i], make_float2(2 * i / kE < s.count ? centre[r] : 0.0f, (2 * i + 1) / kE < s.count ? centre[r] : 0.0f));
-        squares[i] = mul2(d[r][i], d[r][i]);
-      }
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) squares[i] = mul2(d[r][i], d[r][i]);
       sums[r] = pairs_sum<kPairs>(d[r]);
       sums[kR + r] = pairs_sum<kPairs>(squares);
+      if constexpr (kShift) {
+        extra[r] = s.extra >= 0 ? extra[r] - centre[r] : 0.0f;
+        sums[r] += extra[r];
+        sums[kR + r] = fmaf(extra[r], extra[r], sums[kR + r]);
+      }
     }
     team_sum<2 * kR, kTeam>(sums, slots + kR * 32, s.team, s.threads);
 #pragma unroll
@@ -427,13 +498,15 @@ __global__ void __launch_bounds__(kStreamThreads) norm_stream_kernel(const NormS
       const float rest = sums[r] * a.inv_h, rstd = rstd_of(rest, sums[kR + r] * a.inv_h, a.eps);
       if (row + r >= s.n) break;
       if (s.thread == 0) {
-        a.mean[row + r] = centre[r] + rest;
-        a.rstd[row + r] = rstd;
+        a.mean[s.index(row + r)] = centre[r] + rest;
+        a.rstd[s.index(row + r)] = rstd;
       }
       const float shift = -rest * rstd;
 #pragma unroll
       for (int i = 0; i < kPairs; ++i) d[r][i] = fma2(fma2(d[r][i], both(rstd), both(shift)), w[i], b[i]);
-      write_pairs<T, kE, kPairs>(reinterpret_cast<T*>(to + r * a.out.pitch), s.pitch(), s.count, d[r]);
+      s.write(to + s.bytes_to(a.out, r), d[r]);
+      if constexpr (kShift)
+        if (s.extra >= 0) store(s.extra_of(a.out, row + r), fmaf(fmaf(extra[r], rstd, shift), extra_w, extra_b));
     }
   }
 }
@@ -500,11 +573,6 @@ __global__ void __launch_bounds__(kBlockThreads) norm_block_kernel(const NormStr
   }
 }
 
-// Element j of a vector of bf16 or fp32.
-__device__ __forceinline__ float element(const void* p, int bf16, int j) {
-  return bf16 ? load(static_cast<const __nv_bfloat16*>(p) + j) : load(static_cast<const float*>(p) + j);
-}
-
 // main_grad[j] += v, in 32 bits; nothing without a main_grad.
 __device__ __forceinline__ void add_to_main_grad(void* to, int bf16, int j, float v) {
   if (!to) return;
@@ -523,12 +591,13 @@ struct NormGradStream {
   int main_grad_bf16, alone;
   int weight_bf16, n, H, team_threads;
   int blocks;                // of a cluster
+  int period;                // rows whose places in 16 bytes differ
   float inv_h;
 };
 
 // A block's teams take batches in turn, a thread the same columns of every row: their weights and the sums
 // for the main_grads stay in its registers.
-template <typename T, int kE, int kColumns, int kR, int kStages, int kTeam, bool kCluster>
+template <typename T, int kE, int kColumns, int kR, int kStages, int kTeam, bool kShift, bool kCluster>
 __global__ void __launch_bounds__(kStreamThreads) norm_grad_stream_kernel(const NormGradStream a) {
   extern __shared__ float4 shared[];
   __shared__ float box[2][kCluster ? kMostBlocks : 1][kCluster ? 2 * kR : 1];
@@ -536,21 +605,19 @@ __global__ void __launch_bounds__(kStreamThreads) norm_grad_stream_kernel(const 
   ptx::pdl_launch_dependents();
   // two batches' slots for every team, then the ring
   constexpr int kSlots = kTeam ? 0 : 2 * 2 * kR * 32, kPairs = kColumns / 2;
-  using S = Stream<T, kE, kColumns, kR, 2, kStages, kTeam>;
+  using S = Stream<T, kE, kColumns, kR, 2, kStages, kTeam, kShift>;
   const int teams = blockDim.x / (kTeam ? kTeam : a.team_threads);
   float* slots = reinterpret_cast<float*>(shared);
-  S s(a.team_threads, a.n, a.H, blocks, reinterpret_cast<char*>(slots + teams * kSlots));
+  S s(a.team_threads, a.n, a.H, blocks, a.period, a.in[0], reinterpret_cast<char*>(slots + teams * kSlots));
   uint32_t row = s.row, turn = s.first();
-  char* to = const_cast<char*>(a.grad_x.p) + row * a.grad_x.pitch + s.column(0) * static_cast<int>(sizeof(T));
-  s.source(0, a.in[0]);
-  s.source(1, a.in[1]);
+  char* to = const_cast<char*>(s.begin(a.grad_x));
   s.start(a.in);
   float means[kR], rstds[kR];
   auto moments = [&](uint32_t at) {
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
-      means[r] = at + r < s.n ? __ldg(a.mean + at + r) : 0.0f;
-      rstds[r] = at + r < s.n ? __ldg(a.rstd + at + r) : 0.0f;
+      means[r] = at + r < s.n ? __ldg(a.mean + s.index(at + r)) : 0.0f;
+      rstds[r] = at + r < s.n ? __ldg(a.rstd + s.index(at + r)) : 0.0f;
     }
   };
   moments(row);
@@ -562,9 +629,14 @@ __global__ void __launch_bounds__(kStreamThreads) norm_grad_stream_kernel(const 
     slots += s.team * kSlots;
   }
   float2 w[kPairs], dw[kPairs], db[kPairs];
-  read_vector<kE, kPairs>(a.weight, a.weight_bf16, s.column(0), s.pitch(), s.count, 1.0f, w);
+  s.read_vector(a.weight, a.weight_bf16, 1.0f, w);
 #pragma unroll
   for (int i = 0; i < kPairs; ++i) dw[i] = db[i] = both(0.0f);
+  const float extra_w = kShift && s.extra >= 0 && a.weight ? element(a.weight, a.weight_bf16, s.extra) : 1.0f;
+  float extra_dw = 0.0f, extra_db = 0.0f, extra_xs[kR], extra_gs[kR], extra_n[kR], extra_u[kR];
+  if constexpr (kShift)
+#pragma unroll
+    for (int r = 0; r < kR; ++r) extra_xs[r] = s.read_extra(a.in[0], row + r), extra_gs[r] = s.read_extra(a.in[1], row + r);
   int flip = 0;
   for (; turn < s.n; turn += s.step, row += s.step, to += a.grad_x.advance, flip ^= 1) {
     const int stage = s.next(a.in);
@@ -587,6 +659,16 @@ __global__ void __launch_bounds__(kStreamThreads) norm_grad_stream_kernel(const 
       }
       sums[r] = s1.x + s1.y;
       sums[kR + r] = s2.x + s2.y;
+      if constexpr (kShift) {
+        extra_n[r] = (extra_xs[r] - mean[r]) * rstd[r];
+        extra_u[r] = extra_gs[r] * extra_w;
+        extra_dw = fmaf(extra_gs[r], extra_n[r], extra_dw);
+        extra_db += extra_gs[r];
+        sums[r] += extra_u[r];
+        sums[kR + r] = fmaf(extra_u[r], extra_n[r], sums[kR + r]);
+        extra_xs[r] = s.read_extra(a.in[0], row + s.step + r);
+        extra_gs[r] = s.read_extra(a.in[1], row + s.step + r);
+      }
     }
     team_sum<2 * kR, kTeam>(sums, slots + flip * 2 * kR * 32, s.team, s.threads);
     if constexpr (kCluster) cluster_sum(sums, box, box_flip, blocks, static_cast<int>(ptx::cluster_rank()));
@@ -605,7 +687,9 @@ __global__ void __launch_bounds__(kStreamThreads) norm_grad_stream_kernel(const 
         const float2 n = mul2(sub2(x[i], both(mean[r])), both(rstd[r])), u = mul2(g[i], w[i]);
         x[i] = fma2(n, both(c2), fma2(u, both(rstd[r]), both(c1)));
       }
-      write_pairs<T, kE, kPairs>(reinterpret_cast<T*>(to + r * a.grad_x.pitch), s.pitch(), s.count, x);
+      s.write(to + s.bytes_to(a.grad_x, r), x);
+      if constexpr (kShift)
+        if (s.extra >= 0) store(s.extra_of(a.grad_x, row + r), fmaf(extra_n[r], c2, fmaf(extra_u[r], rstd[r], c1)));
     }
   }
   if (!a.partial) return;
@@ -613,49 +697,51 @@ __global__ void __launch_bounds__(kStreamThreads) norm_grad_stream_kernel(const 
   float* out = a.partial + static_cast<long long>(s.group) * 2 * a.H;
   float* meet = reinterpret_cast<float*>(shared);
   if constexpr (S::kBytes > 2) ptx::cp_async_wait<0>();        // (the ring is about to be used for them)
+  constexpr int kMine = kColumns + kShift;           // the extra element's sums are the last
+  auto column = [&](int c) { return c == kColumns ? s.extra : s.column(c / kE) + c % kE; };
+  auto in_row = [&](int c) { return c == kColumns ? s.extra >= 0 : s.in_row(c); };
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
-    float mine[kColumns];
+    float mine[kMine];
 #pragma unroll
     for (int c = 0; c < kColumns; ++c) {
       const float2 v = half ? db[c / 2] : dw[c / 2];
       mine[c] = c % 2 ? v.y : v.x;
     }
+    if constexpr (kShift) mine[kColumns] = half ? extra_db : extra_dw;
     if (teams > 1) {
       __syncthreads();
 #pragma unroll
-      for (int c = 0; c < kColumns; ++c) meet[(s.team * kColumns + c) * s.threads + s.thread] = mine[c];
+      for (int c = 0; c < kMine; ++c) meet[(s.team * kMine + c) * s.threads + s.thread] = mine[c];
       __syncthreads();
-      for (int c = s.team; c < kColumns; c += teams) {
+      for (int c = s.team; c < kMine; c += teams) {
         float v = 0.0f;
-        for (int t = 0; t < teams; ++t) v += meet[(t * kColumns + c) * s.threads + s.thread];
-        if (c / kE >= s.count) continue;
-        const int j = s.column(c / kE) + c % kE;
-        if (a.alone) add_to_main_grad(a.main_grads[half], a.main_grad_bf16, j, v);
-        else out[half * a.H + j] = v;
+        for (int t = 0; t < teams; ++t) v += meet[(t * kMine + c) * s.threads + s.thread];
+        if (!in_row(c)) continue;
+        if (a.alone) add_to_main_grad(a.main_grads[half], a.main_grad_bf16, column(c), v);
+        else out[half * a.H + column(c)] = v;
       }
     } else if (a.alone) {
       void* to = a.main_grads[half];
       if (!to) continue;
-      float before[kColumns];                      // all read before the first is written
+      float before[kMine];                         // all read before the first is written
 #pragma unroll
-      for (int c = 0; c < kColumns; ++c)
-        before[c] = c / kE < s.count ? element(to, a.main_grad_bf16, s.column(c / kE) + c % kE) : 0.0f;
+      for (int c = 0; c < kMine; ++c) before[c] = in_row(c) ? element(to, a.main_grad_bf16, column(c)) : 0.0f;
 #pragma unroll
-      for (int c = 0; c < kColumns; ++c) {
-        if (c / kE >= s.count) continue;
-        const int j = s.column(c / kE) + c % kE;
-        if (a.main_grad_bf16) store(static_cast<__nv_bfloat16*>(to) + j, before[c] + mine[c]);
-        else static_cast<float*>(to)[j] = before[c] + mine[c];
+      for (int c = 0; c < kMine; ++c) {
+        if (!in_row(c)) continue;
+        if (a.main_grad_bf16) store(static_cast<__nv_bfloat16*>(to) + column(c), before[c] + mine[c]);
+        else static_cast<float*>(to)[column(c)] = before[c] + mine[c];
       }
     } else {
 #pragma unroll
-      for (int c = 0; c < kColumns; c += kE < 4 ? 1 : 4) {
-        if (c / kE >= s.count) continue;
-        const int j = s.column(c / kE) + c % kE;
+      for (int c = 0; c < kMine; c += kE < 4 || kShift ? 1 : 4) {
+        if (!in_row(c)) continue;
         // (rows whose vectors move whole have a multiple of four elements, and shares lie at 256 bytes)
-        if constexpr (kE >= 4) *reinterpret_cast<float4*>(out + half * a.H + j) = make_float4(mine[c], mine[c + 1], mine[c + 2], mine[c + 3]);
-        else out[half * a.H + j] = mine[c];
+        if constexpr (kE >= 4 && !kShift)
+          *reinterpret_cast<float4*>(out + half * a.H + column(c)) = make_float4(mine[c], mine[c + 1], mine[c + 2], mine[c + 3]);
+        else
+          out[half * a.H + column(c)] = mine[c];
       }
     }
   }
@@ -823,10 +909,11 @@ StreamShape make_stream_shape(int H, int access, int team, int columns, int rows
   return s;
 }
 
-// No more groups than rows for all their teams.
-void set_groups(StreamShape& s, int n, int rows, int most) {
-  const long long want = (static_cast<long long>(n) + rows * s.teams - 1) / (rows * s.teams);
-  s.groups = static_cast<int>(want < most ? want : most);
+// No more groups than rows for all their teams; as many for each of `period` places.
+void set_groups(StreamShape& s, int n, int rows, int most, int period) {
+  const long long each = (static_cast<long long>(n) + period - 1) / period;
+  const long long want = (each + rows * s.teams - 1) / (rows * s.teams);
+  s.groups = static_cast<int>(want < most / period ? want : most / period) * period;
 }
 
 Rows make_rows(const void* p, long long stride, size_t size, const StreamShape& s, int rows) {
@@ -903,20 +990,21 @@ NormStream norm_stream(const NormArgs& a, size_t size, const StreamShape& s, int
   k.n = a.n;
   k.H = a.H;
   k.team_threads = s.threads;
+  k.period = a.period;
   k.eps = a.eps;
   k.inv_h = a.inv_h;
   return k;
 }
 
-template <typename T, int kE, int kColumns, int kTeam>
+template <typename T, int kE, int kColumns, int kTeam, bool kShift>
 cudaError_t launch_stream(const NormArgs& a, cudaStream_t stream) {
   constexpr int kR = batch_rows<T, kColumns>(), kStages = stages<T, kE>(1);
   static StreamSetUp state;
-  const auto kernel = norm_stream_kernel<T, kE, kColumns, kR, kStages, kTeam>;
+  const auto kernel = norm_stream_kernel<T, kE, kColumns, kR, kStages, kTeam, kShift>;
   const cudaError_t e = set_up(kernel, state, a.dev);
   if (e != cudaSuccess) return e;
   StreamShape s = make_stream_shape(a.H, kE, kTeam, kColumns, kR, 3 * 32, kStages * kR * kColumns * static_cast<int>(sizeof(T)));
-  set_groups(s, a.n, kR, a.num_sms);
+  set_groups(s, a.n, kR, a.num_sms, a.period);
   kernel<<<s.groups, s.teams * s.threads, s.bytes, stream>>>(norm_stream(a, sizeof(T), s, kR));
   return cudaGetLastError();
 }
@@ -928,18 +1016,19 @@ cudaError_t launch_block(const NormArgs& a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-template <typename T, int kE, int kColumns, int kTeam, bool kCluster = false>
+template <typename T, int kE, int kColumns, int kTeam, bool kShift, bool kCluster = false>
 cudaError_t launch_stream(NormGradArgs a, cudaStream_t stream) {
-  constexpr int kR = batch_rows<T, kColumns>(), kStages = stages<T, kE>(2);
+  // (the extra elements of four rows do not fit beside the columns' sums)
+  constexpr int kR = batch_rows<T, kColumns>() / (kShift && kColumns == 8 && sizeof(T) == 2 ? 2 : 1), kStages = stages<T, kE>(2);
   static StreamSetUp state;
-  const auto kernel = norm_grad_stream_kernel<T, kE, kColumns, kR, kStages, kTeam, kCluster>;
+  const auto kernel = norm_grad_stream_kernel<T, kE, kColumns, kR, kStages, kTeam, kShift, kCluster>;
   StreamShape s = make_stream_shape(a.H, kE, kTeam, kColumns, kR, 4 * 32, kStages * kR * 2 * kColumns * static_cast<int>(sizeof(T)));
-  const size_t meet = static_cast<size_t>(s.teams) * s.threads * kColumns * sizeof(float);
+  const size_t meet = static_cast<size_t>(s.teams) * s.threads * (kColumns + 1) * sizeof(float);
   if (s.bytes < meet) s.bytes = meet;
   int most = 0;
   cudaError_t e = set_up(kernel, state, a.dev);
   if (e != cudaSuccess || (e = groups_at_once(kernel, state, s, a.dev, a.parts, &most)) != cudaSuccess) return e;
-  set_groups(s, a.n, kR, most < a.parts ? most : a.parts);
+  set_groups(s, a.n, kR, most < a.parts ? most : a.parts, a.period);
   a.parts = s.groups;
   NormGradStream k{};
   k.in[0] = make_rows(a.x, a.x_stride, sizeof(T), s, kR);
@@ -958,6 +1047,7 @@ cudaError_t launch_stream(NormGradArgs a, cudaStream_t stream) {
   k.H = a.H;
   k.team_threads = s.threads;
   k.blocks = s.blocks;
+  k.period = a.period;
   k.inv_h = a.inv_h;
   cudaLaunchAttribute attr{};
   const cudaLaunchConfig_t cfg = stream_config(s, &attr, stream);
@@ -965,30 +1055,32 @@ cudaError_t launch_stream(NormGradArgs a, cudaStream_t stream) {
   return k.alone ? cudaGetLastError() : launch_join(a, stream);
 }
 
-template <typename T, int kE, int kColumns, typename Args>
+template <typename T, int kE, int kColumns, bool kShift, typename Args>
 cudaError_t by_team(const Args& a, cudaStream_t stream) {
-  if (a.H <= 4 * kColumns) return launch_stream<T, kE, kColumns, 4>(a, stream);
-  if (a.H <= 8 * kColumns) return launch_stream<T, kE, kColumns, 8>(a, stream);
-  if (a.H <= 16 * kColumns) return launch_stream<T, kE, kColumns, 16>(a, stream);
-  if (a.H <= 32 * kColumns) return launch_stream<T, kE, kColumns, 32>(a, stream);
-  return launch_stream<T, kE, kColumns, 0>(a, stream);
+  const int H = a.H;
+  // (extra elements, up to two accesses' less two, are a thread's each)
+  if constexpr (!kShift)
+    if (H <= 4 * kColumns) return launch_stream<T, kE, kColumns, 4, kShift>(a, stream);
+  if constexpr (!kShift || kE <= 4)
+    if (H <= 8 * kColumns) return launch_stream<T, kE, kColumns, 8, kShift>(a, stream);
+  if (H <= 16 * kColumns) return launch_stream<T, kE, kColumns, 16, kShift>(a, stream);
+  if (H <= 32 * kColumns) return launch_stream<T, kE, kColumns, 32, kShift>(a, stream);
+  return launch_stream<T, kE, kColumns, 0, kShift>(a, stream);
 }
 
 // One of the kernels by a row's elements.  A thread has sixteen of them, which spreads a sum's shuffles
 // over the most (65536 x 1024 bf16 forward: 44 us, with eight 51), but for short rows of fp32,
 // of which a batch would be one (65536 x 1024 forward: 93 us, with eight 80), and short rows'
 // gradient, where the columns' sums take the registers (65536 x 256 bf16: 33 us, with eight 23).
-template <typename T, int kE>
+template <typename T, int kE, bool kShift>
 cudaError_t stream_rows(const NormArgs& a, cudaStream_t stream) {
-  if (a.H > kStreamHidden) return launch_block<T, kE>(a, stream);
-  if (sizeof(T) == 4 && a.H <= 1024) return by_team<T, kE, 8>(a, stream);
-  return by_team<T, kE, 16>(a, stream);
+  if (sizeof(T) == 4 && a.H <= 1024) return by_team<T, kE, 8, kShift>(a, stream);
+  return by_team<T, kE, 16, kShift>(a, stream);
 }
-template <typename T, int kE>
+template <typename T, int kE, bool kShift>
 cudaError_t stream_rows(const NormGradArgs& a, cudaStream_t stream) {
-  if (a.H > kStreamHidden) return launch_stream<T, kE, 16, 0, true>(a, stream);
-  if (a.H <= 1024) return by_team<T, kE, 8>(a, stream);
-  return launch_stream<T, kE, 16, 0>(a, stream);
+  if (a.H <= 1024) return by_team<T, kE, 8, kShift>(a, stream);
+  return launch_stream<T, kE, 16, 0, kShift>(a, stream);
 }
 
 template <typename T>
@@ -999,43 +1091,70 @@ cudaError_t grad_loops(const NormGradArgs& a, cudaStream_t stream) {
   return launch_join(a, stream);
 }
 
-// Whether rows and vectors can be moved `elements` at a time.
-bool rows_aligned(const void* p, long long stride, int rows, int elements, size_t size) {
-  return reinterpret_cast<uintptr_t>(p) % (elements * size) == 0 && (rows == 1 || stride % elements == 0);
-}
+// The places of some arrays' rows in 16 bytes.
+struct Places {
+  bool alike = true;         // the same for all arrays, row by row
+  bool whole = true;         // every row begins at 16 bytes
+  int period = 1;            // rows after which they repeat
+  uintptr_t begin = 0, step = 0;
+
+  void add(const void* p, long long stride, int rows, size_t size, bool first) {
+    const uintptr_t b = reinterpret_cast<uintptr_t>(p) % 16, d = rows > 1 ? static_cast<uintptr_t>(stride) * size % 16 : 0;
+    if (first) begin = b, step = d;
+    alike &= b == begin && d == step;
+    whole &= b == 0 && d == 0;
+    for (period = 1; step * period % 16; ++period) {}
+  }
+};
+
+// Whether a vector's kE elements from a multiple of them on are one access.
 bool vector_aligned(const void* p, int bf16, int elements) {
   return reinterpret_cast<uintptr_t>(p) % (elements * (bf16 ? 2 : 4)) == 0;
 }
-bool moves(const NormArgs& a, int elements, size_t size) {
-  return a.H % elements == 0 && rows_aligned(a.x, a.x_stride, a.n, elements, size) &&
-         rows_aligned(a.out, a.out_stride, a.n, elements, size) && vector_aligned(a.weight, a.weight_bf16, elements) &&
-         vector_aligned(a.bias, a.weight_bf16, elements);
-}
-bool moves(const NormGradArgs& a, int elements, size_t size) {
-  return a.H % elements == 0 && rows_aligned(a.x, a.x_stride, a.n, elements, size) &&
-         rows_aligned(a.grad, a.grad_stride, a.n, elements, size) &&
-         rows_aligned(a.grad_x, a.grad_x_stride, a.n, elements, size) && vector_aligned(a.weight, a.weight_bf16, elements);
+
+// The form that suits rows: whole accesses, whole accesses after a shift, or single elements.
+enum Form { kWholeRows, kShiftedRows, kElements };
+
+template <int kE>
+Form form_of(const Places& places, int H, bool vectors) {
+  if (places.whole && H % kE == 0 && vectors) return kWholeRows;
+  return places.alike && H <= kStreamHidden ? kShiftedRows : kElements;
 }
 
 template <typename T>
-cudaError_t forward(const NormArgs& a, cudaStream_t stream) {
-  constexpr int kWhole = 16 / sizeof(T), kWord = 4 / sizeof(T);
+cudaError_t forward(NormArgs a, cudaStream_t stream) {
+  constexpr int kE = 16 / sizeof(T);
+  Places places;
+  places.add(a.x, a.x_stride, a.n, sizeof(T), true);
+  places.add(a.out, a.out_stride, a.n, sizeof(T), false);
+  const Form form = form_of<kE>(places, a.H, vector_aligned(a.weight, a.weight_bf16, kE) && vector_aligned(a.bias, a.weight_bf16, kE));
+  a.period = form == kShiftedRows ? places.period : 1;
   if (a.H > kBlockHidden) {
     norm_kernel<T><<<a.n, kRowThreads, 0, stream>>>(a);
     return cudaGetLastError();
   }
-  if (moves(a, kWhole, sizeof(T))) return stream_rows<T, kWhole>(a, stream);
-  if (moves(a, kWord, sizeof(T))) return stream_rows<T, kWord>(a, stream);
-  return stream_rows<T, 1>(a, stream);
+  if (a.H > kStreamHidden) return form == kWholeRows ? launch_block<T, kE>(a, stream) : launch_block<T, 1>(a, stream);
+  return form == kWholeRows     ? stream_rows<T, kE, false>(a, stream)
+         : form == kShiftedRows ? stream_rows<T, kE, true>(a, stream)
+                                : stream_rows<T, 1, false>(a, stream);
 }
 
 template <typename T>
-cudaError_t grad(const NormGradArgs& a, cudaStream_t stream) {
-  constexpr int kWhole = 16 / sizeof(T), kWord = 4 / sizeof(T);
+cudaError_t grad(NormGradArgs a, cudaStream_t stream) {
+  constexpr int kE = 16 / sizeof(T);
+  Places places;
+  places.add(a.x, a.x_stride, a.n, sizeof(T), true);
+  places.add(a.grad, a.grad_stride, a.n, sizeof(T), false);
+  places.add(a.grad_x, a.grad_x_stride, a.n, sizeof(T), false);
+  Form form = form_of<kE>(places, a.H, vector_aligned(a.weight, a.weight_bf16, kE));
+  if (form == kShiftedRows && a.parts < places.period) form = kElements;       // (too few rows for a share of each place)
+  a.period = form == kShiftedRows ? places.period : 1;
   if (a.H > kNormHeld) return grad_loops<T>(a, stream);
-  if (moves(a, kWhole, sizeof(T))) return stream_rows<T, kWhole>(a, stream);
-  if (moves(a, kWord, sizeof(T))) return stream_rows<T, kWord>(a, stream);
-  return stream_rows<T, 1>(a, stream);
+  if (a.H > kStreamHidden)
+    return form == kWholeRows ? launch_stream<T, kE, 16, 0, false, true>(a, stream) : launch_stream<T, 1, 16, 0, false, true>(a, stream);
+  return form == kWholeRows     ? stream_rows<T, kE, false>(a, stream)
+         : form == kShiftedRows ? stream_rows<T, kE, true>(a, stream)
+                                : stream_rows<T, 1, false>(a, stream);
 }
 
 }  // namespace

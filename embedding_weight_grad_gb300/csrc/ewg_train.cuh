@@ -25,6 +25,7 @@ struct NormArgs {
   float* mean;               // [n] each
   float* rstd;
   int dev, num_sms;
+  int period;                // rows whose places in 16 bytes differ (set by the launcher)
 };
 
 struct NormGradArgs {
@@ -47,6 +48,7 @@ struct NormGradArgs {
   float* partial;            // [parts][2][H]: shares of the sums over the rows
   int parts;                 // shares of the rows
   int dev;
+  int period;                // rows whose places in 16 bytes differ (set by the launcher)
 };
 
 struct NormGradLayout {
