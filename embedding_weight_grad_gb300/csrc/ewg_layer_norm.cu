@@ -281,7 +281,7 @@ struct Rows {
 // kShift: rows that begin anywhere, all arrays' alike.  Their places in 16 bytes repeat every `period` rows; a
 // group takes rows of one place only, so that columns stay with their threads.  Accesses begin at the first 16 bytes
 // within the row; the elements before them and behind the last whole one, less than two accesses' together, are
-// the team's first threads' extra ones, one each, which are loaded by themselves a batch ahead.
+// the team's first threads' extra ones, one each, in four bytes of their own behind the ring.
 template <typename T, int kE, int kColumns, int kR, int kArrays, int kStages, int kTeam, bool kShift>
 struct Stream {
   static constexpr int kPairs = kColumns / 2;
@@ -290,7 +290,7 @@ struct Stream {
   int threads, teams, team, thread, lead, group;      // (group: which of the grid's blocks or clusters)
   int count;                         // of the thread's kK accesses to a row those that lie in it
   int period, place_of, head;        // kShift: which of the period's rows are the group's; their elements before the accesses
-  int extra = -1;                    // the column of the thread's extra element
+  int extra = -1, extra_half = 0;    // the column of the thread's extra element; whether it is the upper one of its four bytes
   uint32_t n, row, step;             // rows; the first row of the team's next batch to be copied; rows of all teams' batches
   const char* from[kArrays];         // of `row`, the thread's first access
   char* ring;
@@ -323,6 +323,7 @@ struct Stream {
       const int behind = head + accesses * kE;               // (the first column behind the accesses)
       if (thread < head) extra = thread;
       else if (thread < head + H - behind) extra = behind + thread - head;
+      if (sizeof(T) == 2) extra_half = reinterpret_cast<uintptr_t>(extra_of(like, 0)) / 2 % 2;
     }
     ring = shared + threadIdx.x * kBytes;
     step = groups * teams * kR;
@@ -343,6 +344,10 @@ struct Stream {
   }
   __device__ __forceinline__ char* place(int st, int r, int array) const {
     return ring + ((st * kR + r) * kArrays + array) * kK * static_cast<int>(blockDim.x) * kBytes;
+  }
+  __device__ __forceinline__ char* extra_place(int st, int r, int array) const {
+    return ring - threadIdx.x * kBytes + kStages * kR * kArrays * kK * static_cast<int>(blockDim.x) * kBytes +
+           (((st * kR + r) * kArrays + array) * static_cast<int>(blockDim.x) + threadIdx.x) * 4;
   }
   // Begins the copy of the next batch; what is not there becomes zeros.
   __device__ __forceinline__ void copy(int st, const Rows (&rows)[kArrays]) {
@@ -369,6 +374,20 @@ struct Stream {
             *reinterpret_cast<T*>(at) = there ? *reinterpret_cast<const T*>(src) : T(0.0f);
         }
       }
+      if constexpr (kShift) {
+        if (extra >= 0) {
+#pragma unroll
+          for (int r = 0; r < kR; ++r) {
+            // the upper element of four bytes comes with the one before it, but for the array's first
+            const T* p = extra_of(rows[array], row + r);
+            char* to = extra_place(st, r, array);
+            const int bytes = row + r < n ? sizeof(T) == 2 && !extra_half ? 2 : 4 : 0;
+            const void* src = bytes ? static_cast<const void*>(p - extra_half) : static_cast<const void*>(none);
+            if (bytes && src < static_cast<const void*>(rows[array].p)) *reinterpret_cast<T*>(to + 2) = *p;
+            else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(ptx::smem_u32(to)), "l"(src), "r"(bytes) : "memory");
+          }
+        }
+      }
       from[array] += rows[array].advance;
     }
     row += step;
@@ -392,12 +411,12 @@ struct Stream {
   __device__ __forceinline__ void read(int st, int r, int array, float2 (&f)[kPairs]) const {
     read_pairs<T, kE, kPairs>(place(st, r, array), blockDim.x * kBytes, f);
   }
-  // The address of the thread's extra element of the group's row r; and that element, 0 where there is none.
+  // The address of the thread's extra element of the group's row r; and that element of a batch, 0 where there is none.
   __device__ __forceinline__ T* extra_of(const Rows& rows, uint32_t r) const {
     return reinterpret_cast<T*>(const_cast<char*>(rows.p) + index(r) * rows.pitch) + extra;
   }
-  __device__ __forceinline__ float read_extra(const Rows& rows, uint32_t r) const {
-    return extra >= 0 && r < n ? load(extra_of(rows, r)) : 0.0f;
+  __device__ __forceinline__ float read_extra(int st, int r, int array) const {
+    return extra >= 0 ? load(reinterpret_cast<const T*>(extra_place(st, r, array)) + extra_half) : 0.0f;
   }
   // Whether the thread's element c is in the row.
   __device__ __forceinline__ bool in_row(int c) const { return c / kE < count; }
@@ -454,10 +473,7 @@ __global__ void __launch_bounds__(kStreamThreads) norm_stream_kernel(const NormS
   s.read_vector(a.bias, a.weight_bf16, 0.0f, b);
   const float extra_w = kShift && s.extra >= 0 && a.weight ? element(a.weight, a.weight_bf16, s.extra) : 1.0f;
   const float extra_b = kShift && s.extra >= 0 && a.bias ? element(a.bias, a.weight_bf16, s.extra) : 0.0f;
-  float extras[kR], extra[kR];
-  if constexpr (kShift)
-#pragma unroll
-    for (int r = 0; r < kR; ++r) extras[r] = s.read_extra(a.x[0], row + r);
+  float extra[kR];
   for (; turn < s.n; turn += s.step, row += s.step, to += a.out.advance) {
     const int stage = s.next(a.x);
     float2 d[kR][kPairs];
@@ -467,9 +483,8 @@ __global__ void __launch_bounds__(kStreamThreads) norm_stream_kernel(const NormS
       s.read(stage, r, 0, d[r]);
       centre[r] = pairs_sum<kPairs>(d[r]);
       if constexpr (kShift) {
-        extra[r] = extras[r];
+        extra[r] = s.read_extra(stage, r, 0);
         centre[r] += extra[r];
-        extras[r] = s.read_extra(a.x[0], row + s.step + r);
       }
     }
     team_sum<kR, kTeam>(centre, slots, s.team, s.threads);
@@ -633,10 +648,7 @@ __global__ void __launch_bounds__(kStreamThreads) norm_grad_stream_kernel(const 
 #pragma unroll
   for (int i = 0; i < kPairs; ++i) dw[i] = db[i] = both(0.0f);
   const float extra_w = kShift && s.extra >= 0 && a.weight ? element(a.weight, a.weight_bf16, s.extra) : 1.0f;
-  float extra_dw = 0.0f, extra_db = 0.0f, extra_xs[kR], extra_gs[kR], extra_n[kR], extra_u[kR];
-  if constexpr (kShift)
-#pragma unroll
-    for (int r = 0; r < kR; ++r) extra_xs[r] = s.read_extra(a.in[0], row + r), extra_gs[r] = s.read_extra(a.in[1], row + r);
+  float extra_dw = 0.0f, extra_db = 0.0f;
   int flip = 0;
   for (; turn < s.n; turn += s.step, row += s.step, to += a.grad_x.advance, flip ^= 1) {
     const int stage = s.next(a.in);
@@ -660,14 +672,11 @@ __global__ void __launch_bounds__(kStreamThreads) norm_grad_stream_kernel(const 
       sums[r] = s1.x + s1.y;
       sums[kR + r] = s2.x + s2.y;
       if constexpr (kShift) {
-        extra_n[r] = (extra_xs[r] - mean[r]) * rstd[r];
-        extra_u[r] = extra_gs[r] * extra_w;
-        extra_dw = fmaf(extra_gs[r], extra_n[r], extra_dw);
-        extra_db += extra_gs[r];
-        sums[r] += extra_u[r];
-        sums[kR + r] = fmaf(extra_u[r], extra_n[r], sums[kR + r]);
-        extra_xs[r] = s.read_extra(a.in[0], row + s.step + r);
-        extra_gs[r] = s.read_extra(a.in[1], row + s.step + r);
+        const float n = (s.read_extra(stage, r, 0) - mean[r]) * rstd[r], extra_g = s.read_extra(stage, r, 1);
+        extra_dw = fmaf(extra_g, n, extra_dw);
+        extra_db += extra_g;
+        sums[r] = fmaf(extra_g, extra_w, sums[r]);
+        sums[kR + r] = fmaf(extra_g * extra_w, n, sums[kR + r]);
       }
     }
     team_sum<2 * kR, kTeam>(sums, slots + flip * 2 * kR * 32, s.team, s.threads);
@@ -689,7 +698,10 @@ __global__ void __launch_bounds__(kStreamThreads) norm_grad_stream_kernel(const 
       }
       s.write(to + s.bytes_to(a.grad_x, r), x);
       if constexpr (kShift)
-        if (s.extra >= 0) store(s.extra_of(a.grad_x, row + r), fmaf(extra_n[r], c2, fmaf(extra_u[r], rstd[r], c1)));
+        if (s.extra >= 0) {
+          const float n = (s.read_extra(stage, r, 0) - mean[r]) * rstd[r], u = s.read_extra(stage, r, 1) * extra_w;
+          store(s.extra_of(a.grad_x, row + r), fmaf(n, c2, fmaf(u, rstd[r], c1)));
+        }
     }
   }
   if (!a.partial) return;
@@ -1003,7 +1015,7 @@ cudaError_t launch_stream(const NormArgs& a, cudaStream_t stream) {
   const auto kernel = norm_stream_kernel<T, kE, kColumns, kR, kStages, kTeam, kShift>;
   const cudaError_t e = set_up(kernel, state, a.dev);
   if (e != cudaSuccess) return e;
-  StreamShape s = make_stream_shape(a.H, kE, kTeam, kColumns, kR, 3 * 32, kStages * kR * kColumns * static_cast<int>(sizeof(T)));
+  StreamShape s = make_stream_shape(a.H, kE, kTeam, kColumns, kR, 3 * 32, kStages * kR * (kColumns * static_cast<int>(sizeof(T)) + 4 * kShift));
   set_groups(s, a.n, kR, a.num_sms, a.period);
   kernel<<<s.groups, s.teams * s.threads, s.bytes, stream>>>(norm_stream(a, sizeof(T), s, kR));
   return cudaGetLastError();
@@ -1018,11 +1030,11 @@ cudaError_t launch_block(const NormArgs& a, cudaStream_t stream) {
 
 template <typename T, int kE, int kColumns, int kTeam, bool kShift, bool kCluster = false>
 cudaError_t launch_stream(NormGradArgs a, cudaStream_t stream) {
-  // (the extra elements of four rows do not fit beside the columns' sums)
+  // (the extra elements of four rows do not fit)
   constexpr int kR = batch_rows<T, kColumns>() / (kShift && kColumns == 8 && sizeof(T) == 2 ? 2 : 1), kStages = stages<T, kE>(2);
   static StreamSetUp state;
   const auto kernel = norm_grad_stream_kernel<T, kE, kColumns, kR, kStages, kTeam, kShift, kCluster>;
-  StreamShape s = make_stream_shape(a.H, kE, kTeam, kColumns, kR, 4 * 32, kStages * kR * 2 * kColumns * static_cast<int>(sizeof(T)));
+  StreamShape s = make_stream_shape(a.H, kE, kTeam, kColumns, kR, 4 * 32, kStages * kR * 2 * (kColumns * static_cast<int>(sizeof(T)) + 4 * kShift));
   const size_t meet = static_cast<size_t>(s.teams) * s.threads * (kColumns + 1) * sizeof(float);
   if (s.bytes < meet) s.bytes = meet;
   int most = 0;
