@@ -875,7 +875,7 @@ def adamw_plan(params, grads, *, state_bits: int = 32, copies=None, weight_decay
 def _scalar(name, value, dtype, index):
     """(value, pointer) of a number or of a device scalar."""
     if not isinstance(value, torch.Tensor):
-        return value, None
+        return int(value) if dtype == torch.int64 else float(value), None
     if value.numel() != 1 or value.dtype != dtype or value.get_device() != index:
         raise ValueError(f"{name} must be a number, or one {dtype} element on the params' device")
     return 0, value.data_ptr()

@@ -9,7 +9,7 @@ param: 3 u of its two terms, and its rounding.
 The codes of 8-bit states follow from the inputs by single operations in 32 bits, each rounded to
 nearest; the same operations in torch give the same bits.
 """
-import math
+import ctypes
 
 import pytest
 import torch
@@ -388,6 +388,29 @@ def test_empty_plans_and_tensors():
         steps(d, bits)
         e = [torch.empty(0, device=DEV)]
         ewg.adamw_step(ewg.adamw_plan(e, [torch.empty(0, device=DEV)], state_bits=bits), 1, lr=1e-3)
+
+
+def test_plans_that_are_none():
+    """Bytes that no plan call wrote, a plan cut off, and one that is a copy."""
+    d = make([3000, 40])
+    plan = plan_of(d, 32, 0.0)
+    L, stream = ewg.lib(), torch.cuda.current_stream().cuda_stream
+    raw = bytes(plan._buffer)
+
+    def step(data, nbytes):
+        buf = (ctypes.c_uint64 * (len(data) // 8)).from_buffer_copy(data)
+        return L.ewg_adamw_step(buf, nbytes, 1, None, 1e-3, None, 0.9, 0.999, 1e-8, 1.0, None, stream)
+    before = d["params"][0].clone()
+    assert step(bytes(len(raw)), len(raw)) == ewg.ERR_INVALID
+    for nbytes in (0, 16, 100):
+        assert step(raw, nbytes) == ewg.ERR_INVALID
+    assert L.ewg_adamw_step(None, 1000, 1, None, 1e-3, None, 0.9, 0.999, 1e-8, 1.0, None, stream) == ewg.ERR_INVALID
+    torch.cuda.synchronize()
+    assert torch.equal(d["params"][0], before)
+    assert step(raw, len(raw)) == ewg.OK
+    e = make([3000, 40])
+    ewg.adamw_step(plan_of(e, 32, 0.0), 1, lr=1e-3)
+    assert torch.equal(d["params"][0], e["params"][0])
 
 
 def test_refusals():

@@ -140,6 +140,36 @@ def test_strides_and_alignment(n, H, pad, lead, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("pad,lead", [(0, 0), (0, 1), (0, 3), (1, 0), (1, 7), (2, 2), (3, 5), (4, 4), (7, 1), (8, 6)])
+@pytest.mark.parametrize("H", [1, 2, 3, 7, 8, 9, 15, 17, 63, 64, 65, 127, 250, 511, 513, 769, 1001, 1025, 2047, 4099, 7167, 8189,
+                               8192])
+def test_rows_of_one_alignment(H, pad, lead, dtype):
+    """All arrays' rows begin at the same places in 16 bytes, whatever these are; what lies before, between and
+    behind the rows is left alone."""
+    w, b = vectors(H, FP32)
+    mg0 = torch.ones(H, device=DEV)
+    for n in (1, 3, 9, 41, 700 if H < 3000 else 160):
+        x, g = rows(n, H, dtype, seed=H, pad=pad, lead=lead), rows(n, H, dtype, seed=9, pad=pad, lead=lead)
+
+        def target():
+            buf = torch.full((n * (H + pad) + lead + 16,), 7.0, dtype=dtype, device=DEV)
+            return buf, buf[lead:lead + n * (H + pad)].view(n, H + pad)[:, :H]
+
+        def check_guard(buf, y):
+            y.fill_(7.0)
+            assert bool((buf == 7.0).all())
+        buf, out = target()
+        r = ewg.layer_norm(x, w, b, out=out)
+        check_forward(x, w, b, 1e-5, r)
+        check_guard(buf, out)
+        buf, out = target()
+        mgs = [mg0.clone(), mg0.clone()]
+        ewg.layer_norm_backward(g, x, r.mean, r.rstd, w, weight_main_grad=mgs[0], bias_main_grad=mgs[1], out=out)
+        check_backward(g, x, r.mean, r.rstd, w, out, [mg0, mg0], mgs)
+        check_guard(buf, out)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
 @pytest.mark.parametrize("vec_dtype", [BF16, FP32])
 @pytest.mark.parametrize("mg_dtype", [BF16, FP32])
 @pytest.mark.parametrize("H", [120, 1001, 4096])
