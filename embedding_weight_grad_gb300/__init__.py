@@ -411,9 +411,13 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+# The current device's index, asked for a tensor of some device (so that there is one).
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _enqueue(index, call, *args):
     """call(*args, current stream) with device `index` current; raises on an error code."""
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         code = call(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
@@ -792,9 +796,12 @@ class AdamWPlan:
         self._index = index
         self._all = [t for group in (params, grads, exp_avg, exp_avg_sq, scales or (), copies or ())
                      for t in group if t is not None]
-        self._addresses = list(map(_data_ptr, self._all))
-        self._written = [t for group in (params, exp_avg, exp_avg_sq, scales or (), copies or ())
-                         for t in group if t is not None]
+        # every step looks whether the params and their gradients are where they were; the others' memory
+        # is the plan's own too, as long as it lives
+        self._moving = params + grads
+        self._addresses = list(map(_data_ptr, self._moving))
+        self._held = [t.detach() for t in self._all]
+        self._written = params + [t for t in copies or () if t is not None]
         self._buffer = None            # of ewg_adamw_plan, and its bytes
         self._bytes = 0
 
@@ -888,12 +895,13 @@ def adamw_step(plan: AdamWPlan, step, *, lr, betas: tuple = (0.9, 0.999), eps: f
     grad_scale multiplies the gradients: a clipping factor, or the inverse of a loss scale.  step
     (int64), lr and grad_scale (fp32) may be CUDA tensors of one element, which the step reads on
     the device: a captured step then follows their values.  The work is enqueued on the current
-    stream.  Raises ValueError if a tensor of the plan has moved to another address.
+    stream.  Raises ValueError if a param or gradient of the plan has moved to another address (states and
+    copies stay the tensors that they were).
     """
     if not plan.params:
         return
-    if list(map(_data_ptr, plan._all)) != plan._addresses:
-        raise ValueError("a tensor of the plan has moved to another address: make a new plan")
+    if list(map(_data_ptr, plan._moving)) != plan._addresses:
+        raise ValueError("a param or gradient of the plan has moved to another address: make a new plan")
     index = plan._index
     step, step_ptr = _scalar("step", step, torch.int64, index)
     lr, lr_ptr = _scalar("lr", lr, torch.float32, index)

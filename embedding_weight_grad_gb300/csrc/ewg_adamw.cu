@@ -340,6 +340,10 @@ cudaError_t launch(const AdamwEntry* entries, int num, const AdamwHyper& h, int 
 
 cudaError_t launch_adamw(const AdamwEntry* entries, int num, int state_bits, const AdamwHyper& h, int num_sms,
                          cudaStream_t stream) {
+  // (a launch's argument is copied whole, whatever it holds)
+  if (num <= kAdamwFew)
+    return state_bits == 32 ? launch<32, kAdamwFew>(entries, num, h, num_sms, stream)
+                            : launch<8, kAdamwFew>(entries, num, h, num_sms, stream);
   return state_bits == 32 ? launch<32, kAdamwEntries>(entries, num, h, num_sms, stream)
                           : launch<8, kAdamwEntries>(entries, num, h, num_sms, stream);
 }

@@ -100,6 +100,7 @@ enum {
 // What a launch carries as its argument: the entries of up to this many tensors, of 32764 bytes that
 // an argument may have.
 constexpr int kAdamwEntries = 400;
+constexpr int kAdamwFew = 48;          // entries of the smaller of two arguments
 
 struct AdamwHyper {
   long long step;

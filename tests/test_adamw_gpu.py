@@ -372,12 +372,17 @@ def test_autograd_is_told_and_moved_tensors_are_refused():
     d = make([100, 200], copy=True)
     d["params"] = [p.requires_grad_() for p in d["params"]]
     plan = plan_of(d, 32, 0.0)
-    versions = [t._version for t in plan.params + plan.copies + plan.exp_avg]
+    versions = [t._version for t in plan.params + plan.copies]
+    grad_version = plan.grads[0]._version
     ewg.adamw_step(plan, 1, lr=1e-3)
-    assert [t._version for t in plan.params + plan.copies + plan.exp_avg] == [v + 1 for v in versions]
-    assert plan.grads[0]._version == d["grads"][0]._version
-    plan.params[0].data = torch.zeros(100, device=DEV)
-    with pytest.raises(ValueError, match="moved"):
+    assert [t._version for t in plan.params + plan.copies] == [v + 1 for v in versions]
+    assert plan.grads[0]._version == grad_version
+    for which in (plan.params, plan.grads):
+        kept = which[0].data
+        which[0].data = torch.zeros(100, device=DEV)
+        with pytest.raises(ValueError, match="moved"):
+            ewg.adamw_step(plan, 2, lr=1e-3)
+        which[0].data = kept
         ewg.adamw_step(plan, 2, lr=1e-3)
 
 
