@@ -638,10 +638,10 @@ def orthogonalize_update(grad: torch.Tensor, *, steps: int = 5,
 
 class LayerNorm(NamedTuple):
     """What layer_norm returns: the normalised rows, and fp32 tensors of x.shape[:-1] that
-    layer_norm_backward takes."""
+    layer_norm_backward takes (None without stats)."""
     out: torch.Tensor
-    mean: torch.Tensor
-    rstd: torch.Tensor             # 1 / sqrt(variance + eps)
+    mean: Optional[torch.Tensor]
+    rstd: Optional[torch.Tensor]   # 1 / sqrt(variance + eps)
 
 
 # (These calls are often bound by the host, so that their checks are few and taken once.)
@@ -682,14 +682,15 @@ def _norm_vectors(name, what, v, w, H, index):
 
 
 def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
-               bias: torch.Tensor | None = None, *, eps: float = 1e-5,
+               bias: torch.Tensor | None = None, *, eps: float = 1e-5, stats: bool = True,
                out: torch.Tensor | None = None) -> LayerNorm:
     """Each row of x [..., hidden] less its mean, over its standard deviation, times weight, plus
     bias (see ewg_layer_norm in include/ewg.h), with the rows' means and 1 / standard deviations.
 
     x: bf16 or fp32, rows of unit inner stride; weight and bias: contiguous [hidden], both bf16 or
     both fp32, whatever x is (without them ones and zeros); out: where to write, of x's shape and
-    dtype; out=x replaces x.  The work is enqueued on the current stream.
+    dtype; out=x replaces x.  stats=False leaves out the means and standard deviations, where
+    nothing goes back through the rows.  The work is enqueued on the current stream.
 
     The results carry no autograd graph: their gradient is layer_norm_backward.
     """
@@ -701,10 +702,13 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
     else:
         out_stride = H
         out = torch.empty_like(x) if stride == H else torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    rstd = torch.empty_like(mean)
+    mean = rstd = mean_ptr = rstd_ptr = None
+    if stats:
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
+        mean_ptr, rstd_ptr = mean.data_ptr(), rstd.data_ptr()
     _enqueue(index, lib().ewg_layer_norm, x.data_ptr(), x_code, n, H, stride, w, b, code, eps,
-             out.data_ptr(), out_stride, mean.data_ptr(), rstd.data_ptr())
+             out.data_ptr(), out_stride, mean_ptr, rstd_ptr)
     if given:
         _written(out)
     return LayerNorm(out, mean, rstd)

@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(kStreamThreads) norm_stream_kernel(const NormS
       // what the centre is off the mean, the deviations' own mean shows
       const float rest = sums[r] * a.inv_h, rstd = rstd_of(rest, sums[kR + r] * a.inv_h, a.eps);
       if (row + r >= s.n) break;
-      if (s.thread == 0) {
+      if (s.thread == 0 && a.mean) {
         a.mean[s.index(row + r)] = centre[r] + rest;
         a.rstd[s.index(row + r)] = rstd;
       }
@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(kBlockThreads) norm_block_kernel(const NormStr
   sums[1] = squares.x + squares.y;
   team_sum<2, 0>(sums, slots[1], 0, threads);
   const float rest = sums[0] * a.inv_h, rstd = rstd_of(rest, sums[1] * a.inv_h, a.eps), shift = -rest * rstd;
-  if (thread == 0) {
+  if (thread == 0 && a.mean) {
     a.mean[row] = centre[0] + rest;
     a.rstd[row] = rstd;
   }
@@ -807,7 +807,7 @@ __global__ void __launch_bounds__(kRowThreads) norm_kernel(NormArgs a) {
   // what `near` is off the mean, the deviations' own mean shows
   const float rest = s.x * a.inv_h;
   const float rstd = rstd_of(rest, s.y * a.inv_h, a.eps);
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 0 && a.mean) {
     a.mean[row] = near + rest;
     a.rstd[row] = rstd;
   }

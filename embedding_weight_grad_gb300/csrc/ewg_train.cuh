@@ -22,7 +22,7 @@ struct NormArgs {
   float inv_h;               // 1 / H
   void* out;
   long long out_stride;
-  float* mean;               // [n] each
+  float* mean;               // [n] each, or both null
   float* rstd;
   int dev, num_sms;
   int period;                // rows whose places in 16 bytes differ (set by the launcher)

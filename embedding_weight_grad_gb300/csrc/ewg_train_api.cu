@@ -153,13 +153,14 @@ int ewg_layer_norm(const void* x, int x_dtype, int64_t rows, int64_t hidden, int
   if (!(eps >= 0) || !std::isfinite(static_cast<float>(eps))) return fail(EWG_ERR_UNSUPPORTED, "eps must be finite and >= 0");
   if ((rc = check_norm_sizes(rows, hidden))) return rc;
   if (rows == 0) return EWG_OK;
+  if (!mean != !rstd) return fail(EWG_ERR_UNSUPPORTED, "mean and rstd belong together");
   const size_t ws = weight || bias ? elem_size(weight_dtype) : 0;
   Array in[3] = {{}, flat("weight", weight, hidden, ws), flat("bias", bias, hidden, ws)};
   Array res[3] = {{}, flat("mean", mean, rows, 4), flat("rstd", rstd, rows, 4)};
   if ((rc = check_rows("x", x, x_dtype, rows, hidden, row_stride, mem, &in[0])) ||
       (rc = check_optional(in[1], ws, mem)) || (rc = check_optional(in[2], ws, mem)) ||
       (rc = check_rows("out", out, x_dtype, rows, hidden, out_row_stride, mem, &res[0])) ||
-      (rc = check_array(res[1], 4, mem)) || (rc = check_array(res[2], 4, mem)))
+      (rc = check_optional(res[1], 4, mem)) || (rc = check_optional(res[2], 4, mem)))
     return rc;
   const bool in_place = same_rows(x, row_stride, out, out_row_stride, rows);
   for (int i = 0; i < 3; ++i) {

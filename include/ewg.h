@@ -405,7 +405,7 @@ int ewg_orthogonalize_transposed(const void* grad, int grad_dtype, int64_t batch
  *           stands for ones and zeros (weight_dtype is then of no account if both are)
  *   out     [rows][hidden] of x's dtype, out_row_stride between rows; apart from every input, or
  *           x itself (same address and stride), which it then replaces
- *   mean, rstd       [rows] fp32
+ *   mean, rstd       [rows] fp32; both NULL: not wanted (nothing goes back through the rows)
  *
  * A row with a NaN or an infinity gives NaN, and so does one whose squared deviations' sum, in
  * fp32, leaves its range.  A row of equal elements has rstd 1 / sqrt(eps); with eps = 0 its results

@@ -262,6 +262,14 @@ def test_small_and_large_numbers(H):
             check_forward(x, w, b, eps, ewg.layer_norm(x, w, b, eps=eps))
 
 
+@pytest.mark.parametrize("H", [24, 1001, 8192, 20000, 40000])
+def test_without_stats(H):
+    x = rows(33, H, BF16, seed=H)
+    w, b = vectors(H, BF16)
+    r = ewg.layer_norm(x, w, b, stats=False)
+    assert r.mean is None and r.rstd is None and torch.equal(r.out, ewg.layer_norm(x, w, b).out)
+
+
 def test_shapes():
     x = rows(12, 96, BF16)
     w, b = vectors(96, BF16)
@@ -326,9 +334,9 @@ def test_gradient_against_differences(H):
             assert abs((grad.double() * v).sum() - slope) < 1e-5 * size
 
 
-def test_same_call_same_bits_and_streams():
+@pytest.mark.parametrize("n,H", [(3001, 2048), (3001, 1001), (700, 12000)])
+def test_same_call_same_bits_and_streams(n, H):
     """Twice on each of two streams at once, and captured and replayed."""
-    n, H = 3001, 2048
     x, g = rows(n, H, BF16, seed=1), rows(n, H, BF16, seed=2)
     w, b = vectors(H, FP32)
     r = ewg.layer_norm(x, w, b)
