@@ -9,7 +9,7 @@
 //     dx = rstd (u - avg(u) - n avg(u n))     dw_j = sum over rows of g n     db_j = sum over rows of g
 //
 // Both are bound by memory: forward each element is read and written once, for its gradient two are read and
-// one written (131072 x 8192 bf16: 668 us, 6.4 TB/s, and 966 us, 6.7 TB/s; 8192 x 7168: 45 and 60 us, where a copy of
+// one written (131072 x 8192 bf16: 616 us, 7.0 TB/s, and 966 us, 6.7 TB/s; 8192 x 7168: 42 and 60 us, where a copy of
 // the forward pass's bytes takes 36).  What stands in the way are the sums over a row: a barrier and a chain of
 // shuffles, during which a team computes nothing else.  So a thread has many elements of a row (sixteen, which
 // spreads the shuffles), several rows go through a sum together, and the rows after them are being copied to
@@ -455,11 +455,18 @@ struct NormStream {
   float eps, inv_h;
 };
 
-template <typename T, int kE, int kColumns, int kR, int kStages, int kTeam, bool kShift>
+// Floats for each of a batch's rows, of a team of several warps.
+__host__ __device__ constexpr int norm_slots(bool ahead) { return (ahead ? 2 * 4 : 3) * 32; }
+
+// A batch takes two sums over its rows, one after the other: the elements', then the deviations' and their squares'.
+// kAhead: the second one goes together with the next batch's first, for one barrier a batch instead of two, and
+// every batch is read from shared memory twice.
+template <typename T, int kE, int kColumns, int kR, int kStages, int kTeam, bool kShift, bool kAhead>
 __global__ void __launch_bounds__(kStreamThreads) norm_stream_kernel(const NormStream a) {
   extern __shared__ float4 shared[];
-  // slots of both sums for every team, then the ring
-  constexpr int kSlots = kTeam ? 0 : 3 * kR * 32, kPairs = kColumns / 2;
+  constexpr int kSums = (kAhead ? 4 : 2) * kR;             // (with kAhead 3 kR, filled up to a power of two)
+  // slots of the sums for every team (with kAhead of two batches, which take turns), then the ring
+  constexpr int kSlots = kTeam ? 0 : norm_slots(kAhead) * kR, kPairs = kColumns / 2;
   const int teams = blockDim.x / (kTeam ? kTeam : a.team_threads);
   float* slots = reinterpret_cast<float*>(shared);
   Stream<T, kE, kColumns, kR, 1, kStages, kTeam, kShift> s(a.team_threads, a.n, a.H, 1, a.period, a.x[0],
@@ -477,21 +484,47 @@ __global__ void __launch_bounds__(kStreamThreads) norm_stream_kernel(const NormS
   s.read_vector(a.bias, a.weight_bf16, 0.0f, b);
   const float extra_w = kShift && s.extra >= 0 && a.weight ? element(a.weight, a.weight_bf16, s.extra) : 1.0f;
   const float extra_b = kShift && s.extra >= 0 && a.bias ? element(a.bias, a.weight_bf16, s.extra) : 0.0f;
-  float extra[kR];
-  for (; turn < s.n; turn += s.step, row += s.step, to += a.out.advance) {
-    const int stage = s.next(a.x);
-    float2 d[kR][kPairs];
-    float centre[kR], sums[2 * kR];
+  int stage = 0, flip = 0;
+  // A row of the batch, and the thread's part of its sum.
+  const auto read = [&](int r, float2 (&x)[kPairs], float& more) {
+    s.read(stage, r, 0, x);
+    float sum = pairs_sum<kPairs>(x);
+    if constexpr (kShift) {
+      more = s.read_extra(stage, r, 0);
+      sum += more;
+    }
+    return sum;
+  };
+  // The next batch's rows' sums alone, into the last ones.
+  const auto next_sums = [&](float (&sums)[kSums]) {
+    stage = s.next(a.x);
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
-      s.read(stage, r, 0, d[r]);
-      centre[r] = pairs_sum<kPairs>(d[r]);
-      if constexpr (kShift) {
-        extra[r] = s.read_extra(stage, r, 0);
-        centre[r] += extra[r];
-      }
+      float2 x[kPairs];
+      float more;
+      sums[kSums / 2 + r] = read(r, x, more);
     }
-    team_sum<kR, kTeam>(centre, slots, s.team, s.threads);
+  };
+  float centre[kR], extra[kR];
+  if constexpr (kAhead) {
+    float sums[kSums] = {};
+    next_sums(sums);
+    team_sum<kSums, kTeam>(sums, slots, s.team, s.threads);
+#pragma unroll
+    for (int r = 0; r < kR; ++r) centre[r] = sums[kSums / 2 + r];
+  }
+  for (; turn < s.n; turn += s.step, row += s.step, to += a.out.advance) {
+    float2 d[kR][kPairs];
+    float sums[kSums];
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int r = 0; r < kR; ++r) read(r, d[r], extra[r]);
+    } else {
+      stage = s.next(a.x);
+#pragma unroll
+      for (int r = 0; r < kR; ++r) centre[r] = read(r, d[r], extra[r]);
+      team_sum<kR, kTeam>(centre, slots + kSums * 32, s.team, s.threads);
+    }
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
       centre[r] = centre_of<T>(centre[r] * a.inv_h);
@@ -510,7 +543,13 @@ __global__ void __launch_bounds__(kStreamThreads) norm_stream_kernel(const NormS
         sums[kR + r] = fmaf(extra[r], extra[r], sums[kR + r]);
       }
     }
-    team_sum<2 * kR, kTeam>(sums, slots + kR * 32, s.team, s.threads);
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int r = 0; r < kR; ++r) sums[3 * kR + r] = 0.0f;
+      next_sums(sums);                     // (the batch itself is in registers)
+      flip ^= 1;
+    }
+    team_sum<kSums, kTeam>(sums, slots + flip * kSums * 32, s.team, s.threads);
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
       // what the centre is off the mean, the deviations' own mean shows
@@ -526,6 +565,10 @@ __global__ void __launch_bounds__(kStreamThreads) norm_stream_kernel(const NormS
       s.write(to + s.bytes_to(a.out, r), d[r]);
       if constexpr (kShift)
         if (s.extra >= 0) store(s.extra_of(a.out, row + r), fmaf(fmaf(extra[r], rstd, shift), extra_w, extra_b));
+    }
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int r = 0; r < kR; ++r) centre[r] = sums[kSums / 2 + r];
     }
   }
 }
@@ -1012,17 +1055,28 @@ NormStream norm_stream(const NormArgs& a, size_t size, const StreamShape& s, int
   return k;
 }
 
-template <typename T, int kE, int kColumns, int kTeam, bool kShift>
+template <typename T, int kE, int kColumns, int kTeam, bool kShift, bool kAhead>
 cudaError_t launch_stream(const NormArgs& a, cudaStream_t stream) {
   constexpr int kR = batch_rows<T, kColumns>(), kStages = stages<T, kE>(1);
   static StreamSetUp state;
-  const auto kernel = norm_stream_kernel<T, kE, kColumns, kR, kStages, kTeam, kShift>;
+  const auto kernel = norm_stream_kernel<T, kE, kColumns, kR, kStages, kTeam, kShift, kAhead>;
   const cudaError_t e = set_up(kernel, state, a.dev);
   if (e != cudaSuccess) return e;
-  StreamShape s = make_stream_shape(a.H, kE, kTeam, kColumns, kR, 3 * 32, kStages * kR * (kColumns * static_cast<int>(sizeof(T)) + 4 * kShift));
+  StreamShape s = make_stream_shape(a.H, kE, kTeam, kColumns, kR, norm_slots(kAhead), kStages * kR * (kColumns * static_cast<int>(sizeof(T)) + 4 * kShift));
   set_groups(s, a.n, kR, a.num_sms, a.period);
   kernel<<<s.groups, s.teams * s.threads, s.bytes, stream>>>(norm_stream(a, sizeof(T), s, kR));
   return cudaGetLastError();
+}
+
+template <typename T, int kE, int kColumns, int kTeam, bool kShift>
+cudaError_t launch_stream(const NormArgs& a, cudaStream_t stream) {
+  // Of up to three teams an SM none may be left to work while the others wait for their sums: taken with the next
+  // batch's these take 616 us instead of 672 for 131072 x 8192 bf16, 42.3 instead of 44.4 for 8192 x 7168, 52.0 instead of
+  // 53.7 for 32768 x 2304; four teams of 2048 columns 44.2 instead of 42.5, fp32 rows of 8192 92 instead of 82.  The first
+  // batch's sums come alone, which few rows do not make up for: 1216 x 7168 takes 11.0 us so, 10.5 without.
+  if constexpr (sizeof(T) == 2 && kE == 8 && kColumns == 16 && kTeam == 0)
+    if (a.H > 2048 && a.n > 16 * a.num_sms) return launch_stream<T, kE, kColumns, kTeam, kShift, true>(a, stream);
+  return launch_stream<T, kE, kColumns, kTeam, kShift, false>(a, stream);
 }
 
 template <typename T, int kE>

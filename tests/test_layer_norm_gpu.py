@@ -252,6 +252,33 @@ def test_nan_and_infinity_stay_in_their_row(H, bad):
         check_backward(g[keep], x[keep], r.mean[keep], r.rstd[keep], w, got[keep])
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("pad", [0, 3])
+@pytest.mark.parametrize("n,H", [(2432, 4096), (2433, 2048), (2435, 2056), (3001, 2303), (2440, 2816), (4864, 4099), (2501, 5000),
+                                 (5003, 7168), (2436, 8189), (2737, 8192)])
+def test_wide_rows_in_number(n, H, pad, dtype):
+    """Every block takes many batches, the last ones short; rows that hold no numbers are nobody else's matter."""
+    x = rows(n, H, dtype, seed=H, pad=pad)
+    w, b = vectors(H, dtype)
+    r = ewg.layer_norm(x, w, b)
+    check_forward(x, w, b, 1e-5, r)
+    y = x.clone()
+    r2 = ewg.layer_norm(y, w, b, out=y)
+    if pad == 0:
+        assert torch.equal(r2.out, r.out) and torch.equal(r2.mean, r.mean) and torch.equal(r2.rstd, r.rstd)
+        assert torch.equal(ewg.layer_norm(x, w, b, stats=False).out, r.out)
+    bad = torch.arange(5, n, 7, device=DEV)
+    x[bad[0::3], 0] = float("nan")
+    x[bad[1::3], H - 1] = float("inf")
+    x[bad[2::3], H // 2] = -float("inf")
+    r2 = ewg.layer_norm(x, w, b)
+    assert bool(r2.out[bad].isnan().all()) and bool(r2.rstd[bad].isnan().all())
+    keep = torch.ones(n, dtype=torch.bool, device=DEV)
+    keep[bad] = False
+    assert torch.equal(r2.out[keep], r.out[keep]) and torch.equal(r2.mean[keep], r.mean[keep])
+    assert torch.equal(r2.rstd[keep], r.rstd[keep])
+
+
 @pytest.mark.parametrize("H", [16, 1001, 7168])
 def test_small_and_large_numbers(H):
     """Sums of squares stay in range from 2^-60 to 2^50; eps takes over for the smallest."""
