@@ -19,6 +19,12 @@ using namespace ewg::host;
 
 bool is_float(int dtype) { return dtype == EWG_BF16 || dtype == EWG_FP32; }
 
+// eps is added in fp32, where 1 / eps has to be a number too (a subnormal one counts as 0 in some operations).
+int check_eps(double eps) {
+  if (eps == 0 || (eps >= 0x1p-126 && eps <= 0x1p126)) return EWG_OK;
+  return fail(EWG_ERR_UNSUPPORTED, "eps must be 0 or in [2^-126, 2^126]");
+}
+
 int check_norm_sizes(int64_t rows, int64_t hidden) {
   if (rows < 0 || rows > INT32_MAX) return fail(EWG_ERR_UNSUPPORTED, "rows outside [0, 2^31)");
   if (hidden < 1 || hidden > EWG_MAX_HIDDEN) return fail(EWG_ERR_UNSUPPORTED, "hidden outside [1, EWG_MAX_HIDDEN]");
@@ -150,7 +156,7 @@ int ewg_layer_norm(const void* x, int x_dtype, int64_t rows, int64_t hidden, int
   DeviceMemory mem(dev);
   if (!is_float(x_dtype)) return fail(EWG_ERR_UNSUPPORTED, "x must be bf16 or fp32");
   if ((weight || bias) && !is_float(weight_dtype)) return fail(EWG_ERR_UNSUPPORTED, "weight and bias must be bf16 or fp32");
-  if (!(eps >= 0) || !std::isfinite(static_cast<float>(eps))) return fail(EWG_ERR_UNSUPPORTED, "eps must be finite and >= 0");
+  if ((rc = check_eps(eps))) return rc;
   if ((rc = check_norm_sizes(rows, hidden))) return rc;
   if (rows == 0) return EWG_OK;
   if (!mean != !rstd) return fail(EWG_ERR_UNSUPPORTED, "mean and rstd belong together");
@@ -291,7 +297,7 @@ int ewg_adamw_step(const void* plan, size_t plan_bytes, int64_t step, const int6
   if (!grad_scale_on_device && !fine(grad_scale)) return fail(EWG_ERR_UNSUPPORTED, "grad_scale must be finite");
   for (double b : {beta1, beta2})
     if (!(b >= 0 && static_cast<float>(b) < 1.0f)) return fail(EWG_ERR_UNSUPPORTED, "betas must be in [0, 1)");
-  if (!(fine(eps) && eps >= 0)) return fail(EWG_ERR_UNSUPPORTED, "eps must be finite and >= 0");
+  if ((rc = check_eps(eps))) return rc;
   DeviceMemory mem(dev);
   if ((rc = check_optional(flat("step", step_on_device, 1, 8), 8, mem)) ||
       (rc = check_optional(flat("lr", lr_on_device, 1, 4), 4, mem)) ||

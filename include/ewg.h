@@ -408,11 +408,12 @@ int ewg_orthogonalize_transposed(const void* grad, int grad_dtype, int64_t batch
  *   mean, rstd       [rows] fp32; both NULL: not wanted (nothing goes back through the rows)
  *
  * A row with a NaN or an infinity gives NaN, and so does one whose squared deviations' sum, in
- * fp32, leaves its range.  A row of equal elements has rstd 1 / sqrt(eps); with eps = 0 its results
- * mean nothing.
+ * fp32, leaves its range.  A row of equal elements has rstd 1 / sqrt(eps); its
+ * results mean nothing with an eps of 0, or one that is not large beside the square of the mean's
+ * rounding (2^-24 of the mean).
  *
- * Requires 0 <= rows < 2^31 (0: nothing is enqueued), 1 <= hidden <= EWG_MAX_HIDDEN, finite
- * eps >= 0.  Enqueues one kernel; allocates nothing.
+ * Requires 0 <= rows < 2^31 (0: nothing is enqueued), 1 <= hidden <= EWG_MAX_HIDDEN, and an eps
+ * of 0 or in [2^-126, 2^126].  Enqueues one kernel; allocates nothing.
  */
 int ewg_layer_norm(const void* x, int x_dtype, int64_t rows, int64_t hidden, int64_t row_stride,
                    const void* weight, const void* bias, int weight_dtype, double eps, void* out,
@@ -518,7 +519,8 @@ int ewg_adamw_plan(const ewg_adamw_tensor* tensors, int64_t num_tensors, int sta
  *           scalar (int64, fp32, fp32) that is read in the value's place (a step below 1 as 1),
  *           so that a captured call follows a schedule
  *
- * Requires step >= 1, finite lr >= 0, 0 <= beta1, beta2 < 1, finite eps >= 0, finite grad_scale.
+ * Requires step >= 1, finite lr >= 0, 0 <= beta1, beta2 < 1, an eps of 0 or in [2^-126, 2^126], finite
+ * grad_scale.
  * Every element's result depends on its own tensor alone: the same bits in any plan.  Enqueues one
  * kernel for every 400 tensors; allocates nothing.
  */

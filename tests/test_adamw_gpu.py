@@ -238,6 +238,27 @@ def test_no_gradient_so_far(bits):
 
 
 @pytest.mark.parametrize("bits", [32, 8])
+def test_the_ends_of_eps(bits):
+    """Elements without a gradient stay at the least eps too; the largest stops every element's way.  What lies
+    outside would be 0 or infinite in fp32, or have such an inverse."""
+    d = make([2000], bits=bits)
+    for key in ("grads", "exp_avg", "exp_avg_sq"):
+        d[key][0].view(torch.uint8 if d[key][0].dtype == E4M3 else d[key][0].dtype)[100:300] = 0
+    p = d["params"][0].clone()
+    plan = plan_of(d, bits, 0.0)
+    for eps in (1e-320, 1e-46, 1e-40, 2.0 ** -127, 2.0 ** 127, 1e39, float("inf")):
+        with pytest.raises(ewg.EwgError, match="eps"):
+            ewg.adamw_step(plan, 5, lr=1e-2, eps=eps)
+    assert torch.equal(d["params"][0], p)
+    ewg.adamw_step(plan, 5, lr=1e-2, eps=2.0 ** -126)
+    assert torch.equal(d["params"][0][100:300], p[100:300]) and bool(d["params"][0].isfinite().all())
+    assert not bool((d["params"][0] == p)[:100].all())
+    p = d["params"][0].clone()
+    ewg.adamw_step(plan, 6, lr=1e-2, eps=2.0 ** 126)
+    assert torch.equal(d["params"][0], p)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 def test_a_gradient_that_is_not_finite(bad, bits):
     """Its element becomes NaN; in 8 bits its block's state too, and no other block's."""

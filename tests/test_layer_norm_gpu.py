@@ -279,6 +279,19 @@ def test_wide_rows_in_number(n, H, pad, dtype):
     assert torch.equal(r2.rstd[keep], r.rstd[keep])
 
 
+@pytest.mark.parametrize("H", [16, 1024, 8192, 32768, 131072])
+def test_the_ends_of_eps(H):
+    """A row of equal elements whose mean is exact gives the bias at the least eps too."""
+    x = torch.full((3, H), 2.0, device=DEV)
+    w, b = vectors(H, FP32)
+    for eps in (1e-320, 1e-46, 1e-40, 2.0 ** -127, 2.0 ** 127, 1e39, float("inf")):
+        with pytest.raises(ewg.EwgError, match="eps"):
+            ewg.layer_norm(x, w, b, eps=eps)
+    for eps in (2.0 ** -126, 2.0 ** 126):
+        r = ewg.layer_norm(x, w, b, eps=eps)
+        assert torch.equal(r.out, b.expand(3, H)) and bool((r.rstd == eps ** -0.5).all())
+
+
 @pytest.mark.parametrize("H", [16, 1001, 7168])
 def test_small_and_large_numbers(H):
     """Sums of squares stay in range from 2^-60 to 2^50; eps takes over for the smallest."""
