@@ -23,7 +23,8 @@
 // Tried and slower: every thread's next row in registers instead of shared memory (8192 x 7168 backward 96 us),
 // 1024 threads of eight columns (85 us), deviations from the average of a row's first 32 elements,
 // which saves one of the forward pass's two barriers (48 us), twice the rows in a batch, read again from shared memory
-// for each sum (45 us, and 65536 x 1024 46 instead of 44).
+// for each sum (45 us, and 65536 x 1024 46 instead of 44), a cluster's sums by asynchronous stores that an mbarrier counts
+// (4096 x 16384 backward 81 us instead of 87 in bf16, but 163 instead of 139 in fp32).
 #include <atomic>
 #include <cfloat>
 
@@ -241,25 +242,28 @@ __device__ __forceinline__ void team_sum(float (&v)[kM], float* slots, int team,
   }
 }
 
-// Sums of kM numbers over the blocks of a cluster, all threads of each having its own; `box` [2][kMostBlocks][kM]
-// is in every block's shared memory, its halves taken in turn, so that one barrier is enough.
+// Sums of kM numbers over the blocks of a cluster, all threads of each having its own: they leave in cluster_send and
+// arrive in cluster_take.  `box` [2][kMostBlocks][kM] is in every block's shared memory, its halves taken in
+// turn, so that one barrier is enough: who sends into a half has seen all threads arrive that read it before.
 constexpr int kMostBlocks = 8;          // of a cluster, as many as any device runs
 
-template <int kM, int kBox>
-__device__ __forceinline__ void cluster_sum(float (&v)[kM], float (&box)[2][kMostBlocks][kBox], int& flip, int blocks, int rank) {
-  static_assert(kM <= kBox);
+template <int kM>
+__device__ __forceinline__ void cluster_send(const float (&v)[kM], float (&box)[kMostBlocks][kM], int blocks, int rank) {
   if (threadIdx.x < blocks) {
-    const uint32_t to = ptx::map_to_rank(ptx::smem_u32(&box[flip][rank][0]), threadIdx.x);
+    const uint32_t to = ptx::map_to_rank(ptx::smem_u32(&box[rank][0]), threadIdx.x);
 #pragma unroll
     for (int i = 0; i < kM; ++i) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 4 * i), "f"(v[i]) : "memory");
   }
-  ptx::cluster_sync_all();
+  ptx::cluster_arrive();
+}
+template <int kM>
+__device__ __forceinline__ void cluster_take(float (&v)[kM], const float (&box)[kMostBlocks][kM], int blocks) {
+  ptx::cluster_wait();
 #pragma unroll
   for (int i = 0; i < kM; ++i) v[i] = 0.0f;
   for (int b = 0; b < blocks; ++b)
 #pragma unroll
-    for (int i = 0; i < kM; ++i) v[i] += box[flip][b][i];
-  flip ^= 1;
+    for (int i = 0; i < kM; ++i) v[i] += box[b][i];
 }
 
 // ---- rows that a block holds (or, for the gradient of those of more than 8192 elements, a cluster of up to
@@ -411,6 +415,10 @@ struct Stream {
     if constexpr (kBytes > 2) ptx::cp_async_wait<kStages - 1>();
     stage = now == kStages - 1 ? 0 : now + 1;
     return now;
+  }
+  // Waits for all copies but those of the last kStages - 2 batches (where two batches are in use).
+  __device__ __forceinline__ void wait_for_next() const {
+    if constexpr (kBytes > 2) ptx::cp_async_wait<kStages - 2>();
   }
   __device__ __forceinline__ void read(int st, int r, int array, float2 (&f)[kPairs]) const {
     read_pairs<T, kE, kPairs>(place(st, r, array), blockDim.x * kBytes, f);
@@ -662,7 +670,6 @@ struct NormGradStream {
 template <typename T, int kE, int kColumns, int kR, int kStages, int kTeam, bool kShift, bool kCluster>
 __global__ void __launch_bounds__(kStreamThreads) norm_grad_stream_kernel(const NormGradStream a) {
   extern __shared__ float4 shared[];
-  __shared__ float box[2][kCluster ? kMostBlocks : 1][kCluster ? 2 * kR : 1];
   const int blocks = kCluster ? a.blocks : 1;
   ptx::pdl_launch_dependents();
   // two batches' slots for every team, then the ring
@@ -683,7 +690,6 @@ __global__ void __launch_bounds__(kStreamThreads) norm_grad_stream_kernel(const 
     }
   };
   moments(row);
-  int box_flip = 0;
   if constexpr (kCluster) ptx::cluster_sync_all();         // (all blocks are there before their memory is written)
   if constexpr (kSlots > 0) {
     for (int i = threadIdx.x; i < teams * kSlots; i += blockDim.x) slots[i] = 0.0f;
@@ -697,12 +703,8 @@ __global__ void __launch_bounds__(kStreamThreads) norm_grad_stream_kernel(const 
   const float extra_w = kShift && s.extra >= 0 && a.weight ? element(a.weight, a.weight_bf16, s.extra) : 1.0f;
   float extra_dw = 0.0f, extra_db = 0.0f;
   int flip = 0;
-  for (; turn < s.n; turn += s.step, row += s.step, to += a.grad_x.advance, flip ^= 1) {
-    const int stage = s.next(a.in);
-    float mean[kR], rstd[kR], sums[2 * kR];
-#pragma unroll
-    for (int r = 0; r < kR; ++r) mean[r] = means[r], rstd[r] = rstds[r];
-    moments(row + s.step);
+  // A batch's sums over the thread's columns, and what it adds to the columns' own.
+  const auto add_up = [&](int stage, const float (&mean)[kR], const float (&rstd)[kR], float (&sums)[2 * kR]) {
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
       float2 x[kPairs], g[kPairs], s1 = both(0.0f), s2 = both(0.0f);
@@ -727,8 +729,11 @@ __global__ void __launch_bounds__(kStreamThreads) norm_grad_stream_kernel(const 
       }
     }
     team_sum<2 * kR, kTeam>(sums, slots + flip * 2 * kR * 32, s.team, s.threads);
-    if constexpr (kCluster) cluster_sum(sums, box, box_flip, blocks, static_cast<int>(ptx::cluster_rank()));
-    // the rows are read again rather than kept: registers hold the columns' sums
+    flip ^= 1;
+  };
+  // Its gradient, from the sums over its rows.  The rows are read again rather than kept: registers hold the
+  // columns' sums.
+  const auto write = [&](int stage, const float (&mean)[kR], const float (&rstd)[kR], const float (&sums)[2 * kR]) {
     asm volatile("" ::: "memory");
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
@@ -749,6 +754,52 @@ __global__ void __launch_bounds__(kStreamThreads) norm_grad_stream_kernel(const 
           const float n = (s.read_extra(stage, r, 0) - mean[r]) * rstd[r], u = s.read_extra(stage, r, 1) * extra_w;
           store(s.extra_of(a.grad_x, row + r), fmaf(n, c2, fmaf(u, rstd[r], c1)));
         }
+    }
+  };
+  float mean[kR], rstd[kR], sums[2 * kR];
+  const auto take_moments = [&](uint32_t next) {
+#pragma unroll
+    for (int r = 0; r < kR; ++r) mean[r] = means[r], rstd[r] = rstds[r];
+    moments(next);
+  };
+  if constexpr (!kCluster) {
+    for (; turn < s.n; turn += s.step, row += s.step, to += a.grad_x.advance) {
+      const int stage = s.next(a.in);
+      take_moments(row + s.step);
+      add_up(stage, mean, rstd, sums);
+      write(stage, mean, rstd, sums);
+    }
+  } else if (row < s.n) {
+    // A cluster's sums take their time: the next batch's are sent before a batch is written (4096 x 16384 bf16: 87 us
+    // instead of 89, fp32 139 instead of 160; 1024 x 65536 bf16: 113 instead of 122).  Two batches are in use then,
+    // and the copies of one or two more on their way.
+    __shared__ float box[2][kMostBlocks][2 * kR];
+    const int rank = static_cast<int>(ptx::cluster_rank());
+    int stage = 0;
+    s.wait_for_next();
+    take_moments(row + s.step);
+    add_up(stage, mean, rstd, sums);
+    cluster_send(sums, box[0], blocks, rank);
+    s.copy(kStages - 1, a.in);
+    for (int half = 0;; half ^= 1) {
+      float total[2 * kR], mean_now[kR], rstd_now[kR];
+      cluster_take(total, box[half], blocks);
+#pragma unroll
+      for (int r = 0; r < kR; ++r) mean_now[r] = mean[r], rstd_now[r] = rstd[r];
+      const bool more = row + s.step < s.n;
+      const int next = stage == kStages - 1 ? 0 : stage + 1;
+      if (more) {
+        s.wait_for_next();
+        take_moments(row + 2 * s.step);
+        add_up(next, mean, rstd, sums);
+        cluster_send(sums, box[half ^ 1], blocks, rank);
+      }
+      write(stage, mean_now, rstd_now, total);
+      if (!more) break;
+      s.copy(stage, a.in);
+      stage = next;
+      row += s.step;
+      to += a.grad_x.advance;
     }
   }
   if (!a.partial) return;
@@ -1035,7 +1086,7 @@ cudaError_t groups_at_once(K kernel, StreamSetUp& state, StreamShape s, int dev,
 template <typename T, int kColumns>
 constexpr int batch_rows() { return 64 / (kColumns * static_cast<int>(sizeof(T))); }
 template <typename T, int kE>
-constexpr int stages(int arrays) { return kE * sizeof(T) == 2 ? 1 : sizeof(T) == 4 && arrays == 1 ? 4 : 3; }
+constexpr int stages(int arrays, bool cluster) { return kE * sizeof(T) == 2 ? 1 + cluster : sizeof(T) == 4 && arrays == 1 ? 4 : 3; }
 
 NormStream norm_stream(const NormArgs& a, size_t size, const StreamShape& s, int rows) {
   NormStream k{};
@@ -1057,7 +1108,7 @@ NormStream norm_stream(const NormArgs& a, size_t size, const StreamShape& s, int
 
 template <typename T, int kE, int kColumns, int kTeam, bool kShift, bool kAhead>
 cudaError_t launch_stream(const NormArgs& a, cudaStream_t stream) {
-  constexpr int kR = batch_rows<T, kColumns>(), kStages = stages<T, kE>(1);
+  constexpr int kR = batch_rows<T, kColumns>(), kStages = stages<T, kE>(1, false);
   static StreamSetUp state;
   const auto kernel = norm_stream_kernel<T, kE, kColumns, kR, kStages, kTeam, kShift, kAhead>;
   const cudaError_t e = set_up(kernel, state, a.dev);
@@ -1089,7 +1140,7 @@ cudaError_t launch_block(const NormArgs& a, cudaStream_t stream) {
 template <typename T, int kE, int kColumns, int kTeam, bool kShift, bool kCluster = false>
 cudaError_t launch_stream(NormGradArgs a, cudaStream_t stream) {
   // (the extra elements of four rows do not fit)
-  constexpr int kR = batch_rows<T, kColumns>() / (kShift && kColumns == 8 && sizeof(T) == 2 ? 2 : 1), kStages = stages<T, kE>(2);
+  constexpr int kR = batch_rows<T, kColumns>() / (kShift && kColumns == 8 && sizeof(T) == 2 ? 2 : 1), kStages = stages<T, kE>(2, kCluster);
   static StreamSetUp state;
   const auto kernel = norm_grad_stream_kernel<T, kE, kColumns, kR, kStages, kTeam, kShift, kCluster>;
   StreamShape s = make_stream_shape(a.H, kE, kTeam, kColumns, kR, 4 * 32, kStages * kR * 2 * (kColumns * static_cast<int>(sizeof(T)) + 4 * kShift));
