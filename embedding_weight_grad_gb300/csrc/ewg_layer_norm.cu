@@ -581,65 +581,78 @@ __global__ void __launch_bounds__(kStreamThreads) norm_stream_kernel(const NormS
   }
 }
 
-// A block takes one row, 32 elements a thread in registers; several blocks of an SM hide one another's sums.
+// A block takes a row at a time, 32 elements a thread in registers; several blocks of an SM hide one another's sums.
+// kStages: a block stays on its SM and the rows that it takes after this one are being copied ahead; 0: it takes one.
 constexpr int kBlockThreads = 1024, kBlockPairs = 16;
-constexpr int kBlockHidden = kBlockThreads * 2 * kBlockPairs;
+constexpr int kBlockHidden = kBlockThreads * 2 * kBlockPairs, kBlockStages = 2;
 
-template <typename T, int kE>
+template <typename T, int kE, int kStages>
 __global__ void __launch_bounds__(kBlockThreads) norm_block_kernel(const NormStream a) {
+  extern __shared__ float4 shared[];
   __shared__ float slots[2][2 * 32];
   const int threads = blockDim.x, thread = threadIdx.x;
-  const int count = thread < a.H / kE ? (a.H / kE - thread + threads - 1) / threads : 0;
-  const long long row = blockIdx.x;
-  const T* x = reinterpret_cast<const T*>(a.x[0].p + row * a.x[0].pitch) + thread * kE;
-  float2 d[kBlockPairs];
-#pragma unroll
-  for (int i = 0; i < kBlockPairs; ++i) d[i] = both(0.0f);
-#pragma unroll
-  for (int k = 0; k < 2 * kBlockPairs / kE; ++k) {
-    if (k >= count) continue;
-    if constexpr (kE == 1) (k % 2 ? d[k / 2].y : d[k / 2].x) = load(x + k * threads);
-    else Access<T, kE>::unpack(*reinterpret_cast<const typename Access<T, kE>::Raw*>(x + k * threads * kE), d + k * kE / 2);
-  }
+  using S = Stream<T, kE, 2 * kBlockPairs, 1, 1, kStages ? kStages : 1, 0, false>;
+  S s(threads, a.n, a.H, 1, 1, a.x[0], reinterpret_cast<char*>(shared));
+  const int count = s.count;
+  uint32_t row = s.row;
+  char* to = const_cast<char*>(s.begin(a.out));
+  if constexpr (kStages > 0) s.start(a.x);
   if (thread < 2 * 32) slots[0][thread] = slots[1][thread] = 0.0f;
   __syncthreads();
-  float centre[1] = {pairs_sum<kBlockPairs>(d)}, sums[2];
-  team_sum<1, 0>(centre, slots[0], 0, threads);
-  centre[0] = centre_of<T>(centre[0] * a.inv_h);
-  float2 squares = both(0.0f);
+  for (; row < a.n; row += gridDim.x, to += a.out.advance) {
+    float2 d[kBlockPairs];
+    if constexpr (kStages > 0) {
+      s.read(s.next(a.x), 0, 0, d);
+    } else {
+      const T* x = reinterpret_cast<const T*>(s.begin(a.x[0]));
 #pragma unroll
-  for (int i = 0; i < kBlockPairs; ++i) {
-    d[i] = sub2(d[i], make_float2(2 * i / kE < count ? centre[0] : 0.0f, (2 * i + 1) / kE < count ? centre[0] : 0.0f));
-    squares = fma2(d[i], d[i], squares);
-  }
-  sums[0] = pairs_sum<kBlockPairs>(d);
-  sums[1] = squares.x + squares.y;
-  team_sum<2, 0>(sums, slots[1], 0, threads);
-  const float rest = sums[0] * a.inv_h, rstd = rstd_of(rest, sums[1] * a.inv_h, a.eps), shift = -rest * rstd;
-  if (thread == 0 && a.mean) {
-    a.mean[row] = centre[0] + rest;
-    a.rstd[row] = rstd;
-  }
-  T* out = reinterpret_cast<T*>(const_cast<char*>(a.out.p) + row * a.out.pitch) + thread * kE;
+      for (int i = 0; i < kBlockPairs; ++i) d[i] = both(0.0f);
 #pragma unroll
-  for (int k = 0; k < 2 * kBlockPairs / kE; ++k) {
-    if (k >= count) continue;
-    constexpr int kP = kE > 1 ? kE / 2 : 1;
-    float2 w[kP], b[kP], y[kP];
-#pragma unroll
-    for (int i = 0; i < kP; ++i) w[i] = both(1.0f), b[i] = both(0.0f);
-    const int j = (k * threads + thread) * kE;
-    if (a.weight && a.weight_bf16) vector_part<__nv_bfloat16, kE>(static_cast<const __nv_bfloat16*>(a.weight) + j, w);
-    else if (a.weight) vector_part<float, kE>(static_cast<const float*>(a.weight) + j, w);
-    if (a.bias && a.weight_bf16) vector_part<__nv_bfloat16, kE>(static_cast<const __nv_bfloat16*>(a.bias) + j, b);
-    else if (a.bias) vector_part<float, kE>(static_cast<const float*>(a.bias) + j, b);
-#pragma unroll
-    for (int i = 0; i < kP; ++i) {
-      const float2 v = kE > 1 ? d[k * kP + i] : both(k % 2 ? d[k / 2].y : d[k / 2].x);
-      y[i] = fma2(fma2(v, both(rstd), both(shift)), w[i], b[i]);
+      for (int k = 0; k < 2 * kBlockPairs / kE; ++k) {
+        if (k >= count) continue;
+        if constexpr (kE == 1) (k % 2 ? d[k / 2].y : d[k / 2].x) = load(x + k * threads);
+        else Access<T, kE>::unpack(*reinterpret_cast<const typename Access<T, kE>::Raw*>(x + k * threads * kE), d + k * kE / 2);
+      }
     }
-    if constexpr (kE == 1) store(out + k * threads, y[0].x);
-    else *reinterpret_cast<typename Access<T, kE>::Raw*>(out + k * threads * kE) = Access<T, kE>::pack(y);
+    float centre[1] = {pairs_sum<kBlockPairs>(d)}, sums[2];
+    team_sum<1, 0>(centre, slots[0], 0, threads);
+    centre[0] = centre_of<T>(centre[0] * a.inv_h);
+    float2 squares = both(0.0f);
+#pragma unroll
+    for (int i = 0; i < kBlockPairs; ++i) {
+      d[i] = sub2(d[i], make_float2(2 * i / kE < count ? centre[0] : 0.0f, (2 * i + 1) / kE < count ? centre[0] : 0.0f));
+      squares = fma2(d[i], d[i], squares);
+    }
+    sums[0] = pairs_sum<kBlockPairs>(d);
+    sums[1] = squares.x + squares.y;
+    team_sum<2, 0>(sums, slots[1], 0, threads);
+    const float rest = sums[0] * a.inv_h, rstd = rstd_of(rest, sums[1] * a.inv_h, a.eps), shift = -rest * rstd;
+    if (thread == 0 && a.mean) {
+      a.mean[row] = centre[0] + rest;
+      a.rstd[row] = rstd;
+    }
+    T* out = reinterpret_cast<T*>(to);
+#pragma unroll
+    for (int k = 0; k < 2 * kBlockPairs / kE; ++k) {
+      if (k >= count) continue;
+      constexpr int kP = kE > 1 ? kE / 2 : 1;
+      float2 w[kP], b[kP], y[kP];
+#pragma unroll
+      for (int i = 0; i < kP; ++i) w[i] = both(1.0f), b[i] = both(0.0f);
+      const int j = (k * threads + thread) * kE;
+      if (a.weight && a.weight_bf16) vector_part<__nv_bfloat16, kE>(static_cast<const __nv_bfloat16*>(a.weight) + j, w);
+      else if (a.weight) vector_part<float, kE>(static_cast<const float*>(a.weight) + j, w);
+      if (a.bias && a.weight_bf16) vector_part<__nv_bfloat16, kE>(static_cast<const __nv_bfloat16*>(a.bias) + j, b);
+      else if (a.bias) vector_part<float, kE>(static_cast<const float*>(a.bias) + j, b);
+#pragma unroll
+      for (int i = 0; i < kP; ++i) {
+        const float2 v = kE > 1 ? d[k * kP + i] : both(k % 2 ? d[k / 2].y : d[k / 2].x);
+        y[i] = fma2(fma2(v, both(rstd), both(shift)), w[i], b[i]);
+      }
+      if constexpr (kE == 1) store(out + k * threads, y[0].x);
+      else *reinterpret_cast<typename Access<T, kE>::Raw*>(out + k * threads * kE) = Access<T, kE>::pack(y);
+    }
+    if constexpr (kStages == 0) break;
   }
 }
 
@@ -1130,10 +1143,21 @@ cudaError_t launch_stream(const NormArgs& a, cudaStream_t stream) {
   return launch_stream<T, kE, kColumns, kTeam, kShift, false>(a, stream);
 }
 
-template <typename T, int kE>
+int block_threads(int H) { return ((H + 2 * kBlockPairs - 1) / (2 * kBlockPairs) + 31) / 32 * 32; }
+
+template <typename T, int kE, int kStages>
 cudaError_t launch_block(const NormArgs& a, cudaStream_t stream) {
-  const StreamShape s{((a.H + 2 * kBlockPairs - 1) / (2 * kBlockPairs) + 31) / 32 * 32, 1, 1, 1, 0};
-  norm_block_kernel<T, kE><<<a.n, s.threads, 0, stream>>>(norm_stream(a, sizeof(T), s, 1));
+  static StreamSetUp state;
+  const auto kernel = norm_block_kernel<T, kE, kStages>;
+  StreamShape s{block_threads(a.H), 1, 1, a.n, 0};
+  if constexpr (kStages > 0) {
+    s.bytes = static_cast<size_t>(s.threads) * kStages * 2 * kBlockPairs * sizeof(T);
+    const cudaError_t e = set_up(kernel, state, a.dev);
+    if (e != cudaSuccess) return e;
+    const int most = a.num_sms * (kBlockThreads / s.threads);
+    if (s.groups > most) s.groups = most;
+  }
+  kernel<<<s.groups, s.threads, s.bytes, stream>>>(norm_stream(a, sizeof(T), s, 1));
   return cudaGetLastError();
 }
 
@@ -1255,7 +1279,19 @@ cudaError_t forward(NormArgs a, cudaStream_t stream) {
     norm_kernel<T><<<a.n, kRowThreads, 0, stream>>>(a);
     return cudaGetLastError();
   }
-  if (a.H > kStreamHidden) return form == kWholeRows ? launch_block<T, kE>(a, stream) : launch_block<T, 1>(a, stream);
+  if (a.H > kStreamHidden) {
+    if (form != kWholeRows) return launch_block<T, 1, 0>(a, stream);
+    // bf16 rows are copied ahead where the weights and biases still fit into the L1 cache beside the rings (4096 x
+    // 12288: 47 us instead of 51; 16384 with fp32 vectors, which do not, 61 instead of 59), and where the
+    // SM has no other block (2048 x 24576: 53 instead of 64, 32768: 69 instead of 79).
+    if constexpr (sizeof(T) == 2) {
+      const int blocks = kBlockThreads / block_threads(a.H);
+      const size_t rings = static_cast<size_t>(blocks) * a.H * sizeof(T) * kBlockStages;
+      const size_t vectors = static_cast<size_t>((a.weight != nullptr) + (a.bias != nullptr)) * a.H * (a.weight_bf16 ? 2 : 4);
+      if (blocks == 1 || rings + vectors <= 216 * 1024) return launch_block<T, kE, kBlockStages>(a, stream);
+    }
+    return launch_block<T, kE, 0>(a, stream);
+  }
   return form == kWholeRows     ? stream_rows<T, kE, false>(a, stream)
          : form == kShiftedRows ? stream_rows<T, kE, true>(a, stream)
                                 : stream_rows<T, 1, false>(a, stream);

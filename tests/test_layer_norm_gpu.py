@@ -279,6 +279,34 @@ def test_wide_rows_in_number(n, H, pad, dtype):
     assert torch.equal(r2.rstd[keep], r.rstd[keep])
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("vec_dtype", [BF16, FP32])
+@pytest.mark.parametrize("n,H", [(1001, 9000), (701, 12288), (701, 16384), (333, 24576), (307, 32768), (95, 65536), (401, 8193)])
+def test_rows_of_more_than_8192_in_number(n, H, vec_dtype, dtype):
+    """Every block and cluster takes several batches, in place too; rows that hold no numbers are nobody else's matter."""
+    x = rows(n, H, dtype, seed=H)
+    w, b = vectors(H, vec_dtype)
+    r, g, got = both(x, w, b)
+    y = x.clone()
+    r2 = ewg.layer_norm(y, w, b, out=y)
+    assert torch.equal(r2.out, r.out) and torch.equal(r2.mean, r.mean) and torch.equal(r2.rstd, r.rstd)
+    for target in (0, 1):
+        pair = [g.clone(), x.clone()]
+        assert torch.equal(ewg.layer_norm_backward(*pair, r.mean, r.rstd, w, out=pair[target]), got)
+    bad = torch.arange(3, n, 5, device=DEV)
+    x[bad[0::3], 0] = float("nan")
+    x[bad[1::3], H - 1] = float("inf")
+    x[bad[2::3], H // 2] = -float("inf")
+    r2 = ewg.layer_norm(x, w, b)
+    assert bool(r2.out[bad].isnan().all()) and bool(r2.rstd[bad].isnan().all())
+    got2 = ewg.layer_norm_backward(g, x, r2.mean, r2.rstd, w)
+    assert bool(got2[bad].isnan().all())
+    keep = torch.ones(n, dtype=torch.bool, device=DEV)
+    keep[bad] = False
+    for a, c in ((r2.out, r.out), (r2.mean, r.mean), (r2.rstd, r.rstd), (got2, got)):
+        assert torch.equal(a[keep], c[keep])
+
+
 @pytest.mark.parametrize("H", [16, 1024, 8192, 32768, 131072])
 def test_the_ends_of_eps(H):
     """A row of equal elements whose mean is exact gives the bias at the least eps too."""
