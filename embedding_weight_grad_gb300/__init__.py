@@ -738,8 +738,9 @@ def layer_norm_backward(grad: torch.Tensor, x: torch.Tensor, mean: torch.Tensor,
     grad: of x's shape and dtype; mean and rstd: what layer_norm returned for x; weight: as given to
     it.  The main_grads are contiguous [hidden], both bf16 or both fp32, whatever the weight
     is.  out: where to write; out=grad or out=x replaces it.  workspace:
-    layer_norm_workspace(x.shape), allocated when not given.  The work is enqueued on the current
-    stream; the same call gives the same bits.
+    layer_norm_workspace(x.shape), allocated when not given; calls that may run at the same time (two
+    streams, two captured graphs) need one each.  The work is enqueued on the current stream; the
+    same call gives the same bits.
     """
     name = "layer_norm_backward"
     index, H, n, x_stride, x_code = _norm_input(name, x)

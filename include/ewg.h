@@ -444,7 +444,9 @@ size_t ewg_layer_norm_workspace_bytes(int64_t rows, int64_t hidden);
  *              address and stride), which it then replaces
  *   weight_main_grad, bias_main_grad   [hidden] contiguous, both of main_grad_dtype (EWG_BF16 or
  *              EWG_FP32), apart from everything else; NULL: not wanted
- *   workspace  ewg_layer_norm_workspace_bytes(rows, hidden) device bytes, 256-byte aligned
+ *   workspace  ewg_layer_norm_workspace_bytes(rows, hidden) device bytes, 256-byte aligned; calls
+ *              that may run at the same time (two streams, two captured graphs) need one each,
+ *              and main_grads of their own
  *
  * Requires sizes as ewg_layer_norm; rows = 0 enqueues nothing and leaves the main_grads as they
  * are.  Enqueues one to three kernels; allocates nothing.
