@@ -782,6 +782,7 @@ class _AdamWTensor(ctypes.Structure):
 
 
 _data_ptr = torch.Tensor.data_ptr
+_storage_ptr = torch.UntypedStorage.data_ptr
 
 
 class AdamWPlan:
@@ -801,14 +802,20 @@ class AdamWPlan:
         self._index = index
         self._all = [t for group in (params, grads, exp_avg, exp_avg_sq, scales or (), copies or ())
                      for t in group if t is not None]
-        # every step looks whether the params and their gradients are where they were; the others' memory
-        # is the plan's own too, as long as it lives
-        self._moving = params + grads
-        self._addresses = list(map(_data_ptr, self._moving))
-        self._held = [t.detach() for t in self._all]
+        # Every step looks whether all tensors are where they were, and whether the memory that they were in is: it is
+        # held, but may have been resized, and a tensor that was put elsewhere lie in what became of it.
+        storages = {}
+        for t in self._all:
+            storage = t.untyped_storage()
+            storages[storage._cdata] = storage
+        self._storages = list(storages.values())
+        self._addresses = self._places()
         self._written = params + [t for t in copies or () if t is not None]
         self._buffer = None            # of ewg_adamw_plan, and its bytes
         self._bytes = 0
+
+    def _places(self):
+        return [*map(_data_ptr, self._all), *map(_storage_ptr, self._storages)]
 
 
 def _state_list(name, given, params, dtype, shapes):
@@ -900,13 +907,13 @@ def adamw_step(plan: AdamWPlan, step, *, lr, betas: tuple = (0.9, 0.999), eps: f
     grad_scale multiplies the gradients: a clipping factor, or the inverse of a loss scale.  step
     (int64), lr and grad_scale (fp32) may be CUDA tensors of one element, which the step reads on
     the device: a captured step then follows their values.  The work is enqueued on the current
-    stream.  Raises ValueError if a param or gradient of the plan has moved to another address (states and
-    copies stay the tensors that they were).
+    stream.  Raises ValueError if a tensor of the plan has moved to another address, or the memory that it
+    was in has been given back.
     """
     if not plan.params:
         return
-    if list(map(_data_ptr, plan._moving)) != plan._addresses:
-        raise ValueError("a param or gradient of the plan has moved to another address: make a new plan")
+    if plan._places() != plan._addresses:
+        raise ValueError("a tensor of the plan has moved to another address: make a new plan")
     index = plan._index
     step, step_ptr = _scalar("step", step, torch.int64, index)
     lr, lr_ptr = _scalar("lr", lr, torch.float32, index)
