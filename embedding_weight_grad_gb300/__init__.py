@@ -810,7 +810,8 @@ class AdamWPlan:
             storages[storage._cdata] = storage
         self._storages = list(storages.values())
         self._addresses = self._places()
-        self._written = params + [t for t in copies or () if t is not None]
+        self._written = [t for group in (params, exp_avg, exp_avg_sq, scales or (), copies or ())
+                         for t in group if t is not None]
         self._buffer = None            # of ewg_adamw_plan, and its bytes
         self._bytes = 0
 

@@ -75,3 +75,23 @@ def test_tensors_of_one_bucket(monkeypatch):
     with pytest.raises(ValueError, match="moved"):
         ewg.adamw_step(plan, 2, lr=1e-3)
     assert len(steps) == 1
+
+
+def test_autograd_is_told_of_all_that_is_written(plan):
+    """Of params, copies and states; gradients are only read."""
+    versions = {k: [t._version for t in getattr(plan, k)] for k in GROUPS}
+    ewg.adamw_step(plan, 1, lr=1e-3)
+    for k in GROUPS:
+        assert [t._version for t in getattr(plan, k)] == [v + (k != "grads") for v in versions[k]], k
+
+
+def test_a_graph_that_saved_an_average(monkeypatch):
+    """Its backward pass raises instead of using what the step left there."""
+    p, g, m, v = (torch.ones(8) for _ in range(4))
+    monkeypatch.setattr(ewg, "_enqueue", lambda *a: None)
+    plan = ewg.AdamWPlan([p], [g], [None], [m], [v], None, 32, -1)
+    w = torch.ones(8, requires_grad=True)
+    loss = (w * m).sum()
+    ewg.adamw_step(plan, 1, lr=1e-3)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
