@@ -18,14 +18,15 @@
 // A warp takes 256 elements, eight neighbours a lane in one access of each array; where an array is not
 // aligned to that, one of every 32.  In 32 bits the step is bound by memory (50257 x 1024 fp32 with a bf16 copy, 30 bytes
 // an element: 224 us, 7.0 TB/s), in 8 with fp32 params too (129280 x 7168: 2540 us, 6.6 TB/s); with bf16 params and
-// gradients, 10 bytes an element, by its 60 instructions (50257 x 1024: 111 us, 4.6 TB/s; three elements off
-// alignment 129), of which the root takes ten and the two codes twelve.  The tensors' addresses are the
+// gradients, 10 bytes an element, by its 62 instructions (50257 x 1024: 114 us, 4.5 TB/s; three elements off
+// alignment 131), of which the root takes ten and the two codes twelve.  The tensors' addresses are the
 // launch's argument, so that nothing has to be uploaded and a captured call keeps them.
 //
 // Tried and slower: a warp's next block loaded ahead (bf16 in 8 bits the same, fp32 in 32 bits 3 % slower:
 // neighbouring blocks are then further apart in time), four neighbouring blocks a warp (6 %), bf16 arrays off
 // alignment by aligned accesses and shuffles (30 %), the first block's loads begun before the wait for the step's own
 // numbers (8 bits 4 to 11 %, 32 bits the same).
+#include <cfloat>
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -182,6 +183,13 @@ __device__ __forceinline__ float reciprocal(float x) {
   return y;
 }
 
+// x, or the largest number of its sign where it is infinite: an infinite param stays what it is.
+__device__ __forceinline__ float finite(float x) {
+  float y;
+  asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(FLT_MAX));
+  return y;
+}
+
 // The larger magnitude (of either sign), NaN if either is.
 __device__ __forceinline__ float larger(float a, float b) {
   float y;
@@ -230,6 +238,7 @@ __device__ __forceinline__ void to_codes(const float2 (&x)[4], float inverse, ui
 // A warp's block of 256 elements.
 template <typename P, typename G, int kBits, int kMode>
 __device__ __forceinline__ void update_block(const AdamwEntry& e, const AdamwHyper& h, const Step& s, long long base, int lane) {
+  using ptx::add2;
   using ptx::fma2;
   using ptx::mul2;
   const int count = e.count - base < kAdamwBlock ? static_cast<int>(e.count - base) : kAdamwBlock;
@@ -252,7 +261,7 @@ __device__ __forceinline__ void update_block(const AdamwEntry& e, const AdamwHyp
       v[i] = mul2(v[i], v[i]);
     }
   }
-  const float2 keep = both(1.0f - s.lr * e.weight_decay);
+  const float2 decay = both(-s.lr * e.weight_decay);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     // (each operation rounded by itself: the codes go by every bit of the moments)
@@ -262,7 +271,10 @@ __device__ __forceinline__ void update_block(const AdamwEntry& e, const AdamwHyp
     root[i] = make_float2(sqrtf(v[i].x), sqrtf(v[i].y));
     const float2 under = fma2(root[i], both(s.root_factor), both(h.eps));
     const float2 over = mul2(m[i], both(-s.rate));
-    p[i] = fma2(p[i], keep, mul2(over, make_float2(reciprocal(under.x), reciprocal(under.y))));
+    // The decay is added to the step and both to the param: 1 - lr wd by itself would be rounded by up to 2^-25, which
+    // is as much as a small decay.
+    const float2 lost = mul2(make_float2(finite(p[i].x), finite(p[i].y)), decay);
+    p[i] = add2(p[i], fma2(over, make_float2(reciprocal(under.x), reciprocal(under.y)), lost));
   }
   place.write(param, p);
   if constexpr (sizeof(P) == 4)

@@ -503,8 +503,9 @@ int ewg_adamw_plan(const ewg_adamw_tensor* tensors, int64_t num_tensors, int sta
  *     param = (1 - lr weight_decay) param
  *             - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
  *
- * and param is rounded once (a bf16 param without an fp32 master loses changes below half its
- * step).  The copy is the new param in bf16.  With eps = 0 an element without a gradient so far is
+ * and param is rounded once: what the decay takes and the update are added up first, so that a decay
+ * below fp32's rounding of 1 is no less exact (a bf16 param without an fp32 master loses changes below half its
+ * step).  An infinite param stays what it is.  The copy is the new param in bf16.  With eps = 0 an element without a gradient so far is
  * 0 / 0.
  *
  * States in 8 bits: after the step, which uses m and v unrounded, m and sqrt(v) are taken

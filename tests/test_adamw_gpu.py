@@ -475,3 +475,49 @@ def test_refusals():
         i = torch.zeros(10, device=DEV)
     with pytest.raises(ValueError, match="inference"):
         ewg.adamw_plan([i], [torch.zeros(10, device=DEV)])
+
+def half_ulp(x):
+    """Half of the step between fp32 numbers of x's size."""
+    return torch.ldexp(torch.ones_like(x), torch.frexp(x).exponent - 25)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("decay", [0.01, 0.1])
+@pytest.mark.parametrize("lr", [1e-3, 1e-5, 3.5e-6, 3e-7, 1e-7])
+def test_small_decays(lr, decay, shift, bits):
+    """lr weight_decay near fp32's rounding of 1: the new param is off by its own rounding, half a step between fp32
+    numbers, by 5 u of what the decay takes (lr, weight_decay, their product and its two uses round once each) and
+    by what the update itself may be off, whose own rounding is one of its 25 u."""
+    for grads in (False, True):
+        d = make([20000, 77], bits=bits, shift=shift)
+        if not grads:
+            for key in ("grads", "exp_avg", "exp_avg_sq"):
+                for t in d[key]:
+                    t.view(torch.uint8 if t.dtype == E4M3 else t.dtype).zero_()
+        refs = [Reference(d, k, bits, 2000, lr, (0.9, 0.999), 1e-8, decay, 1.0) for k in range(2)]
+        before = [p.double() for p in d["params"]]
+        ewg.adamw_step(plan_of(d, bits, decay), 2000, lr=lr)
+        for k, r in enumerate(refs):
+            p, lost = before[k], lr * decay * before[k]
+            step = p - lost - r.p
+            update = r.p_tol - 3 * U * (p.abs() + step.abs()) + U * step.abs()      # (of p_tol the part that is the update's)
+            rounding = torch.maximum(half_ulp(p), half_ulp(r.p))
+            near(d["params"][k].double(), r.p, rounding + 5 * U * lost.abs() + update, "param")
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("decay", [0.0, 0.1])
+def test_params_that_are_not_finite(decay, bits):
+    """An infinite param stays what it is, a NaN too, and neither is a neighbour's matter."""
+    d = make([1000], bits=bits)
+    plain = d["params"][0].clone()
+    e = {**make([1000], bits=bits), "params": [plain]}
+    bad = torch.tensor([float("inf"), -float("inf"), float("nan")], device=DEV)
+    d["params"][0][10:13] = bad
+    ewg.adamw_step(plan_of(d, bits, decay), 3, lr=1e-2)
+    ewg.adamw_step(plan_of(e, bits, decay), 3, lr=1e-2)
+    assert torch.equal(d["params"][0][10:12], bad[:2]) and bool(d["params"][0][12].isnan())
+    keep = torch.ones(1000, dtype=torch.bool, device=DEV)
+    keep[10:13] = False
+    assert torch.equal(d["params"][0][keep], plain[keep])
