@@ -493,3 +493,70 @@ def test_refusals():
                  lambda: back(weight_main_grad=w), lambda: back(workspace=ewg.layer_norm_workspace(x.shape)[1:])):
         with pytest.raises(ewg.EwgError):
             call()
+
+
+# Rows that no block holds: a thread adds up 32 numbers at a time, 32 of these sums and then at most 64 of those, and
+# the threads' sums meet in 13 additions: at most 142 in a row, however wide the row is.  K: with 1 / H and the product by it.
+WIDE = 144
+WIDEST = 1 << 24
+
+
+@pytest.mark.parametrize("value", [8.1, 1.1, 3.3, -1.9])
+@pytest.mark.parametrize("H", [32769, 1 << 20, (1 << 22) + 3, WIDEST - 1, WIDEST])
+def test_equal_elements_of_very_wide_rows(H, value):
+    """The first centre is off by e = K u of the value c.  The deviations are all c e, exactly, and their mean is off by K u
+    of that, which leaves the mean its own rounding.  The variance is what the squares' mean (K u) and the mean's square
+    (2 K u) are off, with two roundings: at most (3 K + 4) u (c e)^2."""
+    x = torch.full((1, H), value, dtype=FP32, device=DEV)
+    c, eps = x[0, 0].item(), 1e-10
+    r = ewg.layer_norm(x, None, None, eps=eps)
+    off = WIDE * U * abs(c)
+    assert abs(r.mean.item() - c) <= U * abs(c) + 2 * WIDE * U * off, (r.mean.item() - c) / (U * abs(c))
+    most = (3 * WIDE + 4) * U * off ** 2
+    want = eps ** -0.5
+    assert abs(r.rstd.item() - want) <= (most / (2 * eps) + 4 * U) * want
+    # (the mean's rounding is no deviation: what it leaves of each element is the centre's rest, off by K u)
+    assert r.out.abs().max().item() <= (2 * WIDE + 4) * U * off * want * (1 + 4 * U)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("n,H,offset", [(1, WIDEST, 0.0), (2, (1 << 22) + 3, 0.0), (3, 65537, 0.0), (1, WIDEST, 1.0)])
+def test_very_wide_rows(n, H, offset, dtype):
+    """As check_forward and check_backward, with a K that does not grow with H, and a gradient whose mean is not 0.  The
+    deviations are taken from a number near the mean, off it by K u avg|x|, in bf16 by half a step of the mean
+    besides; what is added up are the deviations from that."""
+    gen = torch.Generator(device=DEV).manual_seed(H)
+    x = (offset + torch.randn(n, H, generator=gen, device=DEV) * 0.5).to(dtype)
+    g = (1.1 + torch.randn(n, H, generator=gen, device=DEV) * 0.01).to(dtype)
+    w = (1 + 0.1 * torch.randn(H, generator=gen, device=DEV))
+    K, eps = WIDE, 1e-5
+    x64, g64, w64 = x.double(), g.double(), w.double()
+    mean = x64.mean(1, keepdim=True)
+    d = x64 - mean
+    near_mean = K * U * x64.abs().mean(1, keepdim=True) + (2.0 ** -8 * mean.abs() if dtype == BF16 else 0)
+    avg = d.abs().mean(1, keepdim=True) + near_mean
+    var = d.square().mean(1, keepdim=True)
+    square = var + near_mean ** 2
+    rstd = (var + eps).rsqrt()
+    r = ewg.layer_norm(x, w, None, eps=eps)
+    rest = (K + 2) * U * avg
+    near(r.mean, mean[:, 0], (rest + 2 * U * mean.abs())[:, 0], "mean")
+    var_tol = (K + 4) * U * square + 2 * near_mean * rest + rest ** 2 + 2 * U * var
+    r_tol = (var_tol / (2 * (var + eps)) + 5 * U) * 1.01
+    near(r.rstd, rstd[:, 0], (r_tol * rstd)[:, 0], "rstd")
+    want = d * rstd * w64
+    tol = rstd * w64.abs() * (rest + 3 * U * (d.abs() + near_mean)) + (r_tol + 3 * U) * want.abs()
+    near(r.out, want, tol + (half_step(BF16) * (want.abs() + tol) if dtype == BF16 else 0), "out")
+    mgs = [torch.ones(H, device=DEV) for _ in range(2)]
+    got = ewg.layer_norm_backward(g, x, r.mean, r.rstd, w, weight_main_grad=mgs[0], bias_main_grad=mgs[1])
+    r64 = r.rstd.double()[:, None]
+    hat = (x64 - r.mean.double()[:, None]) * r64
+    u = g64 * w64
+    c1, c2 = u.mean(1, keepdim=True), (u * hat).mean(1, keepdim=True)
+    a1, a2 = u.abs().mean(1, keepdim=True), (u * hat).abs().mean(1, keepdim=True)
+    want = r64 * (u - c1 - hat * c2)
+    tol = r64 * U * (4 * (u.abs() + c1.abs() + (hat * c2).abs()) + (K + 3) * a1 + hat.abs() * (K + 6) * a2) + U * want.abs()
+    near(got, want, tol + (half_step(dtype) * (want.abs() + tol) if dtype == BF16 else 0), "grad_x")
+    for mg, term in zip(mgs, (g64 * hat, g64)):
+        total = 1 + term.sum(0)
+        near(mg, total, (n + 8) * U * (term.abs().sum(0) + total.abs()), "main_grad")
