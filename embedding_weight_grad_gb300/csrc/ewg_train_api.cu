@@ -49,6 +49,14 @@ bool same_rows(const void* a, int64_t a_stride, const void* b, int64_t b_stride,
   return a == b && (rows == 1 || a_stride == b_stride);
 }
 
+// Whether a step of the entry's tensor writes memory of `r`.
+bool writes(const ewg::AdamwEntry& e, int state_bits, const Range& r) {
+  const int64_t n = e.count, blocks = (n + ewg::kAdamwBlock - 1) / ewg::kAdamwBlock, state = state_bits / 8;
+  auto in = [&](const void* p, int64_t count, size_t size) { return p && overlap(span(p, 1, count, count, size), r); };
+  return in(e.param, n, e.flags & ewg::kAdamwParamBf16 ? 2 : 4) || in(e.exp_avg, n, state) || in(e.exp_avg_sq, n, state) ||
+         in(e.scales, blocks, 8) || in(e.copy, n, 2);
+}
+
 int plan_adamw(const ewg_adamw_tensor* tensors, int64_t num, int state_bits, void* plan, size_t plan_bytes) {
   int dev = 0, sms = 0;
   int rc = current_device(&dev, &sms);
@@ -299,10 +307,16 @@ int ewg_adamw_step(const void* plan, size_t plan_bytes, int64_t step, const int6
     if (!(b >= 0 && static_cast<float>(b) < 1.0f)) return fail(EWG_ERR_UNSUPPORTED, "betas must be in [0, 1)");
   if ((rc = check_eps(eps))) return rc;
   DeviceMemory mem(dev);
-  if ((rc = check_optional(flat("step", step_on_device, 1, 8), 8, mem)) ||
-      (rc = check_optional(flat("lr", lr_on_device, 1, 4), 4, mem)) ||
-      (rc = check_optional(flat("grad_scale", grad_scale_on_device, 1, 4), 4, mem)))
-    return rc;
+  const auto* entries = reinterpret_cast<const ewg::AdamwEntry*>(static_cast<const char*>(plan) + sizeof head);
+  // blocks read these when they start, others have written by then
+  for (const Array& scalar : {flat("step", step_on_device, 1, 8), flat("lr", lr_on_device, 1, 4),
+                              flat("grad_scale", grad_scale_on_device, 1, 4)}) {
+    if (!scalar.p) continue;
+    if ((rc = check_array(scalar, scalar.r.hi - scalar.r.lo, mem))) return rc;
+    for (int64_t i = 0; i < head.entries; ++i)
+      if (writes(entries[i], head.state_bits, scalar.r))
+        return fail(EWG_ERR_UNSUPPORTED, std::string(scalar.name) + " lies in memory that is written by the step");
+  }
   ewg::AdamwHyper h{};
   h.step = step;
   h.step_ptr = reinterpret_cast<const long long*>(step_on_device);
@@ -317,7 +331,6 @@ int ewg_adamw_step(const void* plan, size_t plan_bytes, int64_t step, const int6
   h.rest2 = static_cast<float>(1.0 - beta2);
   h.log_beta2 = static_cast<float>(std::log(beta2));
   h.eps = static_cast<float>(eps);
-  const auto* entries = reinterpret_cast<const ewg::AdamwEntry*>(static_cast<const char*>(plan) + sizeof head);
   for (int64_t i = 0; i < head.entries; i += ewg::kAdamwEntries) {
     const int num = static_cast<int>(std::min<int64_t>(ewg::kAdamwEntries, head.entries - i));
     const cudaError_t e = ewg::launch_adamw(entries + i, num, head.state_bits, h, sms, static_cast<cudaStream_t>(stream));

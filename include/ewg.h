@@ -483,7 +483,8 @@ size_t ewg_adamw_plan_bytes(int64_t num_tensors);
  * host memory of the caller's (8-byte aligned, ewg_adamw_plan_bytes(num_tensors) bytes).
  * Nothing is enqueued, and the tensors' contents are not read.  The plan holds the tensors'
  * addresses: it may be used as long as they stay allocated, on the device that was current.
- * It can be copied, and used by several threads.
+ * It can be copied, and used by several threads (but steps of the same tensors that may run at the same
+ * time, on two streams or in two captured graphs, would get into each other's way).
  *
  * state_bits: 32, or 8.  In 8 bits the two moments of an element are e4m3 codes: its average is
  * code * scales[element / EWG_ADAMW_BLOCK][0], and the root of its second average code *
@@ -520,7 +521,7 @@ int ewg_adamw_plan(const ewg_adamw_tensor* tensors, int64_t num_tensors, int sta
  *
  *   step, lr, grad_scale     their values; where the pointer beside it is not NULL, it is a device
  *           scalar (int64, fp32, fp32) that is read in the value's place (a step below 1 as 1),
- *           so that a captured call follows a schedule
+ *           so that a captured call follows a schedule; apart from all that the step writes
  *
  * Requires step >= 1, finite lr >= 0, 0 <= beta1, beta2 < 1, an eps of 0 or in [2^-126, 2^126], finite
  * grad_scale.

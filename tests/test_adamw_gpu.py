@@ -521,3 +521,31 @@ def test_params_that_are_not_finite(decay, bits):
     keep = torch.ones(1000, dtype=torch.bool, device=DEV)
     keep[10:13] = False
     assert torch.equal(d["params"][0][keep], plain[keep])
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_scalars_that_the_step_would_write(bits):
+    """step, lr and grad_scale are read by blocks that start at any time: they may not lie in what others write."""
+    sizes = [k + 10 for k in range(401)]                                # (two launches, the last tensor in the second)
+    d = make(sizes, bits=bits, copy=True)
+    plan = plan_of(d, bits, 0.0)
+    before = [t.clone() for t in plan.params]
+    for k in (0, 3, 400):
+        scalars = [d["params"][k][-1:], d["params"][k][:1]]
+        if bits == 32:
+            scalars += [d["exp_avg"][k][2:3], d["exp_avg_sq"][k][-1:]]
+        else:
+            scalars += [d["scales"][k][-1, 1:], *(d[key][k].view(torch.uint8)[4:8].view(FP32) for key in ("exp_avg", "exp_avg_sq"))]
+        scalars.append(d["copies"][k][2:4].view(FP32))
+        for t in scalars:
+            for where in (dict(lr=t), dict(grad_scale=t)):
+                with pytest.raises(ewg.EwgError, match="written"):
+                    ewg.adamw_step(plan, 1, **{"lr": 1e-3, **where})
+    states = d["exp_avg"] if bits == 32 else d["scales"]
+    with pytest.raises(ewg.EwgError, match="written"):
+        flat = states[100].flatten()
+        at = flat.data_ptr() // 4 % 2
+        ewg.adamw_step(plan, flat[at:at + 2].view(torch.int64), lr=1e-3)
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, b) for p, b in zip(plan.params, before))
+    ewg.adamw_step(plan, 1, lr=d["grads"][0][:1].abs(), grad_scale=d["grads"][7][:1])      # (gradients are only read)
