@@ -1196,7 +1196,7 @@ cudaError_t launch_stream(NormGradArgs a, cudaStream_t stream) {
   if (s.bytes < meet) s.bytes = meet;
   int most = 0;
   cudaError_t e = set_up(kernel, state, a.dev);
-  if (e != cudaSuccess || (e = groups_at_once(kernel, state, s, a.dev, a.parts, &most)) != cudaSuccess) return e;
+  if (e != cudaSuccess || (e = groups_at_once(kernel, state, s, a.dev, a.num_sms, &most)) != cudaSuccess) return e;
   set_groups(s, a.n, kR, most < a.parts ? most : a.parts, a.period);
   a.parts = s.groups;
   NormGradStream k{};

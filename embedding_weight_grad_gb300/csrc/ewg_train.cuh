@@ -47,7 +47,7 @@ struct NormGradArgs {
   float2* row_sums;          // [n]: avg(u) and avg(u n), for rows of more than kNormHeld elements
   float* partial;            // [parts][2][H]: shares of the sums over the rows
   int parts;                 // shares of the rows
-  int dev;
+  int dev, num_sms;
   int period;                // rows whose places in 16 bytes differ (set by the launcher)
 };
 

@@ -268,6 +268,7 @@ int ewg_layer_norm_backward(const void* grad, int64_t grad_row_stride, const voi
   a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + L.partial);
   a.parts = L.parts;
   a.dev = dev;
+  a.num_sms = sms;
   const cudaError_t e = ewg::launch_norm_grad(a, dtype == EWG_BF16, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? EWG_OK : cuda_fail(e, "layer norm gradient launch");
 }

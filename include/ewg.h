@@ -434,8 +434,8 @@ size_t ewg_layer_norm_workspace_bytes(int64_t rows, int64_t hidden);
  *
  * avg over the row.  Everything is computed and summed in 32 bits; grad_x is rounded once, and
  * a sum over the rows is added to its main_grad element in 32 bits and rounded to the main_grad's
- * dtype.  The order of the sums depends on rows, hidden, the arrays' alignment and, for hidden above
- * 8192, the device: the same call gives the same bits.
+ * dtype.  The order of the sums depends on rows, hidden, the arrays' alignment and the device: the
+ * same call gives the same bits.
  *
  *   grad, x    [rows][hidden] of `dtype` (EWG_BF16 or EWG_FP32), unit inner stride, any alignment
  *   mean, rstd [rows] fp32, as ewg_layer_norm left them
