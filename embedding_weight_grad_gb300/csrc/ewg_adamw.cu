@@ -9,9 +9,10 @@
 // sqrt(v), each relative to a scale (largest magnitude / 448).  A second average changes by
 // a thousandth of itself a step, and e4m3 has steps of a tenth: rounded to nearest, an element keeps
 // its code for good unless the whole block's scale moves (with b2 = 0.999, where half of a block's
-// gradients fall to 0.3 of what they were, their roots stay 2.3 times too large after 2000 steps).  So the
-// rounding's threshold runs evenly through [0, 1) over steps and elements (an additive sequence),
-// and the changes add up (then 0.99 of what they should be).  Rounding is an integer addition: times 2^-120,
+// gradients fall to 0.3 of what they were, their roots are still 2.2 times too large after 2000 steps).  So the
+// rounding's threshold runs evenly through [0, 1) over steps and elements (an additive sequence: M. Roberts's
+// R2, by the plastic number), and the changes add up (the roots are then 0.95 of what they should be; where the gradients
+// triple 1.04, rounded to nearest 0.35).  Rounding is an integer addition: times 2^-120,
 // e4m3's exponents are fp32's lowest, its steps below 2^-6 fp32's subnormals, and a code the upper 7
 // bits of a number's 27.
 //

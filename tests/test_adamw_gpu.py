@@ -549,3 +549,30 @@ def test_scalars_that_the_step_would_write(bits):
     torch.cuda.synchronize()
     assert all(torch.equal(p, b) for p, b in zip(plan.params, before))
     ewg.adamw_step(plan, 1, lr=d["grads"][0][:1].abs(), grad_scale=d["grads"][7][:1])      # (gradients are only read)
+
+@pytest.mark.parametrize("factor", [0.3, 3.0])
+def test_8_bits_follow_a_change_of_the_gradients(factor):
+    """b2 = 0.999, half of each block's gradients fall to 0.3 of what they were (or rise to 3 times that), the other
+    half holds the scale: a second average changes by a thousandth of itself a step, far less than the width of a
+    level, and after 2000 steps its root is what it is without rounding.
+
+    Asked of the mean over 4096 roots, whose thresholds differ: nearer than half a level at its widest, 1/16 of it.
+    (Rounded to nearest the roots stay where they were, 2.2 times too large or 0.35 of what they should be.)"""
+    n, T, b2 = 8192, 2000, 0.999
+    sizes = torch.linspace(0.2, 0.3, n, device=DEV)
+    changed = torch.arange(n, device=DEV) % 2 == 1
+    g = sizes.clone()
+    g[::256] = 1.0
+    p = torch.zeros(n, device=DEV)
+    plan = ewg.adamw_plan([p], [g], state_bits=8, weight_decay=0.0)
+    ewg.adamw_step(plan, 1, lr=0.0, betas=(0.9, 0.0))                    # the second average is g^2
+    g[changed] *= factor
+    for t in range(2, T + 2):
+        ewg.adamw_step(plan, t, lr=0.0, betas=(0.9, b2))
+    root = values8(plan.exp_avg_sq[0], plan.scales[0], 1).double()
+    before, now = sizes.double(), g.double()
+    want = (now ** 2 + b2 ** T * (before ** 2 - now ** 2)).sqrt()
+    ratio = (root / want)[changed].mean().item()
+    assert abs(ratio - 1) < 1 / 16, ratio
+    still = (root / want)[~changed].mean().item()
+    assert abs(still - 1) < 1 / 16, still
