@@ -1243,8 +1243,11 @@ cudaError_t by_team(const Args& a, cudaStream_t stream) {
 // gradient, where the columns' sums take the registers (65536 x 256 bf16: 33 us, with eight 23).
 template <typename T, int kE, bool kShift>
 cudaError_t stream_rows(const NormArgs& a, cudaStream_t stream) {
-  if (sizeof(T) == 4 && a.H <= 1024) return by_team<T, kE, 8, kShift>(a, stream);
-  return by_team<T, kE, 16, kShift>(a, stream);
+  if constexpr (sizeof(T) == 2) {
+    return by_team<T, kE, 16, kShift>(a, stream);
+  } else {
+    return a.H <= 1024 ? by_team<T, kE, 8, kShift>(a, stream) : launch_stream<T, kE, 16, 0, kShift>(a, stream);
+  }
 }
 template <typename T, int kE, bool kShift>
 cudaError_t stream_rows(const NormGradArgs& a, cudaStream_t stream) {
