@@ -19,8 +19,8 @@
 // A warp takes 256 elements, eight neighbours a lane in one access of each array; where an array is not
 // aligned to that, one of every 32.  In 32 bits the step is bound by memory (50257 x 1024 fp32 with a bf16 copy, 30 bytes
 // an element: 224 us, 7.0 TB/s), in 8 with fp32 params too (129280 x 7168: 2540 us, 6.6 TB/s); with bf16 params and
-// gradients, 10 bytes an element, by its 62 instructions (50257 x 1024: 114 us, 4.5 TB/s; three elements off
-// alignment 131), of which the root takes ten and the two codes twelve.  The tensors' addresses are the
+// gradients, 10 bytes an element, by its 63 instructions and its loads (50257 x 1024: 114 us, 4.5 TB/s; three
+// elements off alignment 130), of which the root takes ten and the two codes twelve.  The tensors' addresses are the
 // launch's argument, so that nothing has to be uploaded and a captured call keeps them.
 //
 // Tried and slower: a warp's next block loaded ahead (bf16 in 8 bits the same, fp32 in 32 bits 3 % slower:
@@ -343,8 +343,9 @@ cudaError_t launch(const AdamwEntry* entries, int num, const AdamwHyper& h, int 
   const AdamwEntry& last = entries[num - 1];
   a.tiles = last.first_tile + static_cast<int>((last.count + kAdamwTile - 1) / kAdamwTile);
   // In 32 bits a block of threads takes one tile, so that the tiles on the way are neighbours in memory (50257 x
-  // 1024 fp32: 210 us; 8 blocks an SM that go on in steps of the grid: 226).  In 8 bits the step's
-  // own numbers cost more than that brings: 32 blocks an SM (132 us; one tile each 146, 8 an SM 135).
+  // 1024 fp32 with a bf16 copy: 224 us; 8 blocks an SM that go on in steps of the grid: 242).  In 8 bits the step's
+  // own numbers cost more than that brings: 32 blocks an SM (the same 140 us, bf16 without a copy 114; one tile
+  // each 150 and 135, 8 blocks an SM 149 and 115).
   const int most = kBits == 32 ? a.tiles : num_sms * 32;
   adamw_kernel<kBits, kTable><<<a.tiles < most ? a.tiles : most, kThreads, 0, stream>>>(a);
   return cudaGetLastError();

@@ -18,7 +18,8 @@
 //
 // Rows that do not begin at 16 bytes repeat their places in them after at most eight rows.  A group takes rows of
 // one place, so that its accesses are whole ones too, and the few elements beside them go by themselves
-// (65536 x 1001 fp32: 92 and 124 us, element by element 117 and 163; bf16 54 and 78, 82 and 153).
+// (65536 x 1001 fp32: 93 and 124 us, bf16 53 and 78).  Where the arrays' rows begin differently they move element by
+// element (fp32 110 and 167 us, bf16 87 and 155).
 //
 // Tried and slower: every thread's next row in registers instead of shared memory (8192 x 7168 backward 96 us),
 // 1024 threads of eight columns (85 us), deviations from the average of a row's first 32 elements,

@@ -407,8 +407,8 @@ int ewg_orthogonalize_transposed(const void* grad, int grad_dtype, int64_t batch
  *           x itself (same address and stride), which it then replaces
  *   mean, rstd       [rows] fp32; both NULL: not wanted (nothing goes back through the rows)
  *
- * A row with a NaN or an infinity gives NaN, and so does one whose squared deviations' sum, in
- * fp32, leaves its range.  A row of equal elements has rstd 1 / sqrt(eps); its
+ * A row with a NaN or an infinity gives NaN, and so does one whose elements' or squared deviations' sum
+ * leaves fp32's range.  A row of equal elements has rstd 1 / sqrt(eps); its
  * results mean nothing with an eps of 0, or one that is not large beside the square of the mean's
  * rounding (2^-24 of the mean).
  *
