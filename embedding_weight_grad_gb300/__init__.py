@@ -908,8 +908,8 @@ def adamw_step(plan: AdamWPlan, step, *, lr, betas: tuple = (0.9, 0.999), eps: f
     grad_scale multiplies the gradients: a clipping factor, or the inverse of a loss scale.  step
     (int64), lr and grad_scale (fp32) may be CUDA tensors of one element, which the step reads on
     the device: a captured step then follows their values (they may not lie in what the step
-    writes).  The work is enqueued on the current stream.  Raises ValueError if a tensor of the plan has moved to another address, or the memory that it
-    was in has been given back.
+    writes).  The work is enqueued on the current stream.  Raises ValueError if a tensor of the plan
+    has moved to another address, or the memory that it was in has been given back.
     """
     if not plan.params:
         return

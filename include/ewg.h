@@ -407,8 +407,8 @@ int ewg_orthogonalize_transposed(const void* grad, int grad_dtype, int64_t batch
  *           x itself (same address and stride), which it then replaces
  *   mean, rstd       [rows] fp32; both NULL: not wanted (nothing goes back through the rows)
  *
- * A row with a NaN or an infinity gives NaN, and so does one whose elements' or squared deviations' sum
- * leaves fp32's range.  A row of equal elements has rstd 1 / sqrt(eps); its
+ * A row with a NaN or an infinity gives NaN, and so does one whose elements' or squared
+ * deviations' sum leaves fp32's range.  A row of equal elements has rstd 1 / sqrt(eps); its
  * results mean nothing with an eps of 0, or one that is not large beside the square of the mean's
  * rounding (2^-24 of the mean).
  *
@@ -483,8 +483,8 @@ size_t ewg_adamw_plan_bytes(int64_t num_tensors);
  * host memory of the caller's (8-byte aligned, ewg_adamw_plan_bytes(num_tensors) bytes).
  * Nothing is enqueued, and the tensors' contents are not read.  The plan holds the tensors'
  * addresses: it may be used as long as they stay allocated, on the device that was current.
- * It can be copied, and used by several threads (but steps of the same tensors that may run at the same
- * time, on two streams or in two captured graphs, would get into each other's way).
+ * It can be copied, and used by several threads (but steps of the same tensors that may run at
+ * the same time, on two streams or in two captured graphs, would get into each other's way).
  *
  * state_bits: 32, or 8.  In 8 bits the two moments of an element are e4m3 codes: its average is
  * code * scales[element / EWG_ADAMW_BLOCK][0], and the root of its second average code *
@@ -504,10 +504,10 @@ int ewg_adamw_plan(const ewg_adamw_tensor* tensors, int64_t num_tensors, int sta
  *     param = (1 - lr weight_decay) param
  *             - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
  *
- * and param is rounded once: what the decay takes and the update are added up first, so that a decay
- * below fp32's rounding of 1 is no less exact (a bf16 param without an fp32 master loses changes below half its
- * step).  An infinite param stays what it is.  The copy is the new param in bf16.  With eps = 0 an element without a gradient so far is
- * 0 / 0.
+ * and param is rounded once: what the decay takes and the update are added up first, so that a
+ * decay below fp32's rounding of 1 is no less exact (a bf16 param without an fp32 master loses
+ * changes below half its step).  An infinite param stays what it is (lr weight_decay <= 1).  The
+ * copy is the new param in bf16.  With eps = 0 an element without a gradient so far is 0 / 0.
  *
  * States in 8 bits: after the step, which uses m and v unrounded, m and sqrt(v) are taken
  * relative to their block's scale, its largest magnitude times fl(1 / 448), and rounded to e4m3:
